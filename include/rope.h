@@ -48,7 +48,9 @@ typedef enum {
     ROPE_ERR_UNSUPPORTED = 2,      /* dtype or layout value outside the enums    */
     ROPE_ERR_CUDA = 3,             /* a CUDA call failed (launch, sync, ...)     */
     ROPE_ERR_POS_OUT_OF_RANGE = 4, /* a position index was outside the table     */
-    ROPE_ERR_KERNEL_TIMEOUT = 5    /* a bounded wait inside a kernel expired      */
+    ROPE_ERR_KERNEL_TIMEOUT = 5,   /* a bounded wait inside a kernel expired      */
+    ROPE_ERR_BAD_INDEX = 6         /* a sequence offset, a length or a page number
+                                      of a serving call was out of range          */
 } rope_status;
 
 typedef enum { ROPE_SPLIT_HALF = 0, ROPE_INTERLEAVED = 1 } rope_layout;
@@ -337,11 +339,73 @@ rope_status rope_attention_fwd_noalloc(const void *q, const void *k, const void 
                                        int32_t dtype, int64_t table_rows, void *stream);
 
 /*
+ * Serving: packed sequences and a paged cache.
+ *
+ * Packed sequences.  The tokens of n_seqs sequences lie one after the other
+ *   in [total, H, D] tensors; sequence b holds the tokens cu[b] .. cu[b+1] - 1
+ *   (cu: device int32[n_seqs + 1], 0 <= cu[b] <= cu[b+1] <= total; lengths of
+ *   zero are allowed, and so are rows before cu[0] and from cu[n_seqs] on,
+ *   which belong to no sequence: the rows of an output there keep what they
+ *   hold).  A token stride, in elements and a multiple of 8, lets an input be
+ *   a view of a fused projection's output; heads and features are dense.
+ * Paged cache.  k_pages, v_pages: device [n_pages, Hk, page_size, D] of the
+ *   element type; page_size is 16, 32, 64 or 128.  A block list (device
+ *   int32) names the pages of a sequence in order: its key i lies in row
+ *   i mod page_size of page list[i / page_size].  Entries past a sequence's
+ *   last key are not read.  Cached keys are rotated keys.
+ * Element types ROPE_BF16 and ROPE_F16; D is 64 or 128; rotary_dim is a
+ *   multiple of 16, 16 <= rotary_dim <= D; pointers to 16-bit and fp32 data
+ *   are 16-byte aligned.  What only the device can see -- offsets, lengths,
+ *   page numbers, positions -- is checked there: nothing out of range is read
+ *   or written, and rope_check_errors reports ROPE_ERR_BAD_INDEX (positions:
+ *   ROPE_ERR_POS_OUT_OF_RANGE).
+ */
+
+/*
+ * rope_cache_append -- rotate new keys and write them, and their values, into
+ * the pages of a cache.
+ *
+ * Token t of sequence b becomes key s = cache_lens[b] + t - cu[b] of its
+ * sequence:
+ *   k_pages[p, h, s mod page_size, :] = rot(k[t, h, :]),
+ *   v_pages[p, h, s mod page_size, :] = v[t, h, :],
+ *   p = block_table[b * max_blocks + s / page_size].
+ * k, v: device [total, Hk, D], token strides k_stride, v_stride.
+ * block_table: device int32[n_seqs, max_blocks].
+ * cache_lens: device int32[n_seqs], the keys each sequence holds already
+ *   (read only: the caller advances it).
+ * pos: device int32[total] or NULL.  The key of token t is rotated with table
+ *   row pos[t] (-1: not rotated), or pos_offset + s when pos is NULL
+ *   (pos_offset >= 0: the length of a prefix kept elsewhere).  A row outside
+ *   the table leaves the key unrotated (it is written) and raises the flag.
+ * Tokens with a page number or a block outside the ranges are not written
+ *   and raise the flag.  When two tokens go to the same row of the same page,
+ *   either may be the one that remains.
+ * Arithmetic: as rope_apply_qk (one rounding; the same bits); values are copied.
+ * total = 0 or n_seqs = 0 or Hk = 0: nothing to do, ROPE_OK.
+ * Errors: ROPE_ERR_UNSUPPORTED for other dtypes, layouts, D, rotary_dim,
+ *   page_size, strides not a multiple of 8 or pointers not 16-byte aligned;
+ *   ROPE_ERR_INVALID_ARG for bad sizes, a token stride below Hk * D, null
+ *   pointers, a pool overlapping another argument; ROPE_ERR_CUDA if the
+ *   launch fails.
+ */
+rope_status rope_cache_append(const void *k, const void *v, void *k_pages, void *v_pages,
+                              const int32_t *block_table, const int32_t *cu_seqlens,
+                              const int32_t *cache_lens, const float *cos, const float *sin,
+                              const int32_t *pos, int64_t pos_offset, int64_t n_seqs,
+                              int64_t total, int64_t k_stride, int64_t v_stride, int32_t Hk,
+                              int32_t D, int32_t rotary_dim, int32_t layout, int32_t page_size,
+                              int64_t n_pages, int64_t max_blocks, int32_t dtype,
+                              int64_t table_rows, void *stream);
+
+/*
  * rope_check_errors -- synchronise `stream`, then report and clear the
  * current device's error flag.
  * Returns ROPE_ERR_CUDA if the stream reports an error, else
  * ROPE_ERR_KERNEL_TIMEOUT if a wait inside an attention kernel expired
  * (about 2 s; that launch stopped early and its output is incomplete), else
+ * ROPE_ERR_BAD_INDEX if a serving call since the last check met a sequence
+ * offset, a length or a page number out of range, else
  * ROPE_ERR_POS_OUT_OF_RANGE if any launch since the last check met an
  * out-of-range position index, else ROPE_OK.  The flag is shared by all
  * streams of the device.

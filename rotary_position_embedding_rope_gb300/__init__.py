@@ -19,6 +19,10 @@ rotates Q and K with their own XPOS tables.  ``attention`` calls
 ``rope_attention_fwd`` (``rope_attention_fwd_masked`` with an ``attn_mask``):
 attention with the rotation fused into the Q/K tile loads (or, with a key
 workspace, keys rotated once beforehand).
+``cache_append`` writes new keys (rotated) and values into a paged cache,
+``attention_packed`` attends over packed prompts of different lengths and
+``attention_shared_prefix`` runs one new token per sequence over a prefix all
+sequences share and each one's own pages.
 ``host.HostRotator`` and ``host.HostAttention`` run the rotation and the
 attention on tensors that live in pinned host memory, overlapping the copies
 with the calls.
@@ -34,7 +38,8 @@ from . import _build
 
 __all__ = [
     "RopeError", "ROPE_OK", "ROPE_ERR_INVALID_ARG", "ROPE_ERR_UNSUPPORTED", "ROPE_ERR_CUDA",
-    "ROPE_ERR_POS_OUT_OF_RANGE", "ROPE_ERR_KERNEL_TIMEOUT", "VARIANT_ELEMENTWISE", "VARIANT_VECTOR",
+    "ROPE_ERR_POS_OUT_OF_RANGE", "ROPE_ERR_KERNEL_TIMEOUT", "ROPE_ERR_BAD_INDEX",
+    "VARIANT_ELEMENTWISE", "VARIANT_VECTOR",
     "ROPE_SPLIT_HALF", "ROPE_INTERLEAVED", "ROPE_F32", "ROPE_BF16", "ROPE_F16", "ROPE_FREQ_LANG",
     "ROPE_FREQ_PIXEL", "ROPE_FREQ_CONSTANT", "ROPE_MASK_NONE", "ROPE_MASK_KEYS",
     "ROPE_MASK_QUERY_KEYS", "library_path", "load_library",
@@ -43,14 +48,14 @@ __all__ = [
     "rope_apply_qk_out", "rope_attention_fwd", "rope_attention_fwd_masked",
     "rope_attention_fwd_noalloc", "rope_check_errors", "rope_probe_wait_expiry",
     "rope_status_string", "rope_qk_kernel_variant", "rope_force_kernel_variant",
-    "rope_tune_rotation_launch",
+    "rope_tune_rotation_launch", "rope_cache_append",
     # conveniences
     "build_tables", "build_tables_ex", "apply_qk", "apply_q", "apply_qk_xpos", "rotate_qk",
-    "attention", "attention_workspace", "PreparedApply",
+    "attention", "attention_workspace", "PreparedApply", "cache_append",
 ]
 
 (ROPE_OK, ROPE_ERR_INVALID_ARG, ROPE_ERR_UNSUPPORTED, ROPE_ERR_CUDA, ROPE_ERR_POS_OUT_OF_RANGE,
- ROPE_ERR_KERNEL_TIMEOUT) = range(6)
+ ROPE_ERR_KERNEL_TIMEOUT, ROPE_ERR_BAD_INDEX) = range(7)
 VARIANT_ELEMENTWISE, VARIANT_VECTOR = 2, 3
 ROPE_SPLIT_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_F32, ROPE_BF16, ROPE_F16 = 0, 1, 2
@@ -139,6 +144,9 @@ def load_library() -> ctypes.CDLL:
     lib.rope_force_kernel_variant.restype = c.c_int
     lib.rope_tune_rotation_launch.argtypes = [c.c_int32, c.c_int32, c.c_int32]
     lib.rope_tune_rotation_launch.restype = c.c_int
+    lib.rope_cache_append.argtypes = [P] * 10 + [c.c_int64] * 5 + [c.c_int32] * 5 + \
+        [c.c_int64, c.c_int64, c.c_int32, c.c_int64, P]
+    lib.rope_cache_append.restype = c.c_int
     _lib = lib
     return lib
 
@@ -603,3 +611,134 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Tens
                          (tuple(attn_mask.shape),))
     rope_attention_fwd_masked(*args, attn_mask, kind, k_workspace, ws_bytes, stream)
     return o
+
+
+# --------------------------------------------------------------------------
+# serving: packed sequences and a paged cache
+# --------------------------------------------------------------------------
+def rope_cache_append(k, v, k_pages, v_pages, block_table, cu_seqlens, cache_lens, cos, sin, pos,
+                      pos_offset, n_seqs, total, k_stride, v_stride, Hk, D, rotary_dim, layout,
+                      page_size, n_pages, max_blocks, dtype, table_rows, stream=None):
+    st = load_library().rope_cache_append(
+        _addr(k, "k"), _addr(v, "v"), _addr(k_pages, "k_pages"), _addr(v_pages, "v_pages"),
+        _addr(block_table, "block_table"), _addr(cu_seqlens, "cu_seqlens"),
+        _addr(cache_lens, "cache_lens"), _addr(cos, "cos"), _addr(sin, "sin"), _addr(pos, "pos"),
+        int(pos_offset), int(n_seqs), int(total), int(k_stride), int(v_stride), int(Hk), int(D),
+        int(rotary_dim), int(layout), int(page_size), int(n_pages), int(max_blocks), int(dtype),
+        int(table_rows), _stream(stream))
+    _check(st, "rope_cache_append")
+
+
+class _Call:
+    """One serving call: the device its tensors live on and the stream it runs
+    on, with that device current while the library is called."""
+
+    def __init__(self, first: torch.Tensor, stream):
+        if not first.is_cuda:
+            raise ValueError("expected CUDA tensors, got one on %s" % first.device)
+        self.device = first.device
+        if stream is None:
+            self.stream = torch.cuda.current_stream(self.device).cuda_stream
+        elif isinstance(stream, int):
+            self.stream = stream
+        else:
+            if stream.device != self.device:
+                raise ValueError("the stream belongs to %s, the tensors to %s" %
+                                 (stream.device, self.device))
+            self.stream = stream.cuda_stream
+
+    def rows(self, x, name, H=None, D=None, dtype=None):
+        """(address, token stride) of a [T, H, D] tensor, dense but for its tokens."""
+        if x.dim() != 3:
+            raise ValueError("%s must be [tokens, heads, D], got %s" % (name, tuple(x.shape)))
+        t, h, d = x.shape
+        if (H is not None and h != H) or (D is not None and d != D):
+            raise ValueError("%s must be [tokens, %s, %s], got %s" % (name, H, D, tuple(x.shape)))
+        if (dtype is not None and x.dtype != dtype) or x.device != self.device:
+            raise ValueError("%s must be a %s tensor on %s" % (name, dtype, self.device))
+        st, sh, sd = x.stride()
+        if x.numel() > 0 and ((d > 1 and sd != 1) or (h > 1 and sh != d)):
+            raise ValueError("%s: heads and features must be dense (strides %s)" %
+                             (name, x.stride()))
+        return (x.data_ptr() if x.numel() else None), (st if t > 1 else h * d)
+
+    def dense(self, x, name, dtype, shape=None):
+        """Address of a contiguous tensor of the given type (and shape)."""
+        if x is None:
+            return None
+        if x.dtype != dtype or x.device != self.device:
+            raise ValueError("%s must be a %s tensor on %s, got %s on %s" %
+                             (name, dtype, self.device, x.dtype, x.device))
+        if shape is not None and tuple(x.shape) != shape:
+            raise ValueError("%s must be %s, got %s" % (name, shape, tuple(x.shape)))
+        if not x.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        return x.data_ptr() if x.numel() else None
+
+    def tables(self, cos, sin, rotary_dim):
+        """(cos address, sin address, rotary_dim, rows)."""
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be [rows, rotary_dim / 2] tables of the same shape")
+        rd = 2 * cos.shape[1] if rotary_dim is None else rotary_dim
+        if cos.shape[1] * 2 != rd:
+            raise ValueError("table width %d does not match rotary_dim %d" % (cos.shape[1], rd))
+        return (self.dense(cos, "cos", torch.float32), self.dense(sin, "sin", torch.float32), rd,
+                cos.shape[0])
+
+    def cache(self, k_pages, v_pages, dtype):
+        """(k address, v address, pages, Hk, page size, D) of a cache's pools."""
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+            raise ValueError("k_pages and v_pages must be [pages, Hk, page_size, D] of one shape")
+        return (self.dense(k_pages, "k_pages", dtype), self.dense(v_pages, "v_pages", dtype),
+                *k_pages.shape)
+
+    def run(self, fn, name, *args):
+        if self.device.index == torch.cuda.current_device():
+            st = fn(*args, self.stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = fn(*args, self.stream)
+        if st != ROPE_OK:
+            raise RopeError(st, name)
+
+
+def _type16(x: torch.Tensor, what: str) -> int:
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("%s takes bf16 or fp16 tensors, got %s" % (what, x.dtype))
+    return _DTYPE_CODE[x.dtype]
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 block_table: torch.Tensor, cu_seqlens: torch.Tensor, cache_lens: torch.Tensor,
+                 cos: torch.Tensor, sin: torch.Tensor, pos: torch.Tensor | None = None,
+                 pos_offset: int = 0, rotary_dim: int | None = None, layout: str = "split_half",
+                 stream=None) -> None:
+    """Rotate new keys and write them, with their values, into a paged cache.
+
+    k, v: [T, Hk, D] packed new tokens (views with a token stride are taken as
+    they are); sequence b owns tokens cu_seqlens[b] .. cu_seqlens[b+1] - 1,
+    which become its keys cache_lens[b], cache_lens[b] + 1, ...
+    k_pages, v_pages: [pages, Hk, page_size, D], page_size 16, 32, 64 or 128.
+    block_table: int32 [n_seqs, max_blocks]; cu_seqlens: int32 [n_seqs + 1];
+    cache_lens: int32 [n_seqs] (not advanced by the call).
+    pos: int32 [T] table rows (-1 = not rotated), or None for pos_offset + the
+    key's index in its sequence.
+    """
+    c = _Call(k, stream)
+    code = _type16(k, "cache_append")
+    kp, vp, n_pages, Hk, page, D = c.cache(k_pages, v_pages, k.dtype)
+    ka, ks = c.rows(k, "k", Hk, D, k.dtype)
+    va, vs = c.rows(v, "v", Hk, D, k.dtype)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same tokens")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [n_seqs, max_blocks]")
+    n, blocks = block_table.shape
+    ca, sa, rd, rows = c.tables(cos, sin, rotary_dim)
+    i32 = torch.int32
+    c.run(load_library().rope_cache_append, "rope_cache_append", ka, va, kp, vp,
+          c.dense(block_table, "block_table", i32), c.dense(cu_seqlens, "cu_seqlens", i32, (n + 1,)),
+          c.dense(cache_lens, "cache_lens", i32, (n,)), ca, sa, c.dense(pos, "pos", i32, (T,)),
+          pos_offset, n, T, ks, vs, Hk, D, rd, _LAYOUT_CODE[layout], page, n_pages, blocks, code,
+          rows)

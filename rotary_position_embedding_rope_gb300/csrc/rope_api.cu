@@ -10,6 +10,7 @@
 
 #include "rope.h"
 #include "rope_internal.cuh"
+#include "rope_serving.cuh"
 
 namespace rope {
 
@@ -17,7 +18,9 @@ namespace rope {
 // Device flag word: bit 0 is set (atomicOr) by the rotation kernels when a
 // position index is outside [0, table_rows) and not -1; bit 1 when a wait of
 // an attention kernel (or of rope_probe_wait_expiry) ran out of its time
-// budget.  One word per device; the kernels get its address as an argument.
+// budget; bit 2 when a serving kernel met a sequence offset, a length or a page
+// number out of range.  One word per device; the kernels get its address as an
+// argument.
 // g_flag_taken receives the value read-and-cleared by rope_check_errors.
 // ---------------------------------------------------------------------------
 __device__ int32_t g_range_flag;
@@ -51,6 +54,12 @@ static cudaError_t flag_addresses(int32_t **flag, int32_t **taken)
     *flag = g_flag_addr[dev];
     *taken = g_taken_addr[dev];
     return cudaSuccess;
+}
+
+cudaError_t device_flag(int32_t **flag)
+{
+    int32_t *taken = nullptr;
+    return flag_addresses(flag, &taken);
 }
 
 __global__ void take_flag_kernel(int32_t *flag, int32_t *taken)
@@ -709,6 +718,8 @@ rope_status rope_check_errors(void *stream)
         return ROPE_ERR_CUDA;
     if (value & 2)
         return ROPE_ERR_KERNEL_TIMEOUT;
+    if (value & 4)
+        return ROPE_ERR_BAD_INDEX;
     return value ? ROPE_ERR_POS_OUT_OF_RANGE : ROPE_OK;
 }
 
@@ -757,6 +768,7 @@ const char *rope_status_string(rope_status status)
     case ROPE_ERR_CUDA: return "ROPE_ERR_CUDA";
     case ROPE_ERR_POS_OUT_OF_RANGE: return "ROPE_ERR_POS_OUT_OF_RANGE";
     case ROPE_ERR_KERNEL_TIMEOUT: return "ROPE_ERR_KERNEL_TIMEOUT";
+    case ROPE_ERR_BAD_INDEX: return "ROPE_ERR_BAD_INDEX";
     default: return "ROPE_STATUS_UNKNOWN";
     }
 }

@@ -1,0 +1,66 @@
+"""The serving entry points without a GPU: what they refuse on the host,
+before touching the device.  No call here launches work."""
+import pytest
+import torch
+
+import rotary_position_embedding_rope_gb300 as R
+from rotary_position_embedding_rope_gb300 import _build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return R.load_library()
+
+
+A = 0x1000000  # fake, aligned "device" addresses: never dereferenced on these paths
+INV, UNS = R.ROPE_ERR_INVALID_ARG, R.ROPE_ERR_UNSUPPORTED
+
+APPEND = dict(k=A, v=2 * A, kp=3 * A, vp=4 * A, table=5 * A, cu=6 * A, lens=7 * A, cos=8 * A,
+              sin=9 * A, pos=None, off=0, n=2, total=10, ks=128, vs=128, Hk=2, D=64, rd=64, layout=0,
+              page=16, n_pages=8, blocks=4, dtype=1, rows=64)
+
+
+def append_args(**over):
+    a = dict(APPEND, **over)
+    return [a[x] for x in ("k", "v", "kp", "vp", "table", "cu", "lens", "cos", "sin", "pos", "off",
+                           "n", "total", "ks", "vs", "Hk", "D", "rd", "layout", "page", "n_pages",
+                           "blocks", "dtype", "rows")] + [None]
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=0), UNS), (dict(dtype=3), UNS), (dict(layout=2), UNS), (dict(D=96, ks=192, vs=192), UNS),
+    (dict(rd=8), UNS), (dict(rd=40), UNS), (dict(rd=80), UNS), (dict(page=8), UNS),
+    (dict(page=48), UNS), (dict(page=256), UNS), (dict(ks=132), UNS), (dict(vs=130), UNS),
+    (dict(k=A + 8), UNS), (dict(vp=4 * A + 2), UNS), (dict(cos=8 * A + 4), UNS),
+    (dict(n=-1), INV), (dict(total=-1), INV), (dict(total=1 << 31), INV), (dict(Hk=-1), INV),
+    (dict(ks=120), INV), (dict(vs=0), INV), (dict(off=-1), INV), (dict(rows=0), INV),
+    (dict(n_pages=0), INV), (dict(blocks=0), INV), (dict(k=None), INV), (dict(v=None), INV),
+    (dict(kp=None), INV), (dict(table=None), INV), (dict(cu=None), INV), (dict(lens=None), INV),
+    (dict(sin=None), INV), (dict(table=5 * A + 2), INV),
+    (dict(vp=3 * A + 64), INV),                 # the pools overlap
+    (dict(k=3 * A + 128), INV),                 # a pool overlaps its input
+    (dict(cu=4 * A + 64), INV),                 # a pool overlaps the offsets
+    (dict(n_pages=1 << 31), INV), (dict(n=1 << 30, blocks=1 << 40), INV),
+])
+def test_append_refuses(lib, over, status):
+    assert lib.rope_cache_append(*append_args(**over)) == status
+
+
+@pytest.mark.parametrize("over", [dict(total=0, k=None, v=None), dict(n=0, table=None, cu=None, lens=None),
+                                  dict(Hk=0, kp=None, vp=None)])
+def test_append_of_nothing(lib, over):
+    assert lib.rope_cache_append(*append_args(**over)) == R.ROPE_OK
+
+
+def test_status_name(lib):
+    assert R.rope_status_string(R.ROPE_ERR_BAD_INDEX) == "ROPE_ERR_BAD_INDEX"
+
+
+def test_python_refuses_cpu_tensors():
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    pool = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
+    i = torch.zeros(3, dtype=torch.int32)
+    t = torch.zeros(8, 32)
+    with pytest.raises(ValueError, match="CUDA"):
+        R.cache_append(x, x, pool, pool, i[:2].view(2, 1), i, i[:2], t, t)
