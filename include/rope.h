@@ -399,6 +399,55 @@ rope_status rope_cache_append(const void *k, const void *v, void *k_pages, void 
                               int64_t table_rows, void *stream);
 
 /*
+ * rope_attention_packed_fwd -- attention with rotary Q/K over packed
+ * sequences of different lengths (whole prompts, or their last tokens).
+ *
+ *   o_i = softmax(scale * rot(q_i) rot(K_b)^T + mask) V_b
+ *
+ * for the tokens i of sequence b, whose queries are tokens cu_seqlens_q[b] ..
+ * and whose keys are tokens cu_seqlens_k[b] .. of their tensors.  With causal,
+ * query i of Lq sees key j of Lk when j <= i + Lk - Lq; a query that sees no
+ * key gets zeros.
+ * q: device [total_q, Hq, D], token stride q_stride; k, v: device [total_k,
+ *    Hk, D], token strides k_stride, v_stride; o: device [total_q, Hq, D],
+ *    dense, written (rows of no sequence are not).  Hq is a multiple of Hk.
+ * cu_seqlens_q, cu_seqlens_k: device int32[n_seqs + 1]; they may be the same.
+ * pos_q, pos_k: device int32[total_q], int32[total_k] or NULL.  NULL: a
+ *    token's table row is its index among its sequence's queries (keys).
+ *    -1: not rotated; other rows outside the table are not rotated and raise
+ *    the flag.
+ * causal, softmax_scale: as rope_attention_fwd.
+ * workspace: device, 128-byte aligned, at least
+ *    rope_attention_packed_workspace(...) bytes; overwritten (the rotated
+ *    keys, the list of work and the copy engine's maps).
+ * A sequence offset out of range or out of order (ROPE_ERR_BAD_INDEX), or a
+ *    sequence longer than the table when its positions are NULL
+ *    (ROPE_ERR_POS_OUT_OF_RANGE), is found on the device: the flag is raised
+ *    and nothing of o is written.
+ * Arithmetic: as rope_attention_fwd.
+ * Errors: ROPE_ERR_UNSUPPORTED for other dtypes, D, rotary_dim, layouts,
+ *    strides not a multiple of 8 or unaligned pointers; ROPE_ERR_INVALID_ARG
+ *    for bad sizes, token strides below a token's row, null pointers, a
+ *    workspace too small, o or the workspace overlapping another argument;
+ *    ROPE_ERR_CUDA if a launch fails.  Asynchronous on `stream`; a wait inside
+ *    the kernel is bounded as in rope_attention_fwd.
+ */
+rope_status rope_attention_packed_fwd(const void *q, const void *k, const void *v, void *o,
+                                      const float *cos, const float *sin, const int32_t *pos_q,
+                                      const int32_t *pos_k, const int32_t *cu_seqlens_q,
+                                      const int32_t *cu_seqlens_k, int64_t n_seqs, int64_t total_q,
+                                      int64_t total_k, int64_t q_stride, int64_t k_stride,
+                                      int64_t v_stride, int32_t Hq, int32_t Hk, int32_t D,
+                                      int32_t rotary_dim, int32_t layout, int32_t causal,
+                                      float softmax_scale, int32_t dtype, int64_t table_rows,
+                                      void *workspace, int64_t workspace_bytes, void *stream);
+
+/* rope_attention_packed_workspace -- bytes of workspace for a call of these
+ * sizes (0 when there is nothing to do, -1 for sizes it does not take). */
+int64_t rope_attention_packed_workspace(int64_t n_seqs, int64_t total_q, int64_t total_k, int32_t Hq,
+                                        int32_t Hk, int32_t D);
+
+/*
  * rope_check_errors -- synchronise `stream`, then report and clear the
  * current device's error flag.
  * Returns ROPE_ERR_CUDA if the stream reports an error, else

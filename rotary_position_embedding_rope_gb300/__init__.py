@@ -49,9 +49,11 @@ __all__ = [
     "rope_attention_fwd_noalloc", "rope_check_errors", "rope_probe_wait_expiry",
     "rope_status_string", "rope_qk_kernel_variant", "rope_force_kernel_variant",
     "rope_tune_rotation_launch", "rope_cache_append",
+    "rope_attention_packed_fwd", "rope_attention_packed_workspace",
     # conveniences
     "build_tables", "build_tables_ex", "apply_qk", "apply_q", "apply_qk_xpos", "rotate_qk",
     "attention", "attention_workspace", "PreparedApply", "cache_append",
+    "attention_packed",
 ]
 
 (ROPE_OK, ROPE_ERR_INVALID_ARG, ROPE_ERR_UNSUPPORTED, ROPE_ERR_CUDA, ROPE_ERR_POS_OUT_OF_RANGE,
@@ -147,6 +149,11 @@ def load_library() -> ctypes.CDLL:
     lib.rope_cache_append.argtypes = [P] * 10 + [c.c_int64] * 5 + [c.c_int32] * 5 + \
         [c.c_int64, c.c_int64, c.c_int32, c.c_int64, P]
     lib.rope_cache_append.restype = c.c_int
+    lib.rope_attention_packed_fwd.argtypes = [P] * 10 + [c.c_int64] * 6 + [c.c_int32] * 6 + \
+        [c.c_float, c.c_int32, c.c_int64, P, c.c_int64, P]
+    lib.rope_attention_packed_fwd.restype = c.c_int
+    lib.rope_attention_packed_workspace.argtypes = [c.c_int64] * 3 + [c.c_int32] * 3
+    lib.rope_attention_packed_workspace.restype = c.c_int64
     _lib = lib
     return lib
 
@@ -629,6 +636,26 @@ def rope_cache_append(k, v, k_pages, v_pages, block_table, cu_seqlens, cache_len
     _check(st, "rope_cache_append")
 
 
+def rope_attention_packed_fwd(q, k, v, o, cos, sin, pos_q, pos_k, cu_seqlens_q, cu_seqlens_k, n_seqs,
+                              total_q, total_k, q_stride, k_stride, v_stride, Hq, Hk, D, rotary_dim,
+                              layout, causal, softmax_scale, dtype, table_rows, workspace,
+                              workspace_bytes, stream=None):
+    st = load_library().rope_attention_packed_fwd(
+        _addr(q, "q"), _addr(k, "k"), _addr(v, "v"), _addr(o, "o"), _addr(cos, "cos"),
+        _addr(sin, "sin"), _addr(pos_q, "pos_q"), _addr(pos_k, "pos_k"),
+        _addr(cu_seqlens_q, "cu_seqlens_q"), _addr(cu_seqlens_k, "cu_seqlens_k"), int(n_seqs),
+        int(total_q), int(total_k), int(q_stride), int(k_stride), int(v_stride), int(Hq), int(Hk),
+        int(D), int(rotary_dim), int(layout), int(causal), float(softmax_scale), int(dtype),
+        int(table_rows), _addr(workspace, "workspace"), int(workspace_bytes), _stream(stream))
+    _check(st, "rope_attention_packed_fwd")
+
+
+def rope_attention_packed_workspace(n_seqs, total_q, total_k, Hq, Hk, D) -> int:
+    """Bytes of workspace (-1 for sizes the call does not take)."""
+    return load_library().rope_attention_packed_workspace(int(n_seqs), int(total_q), int(total_k),
+                                                          int(Hq), int(Hk), int(D))
+
+
 class _Call:
     """One serving call: the device its tensors live on and the stream it runs
     on, with that device current while the library is called."""
@@ -692,6 +719,22 @@ class _Call:
         return (self.dense(k_pages, "k_pages", dtype), self.dense(v_pages, "v_pages", dtype),
                 *k_pages.shape)
 
+    def workspace(self, given, need, name):
+        """(address, bytes) of the call's workspace: the given tensor, or a new
+        one that stays alive until the call's stream is done with it."""
+        if need < 0:
+            raise RopeError(ROPE_ERR_INVALID_ARG, name)
+        if given is not None:
+            if given.device != self.device or not given.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor on %s" % self.device)
+            return given.data_ptr(), given.numel() * given.element_size()
+        if need == 0:
+            return None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        if self.stream != torch.cuda.current_stream(self.device).cuda_stream:
+            ws.record_stream(torch.cuda.ExternalStream(self.stream, self.device))
+        return ws.data_ptr(), need
+
     def run(self, fn, name, *args):
         if self.device.index == torch.cuda.current_device():
             st = fn(*args, self.stream)
@@ -742,3 +785,54 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
           c.dense(cache_lens, "cache_lens", i32, (n,)), ca, sa, c.dense(pos, "pos", i32, (T,)),
           pos_offset, n, T, ks, vs, Hk, D, rd, _LAYOUT_CODE[layout], page, n_pages, blocks, code,
           rows)
+
+
+def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                     cos: torch.Tensor, sin: torch.Tensor, cu_seqlens_k: torch.Tensor | None = None,
+                     pos_q: torch.Tensor | None = None, pos_k: torch.Tensor | None = None,
+                     rotary_dim: int | None = None, layout: str = "split_half", causal: bool = False,
+                     scale: float | None = None, out: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """softmax(scale * rot(q) rot(k)^T + mask) v for packed sequences of different lengths.
+
+    q: [Tq, Hq, D]; k, v: [Tk, Hk, D] (views with a token stride are taken as
+    they are); returns [Tq, Hq, D].  Sequence b's queries are tokens
+    cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1, its keys those of cu_seqlens_k
+    (None: the same); both int32 [n_seqs + 1].  With causal, the queries are
+    the last tokens of their sequence: query i of Lq sees the keys
+    j <= i + Lk - Lq.  A query that sees no key gets zeros; rows of ``out``
+    that belong to no sequence keep what they hold.
+    pos_q, pos_k: int32 [Tq], [Tk] table rows (-1 = not rotated), or None for
+    a token's index among its sequence's queries (keys).
+    workspace: None, or a uint8 tensor of rope_attention_packed_workspace(...)
+    bytes to use (128-byte aligned; its contents do not matter).
+    """
+    c = _Call(q, stream)
+    code = _type16(q, "attention_packed")
+    qa, qs = c.rows(q, "q", dtype=q.dtype)
+    Tq, Hq, D = q.shape
+    ka, ks = c.rows(k, "k", D=D, dtype=q.dtype)
+    Tk, Hk, _ = k.shape
+    va, vs = c.rows(v, "v", Hk, D, q.dtype)
+    if v.shape[0] != Tk:
+        raise ValueError("k and v must have the same tokens")
+    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 1:
+        raise ValueError("cu_seqlens_q must be int32 [n_seqs + 1]")
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    n = cu_seqlens_q.shape[0] - 1
+    ca, sa, rd, rows = c.tables(cos, sin, rotary_dim)
+    if out is None:
+        out = torch.empty((Tq, Hq, D), dtype=q.dtype, device=q.device)
+        if c.stream != torch.cuda.current_stream(c.device).cuda_stream:
+            out.record_stream(torch.cuda.ExternalStream(c.stream, c.device))
+    i32 = torch.int32
+    lib = load_library()
+    ws, ws_bytes = c.workspace(workspace, lib.rope_attention_packed_workspace(n, Tq, Tk, Hq, Hk, D),
+                               "rope_attention_packed_workspace")
+    c.run(lib.rope_attention_packed_fwd, "rope_attention_packed_fwd", qa, ka, va,
+          c.dense(out, "out", q.dtype, (Tq, Hq, D)), ca, sa, c.dense(pos_q, "pos_q", i32, (Tq,)),
+          c.dense(pos_k, "pos_k", i32, (Tk,)), c.dense(cu_seqlens_q, "cu_seqlens_q", i32, (n + 1,)),
+          c.dense(cu_seqlens_k, "cu_seqlens_k", i32, (n + 1,)), n, Tq, Tk, qs, ks, vs, Hq, Hk, D, rd,
+          _LAYOUT_CODE[layout], int(causal), -1.0 if scale is None else scale, code, rows, ws, ws_bytes)
+    return out

@@ -60,10 +60,15 @@ struct PackedLayout {
     int64_t entries, maps, keys;     // byte offsets
     int64_t bytes;
 };
+// Query heads of one group that share a tile: the largest power of two, up to
+// 16, that divides Hq / Hk.
 int32_t packed_group_heads(int32_t Hq, int32_t Hk);
+// False when a size overflows.
 bool packed_layout(int64_t n_seqs, int64_t total_q, int64_t total_k, int32_t Hq, int32_t Hk,
                    int32_t D, PackedLayout *out);
-cudaError_t launch_attention_packed(const PackedArgs &a, int32_t D, int32_t layout, int32_t dtype,
-                                    cudaStream_t st);
+cudaError_t launch_packed_bf16(const PackedArgs &c, const PackedLayout &lay, int32_t D, int32_t layout,
+                               cudaStream_t st);
+cudaError_t launch_packed_f16(const PackedArgs &c, const PackedLayout &lay, int32_t D, int32_t layout,
+                              cudaStream_t st);
 
 }  // namespace rope

@@ -77,7 +77,37 @@ int32_t page_shift(int32_t page_size)
 
 constexpr int64_t kMaxInt32 = 0x7fffffff;
 
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
 }  // namespace
+
+int32_t packed_group_heads(int32_t Hq, int32_t Hk)
+{
+    int32_t gp = 1;
+    while (gp < 16 && Hq / Hk % (2 * gp) == 0)
+        gp *= 2;
+    return gp;
+}
+
+bool packed_layout(int64_t n_seqs, int64_t total_q, int64_t total_k, int32_t Hq, int32_t Hk,
+                   int32_t D, PackedLayout *out)
+{
+    // a sequence of n tokens has at most n / tokens + 1 query tiles, and the
+    // empty ones have none
+    const int64_t tokens = 256 / packed_group_heads(Hq, Hk);
+    out->tiles = total_q / tokens + (n_seqs < total_q ? n_seqs : total_q);
+    const int64_t entries = product({out->tiles, 32}), maps = product({n_seqs, 4 * 128});
+    const int64_t keys = product({total_k, Hk, D, 2});
+    if (entries < 0 || maps < 0 || keys < 0 || entries > (1ll << 60) || maps > (1ll << 60) ||
+        keys > (1ll << 60))
+        return false;
+    out->entries = 128;
+    out->maps = round_up(out->entries + entries, 128);
+    out->keys = out->maps + maps;
+    out->bytes = out->keys + keys;
+    return true;
+}
+
 }  // namespace rope
 
 using namespace rope;
@@ -146,6 +176,92 @@ rope_status rope_cache_append(const void *k, const void *v, void *k_pages, void 
     return launch_cache_append(a, D, layout, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? ROPE_OK
                : ROPE_ERR_CUDA;
+}
+
+int64_t rope_attention_packed_workspace(int64_t n_seqs, int64_t total_q, int64_t total_k, int32_t Hq,
+                                        int32_t Hk, int32_t D)
+{
+    PackedLayout lay;
+    if (n_seqs < 0 || n_seqs >= kMaxInt32 || total_q < 0 || total_q > kMaxInt32 || total_k < 0 ||
+        total_k > kMaxInt32 || Hq < 0 || Hk < 0 || (D != 64 && D != 128))
+        return -1;
+    if (n_seqs == 0 || total_q == 0 || Hq == 0)
+        return 0;
+    if (Hk == 0 || Hq % Hk != 0 || !packed_layout(n_seqs, total_q, total_k, Hq, Hk, D, &lay))
+        return -1;
+    return lay.bytes;
+}
+
+rope_status rope_attention_packed_fwd(const void *q, const void *k, const void *v, void *o,
+                                      const float *cos, const float *sin, const int32_t *pos_q,
+                                      const int32_t *pos_k, const int32_t *cu_seqlens_q,
+                                      const int32_t *cu_seqlens_k, int64_t n_seqs, int64_t total_q,
+                                      int64_t total_k, int64_t q_stride, int64_t k_stride,
+                                      int64_t v_stride, int32_t Hq, int32_t Hk, int32_t D,
+                                      int32_t rotary_dim, int32_t layout, int32_t causal,
+                                      float softmax_scale, int32_t dtype, int64_t table_rows,
+                                      void *workspace, int64_t workspace_bytes, void *stream)
+{
+    rope_status st = check_shape(dtype, layout, D, rotary_dim);
+    if (st != ROPE_OK)
+        return st;
+    if ((causal != 0 && causal != 1) || softmax_scale != softmax_scale || n_seqs < 0 ||
+        n_seqs >= kMaxInt32 || total_q < 0 || total_q > kMaxInt32 || total_k < 0 ||
+        total_k > kMaxInt32 || Hq < 0 || Hk < 0 || table_rows < 0 || workspace_bytes < 0)
+        return ROPE_ERR_INVALID_ARG;
+    if (Hq > 0 && (Hk == 0 || Hq % Hk != 0))
+        return ROPE_ERR_INVALID_ARG;
+    const int64_t qrow = (int64_t)Hq * D, krow = (int64_t)Hk * D;
+    if (q_stride < qrow || k_stride < krow || v_stride < krow)
+        return ROPE_ERR_INVALID_ARG;
+    const int64_t qb = view_bytes(total_q, q_stride, qrow), kb = view_bytes(total_k, k_stride, krow),
+                  vb = view_bytes(total_k, v_stride, krow), ob = product({total_q, qrow, 2}),
+                  tab = product({table_rows, rotary_dim / 2, 4});
+    if (qb < 0 || kb < 0 || vb < 0 || ob < 0 || tab < 0)
+        return ROPE_ERR_INVALID_ARG;
+    if (total_q == 0 || n_seqs == 0 || Hq == 0)
+        return ROPE_OK;                                  // no output rows
+    if (!q || !o || !cos || !sin || !cu_seqlens_q || !cu_seqlens_k || (total_k > 0 && (!k || !v)) ||
+        table_rows < 1)
+        return ROPE_ERR_INVALID_ARG;
+    PackedLayout lay;
+    if (!packed_layout(n_seqs, total_q, total_k, Hq, Hk, D, &lay) || !workspace ||
+        workspace_bytes < lay.bytes)
+        return ROPE_ERR_INVALID_ARG;
+    if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(q, 16) ||
+        !aligned(o, 16) || !aligned(cos, 16) || !aligned(sin, 16) || !aligned(workspace, 128) ||
+        (total_k > 0 && (!aligned(k, 16) || !aligned(v, 16))))
+        return ROPE_ERR_UNSUPPORTED;
+    if (!aligned(pos_q, 4) || !aligned(pos_k, 4) || !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4))
+        return ROPE_ERR_INVALID_ARG;
+    const Range outs[2] = {{o, ob}, {workspace, lay.bytes}};
+    const Range ins[9] = {{q, qb}, {k, kb}, {v, vb}, {cos, tab}, {sin, tab}, {pos_q, 4 * total_q},
+                          {pos_k, 4 * total_k}, {cu_seqlens_q, 4 * (n_seqs + 1)},
+                          {cu_seqlens_k, 4 * (n_seqs + 1)}};
+    if (overlap(outs[0], outs[1]))
+        return ROPE_ERR_INVALID_ARG;
+    for (const Range &out : outs)
+        for (const Range &in : ins)
+            if (overlap(out, in))
+                return ROPE_ERR_INVALID_ARG;
+    PackedArgs a;
+    std::memset(&a, 0, sizeof a);
+    RowsArgs &r = a.keys;
+    r.k = k; r.v = v; r.k_stride = k_stride; r.v_stride = v_stride;
+    r.cu = cu_seqlens_k; r.pos = pos_k; r.cos = cos; r.sin = sin;
+    r.table_rows = table_rows; r.total = total_k;
+    r.n_seqs = (int32_t)n_seqs; r.Hk = Hk; r.rotary_dim = rotary_dim;
+    if (device_flag(&r.flag) != cudaSuccess)
+        return ROPE_ERR_CUDA;
+    a.q = q; a.q_stride = q_stride; a.o = o;
+    a.cu_q = cu_seqlens_q; a.pos_q = pos_q; a.total_q = total_q;
+    a.Hq = Hq; a.causal = causal; a.workspace = workspace;
+    const double scale = softmax_scale > 0.0f ? softmax_scale : 1.0 / std::sqrt((double)D);
+    a.scale_log2 = (float)(scale * 1.4426950408889634);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == ROPE_BF16 ? launch_packed_bf16(a, lay, D, layout, s)
+                                             : launch_packed_f16(a, lay, D, layout, s);
+    return e == cudaSuccess ? ROPE_OK : ROPE_ERR_CUDA;
 }
 
 }  // extern "C"

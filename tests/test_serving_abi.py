@@ -64,3 +64,46 @@ def test_python_refuses_cpu_tensors():
     t = torch.zeros(8, 32)
     with pytest.raises(ValueError, match="CUDA"):
         R.cache_append(x, x, pool, pool, i[:2].view(2, 1), i, i[:2], t, t)
+
+
+PACKED = dict(q=A, k=2 * A, v=3 * A, o=4 * A, cos=5 * A, sin=6 * A, pq=None, pk=None, cuq=7 * A, cuk=8 * A,
+              n=2, tq=10, tk=12, qs=512, ks=256, vs=256, Hq=4, Hk=2, D=128, rd=128, layout=0, causal=1, scale=-1.0,
+              dtype=1, rows=64, ws=9 * A, wsb=1 << 20)
+
+
+def packed_args(**over):
+    a = dict(PACKED, **over)
+    return [a[x] for x in ("q", "k", "v", "o", "cos", "sin", "pq", "pk", "cuq", "cuk", "n", "tq", "tk", "qs", "ks",
+                           "vs", "Hq", "Hk", "D", "rd", "layout", "causal", "scale", "dtype", "rows", "ws",
+                           "wsb")] + [None]
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=0), UNS), (dict(dtype=3), UNS), (dict(layout=2), UNS), (dict(D=96), UNS), (dict(rd=8), UNS),
+    (dict(rd=136), UNS), (dict(qs=516), UNS), (dict(ks=260), UNS), (dict(vs=258), UNS), (dict(q=A + 8), UNS),
+    (dict(o=4 * A + 8), UNS), (dict(cos=5 * A + 4), UNS), (dict(ws=9 * A + 64), UNS),
+    (dict(causal=2), INV), (dict(scale=float("nan")), INV), (dict(n=-1), INV), (dict(tq=-1), INV),
+    (dict(tk=1 << 31), INV), (dict(Hq=3, qs=384), INV), (dict(Hk=0, ks=0, vs=0), INV), (dict(Hk=-1), INV),
+    (dict(qs=504), INV), (dict(ks=128), INV), (dict(rows=0), INV), (dict(rows=-1), INV), (dict(q=None), INV),
+    (dict(k=None), INV), (dict(v=None), INV), (dict(o=None), INV), (dict(cuq=None), INV), (dict(cuk=None), INV),
+    (dict(ws=None), INV), (dict(wsb=100), INV), (dict(wsb=-1), INV), (dict(pq=7 * A + 2), INV),
+    (dict(o=A + 1024), INV), (dict(o=2 * A), INV), (dict(ws=A), INV), (dict(ws=4 * A), INV), (dict(o=7 * A), INV),
+])
+def test_packed_refuses(lib, over, status):
+    assert lib.rope_attention_packed_fwd(*packed_args(**over)) == status
+
+
+@pytest.mark.parametrize("over", [dict(tq=0, q=None, o=None), dict(n=0, cuq=None, cuk=None),
+                                  dict(Hq=0, Hk=0, qs=0, ks=0, vs=0, q=None, k=None, v=None, o=None)])
+def test_packed_of_nothing(lib, over):
+    assert lib.rope_attention_packed_fwd(*packed_args(ws=None, wsb=0, **over)) == R.ROPE_OK
+
+
+def test_packed_workspace(lib):
+    ws = lib.rope_attention_packed_workspace
+    need = ws(2, 10, 12, 4, 2, 128)
+    assert need >= 2 * 4 * 128 + 12 * 2 * 128 * 2 and need % 128 == 0
+    assert lib.rope_attention_packed_fwd(*packed_args(wsb=need - 1)) == INV
+    assert ws(0, 10, 12, 4, 2, 128) == ws(2, 0, 12, 4, 2, 128) == ws(2, 10, 12, 0, 0, 128) == 0
+    assert ws(-1, 10, 12, 4, 2, 128) == ws(2, 10, 12, 4, 3, 128) == ws(2, 10, 12, 4, 2, 96) == -1
+    assert ws(2, 10, 1 << 31, 4, 2, 128) == -1
