@@ -26,15 +26,10 @@
 // causal diagonal spans fewer tokens.  A Q or O box is 64 features x GP heads
 // x tokens.
 //
-// The cluster's roles, barriers and phases are those of rope_attn_2sm_kernel
-// (rope_attention.cuh): 224 threads a CTA, warps 0-3 the softmax of its 128
-// rows, the leader's warps 4 and 5 the S = Q K^T and O += P V products of both
-// CTAs, warp 6 the CTA's copies; three S buffers in TMEM, released by the
-// products that read P from them.  What differs:
-//   * the work list and the maps come from the workspace;
-//   * warp 6 also fetches the cos/sin rows of the tile's tokens, one bulk copy
-//     per row at any position (pos_q), into the same barrier as the query tile;
-//   * D = 64 runs here too (V halves of 32 features, 64-byte swizzle).
+// The products, their TMEM buffers and the stages are those of
+// rope_attn_2sm_kernel (rope_attention.cuh): M = 256 over the pair, three S
+// buffers released by the products that read P from them.  D = 64 runs here too
+// (V halves of 32 features, 64-byte swizzle).
 #pragma once
 
 #include "rope_attention.cuh"
@@ -67,16 +62,6 @@ struct PackedPlan {
     int64_t step[kPackedMaps];                 // bytes from token to token
     int32_t *flag;
     int32_t map_blocks;                        // grid: the planner, the maps, then the rotation
-};
-
-struct PackedKernelArgs {
-    AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, causal, flag
-    const PackedEntry *entries;
-    const int32_t *n_entries;
-    const CUtensorMap *maps;
-    const int32_t *pos_q;
-    int32_t head_units;                        // Hq / GP
-    int32_t units_per_kv;                      // (Hq / Hk) / GP
 };
 
 struct PackedMapTemplates {
@@ -245,6 +230,8 @@ __global__ void __launch_bounds__(kPackedPrepThreads)
     __shared__ __align__(128) CUtensorMap buf[kPackedPrepThreads / 32];
     __shared__ int32_t bins[kPackedBins];      // the planner's; else the first offsets
     const int tid = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();                             // the attention's CTAs may set up beside this
     if (blockIdx.x == 0) {
         packed_list(p, bins);
         return;
@@ -325,26 +312,36 @@ __global__ void __launch_bounds__(kPackedPrepThreads)
 
 // ---------------------------------------------------------------------------
 // 2. the attention
+//
+// 384 threads a CTA, three warpgroups:
+//   warps 0-3   the softmax of the CTA's 128 rows (thread t = row t), nothing
+//               else: a unit's first tile follows the previous unit's last;
+//   warps 4-7   the helpers: they rotate the next unit's query tile in the
+//               other of two query buffers and write the finished unit's output,
+//               both while the softmax warps are busy with key tiles;
+//   warps 8-11  the leader's S = Q K^T issue, its O += P V issue, the CTA's
+//               copies, and one idle warp.
+// The softmax holds a row's 128 scores in registers, so the warpgroups trade
+// registers (setmaxnreg): 240 / 144 / 104 of the 168 they start with.
+//
+// With query rotation and epilogue on the softmax warps' path (their loop then
+// ran tiles, rotation, epilogue in turn, 224 threads a CTA) eight causal prompts
+// of 16.4k tokens in all, Hq 32, Hk 8, D 128 took 384 us in this kernel; with
+// the helpers 336 us (0.383 TFLOP of visible pairs: 1140 TFLOP/s).
 
-// Shared memory of a CTA: the query tile, the stages of key and value halves,
-// the cos and the sin rows of the tile's tokens, the output tile.  A token's
-// table row of 2 * rotary_dim bytes sits at packed_table_offset: 16 bytes of
-// padding after every second row spread the rows over the banks (a full row
-// of padding each would not fit the 227 KB with 128 tokens a tile).
+constexpr int kPackedThreads = 384;
+constexpr int kPackedSIssueWarp = 8, kPackedPVIssueWarp = 9, kPackedTmaWarp = 10;
 constexpr int kPackedStages = k2Stages;
-__host__ __device__ constexpr uint32_t packed_table_offset(uint32_t t, uint32_t row_bytes)
-{
-    return t * row_bytes + (t >> 1) * 16;
-}
+constexpr int kPackedStats = 4;                // units whose row statistics are kept
 template <int D>
-constexpr uint32_t kPackedTile = kAttnRows * D * 2;
+static constexpr uint32_t kPackedTile = kAttnRows * D * 2;
 template <int D>
-constexpr uint32_t kPackedHalf = 64 * D * 2;   // 64 keys of D features, or 128 of D / 2
+static constexpr uint32_t kPackedHalf = 64 * D * 2;   // 64 keys of D features, or 128 of D / 2
+// two query tiles, the stages of key and value halves, the output tile, the
+// row statistics (max and sum)
 template <int D>
-constexpr uint32_t kPackedTable = packed_table_offset(kAttnRows, 2 * D);
-template <int D>
-constexpr uint32_t kPackedSmem = 2 * kPackedTile<D> + kPackedStages * 2 * kPackedHalf<D> +
-                                 2 * kPackedTable<D>;
+static constexpr uint32_t kPackedSmem = 3 * kPackedTile<D> + kPackedStages * 2 * kPackedHalf<D> +
+                                        kPackedStats * kAttnRows * 8;
 
 // V's MN-major operand: D = 128: 64 features x 128 keys, 128-byte swizzle;
 // D = 64: 32 features x 128 keys, 64-byte swizzle (descriptor layout 4), 8-row
@@ -356,92 +353,148 @@ __device__ __forceinline__ uint64_t packed_v_desc(uint32_t addr, int kk)
                     : umma_desc(addr + kk * 1024u, 64u * 128u, 512u, 4u);
 }
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(attn_smem_u32(dst)), "l"(src), "r"(bytes), "r"(attn_smem_u32(bar))
-                 : "memory");
-}
-
 // A map written by the prepare kernel, before this thread's first copy with it.
 __device__ __forceinline__ void acquire_map(const CUtensorMap *m)
 {
     asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
 }
 
-// Rotates the query tile in place: rows r = token * GP + head, table rows of
-// the tokens in sC / sS.  Tokens past Lq hold zeros, tokens that are not
-// rotated (position -1 or out of range) have no table row.
-template <typename T, int LAYOUT, int NF>
-__device__ __forceinline__ void rotate_packed_tile(uint8_t *sQ, const uint8_t *sC, const uint8_t *sS,
-                                                   int32_t tok0, int32_t Lq, int lg,
-                                                   const int32_t *pos, const AttnArgs &a, int tid)
+// One box of a key or value half into this CTA's stage; its bytes count on the
+// leader's barrier.
+__device__ __forceinline__ void load_half_box(uint8_t *dst, const CUtensorMap *map, int x, int y, int z,
+                                              uint64_t *bar, uint32_t rank)
 {
+    if (rank == 0)
+        tma_load_3d(dst, map, x, y, z, bar);
+    else
+        tma_load_3d_to_leader(dst, map, x, y, z, peer_addr(bar, 0));
+}
+
+// One unit of work of a cluster: the rows (token, head) of tokens tok0 .. and
+// heads head0 .. head0 + GP - 1 against the key tiles first .. first + n_tiles - 1
+// of key head kv.
+struct PackedUnit {
+    int32_t seq, tok0, tokens;                 // tokens: of the sequence (or the batch)
+    int32_t q_start;                           // the sequence's first token
+    int32_t first, n_tiles, n_keys;            // n_keys: of the sequence (or the prefix)
+    int32_t head0, kv, split;
+};
+
+// Where the units come from and where K and V lie.  PackedSource: the list and
+// the maps the prepare kernel wrote; rows end in bf16 / fp16 outputs.
+struct PackedSource {
+    static constexpr bool kPrefix = false;
+    AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, causal, flag
+    const PackedEntry *entries;
+    const int32_t *n_entries;
+    const CUtensorMap *maps;
+    const int32_t *pos_q;
+    int32_t head_units;                        // Hq / GP
+    int32_t units_per_kv;                      // (Hq / Hk) / GP
+
+    __device__ __forceinline__ int64_t units() const { return (int64_t)__ldg(n_entries) * head_units; }
+    __device__ __forceinline__ PackedUnit unit(int64_t L, int lg) const
+    {
+        const int64_t i = L / head_units;
+        const int32_t hu = (int32_t)(L - i * head_units);
+        const int4 x = __ldg(reinterpret_cast<const int4 *>(entries + i));
+        const int2 y = __ldg(reinterpret_cast<const int2 *>(entries + i) + 2);
+        PackedUnit u;
+        u.seq = x.x; u.tok0 = x.y; u.tokens = x.z; u.n_keys = x.w;
+        u.q_start = y.x; u.n_tiles = y.y; u.first = 0; u.split = 0;
+        u.head0 = hu << lg;
+        u.kv = hu / units_per_kv;
+        return u;
+    }
+    __device__ __forceinline__ int32_t tiles(int64_t L) const
+    {
+        return __ldg(&entries[L / head_units].n_tiles);
+    }
+    // table row of token t of the unit's sequence (-1: not rotated)
+    __device__ __forceinline__ int64_t table_row(const PackedUnit &u, int32_t t) const
+    {
+        return attn_row(pos_q != nullptr ? pos_q + u.q_start : nullptr, t, a.table_rows, a.flag);
+    }
+    // this CTA's half of key tile kt (64 keys) and of value tile kt (D / 2 features)
+    template <int D>
+    __device__ __forceinline__ void load_keys(const PackedUnit &u, int32_t kt, uint8_t *dst, uint64_t *bar,
+                                              uint32_t rank, int lane) const
+    {
+        if (lane < D / 64)
+            load_half_box(dst + lane * 8192, maps + (int64_t)u.seq * kPackedMaps, lane * 64,
+                          kt * kAttnKeys + 64 * (int)rank, u.kv, bar, rank);
+    }
+    template <int D>
+    __device__ __forceinline__ void load_values(const PackedUnit &u, int32_t kt, uint8_t *dst,
+                                                uint64_t *bar, uint32_t rank, int lane) const
+    {
+        if (lane == 0)
+            load_half_box(dst, maps + (int64_t)u.seq * kPackedMaps + 1, D / 2 * (int)rank, kt * kAttnKeys,
+                          u.kv, bar, rank);
+    }
+};
+
+// Rotates one query tile in place (rows r = token * GP + head; tokens past the
+// sequence's end hold zeros): a thread per row, its table row read from global
+// memory.  The helpers run this beside the tile loop, so its latency is hidden.
+template <typename T, int LAYOUT>
+__device__ __forceinline__ void rotate_packed_row(uint8_t *sQ, int64_t trow, const AttnArgs &a, int r)
+{
+    if (trow < 0)
+        return;
     constexpr int NQ = LAYOUT == 0 ? 2 : 1;
     const int rd = a.rotary_dim, h8 = rd / 16;
     const int per_row = LAYOUT == 0 ? rd / 16 : rd / 8;
-    const int tok = tid >> lg;                 // a thread owns one row of the tile
-    bool rot = tok0 + tok < Lq;
-    if (rot && pos != nullptr) {
-        const int32_t r = __ldg(pos + tok0 + tok);
-        rot = r >= 0 && r < a.table_rows;
-    }
-    if (!rot)
-        return;
-    const uint8_t *c0 = sC + packed_table_offset(tok, 2 * rd), *s0 = sS + packed_table_offset(tok, 2 * rd);
-#pragma unroll 1
-    for (int p = 0; p < per_row; p += NF) {
-        KeyItem it[NF];
+    const float4 *c = reinterpret_cast<const float4 *>(a.cos + trow * (rd / 2));
+    const float4 *s = reinterpret_cast<const float4 *>(a.sin + trow * (rd / 2));
+#pragma unroll 2
+    for (int p = 0; p < per_row; ++p) {
+        KeyItem it;
+        it.o1 = sw128(r, p);
+        it.o2 = sw128(r, p + h8);
+        it.rot = true;
+        it.x1 = *reinterpret_cast<const uint4 *>(sQ + it.o1);
+        if (LAYOUT == 0)
+            it.x2 = *reinterpret_cast<const uint4 *>(sQ + it.o2);
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            if (f == 0 || p + f < per_row) {
-                it[f].o1 = sw128(tid, p + f);
-                it[f].o2 = sw128(tid, p + f + h8);
-                it[f].rot = true;
-                it[f].x1 = *reinterpret_cast<const uint4 *>(sQ + it[f].o1);
-                if (LAYOUT == 0)
-                    it[f].x2 = *reinterpret_cast<const uint4 *>(sQ + it[f].o2);
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    const float4 c4 = *reinterpret_cast<const float4 *>(c0 + ((p + f) * NQ + q) * 16);
-                    const float4 s4 = *reinterpret_cast<const float4 *>(s0 + ((p + f) * NQ + q) * 16);
-                    it[f].cs[4 * q] = c4.x; it[f].cs[4 * q + 1] = c4.y;
-                    it[f].cs[4 * q + 2] = c4.z; it[f].cs[4 * q + 3] = c4.w;
-                    it[f].sn[4 * q] = s4.x; it[f].sn[4 * q + 1] = s4.y;
-                    it[f].sn[4 * q + 2] = s4.z; it[f].sn[4 * q + 3] = s4.w;
-                }
-            }
+        for (int q = 0; q < NQ; ++q) {
+            const float4 c4 = __ldg(c + p * NQ + q), s4 = __ldg(s + p * NQ + q);
+            it.cs[4 * q] = c4.x; it.cs[4 * q + 1] = c4.y; it.cs[4 * q + 2] = c4.z; it.cs[4 * q + 3] = c4.w;
+            it.sn[4 * q] = s4.x; it.sn[4 * q + 1] = s4.y; it.sn[4 * q + 2] = s4.z; it.sn[4 * q + 3] = s4.w;
         }
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-            if (f == 0 || p + f < per_row)
-                store_key_item<T, LAYOUT>(it[f], sQ);
+        store_key_item<T, LAYOUT>(it, sQ);
     }
 }
 
-template <typename T, int LAYOUT, int D>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(k2Threads, 1)
-    rope_attn_packed_kernel(const PackedKernelArgs g_args, const int lg)
+template <typename T, int LAYOUT, int D, typename Source>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
+    rope_attn_packed_kernel(const __grid_constant__ Source src, const int lg)
 {
     constexpr uint32_t kTile = kPackedTile<D>, kHalf = kPackedHalf<D>;
     constexpr uint32_t ab_format = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-    const AttnArgs &a = g_args.a;
+    const AttnArgs &a = src.a;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *sQ = smem;
-    uint8_t *sStages = sQ + kTile;
+    uint8_t *sStages = smem + 2 * kTile;
     uint8_t *sO = sStages + kPackedStages * 2 * kHalf;
-    uint8_t *sC = sO + kTile;
-    uint8_t *sS = sC + kPackedTable<D>;
-    auto sK = [&](int st) { return sStages + st * 2 * kHalf; };
-    auto sV = [&](int st) { return sStages + st * 2 * kHalf + kHalf; };
-    // as in rope_attn_2sm_kernel: both CTAs' key / value halves landed (leader
-    // only); S buffer ready, which releases key stage b (multicast); P ready
-    // (leader only, each row warp of both CTAs); O += P V done, which releases
-    // value stage b (multicast); query tile and table rows landed; both query
-    // tiles rotated (leader only); every MMA of an issuer finished.  Every
-    // parity wait is for the phase right after the last one known complete.
+    float2 *sStat = reinterpret_cast<float2 *>(sO + kTile);   // [kPackedStats][128] (max, sum)
+    auto sQ = [&](uint32_t b) { return smem + b * kTile; };
+    auto sK = [&](uint32_t st) { return sStages + st * 2 * kHalf; };
+    auto sV = [&](uint32_t st) { return sStages + st * 2 * kHalf + kHalf; };
+    // Per tile, modulo three (as in rope_attn_2sm_kernel): both CTAs' key /
+    // value halves landed (leader only); S ready, which releases the key stage
+    // (multicast); P ready (leader only, each softmax warp of both CTAs); O += P V
+    // done, which releases the value stage (multicast).
+    // Per unit with key tiles: query tile landed and rotated (leader only, each
+    // helper warp of both CTAs), per query buffer; its last S done (multicast),
+    // per query buffer; its last O += P V done (multicast); its row statistics
+    // written (each softmax warp), per statistics buffer; its O read (leader
+    // only, each helper warp of both CTAs).  At the end: all MMAs of an issuer.
+    // A parity wait is sound only for the phase right after the last one known
+    // complete: every barrier below is waited for phase by phase, or its next
+    // phase cannot complete before the waiter has moved on.
     __shared__ __align__(8) uint64_t bar_kfull[kPackedStages], bar_vfull[kPackedStages],
-        bar_s[k2SBufs], bar_p[k2SBufs], bar_o[k2SBufs], bar_q, bar_qr, bar_drain[2];
+        bar_s[k2SBufs], bar_p[k2SBufs], bar_o[k2SBufs], bar_q[2], bar_qr[2], bar_qfree[2], bar_odone,
+        bar_stat[kPackedStats], bar_ofree, bar_drain[2];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
@@ -449,36 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(k2Threads, 1)
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const bool leader = rank == 0;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool math = warp < 4;
     const int tokens = kAttnRows >> lg;            // of a CTA's tile
-    // The work units: unit L is entry L / head_units of the list (longest
-    // first) for head unit L mod head_units.  Cluster c takes unit
-    // r * clusters + c in even rounds r and r * clusters + clusters - 1 - c in
-    // odd ones, so a cluster that got the longer work of one round gets the
-    // shorter of the next.
-    const int64_t n_units = (int64_t)__ldg(g_args.n_entries) * g_args.head_units;
-    const int64_t clusters = gridDim.x >> 1, cid = blockIdx.x >> 1;
-    auto unit_at = [&](int64_t r) {
-        return r * clusters + ((r & 1) ? clusters - 1 - cid : cid);
-    };
-    struct Unit {
-        PackedEntry e;
-        int32_t head0, kv;
-    };
-    auto unit_work = [&](int64_t r) {
-        const int64_t L = unit_at(r);
-        const int64_t i = L / g_args.head_units;
-        const int32_t hu = (int32_t)(L - i * g_args.head_units);
-        Unit u;
-        const int4 x = __ldg(reinterpret_cast<const int4 *>(g_args.entries + i));
-        const int2 y = __ldg(reinterpret_cast<const int2 *>(g_args.entries + i) + 2);
-        u.e.seq = x.x; u.e.tok0 = x.y; u.e.Lq = x.z; u.e.Lk = x.w;
-        u.e.q_start = y.x; u.e.n_tiles = y.y;
-        u.head0 = hu << lg;
-        u.kv = hu / g_args.units_per_kv;
-        return u;
-    };
-    auto unit_tiles = [&](int64_t r) { return __ldg(&g_args.entries[unit_at(r) / g_args.head_units].n_tiles); };
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -487,19 +511,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(k2Threads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
+        constexpr uint32_t kBoth = 2 * (kAttnRows / 32);
         for (int s = 0; s < kPackedStages; ++s) {
             mbar_init(&bar_kfull[s], 1);
             mbar_init(&bar_vfull[s], 1);
         }
         for (int b = 0; b < k2SBufs; ++b) {
             mbar_init(&bar_s[b], 1);
-            mbar_init(&bar_p[b], 2 * (kAttnRows / 32));
+            mbar_init(&bar_p[b], kBoth);
             mbar_init(&bar_o[b], 1);
         }
-        mbar_init(&bar_q, 1);
-        mbar_init(&bar_qr, 2 * (kAttnRows / 32));
-        mbar_init(&bar_drain[0], 1);
-        mbar_init(&bar_drain[1], 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bar_q[b], 1);
+            mbar_init(&bar_qr[b], kBoth);
+            mbar_init(&bar_qfree[b], 1);
+            mbar_init(&bar_drain[b], 1);
+        }
+        for (int b = 0; b < kPackedStats; ++b)
+            mbar_init(&bar_stat[b], kAttnRows / 32);
+        mbar_init(&bar_odone, 1);
+        mbar_init(&bar_ofree, kBoth);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -513,30 +544,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(k2Threads, 1)
         *abort = 1;
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_abort), "r"(1) : "memory");
     };
+    // arrival of a warp on a barrier of the leader
+    auto arrive_leader = [&](uint64_t *bar) {
+        __syncwarp();
+        if (lane == 0) {
+            if (leader)
+                mbar_arrive(bar);
+            else
+                mbar_arrive_remote(peer_addr(bar, 0));
+        }
+    };
+    // what ran before this launch (the prepare kernel) is complete from here on
+    pdl_wait();
+    // The work units, longest first.  Cluster c takes unit r * clusters + c in
+    // even rounds r and r * clusters + clusters - 1 - c in odd ones, so a cluster
+    // that got the longer work of one round gets the shorter of the next.
+    const int64_t n_units = src.units();
+    const int64_t clusters = gridDim.x >> 1, cid = blockIdx.x >> 1;
+    auto unit_at = [&](int64_t r) {
+        return r * clusters + ((r & 1) ? clusters - 1 - cid : cid);
+    };
+    // the first round from r on that has a unit with key tiles; past the last
+    // unit: any round that fails unit_at(r) < n_units
+    auto next_round = [&](int64_t r) {
+        while (unit_at(r) < n_units && src.tiles(unit_at(r)) == 0)
+            ++r;
+        return r;
+    };
     bool ok = true;
 
-    if (math) {
-        // ---- the row block.  Pass r: the key tiles of unit r, then the query
-        // tile of unit r + 1, then the epilogue of unit r, so that the next
-        // unit's first S products run while the epilogue waits for the last
-        // O += P V.  The first pass (r = -1) only rotates the first query tile.
+    if (warp < 4) {
+        // ---- the softmax of this CTA's rows
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const uint32_t o_base = tmem + k2OCol + lanes;
         uint32_t sb = 0, s_ph = 0;                 // S buffer of this tile and its phase parity
         uint32_t ob = 0, o_ph = 0;                 // the same for the previous tile (O barriers)
-        uint32_t qn = 0;                           // units with key tiles so far
-        int32_t o_seq = -1;                        // the sequence whose O map was acquired
-        for (int64_t r = -1; ok && (r < 0 || unit_at(r) < n_units); ++r) {
-            const bool real = r >= 0;
-            int32_t n_tiles = 0, sk = 0;
-            int64_t qi = 0, shift = 0;
-            if (real) {
-                const Unit u = unit_work(r);
-                n_tiles = u.e.n_tiles;
-                sk = u.e.Lk;
-                shift = (int64_t)u.e.Lk - u.e.Lq;
-                qi = u.e.tok0 + (int)rank * tokens + (tid >> lg);
-            }
+        uint32_t stat = 0;
+        for (int64_t r = next_round(0); ok && unit_at(r) < n_units; r = next_round(r + 1)) {
+            const PackedUnit u = src.unit(unit_at(r), lg);
+            const int32_t n_tiles = u.n_tiles;
+            const int64_t shift = (int64_t)u.n_keys - u.tokens;
+            const int64_t qi = u.tok0 + (int)rank * tokens + (tid >> lg);
+            const int64_t k0 = (int64_t)u.first * kAttnKeys;
             float m_ref = -INFINITY, l_run = 0.0f;
             for (int32_t kt = 0; kt < n_tiles; ++kt) {
                 const uint32_t b = sb;
@@ -549,19 +599,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(k2Threads, 1)
                     o_ok = __all_sync(0xffffffffu, attn_wait(&bar_o[ob], o_ph, abort));
                     return o_ok;
                 };
-                softmax_tile<T, D, true, false>(tmem + (uint32_t)b * kAttnKeys + lanes, o_base, qi,
-                                                (int64_t)kt * kAttnKeys, shift, a, 0, kt > 0, m_ref,
-                                                l_run, o_ready, (int64_t)sk);
+                softmax_tile<T, D, true, false>(tmem + b * kAttnKeys + lanes, o_base, qi,
+                                                k0 + (int64_t)kt * kAttnKeys, shift, a, 0, kt > 0, m_ref,
+                                                l_run, o_ready, (int64_t)u.n_keys);
                 ok = o_ok;
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
-                    if (leader)
-                        mbar_arrive(&bar_p[b]);
-                    else
-                        mbar_arrive_remote(peer_addr(&bar_p[b], 0));
-                }
+                arrive_leader(&bar_p[b]);
                 ob = sb;
                 o_ph = s_ph;
                 if (++sb == k2SBufs) {
@@ -571,265 +615,278 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(k2Threads, 1)
                 if (!ok)
                     break;
             }
-            if (!ok)
-                break;
-            // the next unit's query tile, once it has landed: rotated in place
-            if (unit_at(r + 1) < n_units && unit_tiles(r + 1) > 0) {
-                const Unit n = unit_work(r + 1);
-                ok = __all_sync(0xffffffffu, attn_wait(&bar_q, qn & 1u, abort));
+            // (the buffer's previous unit, four before this one, is written: the
+            // last O += P V of the unit after it waited for its O to be read)
+            sStat[stat * kAttnRows + tid] = make_float2(m_ref, l_run);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bar_stat[stat]);
+            stat = (stat + 1) % kPackedStats;
+        }
+        if (!ok)
+            raise_abort();
+    } else if (warp < 8) {
+        // ---- the helpers.  Pass r: rotate the query tile of the unit after
+        // round r's, then write round r's output.  The first pass only rotates.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 144;");
+        const int row = tid - 128, wq = warp - 4;  // row of the tile = TMEM lane
+        const uint32_t o_base = tmem + k2OCol + ((uint32_t)(wq * 32) << 16);
+        uint32_t qn = 0, un = 0;                   // query tiles rotated, units with tiles written
+        int32_t o_seq = -1;                        // the sequence whose O map was acquired
+        int64_t rq = next_round(0);                // the round whose query tile is next
+        for (int64_t r = -1; ok && (r < 0 || unit_at(r) < n_units); ++r) {
+            // the next query tile, at most one ahead of the unit being written (a
+            // second one would wait for products that wait for this output)
+            if (unit_at(rq) < n_units && qn < un + 2) {
+                const PackedUnit u = src.unit(unit_at(rq), lg);
+                const uint32_t b = qn & 1u;
+                const int32_t tok = u.tok0 + (int)rank * tokens + (row >> lg);
+                const int64_t trow = tok < u.tokens ? src.table_row(u, tok) : -1;
+                ok = __all_sync(0xffffffffu, attn_wait(&bar_q[b], (qn >> 1) & 1u, abort));
                 if (!ok)
                     break;
-                rotate_packed_tile<T, LAYOUT, 2>(
-                    sQ, sC, sS, n.e.tok0 + (int)rank * tokens, n.e.Lq, lg,
-                    g_args.pos_q != nullptr ? g_args.pos_q + n.e.q_start : nullptr, a, tid);
+                rotate_packed_row<T, LAYOUT>(sQ(b), trow, a, row);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                arrive_leader(&bar_qr[b]);
+                ++qn;
+                rq = next_round(rq + 1);
+            }
+            if (r < 0)
+                continue;
+            const PackedUnit u = src.unit(unit_at(r), lg);
+            float2 stat = make_float2(-INFINITY, 0.0f);
+            if (u.n_tiles > 0) {
+                ok = __all_sync(0xffffffffu,
+                                attn_wait(&bar_stat[un % kPackedStats], (un / kPackedStats) & 1u, abort) &&
+                                    attn_wait(&bar_odone, un & 1u, abort));
+                if (!ok)
+                    break;
+                stat = sStat[(un % kPackedStats) * kAttnRows + row];
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            }
+            const int32_t y0 = u.tok0 + (int)rank * tokens + wq * (32 >> lg);
+            if constexpr (Source::kPrefix) {
+                src.template store_rows<D>(u, o_base, y0, lane, lg, stat);
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            } else {
+                // O / l of the warp's 32 rows, staged and stored by TMA (boxes
+                // of 64 features x GP heads x 32 / GP tokens; tokens past the
+                // sequence's end are not written, and a box that starts past
+                // it is not issued)
+                if (lane == 0)
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+                stage_o_row<T, D>(o_base, sO, row, u.n_tiles > 0, stat.y);
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_remote(peer_addr(&bar_qr, 0));
-                ++qn;
-            }
-            if (!real)
-                continue;
-            if (n_tiles > 0)
-                ok = __all_sync(0xffffffffu, attn_wait(&bar_o[ob], o_ph, abort));
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            if (!ok)
-                break;
-            // O / l of the warp's 32 rows, staged and stored by TMA (boxes of
-            // 64 features x GP heads x 32 / GP tokens; tokens past Lq are not
-            // written, and a box that starts past it is not issued)
-            if (lane == 0)
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            __syncwarp();
-            stage_o_row<T, D>(o_base, sO, tid, n_tiles > 0, l_run);
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            const Unit u = unit_work(r);
-            const int32_t y0 = u.e.tok0 + (int)rank * tokens + warp * (32 >> lg);
-            if (lane == 0 && y0 < u.e.Lq) {
-                const CUtensorMap *om = g_args.maps + (int64_t)u.e.seq * kPackedMaps + 3;
-                if (u.e.seq != o_seq)
-                    acquire_map(om);
-                o_seq = u.e.seq;
+                if (lane == 0 && y0 < u.tokens) {
+                    const CUtensorMap *om = src.maps + (int64_t)u.seq * kPackedMaps + 3;
+                    if (u.seq != o_seq)
+                        acquire_map(om);
+                    o_seq = u.seq;
 #pragma unroll
-                for (int bx = 0; bx < D / 64; ++bx)
-                    tma_store_3d(om, sO + bx * kBoxBytes + warp * 32 * 128, bx * 64, u.head0, y0);
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    for (int bx = 0; bx < D / 64; ++bx)
+                        tma_store_3d(om, sO + bx * kBoxBytes + wq * 32 * 128, bx * 64, u.head0, y0);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+            }
+            if (u.n_tiles > 0) {
+                arrive_leader(&bar_ofree);
+                ++un;
             }
         }
         drain_o_stores();
         if (!ok)
             raise_abort();
-    } else if (warp == k2SIssueWarp && leader) {
-        // ---- S = Q K^T for both CTAs into S buffer g mod 3
-        const uint32_t idesc = umma_idesc(256, kAttnKeys, ab_format, 0);
-        const uint32_t q_addr = attn_smem_u32(sQ);
-        uint32_t sb = 0, ph = 0, qn = 0;           // buffer (and stage) of tile g, its parity
-        bool first = true;                         // the first pass over the buffers
-        for (int64_t r = 0; ok && unit_at(r) < n_units; ++r) {
-            const int32_t n_tiles = unit_tiles(r);
-            if (n_tiles == 0)
-                continue;
-            ok = __all_sync(0xffffffffu, attn_wait(&bar_qr, qn & 1u, abort));
-            ++qn;
-            for (int32_t kt = 0; ok && kt < n_tiles; ++kt) {
-                ok = __all_sync(0xffffffffu, attn_wait(&bar_kfull[sb], ph, abort) &&
-                                                 (first || attn_wait(&bar_o[sb], ph ^ 1u, abort)));
-                if (!ok)
-                    break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                if (lane == 0) {
-                    const uint32_t k_addr = attn_smem_u32(sK(sb));
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if (warp == kPackedSIssueWarp && leader) {
+            // ---- S = Q K^T for both CTAs into S buffer g mod 3
+            const uint32_t idesc = umma_idesc(256, kAttnKeys, ab_format, 0);
+            uint32_t sb = 0, ph = 0, qn = 0;       // buffer (and stage) of tile g, its parity
+            bool first = true;                     // the first pass over the buffers
+            for (int64_t r = next_round(0); ok && unit_at(r) < n_units; r = next_round(r + 1)) {
+                const int32_t n_tiles = src.tiles(unit_at(r));
+                const uint32_t qb = qn & 1u;
+                const uint32_t q_addr = attn_smem_u32(sQ(qb));
+                ok = __all_sync(0xffffffffu, attn_wait(&bar_qr[qb], (qn >> 1) & 1u, abort));
+                ++qn;
+                for (int32_t kt = 0; ok && kt < n_tiles; ++kt) {
+                    ok = __all_sync(0xffffffffu, attn_wait(&bar_kfull[sb], ph, abort) &&
+                                                     (first || attn_wait(&bar_o[sb], ph ^ 1u, abort)));
+                    if (!ok)
+                        break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    if (lane == 0) {
+                        const uint32_t k_addr = attn_smem_u32(sK(sb));
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        umma2_ss(tmem + sb * kAttnKeys,
-                                 umma_desc(q_addr + (kk >> 2) * kBoxBytes + (kk & 3) * 32u, 16u,
-                                           1024u, kSwizzle128),
-                                 umma_desc(k_addr + (kk >> 2) * 8192u + (kk & 3) * 32u, 16u,
-                                           1024u, kSwizzle128),
-                                 idesc, kk > 0);
-                    umma2_commit(&bar_s[sb], 3);
-                }
-                __syncwarp();
-                if (++sb == k2SBufs) {
-                    sb = 0;
-                    ph ^= 1u;
-                    first = false;
-                }
-            }
-        }
-        if (lane == 0)
-            umma2_commit(&bar_drain[0], 1);
-        __syncwarp();
-        if (!__all_sync(0xffffffffu, attn_wait(&bar_drain[0], 0u)))
-            ok = false;
-        if (!ok)
-            raise_abort();
-    } else if (warp == k2PVIssueWarp && leader) {
-        // ---- O += P V for both CTAs once both P are in TMEM
-        const uint32_t idesc = umma_idesc(256, D, ab_format, 1);
-        uint32_t sb = 0, ph = 0;
-        for (int64_t r = 0; ok && unit_at(r) < n_units; ++r) {
-            const int32_t n_tiles = unit_tiles(r);
-            for (int32_t kt = 0; ok && kt < n_tiles; ++kt) {
-                ok = __all_sync(0xffffffffu, attn_wait(&bar_p[sb], ph, abort) &&
-                                                 attn_wait(&bar_vfull[sb], ph, abort));
-                if (!ok)
-                    break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                if (lane == 0) {
-                    const uint32_t v_addr = attn_smem_u32(sV(sb));
-#pragma unroll
-                    for (int kk = 0; kk < kAttnKeys / 16; ++kk)
-                        umma2_ts(tmem + k2OCol, tmem + sb * kAttnKeys + kk * 8,
-                                 packed_v_desc<D>(v_addr, kk), idesc, (kt > 0 || kk > 0) ? 1u : 0u);
-                    umma2_commit(&bar_o[sb], 3);
-                }
-                __syncwarp();
-                if (++sb == k2SBufs) {
-                    sb = 0;
-                    ph ^= 1u;
-                }
-            }
-        }
-        if (lane == 0)
-            umma2_commit(&bar_drain[1], 1);
-        __syncwarp();
-        if (!__all_sync(0xffffffffu, attn_wait(&bar_drain[1], 0u)))
-            ok = false;
-        if (!ok)
-            raise_abort();
-    } else if (warp == k2TmaWarp) {
-        // ---- per unit: the query tile and its tokens' table rows once the
-        // previous unit's last S has read the old one, then this CTA's halves
-        // of key and value tile g into stage g mod 3 once tile g - 3 released it
-        uint32_t sb = 0, ph = 0, qn = 0;
-        uint32_t pb = 0, p_ph = 0;                 // the previous tile's buffer and parity
-        bool first = true, any = false;
-        uint32_t k_ph[kPackedStages], v_ph[kPackedStages];   // parity of the last copy (2: none)
-#pragma unroll
-        for (int s = 0; s < kPackedStages; ++s)
-            k_ph[s] = v_ph[s] = 2;
-        int32_t seq = -1;
-        const uint32_t row_bytes = 2u * (uint32_t)a.rotary_dim;
-        for (int64_t r = 0; ok && unit_at(r) < n_units; ++r) {
-            const Unit u = unit_work(r);
-            const int32_t n_tiles = u.e.n_tiles;
-            if (n_tiles == 0)
-                continue;
-            const CUtensorMap *maps = g_args.maps + (int64_t)u.e.seq * kPackedMaps;
-            if (u.e.seq != seq) {
-                acquire_map(maps);
-                acquire_map(maps + 1);
-                acquire_map(maps + 2);
-                seq = u.e.seq;
-            }
-            // the table rows of this lane's tokens (-1: none)
-            const int32_t tok0 = u.e.tok0 + (int)rank * tokens;
-            int32_t trow[4];
-            uint32_t n_rows = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = lane + 32 * i;
-                trow[i] = -1;
-                if (t < tokens && tok0 + t < u.e.Lq) {
-                    trow[i] = tok0 + t;
-                    if (g_args.pos_q != nullptr) {
-                        trow[i] = __ldg(g_args.pos_q + u.e.q_start + tok0 + t);
-                        if (trow[i] < 0 || trow[i] >= a.table_rows) {
-                            if (trow[i] != -1)
-                                atomicOr(a.flag, kFlagPosition);
-                            trow[i] = -1;
-                        }
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            umma2_ss(tmem + sb * kAttnKeys,
+                                     umma_desc(q_addr + (kk >> 2) * kBoxBytes + (kk & 3) * 32u, 16u,
+                                               1024u, kSwizzle128),
+                                     umma_desc(k_addr + (kk >> 2) * 8192u + (kk & 3) * 32u, 16u,
+                                               1024u, kSwizzle128),
+                                     idesc, kk > 0);
+                        umma2_commit(&bar_s[sb], 3);
+                        if (kt + 1 == n_tiles)
+                            umma2_commit(&bar_qfree[qb], 3);
+                    }
+                    __syncwarp();
+                    if (++sb == k2SBufs) {
+                        sb = 0;
+                        ph ^= 1u;
+                        first = false;
                     }
                 }
-                n_rows += trow[i] >= 0 ? 1u : 0u;
             }
-            n_rows = __reduce_add_sync(0xffffffffu, n_rows);
-            if (any)
-                ok = __all_sync(0xffffffffu, attn_wait(&bar_s[pb], p_ph, abort));
-            if (!ok)
-                break;
             if (lane == 0)
-                mbar_expect_tx(&bar_q, kTile + n_rows * 2u * row_bytes);
+                umma2_commit(&bar_drain[0], 1);
             __syncwarp();
-            if (lane < D / 64)
-                tma_load_3d(sQ + lane * kBoxBytes, maps + 2, lane * 64, u.head0, tok0, &bar_q);
-            // (a box that starts past Lq arrives as zeros)
+            if (!__all_sync(0xffffffffu, attn_wait(&bar_drain[0], 0u)))
+                ok = false;
+        } else if (warp == kPackedPVIssueWarp && leader) {
+            // ---- O += P V for both CTAs once both P are in TMEM
+            const uint32_t idesc = umma_idesc(256, D, ab_format, 1);
+            uint32_t sb = 0, ph = 0, un = 0;
+            for (int64_t r = next_round(0); ok && unit_at(r) < n_units; r = next_round(r + 1)) {
+                const int32_t n_tiles = src.tiles(unit_at(r));
+                // both CTAs have read the previous unit's O
+                if (un > 0)
+                    ok = __all_sync(0xffffffffu, attn_wait(&bar_ofree, (un - 1) & 1u, abort));
+                ++un;
+                for (int32_t kt = 0; ok && kt < n_tiles; ++kt) {
+                    ok = __all_sync(0xffffffffu, attn_wait(&bar_p[sb], ph, abort) &&
+                                                     attn_wait(&bar_vfull[sb], ph, abort));
+                    if (!ok)
+                        break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    if (lane == 0) {
+                        const uint32_t v_addr = attn_smem_u32(sV(sb));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (trow[i] >= 0) {
-                    const uint32_t at = packed_table_offset(lane + 32 * i, row_bytes);
-                    const int64_t src = (int64_t)trow[i] * (a.rotary_dim / 2);
-                    bulk_load(sC + at, a.cos + src, row_bytes, &bar_q);
-                    bulk_load(sS + at, a.sin + src, row_bytes, &bar_q);
-                }
-            }
-            ++qn;
-            for (int32_t kt = 0; ok && kt < n_tiles; ++kt) {
-                const int k0 = kt * kAttnKeys;
-                if (!first)
-                    ok = __all_sync(0xffffffffu, attn_wait(&bar_s[sb], ph ^ 1u, abort));
-                if (!ok)
-                    break;
-                // keys k0 + 64 rank .. + 63; both CTAs' bytes complete the
-                // leader's barrier
-                if (leader && lane == 0)
-                    mbar_expect_tx(&bar_kfull[sb], 2 * kHalf);
-                __syncwarp();
-                if (lane < D / 64) {
-                    if (leader)
-                        tma_load_3d(sK(sb) + lane * 8192, maps, lane * 64, k0, u.kv, &bar_kfull[sb]);
-                    else
-                        tma_load_3d_to_leader(sK(sb) + lane * 8192, maps, lane * 64, k0 + 64, u.kv,
-                                              peer_addr(&bar_kfull[sb], 0));
-                }
-                k_ph[sb] = ph;
-                if (!first)
-                    ok = __all_sync(0xffffffffu, attn_wait(&bar_o[sb], ph ^ 1u, abort));
-                if (!ok)
-                    break;
-                // features D/2 rank .. of the tile's 128 keys
-                if (lane == 0) {
-                    if (leader) {
-                        mbar_expect_tx(&bar_vfull[sb], 2 * kHalf);
-                        tma_load_3d(sV(sb), maps + 1, 0, k0, u.kv, &bar_vfull[sb]);
-                    } else {
-                        tma_load_3d_to_leader(sV(sb), maps + 1, D / 2, k0, u.kv,
-                                              peer_addr(&bar_vfull[sb], 0));
+                        for (int kk = 0; kk < kAttnKeys / 16; ++kk)
+                            umma2_ts(tmem + k2OCol, tmem + sb * kAttnKeys + kk * 8,
+                                     packed_v_desc<D>(v_addr, kk), idesc, (kt > 0 || kk > 0) ? 1u : 0u);
+                        umma2_commit(&bar_o[sb], 3);
+                        if (kt + 1 == n_tiles)
+                            umma2_commit(&bar_odone, 3);
+                    }
+                    __syncwarp();
+                    if (++sb == k2SBufs) {
+                        sb = 0;
+                        ph ^= 1u;
                     }
                 }
+            }
+            if (lane == 0)
+                umma2_commit(&bar_drain[1], 1);
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, attn_wait(&bar_drain[1], 0u)))
+                ok = false;
+        } else if (warp == kPackedTmaWarp) {
+            // ---- the first query tile; then per unit its halves of key and
+            // value tile g into stage g mod 3 once tile g - 3 released it, and,
+            // behind the unit's third tile (or its last), the next unit's query
+            // tile once the unit before this one has read its buffer
+            uint32_t sb = 0, ph = 0, qn = 0;
+            bool first = true;
+            uint32_t k_ph[kPackedStages], v_ph[kPackedStages];   // parity of the last copy (2: none)
+#pragma unroll
+            for (int s = 0; s < kPackedStages; ++s)
+                k_ph[s] = v_ph[s] = 2;
+            int32_t seq = -1;
+            auto load_query = [&](int64_t r) {
+                const uint32_t b = qn & 1u;
+                if (qn >= 2)
+                    ok = __all_sync(0xffffffffu, attn_wait(&bar_qfree[b], ((qn >> 1) - 1) & 1u, abort));
+                if (!ok)
+                    return;
+                const PackedUnit u = src.unit(unit_at(r), lg);
+                const CUtensorMap *map;
+                if constexpr (Source::kPrefix) {
+                    map = &src.q_map;
+                } else {
+                    map = src.maps + (int64_t)u.seq * kPackedMaps + 2;
+                    acquire_map(map);
+                }
+                if (lane == 0)
+                    mbar_expect_tx(&bar_q[b], kTile);
                 __syncwarp();
-                v_ph[sb] = ph;
-                pb = sb;
-                p_ph = ph;
-                any = true;
-                if (++sb == k2SBufs) {
-                    sb = 0;
-                    ph ^= 1u;
-                    first = false;
+                // (tokens past the sequence's end arrive as zeros)
+                if (lane < D / 64)
+                    tma_load_3d(sQ(b) + lane * kBoxBytes, map, lane * 64, u.head0,
+                                u.tok0 + (int)rank * tokens, &bar_q[b]);
+                ++qn;
+            };
+            int64_t r = next_round(0);
+            if (unit_at(r) < n_units)
+                load_query(r);
+            while (ok && unit_at(r) < n_units) {
+                const PackedUnit u = src.unit(unit_at(r), lg);
+                const int64_t rn = next_round(r + 1);
+                if constexpr (!Source::kPrefix) {
+                    if (u.seq != seq) {
+                        acquire_map(src.maps + (int64_t)u.seq * kPackedMaps);
+                        acquire_map(src.maps + (int64_t)u.seq * kPackedMaps + 1);
+                        seq = u.seq;
+                    }
+                }
+                for (int32_t kt = 0; ok && kt < u.n_tiles; ++kt) {
+                    if (!first)
+                        ok = __all_sync(0xffffffffu, attn_wait(&bar_s[sb], ph ^ 1u, abort));
+                    if (!ok)
+                        break;
+                    // keys 64 rank .. + 63 of the tile; both CTAs' bytes
+                    // complete the leader's barrier
+                    if (leader && lane == 0)
+                        mbar_expect_tx(&bar_kfull[sb], 2 * kHalf);
+                    __syncwarp();
+                    src.template load_keys<D>(u, kt, sK(sb), &bar_kfull[sb], rank, lane);
+                    k_ph[sb] = ph;
+                    if (!first)
+                        ok = __all_sync(0xffffffffu, attn_wait(&bar_o[sb], ph ^ 1u, abort));
+                    if (!ok)
+                        break;
+                    // features D/2 rank .. of the tile's 128 keys
+                    if (leader && lane == 0)
+                        mbar_expect_tx(&bar_vfull[sb], 2 * kHalf);
+                    __syncwarp();
+                    src.template load_values<D>(u, kt, sV(sb), &bar_vfull[sb], rank, lane);
+                    __syncwarp();
+                    v_ph[sb] = ph;
+                    if (++sb == k2SBufs) {
+                        sb = 0;
+                        ph ^= 1u;
+                        first = false;
+                    }
+                    if (kt == (u.n_tiles < 3 ? u.n_tiles : 3) - 1 && unit_at(rn) < n_units)
+                        load_query(rn);
+                }
+                r = rn;
+            }
+            if (!ok) {
+                // one more bounded wait for the last query tiles and, in the
+                // leader (its barriers count both CTAs' bytes), the last copies
+                // into each stage
+                raise_abort();
+                for (uint32_t i = qn < 2 ? 0 : qn - 2; i < qn; ++i)
+                    (void)attn_wait(&bar_q[i & 1u], (i >> 1) & 1u);
+#pragma unroll
+                for (int s = 0; s < kPackedStages; ++s) {
+                    if (leader && k_ph[s] < 2)
+                        (void)attn_wait(&bar_kfull[s], k_ph[s]);
+                    if (leader && v_ph[s] < 2)
+                        (void)attn_wait(&bar_vfull[s], v_ph[s]);
                 }
             }
         }
-        if (!ok) {
+        if (!ok)
             raise_abort();
-            // one more bounded wait for the last query tile and, in the leader
-            // (its barriers count both CTAs' bytes), the last copies into each stage
-            if (qn > 0)
-                (void)attn_wait(&bar_q, (qn - 1) & 1u);
-#pragma unroll
-            for (int s = 0; s < kPackedStages; ++s) {
-                if (leader && k_ph[s] < 2)
-                    (void)attn_wait(&bar_kfull[s], k_ph[s]);
-                if (leader && v_ph[s] < 2)
-                    (void)attn_wait(&bar_vfull[s], v_ph[s]);
-            }
-        }
     }
     // every role has left its loops; the pair meets once more before TMEM is
     // freed, so no MMA of the leader still reads the follower's memory
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncwarp();
     cluster_sync_all();
     if (tid == 0 && *abort)
         atomicOr(a.flag, kFlagTimeout);
@@ -854,6 +911,58 @@ static bool encode_3d(EncodeTiledFn enc, CUtensorMap *m, const void *base, CUten
     const cuuint32_t e[3] = {1, 1, 1};
     return enc(m, dt, 3, const_cast<void *>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Multiprocessors of the current device, looked up once per device.
+static cudaError_t sm_count(int *sms, int *device)
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64)
+        return cudaErrorInvalidDevice;
+    int n = known[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess)
+            return e;
+        known[dev].store(n, std::memory_order_release);
+    }
+    *sms = n;
+    *device = dev;
+    return cudaSuccess;
+}
+
+// Raises a kernel's shared-memory limit, once per device.
+static cudaError_t raise_smem(const void *kernel, int bytes, int device, std::atomic<uint64_t> &raised)
+{
+    const uint64_t bit = (uint64_t)1 << device;
+    if (raised.load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        raised.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
+// The attention kernel over at most `most` units, one cluster per pair of SMs.
+template <typename T, int LAYOUT, int D, typename Source>
+static cudaError_t launch_packed_kernel(const Source &src, int64_t most, int lg, cudaStream_t st)
+{
+    static std::atomic<uint64_t> raised{0};
+    // at least 120 KB, so that one CTA holds an SM (and its TMEM)
+    constexpr int kSmem = kPackedSmem<D> > 120 * 1024 ? (int)kPackedSmem<D> : 120 * 1024;
+    auto *kernel = rope_attn_packed_kernel<T, LAYOUT, D, Source>;
+    int sms = 0, dev = 0;
+    cudaError_t e = sm_count(&sms, &dev);
+    if (e == cudaSuccess)
+        e = raise_smem(reinterpret_cast<const void *>(kernel), kSmem, dev, raised);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t clusters = most < sms / 2 ? most : sms / 2;
+    return launch_hot(kernel, dim3((unsigned)(2 * clusters)), dim3(kPackedThreads), kSmem, st, src, lg);
 }
 
 template <typename T, int LAYOUT, int D>
@@ -913,12 +1022,12 @@ static cudaError_t launch_packed(const PackedArgs &c, const PackedLayout &lay, c
     const int64_t blocks = (units + groups - 1) / groups + 1 + p.map_blocks;
     if (blocks > 0x7fffffff)
         return cudaErrorInvalidConfiguration;
-    rope_packed_prepare_kernel<T, LAYOUT, D><<<(unsigned)blocks, kPackedPrepThreads, 0, st>>>(rows, p, tmpl);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_hot(rope_packed_prepare_kernel<T, LAYOUT, D>, dim3((unsigned)blocks),
+                               dim3(kPackedPrepThreads), 0, st, rows, p, tmpl);
     if (e != cudaSuccess)
         return e;
 
-    PackedKernelArgs ka;
+    PackedSource ka;
     memset(&ka, 0, sizeof ka);
     ka.a.cos = k.cos; ka.a.sin = k.sin; ka.a.rotary_dim = k.rotary_dim; ka.a.table_rows = k.table_rows;
     ka.a.scale_log2 = c.scale_log2; ka.a.causal = c.causal; ka.a.flag = k.flag;
@@ -927,35 +1036,7 @@ static cudaError_t launch_packed(const PackedArgs &c, const PackedLayout &lay, c
     ka.head_units = c.Hq / gp;
     ka.units_per_kv = c.Hq / k.Hk / gp;
 
-    static std::atomic<uint64_t> raised{0};        // bit d: shared-memory limit raised on device d
-    static std::atomic<int> sm_count[64];          // multiprocessors of device d (0: not read yet)
-    // at least 120 KB, so that one CTA holds an SM (and its TMEM)
-    constexpr int kSmem = kPackedSmem<D> > 120 * 1024 ? (int)kPackedSmem<D> : 120 * 1024;
-    auto *kernel = rope_attn_packed_kernel<T, LAYOUT, D>;
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
-        return e;
-    if (dev < 0 || dev >= 64)
-        return cudaErrorInvalidDevice;
-    int sms = sm_count[dev].load(std::memory_order_acquire);
-    if (sms == 0) {
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess)
-            return e;
-        sm_count[dev].store(sms, std::memory_order_release);
-    }
-    const uint64_t bit = (uint64_t)1 << dev;
-    if (!(raised.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e != cudaSuccess)
-            return e;
-        raised.fetch_or(bit, std::memory_order_acq_rel);
-    }
-    const int64_t most = lay.tiles * ka.head_units;
-    const int64_t clusters = most < sms / 2 ? most : sms / 2;
-    kernel<<<dim3((unsigned)(2 * clusters)), k2Threads, kSmem, st>>>(ka, lg);
-    return cudaGetLastError();
+    return launch_packed_kernel<T, LAYOUT, D>(ka, lay.tiles * ka.head_units, lg, st);
 }
 
 template <typename T>
