@@ -448,6 +448,58 @@ int64_t rope_attention_packed_workspace(int64_t n_seqs, int64_t total_q, int64_t
                                         int32_t Hk, int32_t D);
 
 /*
+ * rope_attention_decode_fwd -- attention of one new token per sequence, over
+ * a prefix that all sequences of the batch share and a suffix of each one's
+ * own, both in the pages of a cache of rotated keys (rope_cache_append).
+ *
+ *   o_b = softmax(scale * rot(q_b) [K_prefix; K_b]^T) [V_prefix; V_b]
+ *
+ * The prefix's keys and values are read once for the whole batch.
+ * q: device [B, Hq, D], row stride q_stride (elements, a multiple of 8);
+ *    o: device [B, Hq, D], dense, written.  Hq is a multiple of Hk.
+ * k_pages, v_pages: the cache, [n_pages, Hk, page_size, D].
+ * prefix_table, prefix_len: device int32, ceil(prefix_len / page_size) pages;
+ *    prefix_len = 0: no prefix (the table may be NULL).
+ * block_table: device int32[B, max_blocks]; seq_lens: device int32[B], the
+ *    keys of each suffix, the new token's own among them (0 <= seq_lens[b] <=
+ *    max_blocks * page_size; 0: the prefix alone).  A sequence without any key
+ *    gets zeros.  Sequences may share pages.
+ * pos_q: device int32[B] or NULL.  Query b is rotated with table row pos_q[b]
+ *    (-1: not rotated), or prefix_len + seq_lens[b] - 1 when NULL.
+ * softmax_scale: > 0, or <= 0 for 1/sqrt(D).
+ * workspace: device, 128-byte aligned, at least
+ *    rope_attention_decode_workspace(...) bytes; overwritten.
+ * A length out of range is cut to the range, a page number out of range reads
+ *    as zeros: the flag is raised (ROPE_ERR_BAD_INDEX), and the outputs of the
+ *    sequences that use it mean nothing.  A query position outside the table
+ *    is not rotated and raises ROPE_ERR_POS_OUT_OF_RANGE.
+ * Arithmetic: rot(q) and the softmax probabilities are rounded to `dtype`
+ *    for the products; sums, maxima and partial outputs are fp32; o is rounded
+ *    once.  The split of the work depends on the sizes and the lengths alone:
+ *    the same call gives the same bits.
+ * Errors: ROPE_ERR_UNSUPPORTED for other dtypes, D, rotary_dim, layouts, page
+ *    sizes, B > 32768, a stride not a multiple of 8 or unaligned pointers;
+ *    ROPE_ERR_INVALID_ARG for bad sizes, null pointers, a workspace too small,
+ *    o or the workspace overlapping another argument; ROPE_ERR_CUDA if a
+ *    launch fails.  Asynchronous on `stream`; waits inside the kernels are
+ *    bounded as in rope_attention_fwd.
+ */
+rope_status rope_attention_decode_fwd(const void *q, const void *k_pages, const void *v_pages, void *o,
+                                      const int32_t *block_table, const int32_t *seq_lens,
+                                      const int32_t *prefix_table, int64_t prefix_len,
+                                      const float *cos, const float *sin, const int32_t *pos_q,
+                                      int64_t B, int64_t q_stride, int32_t Hq, int32_t Hk, int32_t D,
+                                      int32_t rotary_dim, int32_t layout, float softmax_scale,
+                                      int32_t page_size, int64_t n_pages, int64_t max_blocks,
+                                      int32_t dtype, int64_t table_rows, void *workspace,
+                                      int64_t workspace_bytes, void *stream);
+
+/* rope_attention_decode_workspace -- bytes of workspace for a call of these
+ * sizes (0 when there is nothing to do, -1 for sizes it does not take). */
+int64_t rope_attention_decode_workspace(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_size,
+                                        int64_t max_blocks, int64_t prefix_len);
+
+/*
  * rope_check_errors -- synchronise `stream`, then report and clear the
  * current device's error flag.
  * Returns ROPE_ERR_CUDA if the stream reports an error, else

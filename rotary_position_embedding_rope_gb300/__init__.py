@@ -50,10 +50,11 @@ __all__ = [
     "rope_status_string", "rope_qk_kernel_variant", "rope_force_kernel_variant",
     "rope_tune_rotation_launch", "rope_cache_append",
     "rope_attention_packed_fwd", "rope_attention_packed_workspace",
+    "rope_attention_decode_fwd", "rope_attention_decode_workspace",
     # conveniences
     "build_tables", "build_tables_ex", "apply_qk", "apply_q", "apply_qk_xpos", "rotate_qk",
     "attention", "attention_workspace", "PreparedApply", "cache_append",
-    "attention_packed",
+    "attention_packed", "attention_shared_prefix",
 ]
 
 (ROPE_OK, ROPE_ERR_INVALID_ARG, ROPE_ERR_UNSUPPORTED, ROPE_ERR_CUDA, ROPE_ERR_POS_OUT_OF_RANGE,
@@ -154,6 +155,11 @@ def load_library() -> ctypes.CDLL:
     lib.rope_attention_packed_fwd.restype = c.c_int
     lib.rope_attention_packed_workspace.argtypes = [c.c_int64] * 3 + [c.c_int32] * 3
     lib.rope_attention_packed_workspace.restype = c.c_int64
+    lib.rope_attention_decode_fwd.argtypes = [P] * 7 + [c.c_int64, P, P, P, c.c_int64, c.c_int64] + \
+        [c.c_int32] * 5 + [c.c_float, c.c_int32, c.c_int64, c.c_int64, c.c_int32, c.c_int64, P, c.c_int64, P]
+    lib.rope_attention_decode_fwd.restype = c.c_int
+    lib.rope_attention_decode_workspace.argtypes = [c.c_int64] + [c.c_int32] * 4 + [c.c_int64] * 2
+    lib.rope_attention_decode_workspace.restype = c.c_int64
     _lib = lib
     return lib
 
@@ -656,6 +662,27 @@ def rope_attention_packed_workspace(n_seqs, total_q, total_k, Hq, Hk, D) -> int:
                                                           int(Hq), int(Hk), int(D))
 
 
+def rope_attention_decode_fwd(q, k_pages, v_pages, o, block_table, seq_lens, prefix_table, prefix_len,
+                              cos, sin, pos_q, B, q_stride, Hq, Hk, D, rotary_dim, layout,
+                              softmax_scale, page_size, n_pages, max_blocks, dtype, table_rows,
+                              workspace, workspace_bytes, stream=None):
+    st = load_library().rope_attention_decode_fwd(
+        _addr(q, "q"), _addr(k_pages, "k_pages"), _addr(v_pages, "v_pages"), _addr(o, "o"),
+        _addr(block_table, "block_table"), _addr(seq_lens, "seq_lens"),
+        _addr(prefix_table, "prefix_table"), int(prefix_len), _addr(cos, "cos"), _addr(sin, "sin"),
+        _addr(pos_q, "pos_q"), int(B), int(q_stride), int(Hq), int(Hk), int(D), int(rotary_dim),
+        int(layout), float(softmax_scale), int(page_size), int(n_pages), int(max_blocks), int(dtype),
+        int(table_rows), _addr(workspace, "workspace"), int(workspace_bytes), _stream(stream))
+    _check(st, "rope_attention_decode_fwd")
+
+
+def rope_attention_decode_workspace(B, Hq, Hk, D, page_size, max_blocks, prefix_len) -> int:
+    """Bytes of workspace (-1 for sizes the call does not take)."""
+    return load_library().rope_attention_decode_workspace(int(B), int(Hq), int(Hk), int(D),
+                                                          int(page_size), int(max_blocks),
+                                                          int(prefix_len))
+
+
 class _Call:
     """One serving call: the device its tensors live on and the stream it runs
     on, with that device current while the library is called."""
@@ -835,4 +862,56 @@ def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
           c.dense(pos_k, "pos_k", i32, (Tk,)), c.dense(cu_seqlens_q, "cu_seqlens_q", i32, (n + 1,)),
           c.dense(cu_seqlens_k, "cu_seqlens_k", i32, (n + 1,)), n, Tq, Tk, qs, ks, vs, Hq, Hk, D, rd,
           _LAYOUT_CODE[layout], int(causal), -1.0 if scale is None else scale, code, rows, ws, ws_bytes)
+    return out
+
+
+def attention_shared_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                            block_table: torch.Tensor, seq_lens: torch.Tensor,
+                            prefix_table: torch.Tensor | None, prefix_len: int, cos: torch.Tensor,
+                            sin: torch.Tensor, pos_q: torch.Tensor | None = None,
+                            rotary_dim: int | None = None, layout: str = "split_half",
+                            scale: float | None = None, out: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence over a shared prefix and its own suffix.
+
+    q: [B, Hq, D] (a view with a row stride is taken as it is), one query per
+    sequence; returns [B, Hq, D].  k_pages, v_pages: the cache that
+    cache_append writes, [pages, Hk, page_size, D] of rotated keys.
+    prefix_table: int32 pages of the prefix_len keys that all sequences share
+    (None with prefix_len 0), read once for the whole batch.
+    block_table: int32 [B, max_blocks]; seq_lens: int32 [B], the keys of each
+    suffix, the new token's own among them (cache_append it first).
+    pos_q: int32 [B] table rows (-1 = not rotated), or None for
+    prefix_len + seq_lens - 1.
+    workspace: None, or a uint8 tensor of rope_attention_decode_workspace(...)
+    bytes to use (128-byte aligned; its contents do not matter).
+    """
+    c = _Call(q, stream)
+    code = _type16(q, "attention_shared_prefix")
+    qa, qs = c.rows(q, "q", dtype=q.dtype)
+    B, Hq, D = q.shape
+    kp, vp, n_pages, Hk, page, d = c.cache(k_pages, v_pages, q.dtype)
+    if d != D:
+        raise ValueError("the cache holds heads of %d features, q of %d" % (d, D))
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [%d, max_blocks]" % B)
+    blocks = block_table.shape[1]
+    ca, sa, rd, rows = c.tables(cos, sin, rotary_dim)
+    i32 = torch.int32
+    pt = c.dense(prefix_table, "prefix_table", i32)
+    if prefix_len > 0 and (prefix_table is None or prefix_table.numel() * page < prefix_len):
+        raise ValueError("prefix_table must name the pages of %d keys" % prefix_len)
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+        if c.stream != torch.cuda.current_stream(c.device).cuda_stream:
+            out.record_stream(torch.cuda.ExternalStream(c.stream, c.device))
+    lib = load_library()
+    ws, ws_bytes = c.workspace(workspace, lib.rope_attention_decode_workspace(B, Hq, Hk, D, page, blocks,
+                                                                              prefix_len),
+                               "rope_attention_decode_workspace")
+    c.run(lib.rope_attention_decode_fwd, "rope_attention_decode_fwd", qa, kp, vp,
+          c.dense(out, "out", q.dtype, (B, Hq, D)), c.dense(block_table, "block_table", i32),
+          c.dense(seq_lens, "seq_lens", i32, (B,)), pt, prefix_len, ca, sa,
+          c.dense(pos_q, "pos_q", i32, (B,)), B, qs, Hq, Hk, D, rd, _LAYOUT_CODE[layout],
+          -1.0 if scale is None else scale, page, n_pages, blocks, code, rows, ws, ws_bytes)
     return out

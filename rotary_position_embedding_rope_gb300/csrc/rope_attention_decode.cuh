@@ -1,0 +1,750 @@
+// rope_attention_decode.cuh -- attention of one new token per sequence over a
+// prefix that all sequences share and a suffix of each one's own, both in the
+// pages of a cache (rope_attention_decode_fwd).
+//
+//   o_b = softmax(scale * rot(q_b) [K_prefix; K_b]^T) [V_prefix; V_b]
+//
+// A softmax over a concatenation is a merge of the parts' softmaxes: with part
+// i's maximum m_i, sum l_i = sum_j 2^(s_j - m_i) and output O_i = sum_j 2^(s_j -
+// m_i) v_j, and M = max m_i,
+//   o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+// So the parts run apart, and each key is read once:
+//   1. the prefix, once for the whole batch: its rows (sequence, head) are the
+//      rows of rope_attn_packed_kernel's tiles (the batch is a "sequence" of B
+//      tokens), its keys come from pages, its key tiles are split over clusters
+//      when there are few rows; every unit leaves an fp32 (O, m, l);
+//   2. rope_decode_suffix_kernel: every warp an equal run of 16-key chunks of
+//      all suffixes, laid end to end, so that ragged lengths balance;
+//   3. rope_decode_merge_kernel.
+// 1 and 2 do not depend on one another: 2 is launched while 1 runs and fills
+// the SMs that 1 leaves.
+//
+// What bounds it: bytes -- the prefix once, every suffix once; from about 300
+// rows per key head on, the prefix products.
+#pragma once
+
+#include "rope_attention_packed.cuh"
+
+namespace rope {
+
+// ---------------------------------------------------------------------------
+// 1. the prefix: units of (row tile, head unit, split of the key tiles)
+struct PrefixSource {
+    static constexpr bool kPrefix = true;
+    AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, flag
+    CUtensorMap k_map, v_map, v_tail, q_map;   // v_tail: pages of n_keys mod page rows
+    const int32_t *pages;                      // the prefix's block list
+    const int32_t *pos_q, *lens;               // [B]
+    int64_t max_keys;                          // most keys of a suffix (longer lengths are bad)
+    float *out;                                // [splits][B][Hq][D]
+    float2 *stats;                             // [splits][B][Hq] (m, l)
+    int64_t n_pages;
+    int32_t n_keys, n_key_tiles, B, Hq, Hk, page_shift;
+    int32_t row_tiles, head_units, units_per_kv, splits, tiles_per_split;
+
+    __device__ __forceinline__ int64_t units() const
+    {
+        return (int64_t)row_tiles * head_units * splits;
+    }
+    // consecutive units: the row tiles of one key range and key head, so that
+    // the clusters that read the same keys do so at about the same time
+    __device__ __forceinline__ PackedUnit unit(int64_t L, int lg) const
+    {
+        const int64_t i = L / row_tiles;
+        PackedUnit u;
+        u.tok0 = (int32_t)(L - i * row_tiles) * (2 * kAttnRows >> lg);
+        const int32_t hu = (int32_t)(i % head_units);
+        u.split = (int32_t)(i / head_units);
+        u.seq = 0; u.q_start = 0; u.tokens = B; u.n_keys = n_keys;
+        u.head0 = hu << lg;
+        u.kv = hu / units_per_kv;
+        u.first = u.split * tiles_per_split;
+        const int32_t left = n_key_tiles - u.first;
+        u.n_tiles = left < tiles_per_split ? left : tiles_per_split;
+        return u;
+    }
+    __device__ __forceinline__ int32_t tiles(int64_t L) const
+    {
+        const int32_t first = (int32_t)(L / row_tiles / head_units) * tiles_per_split;
+        const int32_t left = n_key_tiles - first;
+        return left < tiles_per_split ? left : tiles_per_split;
+    }
+    __device__ __forceinline__ int64_t table_row(const PackedUnit &, int32_t t) const;
+
+    // z of a prefix page in the pools' maps; past the last page, and for a bad
+    // page number, an index that arrives as zeros
+    __device__ __forceinline__ int32_t page_z(int32_t i, int32_t kv) const
+    {
+        const int32_t none = (int32_t)(n_pages * Hk);
+        if ((int64_t)i << page_shift >= n_keys)
+            return none;
+        const int32_t p = __ldg(pages + i);
+        if (p < 0 || p >= n_pages) {
+            atomicOr(a.flag, kFlagIndex);
+            return none;
+        }
+        return p * Hk + kv;
+    }
+    template <int D>
+    __device__ __forceinline__ void load_keys(const PackedUnit &u, int32_t kt, uint8_t *dst, uint64_t *bar,
+                                              uint32_t rank, int lane) const
+    {
+        const int32_t shift = page_shift < 6 ? page_shift : 6;      // keys of a box: a page or half of one
+        const int32_t boxes = (64 >> shift) * (D / 64);
+        if (lane < boxes) {
+            const int32_t i = lane / (D / 64), x = lane % (D / 64);
+            const int32_t key = (u.first + kt) * kAttnKeys + 64 * (int)rank + (i << shift);
+            load_half_box(dst + x * 8192 + (i << shift) * 128, &k_map, x * 64,
+                          key & ((1 << page_shift) - 1), page_z(key >> page_shift, u.kv), bar, rank);
+        }
+    }
+    template <int D>
+    __device__ __forceinline__ void load_values(const PackedUnit &u, int32_t kt, uint8_t *dst,
+                                                uint64_t *bar, uint32_t rank, int lane) const
+    {
+        const int32_t boxes = kAttnKeys >> page_shift;
+        if (lane < boxes) {
+            const int32_t page = ((u.first + kt) * kAttnKeys >> page_shift) + lane;
+            // the last, partly filled page: rows past the prefix arrive as zeros
+            const bool tail = page == n_keys >> page_shift;
+            load_half_box(dst + (lane << page_shift) * D, tail ? &v_tail : &v_map, D / 2 * (int)rank, 0,
+                          page_z(page, u.kv), bar, rank);
+        }
+    }
+    // One helper warp: its rows' O, m and l, in fp32
+    template <int D>
+    __device__ __forceinline__ void store_rows(const PackedUnit &u, uint32_t o_base, int32_t y0, int lane,
+                                               int lg, float2 stat) const
+    {
+        const int32_t tok = y0 + (lane >> lg);
+        const int64_t row = ((int64_t)u.split * B + tok) * Hq + u.head0 + (lane & ((1 << lg) - 1));
+        if (tok < B)
+            stats[row] = stat;
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+            float ov[32];
+            tmem_ld32(o_base + c0, ov);
+            if (tok < B) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 4)
+                    *reinterpret_cast<float4 *>(out + row * D + c0 + c) =
+                        make_float4(ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
+            }
+        }
+    }
+};
+
+// The keys of sequence b's suffix; a length out of range raises the flag and
+// is cut to the range.
+__device__ __forceinline__ int32_t suffix_keys(const int32_t *lens, int32_t b, int64_t most, int32_t *flag)
+{
+    const int32_t n = __ldg(lens + b);
+    if (n < 0 || n > most) {
+        atomicOr(flag, kFlagIndex);
+        return n < 0 ? 0 : (int32_t)most;
+    }
+    return n;
+}
+
+// Table row of sequence b's query: pos_q, or the index of its last key (which
+// is the new token's); -1: not rotated.
+__device__ __forceinline__ int64_t query_row(const int32_t *pos_q, int32_t b, int64_t keys,
+                                             int64_t table_rows, int32_t *flag)
+{
+    const int64_t r = pos_q != nullptr ? (int64_t)__ldg(pos_q + b) : keys - 1;
+    if (r == -1)
+        return -1;
+    if (r < 0 || r >= table_rows) {
+        atomicOr(flag, kFlagPosition);
+        return -1;
+    }
+    return r;
+}
+
+__device__ __forceinline__ int64_t PrefixSource::table_row(const PackedUnit &, int32_t t) const
+{
+    const int64_t keys = pos_q != nullptr ? 0 : (int64_t)n_keys + suffix_keys(lens, t, max_keys, a.flag);
+    return query_row(pos_q, t, keys, a.table_rows, a.flag);
+}
+
+// ---------------------------------------------------------------------------
+// 2. the suffixes
+//
+// A pair is (sequence, key head, row group): up to 16 query heads of one group,
+// the 16 rows of an mma.  The 16-key chunks of all pairs, sequence after
+// sequence, form one long list; warp w of the grid owns chunks [w * per, (w +
+// 1) * per) of it, whatever pairs they belong to, and leaves an fp32 (O, m, l)
+// for each pair it touches in slot w + pair (either index grows by one from
+// one slot to the next, so slots are distinct).  Nothing waits on anything
+// between warps.
+//
+// mma.sync (m16n8k16) instead of tcgen05: a decode step has at most 16 rows per
+// key here, the work is one pass over the keys, and a warp that owns its keys,
+// its stages and its softmax needs no barrier but the copies' own.  K and V
+// arrive by TMA (boxes of 64 features x 16 keys, 128-byte swizzle, so ldmatrix
+// reads without conflicts), three stages (D = 128; six for D = 64) a warp, eight
+// warps an SM: 192 KB in flight or in use.
+constexpr int kDecWarps = 8;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecKeys = 16;
+template <int D>
+static constexpr int kDecStages = D == 128 ? 3 : 6;
+template <int D>
+static constexpr int kDecStageBytes = 2 * kDecKeys * D * 2;
+template <int D>
+static constexpr int kDecQStride = D * 2 + 16;                 // padded rows of the query tile
+template <int D>
+static constexpr int kDecSmem = kDecWarps * (kDecStages<D> * kDecStageBytes<D> + 16 * kDecQStride<D>);
+
+struct DecodeArgs {
+    AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, flag
+    CUtensorMap k_map, v_map;                  // boxes of 64 features x 16 keys
+    const void *q;                             // [B][Hq][D], row stride q_stride
+    int64_t q_stride;
+    void *o;                                   // [B][Hq][D]
+    const int32_t *table, *lens, *pos_q;
+    int64_t max_blocks, n_pages;
+    int32_t B, Hq, Hk, page_shift, n_prefix;
+    int32_t row_groups, rows;                  // of a key head's query heads; rows of a group
+    int32_t min_chunks;                        // of a warp
+    // partial results
+    int32_t *chunk_start;                      // [B + 1]: chunks per pair of the sequences before b
+    float *out;                                // [slots][rows][D]
+    float2 *stats;                             // [slots][rows]
+    const float *prefix_out;                   // [splits][B][Hq][D]
+    const float2 *prefix_stats;
+    int32_t splits, warps;                     // warps: of the suffix grid (0: no suffixes)
+};
+
+__device__ __forceinline__ int64_t decode_per_warp(int64_t chunks, int32_t warps, int32_t min_chunks)
+{
+    const int64_t per = (chunks + warps - 1) / warps;
+    return per < min_chunks ? min_chunks : per;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+                     "{%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+                     "{%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A place in the list of chunks.
+struct ChunkAt {
+    int32_t b, hr, ch, n;                      // sequence, key head and row group, chunk of n
+    __device__ __forceinline__ void next(const DecodeArgs &g, int64_t most)
+    {
+        if (++ch < n)
+            return;
+        ch = 0;
+        if (++hr < g.Hk * g.row_groups)
+            return;
+        hr = 0;
+        do {
+            if (++b >= g.B) {
+                n = 0;
+                return;
+            }
+            n = (suffix_keys(g.lens, b, most, g.a.flag) + kDecKeys - 1) / kDecKeys;
+        } while (n == 0);
+    }
+};
+
+// 16 rows of rotated queries of pair (b, hr) into the warp's tile (zeros past
+// the group's rows), then as the A operand of every 16-feature step.
+template <typename T, int LAYOUT, int D>
+__device__ __forceinline__ void load_query_rows(const DecodeArgs &g, const ChunkAt &at, int64_t keys,
+                                                uint8_t *tile, uint32_t (&qf)[D / 16][4])
+{
+    constexpr int L = D / 16, kRowsAtOnce = 32 / L;
+    const int lane = threadIdx.x & 31, j = lane % L;
+    const int32_t kv = at.hr / g.row_groups, group = g.Hq / g.Hk;
+    const int32_t r0 = (at.hr - kv * g.row_groups) * g.rows;
+    const RowPart part = row_part<LAYOUT>(j, g.a.rotary_dim);
+    const int64_t trow = query_row(g.pos_q, at.b, keys, g.a.table_rows, g.a.flag);
+    const T *base = static_cast<const T *>(g.q) + at.b * g.q_stride + (int64_t)(kv * group + r0) * D;
+    uint4 x0[16 / kRowsAtOnce], x1[16 / kRowsAtOnce];
+#pragma unroll
+    for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
+        const int r = i * kRowsAtOnce + lane / L;
+        x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
+        if (r < g.rows && r0 + r < group) {
+            x0[i] = __ldg(reinterpret_cast<const uint4 *>(base + r * D + part.o0));
+            x1[i] = __ldg(reinterpret_cast<const uint4 *>(base + r * D + part.o1));
+        }
+    }
+    if (part.rot && trow >= 0) {
+        float c[8], s[8];
+        const int64_t w = trow * (g.a.rotary_dim / 2) + 8 * j;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(g.a.cos + w) + q);
+            const float4 s4 = __ldg(reinterpret_cast<const float4 *>(g.a.sin + w) + q);
+            c[4 * q] = c4.x; c[4 * q + 1] = c4.y; c[4 * q + 2] = c4.z; c[4 * q + 3] = c4.w;
+            s[4 * q] = s4.x; s[4 * q + 1] = s4.y; s[4 * q + 2] = s4.z; s[4 * q + 3] = s4.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 16 / kRowsAtOnce; ++i)
+            rotate_part<T, LAYOUT>(x0[i], x1[i], c, s);
+    }
+    __syncwarp();                              // the tile's last readers are done
+#pragma unroll
+    for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
+        const int r = i * kRowsAtOnce + lane / L;
+        *reinterpret_cast<uint4 *>(tile + r * kDecQStride<D> + part.o0 * 2) = x0[i];
+        *reinterpret_cast<uint4 *>(tile + r * kDecQStride<D> + part.o1 * 2) = x1[i];
+    }
+    __syncwarp();
+    // lanes 0-15: rows 0-15, features 0-7 of the step; lanes 16-31: features 8-15
+    const uint32_t addr = attn_smem_u32(tile) + (lane & 15) * kDecQStride<D> + (lane >> 4) * 16;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+        ldsm4(addr + k * 32, qf[k]);
+}
+
+template <typename T, int LAYOUT, int D>
+__global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(const __grid_constant__ DecodeArgs g)
+{
+    constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>, kBox = kDecKeys * 128;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bar[kDecWarps][kStages];
+    __shared__ int32_t warp_sum[kDecWarps];
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t most = g.max_blocks << g.page_shift;
+    if (tid < kDecWarps * kStages)
+        mbar_init(&bar[0][0] + tid, 1);
+    if (tid == 0)
+        abort_flag = 0;
+    // chunks of the sequences before b, by every CTA for itself (in the stages'
+    // memory; one CTA writes it out for the merge)
+    int32_t *start = reinterpret_cast<int32_t *>(smem);
+    int32_t carry = 0;
+    for (int32_t b0 = 0; b0 < g.B; b0 += kDecThreads) {
+        const int32_t b = b0 + tid;
+        const int32_t n =
+            b < g.B ? (suffix_keys(g.lens, b, most, g.a.flag) + kDecKeys - 1) / kDecKeys : 0;
+        int32_t inc = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d)
+                inc += o;
+        }
+        if (lane == 31)
+            warp_sum[warp] = inc;
+        __syncthreads();
+        int32_t before = carry;
+        for (int w = 0; w < warp; ++w)
+            before += warp_sum[w];
+        if (b < g.B)
+            start[b] = before + inc - n;
+        for (int w = 0; w < kDecWarps; ++w)
+            carry += warp_sum[w];
+        __syncthreads();
+    }
+    if (tid == 0)
+        start[g.B] = carry;
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int32_t b = tid; b <= g.B; b += kDecThreads)
+            g.chunk_start[b] = start[b];
+    const int32_t heads = g.Hk * g.row_groups;
+    const int64_t total = (int64_t)carry * heads;
+    const int64_t per = decode_per_warp(total, g.warps, g.min_chunks);
+    const int32_t w = blockIdx.x * kDecWarps + warp;
+    int64_t c = w * per;
+    int64_t left = total - c < per ? total - c : per;          // chunks of this warp
+    ChunkAt at = {0, 0, 0, 0};
+    if (left > 0) {
+        const int32_t b = find_sequence(start, g.B + 1, c / heads);
+        // (the last b whose start is at most c / heads has chunks)
+        at.b = b;
+        at.n = start[b + 1] - start[b];
+        const int64_t in = c - (int64_t)start[b] * heads;
+        at.hr = (int32_t)(in / at.n);
+        at.ch = (int32_t)(in - (int64_t)at.hr * at.n);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();                                           // start[] is read: the stages are free
+    pdl_trigger();
+
+    uint8_t *stages = smem + warp * kStages * kStage;
+    uint8_t *qtile = smem + kDecWarps * kStages * kStage + warp * 16 * kDecQStride<D>;
+    volatile int *abort = &abort_flag;
+    // the copies run kStages chunks ahead; the page of the next one is looked up
+    // a step early
+    ChunkAt ahead = at;
+    int64_t to_load = left;
+    auto look_up = [&]() {
+        const int64_t block = (int64_t)ahead.ch * kDecKeys >> g.page_shift;
+        return to_load > 0 ? __ldg(g.table + ahead.b * g.max_blocks + block) : 0;
+    };
+    int32_t page = look_up();
+    auto load = [&](int st) {
+        int32_t z = page * g.Hk + ahead.hr / g.row_groups;
+        if (page < 0 || page >= g.n_pages) {
+            if (lane == 0)
+                atomicOr(g.a.flag, kFlagIndex);
+            z = (int32_t)(g.n_pages * g.Hk);                   // arrives as zeros
+        }
+        const int32_t y = ahead.ch * kDecKeys & ((1 << g.page_shift) - 1);
+        if (lane == 0)
+            mbar_expect_tx(&bar[warp][st], kStage);
+        __syncwarp();
+        if (lane < 2 * (D / 64)) {
+            const int x = lane % (D / 64);
+            const bool v = lane >= D / 64;
+            tma_load_3d(stages + st * kStage + (v ? kStage / 2 : 0) + x * kBox, v ? &g.v_map : &g.k_map,
+                        x * 64, y, z, &bar[warp][st]);
+        }
+        --to_load;
+        ahead.next(g, most);
+        page = look_up();
+    };
+    bool ok = true;
+    int64_t issued = 0, done = 0;
+    for (int st = 0; st < kStages && to_load > 0; ++st, ++issued)
+        load(st);
+
+    uint32_t qf[D / 16][4];
+    float o[D / 8][4];
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;   // rows lane / 4 and + 8
+    int32_t keys = 0;                                          // of the pair's suffix
+    bool fresh = true;
+    int st = 0;
+    uint32_t ph = 0;
+    // ldmatrix rows: K (two 8-key tiles x two 8-feature halves of a step), V (two
+    // 8-key halves x two 8-feature tiles)
+    const int k_row = (lane & 7) + ((lane >> 4) << 3), k_half = (lane >> 3) & 1;
+    const int v_row = lane & 15, v_half = lane >> 4;
+    const uint32_t base = attn_smem_u32(stages);
+    for (; ok && left > 0; --left, ++done) {
+        if (fresh) {
+            keys = suffix_keys(g.lens, at.b, most, g.a.flag);
+            load_query_rows<T, LAYOUT, D>(g, at, (int64_t)g.n_prefix + keys, qtile, qf);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+            m0 = m1 = -INFINITY;
+            l0 = l1 = 0.0f;
+            fresh = false;
+        }
+        ok = __all_sync(0xffffffffu, attn_wait(&bar[warp][st], ph, abort));
+        if (!ok)
+            break;
+        const uint32_t kb = base + st * kStage, vb = kb + kStage / 2;
+        // S = q K^T: 16 rows x 16 keys
+        float s0[4] = {0, 0, 0, 0}, s1[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            uint32_t b[4];
+            const int chunk = (k & 3) * 2 + k_half;
+            ldsm4(kb + (k >> 2) * kBox + k_row * 128 + ((chunk ^ (k_row & 7)) << 4), b);
+            mma16816<T>(s0, qf[k], b[0], b[1]);
+            mma16816<T>(s1, qf[k], b[2], b[3]);
+        }
+        // keys of this lane: 2 (lane mod 4) + {0, 1} of either 8-key tile
+        const int32_t nk = keys - at.ch * kDecKeys;            // visible keys of the chunk
+        const int c0 = 2 * (lane & 3);
+        uint32_t vis0 = 0xffffffffu, vis1 = 0xffffffffu;       // value rows: halves of a register
+        float sc[4] = {s0[0], s0[1], s1[0], s1[1]}, sd[4] = {s0[2], s0[3], s1[2], s1[3]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sc[i] *= g.a.scale_log2;
+            sd[i] *= g.a.scale_log2;
+        }
+        if (nk < kDecKeys) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = c0 + (i & 1) + (i >> 1) * 8;
+                if (key >= nk) {
+                    sc[i] = sd[i] = -INFINITY;
+                    // what lies behind the last key (anything) must not meet a zero
+                    (i >> 1 ? vis1 : vis0) &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+                }
+            }
+        }
+        float x0 = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+        float x1 = fmaxf(fmaxf(sd[0], sd[1]), fmaxf(sd[2], sd[3]));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+        // the reference maxima move only when exceeded by more than 8 (a factor
+        // of 256), so O is seldom rescaled
+        const bool up0 = x0 > m0 + 8.0f, up1 = x1 > m1 + 8.0f;
+        if (__any_sync(0xffffffffu, up0 || up1)) {
+            const float f0 = up0 ? (m0 == -INFINITY ? 0.0f : fast_exp2(m0 - x0)) : 1.0f;
+            const float f1 = up1 ? (m1 == -INFINITY ? 0.0f : fast_exp2(m1 - x1)) : 1.0f;
+            m0 = up0 ? x0 : m0;
+            m1 = up1 ? x1 : m1;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                o[i][0] *= f0;
+                o[i][1] *= f0;
+                o[i][2] *= f1;
+                o[i][3] *= f1;
+            }
+        }
+        const float n0 = m0 == -INFINITY ? 0.0f : m0, n1 = m1 == -INFINITY ? 0.0f : m1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sc[i] = fast_exp2(sc[i] - n0);
+            sd[i] = fast_exp2(sd[i] - n1);
+        }
+        l0 += (sc[0] + sc[1]) + (sc[2] + sc[3]);
+        l1 += (sd[0] + sd[1]) + (sd[2] + sd[3]);
+        // P rounded to the element type for the P V product (the sums keep fp32)
+        const uint32_t p[4] = {Elt<T>::f2_to_word(sc[0], sc[1]), Elt<T>::f2_to_word(sd[0], sd[1]),
+                               Elt<T>::f2_to_word(sc[2], sc[3]), Elt<T>::f2_to_word(sd[2], sd[3])};
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+            uint32_t b[4];
+            const int chunk = (n & 3) * 2 + v_half;
+            ldsm4_t(vb + (n >> 2) * kBox + v_row * 128 + ((chunk ^ (v_row & 7)) << 4), b);
+            mma16816<T>(o[2 * n], p, b[0] & vis0, b[1] & vis1);
+            mma16816<T>(o[2 * n + 1], p, b[2] & vis0, b[3] & vis1);
+        }
+        __syncwarp();                                          // the stage is read
+        if (to_load > 0) {
+            load(st);
+            ++issued;
+        }
+        if (++st == kStages) {
+            st = 0;
+            ph ^= 1u;
+        }
+        const int32_t pair = at.b * heads + at.hr;
+        const int64_t slot = (int64_t)w + pair;
+        const ChunkAt was = at;
+        at.next(g, most);
+        if (left == 1 || at.b != was.b || at.hr != was.hr) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+            const int r = lane >> 2;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int rr = r + 8 * half;
+                if (rr < g.rows) {
+                    float *dst = g.out + (slot * g.rows + rr) * D + c0;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i)
+                        *reinterpret_cast<float2 *>(dst + 8 * i) =
+                            make_float2(o[i][2 * half], o[i][2 * half + 1]);
+                    if ((lane & 3) == 0)
+                        g.stats[slot * g.rows + rr] = half ? make_float2(m1, l1) : make_float2(m0, l0);
+                }
+            }
+            fresh = true;
+        }
+    }
+    if (!ok) {
+        *abort = 1;
+        if (lane == 0)
+            atomicOr(g.a.flag, kFlagTimeout);
+        // one more bounded wait for the copies in flight
+        for (int64_t i = done; i < issued; ++i)
+            (void)attn_wait(&bar[warp][i % kStages], (uint32_t)(i / kStages) & 1u);
+    }
+    // the prefix's grid, launched before this one, is complete before this one is
+    pdl_wait();
+}
+
+// ---------------------------------------------------------------------------
+// 3. the merge: a warp per (sequence, query head), a lane per D / 32 features
+template <typename T, int D>
+__global__ void __launch_bounds__(128) rope_decode_merge_kernel(const __grid_constant__ DecodeArgs g)
+{
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    pdl_wait();
+    if (row >= (int64_t)g.B * g.Hq)
+        return;
+    const int32_t b = (int32_t)(row / g.Hq), h = (int32_t)(row - (int64_t)b * g.Hq);
+    const int32_t group = g.Hq / g.Hk, kv = h / group, in_group = h - kv * group;
+    const int32_t rg = in_group / g.rows, r = in_group - rg * g.rows;
+    const int32_t heads = g.Hk * g.row_groups;
+    int64_t first = 0, last = -1;                  // slots of the pair
+    if (g.warps > 0) {
+        const int64_t c0 = g.chunk_start[b], c1 = g.chunk_start[b + 1];
+        if (c1 > c0) {
+            const int64_t per =
+                decode_per_warp((int64_t)g.chunk_start[g.B] * heads, g.warps, g.min_chunks);
+            const int32_t hr = kv * g.row_groups + rg;
+            const int64_t at = c0 * heads + hr * (c1 - c0), pair = (int64_t)b * heads + hr;
+            first = at / per + pair;
+            last = (at + (c1 - c0) - 1) / per + pair;
+        }
+    }
+    float m = -INFINITY, l = 0.0f, o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        o[i] = 0.0f;
+    auto take = [&](const float2 *stat, const float *src) {
+        const float2 s = *stat;
+        float x[V];
+        if constexpr (V == 4) {
+            const float4 t = *reinterpret_cast<const float4 *>(src + lane * V);
+            x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+        } else {
+            const float2 t = *reinterpret_cast<const float2 *>(src + lane * V);
+            x[0] = t.x; x[1] = t.y;
+        }
+        if (s.y == 0.0f)
+            return;                                // no key (O is not looked at)
+        const float top = fmaxf(m, s.x);
+        const float f = m == -INFINITY ? 0.0f : exp2f(m - top), e = exp2f(s.x - top);
+        l = l * f + s.y * e;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            o[i] = o[i] * f + x[i] * e;
+        m = top;
+    };
+    for (int32_t s = 0; s < g.splits; ++s) {
+        const int64_t at = (int64_t)s * g.B * g.Hq + row;
+        take(g.prefix_stats + at, g.prefix_out + at * D);
+    }
+    for (int64_t s = first; s <= last; ++s)
+        take(g.stats + s * g.rows + r, g.out + (s * g.rows + r) * D);
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    T *dst = static_cast<T *>(g.o) + row * D + lane * V;
+    if constexpr (V == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(Elt<T>::f2_to_word(o[0] * inv, o[1] * inv),
+                                                     Elt<T>::f2_to_word(o[2] * inv, o[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = Elt<T>::f2_to_word(o[0] * inv, o[1] * inv);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+template <typename T, int LAYOUT, int D>
+static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, cudaStream_t st)
+{
+    EncodeTiledFn enc = encode_tiled();
+    if (enc == nullptr)
+        return cudaErrorNotSupported;
+    const CUtensorMapDataType dt = std::is_same<T, __nv_bfloat16>::value
+                                       ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    uint8_t *ws = static_cast<uint8_t *>(c.workspace);
+    const int64_t page = (int64_t)1 << c.page_shift, z = c.n_pages * c.Hk;
+    AttnArgs a;
+    memset(&a, 0, sizeof a);
+    a.cos = c.cos; a.sin = c.sin; a.rotary_dim = c.rotary_dim; a.table_rows = c.table_rows;
+    a.scale_log2 = c.scale_log2; a.flag = c.flag;
+
+    DecodeArgs g;
+    memset(&g, 0, sizeof g);
+    g.a = a;
+    g.q = c.q; g.q_stride = c.q_stride; g.o = c.o;
+    g.table = c.table; g.lens = c.lens; g.pos_q = c.pos_q;
+    g.max_blocks = c.max_blocks; g.n_pages = c.n_pages;
+    g.B = c.B; g.Hq = c.Hq; g.Hk = c.Hk; g.page_shift = c.page_shift; g.n_prefix = c.n_prefix;
+    g.row_groups = lay.row_groups; g.rows = lay.rows; g.min_chunks = lay.min_chunks;
+    g.chunk_start = reinterpret_cast<int32_t *>(ws);
+    g.out = reinterpret_cast<float *>(ws + lay.out);
+    g.stats = reinterpret_cast<float2 *>(ws + lay.stats);
+    g.prefix_out = reinterpret_cast<float *>(ws + lay.prefix_out);
+    g.prefix_stats = reinterpret_cast<float2 *>(ws + lay.prefix_stats);
+    g.splits = c.n_prefix > 0 ? lay.splits : 0;
+    g.warps = lay.suffix_ctas * kDecWarps;
+
+    if (c.n_prefix > 0) {
+        const int32_t gp = packed_group_heads(c.Hq, c.Hk);
+        const int lg = __builtin_ctz((unsigned)gp);
+        const uint32_t box = (uint32_t)(page < 64 ? page : 64), tail = (uint32_t)(c.n_prefix % page);
+        PrefixSource s;
+        memset(&s, 0, sizeof s);
+        s.a = a;
+        if (!encode_3d(enc, &s.k_map, c.k_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, box, 1}, sw) ||
+            !encode_3d(enc, &s.v_map, c.v_pages, dt, {D, page, z}, {D * 2, page * D * 2},
+                       {(uint32_t)D / 2, (uint32_t)page, 1}, D == 128 ? sw : CU_TENSOR_MAP_SWIZZLE_64B) ||
+            !encode_3d(enc, &s.v_tail, c.v_pages, dt, {D, tail > 0 ? tail : page, z}, {D * 2, page * D * 2},
+                       {(uint32_t)D / 2, (uint32_t)page, 1}, D == 128 ? sw : CU_TENSOR_MAP_SWIZZLE_64B) ||
+            !encode_3d(enc, &s.q_map, c.q, dt, {D, c.Hq, c.B}, {D * 2, c.q_stride * 2},
+                       {64, (uint32_t)gp, (uint32_t)(kAttnRows / gp)}, sw))
+            return cudaErrorInvalidValue;
+        s.pages = c.prefix_table; s.pos_q = c.pos_q; s.lens = c.lens;
+        s.max_keys = c.max_blocks << c.page_shift;
+        s.out = reinterpret_cast<float *>(ws + lay.prefix_out);
+        s.stats = reinterpret_cast<float2 *>(ws + lay.prefix_stats);
+        s.n_pages = c.n_pages;
+        s.n_keys = c.n_prefix; s.n_key_tiles = (c.n_prefix + kAttnKeys - 1) / kAttnKeys;
+        s.B = c.B; s.Hq = c.Hq; s.Hk = c.Hk; s.page_shift = c.page_shift;
+        s.row_tiles = lay.row_tiles; s.head_units = c.Hq / gp; s.units_per_kv = c.Hq / c.Hk / gp;
+        s.splits = lay.splits; s.tiles_per_split = lay.tiles_per_split;
+        const cudaError_t e = launch_packed_kernel<T, LAYOUT, D>(
+            s, (int64_t)s.row_tiles * s.head_units * s.splits, lg, st);
+        if (e != cudaSuccess)
+            return e;
+    }
+    if (g.warps > 0) {
+        if (!encode_3d(enc, &g.k_map, c.k_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, kDecKeys, 1}, sw) ||
+            !encode_3d(enc, &g.v_map, c.v_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, kDecKeys, 1}, sw))
+            return cudaErrorInvalidValue;
+        static std::atomic<uint64_t> raised{0};
+        auto *kernel = rope_decode_suffix_kernel<T, LAYOUT, D>;
+        int sms = 0, dev = 0;
+        cudaError_t e = sm_count(&sms, &dev);
+        if (e == cudaSuccess)
+            e = raise_smem(reinterpret_cast<const void *>(kernel), kDecSmem<D>, dev, raised);
+        if (e != cudaSuccess)
+            return e;
+        // without a prefix the suffix kernel comes first in the stream and may
+        // not start before what precedes it is complete
+        if (c.n_prefix > 0) {
+            e = launch_hot(kernel, dim3((unsigned)lay.suffix_ctas), dim3(kDecThreads), (size_t)kDecSmem<D>, st, g);
+        } else {
+            kernel<<<lay.suffix_ctas, kDecThreads, kDecSmem<D>, st>>>(g);
+            e = cudaGetLastError();
+        }
+        if (e != cudaSuccess)
+            return e;
+    }
+    const int64_t rows = (int64_t)c.B * c.Hq;
+    const unsigned blocks = (unsigned)((rows + 3) / 4);
+    return launch_hot(rope_decode_merge_kernel<T, D>, dim3(blocks), dim3(128), 0, st, g);
+}
+
+template <typename T>
+cudaError_t launch_decode_type(const DecodeCall &c, const DecodeLayout &lay, int32_t D, int32_t layout,
+                               cudaStream_t st)
+{
+    if (layout == 0)
+        return D == 64 ? launch_decode<T, 0, 64>(c, lay, st) : launch_decode<T, 0, 128>(c, lay, st);
+    return D == 64 ? launch_decode<T, 1, 64>(c, lay, st) : launch_decode<T, 1, 128>(c, lay, st);
+}
+
+}  // namespace rope

@@ -556,6 +556,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
     };
     // what ran before this launch (the prepare kernel) is complete from here on
     pdl_wait();
+    if constexpr (Source::kPrefix)
+        pdl_trigger();                             // the suffix kernel needs nothing of this one
     // The work units, longest first.  Cluster c takes unit r * clusters + c in
     // even rounds r and r * clusters + clusters - 1 - c in odd ones, so a cluster
     // that got the longer work of one round gets the shorter of the next.

@@ -71,4 +71,37 @@ cudaError_t launch_packed_bf16(const PackedArgs &c, const PackedLayout &lay, int
 cudaError_t launch_packed_f16(const PackedArgs &c, const PackedLayout &lay, int32_t D, int32_t layout,
                               cudaStream_t st);
 
+// Attention of one token per sequence over a shared prefix and a suffix each
+// (rope_attention_decode.cuh).
+struct DecodeCall {
+    const void *q;                   // [B][Hq][D], row stride q_stride
+    int64_t q_stride;
+    const void *k_pages, *v_pages;   // [n_pages][Hk][page][D]
+    void *o;                         // [B][Hq][D]
+    const int32_t *table, *lens;     // [B][max_blocks], [B]
+    const int32_t *prefix_table;
+    const int32_t *pos_q;            // [B] or nullptr
+    const float *cos, *sin;
+    int64_t table_rows, n_pages, max_blocks;
+    int32_t B, Hq, Hk, rotary_dim, page_shift, n_prefix;
+    float scale_log2;
+    void *workspace;
+    int32_t *flag;
+};
+
+// How a decode call is split, and its workspace.
+struct DecodeLayout {
+    int32_t row_tiles, splits, tiles_per_split;      // prefix: units are tiles x head units x splits
+    int32_t row_groups, rows, min_chunks, suffix_ctas;
+    int64_t out, stats, prefix_out, prefix_stats;    // byte offsets
+    int64_t bytes;
+};
+// False when a size overflows or is not taken.
+bool decode_layout(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_shift, int64_t max_blocks,
+                   int64_t n_prefix, DecodeLayout *out);
+cudaError_t launch_decode_bf16(const DecodeCall &c, const DecodeLayout &lay, int32_t D, int32_t layout,
+                               cudaStream_t st);
+cudaError_t launch_decode_f16(const DecodeCall &c, const DecodeLayout &lay, int32_t D, int32_t layout,
+                              cudaStream_t st);
+
 }  // namespace rope

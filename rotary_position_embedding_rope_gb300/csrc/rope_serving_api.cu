@@ -108,6 +108,64 @@ bool packed_layout(int64_t n_seqs, int64_t total_q, int64_t total_k, int32_t Hq,
     return true;
 }
 
+// The SMs the split rules are made for (any other number gives the same
+// results, less evenly spread).
+constexpr int32_t kSms = 152;
+constexpr int32_t kMaxDecodeBatch = 32768;
+
+bool decode_layout(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_shift, int64_t max_blocks,
+                   int64_t n_prefix, DecodeLayout *out)
+{
+    std::memset(out, 0, sizeof *out);
+    const int32_t group = Hq / Hk, gp = packed_group_heads(Hq, Hk);
+    const int64_t rows = product({B, Hq});
+    if (rows < 0 || rows > kMaxInt32)
+        return false;
+    // The prefix: clusters of 256 rows.  With fewer units than clusters (76) the
+    // key tiles are split; the rounds of units times a unit's tiles, with about
+    // four tiles' time for its start and its fp32 partial result, is least.
+    const int64_t tiles = (n_prefix + 127) / 128, clusters = kSms / 2;
+    out->row_tiles = (int32_t)((B + 256 / gp - 1) / (256 / gp));
+    const int64_t units = out->row_tiles * (int64_t)(Hq / gp);
+    out->splits = 1;
+    int64_t best = -1;
+    for (int64_t s = 1; s <= tiles && s <= clusters; ++s) {
+        const int64_t cost = (units * s + clusters - 1) / clusters * ((tiles + s - 1) / s + 4);
+        if (best < 0 || cost < best) {
+            best = cost;
+            out->splits = (int32_t)s;
+        }
+    }
+    out->tiles_per_split = (int32_t)((tiles + out->splits - 1) / out->splits);
+    if (tiles > 0)
+        out->splits = (int32_t)((tiles + out->tiles_per_split - 1) / out->tiles_per_split);
+    // The suffixes: equal runs of 16-key chunks for the warps of one CTA an SM.
+    out->rows = group < 16 ? group : 16;
+    out->row_groups = (group + out->rows - 1) / out->rows;
+    out->min_chunks = 2;
+    const int64_t chunks = product({B, max_blocks, (int64_t)1 << page_shift >> 4});
+    if (chunks < 0 || chunks > kMaxInt32)
+        return false;
+    const int64_t heads = product({Hk, out->row_groups}), all = product({chunks, heads});
+    const int64_t pairs = product({B, heads});
+    if (all < 0 || pairs < 0 || pairs > kMaxInt32 - kSms * 8)
+        return false;
+    const int64_t ctas = (all + 8 * out->min_chunks - 1) / (8 * out->min_chunks);
+    out->suffix_ctas = (int32_t)(ctas < kSms ? ctas : kSms);
+    const int64_t slots = out->suffix_ctas > 0 ? out->suffix_ctas * 8 + pairs : 0;
+    const int64_t o = product({slots, out->rows, D, 4}), s = product({slots, out->rows, 8});
+    const int64_t parts = n_prefix > 0 ? out->splits : 0;
+    const int64_t po = product({parts, rows, D, 4}), ps = product({parts, rows, 8});
+    if (o < 0 || s < 0 || po < 0 || ps < 0 || o > (1ll << 60) || po > (1ll << 60))
+        return false;
+    out->out = round_up(4 * (B + 1), 128);
+    out->stats = out->out + o;
+    out->prefix_out = round_up(out->stats + s, 128);
+    out->prefix_stats = out->prefix_out + po;
+    out->bytes = round_up(out->prefix_stats + ps, 128);
+    return true;
+}
+
 }  // namespace rope
 
 using namespace rope;
@@ -261,6 +319,96 @@ rope_status rope_attention_packed_fwd(const void *q, const void *k, const void *
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == ROPE_BF16 ? launch_packed_bf16(a, lay, D, layout, s)
                                              : launch_packed_f16(a, lay, D, layout, s);
+    return e == cudaSuccess ? ROPE_OK : ROPE_ERR_CUDA;
+}
+
+int64_t rope_attention_decode_workspace(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_size,
+                                        int64_t max_blocks, int64_t prefix_len)
+{
+    const int32_t shift = page_shift(page_size);
+    DecodeLayout lay;
+    if (B < 0 || B > kMaxDecodeBatch || Hq < 0 || Hk < 0 || (D != 64 && D != 128) || shift < 0 ||
+        max_blocks < 0 || prefix_len < 0 || prefix_len > kMaxInt32 - 128)
+        return -1;
+    if (B == 0 || Hq == 0)
+        return 0;
+    if (Hk == 0 || Hq % Hk != 0 || !decode_layout(B, Hq, Hk, D, shift, max_blocks, prefix_len, &lay))
+        return -1;
+    return lay.bytes;
+}
+
+rope_status rope_attention_decode_fwd(const void *q, const void *k_pages, const void *v_pages, void *o,
+                                      const int32_t *block_table, const int32_t *seq_lens,
+                                      const int32_t *prefix_table, int64_t prefix_len,
+                                      const float *cos, const float *sin, const int32_t *pos_q,
+                                      int64_t B, int64_t q_stride, int32_t Hq, int32_t Hk, int32_t D,
+                                      int32_t rotary_dim, int32_t layout, float softmax_scale,
+                                      int32_t page_size, int64_t n_pages, int64_t max_blocks,
+                                      int32_t dtype, int64_t table_rows, void *workspace,
+                                      int64_t workspace_bytes, void *stream)
+{
+    rope_status st = check_shape(dtype, layout, D, rotary_dim);
+    if (st != ROPE_OK)
+        return st;
+    const int32_t shift = page_shift(page_size);
+    if (shift < 0)
+        return ROPE_ERR_UNSUPPORTED;
+    if (softmax_scale != softmax_scale || B < 0 || Hq < 0 || Hk < 0 || n_pages < 0 || max_blocks < 0 ||
+        prefix_len < 0 || prefix_len > kMaxInt32 - 128 || table_rows < 0 || workspace_bytes < 0)
+        return ROPE_ERR_INVALID_ARG;
+    if (B > kMaxDecodeBatch)
+        return ROPE_ERR_UNSUPPORTED;
+    if (Hq > 0 && (Hk == 0 || Hq % Hk != 0))
+        return ROPE_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)Hq * D;
+    if (q_stride < row)
+        return ROPE_ERR_INVALID_ARG;
+    const int64_t z = product({n_pages, Hk});
+    const int64_t qb = view_bytes(B, q_stride, row), ob = product({B, row, 2});
+    const int64_t pool = product({n_pages, Hk, page_size, D, 2});
+    const int64_t tab = product({table_rows, rotary_dim / 2, 4}), blocks = product({B, max_blocks, 4});
+    if (z < 0 || z > kMaxInt32 - 1 || qb < 0 || ob < 0 || pool < 0 || tab < 0 || blocks < 0)
+        return ROPE_ERR_INVALID_ARG;
+    if (B == 0 || Hq == 0)
+        return ROPE_OK;
+    const bool any_keys = prefix_len > 0 || max_blocks > 0;
+    if (!q || !o || !seq_lens || !cos || !sin || table_rows < 1 || (any_keys && (!k_pages || !v_pages)) ||
+        (any_keys && n_pages < 1) || (max_blocks > 0 && !block_table) || (prefix_len > 0 && !prefix_table))
+        return ROPE_ERR_INVALID_ARG;
+    DecodeLayout lay;
+    if (!decode_layout(B, Hq, Hk, D, shift, max_blocks, prefix_len, &lay) || !workspace ||
+        workspace_bytes < lay.bytes)
+        return ROPE_ERR_INVALID_ARG;
+    if (q_stride % 8 != 0 || !aligned(q, 16) || !aligned(o, 16) || !aligned(cos, 16) || !aligned(sin, 16) ||
+        !aligned(workspace, 128) || !aligned(k_pages, 16) || !aligned(v_pages, 16))
+        return ROPE_ERR_UNSUPPORTED;
+    if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(prefix_table, 4) || !aligned(pos_q, 4))
+        return ROPE_ERR_INVALID_ARG;
+    const Range outs[2] = {{o, ob}, {workspace, lay.bytes}};
+    const int64_t prefix_blocks = (prefix_len + page_size - 1) / page_size;
+    const Range ins[9] = {{q, qb}, {k_pages, pool}, {v_pages, pool}, {block_table, blocks},
+                          {seq_lens, 4 * B}, {prefix_table, 4 * prefix_blocks}, {cos, tab}, {sin, tab},
+                          {pos_q, 4 * B}};
+    if (overlap(outs[0], outs[1]))
+        return ROPE_ERR_INVALID_ARG;
+    for (const Range &out : outs)
+        for (const Range &in : ins)
+            if (overlap(out, in))
+                return ROPE_ERR_INVALID_ARG;
+    DecodeCall c;
+    std::memset(&c, 0, sizeof c);
+    c.q = q; c.q_stride = q_stride; c.k_pages = k_pages; c.v_pages = v_pages; c.o = o;
+    c.table = block_table; c.lens = seq_lens; c.prefix_table = prefix_table; c.pos_q = pos_q;
+    c.cos = cos; c.sin = sin; c.table_rows = table_rows; c.n_pages = n_pages; c.max_blocks = max_blocks;
+    c.B = (int32_t)B; c.Hq = Hq; c.Hk = Hk; c.rotary_dim = rotary_dim; c.page_shift = shift;
+    c.n_prefix = (int32_t)prefix_len; c.workspace = workspace;
+    const double scale = softmax_scale > 0.0f ? softmax_scale : 1.0 / std::sqrt((double)D);
+    c.scale_log2 = (float)(scale * 1.4426950408889634);
+    if (device_flag(&c.flag) != cudaSuccess)
+        return ROPE_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == ROPE_BF16 ? launch_decode_bf16(c, lay, D, layout, s)
+                                             : launch_decode_f16(c, lay, D, layout, s);
     return e == cudaSuccess ? ROPE_OK : ROPE_ERR_CUDA;
 }
 

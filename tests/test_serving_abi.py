@@ -107,3 +107,48 @@ def test_packed_workspace(lib):
     assert ws(0, 10, 12, 4, 2, 128) == ws(2, 0, 12, 4, 2, 128) == ws(2, 10, 12, 0, 0, 128) == 0
     assert ws(-1, 10, 12, 4, 2, 128) == ws(2, 10, 12, 4, 3, 128) == ws(2, 10, 12, 4, 2, 96) == -1
     assert ws(2, 10, 1 << 31, 4, 2, 128) == -1
+
+
+DECODE = dict(q=A, kp=2 * A, vp=3 * A, o=4 * A, table=5 * A, lens=6 * A, pt=7 * A, P=40, cos=8 * A, sin=9 * A, pq=None,
+              B=3, qs=512, Hq=4, Hk=2, D=128, rd=128, layout=0, scale=-1.0, page=16, n_pages=20, blocks=4, dtype=1,
+              rows=64, ws=10 * A, wsb=1 << 23)
+
+
+def decode_args(**over):
+    a = dict(DECODE, **over)
+    return [a[x] for x in ("q", "kp", "vp", "o", "table", "lens", "pt", "P", "cos", "sin", "pq", "B", "qs", "Hq", "Hk",
+                           "D", "rd", "layout", "scale", "page", "n_pages", "blocks", "dtype", "rows", "ws",
+                           "wsb")] + [None]
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=0), UNS), (dict(layout=3), UNS), (dict(D=80), UNS), (dict(rd=24), UNS), (dict(page=24), UNS),
+    (dict(page=256), UNS), (dict(B=32769), UNS), (dict(qs=516), UNS), (dict(q=A + 2), UNS), (dict(o=4 * A + 8), UNS),
+    (dict(kp=2 * A + 8), UNS), (dict(sin=9 * A + 8), UNS), (dict(ws=10 * A + 16), UNS),
+    (dict(B=-1), INV), (dict(Hq=5, qs=640), INV), (dict(Hk=0), INV), (dict(qs=504), INV), (dict(P=-1), INV),
+    (dict(P=0x7fffffff), INV), (dict(blocks=-1), INV), (dict(n_pages=0), INV), (dict(n_pages=1 << 30), INV),
+    (dict(blocks=1 << 40), INV), (dict(scale=float("nan")), INV), (dict(rows=0), INV), (dict(q=None), INV),
+    (dict(kp=None), INV), (dict(vp=None), INV), (dict(o=None), INV), (dict(table=None), INV), (dict(lens=None), INV),
+    (dict(pt=None), INV), (dict(cos=None), INV), (dict(ws=None), INV), (dict(wsb=1000), INV), (dict(lens=6 * A + 1), INV),
+    (dict(o=A), INV), (dict(o=3 * A + 128), INV), (dict(ws=2 * A), INV), (dict(ws=6 * A - 128), INV), (dict(ws=4 * A), INV),
+])
+def test_decode_refuses(lib, over, status):
+    assert lib.rope_attention_decode_fwd(*decode_args(**over)) == status
+
+
+@pytest.mark.parametrize("over", [dict(B=0, q=None, o=None, lens=None, table=None),
+                                  dict(Hq=0, Hk=0, qs=0, q=None, o=None)])
+def test_decode_of_nothing(lib, over):
+    assert lib.rope_attention_decode_fwd(*decode_args(ws=None, wsb=0, **over)) == R.ROPE_OK
+
+
+def test_decode_workspace(lib):
+    ws = lib.rope_attention_decode_workspace
+    need = ws(3, 4, 2, 128, 16, 4, 40)
+    assert need > 3 * 4 * 128 * 4 and need % 128 == 0
+    assert lib.rope_attention_decode_fwd(*decode_args(wsb=need - 1)) == INV
+    assert ws(0, 4, 2, 128, 16, 4, 40) == ws(3, 0, 0, 128, 16, 4, 40) == 0
+    assert ws(3, 4, 3, 128, 16, 4, 40) == ws(3, 4, 2, 96, 16, 4, 40) == ws(3, 4, 2, 128, 48, 4, 40) == -1
+    assert ws(40000, 4, 2, 128, 16, 4, 40) == ws(3, 4, 2, 128, 16, 4, -1) == -1
+    # nothing but a prefix, nothing but suffixes
+    assert 0 < ws(3, 4, 2, 128, 16, 0, 40) < need and 0 < ws(3, 4, 2, 128, 16, 4, 0) < need
