@@ -685,88 +685,102 @@ def rope_attention_decode_workspace(B, Hq, Hk, D, page_size, max_blocks, prefix_
 
 class _Call:
     """One serving call: the device its tensors live on and the stream it runs
-    on, with that device current while the library is called."""
+    on, with that device current while the library is called.  A decode step
+    makes several such calls per layer, so the checks are a few attribute reads
+    a tensor; a tensor that fails one is looked at again to say why."""
+
+    __slots__ = ("index", "stream", "other")
 
     def __init__(self, first: torch.Tensor, stream):
-        if not first.is_cuda:
+        self.index = first.get_device()
+        if self.index < 0:
             raise ValueError("expected CUDA tensors, got one on %s" % first.device)
-        self.device = first.device
+        self.other = stream is not None
         if stream is None:
-            self.stream = torch.cuda.current_stream(self.device).cuda_stream
+            self.stream = torch._C._cuda_getCurrentRawStream(self.index)
         elif isinstance(stream, int):
             self.stream = stream
         else:
-            if stream.device != self.device:
-                raise ValueError("the stream belongs to %s, the tensors to %s" %
-                                 (stream.device, self.device))
+            if stream.device.index != self.index:
+                raise ValueError("the stream belongs to %s, the tensors to cuda:%d" %
+                                 (stream.device, self.index))
             self.stream = stream.cuda_stream
 
-    def rows(self, x, name, H=None, D=None, dtype=None):
-        """(address, token stride) of a [T, H, D] tensor, dense but for its tokens."""
-        if x.dim() != 3:
-            raise ValueError("%s must be [tokens, heads, D], got %s" % (name, tuple(x.shape)))
-        t, h, d = x.shape
+    def _wrong(self, x, name, dtype, shape=None):
+        if dtype is not None and x.dtype != dtype:
+            raise ValueError("%s must be a %s tensor, got %s" % (name, dtype, x.dtype))
+        if x.get_device() != self.index:
+            raise ValueError("%s must be on cuda:%d, got %s" % (name, self.index, x.device))
+        if shape is not None and tuple(x.shape) != shape:
+            raise ValueError("%s must be %s, got %s" % (name, shape, tuple(x.shape)))
+        raise ValueError("%s must be contiguous (strides %s)" % (name, x.stride()))
+
+    def rows(self, x, name, dtype, H=None, D=None):
+        """(address, token stride, tokens, heads, D) of a [T, H, D] tensor, dense
+        but for its tokens."""
+        if x.dtype is not dtype or x.get_device() != self.index:
+            self._wrong(x, name, dtype)
+        shape = x.shape
+        if len(shape) != 3:
+            raise ValueError("%s must be [tokens, heads, D], got %s" % (name, tuple(shape)))
+        t, h, d = shape
         if (H is not None and h != H) or (D is not None and d != D):
-            raise ValueError("%s must be [tokens, %s, %s], got %s" % (name, H, D, tuple(x.shape)))
-        if (dtype is not None and x.dtype != dtype) or x.device != self.device:
-            raise ValueError("%s must be a %s tensor on %s" % (name, dtype, self.device))
+            raise ValueError("%s must be [tokens, %s, %s], got %s" % (name, H, D, tuple(shape)))
         st, sh, sd = x.stride()
-        if x.numel() > 0 and ((d > 1 and sd != 1) or (h > 1 and sh != d)):
+        if t > 0 and ((d > 1 and sd != 1) or (h > 1 and sh != d)):
             raise ValueError("%s: heads and features must be dense (strides %s)" %
                              (name, x.stride()))
-        return (x.data_ptr() if x.numel() else None), (st if t > 1 else h * d)
+        return x.data_ptr(), (st if t > 1 else h * d), t, h, d
 
     def dense(self, x, name, dtype, shape=None):
         """Address of a contiguous tensor of the given type (and shape)."""
         if x is None:
             return None
-        if x.dtype != dtype or x.device != self.device:
-            raise ValueError("%s must be a %s tensor on %s, got %s on %s" %
-                             (name, dtype, self.device, x.dtype, x.device))
-        if shape is not None and tuple(x.shape) != shape:
-            raise ValueError("%s must be %s, got %s" % (name, shape, tuple(x.shape)))
-        if not x.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        return x.data_ptr() if x.numel() else None
+        if (x.dtype is not dtype or x.get_device() != self.index or not x.is_contiguous() or
+                (shape is not None and x.shape != shape)):
+            self._wrong(x, name, dtype, shape)
+        return x.data_ptr()
 
     def tables(self, cos, sin, rotary_dim):
         """(cos address, sin address, rotary_dim, rows)."""
-        if cos.dim() != 2 or cos.shape != sin.shape:
+        shape = cos.shape
+        if len(shape) != 2 or shape != sin.shape:
             raise ValueError("cos and sin must be [rows, rotary_dim / 2] tables of the same shape")
-        rd = 2 * cos.shape[1] if rotary_dim is None else rotary_dim
-        if cos.shape[1] * 2 != rd:
-            raise ValueError("table width %d does not match rotary_dim %d" % (cos.shape[1], rd))
-        return (self.dense(cos, "cos", torch.float32), self.dense(sin, "sin", torch.float32), rd,
-                cos.shape[0])
+        rows, half = shape
+        if rotary_dim is not None and rotary_dim != 2 * half:
+            raise ValueError("table width %d does not match rotary_dim %d" % (half, rotary_dim))
+        f32 = torch.float32
+        return self.dense(cos, "cos", f32), self.dense(sin, "sin", f32), 2 * half, rows
 
     def cache(self, k_pages, v_pages, dtype):
         """(k address, v address, pages, Hk, page size, D) of a cache's pools."""
-        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+        shape = k_pages.shape
+        if len(shape) != 4 or shape != v_pages.shape:
             raise ValueError("k_pages and v_pages must be [pages, Hk, page_size, D] of one shape")
-        return (self.dense(k_pages, "k_pages", dtype), self.dense(v_pages, "v_pages", dtype),
-                *k_pages.shape)
+        return (self.dense(k_pages, "k_pages", dtype), self.dense(v_pages, "v_pages", dtype), *shape)
+
+    def empty(self, shape, dtype):
+        """A new tensor, alive until the call's stream is done with it."""
+        x = torch.empty(shape, dtype=dtype, device=self.index)
+        if self.other:
+            x.record_stream(torch.cuda.ExternalStream(self.stream, device=self.index))
+        return x
 
     def workspace(self, given, need, name):
-        """(address, bytes) of the call's workspace: the given tensor, or a new
-        one that stays alive until the call's stream is done with it."""
+        """The call's workspace: the given tensor, or a new one (None: none needed)."""
         if need < 0:
             raise RopeError(ROPE_ERR_INVALID_ARG, name)
-        if given is not None:
-            if given.device != self.device or not given.is_contiguous():
-                raise ValueError("workspace must be a contiguous tensor on %s" % self.device)
-            return given.data_ptr(), given.numel() * given.element_size()
-        if need == 0:
-            return None, 0
-        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        if self.stream != torch.cuda.current_stream(self.device).cuda_stream:
-            ws.record_stream(torch.cuda.ExternalStream(self.stream, self.device))
-        return ws.data_ptr(), need
+        if given is None:
+            return self.empty(need, torch.uint8) if need else None
+        if given.get_device() != self.index or not given.is_contiguous():
+            self._wrong(given, "workspace", None)
+        return given
 
     def run(self, fn, name, *args):
-        if self.device.index == torch.cuda.current_device():
+        if self.index == torch.cuda.current_device():
             st = fn(*args, self.stream)
         else:
-            with torch.cuda.device(self.device):
+            with torch.cuda.device(self.index):
                 st = fn(*args, self.stream)
         if st != ROPE_OK:
             raise RopeError(st, name)
@@ -795,18 +809,18 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     key's index in its sequence.
     """
     c = _Call(k, stream)
+    dtype, i32 = k.dtype, torch.int32
     code = _type16(k, "cache_append")
-    kp, vp, n_pages, Hk, page, D = c.cache(k_pages, v_pages, k.dtype)
-    ka, ks = c.rows(k, "k", Hk, D, k.dtype)
-    va, vs = c.rows(v, "v", Hk, D, k.dtype)
-    T = k.shape[0]
-    if v.shape[0] != T:
+    kp, vp, n_pages, Hk, page, D = c.cache(k_pages, v_pages, dtype)
+    ka, ks, T, _, _ = c.rows(k, "k", dtype, Hk, D)
+    va, vs, Tv, _, _ = c.rows(v, "v", dtype, Hk, D)
+    if Tv != T:
         raise ValueError("k and v must have the same tokens")
-    if block_table.dim() != 2:
+    shape = block_table.shape
+    if len(shape) != 2:
         raise ValueError("block_table must be [n_seqs, max_blocks]")
-    n, blocks = block_table.shape
+    n, blocks = shape
     ca, sa, rd, rows = c.tables(cos, sin, rotary_dim)
-    i32 = torch.int32
     c.run(load_library().rope_cache_append, "rope_cache_append", ka, va, kp, vp,
           c.dense(block_table, "block_table", i32), c.dense(cu_seqlens, "cu_seqlens", i32, (n + 1,)),
           c.dense(cache_lens, "cache_lens", i32, (n,)), ca, sa, c.dense(pos, "pos", i32, (T,)),
@@ -835,33 +849,29 @@ def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     bytes to use (128-byte aligned; its contents do not matter).
     """
     c = _Call(q, stream)
+    dtype, i32 = q.dtype, torch.int32
     code = _type16(q, "attention_packed")
-    qa, qs = c.rows(q, "q", dtype=q.dtype)
-    Tq, Hq, D = q.shape
-    ka, ks = c.rows(k, "k", D=D, dtype=q.dtype)
-    Tk, Hk, _ = k.shape
-    va, vs = c.rows(v, "v", Hk, D, q.dtype)
-    if v.shape[0] != Tk:
+    qa, qs, Tq, Hq, D = c.rows(q, "q", dtype)
+    ka, ks, Tk, Hk, _ = c.rows(k, "k", dtype, None, D)
+    va, vs, Tv, _, _ = c.rows(v, "v", dtype, Hk, D)
+    if Tv != Tk:
         raise ValueError("k and v must have the same tokens")
     if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 1:
         raise ValueError("cu_seqlens_q must be int32 [n_seqs + 1]")
-    if cu_seqlens_k is None:
-        cu_seqlens_k = cu_seqlens_q
     n = cu_seqlens_q.shape[0] - 1
+    cuq = c.dense(cu_seqlens_q, "cu_seqlens_q", i32)
+    cuk = cuq if cu_seqlens_k is None else c.dense(cu_seqlens_k, "cu_seqlens_k", i32, (n + 1,))
     ca, sa, rd, rows = c.tables(cos, sin, rotary_dim)
     if out is None:
-        out = torch.empty((Tq, Hq, D), dtype=q.dtype, device=q.device)
-        if c.stream != torch.cuda.current_stream(c.device).cuda_stream:
-            out.record_stream(torch.cuda.ExternalStream(c.stream, c.device))
-    i32 = torch.int32
+        out = c.empty((Tq, Hq, D), dtype)
     lib = load_library()
-    ws, ws_bytes = c.workspace(workspace, lib.rope_attention_packed_workspace(n, Tq, Tk, Hq, Hk, D),
-                               "rope_attention_packed_workspace")
+    ws = c.workspace(workspace, lib.rope_attention_packed_workspace(n, Tq, Tk, Hq, Hk, D),
+                     "rope_attention_packed_workspace")
     c.run(lib.rope_attention_packed_fwd, "rope_attention_packed_fwd", qa, ka, va,
-          c.dense(out, "out", q.dtype, (Tq, Hq, D)), ca, sa, c.dense(pos_q, "pos_q", i32, (Tq,)),
-          c.dense(pos_k, "pos_k", i32, (Tk,)), c.dense(cu_seqlens_q, "cu_seqlens_q", i32, (n + 1,)),
-          c.dense(cu_seqlens_k, "cu_seqlens_k", i32, (n + 1,)), n, Tq, Tk, qs, ks, vs, Hq, Hk, D, rd,
-          _LAYOUT_CODE[layout], int(causal), -1.0 if scale is None else scale, code, rows, ws, ws_bytes)
+          c.dense(out, "out", dtype, (Tq, Hq, D)), ca, sa, c.dense(pos_q, "pos_q", i32, (Tq,)),
+          c.dense(pos_k, "pos_k", i32, (Tk,)), cuq, cuk, n, Tq, Tk, qs, ks, vs, Hq, Hk, D, rd,
+          _LAYOUT_CODE[layout], int(causal), -1.0 if scale is None else scale, code, rows,
+          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes)
     return out
 
 
@@ -887,31 +897,30 @@ def attention_shared_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
     bytes to use (128-byte aligned; its contents do not matter).
     """
     c = _Call(q, stream)
+    dtype, i32 = q.dtype, torch.int32
     code = _type16(q, "attention_shared_prefix")
-    qa, qs = c.rows(q, "q", dtype=q.dtype)
-    B, Hq, D = q.shape
-    kp, vp, n_pages, Hk, page, d = c.cache(k_pages, v_pages, q.dtype)
+    qa, qs, B, Hq, D = c.rows(q, "q", dtype)
+    kp, vp, n_pages, Hk, page, d = c.cache(k_pages, v_pages, dtype)
     if d != D:
         raise ValueError("the cache holds heads of %d features, q of %d" % (d, D))
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B:
         raise ValueError("block_table must be [%d, max_blocks]" % B)
-    blocks = block_table.shape[1]
+    blocks = shape[1]
     ca, sa, rd, rows = c.tables(cos, sin, rotary_dim)
-    i32 = torch.int32
     pt = c.dense(prefix_table, "prefix_table", i32)
     if prefix_len > 0 and (prefix_table is None or prefix_table.numel() * page < prefix_len):
         raise ValueError("prefix_table must name the pages of %d keys" % prefix_len)
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
-        if c.stream != torch.cuda.current_stream(c.device).cuda_stream:
-            out.record_stream(torch.cuda.ExternalStream(c.stream, c.device))
+        out = c.empty((B, Hq, D), dtype)
     lib = load_library()
-    ws, ws_bytes = c.workspace(workspace, lib.rope_attention_decode_workspace(B, Hq, Hk, D, page, blocks,
-                                                                              prefix_len),
-                               "rope_attention_decode_workspace")
+    ws = c.workspace(workspace, lib.rope_attention_decode_workspace(B, Hq, Hk, D, page, blocks,
+                                                                    prefix_len),
+                     "rope_attention_decode_workspace")
     c.run(lib.rope_attention_decode_fwd, "rope_attention_decode_fwd", qa, kp, vp,
-          c.dense(out, "out", q.dtype, (B, Hq, D)), c.dense(block_table, "block_table", i32),
+          c.dense(out, "out", dtype, (B, Hq, D)), c.dense(block_table, "block_table", i32),
           c.dense(seq_lens, "seq_lens", i32, (B,)), pt, prefix_len, ca, sa,
           c.dense(pos_q, "pos_q", i32, (B,)), B, qs, Hq, Hk, D, rd, _LAYOUT_CODE[layout],
-          -1.0 if scale is None else scale, page, n_pages, blocks, code, rows, ws, ws_bytes)
+          -1.0 if scale is None else scale, page, n_pages, blocks, code, rows,
+          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes)
     return out

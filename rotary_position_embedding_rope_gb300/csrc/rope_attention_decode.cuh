@@ -11,13 +11,17 @@
 // So the parts run apart, and each key is read once:
 //   1. the prefix, once for the whole batch: its rows (sequence, head) are the
 //      rows of rope_attn_packed_kernel's tiles (the batch is a "sequence" of B
-//      tokens), its keys come from pages, its key tiles are split over clusters
-//      when there are few rows; every unit leaves an fp32 (O, m, l);
+//      tokens), its keys come from pages, its key tiles are dealt out evenly to
+//      clusters; every piece of a head's keys leaves an fp32 (O, m, l);
 //   2. rope_decode_suffix_kernel: every warp an equal run of 16-key chunks of
 //      all suffixes, laid end to end, so that ragged lengths balance;
 //   3. rope_decode_merge_kernel.
-// 1 and 2 do not depend on one another: 2 is launched while 1 runs and fills
-// the SMs that 1 leaves.
+// 1 and 2 do not depend on one another and run side by side: the prefix kernel
+// gives itself as many clusters as decode_plan finds best for the suffixes'
+// lengths, its other CTAs leave at once, and the suffix kernel, launched while
+// the prefix kernel runs, takes the SMs they leave.  When the batch has no more
+// than 16 rows per key head, the prefix is one more sequence of kernel 2, with
+// all the rows of the batch: a call of two small launches.
 //
 // What bounds it: bytes -- the prefix once, every suffix once; from about 300
 // rows per key head on, the prefix products.
@@ -28,110 +32,74 @@
 namespace rope {
 
 // ---------------------------------------------------------------------------
-// 1. the prefix: units of (row tile, head unit, split of the key tiles)
-struct PrefixSource {
-    static constexpr bool kPrefix = true;
-    AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, flag
-    CUtensorMap k_map, v_map, v_tail, q_map;   // v_tail: pages of n_keys mod page rows
-    const int32_t *pages;                      // the prefix's block list
-    const int32_t *pos_q, *lens;               // [B]
-    int64_t max_keys;                          // most keys of a suffix (longer lengths are bad)
-    float *out;                                // [splits][B][Hq][D]
-    float2 *stats;                             // [splits][B][Hq] (m, l)
-    int64_t n_pages;
-    int32_t n_keys, n_key_tiles, B, Hq, Hk, page_shift;
-    int32_t row_tiles, head_units, units_per_kv, splits, tiles_per_split;
+// How a call is dealt out to the SMs.
 
-    __device__ __forceinline__ int64_t units() const
-    {
-        return (int64_t)row_tiles * head_units * splits;
-    }
-    // consecutive units: the row tiles of one key range and key head, so that
-    // the clusters that read the same keys do so at about the same time
-    __device__ __forceinline__ PackedUnit unit(int64_t L, int lg) const
-    {
-        const int64_t i = L / row_tiles;
-        PackedUnit u;
-        u.tok0 = (int32_t)(L - i * row_tiles) * (2 * kAttnRows >> lg);
-        const int32_t hu = (int32_t)(i % head_units);
-        u.split = (int32_t)(i / head_units);
-        u.seq = 0; u.q_start = 0; u.tokens = B; u.n_keys = n_keys;
-        u.head0 = hu << lg;
-        u.kv = hu / units_per_kv;
-        u.first = u.split * tiles_per_split;
-        const int32_t left = n_key_tiles - u.first;
-        u.n_tiles = left < tiles_per_split ? left : tiles_per_split;
-        return u;
-    }
-    __device__ __forceinline__ int32_t tiles(int64_t L) const
-    {
-        const int32_t first = (int32_t)(L / row_tiles / head_units) * tiles_per_split;
-        const int32_t left = n_key_tiles - first;
-        return left < tiles_per_split ? left : tiles_per_split;
-    }
-    __device__ __forceinline__ int64_t table_row(const PackedUnit &, int32_t t) const;
+constexpr int kDecKeys = 16;                       // keys of a suffix chunk
+constexpr int kDecWarps = 8;                       // suffix warps of an SM
 
-    // z of a prefix page in the pools' maps; past the last page, and for a bad
-    // page number, an index that arrives as zeros
-    __device__ __forceinline__ int32_t page_z(int32_t i, int32_t kv) const
-    {
-        const int32_t none = (int32_t)(n_pages * Hk);
-        if ((int64_t)i << page_shift >= n_keys)
-            return none;
-        const int32_t p = __ldg(pages + i);
-        if (p < 0 || p >= n_pages) {
-            atomicOr(a.flag, kFlagIndex);
-            return none;
-        }
-        return p * Hk + kv;
-    }
-    template <int D>
-    __device__ __forceinline__ void load_keys(const PackedUnit &u, int32_t kt, uint8_t *dst, uint64_t *bar,
-                                              uint32_t rank, int lane) const
-    {
-        const int32_t shift = page_shift < 6 ? page_shift : 6;      // keys of a box: a page or half of one
-        const int32_t boxes = (64 >> shift) * (D / 64);
-        if (lane < boxes) {
-            const int32_t i = lane / (D / 64), x = lane % (D / 64);
-            const int32_t key = (u.first + kt) * kAttnKeys + 64 * (int)rank + (i << shift);
-            load_half_box(dst + x * 8192 + (i << shift) * 128, &k_map, x * 64,
-                          key & ((1 << page_shift) - 1), page_z(key >> page_shift, u.kv), bar, rank);
-        }
-    }
-    template <int D>
-    __device__ __forceinline__ void load_values(const PackedUnit &u, int32_t kt, uint8_t *dst,
-                                                uint64_t *bar, uint32_t rank, int lane) const
-    {
-        const int32_t boxes = kAttnKeys >> page_shift;
-        if (lane < boxes) {
-            const int32_t page = ((u.first + kt) * kAttnKeys >> page_shift) + lane;
-            // the last, partly filled page: rows past the prefix arrive as zeros
-            const bool tail = page == n_keys >> page_shift;
-            load_half_box(dst + (lane << page_shift) * D, tail ? &v_tail : &v_map, D / 2 * (int)rank, 0,
-                          page_z(page, u.kv), bar, rank);
-        }
-    }
-    // One helper warp: its rows' O, m and l, in fp32
-    template <int D>
-    __device__ __forceinline__ void store_rows(const PackedUnit &u, uint32_t o_base, int32_t y0, int lane,
-                                               int lg, float2 stat) const
-    {
-        const int32_t tok = y0 + (lane >> lg);
-        const int64_t row = ((int64_t)u.split * B + tok) * Hq + u.head0 + (lane & ((1 << lg) - 1));
-        if (tok < B)
-            stats[row] = stat;
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-            float ov[32];
-            tmem_ld32(o_base + c0, ov);
-            if (tok < B) {
-#pragma unroll
-                for (int c = 0; c < 32; c += 4)
-                    *reinterpret_cast<float4 *>(out + row * D + c0 + c) =
-                        make_float4(ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
-            }
-        }
-    }
+// The sizes decode_plan goes by.
+struct PlanSizes {
+    int32_t row_tiles, head_units, tiles;          // the prefix: cluster tiles of all units
+    int32_t clusters, sms;                         // most prefix clusters; SMs
+    int32_t tile_ns;                               // a cluster's time per key tile
+    int32_t heads, chunk_bytes;                    // pairs of a sequence; keys and values of a chunk
+    float prefix_bytes;
+};
+
+// The prefix on c clusters: `groups` of them (one cluster per row tile in each)
+// take `per` consecutive (head unit, key tile) each.
+struct PrefixDeal {
+    int32_t clusters, groups, per;
+};
+
+__host__ __device__ inline PrefixDeal prefix_deal(const PlanSizes &p, int32_t c)
+{
+    PrefixDeal d;
+    d.clusters = c;
+    d.groups = c / p.row_tiles > 0 ? c / p.row_tiles : 1;
+    d.per = (p.head_units * p.tiles + d.groups - 1) / d.groups;
+    return d;
+}
+
+// Estimated time, in ns, with c clusters on the prefix and the suffixes' chunks
+// (of one pair per sequence) on the SMs left over -- or, with every cluster on
+// the prefix, after it.  Rates measured here: tile_ns a cluster tile, 4 us
+// from one unit to the next, 45 bytes/ns for the copies of one SM and 6500 for
+// all.  An estimate that is off costs balance, never a result.
+__host__ __device__ inline float plan_ns(const PlanSizes &p, int32_t c, float chunks)
+{
+    const PrefixDeal d = prefix_deal(p, c);
+    const int32_t rounds = (p.row_tiles + c - 1) / c;
+    const float prefix = 5000.0f + (float)rounds * ((float)d.per * (float)p.tile_ns +
+                                                    4000.0f * (float)(1 + d.per / p.tiles));
+    const float bytes = chunks * (float)p.heads * (float)p.chunk_bytes;
+    if (bytes == 0.0f)
+        return prefix;
+    if (2 * c >= p.sms)
+        return prefix + 6000.0f + bytes / 6500.0f;
+    const float suffix = 6000.0f + bytes / (45.0f * (float)(p.sms - 2 * c));
+    const float both = 6000.0f + (bytes + p.prefix_bytes) / 6500.0f;
+    return fmaxf(fmaxf(prefix, suffix), both);
+}
+
+// Clusters for the prefix, by every thread of a CTA of at least p.clusters
+// threads (key: one shared word).
+__device__ __forceinline__ int32_t plan_clusters(const PlanSizes &p, int64_t chunks, unsigned long long *key)
+{
+    if (threadIdx.x == 0)
+        *key = ~0ull;
+    __syncthreads();
+    const int32_t c = threadIdx.x + 1;
+    if (c <= p.clusters)
+        atomicMin(key, (unsigned long long)__float_as_uint(plan_ns(p, c, (float)chunks)) << 32 | (unsigned)c);
+    __syncthreads();
+    return (int32_t)(*key & 0xffffffffu);
+}
+
+// What the merge has to know of the deal, in the workspace.
+struct DecodeDeal {
+    int64_t suffix_per;                            // chunks of a warp
+    int32_t prefix_per, pad;                       // (head unit, key tile)s of a group
 };
 
 // The keys of sequence b's suffix; a length out of range raises the flag and
@@ -161,6 +129,172 @@ __device__ __forceinline__ int64_t query_row(const int32_t *pos_q, int32_t b, in
     return r;
 }
 
+// ---------------------------------------------------------------------------
+// 1. the prefix
+struct PrefixSource {
+    static constexpr bool kPrefix = true;
+    AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, flag
+    CUtensorMap k_map, v_map, v_tail, q_map;   // v_tail: pages of n_keys mod page rows
+    PlanSizes sizes;
+    const int32_t *pages;                      // the prefix's block list
+    const int32_t *pos_q, *lens;               // [B]
+    int64_t max_keys;                          // most keys of a suffix (longer lengths are bad)
+    DecodeDeal *deal;
+    float *out;                                // [parts][B][GP][D]: part group + head unit
+    float2 *stats;                             // [parts][B][GP] (m, l)
+    int64_t n_pages;
+    int32_t n_keys, B, Hk, page_shift, units_per_kv;
+
+    // Virtual cluster v: row tile v mod row_tiles of group v / row_tiles, whose
+    // range of (head unit, key tile) is cut at the heads; a cluster takes v = cid,
+    // cid + clusters, ...  The clusters of a group read the same keys at about the
+    // same time.
+    struct Cursor {
+        int32_t v, at, end;
+    };
+    struct Walk {
+        int32_t cid, clusters, groups, per;
+    };
+    __device__ __forceinline__ Walk walk(int64_t cid, int64_t) const
+    {
+        __shared__ unsigned long long key;
+        __shared__ int32_t warp_sum[kPackedThreads / 32];
+        // chunks of all suffixes, and from them the clusters that work
+        int32_t n = 0;
+        for (int32_t b = threadIdx.x; b < B; b += kPackedThreads)
+            n += (suffix_keys(lens, b, max_keys, a.flag) + kDecKeys - 1) / kDecKeys;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if ((threadIdx.x & 31) == 0)
+            warp_sum[threadIdx.x >> 5] = n;
+        __syncthreads();
+        int64_t chunks = 0;
+        for (int w = 0; w < kPackedThreads / 32; ++w)
+            chunks += warp_sum[w];
+        const PrefixDeal d = prefix_deal(sizes, plan_clusters(sizes, chunks, &key));
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            deal->prefix_per = d.per;
+        return {(int32_t)cid, d.clusters, d.groups, d.per};
+    }
+    __device__ __forceinline__ Cursor start(const Walk &w, int32_t v) const
+    {
+        const int32_t all = sizes.head_units * sizes.tiles;
+        Cursor c;
+        c.v = v;
+        c.at = v / sizes.row_tiles * w.per;
+        c.end = all - c.at < w.per ? all : c.at + w.per;
+        return c;
+    }
+    __device__ __forceinline__ Cursor first(const Walk &w) const
+    {
+        // (a cluster past the plan's starts behind the last virtual one)
+        return start(w, w.cid < w.clusters ? w.cid : w.groups * sizes.row_tiles);
+    }
+    __device__ __forceinline__ bool valid(const Walk &w, const Cursor &c) const
+    {
+        return c.v < w.groups * sizes.row_tiles && c.at < c.end;
+    }
+    __device__ __forceinline__ int32_t tiles(const Walk &, const Cursor &c) const
+    {
+        const int32_t head_end = sizes.tiles - c.at % sizes.tiles;
+        return c.end - c.at < head_end ? c.end - c.at : head_end;
+    }
+    __device__ __forceinline__ void next(const Walk &w, Cursor &c) const
+    {
+        c.at += tiles(w, c);
+        if (c.at >= c.end)
+            c = start(w, c.v + w.clusters);
+    }
+    __device__ __forceinline__ PackedUnit unit(const Walk &w, const Cursor &c, int lg) const
+    {
+        const int32_t hu = c.at / sizes.tiles, group = c.v / sizes.row_tiles;
+        PackedUnit u;
+        u.tok0 = (c.v - group * sizes.row_tiles) * (2 * kAttnRows >> lg);
+        u.seq = 0; u.q_start = 0; u.tokens = B; u.n_keys = n_keys;
+        u.head0 = hu << lg;
+        u.kv = hu / units_per_kv;
+        u.first = c.at - hu * sizes.tiles;
+        u.n_tiles = tiles(w, c);
+        u.part = group + hu;
+        return u;
+    }
+    __device__ __forceinline__ int64_t table_row(const PackedUnit &, int32_t t) const;
+
+    // z of a prefix page in the pools' maps; past the last page, and for a bad
+    // page number, an index that arrives as zeros
+    __device__ __forceinline__ int32_t page_z(int32_t i, int32_t kv) const
+    {
+        const int32_t none = (int32_t)(n_pages * Hk);
+        if ((int64_t)i << page_shift >= n_keys)
+            return none;
+        const int32_t p = __ldg(pages + i);
+        if (p < 0 || p >= n_pages) {
+            atomicOr(a.flag, kFlagIndex);
+            return none;
+        }
+        return p * Hk + kv;
+    }
+    // Where this lane's boxes of a tile lie, looked up before the stage is waited
+    // for: keys (box i of a half, features 64 x ..) and values (page i).
+    template <int D>
+    __device__ __forceinline__ int32_t key_place(const PackedUnit &u, int32_t kt, uint32_t rank, int lane) const
+    {
+        const int32_t shift = page_shift < 6 ? page_shift : 6;      // keys of a box: a page or half of one
+        const int32_t key = (u.first + kt) * kAttnKeys + 64 * (int)rank + (lane / (D / 64) << shift);
+        return lane < (64 >> shift) * (D / 64) ? page_z(key >> page_shift, u.kv) : 0;
+    }
+    template <int D>
+    __device__ __forceinline__ int32_t value_place(const PackedUnit &u, int32_t kt, int lane) const
+    {
+        return lane < kAttnKeys >> page_shift
+                   ? page_z(((u.first + kt) * kAttnKeys >> page_shift) + lane, u.kv)
+                   : 0;
+    }
+    template <int D>
+    __device__ __forceinline__ void load_keys(const PackedUnit &, int32_t, int32_t z, uint8_t *dst,
+                                              uint64_t *bar, uint32_t rank, int lane) const
+    {
+        const int32_t shift = page_shift < 6 ? page_shift : 6;
+        if (lane < (64 >> shift) * (D / 64)) {
+            const int32_t i = lane / (D / 64), x = lane % (D / 64);
+            load_half_box(dst + x * 8192 + (i << shift) * 128, &k_map, x * 64,
+                          (64 * (int)rank + (i << shift)) & ((1 << page_shift) - 1), z, bar, rank);
+        }
+    }
+    template <int D>
+    __device__ __forceinline__ void load_values(const PackedUnit &u, int32_t kt, int32_t z, uint8_t *dst,
+                                                uint64_t *bar, uint32_t rank, int lane) const
+    {
+        if (lane < kAttnKeys >> page_shift) {
+            const int32_t page = ((u.first + kt) * kAttnKeys >> page_shift) + lane;
+            // the last, partly filled page: rows past the prefix arrive as zeros
+            const bool tail = page == n_keys >> page_shift;
+            load_half_box(dst + (lane << page_shift) * D, tail ? &v_tail : &v_map, D / 2 * (int)rank, 0,
+                          z, bar, rank);
+        }
+    }
+    // One helper warp: its rows' O, m and l, in fp32
+    template <int D>
+    __device__ __forceinline__ void store_rows(const PackedUnit &u, uint32_t o_base, int32_t y0, int lane,
+                                               int lg, float2 stat) const
+    {
+        const int32_t tok = y0 + (lane >> lg);
+        const int64_t row = (((int64_t)u.part * B + tok) << lg) + (lane & ((1 << lg) - 1));
+        if (tok < B)
+            stats[row] = stat;
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+            float ov[32];
+            tmem_ld32(o_base + c0, ov);
+            if (tok < B) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 4)
+                    *reinterpret_cast<float4 *>(out + row * D + c0 + c) =
+                        make_float4(ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
+            }
+        }
+    }
+};
+
 __device__ __forceinline__ int64_t PrefixSource::table_row(const PackedUnit &, int32_t t) const
 {
     const int64_t keys = pos_q != nullptr ? 0 : (int64_t)n_keys + suffix_keys(lens, t, max_keys, a.flag);
@@ -184,9 +318,7 @@ __device__ __forceinline__ int64_t PrefixSource::table_row(const PackedUnit &, i
 // arrive by TMA (boxes of 64 features x 16 keys, 128-byte swizzle, so ldmatrix
 // reads without conflicts), three stages (D = 128; six for D = 64) a warp, eight
 // warps an SM: 192 KB in flight or in use.
-constexpr int kDecWarps = 8;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kDecKeys = 16;
 template <int D>
 static constexpr int kDecStages = D == 128 ? 3 : 6;
 template <int D>
@@ -199,27 +331,41 @@ static constexpr int kDecSmem = kDecWarps * (kDecStages<D> * kDecStageBytes<D> +
 struct DecodeArgs {
     AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, flag
     CUtensorMap k_map, v_map;                  // boxes of 64 features x 16 keys
+    PlanSizes sizes;
     const void *q;                             // [B][Hq][D], row stride q_stride
     int64_t q_stride;
     void *o;                                   // [B][Hq][D]
-    const int32_t *table, *lens, *pos_q;
+    const int32_t *table, *prefix_table, *lens, *pos_q;
     int64_t max_blocks, n_pages;
     int32_t B, Hq, Hk, page_shift, n_prefix;
+    int32_t fold;                              // 1: the prefix is sequence B of the suffix kernel
     int32_t row_groups, rows;                  // of a key head's query heads; rows of a group
-    int32_t min_chunks;                        // of a warp
+    int32_t slot_rows;                         // rows kept per slot (with fold also B * group)
+    int32_t lg;                                // log2 of the heads of a prefix tile's token
     // partial results
-    int32_t *chunk_start;                      // [B + 1]: chunks per pair of the sequences before b
-    float *out;                                // [slots][rows][D]
-    float2 *stats;                             // [slots][rows]
-    const float *prefix_out;                   // [splits][B][Hq][D]
+    DecodeDeal *deal;
+    int32_t *chunk_start;                      // [B + fold + 1]: chunks per pair of the sequences before b
+    float *out;                                // [slots][slot_rows][D]
+    float2 *stats;                             // [slots][slot_rows]
+    const float *prefix_out;                   // PrefixSource::out
     const float2 *prefix_stats;
-    int32_t splits, warps;                     // warps: of the suffix grid (0: no suffixes)
+    int32_t prefix_tiles;                      // key tiles of the prefix kernel (0: it does not run)
+    int32_t suffix;                            // 1: the suffix kernel runs
 };
 
-__device__ __forceinline__ int64_t decode_per_warp(int64_t chunks, int32_t warps, int32_t min_chunks)
+// Chunks of a warp: an equal share, and no less than two, so that few warps'
+// results meet in the merge.
+constexpr int kDecMinChunks = 2;
+__device__ __forceinline__ int64_t decode_per_warp(int64_t chunks, int32_t warps)
 {
     const int64_t per = (chunks + warps - 1) / warps;
-    return per < min_chunks ? min_chunks : per;
+    return per < kDecMinChunks ? kDecMinChunks : per;
+}
+
+// Keys of sequence b, the folded prefix (b = B) included.
+__device__ __forceinline__ int32_t decode_keys(const DecodeArgs &g, int32_t b, int64_t most)
+{
+    return b < g.B ? suffix_keys(g.lens, b, most, g.a.flag) : g.n_prefix;
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
@@ -265,41 +411,58 @@ struct ChunkAt {
             return;
         hr = 0;
         do {
-            if (++b >= g.B) {
+            if (++b >= g.B + g.fold) {
                 n = 0;
                 return;
             }
-            n = (suffix_keys(g.lens, b, most, g.a.flag) + kDecKeys - 1) / kDecKeys;
+            n = (decode_keys(g, b, most) + kDecKeys - 1) / kDecKeys;
         } while (n == 0);
     }
 };
 
 // 16 rows of rotated queries of pair (b, hr) into the warp's tile (zeros past
-// the group's rows), then as the A operand of every 16-feature step.
+// the pair's rows), then as the A operand of every 16-feature step.  The rows
+// are heads of one sequence, or, for the folded prefix, of the whole batch.
 template <typename T, int LAYOUT, int D>
-__device__ __forceinline__ void load_query_rows(const DecodeArgs &g, const ChunkAt &at, int64_t keys,
+__device__ __forceinline__ void load_query_rows(const DecodeArgs &g, const ChunkAt &at, int64_t most,
                                                 uint8_t *tile, uint32_t (&qf)[D / 16][4])
 {
-    constexpr int L = D / 16, kRowsAtOnce = 32 / L;
+    constexpr int L = D / 16, kAtOnce = 32 / L, kSteps = 16 / kAtOnce;
     const int lane = threadIdx.x & 31, j = lane % L;
     const int32_t kv = at.hr / g.row_groups, group = g.Hq / g.Hk;
     const int32_t r0 = (at.hr - kv * g.row_groups) * g.rows;
     const RowPart part = row_part<LAYOUT>(j, g.a.rotary_dim);
-    const int64_t trow = query_row(g.pos_q, at.b, keys, g.a.table_rows, g.a.flag);
-    const T *base = static_cast<const T *>(g.q) + at.b * g.q_stride + (int64_t)(kv * group + r0) * D;
-    uint4 x0[16 / kRowsAtOnce], x1[16 / kRowsAtOnce];
+    uint4 x0[kSteps], x1[kSteps];
+    int64_t trow[kSteps];
 #pragma unroll
-    for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
-        const int r = i * kRowsAtOnce + lane / L;
+    for (int i = 0; i < kSteps; ++i) {
+        int32_t r = i * kAtOnce + lane / L, b = at.b;
+        bool live = r < g.rows && r0 + r < group;
+        if (b == g.B) {                        // the folded prefix
+            b = r / group;
+            r -= b * group;
+            live = b < g.B;
+        }
         x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
-        if (r < g.rows && r0 + r < group) {
-            x0[i] = __ldg(reinterpret_cast<const uint4 *>(base + r * D + part.o0));
-            x1[i] = __ldg(reinterpret_cast<const uint4 *>(base + r * D + part.o1));
+        trow[i] = -1;
+        if (live) {
+            const T *row = static_cast<const T *>(g.q) + b * g.q_stride + (int64_t)(kv * group + r0 + r) * D;
+            x0[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o0));
+            x1[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o1));
+            if (part.rot)
+                trow[i] = query_row(g.pos_q, b,
+                                    g.pos_q != nullptr ? 0
+                                                       : (int64_t)g.n_prefix +
+                                                             suffix_keys(g.lens, b, most, g.a.flag),
+                                    g.a.table_rows, g.a.flag);
         }
     }
-    if (part.rot && trow >= 0) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        if (trow[i] < 0)
+            continue;
         float c[8], s[8];
-        const int64_t w = trow * (g.a.rotary_dim / 2) + 8 * j;
+        const int64_t w = trow[i] * (g.a.rotary_dim / 2) + 8 * j;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const float4 c4 = __ldg(reinterpret_cast<const float4 *>(g.a.cos + w) + q);
@@ -307,14 +470,12 @@ __device__ __forceinline__ void load_query_rows(const DecodeArgs &g, const Chunk
             c[4 * q] = c4.x; c[4 * q + 1] = c4.y; c[4 * q + 2] = c4.z; c[4 * q + 3] = c4.w;
             s[4 * q] = s4.x; s[4 * q + 1] = s4.y; s[4 * q + 2] = s4.z; s[4 * q + 3] = s4.w;
         }
-#pragma unroll
-        for (int i = 0; i < 16 / kRowsAtOnce; ++i)
-            rotate_part<T, LAYOUT>(x0[i], x1[i], c, s);
+        rotate_part<T, LAYOUT>(x0[i], x1[i], c, s);
     }
     __syncwarp();                              // the tile's last readers are done
 #pragma unroll
-    for (int i = 0; i < 16 / kRowsAtOnce; ++i) {
-        const int r = i * kRowsAtOnce + lane / L;
+    for (int i = 0; i < kSteps; ++i) {
+        const int r = i * kAtOnce + lane / L;
         *reinterpret_cast<uint4 *>(tile + r * kDecQStride<D> + part.o0 * 2) = x0[i];
         *reinterpret_cast<uint4 *>(tile + r * kDecQStride<D> + part.o1 * 2) = x1[i];
     }
@@ -333,8 +494,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t bar[kDecWarps][kStages];
     __shared__ int32_t warp_sum[kDecWarps];
+    __shared__ unsigned long long plan_key;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t n_seqs = g.B + g.fold;
     const int64_t most = g.max_blocks << g.page_shift;
     if (tid < kDecWarps * kStages)
         mbar_init(&bar[0][0] + tid, 1);
@@ -344,10 +507,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
     // memory; one CTA writes it out for the merge)
     int32_t *start = reinterpret_cast<int32_t *>(smem);
     int32_t carry = 0;
-    for (int32_t b0 = 0; b0 < g.B; b0 += kDecThreads) {
+    for (int32_t b0 = 0; b0 < n_seqs; b0 += kDecThreads) {
         const int32_t b = b0 + tid;
-        const int32_t n =
-            b < g.B ? (suffix_keys(g.lens, b, most, g.a.flag) + kDecKeys - 1) / kDecKeys : 0;
+        const int32_t n = b < n_seqs ? (decode_keys(g, b, most) + kDecKeys - 1) / kDecKeys : 0;
         int32_t inc = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -361,27 +523,38 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
         int32_t before = carry;
         for (int w = 0; w < warp; ++w)
             before += warp_sum[w];
-        if (b < g.B)
+        if (b < n_seqs)
             start[b] = before + inc - n;
         for (int w = 0; w < kDecWarps; ++w)
             carry += warp_sum[w];
         __syncthreads();
     }
     if (tid == 0)
-        start[g.B] = carry;
-    __syncthreads();
-    if (blockIdx.x == 0)
-        for (int32_t b = tid; b <= g.B; b += kDecThreads)
-            g.chunk_start[b] = start[b];
+        start[n_seqs] = carry;
+    // the SMs that the prefix kernel leaves to this one
+    int32_t ctas = gridDim.x;
+    if (g.prefix_tiles > 0) {
+        const int32_t rest = g.sizes.sms - 2 * plan_clusters(g.sizes, carry, &plan_key);
+        if (rest > 0 && rest < ctas)
+            ctas = rest;
+    } else {
+        __syncthreads();
+    }
     const int32_t heads = g.Hk * g.row_groups;
     const int64_t total = (int64_t)carry * heads;
-    const int64_t per = decode_per_warp(total, g.warps, g.min_chunks);
+    const int64_t per = decode_per_warp(total, ctas * kDecWarps);
+    if (blockIdx.x == 0) {
+        for (int32_t b = tid; b <= n_seqs; b += kDecThreads)
+            g.chunk_start[b] = start[b];
+        if (tid == 0)
+            g.deal->suffix_per = per;
+    }
     const int32_t w = blockIdx.x * kDecWarps + warp;
     int64_t c = w * per;
     int64_t left = total - c < per ? total - c : per;          // chunks of this warp
     ChunkAt at = {0, 0, 0, 0};
     if (left > 0) {
-        const int32_t b = find_sequence(start, g.B + 1, c / heads);
+        const int32_t b = find_sequence(start, n_seqs + 1, c / heads);
         // (the last b whose start is at most c / heads has chunks)
         at.b = b;
         at.n = start[b + 1] - start[b];
@@ -401,9 +574,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
     // a step early
     ChunkAt ahead = at;
     int64_t to_load = left;
-    auto look_up = [&]() {
+    auto look_up = [&]() -> int32_t {
         const int64_t block = (int64_t)ahead.ch * kDecKeys >> g.page_shift;
-        return to_load > 0 ? __ldg(g.table + ahead.b * g.max_blocks + block) : 0;
+        if (to_load <= 0)
+            return 0;
+        return __ldg(ahead.b < g.B ? g.table + ahead.b * g.max_blocks + block : g.prefix_table + block);
     };
     int32_t page = look_up();
     auto load = [&](int st) {
@@ -446,8 +621,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
     const uint32_t base = attn_smem_u32(stages);
     for (; ok && left > 0; --left, ++done) {
         if (fresh) {
-            keys = suffix_keys(g.lens, at.b, most, g.a.flag);
-            load_query_rows<T, LAYOUT, D>(g, at, (int64_t)g.n_prefix + keys, qtile, qf);
+            keys = decode_keys(g, at.b, most);
+            load_query_rows<T, LAYOUT, D>(g, at, most, qtile, qf);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
                 o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
@@ -555,14 +730,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int rr = r + 8 * half;
-                if (rr < g.rows) {
-                    float *dst = g.out + (slot * g.rows + rr) * D + c0;
+                if (rr < g.slot_rows) {
+                    float *dst = g.out + (slot * g.slot_rows + rr) * D + c0;
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i)
                         *reinterpret_cast<float2 *>(dst + 8 * i) =
                             make_float2(o[i][2 * half], o[i][2 * half + 1]);
                     if ((lane & 3) == 0)
-                        g.stats[slot * g.rows + rr] = half ? make_float2(m1, l1) : make_float2(m0, l0);
+                        g.stats[slot * g.slot_rows + rr] = half ? make_float2(m1, l1) : make_float2(m0, l0);
                 }
             }
             fresh = true;
@@ -595,49 +770,91 @@ __global__ void __launch_bounds__(128) rope_decode_merge_kernel(const __grid_con
     const int32_t group = g.Hq / g.Hk, kv = h / group, in_group = h - kv * group;
     const int32_t rg = in_group / g.rows, r = in_group - rg * g.rows;
     const int32_t heads = g.Hk * g.row_groups;
-    int64_t first = 0, last = -1;                  // slots of the pair
-    if (g.warps > 0) {
-        const int64_t c0 = g.chunk_start[b], c1 = g.chunk_start[b + 1];
-        if (c1 > c0) {
-            const int64_t per =
-                decode_per_warp((int64_t)g.chunk_start[g.B] * heads, g.warps, g.min_chunks);
-            const int32_t hr = kv * g.row_groups + rg;
-            const int64_t at = c0 * heads + hr * (c1 - c0), pair = (int64_t)b * heads + hr;
-            first = at / per + pair;
-            last = (at + (c1 - c0) - 1) / per + pair;
-        }
+    // the parts: groups of the prefix kernel, slots of the pair, slots of the
+    // folded prefix
+    int32_t n0 = 0, n1 = 0, n2 = 0;
+    int64_t first0 = 0, first1 = 0, first2 = 0;
+    const DecodeDeal deal = *g.deal;
+    if (g.prefix_tiles > 0) {
+        const int32_t hu = h >> g.lg;
+        first0 = hu * g.prefix_tiles / deal.prefix_per + hu;
+        n0 = (int32_t)(((hu + 1) * g.prefix_tiles - 1) / deal.prefix_per + hu - first0 + 1);
     }
+    if (g.suffix) {
+        auto slots = [&](int32_t seq, int32_t hr, int64_t &first, int32_t &n) {
+            const int64_t c0 = g.chunk_start[seq], c1 = g.chunk_start[seq + 1];
+            if (c1 == c0)
+                return;
+            const int64_t at = c0 * heads + hr * (c1 - c0), pair = (int64_t)seq * heads + hr;
+            first = at / deal.suffix_per + pair;
+            n = (int32_t)((at + (c1 - c0) - 1) / deal.suffix_per + pair - first + 1);
+        };
+        slots(b, kv * g.row_groups + rg, first1, n1);
+        if (g.fold)
+            slots(g.B, kv, first2, n2);
+    }
+    // part p: its row among the statistics, and whose
+    auto part = [&](int32_t p, bool &prefix) -> int64_t {
+        prefix = p < n0;
+        if (prefix)
+            return (((first0 + p) * g.B + b) << g.lg) + (h & ((1 << g.lg) - 1));
+        p -= n0;
+        if (p < n1)
+            return (first1 + p) * g.slot_rows + r;
+        return (first2 + p - n1) * g.slot_rows + b * group + in_group;
+    };
+    // Batches of 32 parts: lane i holds part i's maximum and sum, so the loads of
+    // a batch do not wait for one another.
+    const int32_t n_parts = n0 + n1 + n2;
     float m = -INFINITY, l = 0.0f, o[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
         o[i] = 0.0f;
-    auto take = [&](const float2 *stat, const float *src) {
-        const float2 s = *stat;
-        float x[V];
-        if constexpr (V == 4) {
-            const float4 t = *reinterpret_cast<const float4 *>(src + lane * V);
-            x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
-        } else {
-            const float2 t = *reinterpret_cast<const float2 *>(src + lane * V);
-            x[0] = t.x; x[1] = t.y;
+    for (int32_t p0 = 0; p0 < n_parts; p0 += 32) {
+        const int n = n_parts - p0 < 32 ? n_parts - p0 : 32;
+        float2 mine = make_float2(-INFINITY, 0.0f);
+        const float *src = nullptr;
+        if (lane < n) {
+            bool prefix;
+            const int64_t at = part(p0 + lane, prefix);
+            mine = __ldg((prefix ? g.prefix_stats : g.stats) + at);
+            src = (prefix ? g.prefix_out : g.out) + at * D;
         }
-        if (s.y == 0.0f)
-            return;                                // no key (O is not looked at)
-        const float top = fmaxf(m, s.x);
-        const float f = m == -INFINITY ? 0.0f : exp2f(m - top), e = exp2f(s.x - top);
-        l = l * f + s.y * e;
+        float top = mine.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = fmaxf(top, m);
+        const float ref = top == -INFINITY ? 0.0f : top;       // no key so far (or NaN)
+        const float w = exp2f(mine.x - ref), f = exp2f(m - ref);
+        float sum = w * mine.y;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l = l * f + sum;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            o[i] = o[i] * f + x[i] * e;
+            o[i] *= f;
         m = top;
-    };
-    for (int32_t s = 0; s < g.splits; ++s) {
-        const int64_t at = (int64_t)s * g.B * g.Hq + row;
-        take(g.prefix_stats + at, g.prefix_out + at * D);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const float *x = reinterpret_cast<const float *>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
+            float v[V];
+            if constexpr (V == 4) {
+                const float4 t = __ldg(reinterpret_cast<const float4 *>(x + lane * V));
+                v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+            } else {
+                const float2 t = __ldg(reinterpret_cast<const float2 *>(x + lane * V));
+                v[0] = t.x; v[1] = t.y;
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                o[e] += wi != 0.0f ? wi * v[e] : 0.0f;
+        }
     }
-    for (int64_t s = first; s <= last; ++s)
-        take(g.stats + s * g.rows + r, g.out + (s * g.rows + r) * D);
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     T *dst = static_cast<T *>(g.o) + row * D + lane * V;
     if constexpr (V == 4)
         *reinterpret_cast<uint2 *>(dst) = make_uint2(Elt<T>::f2_to_word(o[0] * inv, o[1] * inv),
@@ -665,29 +882,42 @@ static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, c
     a.cos = c.cos; a.sin = c.sin; a.rotary_dim = c.rotary_dim; a.table_rows = c.table_rows;
     a.scale_log2 = c.scale_log2; a.flag = c.flag;
 
+    const int32_t gp = packed_group_heads(c.Hq, c.Hk), lg = __builtin_ctz((unsigned)gp);
+    const bool prefix_kernel = c.n_prefix > 0 && !lay.fold;
+    PlanSizes sizes;
+    memset(&sizes, 0, sizeof sizes);
+    sizes.row_tiles = lay.row_tiles; sizes.head_units = c.Hq / gp;
+    sizes.tiles = (c.n_prefix + kAttnKeys - 1) / kAttnKeys;
+    sizes.clusters = lay.clusters; sizes.sms = lay.sms;
+    sizes.tile_ns = D == 128 ? 850 : 700;
+    sizes.heads = c.Hk * lay.row_groups; sizes.chunk_bytes = kDecStageBytes<D>;
+    sizes.prefix_bytes = 4.0f * D * c.Hk * (float)c.n_prefix;
+
     DecodeArgs g;
     memset(&g, 0, sizeof g);
     g.a = a;
+    g.sizes = sizes;
     g.q = c.q; g.q_stride = c.q_stride; g.o = c.o;
-    g.table = c.table; g.lens = c.lens; g.pos_q = c.pos_q;
+    g.table = c.table; g.prefix_table = c.prefix_table; g.lens = c.lens; g.pos_q = c.pos_q;
     g.max_blocks = c.max_blocks; g.n_pages = c.n_pages;
     g.B = c.B; g.Hq = c.Hq; g.Hk = c.Hk; g.page_shift = c.page_shift; g.n_prefix = c.n_prefix;
-    g.row_groups = lay.row_groups; g.rows = lay.rows; g.min_chunks = lay.min_chunks;
-    g.chunk_start = reinterpret_cast<int32_t *>(ws);
+    g.fold = lay.fold; g.row_groups = lay.row_groups; g.rows = lay.rows; g.slot_rows = lay.slot_rows;
+    g.lg = lg;
+    g.deal = reinterpret_cast<DecodeDeal *>(ws);
+    g.chunk_start = reinterpret_cast<int32_t *>(ws + lay.chunk_start);
     g.out = reinterpret_cast<float *>(ws + lay.out);
     g.stats = reinterpret_cast<float2 *>(ws + lay.stats);
     g.prefix_out = reinterpret_cast<float *>(ws + lay.prefix_out);
     g.prefix_stats = reinterpret_cast<float2 *>(ws + lay.prefix_stats);
-    g.splits = c.n_prefix > 0 ? lay.splits : 0;
-    g.warps = lay.suffix_ctas * kDecWarps;
+    g.prefix_tiles = prefix_kernel ? sizes.tiles : 0;
+    g.suffix = lay.suffix_ctas > 0;
 
-    if (c.n_prefix > 0) {
-        const int32_t gp = packed_group_heads(c.Hq, c.Hk);
-        const int lg = __builtin_ctz((unsigned)gp);
+    if (prefix_kernel) {
         const uint32_t box = (uint32_t)(page < 64 ? page : 64), tail = (uint32_t)(c.n_prefix % page);
         PrefixSource s;
         memset(&s, 0, sizeof s);
         s.a = a;
+        s.sizes = sizes;
         if (!encode_3d(enc, &s.k_map, c.k_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, box, 1}, sw) ||
             !encode_3d(enc, &s.v_map, c.v_pages, dt, {D, page, z}, {D * 2, page * D * 2},
                        {(uint32_t)D / 2, (uint32_t)page, 1}, D == 128 ? sw : CU_TENSOR_MAP_SWIZZLE_64B) ||
@@ -698,19 +928,18 @@ static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, c
             return cudaErrorInvalidValue;
         s.pages = c.prefix_table; s.pos_q = c.pos_q; s.lens = c.lens;
         s.max_keys = c.max_blocks << c.page_shift;
+        s.deal = g.deal;
         s.out = reinterpret_cast<float *>(ws + lay.prefix_out);
         s.stats = reinterpret_cast<float2 *>(ws + lay.prefix_stats);
         s.n_pages = c.n_pages;
-        s.n_keys = c.n_prefix; s.n_key_tiles = (c.n_prefix + kAttnKeys - 1) / kAttnKeys;
-        s.B = c.B; s.Hq = c.Hq; s.Hk = c.Hk; s.page_shift = c.page_shift;
-        s.row_tiles = lay.row_tiles; s.head_units = c.Hq / gp; s.units_per_kv = c.Hq / c.Hk / gp;
-        s.splits = lay.splits; s.tiles_per_split = lay.tiles_per_split;
-        const cudaError_t e = launch_packed_kernel<T, LAYOUT, D>(
-            s, (int64_t)s.row_tiles * s.head_units * s.splits, lg, st);
+        s.n_keys = c.n_prefix;
+        s.B = c.B; s.Hk = c.Hk; s.page_shift = c.page_shift;
+        s.units_per_kv = c.Hq / c.Hk / gp;
+        const cudaError_t e = launch_packed_kernel<T, LAYOUT, D>(s, lay.clusters, lg, st);
         if (e != cudaSuccess)
             return e;
     }
-    if (g.warps > 0) {
+    if (lay.suffix_ctas > 0) {
         if (!encode_3d(enc, &g.k_map, c.k_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, kDecKeys, 1}, sw) ||
             !encode_3d(enc, &g.v_map, c.v_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, kDecKeys, 1}, sw))
             return cudaErrorInvalidValue;
@@ -722,9 +951,9 @@ static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, c
             e = raise_smem(reinterpret_cast<const void *>(kernel), kDecSmem<D>, dev, raised);
         if (e != cudaSuccess)
             return e;
-        // without a prefix the suffix kernel comes first in the stream and may
-        // not start before what precedes it is complete
-        if (c.n_prefix > 0) {
+        // without a prefix kernel this one comes first in the stream and may not
+        // start before what precedes it is complete
+        if (prefix_kernel) {
             e = launch_hot(kernel, dim3((unsigned)lay.suffix_ctas), dim3(kDecThreads), (size_t)kDecSmem<D>, st, g);
         } else {
             kernel<<<lay.suffix_ctas, kDecThreads, kDecSmem<D>, st>>>(g);

@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kPackedPrepThreads)
 //               other of two query buffers and write the finished unit's output,
 //               both while the softmax warps are busy with key tiles;
 //   warps 8-11  the leader's S = Q K^T issue, its O += P V issue, the CTA's
-//               copies, and one idle warp.
+//               copies of queries and keys, and of values.
 // The softmax holds a row's 128 scores in registers, so the warpgroups trade
 // registers (setmaxnreg): 240 / 144 / 104 of the 168 they start with.
 //
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kPackedPrepThreads)
 // the helpers 336 us (0.383 TFLOP of visible pairs: 1140 TFLOP/s).
 
 constexpr int kPackedThreads = 384;
-constexpr int kPackedSIssueWarp = 8, kPackedPVIssueWarp = 9, kPackedTmaWarp = 10;
+constexpr int kPackedSIssueWarp = 8, kPackedPVIssueWarp = 9, kPackedKeyWarp = 10, kPackedValueWarp = 11;
 constexpr int kPackedStages = k2Stages;
 constexpr int kPackedStats = 4;                // units whose row statistics are kept
 template <int D>
@@ -377,7 +377,7 @@ struct PackedUnit {
     int32_t seq, tok0, tokens;                 // tokens: of the sequence (or the batch)
     int32_t q_start;                           // the sequence's first token
     int32_t first, n_tiles, n_keys;            // n_keys: of the sequence (or the prefix)
-    int32_t head0, kv, split;
+    int32_t head0, kv, part;                   // part: which partial result (prefix)
 };
 
 // Where the units come from and where K and V lie.  PackedSource: the list and
@@ -392,40 +392,72 @@ struct PackedSource {
     int32_t head_units;                        // Hq / GP
     int32_t units_per_kv;                      // (Hq / Hk) / GP
 
-    __device__ __forceinline__ int64_t units() const { return (int64_t)__ldg(n_entries) * head_units; }
-    __device__ __forceinline__ PackedUnit unit(int64_t L, int lg) const
+    // A cluster's way through the units, longest first: unit r * clusters + c of
+    // the list in even rounds r and r * clusters + clusters - 1 - c in odd ones,
+    // so a cluster that got the longer work of one round gets the shorter of the
+    // next.
+    struct Cursor {
+        int64_t r;
+    };
+    struct Walk {
+        int64_t n_units, clusters, cid;
+    };
+    __device__ __forceinline__ Walk walk(int64_t cid, int64_t clusters) const
     {
+        return {(int64_t)__ldg(n_entries) * head_units, clusters, cid};
+    }
+    __device__ __forceinline__ int64_t at(const Walk &w, const Cursor &c) const
+    {
+        return c.r * w.clusters + ((c.r & 1) ? w.clusters - 1 - w.cid : w.cid);
+    }
+    __device__ __forceinline__ Cursor first(const Walk &) const { return {0}; }
+    __device__ __forceinline__ void next(const Walk &, Cursor &c) const { ++c.r; }
+    __device__ __forceinline__ bool valid(const Walk &w, const Cursor &c) const { return at(w, c) < w.n_units; }
+    __device__ __forceinline__ int32_t tiles(const Walk &w, const Cursor &c) const
+    {
+        return __ldg(&entries[at(w, c) / head_units].n_tiles);
+    }
+    __device__ __forceinline__ PackedUnit unit(const Walk &w, const Cursor &c, int lg) const
+    {
+        const int64_t L = at(w, c);
         const int64_t i = L / head_units;
         const int32_t hu = (int32_t)(L - i * head_units);
         const int4 x = __ldg(reinterpret_cast<const int4 *>(entries + i));
         const int2 y = __ldg(reinterpret_cast<const int2 *>(entries + i) + 2);
         PackedUnit u;
         u.seq = x.x; u.tok0 = x.y; u.tokens = x.z; u.n_keys = x.w;
-        u.q_start = y.x; u.n_tiles = y.y; u.first = 0; u.split = 0;
+        u.q_start = y.x; u.n_tiles = y.y; u.first = 0; u.part = 0;
         u.head0 = hu << lg;
         u.kv = hu / units_per_kv;
         return u;
-    }
-    __device__ __forceinline__ int32_t tiles(int64_t L) const
-    {
-        return __ldg(&entries[L / head_units].n_tiles);
     }
     // table row of token t of the unit's sequence (-1: not rotated)
     __device__ __forceinline__ int64_t table_row(const PackedUnit &u, int32_t t) const
     {
         return attn_row(pos_q != nullptr ? pos_q + u.q_start : nullptr, t, a.table_rows, a.flag);
     }
+    // (the prefix looks its pages up here, before the stage is waited for)
+    template <int D>
+    __device__ __forceinline__ int32_t key_place(const PackedUnit &, int32_t, uint32_t, int) const
+    {
+        return 0;
+    }
+    template <int D>
+    __device__ __forceinline__ int32_t value_place(const PackedUnit &, int32_t, int) const
+    {
+        return 0;
+    }
     // this CTA's half of key tile kt (64 keys) and of value tile kt (D / 2 features)
     template <int D>
-    __device__ __forceinline__ void load_keys(const PackedUnit &u, int32_t kt, uint8_t *dst, uint64_t *bar,
-                                              uint32_t rank, int lane) const
+    __device__ __forceinline__ void load_keys(const PackedUnit &u, int32_t kt, int32_t, uint8_t *dst,
+                                              uint64_t *bar, uint32_t rank, int lane) const
     {
         if (lane < D / 64)
             load_half_box(dst + lane * 8192, maps + (int64_t)u.seq * kPackedMaps, lane * 64,
                           kt * kAttnKeys + 64 * (int)rank, u.kv, bar, rank);
     }
     template <int D>
-    __device__ __forceinline__ void load_values(const PackedUnit &u, int32_t kt, uint8_t *dst,
+    __device__ __forceinline__ void load_values(const PackedUnit &u, int32_t kt, int32_t, uint8_t *dst,
                                                 uint64_t *bar, uint32_t rank, int lane) const
     {
         if (lane == 0)
@@ -558,20 +590,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
     pdl_wait();
     if constexpr (Source::kPrefix)
         pdl_trigger();                             // the suffix kernel needs nothing of this one
-    // The work units, longest first.  Cluster c takes unit r * clusters + c in
-    // even rounds r and r * clusters + clusters - 1 - c in odd ones, so a cluster
-    // that got the longer work of one round gets the shorter of the next.
-    const int64_t n_units = src.units();
-    const int64_t clusters = gridDim.x >> 1, cid = blockIdx.x >> 1;
-    auto unit_at = [&](int64_t r) {
-        return r * clusters + ((r & 1) ? clusters - 1 - cid : cid);
+    const typename Source::Walk walk = src.walk(blockIdx.x >> 1, gridDim.x >> 1);   // (CTA-wide)
+    using Cursor = typename Source::Cursor;
+    auto valid = [&](const Cursor &c) { return src.valid(walk, c); };
+    auto unit_of = [&](const Cursor &c) { return src.unit(walk, c, lg); };
+    // the first unit with key tiles from c on, and the next one after c
+    auto with_tiles = [&](Cursor c) {
+        while (valid(c) && src.tiles(walk, c) == 0)
+            src.next(walk, c);
+        return c;
     };
-    // the first round from r on that has a unit with key tiles; past the last
-    // unit: any round that fails unit_at(r) < n_units
-    auto next_round = [&](int64_t r) {
-        while (unit_at(r) < n_units && src.tiles(unit_at(r)) == 0)
-            ++r;
-        return r;
+    auto next_with_tiles = [&](Cursor c) {
+        src.next(walk, c);
+        return with_tiles(c);
     };
     bool ok = true;
 
@@ -583,8 +614,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
         uint32_t sb = 0, s_ph = 0;                 // S buffer of this tile and its phase parity
         uint32_t ob = 0, o_ph = 0;                 // the same for the previous tile (O barriers)
         uint32_t stat = 0;
-        for (int64_t r = next_round(0); ok && unit_at(r) < n_units; r = next_round(r + 1)) {
-            const PackedUnit u = src.unit(unit_at(r), lg);
+        for (Cursor c = with_tiles(src.first(walk)); ok && valid(c); c = next_with_tiles(c)) {
+            const PackedUnit u = unit_of(c);
             const int32_t n_tiles = u.n_tiles;
             const int64_t shift = (int64_t)u.n_keys - u.tokens;
             const int64_t qi = u.tok0 + (int)rank * tokens + (tid >> lg);
@@ -628,19 +659,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
         if (!ok)
             raise_abort();
     } else if (warp < 8) {
-        // ---- the helpers.  Pass r: rotate the query tile of the unit after
-        // round r's, then write round r's output.  The first pass only rotates.
+        // ---- the helpers.  A pass: rotate the next unit's query tile, then write
+        // this unit's output.  The first pass only rotates.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 144;");
         const int row = tid - 128, wq = warp - 4;  // row of the tile = TMEM lane
         const uint32_t o_base = tmem + k2OCol + ((uint32_t)(wq * 32) << 16);
         uint32_t qn = 0, un = 0;                   // query tiles rotated, units with tiles written
         int32_t o_seq = -1;                        // the sequence whose O map was acquired
-        int64_t rq = next_round(0);                // the round whose query tile is next
-        for (int64_t r = -1; ok && (r < 0 || unit_at(r) < n_units); ++r) {
+        Cursor cq = with_tiles(src.first(walk));   // the unit whose query tile is next
+        Cursor c = src.first(walk);                // the unit whose output is next
+        for (bool start = true; ok && (start || valid(c)); start = false) {
             // the next query tile, at most one ahead of the unit being written (a
             // second one would wait for products that wait for this output)
-            if (unit_at(rq) < n_units && qn < un + 2) {
-                const PackedUnit u = src.unit(unit_at(rq), lg);
+            if (valid(cq) && qn < un + 2) {
+                const PackedUnit u = unit_of(cq);
                 const uint32_t b = qn & 1u;
                 const int32_t tok = u.tok0 + (int)rank * tokens + (row >> lg);
                 const int64_t trow = tok < u.tokens ? src.table_row(u, tok) : -1;
@@ -651,11 +683,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 arrive_leader(&bar_qr[b]);
                 ++qn;
-                rq = next_round(rq + 1);
+                cq = next_with_tiles(cq);
             }
-            if (r < 0)
+            if (start)
                 continue;
-            const PackedUnit u = src.unit(unit_at(r), lg);
+            const PackedUnit u = unit_of(c);
+            src.next(walk, c);
             float2 stat = make_float2(-INFINITY, 0.0f);
             if (u.n_tiles > 0) {
                 ok = __all_sync(0xffffffffu,
@@ -708,8 +741,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
             const uint32_t idesc = umma_idesc(256, kAttnKeys, ab_format, 0);
             uint32_t sb = 0, ph = 0, qn = 0;       // buffer (and stage) of tile g, its parity
             bool first = true;                     // the first pass over the buffers
-            for (int64_t r = next_round(0); ok && unit_at(r) < n_units; r = next_round(r + 1)) {
-                const int32_t n_tiles = src.tiles(unit_at(r));
+            for (Cursor c = with_tiles(src.first(walk)); ok && valid(c); c = next_with_tiles(c)) {
+                const int32_t n_tiles = src.tiles(walk, c);
                 const uint32_t qb = qn & 1u;
                 const uint32_t q_addr = attn_smem_u32(sQ(qb));
                 ok = __all_sync(0xffffffffu, attn_wait(&bar_qr[qb], (qn >> 1) & 1u, abort));
@@ -751,8 +784,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
             // ---- O += P V for both CTAs once both P are in TMEM
             const uint32_t idesc = umma_idesc(256, D, ab_format, 1);
             uint32_t sb = 0, ph = 0, un = 0;
-            for (int64_t r = next_round(0); ok && unit_at(r) < n_units; r = next_round(r + 1)) {
-                const int32_t n_tiles = src.tiles(unit_at(r));
+            for (Cursor c = with_tiles(src.first(walk)); ok && valid(c); c = next_with_tiles(c)) {
+                const int32_t n_tiles = src.tiles(walk, c);
                 // both CTAs have read the previous unit's O
                 if (un > 0)
                     ok = __all_sync(0xffffffffu, attn_wait(&bar_ofree, (un - 1) & 1u, abort));
@@ -785,25 +818,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
             __syncwarp();
             if (!__all_sync(0xffffffffu, attn_wait(&bar_drain[1], 0u)))
                 ok = false;
-        } else if (warp == kPackedTmaWarp) {
-            // ---- the first query tile; then per unit its halves of key and
-            // value tile g into stage g mod 3 once tile g - 3 released it, and,
-            // behind the unit's third tile (or its last), the next unit's query
-            // tile once the unit before this one has read its buffer
+        } else if (warp == kPackedKeyWarp) {
+            // ---- the first query tile; then per unit this CTA's halves of key
+            // tile g into stage g mod 3 once S(g - 3) released it, and, behind the
+            // unit's third tile (or its last), the next unit's query tile once the
+            // unit before this one has read its buffer
             uint32_t sb = 0, ph = 0, qn = 0;
             bool first = true;
-            uint32_t k_ph[kPackedStages], v_ph[kPackedStages];   // parity of the last copy (2: none)
+            uint32_t last_ph[kPackedStages];       // parity of the last copy (2: none)
 #pragma unroll
             for (int s = 0; s < kPackedStages; ++s)
-                k_ph[s] = v_ph[s] = 2;
-            int32_t seq = -1;
-            auto load_query = [&](int64_t r) {
+                last_ph[s] = 2;
+            int32_t seq = -1;                      // the sequence whose map was acquired
+            auto load_query = [&](const Cursor &c) {
                 const uint32_t b = qn & 1u;
                 if (qn >= 2)
                     ok = __all_sync(0xffffffffu, attn_wait(&bar_qfree[b], ((qn >> 1) - 1) & 1u, abort));
                 if (!ok)
                     return;
-                const PackedUnit u = src.unit(unit_at(r), lg);
+                const PackedUnit u = unit_of(c);
                 const CUtensorMap *map;
                 if constexpr (Source::kPrefix) {
                     map = &src.q_map;
@@ -820,20 +853,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                                 u.tok0 + (int)rank * tokens, &bar_q[b]);
                 ++qn;
             };
-            int64_t r = next_round(0);
-            if (unit_at(r) < n_units)
-                load_query(r);
-            while (ok && unit_at(r) < n_units) {
-                const PackedUnit u = src.unit(unit_at(r), lg);
-                const int64_t rn = next_round(r + 1);
+            Cursor c = with_tiles(src.first(walk));
+            if (valid(c))
+                load_query(c);
+            while (ok && valid(c)) {
+                const PackedUnit u = unit_of(c);
+                const Cursor cn = next_with_tiles(c);
                 if constexpr (!Source::kPrefix) {
-                    if (u.seq != seq) {
+                    if (u.seq != seq)
                         acquire_map(src.maps + (int64_t)u.seq * kPackedMaps);
-                        acquire_map(src.maps + (int64_t)u.seq * kPackedMaps + 1);
-                        seq = u.seq;
-                    }
+                    seq = u.seq;
                 }
                 for (int32_t kt = 0; ok && kt < u.n_tiles; ++kt) {
+                    const int32_t z = src.template key_place<D>(u, kt, rank, lane);
                     if (!first)
                         ok = __all_sync(0xffffffffu, attn_wait(&bar_s[sb], ph ^ 1u, abort));
                     if (!ok)
@@ -843,28 +875,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                     if (leader && lane == 0)
                         mbar_expect_tx(&bar_kfull[sb], 2 * kHalf);
                     __syncwarp();
-                    src.template load_keys<D>(u, kt, sK(sb), &bar_kfull[sb], rank, lane);
-                    k_ph[sb] = ph;
-                    if (!first)
-                        ok = __all_sync(0xffffffffu, attn_wait(&bar_o[sb], ph ^ 1u, abort));
-                    if (!ok)
-                        break;
-                    // features D/2 rank .. of the tile's 128 keys
-                    if (leader && lane == 0)
-                        mbar_expect_tx(&bar_vfull[sb], 2 * kHalf);
-                    __syncwarp();
-                    src.template load_values<D>(u, kt, sV(sb), &bar_vfull[sb], rank, lane);
-                    __syncwarp();
-                    v_ph[sb] = ph;
+                    src.template load_keys<D>(u, kt, z, sK(sb), &bar_kfull[sb], rank, lane);
+                    last_ph[sb] = ph;
                     if (++sb == k2SBufs) {
                         sb = 0;
                         ph ^= 1u;
                         first = false;
                     }
-                    if (kt == (u.n_tiles < 3 ? u.n_tiles : 3) - 1 && unit_at(rn) < n_units)
-                        load_query(rn);
+                    if (kt == (u.n_tiles < 3 ? u.n_tiles : 3) - 1 && valid(cn))
+                        load_query(cn);
                 }
-                r = rn;
+                c = cn;
             }
             if (!ok) {
                 // one more bounded wait for the last query tiles and, in the
@@ -874,12 +895,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 for (uint32_t i = qn < 2 ? 0 : qn - 2; i < qn; ++i)
                     (void)attn_wait(&bar_q[i & 1u], (i >> 1) & 1u);
 #pragma unroll
-                for (int s = 0; s < kPackedStages; ++s) {
-                    if (leader && k_ph[s] < 2)
-                        (void)attn_wait(&bar_kfull[s], k_ph[s]);
-                    if (leader && v_ph[s] < 2)
-                        (void)attn_wait(&bar_vfull[s], v_ph[s]);
+                for (int s = 0; s < kPackedStages; ++s)
+                    if (leader && last_ph[s] < 2)
+                        (void)attn_wait(&bar_kfull[s], last_ph[s]);
+            }
+        } else if (warp == kPackedValueWarp) {
+            // ---- this CTA's halves of value tile g into stage g mod 3 once
+            // O += P V of tile g - 3 released it (a warp of its own: behind the key
+            // copies, the next key tile waited for the product)
+            uint32_t sb = 0, ph = 0;
+            bool first = true;
+            uint32_t last_ph[kPackedStages];
+#pragma unroll
+            for (int s = 0; s < kPackedStages; ++s)
+                last_ph[s] = 2;
+            int32_t seq = -1;
+            for (Cursor c = with_tiles(src.first(walk)); ok && valid(c); c = next_with_tiles(c)) {
+                const PackedUnit u = unit_of(c);
+                if constexpr (!Source::kPrefix) {
+                    if (u.seq != seq)
+                        acquire_map(src.maps + (int64_t)u.seq * kPackedMaps + 1);
+                    seq = u.seq;
                 }
+                for (int32_t kt = 0; ok && kt < u.n_tiles; ++kt) {
+                    const int32_t z = src.template value_place<D>(u, kt, lane);
+                    if (!first)
+                        ok = __all_sync(0xffffffffu, attn_wait(&bar_o[sb], ph ^ 1u, abort));
+                    if (!ok)
+                        break;
+                    // features D/2 rank .. of the tile's 128 keys
+                    if (leader && lane == 0)
+                        mbar_expect_tx(&bar_vfull[sb], 2 * kHalf);
+                    __syncwarp();
+                    src.template load_values<D>(u, kt, z, sV(sb), &bar_vfull[sb], rank, lane);
+                    __syncwarp();
+                    last_ph[sb] = ph;
+                    if (++sb == k2SBufs) {
+                        sb = 0;
+                        ph ^= 1u;
+                        first = false;
+                    }
+                }
+            }
+            if (!ok) {
+                raise_abort();
+#pragma unroll
+                for (int s = 0; s < kPackedStages; ++s)
+                    if (leader && last_ph[s] < 2)
+                        (void)attn_wait(&bar_vfull[s], last_ph[s]);
             }
         }
         if (!ok)

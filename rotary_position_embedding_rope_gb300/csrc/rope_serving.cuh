@@ -91,9 +91,10 @@ struct DecodeCall {
 
 // How a decode call is split, and its workspace.
 struct DecodeLayout {
-    int32_t row_tiles, splits, tiles_per_split;      // prefix: units are tiles x head units x splits
-    int32_t row_groups, rows, min_chunks, suffix_ctas;
-    int64_t out, stats, prefix_out, prefix_stats;    // byte offsets
+    int32_t fold;                                    // the prefix runs with the suffixes
+    int32_t row_tiles, clusters, sms;                // prefix: tiles of rows, most clusters; SMs
+    int32_t row_groups, rows, slot_rows, suffix_ctas;
+    int64_t chunk_start, out, stats, prefix_out, prefix_stats;   // byte offsets
     int64_t bytes;
 };
 // False when a size overflows or is not taken.

@@ -121,44 +121,44 @@ bool decode_layout(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_sh
     const int64_t rows = product({B, Hq});
     if (rows < 0 || rows > kMaxInt32)
         return false;
-    // The prefix: clusters of 256 rows.  With fewer units than clusters (76) the
-    // key tiles are split; the rounds of units times a unit's tiles, with about
-    // four tiles' time for its start and its fp32 partial result, is least.
-    const int64_t tiles = (n_prefix + 127) / 128, clusters = kSms / 2;
-    out->row_tiles = (int32_t)((B + 256 / gp - 1) / (256 / gp));
-    const int64_t units = out->row_tiles * (int64_t)(Hq / gp);
-    out->splits = 1;
-    int64_t best = -1;
-    for (int64_t s = 1; s <= tiles && s <= clusters; ++s) {
-        const int64_t cost = (units * s + clusters - 1) / clusters * ((tiles + s - 1) / s + 4);
-        if (best < 0 || cost < best) {
-            best = cost;
-            out->splits = (int32_t)s;
-        }
-    }
-    out->tiles_per_split = (int32_t)((tiles + out->splits - 1) / out->splits);
-    if (tiles > 0)
-        out->splits = (int32_t)((tiles + out->tiles_per_split - 1) / out->tiles_per_split);
-    // The suffixes: equal runs of 16-key chunks for the warps of one CTA an SM.
     out->rows = group < 16 ? group : 16;
     out->row_groups = (group + out->rows - 1) / out->rows;
-    out->min_chunks = 2;
-    const int64_t chunks = product({B, max_blocks, (int64_t)1 << page_shift >> 4});
+    // With no more than 16 rows per key head (one mma tile) the prefix is one
+    // more sequence of the suffix kernel.
+    const int64_t tiles = (n_prefix + 127) / 128;
+    out->fold = n_prefix > 0 && B * group <= 16;
+    out->slot_rows = out->fold ? (int32_t)(B * group) : out->rows;
+    // Otherwise clusters of 256 rows take its (row tile, head unit, key tile)s:
+    // at most one cluster per pair of SMs, and per group of row tiles one part
+    // for each head unit it touches.
+    out->sms = kSms;
+    out->row_tiles = (int32_t)((B + 256 / gp - 1) / (256 / gp));
+    const int64_t head_units = Hq / gp, work = product({out->row_tiles, head_units, tiles});
+    if (work < 0 || work > kMaxInt32 - 128)
+        return false;
+    out->clusters = (int32_t)(work < kSms / 2 ? (work > 0 ? work : 1) : kSms / 2);
+    const int64_t groups = out->clusters / out->row_tiles > 0 ? out->clusters / out->row_tiles : 1;
+    const int64_t parts = n_prefix > 0 && !out->fold ? groups + head_units : 0;
+    // The suffixes: equal runs of 16-key chunks for the warps of one CTA an SM,
+    // at least two chunks a warp.
+    int64_t chunks = product({B, max_blocks, (int64_t)1 << page_shift >> 4});
     if (chunks < 0 || chunks > kMaxInt32)
         return false;
+    if (out->fold)
+        chunks += (n_prefix + 15) / 16;
     const int64_t heads = product({Hk, out->row_groups}), all = product({chunks, heads});
-    const int64_t pairs = product({B, heads});
-    if (all < 0 || pairs < 0 || pairs > kMaxInt32 - kSms * 8)
+    const int64_t pairs = product({B + 1, heads});
+    if (chunks > kMaxInt32 || all < 0 || pairs < 0 || pairs > kMaxInt32 - kSms * 8)
         return false;
-    const int64_t ctas = (all + 8 * out->min_chunks - 1) / (8 * out->min_chunks);
+    const int64_t ctas = (all + 15) / 16;
     out->suffix_ctas = (int32_t)(ctas < kSms ? ctas : kSms);
     const int64_t slots = out->suffix_ctas > 0 ? out->suffix_ctas * 8 + pairs : 0;
-    const int64_t o = product({slots, out->rows, D, 4}), s = product({slots, out->rows, 8});
-    const int64_t parts = n_prefix > 0 ? out->splits : 0;
-    const int64_t po = product({parts, rows, D, 4}), ps = product({parts, rows, 8});
+    const int64_t o = product({slots, out->slot_rows, D, 4}), s = product({slots, out->slot_rows, 8});
+    const int64_t po = product({parts, B, gp, D, 4}), ps = product({parts, B, gp, 8});
     if (o < 0 || s < 0 || po < 0 || ps < 0 || o > (1ll << 60) || po > (1ll << 60))
         return false;
-    out->out = round_up(4 * (B + 1), 128);
+    out->chunk_start = 128;
+    out->out = round_up(out->chunk_start + 4 * (B + 2), 128);
     out->stats = out->out + o;
     out->prefix_out = round_up(out->stats + s, 128);
     out->prefix_stats = out->prefix_out + po;
