@@ -478,7 +478,7 @@ int64_t rope_attention_packed_workspace(int64_t n_seqs, int64_t total_q, int64_t
  *    once.  The split of the work depends on the sizes and the lengths alone:
  *    the same call gives the same bits.
  * Errors: ROPE_ERR_UNSUPPORTED for other dtypes, D, rotary_dim, layouts, page
- *    sizes, B > 32768, a stride not a multiple of 8 or unaligned pointers;
+ *    sizes, B > 4096, a stride not a multiple of 8 or unaligned pointers;
  *    ROPE_ERR_INVALID_ARG for bad sizes, null pointers, a workspace too small,
  *    o or the workspace overlapping another argument; ROPE_ERR_CUDA if a
  *    launch fails.  Asynchronous on `stream`; waits inside the kernels are

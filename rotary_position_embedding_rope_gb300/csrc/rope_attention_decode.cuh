@@ -13,15 +13,16 @@
 //      rows of rope_attn_packed_kernel's tiles (the batch is a "sequence" of B
 //      tokens), its keys come from pages, its key tiles are dealt out evenly to
 //      clusters; every piece of a head's keys leaves an fp32 (O, m, l);
-//   2. rope_decode_suffix_kernel: every warp an equal run of 16-key chunks of
+//   2. the suffixes (decode_suffixes): every warp an equal run of 16-key chunks of
 //      all suffixes, laid end to end, so that ragged lengths balance;
 //   3. rope_decode_merge_kernel.
-// 1 and 2 do not depend on one another and run side by side: the prefix kernel
-// gives itself as many clusters as decode_plan finds best for the suffixes'
-// lengths, its other CTAs leave at once, and the suffix kernel, launched while
-// the prefix kernel runs, takes the SMs they leave.  When the batch has no more
-// than 16 rows per key head, the prefix is one more sequence of kernel 2, with
-// all the rows of the batch: a call of two small launches.
+// 1 and 2 do not depend on one another and share a launch: every CTA works out
+// from the suffixes' lengths how many clusters the prefix gets (plan_clusters);
+// those run 1, the SMs of the others run 2 beside them.  (As two launches the
+// parts ran one after the other, or the second kernel's last CTAs started behind
+// the first: 64 sequences, 8k prefix, 70 us against XX.)  When the batch has no
+// more than 16 rows per key head, the prefix is one more sequence of 2, with all
+// the rows of the batch, in a kernel of 2 alone.
 //
 // What bounds it: bytes -- the prefix once, every suffix once; from about 300
 // rows per key head on, the prefix products.
@@ -63,19 +64,22 @@ __host__ __device__ inline PrefixDeal prefix_deal(const PlanSizes &p, int32_t c)
 
 // Estimated time, in ns, with c clusters on the prefix and the suffixes' chunks
 // (of one pair per sequence) on the SMs left over -- or, with every cluster on
-// the prefix, after it.  Rates measured here: tile_ns a cluster tile, 4 us
-// from one unit to the next, 45 bytes/ns for the copies of one SM and 6500 for
-// all.  An estimate that is off costs balance, never a result.
+// the prefix, behind it.  Rates measured here: tile_ns a cluster tile, half as
+// long again beside the suffixes' copies, 4 us from one unit to the next, 45
+// bytes/ns for the copies of one SM and 6500 for all.  An estimate that is off
+// costs balance, never a result.
 __host__ __device__ inline float plan_ns(const PlanSizes &p, int32_t c, float chunks)
 {
     const PrefixDeal d = prefix_deal(p, c);
     const int32_t rounds = (p.row_tiles + c - 1) / c;
-    const float prefix = 5000.0f + (float)rounds * ((float)d.per * (float)p.tile_ns +
-                                                    4000.0f * (float)(1 + d.per / p.tiles));
     const float bytes = chunks * (float)p.heads * (float)p.chunk_bytes;
+    const bool beside = 2 * c < p.sms;
+    const float tile = (float)p.tile_ns * (beside && bytes > 0.0f ? 1.5f : 1.0f);
+    const float prefix = 5000.0f + (float)rounds * ((float)d.per * tile +
+                                                    4000.0f * (float)(1 + d.per / p.tiles));
     if (bytes == 0.0f)
         return prefix;
-    if (2 * c >= p.sms)
+    if (!beside)
         return prefix + 6000.0f + bytes / 6500.0f;
     const float suffix = 6000.0f + bytes / (45.0f * (float)(p.sms - 2 * c));
     const float both = 6000.0f + (bytes + p.prefix_bytes) / 6500.0f;
@@ -130,178 +134,6 @@ __device__ __forceinline__ int64_t query_row(const int32_t *pos_q, int32_t b, in
 }
 
 // ---------------------------------------------------------------------------
-// 1. the prefix
-struct PrefixSource {
-    static constexpr bool kPrefix = true;
-    AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, flag
-    CUtensorMap k_map, v_map, v_tail, q_map;   // v_tail: pages of n_keys mod page rows
-    PlanSizes sizes;
-    const int32_t *pages;                      // the prefix's block list
-    const int32_t *pos_q, *lens;               // [B]
-    int64_t max_keys;                          // most keys of a suffix (longer lengths are bad)
-    DecodeDeal *deal;
-    float *out;                                // [parts][B][GP][D]: part group + head unit
-    float2 *stats;                             // [parts][B][GP] (m, l)
-    int64_t n_pages;
-    int32_t n_keys, B, Hk, page_shift, units_per_kv;
-
-    // Virtual cluster v: row tile v mod row_tiles of group v / row_tiles, whose
-    // range of (head unit, key tile) is cut at the heads; a cluster takes v = cid,
-    // cid + clusters, ...  The clusters of a group read the same keys at about the
-    // same time.
-    struct Cursor {
-        int32_t v, at, end;
-    };
-    struct Walk {
-        int32_t cid, clusters, groups, per;
-    };
-    __device__ __forceinline__ Walk walk(int64_t cid, int64_t) const
-    {
-        __shared__ unsigned long long key;
-        __shared__ int32_t warp_sum[kPackedThreads / 32];
-        // chunks of all suffixes, and from them the clusters that work
-        int32_t n = 0;
-        for (int32_t b = threadIdx.x; b < B; b += kPackedThreads)
-            n += (suffix_keys(lens, b, max_keys, a.flag) + kDecKeys - 1) / kDecKeys;
-        n = __reduce_add_sync(0xffffffffu, n);
-        if ((threadIdx.x & 31) == 0)
-            warp_sum[threadIdx.x >> 5] = n;
-        __syncthreads();
-        int64_t chunks = 0;
-        for (int w = 0; w < kPackedThreads / 32; ++w)
-            chunks += warp_sum[w];
-        const PrefixDeal d = prefix_deal(sizes, plan_clusters(sizes, chunks, &key));
-        if (blockIdx.x == 0 && threadIdx.x == 0)
-            deal->prefix_per = d.per;
-        return {(int32_t)cid, d.clusters, d.groups, d.per};
-    }
-    __device__ __forceinline__ Cursor start(const Walk &w, int32_t v) const
-    {
-        const int32_t all = sizes.head_units * sizes.tiles;
-        Cursor c;
-        c.v = v;
-        c.at = v / sizes.row_tiles * w.per;
-        c.end = all - c.at < w.per ? all : c.at + w.per;
-        return c;
-    }
-    __device__ __forceinline__ Cursor first(const Walk &w) const
-    {
-        // (a cluster past the plan's starts behind the last virtual one)
-        return start(w, w.cid < w.clusters ? w.cid : w.groups * sizes.row_tiles);
-    }
-    __device__ __forceinline__ bool valid(const Walk &w, const Cursor &c) const
-    {
-        return c.v < w.groups * sizes.row_tiles && c.at < c.end;
-    }
-    __device__ __forceinline__ int32_t tiles(const Walk &, const Cursor &c) const
-    {
-        const int32_t head_end = sizes.tiles - c.at % sizes.tiles;
-        return c.end - c.at < head_end ? c.end - c.at : head_end;
-    }
-    __device__ __forceinline__ void next(const Walk &w, Cursor &c) const
-    {
-        c.at += tiles(w, c);
-        if (c.at >= c.end)
-            c = start(w, c.v + w.clusters);
-    }
-    __device__ __forceinline__ PackedUnit unit(const Walk &w, const Cursor &c, int lg) const
-    {
-        const int32_t hu = c.at / sizes.tiles, group = c.v / sizes.row_tiles;
-        PackedUnit u;
-        u.tok0 = (c.v - group * sizes.row_tiles) * (2 * kAttnRows >> lg);
-        u.seq = 0; u.q_start = 0; u.tokens = B; u.n_keys = n_keys;
-        u.head0 = hu << lg;
-        u.kv = hu / units_per_kv;
-        u.first = c.at - hu * sizes.tiles;
-        u.n_tiles = tiles(w, c);
-        u.part = group + hu;
-        return u;
-    }
-    __device__ __forceinline__ int64_t table_row(const PackedUnit &, int32_t t) const;
-
-    // z of a prefix page in the pools' maps; past the last page, and for a bad
-    // page number, an index that arrives as zeros
-    __device__ __forceinline__ int32_t page_z(int32_t i, int32_t kv) const
-    {
-        const int32_t none = (int32_t)(n_pages * Hk);
-        if ((int64_t)i << page_shift >= n_keys)
-            return none;
-        const int32_t p = __ldg(pages + i);
-        if (p < 0 || p >= n_pages) {
-            atomicOr(a.flag, kFlagIndex);
-            return none;
-        }
-        return p * Hk + kv;
-    }
-    // Where this lane's boxes of a tile lie, looked up before the stage is waited
-    // for: keys (box i of a half, features 64 x ..) and values (page i).
-    template <int D>
-    __device__ __forceinline__ int32_t key_place(const PackedUnit &u, int32_t kt, uint32_t rank, int lane) const
-    {
-        const int32_t shift = page_shift < 6 ? page_shift : 6;      // keys of a box: a page or half of one
-        const int32_t key = (u.first + kt) * kAttnKeys + 64 * (int)rank + (lane / (D / 64) << shift);
-        return lane < (64 >> shift) * (D / 64) ? page_z(key >> page_shift, u.kv) : 0;
-    }
-    template <int D>
-    __device__ __forceinline__ int32_t value_place(const PackedUnit &u, int32_t kt, int lane) const
-    {
-        return lane < kAttnKeys >> page_shift
-                   ? page_z(((u.first + kt) * kAttnKeys >> page_shift) + lane, u.kv)
-                   : 0;
-    }
-    template <int D>
-    __device__ __forceinline__ void load_keys(const PackedUnit &, int32_t, int32_t z, uint8_t *dst,
-                                              uint64_t *bar, uint32_t rank, int lane) const
-    {
-        const int32_t shift = page_shift < 6 ? page_shift : 6;
-        if (lane < (64 >> shift) * (D / 64)) {
-            const int32_t i = lane / (D / 64), x = lane % (D / 64);
-            load_half_box(dst + x * 8192 + (i << shift) * 128, &k_map, x * 64,
-                          (64 * (int)rank + (i << shift)) & ((1 << page_shift) - 1), z, bar, rank);
-        }
-    }
-    template <int D>
-    __device__ __forceinline__ void load_values(const PackedUnit &u, int32_t kt, int32_t z, uint8_t *dst,
-                                                uint64_t *bar, uint32_t rank, int lane) const
-    {
-        if (lane < kAttnKeys >> page_shift) {
-            const int32_t page = ((u.first + kt) * kAttnKeys >> page_shift) + lane;
-            // the last, partly filled page: rows past the prefix arrive as zeros
-            const bool tail = page == n_keys >> page_shift;
-            load_half_box(dst + (lane << page_shift) * D, tail ? &v_tail : &v_map, D / 2 * (int)rank, 0,
-                          z, bar, rank);
-        }
-    }
-    // One helper warp: its rows' O, m and l, in fp32
-    template <int D>
-    __device__ __forceinline__ void store_rows(const PackedUnit &u, uint32_t o_base, int32_t y0, int lane,
-                                               int lg, float2 stat) const
-    {
-        const int32_t tok = y0 + (lane >> lg);
-        const int64_t row = (((int64_t)u.part * B + tok) << lg) + (lane & ((1 << lg) - 1));
-        if (tok < B)
-            stats[row] = stat;
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-            float ov[32];
-            tmem_ld32(o_base + c0, ov);
-            if (tok < B) {
-#pragma unroll
-                for (int c = 0; c < 32; c += 4)
-                    *reinterpret_cast<float4 *>(out + row * D + c0 + c) =
-                        make_float4(ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
-            }
-        }
-    }
-};
-
-__device__ __forceinline__ int64_t PrefixSource::table_row(const PackedUnit &, int32_t t) const
-{
-    const int64_t keys = pos_q != nullptr ? 0 : (int64_t)n_keys + suffix_keys(lens, t, max_keys, a.flag);
-    return query_row(pos_q, t, keys, a.table_rows, a.flag);
-}
-
-// ---------------------------------------------------------------------------
 // 2. the suffixes
 //
 // A pair is (sequence, key head, row group): up to 16 query heads of one group,
@@ -331,7 +163,6 @@ static constexpr int kDecSmem = kDecWarps * (kDecStages<D> * kDecStageBytes<D> +
 struct DecodeArgs {
     AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, flag
     CUtensorMap k_map, v_map;                  // boxes of 64 features x 16 keys
-    PlanSizes sizes;
     const void *q;                             // [B][Hq][D], row stride q_stride
     int64_t q_stride;
     void *o;                                   // [B][Hq][D]
@@ -487,27 +318,16 @@ __device__ __forceinline__ void load_query_rows(const DecodeArgs &g, const Chunk
         ldsm4(addr + k * 32, qf[k]);
 }
 
-template <typename T, int LAYOUT, int D>
-__global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(const __grid_constant__ DecodeArgs g)
+// Chunks of the sequences before b, for all b (start: B + fold + 1 entries of
+// shared memory), by all NT threads of a CTA; returns the number of all.
+template <int NT>
+__device__ __forceinline__ int32_t scan_chunks(const DecodeArgs &g, int32_t *start, int32_t *warp_sum)
 {
-    constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>, kBox = kDecKeys * 128;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t bar[kDecWarps][kStages];
-    __shared__ int32_t warp_sum[kDecWarps];
-    __shared__ unsigned long long plan_key;
-    __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t n_seqs = g.B + g.fold;
     const int64_t most = g.max_blocks << g.page_shift;
-    if (tid < kDecWarps * kStages)
-        mbar_init(&bar[0][0] + tid, 1);
-    if (tid == 0)
-        abort_flag = 0;
-    // chunks of the sequences before b, by every CTA for itself (in the stages'
-    // memory; one CTA writes it out for the merge)
-    int32_t *start = reinterpret_cast<int32_t *>(smem);
     int32_t carry = 0;
-    for (int32_t b0 = 0; b0 < n_seqs; b0 += kDecThreads) {
+    for (int32_t b0 = 0; b0 < n_seqs; b0 += NT) {
         const int32_t b = b0 + tid;
         const int32_t n = b < n_seqs ? (decode_keys(g, b, most) + kDecKeys - 1) / kDecKeys : 0;
         int32_t inc = n;
@@ -521,55 +341,96 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
             warp_sum[warp] = inc;
         __syncthreads();
         int32_t before = carry;
-        for (int w = 0; w < warp; ++w)
-            before += warp_sum[w];
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            before += w < warp ? warp_sum[w] : 0;
+            carry += warp_sum[w];
+        }
         if (b < n_seqs)
             start[b] = before + inc - n;
-        for (int w = 0; w < kDecWarps; ++w)
-            carry += warp_sum[w];
         __syncthreads();
     }
     if (tid == 0)
         start[n_seqs] = carry;
-    // the SMs that the prefix kernel leaves to this one
-    int32_t ctas = gridDim.x;
-    if (g.prefix_tiles > 0) {
-        const int32_t rest = g.sizes.sms - 2 * plan_clusters(g.sizes, carry, &plan_key);
-        if (rest > 0 && rest < ctas)
-            ctas = rest;
-    } else {
-        __syncthreads();
-    }
+    __syncthreads();
+    return carry;
+}
+
+// A warp's run of chunks.
+struct SuffixRun {
+    ChunkAt at;
+    int32_t w;                                 // the warp among all
+    int64_t left;                              // chunks
+};
+
+// Barriers of the suffix warps of a CTA.
+template <int D>
+struct SuffixShared {
+    uint64_t bar[kDecWarps][kDecStages<D>];
+    int abort_flag;
+};
+
+// The suffixes' share of CTA `cta` of `ctas`, whose first eight warps work:
+// every thread of the CTA calls this, then the working ones decode_suffixes.
+template <int D>
+__device__ __forceinline__ SuffixRun suffix_run(const DecodeArgs &g, const int32_t *start, int32_t carry,
+                                                int32_t cta, int32_t ctas, SuffixShared<D> &sh)
+{
+    constexpr int kStages = kDecStages<D>;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t n_seqs = g.B + g.fold;
+    if (tid < kDecWarps * kStages)
+        mbar_init(&sh.bar[0][0] + tid, 1);
+    if (tid == 0)
+        sh.abort_flag = 0;
+    if (lane == 0 && warp < 2)                 // the maps, before the first copies need them
+        asm volatile("prefetch.tensormap [%0];" ::"l"(warp ? &g.v_map : &g.k_map) : "memory");
     const int32_t heads = g.Hk * g.row_groups;
     const int64_t total = (int64_t)carry * heads;
     const int64_t per = decode_per_warp(total, ctas * kDecWarps);
-    if (blockIdx.x == 0) {
-        for (int32_t b = tid; b <= n_seqs; b += kDecThreads)
+    if (cta == 0) {
+        for (int32_t b = tid; b <= n_seqs; b += blockDim.x)
             g.chunk_start[b] = start[b];
         if (tid == 0)
             g.deal->suffix_per = per;
     }
-    const int32_t w = blockIdx.x * kDecWarps + warp;
-    int64_t c = w * per;
-    int64_t left = total - c < per ? total - c : per;          // chunks of this warp
-    ChunkAt at = {0, 0, 0, 0};
-    if (left > 0) {
+    SuffixRun run;
+    run.w = cta * kDecWarps + warp;
+    run.at = {0, 0, 0, 0};
+    const int64_t c = run.w * per;
+    run.left = warp >= kDecWarps ? 0 : total - c < per ? total - c : per;
+    if (run.left > 0) {
         const int32_t b = find_sequence(start, n_seqs + 1, c / heads);
         // (the last b whose start is at most c / heads has chunks)
-        at.b = b;
-        at.n = start[b + 1] - start[b];
+        run.at.b = b;
+        run.at.n = start[b + 1] - start[b];
         const int64_t in = c - (int64_t)start[b] * heads;
-        at.hr = (int32_t)(in / at.n);
-        at.ch = (int32_t)(in - (int64_t)at.hr * at.n);
+        run.at.hr = (int32_t)(in / run.at.n);
+        run.at.ch = (int32_t)(in - (int64_t)run.at.hr * run.at.n);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();                                           // start[] is read: the stages are free
-    pdl_trigger();
+    __syncthreads();                           // start[] is read: its memory may become stages
+    return run;
+}
 
+// One warp's run; smem: kDecSmem bytes of the CTA.
+template <typename T, int LAYOUT, int D>
+__device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *smem, const SuffixRun &run,
+                                                SuffixShared<D> &sh)
+{
+    constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>, kBox = kDecKeys * 128;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t most = g.max_blocks << g.page_shift;
+    const int32_t heads = g.Hk * g.row_groups, w = run.w;
+    int64_t left = run.left;
+    ChunkAt at = run.at;
+    if (left <= 0)
+        return;
+    uint64_t *bar = sh.bar[warp];
     uint8_t *stages = smem + warp * kStages * kStage;
     uint8_t *qtile = smem + kDecWarps * kStages * kStage + warp * 16 * kDecQStride<D>;
-    volatile int *abort = &abort_flag;
+    volatile int *abort = &sh.abort_flag;
     // the copies run kStages chunks ahead; the page of the next one is looked up
     // a step early
     ChunkAt ahead = at;
@@ -581,6 +442,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
         return __ldg(ahead.b < g.B ? g.table + ahead.b * g.max_blocks + block : g.prefix_table + block);
     };
     int32_t page = look_up();
+    // (several row groups of a key head read the same keys)
+    const uint64_t policy = g.row_groups > 1 ? l2_keep() : l2_once();
     auto load = [&](int st) {
         int32_t z = page * g.Hk + ahead.hr / g.row_groups;
         if (page < 0 || page >= g.n_pages) {
@@ -590,13 +453,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
         }
         const int32_t y = ahead.ch * kDecKeys & ((1 << g.page_shift) - 1);
         if (lane == 0)
-            mbar_expect_tx(&bar[warp][st], kStage);
+            mbar_expect_tx(&bar[st], kStage);
         __syncwarp();
         if (lane < 2 * (D / 64)) {
             const int x = lane % (D / 64);
             const bool v = lane >= D / 64;
-            tma_load_3d(stages + st * kStage + (v ? kStage / 2 : 0) + x * kBox, v ? &g.v_map : &g.k_map,
-                        x * 64, y, z, &bar[warp][st]);
+            tma_load_3d_l2(stages + st * kStage + (v ? kStage / 2 : 0) + x * kBox, v ? &g.v_map : &g.k_map,
+                           x * 64, y, z, &bar[st], policy);
         }
         --to_load;
         ahead.next(g, most);
@@ -630,7 +493,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
             l0 = l1 = 0.0f;
             fresh = false;
         }
-        ok = __all_sync(0xffffffffu, attn_wait(&bar[warp][st], ph, abort));
+        ok = __all_sync(0xffffffffu, attn_wait(&bar[st], ph, abort));
         if (!ok)
             break;
         const uint32_t kb = base + st * kStage, vb = kb + kStage / 2;
@@ -749,11 +612,226 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
             atomicOr(g.a.flag, kFlagTimeout);
         // one more bounded wait for the copies in flight
         for (int64_t i = done; i < issued; ++i)
-            (void)attn_wait(&bar[warp][i % kStages], (uint32_t)(i / kStages) & 1u);
+            (void)attn_wait(&bar[i % kStages], (uint32_t)(i / kStages) & 1u);
     }
-    // the prefix's grid, launched before this one, is complete before this one is
-    pdl_wait();
 }
+
+// The suffixes (and a folded prefix) alone.
+template <typename T, int LAYOUT, int D>
+__global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(const __grid_constant__ DecodeArgs g)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int32_t warp_sum[kDecWarps];
+    __shared__ SuffixShared<D> sh;
+    int32_t *start = reinterpret_cast<int32_t *>(smem);
+    pdl_wait();
+    pdl_trigger();
+    const int32_t carry = scan_chunks<kDecThreads>(g, start, warp_sum);
+    const SuffixRun run = suffix_run<D>(g, start, carry, blockIdx.x, gridDim.x, sh);
+    decode_suffixes<T, LAYOUT, D>(g, smem, run, sh);
+}
+
+// ---------------------------------------------------------------------------
+// 1. the prefix, with the suffixes beside or behind it
+struct PrefixSource {
+    static constexpr bool kPrefix = true;
+    template <int D>
+    static constexpr int smem_bytes()
+    {
+        const int prefix = (int)kPackedSmem<D> + 4 * (kMaxDecodeBatch + 2);
+        return prefix > kDecSmem<D> ? prefix : kDecSmem<D>;
+    }
+    AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, flag
+    CUtensorMap k_map, v_map, v_tail, q_map;   // v_tail: pages of n_keys mod page rows
+    DecodeArgs g;                              // the suffixes
+    PlanSizes sizes;
+    const int32_t *pages;                      // the prefix's block list
+    float *out;                                // [parts][B][GP][D]: part group + head unit
+    float2 *stats;                             // [parts][B][GP] (m, l)
+    int64_t n_pages;
+    int32_t n_keys, B, Hk, page_shift, units_per_kv;
+
+    // Virtual cluster v: row tile v mod row_tiles of group v / row_tiles, whose
+    // range of (head unit, key tile) is cut at the heads; a cluster takes v = cid,
+    // cid + clusters, ...  The clusters of a group read the same keys at about the
+    // same time.
+    struct Cursor {
+        int32_t v, at, end;
+    };
+    struct Walk {
+        int32_t cid, clusters, groups, per;
+        int32_t chunks;                        // of the suffixes
+    };
+    // Behind the prefix's shared memory: the scan of the suffixes' chunks.
+    template <int D>
+    static __device__ __forceinline__ int32_t *chunk_starts(uint8_t *smem)
+    {
+        return reinterpret_cast<int32_t *>(smem + kPackedSmem<D>);
+    }
+    template <int D>
+    __device__ __forceinline__ Walk walk(int64_t cid, int64_t, uint8_t *smem) const
+    {
+        __shared__ unsigned long long key;
+        __shared__ int32_t warp_sum[kPackedThreads / 32];
+        const int32_t chunks = scan_chunks<kPackedThreads>(g, chunk_starts<D>(smem), warp_sum);
+        const PrefixDeal d = prefix_deal(sizes, plan_clusters(sizes, chunks, &key));
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            g.deal->prefix_per = d.per;
+        return {(int32_t)cid, d.clusters, d.groups, d.per, chunks};
+    }
+    // The suffixes, on the CTAs without prefix work, or on all behind it: two
+    // warpgroups, with 216 registers a thread.  setmaxnreg of the roles before:
+    // 240 / 144 / 104.
+    template <typename T, int LAYOUT, int D>
+    __device__ __forceinline__ void finish(const Walk &w, uint8_t *smem) const
+    {
+        __shared__ SuffixShared<D> sh;
+        const int32_t used = 2 * w.clusters < (int32_t)gridDim.x ? 2 * w.clusters : 0;
+        const int32_t cta = (int32_t)blockIdx.x - used;
+        if (!g.suffix || cta < 0)
+            return;
+        const SuffixRun run =
+            suffix_run<D>(g, chunk_starts<D>(smem), w.chunks, cta, (int32_t)gridDim.x - used, sh);
+        const int warp = threadIdx.x >> 5;
+        if (warp < 8) {
+            if (warp < 4)
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 216;");
+            else
+                asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+            decode_suffixes<T, LAYOUT, D>(g, smem, run, sh);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        }
+    }
+    __device__ __forceinline__ Cursor start(const Walk &w, int32_t v) const
+    {
+        const int32_t all = sizes.head_units * sizes.tiles;
+        Cursor c;
+        c.v = v;
+        c.at = v / sizes.row_tiles * w.per;
+        c.end = all - c.at < w.per ? all : c.at + w.per;
+        return c;
+    }
+    __device__ __forceinline__ Cursor first(const Walk &w) const
+    {
+        // (a cluster past the plan's starts behind the last virtual one)
+        return start(w, w.cid < w.clusters ? w.cid : w.groups * sizes.row_tiles);
+    }
+    __device__ __forceinline__ bool valid(const Walk &w, const Cursor &c) const
+    {
+        return c.v < w.groups * sizes.row_tiles && c.at < c.end;
+    }
+    __device__ __forceinline__ int32_t tiles(const Walk &, const Cursor &c) const
+    {
+        const int32_t head_end = sizes.tiles - c.at % sizes.tiles;
+        return c.end - c.at < head_end ? c.end - c.at : head_end;
+    }
+    __device__ __forceinline__ void next(const Walk &w, Cursor &c) const
+    {
+        c.at += tiles(w, c);
+        if (c.at >= c.end)
+            c = start(w, c.v + w.clusters);
+    }
+    __device__ __forceinline__ PackedUnit unit(const Walk &w, const Cursor &c, int lg) const
+    {
+        const int32_t hu = c.at / sizes.tiles, group = c.v / sizes.row_tiles;
+        PackedUnit u;
+        u.tok0 = (c.v - group * sizes.row_tiles) * (2 * kAttnRows >> lg);
+        u.seq = 0; u.q_start = 0; u.tokens = B; u.n_keys = n_keys;
+        u.head0 = hu << lg;
+        u.kv = hu / units_per_kv;
+        u.first = c.at - hu * sizes.tiles;
+        u.n_tiles = tiles(w, c);
+        u.part = group + hu;
+        return u;
+    }
+    __device__ __forceinline__ int64_t table_row(const PackedUnit &, int32_t t) const
+    {
+        return query_row(g.pos_q, t,
+                         g.pos_q != nullptr
+                             ? 0
+                             : (int64_t)n_keys + suffix_keys(g.lens, t, g.max_blocks << page_shift, a.flag),
+                         a.table_rows, a.flag);
+    }
+
+    // z of a prefix page in the pools' maps; past the last page, and for a bad
+    // page number, an index that arrives as zeros
+    __device__ __forceinline__ int32_t page_z(int32_t i, int32_t kv) const
+    {
+        const int32_t none = (int32_t)(n_pages * Hk);
+        if ((int64_t)i << page_shift >= n_keys)
+            return none;
+        const int32_t p = __ldg(pages + i);
+        if (p < 0 || p >= n_pages) {
+            atomicOr(a.flag, kFlagIndex);
+            return none;
+        }
+        return p * Hk + kv;
+    }
+    // (with several row tiles the prefix is read by as many clusters)
+    __device__ __forceinline__ uint64_t policy() const { return sizes.row_tiles > 1 ? l2_keep() : l2_once(); }
+    // Where this lane's boxes of a tile lie, looked up before the stage is waited
+    // for: keys (box i of a half, features 64 x ..) and values (page i).
+    template <int D>
+    __device__ __forceinline__ int32_t key_place(const PackedUnit &u, int32_t kt, uint32_t rank, int lane) const
+    {
+        const int32_t shift = page_shift < 6 ? page_shift : 6;      // keys of a box: a page or half of one
+        const int32_t key = (u.first + kt) * kAttnKeys + 64 * (int)rank + (lane / (D / 64) << shift);
+        return lane < (64 >> shift) * (D / 64) ? page_z(key >> page_shift, u.kv) : 0;
+    }
+    template <int D>
+    __device__ __forceinline__ int32_t value_place(const PackedUnit &u, int32_t kt, int lane) const
+    {
+        return lane < kAttnKeys >> page_shift
+                   ? page_z(((u.first + kt) * kAttnKeys >> page_shift) + lane, u.kv)
+                   : 0;
+    }
+    template <int D>
+    __device__ __forceinline__ void load_keys(const PackedUnit &, int32_t, int32_t z, uint8_t *dst,
+                                              uint64_t *bar, uint32_t rank, int lane) const
+    {
+        const int32_t shift = page_shift < 6 ? page_shift : 6;
+        if (lane < (64 >> shift) * (D / 64)) {
+            const int32_t i = lane / (D / 64), x = lane % (D / 64);
+            load_half_box_l2(dst + x * 8192 + (i << shift) * 128, &k_map, x * 64,
+                             (64 * (int)rank + (i << shift)) & ((1 << page_shift) - 1), z, bar, rank,
+                             policy());
+        }
+    }
+    template <int D>
+    __device__ __forceinline__ void load_values(const PackedUnit &u, int32_t kt, int32_t z, uint8_t *dst,
+                                                uint64_t *bar, uint32_t rank, int lane) const
+    {
+        if (lane < kAttnKeys >> page_shift) {
+            const int32_t page = ((u.first + kt) * kAttnKeys >> page_shift) + lane;
+            // the last, partly filled page: rows past the prefix arrive as zeros
+            const bool tail = page == n_keys >> page_shift;
+            load_half_box_l2(dst + (lane << page_shift) * D, tail ? &v_tail : &v_map, D / 2 * (int)rank, 0,
+                             z, bar, rank, policy());
+        }
+    }
+    // One helper warp: its rows' O, m and l, in fp32
+    template <int D>
+    __device__ __forceinline__ void store_rows(const PackedUnit &u, uint32_t o_base, int32_t y0, int lane,
+                                               int lg, float2 stat) const
+    {
+        const int32_t tok = y0 + (lane >> lg);
+        const int64_t row = (((int64_t)u.part * B + tok) << lg) + (lane & ((1 << lg) - 1));
+        if (tok < B)
+            stats[row] = stat;
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+            float ov[32];
+            tmem_ld32(o_base + c0, ov);
+            if (tok < B) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 4)
+                    *reinterpret_cast<float4 *>(out + row * D + c0 + c) =
+                        make_float4(ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
+            }
+        }
+    }
+};
 
 // ---------------------------------------------------------------------------
 // 3. the merge: a warp per (sequence, query head), a lane per D / 32 features
@@ -884,19 +962,15 @@ static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, c
 
     const int32_t gp = packed_group_heads(c.Hq, c.Hk), lg = __builtin_ctz((unsigned)gp);
     const bool prefix_kernel = c.n_prefix > 0 && !lay.fold;
-    PlanSizes sizes;
-    memset(&sizes, 0, sizeof sizes);
-    sizes.row_tiles = lay.row_tiles; sizes.head_units = c.Hq / gp;
-    sizes.tiles = (c.n_prefix + kAttnKeys - 1) / kAttnKeys;
-    sizes.clusters = lay.clusters; sizes.sms = lay.sms;
-    sizes.tile_ns = D == 128 ? 850 : 700;
-    sizes.heads = c.Hk * lay.row_groups; sizes.chunk_bytes = kDecStageBytes<D>;
-    sizes.prefix_bytes = 4.0f * D * c.Hk * (float)c.n_prefix;
+    const int32_t tiles = (c.n_prefix + kAttnKeys - 1) / kAttnKeys;
+    int sms = 0, dev = 0;
+    cudaError_t e = sm_count(&sms, &dev);
+    if (e != cudaSuccess)
+        return e;
 
     DecodeArgs g;
     memset(&g, 0, sizeof g);
     g.a = a;
-    g.sizes = sizes;
     g.q = c.q; g.q_stride = c.q_stride; g.o = c.o;
     g.table = c.table; g.prefix_table = c.prefix_table; g.lens = c.lens; g.pos_q = c.pos_q;
     g.max_blocks = c.max_blocks; g.n_pages = c.n_pages;
@@ -909,15 +983,19 @@ static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, c
     g.stats = reinterpret_cast<float2 *>(ws + lay.stats);
     g.prefix_out = reinterpret_cast<float *>(ws + lay.prefix_out);
     g.prefix_stats = reinterpret_cast<float2 *>(ws + lay.prefix_stats);
-    g.prefix_tiles = prefix_kernel ? sizes.tiles : 0;
+    g.prefix_tiles = prefix_kernel ? tiles : 0;
     g.suffix = lay.suffix_ctas > 0;
+    if (g.suffix &&
+        (!encode_3d(enc, &g.k_map, c.k_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, kDecKeys, 1}, sw) ||
+         !encode_3d(enc, &g.v_map, c.v_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, kDecKeys, 1}, sw)))
+        return cudaErrorInvalidValue;
 
     if (prefix_kernel) {
         const uint32_t box = (uint32_t)(page < 64 ? page : 64), tail = (uint32_t)(c.n_prefix % page);
         PrefixSource s;
         memset(&s, 0, sizeof s);
         s.a = a;
-        s.sizes = sizes;
+        s.g = g;
         if (!encode_3d(enc, &s.k_map, c.k_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, box, 1}, sw) ||
             !encode_3d(enc, &s.v_map, c.v_pages, dt, {D, page, z}, {D * 2, page * D * 2},
                        {(uint32_t)D / 2, (uint32_t)page, 1}, D == 128 ? sw : CU_TENSOR_MAP_SWIZZLE_64B) ||
@@ -926,42 +1004,32 @@ static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, c
             !encode_3d(enc, &s.q_map, c.q, dt, {D, c.Hq, c.B}, {D * 2, c.q_stride * 2},
                        {64, (uint32_t)gp, (uint32_t)(kAttnRows / gp)}, sw))
             return cudaErrorInvalidValue;
-        s.pages = c.prefix_table; s.pos_q = c.pos_q; s.lens = c.lens;
-        s.max_keys = c.max_blocks << c.page_shift;
-        s.deal = g.deal;
+        // clusters for the prefix and for the suffixes, as far as the SMs go
+        int32_t clusters = lay.clusters + (lay.suffix_ctas + 1) / 2;
+        clusters = clusters < sms / 2 ? clusters : sms / 2;
+        s.sizes.row_tiles = lay.row_tiles; s.sizes.head_units = c.Hq / gp; s.sizes.tiles = tiles;
+        s.sizes.clusters = lay.clusters < clusters ? lay.clusters : clusters;
+        s.sizes.sms = 2 * clusters;
+        s.sizes.tile_ns = D == 128 ? 850 : 700;
+        s.sizes.heads = c.Hk * lay.row_groups; s.sizes.chunk_bytes = kDecStageBytes<D>;
+        s.sizes.prefix_bytes = 4.0f * D * c.Hk * (float)c.n_prefix;
+        s.pages = c.prefix_table;
         s.out = reinterpret_cast<float *>(ws + lay.prefix_out);
         s.stats = reinterpret_cast<float2 *>(ws + lay.prefix_stats);
         s.n_pages = c.n_pages;
         s.n_keys = c.n_prefix;
         s.B = c.B; s.Hk = c.Hk; s.page_shift = c.page_shift;
         s.units_per_kv = c.Hq / c.Hk / gp;
-        const cudaError_t e = launch_packed_kernel<T, LAYOUT, D>(s, lay.clusters, lg, st);
-        if (e != cudaSuccess)
-            return e;
-    }
-    if (lay.suffix_ctas > 0) {
-        if (!encode_3d(enc, &g.k_map, c.k_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, kDecKeys, 1}, sw) ||
-            !encode_3d(enc, &g.v_map, c.v_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, kDecKeys, 1}, sw))
-            return cudaErrorInvalidValue;
+        e = launch_packed_kernel<T, LAYOUT, D>(s, clusters, lg, st);
+    } else if (g.suffix) {
         static std::atomic<uint64_t> raised{0};
         auto *kernel = rope_decode_suffix_kernel<T, LAYOUT, D>;
-        int sms = 0, dev = 0;
-        cudaError_t e = sm_count(&sms, &dev);
+        e = raise_smem(reinterpret_cast<const void *>(kernel), kDecSmem<D>, dev, raised);
         if (e == cudaSuccess)
-            e = raise_smem(reinterpret_cast<const void *>(kernel), kDecSmem<D>, dev, raised);
-        if (e != cudaSuccess)
-            return e;
-        // without a prefix kernel this one comes first in the stream and may not
-        // start before what precedes it is complete
-        if (prefix_kernel) {
             e = launch_hot(kernel, dim3((unsigned)lay.suffix_ctas), dim3(kDecThreads), (size_t)kDecSmem<D>, st, g);
-        } else {
-            kernel<<<lay.suffix_ctas, kDecThreads, kDecSmem<D>, st>>>(g);
-            e = cudaGetLastError();
-        }
-        if (e != cudaSuccess)
-            return e;
     }
+    if (e != cudaSuccess)
+        return e;
     const int64_t rows = (int64_t)c.B * c.Hq;
     const unsigned blocks = (unsigned)((rows + 3) / 4);
     return launch_hot(rope_decode_merge_kernel<T, D>, dim3(blocks), dim3(128), 0, st, g);

@@ -370,6 +370,43 @@ __device__ __forceinline__ void load_half_box(uint8_t *dst, const CUtensorMap *m
         tma_load_3d_to_leader(dst, map, x, y, z, peer_addr(bar, 0));
 }
 
+// L2 policies of copies.  Cached keys and values that a call reads once are
+// marked to leave L2 first: a decode step streams more than L2 holds, and what
+// it needs again (its code, the block lists, the partial results) would be gone.
+__device__ __forceinline__ uint64_t l2_once()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t l2_keep()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void tma_load_3d_l2(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                               uint64_t *bar, uint64_t policy)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;"
+                 ::"r"(attn_smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(attn_smem_u32(bar)),
+                   "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void load_half_box_l2(uint8_t *dst, const CUtensorMap *map, int x, int y, int z,
+                                                 uint64_t *bar, uint32_t rank, uint64_t policy)
+{
+    if (rank == 0)
+        tma_load_3d_l2(dst, map, x, y, z, bar, policy);
+    else
+        asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::"
+                     "complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;"
+                     ::"r"(attn_smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z),
+                       "r"(peer_addr(bar, 0)), "l"(policy)
+                     : "memory");
+}
+
 // One unit of work of a cluster: the rows (token, head) of tokens tok0 .. and
 // heads head0 .. head0 + GP - 1 against the key tiles first .. first + n_tiles - 1
 // of key head kv.
@@ -384,6 +421,11 @@ struct PackedUnit {
 // the maps the prepare kernel wrote; rows end in bf16 / fp16 outputs.
 struct PackedSource {
     static constexpr bool kPrefix = false;
+    template <int D>
+    static constexpr int smem_bytes()
+    {
+        return (int)kPackedSmem<D>;
+    }
     AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, causal, flag
     const PackedEntry *entries;
     const int32_t *n_entries;
@@ -402,7 +444,8 @@ struct PackedSource {
     struct Walk {
         int64_t n_units, clusters, cid;
     };
-    __device__ __forceinline__ Walk walk(int64_t cid, int64_t clusters) const
+    template <int D>
+    __device__ __forceinline__ Walk walk(int64_t cid, int64_t clusters, uint8_t *) const
     {
         return {(int64_t)__ldg(n_entries) * head_units, clusters, cid};
     }
@@ -589,8 +632,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
     // what ran before this launch (the prepare kernel) is complete from here on
     pdl_wait();
     if constexpr (Source::kPrefix)
-        pdl_trigger();                             // the suffix kernel needs nothing of this one
-    const typename Source::Walk walk = src.walk(blockIdx.x >> 1, gridDim.x >> 1);   // (CTA-wide)
+        pdl_trigger();                             // (the merge waits for all of this launch)
+    const typename Source::Walk walk = src.template walk<D>(blockIdx.x >> 1, gridDim.x >> 1, smem);   // (CTA-wide)
     using Cursor = typename Source::Cursor;
     auto valid = [&](const Cursor &c) { return src.valid(walk, c); };
     auto unit_of = [&](const Cursor &c) { return src.unit(walk, c, lg); };
@@ -953,12 +996,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncwarp();
     cluster_sync_all();
-    if (tid == 0 && *abort)
+    const bool failed = *abort != 0;
+    if (tid == 0 && failed)
         atomicOr(a.flag, kFlagTimeout);
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols)
                      : "memory");
+    if constexpr (Source::kPrefix) {
+        if (!failed)                               // (else copies may still be on their way)
+            src.template finish<T, LAYOUT, D>(walk, smem);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1018,7 +1066,8 @@ static cudaError_t launch_packed_kernel(const Source &src, int64_t most, int lg,
 {
     static std::atomic<uint64_t> raised{0};
     // at least 120 KB, so that one CTA holds an SM (and its TMEM)
-    constexpr int kSmem = kPackedSmem<D> > 120 * 1024 ? (int)kPackedSmem<D> : 120 * 1024;
+    constexpr int kUsed = Source::template smem_bytes<D>();
+    constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
     auto *kernel = rope_attn_packed_kernel<T, LAYOUT, D, Source>;
     int sms = 0, dev = 0;
     cudaError_t e = sm_count(&sms, &dev);

@@ -73,6 +73,7 @@ cudaError_t launch_packed_f16(const PackedArgs &c, const PackedLayout &lay, int3
 
 // Attention of one token per sequence over a shared prefix and a suffix each
 // (rope_attention_decode.cuh).
+constexpr int32_t kMaxDecodeBatch = 4096;      // sequences of a call (their scan fits an SM)
 struct DecodeCall {
     const void *q;                   // [B][Hq][D], row stride q_stride
     int64_t q_stride;
@@ -92,7 +93,7 @@ struct DecodeCall {
 // How a decode call is split, and its workspace.
 struct DecodeLayout {
     int32_t fold;                                    // the prefix runs with the suffixes
-    int32_t row_tiles, clusters, sms;                // prefix: tiles of rows, most clusters; SMs
+    int32_t row_tiles, clusters;                     // prefix: tiles of rows, most clusters
     int32_t row_groups, rows, slot_rows, suffix_ctas;
     int64_t chunk_start, out, stats, prefix_out, prefix_stats;   // byte offsets
     int64_t bytes;

@@ -111,7 +111,6 @@ bool packed_layout(int64_t n_seqs, int64_t total_q, int64_t total_k, int32_t Hq,
 // The SMs the split rules are made for (any other number gives the same
 // results, less evenly spread).
 constexpr int32_t kSms = 152;
-constexpr int32_t kMaxDecodeBatch = 32768;
 
 bool decode_layout(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_shift, int64_t max_blocks,
                    int64_t n_prefix, DecodeLayout *out)
@@ -131,7 +130,6 @@ bool decode_layout(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_sh
     // Otherwise clusters of 256 rows take its (row tile, head unit, key tile)s:
     // at most one cluster per pair of SMs, and per group of row tiles one part
     // for each head unit it touches.
-    out->sms = kSms;
     out->row_tiles = (int32_t)((B + 256 / gp - 1) / (256 / gp));
     const int64_t head_units = Hq / gp, work = product({out->row_tiles, head_units, tiles});
     if (work < 0 || work > kMaxInt32 - 128)
@@ -148,11 +146,13 @@ bool decode_layout(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_sh
         chunks += (n_prefix + 15) / 16;
     const int64_t heads = product({Hk, out->row_groups}), all = product({chunks, heads});
     const int64_t pairs = product({B + 1, heads});
-    if (chunks > kMaxInt32 || all < 0 || pairs < 0 || pairs > kMaxInt32 - kSms * 8)
+    if (chunks > kMaxInt32 || all < 0 || pairs < 0 || pairs > kMaxInt32 - (kSms + 1) * 8)
         return false;
     const int64_t ctas = (all + 15) / 16;
     out->suffix_ctas = (int32_t)(ctas < kSms ? ctas : kSms);
-    const int64_t slots = out->suffix_ctas > 0 ? out->suffix_ctas * 8 + pairs : 0;
+    // (beside a prefix kernel, warps of up to that many CTAs and its own)
+    const int64_t most = out->suffix_ctas + 2 * out->clusters < kSms ? out->suffix_ctas + 2 * out->clusters : kSms;
+    const int64_t slots = out->suffix_ctas > 0 ? (most + 1) * 8 + pairs : 0;
     const int64_t o = product({slots, out->slot_rows, D, 4}), s = product({slots, out->slot_rows, 8});
     const int64_t po = product({parts, B, gp, D, 4}), ps = product({parts, B, gp, 8});
     if (o < 0 || s < 0 || po < 0 || ps < 0 || o > (1ll << 60) || po > (1ll << 60))

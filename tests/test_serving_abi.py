@@ -123,7 +123,7 @@ def decode_args(**over):
 
 @pytest.mark.parametrize("over,status", [
     (dict(dtype=0), UNS), (dict(layout=3), UNS), (dict(D=80), UNS), (dict(rd=24), UNS), (dict(page=24), UNS),
-    (dict(page=256), UNS), (dict(B=32769), UNS), (dict(qs=516), UNS), (dict(q=A + 2), UNS), (dict(o=4 * A + 8), UNS),
+    (dict(page=256), UNS), (dict(B=4097), UNS), (dict(qs=516), UNS), (dict(q=A + 2), UNS), (dict(o=4 * A + 8), UNS),
     (dict(kp=2 * A + 8), UNS), (dict(sin=9 * A + 8), UNS), (dict(ws=10 * A + 16), UNS),
     (dict(B=-1), INV), (dict(Hq=5, qs=640), INV), (dict(Hk=0), INV), (dict(qs=504), INV), (dict(P=-1), INV),
     (dict(P=0x7fffffff), INV), (dict(blocks=-1), INV), (dict(n_pages=0), INV), (dict(n_pages=1 << 30), INV),
@@ -149,6 +149,6 @@ def test_decode_workspace(lib):
     assert lib.rope_attention_decode_fwd(*decode_args(wsb=need - 1)) == INV
     assert ws(0, 4, 2, 128, 16, 4, 40) == ws(3, 0, 0, 128, 16, 4, 40) == 0
     assert ws(3, 4, 3, 128, 16, 4, 40) == ws(3, 4, 2, 96, 16, 4, 40) == ws(3, 4, 2, 128, 48, 4, 40) == -1
-    assert ws(40000, 4, 2, 128, 16, 4, 40) == ws(3, 4, 2, 128, 16, 4, -1) == -1
+    assert ws(4097, 4, 2, 128, 16, 4, 40) == ws(3, 4, 2, 128, 16, 4, -1) == -1
     # nothing but a prefix, nothing but suffixes
     assert 0 < ws(3, 4, 2, 128, 16, 0, 40) < need and 0 < ws(3, 4, 2, 128, 16, 4, 0) < need
