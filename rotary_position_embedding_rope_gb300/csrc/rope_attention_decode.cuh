@@ -64,26 +64,24 @@ __host__ __device__ inline PrefixDeal prefix_deal(const PlanSizes &p, int32_t c)
 
 // Estimated time, in ns, with c clusters on the prefix and the suffixes' chunks
 // (of one pair per sequence) on the SMs left over -- or, with every cluster on
-// the prefix, behind it.  Rates measured here: tile_ns a cluster tile, half as
-// long again beside the suffixes' copies, 4 us from one unit to the next, 45
-// bytes/ns for the copies of one SM and 6500 for all.  An estimate that is off
-// costs balance, never a result.
+// the prefix, behind it.  Measured here: tile_ns a cluster tile, 4 us from one
+// unit to the next, 45 bytes/ns for the copies of one SM.  All copies together
+// get 6500 bytes/ns; beyond that both sides slow down alike.  An estimate that
+// is off costs balance, never a result.
 __host__ __device__ inline float plan_ns(const PlanSizes &p, int32_t c, float chunks)
 {
     const PrefixDeal d = prefix_deal(p, c);
     const int32_t rounds = (p.row_tiles + c - 1) / c;
     const float bytes = chunks * (float)p.heads * (float)p.chunk_bytes;
-    const bool beside = 2 * c < p.sms;
-    const float tile = (float)p.tile_ns * (beside && bytes > 0.0f ? 1.5f : 1.0f);
-    const float prefix = 5000.0f + (float)rounds * ((float)d.per * tile +
-                                                    4000.0f * (float)(1 + d.per / p.tiles));
+    const float prefix = (float)rounds * ((float)d.per * (float)p.tile_ns +
+                                          4000.0f * (float)(1 + d.per / p.tiles));
     if (bytes == 0.0f)
         return prefix;
-    if (!beside)
-        return prefix + 6000.0f + bytes / 6500.0f;
-    const float suffix = 6000.0f + bytes / (45.0f * (float)(p.sms - 2 * c));
-    const float both = 6000.0f + (bytes + p.prefix_bytes) / 6500.0f;
-    return fmaxf(fmaxf(prefix, suffix), both);
+    if (2 * c >= p.sms)
+        return prefix + 8000.0f + bytes / 6500.0f;
+    const float suffix = bytes / (45.0f * (float)(p.sms - 2 * c));
+    const float demand = (45.0f * (float)(p.sms - 2 * c) + p.prefix_bytes / prefix) / 6500.0f;
+    return 8000.0f + fmaxf(prefix, suffix) * fmaxf(demand, 1.0f);
 }
 
 // Clusters for the prefix, by every thread of a CTA of at least p.clusters
@@ -431,20 +429,24 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
     uint8_t *stages = smem + warp * kStages * kStage;
     uint8_t *qtile = smem + kDecWarps * kStages * kStage + warp * 16 * kDecQStride<D>;
     volatile int *abort = &sh.abort_flag;
-    // the copies run kStages chunks ahead; the page of the next one is looked up
-    // a step early
+    // The copies run kStages chunks ahead.  Lane i holds the page of block base +
+    // i of sequence `of`, so that a step seldom waits for the block list.
     ChunkAt ahead = at;
     int64_t to_load = left;
-    auto look_up = [&]() -> int32_t {
-        const int64_t block = (int64_t)ahead.ch * kDecKeys >> g.page_shift;
-        if (to_load <= 0)
-            return 0;
-        return __ldg(ahead.b < g.B ? g.table + ahead.b * g.max_blocks + block : g.prefix_table + block);
-    };
-    int32_t page = look_up();
+    int32_t pages = 0, of = -1;
+    int64_t base_block = 0;
     // (several row groups of a key head read the same keys)
     const uint64_t policy = g.row_groups > 1 ? l2_keep() : l2_once();
     auto load = [&](int st) {
+        const int64_t block = (int64_t)ahead.ch * kDecKeys >> g.page_shift;
+        if (of != ahead.b || block < base_block || block >= base_block + 32) {
+            of = ahead.b;
+            base_block = block;
+            const int64_t blocks = ((int64_t)ahead.n * kDecKeys - 1 >> g.page_shift) + 1;
+            const int32_t *list = of < g.B ? g.table + of * g.max_blocks : g.prefix_table;
+            pages = block + lane < blocks ? __ldg(list + block + lane) : 0;
+        }
+        const int32_t page = __shfl_sync(0xffffffffu, pages, (int)(block - base_block));
         int32_t z = page * g.Hk + ahead.hr / g.row_groups;
         if (page < 0 || page >= g.n_pages) {
             if (lane == 0)
@@ -463,7 +465,6 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
         }
         --to_load;
         ahead.next(g, most);
-        page = look_up();
     };
     bool ok = true;
     int64_t issued = 0, done = 0;
@@ -680,8 +681,7 @@ struct PrefixSource {
         return {(int32_t)cid, d.clusters, d.groups, d.per, chunks};
     }
     // The suffixes, on the CTAs without prefix work, or on all behind it: two
-    // warpgroups, with 216 registers a thread.  setmaxnreg of the roles before:
-    // 240 / 144 / 104.
+    // warpgroups, with 216 registers a thread (after the roles' 232 / 128 / 104).
     template <typename T, int LAYOUT, int D>
     __device__ __forceinline__ void finish(const Walk &w, uint8_t *smem) const
     {
@@ -842,6 +842,7 @@ __global__ void __launch_bounds__(128) rope_decode_merge_kernel(const __grid_con
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     pdl_wait();
+    pdl_trigger();
     if (row >= (int64_t)g.B * g.Hq)
         return;
     const int32_t b = (int32_t)(row / g.Hq), h = (int32_t)(row - (int64_t)b * g.Hq);

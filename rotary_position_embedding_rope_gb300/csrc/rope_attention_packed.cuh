@@ -322,17 +322,23 @@ __global__ void __launch_bounds__(kPackedPrepThreads)
 //   warps 8-11  the leader's S = Q K^T issue, its O += P V issue, the CTA's
 //               copies of queries and keys, and of values.
 // The softmax holds a row's 128 scores in registers, so the warpgroups trade
-// registers (setmaxnreg): 240 / 144 / 104 of the 168 they start with.
+// registers (setmaxnreg): 232 / 128 / 104 of the 168 they start with (240 / 144
+// spilled in the tile loop: 340 us against 317 on the prompts below, side by side).
 //
 // With query rotation and epilogue on the softmax warps' path (their loop then
 // ran tiles, rotation, epilogue in turn, 224 threads a CTA) eight causal prompts
 // of 16.4k tokens in all, Hq 32, Hk 8, D 128 took 384 us in this kernel; with
-// the helpers 336 us (0.383 TFLOP of visible pairs: 1140 TFLOP/s).
+// the helpers 336 us, and with the next unit looked up early 305 us.
 
 constexpr int kPackedThreads = 384;
 constexpr int kPackedSIssueWarp = 8, kPackedPVIssueWarp = 9, kPackedKeyWarp = 10, kPackedValueWarp = 11;
 constexpr int kPackedStages = k2Stages;
-constexpr int kPackedStats = 4;                // units whose row statistics are kept
+constexpr int kPackedStats = 8;                // units whose row statistics are kept
+// O buffers in TMEM: beside three S buffers there is room for two of 64 columns,
+// or one of 128.  With two, the next unit's first O += P V does not wait for the
+// helpers to read the last unit's O.
+template <int D>
+static constexpr uint32_t kPackedOBufs = D == 64 ? 2 : 1;
 template <int D>
 static constexpr uint32_t kPackedTile = kAttnRows * D * 2;
 template <int D>
@@ -438,18 +444,19 @@ struct PackedSource {
     // the list in even rounds r and r * clusters + clusters - 1 - c in odd ones,
     // so a cluster that got the longer work of one round gets the shorter of the
     // next.
+    // (launch_packed refuses calls of 2^32 units)
     struct Cursor {
-        int64_t r;
+        uint32_t r;
     };
     struct Walk {
-        int64_t n_units, clusters, cid;
+        uint32_t n_units, clusters, cid;
     };
     template <int D>
     __device__ __forceinline__ Walk walk(int64_t cid, int64_t clusters, uint8_t *) const
     {
-        return {(int64_t)__ldg(n_entries) * head_units, clusters, cid};
+        return {(uint32_t)__ldg(n_entries) * (uint32_t)head_units, (uint32_t)clusters, (uint32_t)cid};
     }
-    __device__ __forceinline__ int64_t at(const Walk &w, const Cursor &c) const
+    __device__ __forceinline__ uint32_t at(const Walk &w, const Cursor &c) const
     {
         return c.r * w.clusters + ((c.r & 1) ? w.clusters - 1 - w.cid : w.cid);
     }
@@ -458,13 +465,13 @@ struct PackedSource {
     __device__ __forceinline__ bool valid(const Walk &w, const Cursor &c) const { return at(w, c) < w.n_units; }
     __device__ __forceinline__ int32_t tiles(const Walk &w, const Cursor &c) const
     {
-        return __ldg(&entries[at(w, c) / head_units].n_tiles);
+        return __ldg(&entries[at(w, c) / (uint32_t)head_units].n_tiles);
     }
     __device__ __forceinline__ PackedUnit unit(const Walk &w, const Cursor &c, int lg) const
     {
-        const int64_t L = at(w, c);
-        const int64_t i = L / head_units;
-        const int32_t hu = (int32_t)(L - i * head_units);
+        const uint32_t L = at(w, c);
+        const uint32_t i = L / (uint32_t)head_units;
+        const int32_t hu = (int32_t)(L - i * (uint32_t)head_units);
         const int4 x = __ldg(reinterpret_cast<const int4 *>(entries + i));
         const int2 y = __ldg(reinterpret_cast<const int2 *>(entries + i) + 2);
         PackedUnit u;
@@ -509,35 +516,104 @@ struct PackedSource {
     }
 };
 
+// Brings a table row to L1, one 128-byte line after the other, by `parts` threads.
+__device__ __forceinline__ void prefetch_table_row(const AttnArgs &a, int64_t trow, int part, int parts)
+{
+    const int64_t at = trow * (a.rotary_dim / 2);
+    for (int i = part * 32; i < a.rotary_dim / 2; i += parts * 32) {
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.cos + at + i));
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.sin + at + i));
+    }
+}
+
 // Rotates one query tile in place (rows r = token * GP + head; tokens past the
 // sequence's end hold zeros): a thread per row, its table row read from global
 // memory.  The helpers run this beside the tile loop, so its latency is hidden.
+//
+// rotate_pairs2 is rotate_pair on two pairs at once (f32x2 instructions, half
+// as many: the helpers share the issue slots of the softmax warps).  With w =
+// c d rounded, c d - w is exact, so (a b - w) - (c d - w), each fma rounded
+// once, is diff_of_products's sum (equal up to the sign of a zero).
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ void rotate_pairs2(uint64_t &x1, uint64_t &x2, uint64_t c, uint64_t s)
+{
+    const uint64_t minus = 0xbf800000bf800000ull, sign = 0x8000000080000000ull;    // (-1, -1), sign bits
+    const uint64_t n2 = x2 ^ sign;
+    const uint64_t w1 = mul_f32x2(n2, s), w2 = mul_f32x2(x2, c);       // -(x2 s), -(-x2 c)
+    const uint64_t y1 = fma_f32x2(fma_f32x2(x2, s, w1), minus, fma_f32x2(x1, c, w1));
+    const uint64_t y2 = fma_f32x2(fma_f32x2(n2, c, w2), minus, fma_f32x2(x1, s, w2));
+    x1 = y1;
+    x2 = y2;
+}
+
+// Eight 16-bit elements as four f32x2 pairs of neighbours, and back.
+template <typename T>
+__device__ __forceinline__ void unpack_x2(const uint4 &u, uint64_t (&p)[4])
+{
+    float f[8];
+    Elt<T>::unpack(u, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        p[i] = f32x2(f[2 * i], f[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack_x2(const uint64_t (&p)[4])
+{
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f32x2_split(p[i], f[2 * i], f[2 * i + 1]);
+    return Elt<T>::pack(f);
+}
+
 template <typename T, int LAYOUT>
 __device__ __forceinline__ void rotate_packed_row(uint8_t *sQ, int64_t trow, const AttnArgs &a, int r)
 {
     if (trow < 0)
         return;
-    constexpr int NQ = LAYOUT == 0 ? 2 : 1;
-    const int rd = a.rotary_dim, h8 = rd / 16;
-    const int per_row = LAYOUT == 0 ? rd / 16 : rd / 8;
-    const float4 *c = reinterpret_cast<const float4 *>(a.cos + trow * (rd / 2));
-    const float4 *s = reinterpret_cast<const float4 *>(a.sin + trow * (rd / 2));
+    const int rd = a.rotary_dim;
+    const ulonglong2 *c = reinterpret_cast<const ulonglong2 *>(a.cos + trow * (rd / 2));
+    const ulonglong2 *s = reinterpret_cast<const ulonglong2 *>(a.sin + trow * (rd / 2));
+    if constexpr (LAYOUT == 0) {
+        const int h8 = rd / 16;                    // chunk p of one half with chunk p of the other
 #pragma unroll 2
-    for (int p = 0; p < per_row; ++p) {
-        KeyItem it;
-        it.o1 = sw128(r, p);
-        it.o2 = sw128(r, p + h8);
-        it.rot = true;
-        it.x1 = *reinterpret_cast<const uint4 *>(sQ + it.o1);
-        if (LAYOUT == 0)
-            it.x2 = *reinterpret_cast<const uint4 *>(sQ + it.o2);
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-            const float4 c4 = __ldg(c + p * NQ + q), s4 = __ldg(s + p * NQ + q);
-            it.cs[4 * q] = c4.x; it.cs[4 * q + 1] = c4.y; it.cs[4 * q + 2] = c4.z; it.cs[4 * q + 3] = c4.w;
-            it.sn[4 * q] = s4.x; it.sn[4 * q + 1] = s4.y; it.sn[4 * q + 2] = s4.z; it.sn[4 * q + 3] = s4.w;
+        for (int p = 0; p < h8; ++p) {
+            uint4 *q1 = reinterpret_cast<uint4 *>(sQ + sw128(r, p));
+            uint4 *q2 = reinterpret_cast<uint4 *>(sQ + sw128(r, p + h8));
+            const ulonglong2 c0 = __ldg(c + 2 * p), c1 = __ldg(c + 2 * p + 1);
+            const ulonglong2 s0 = __ldg(s + 2 * p), s1 = __ldg(s + 2 * p + 1);
+            uint64_t x1[4], x2[4];
+            unpack_x2<T>(*q1, x1);
+            unpack_x2<T>(*q2, x2);
+            rotate_pairs2(x1[0], x2[0], c0.x, s0.x);
+            rotate_pairs2(x1[1], x2[1], c0.y, s0.y);
+            rotate_pairs2(x1[2], x2[2], c1.x, s1.x);
+            rotate_pairs2(x1[3], x2[3], c1.y, s1.y);
+            *q1 = pack_x2<T>(x1);
+            *q2 = pack_x2<T>(x2);
         }
-        store_key_item<T, LAYOUT>(it, sQ);
+    } else {
+#pragma unroll 2
+        for (int p = 0; p < rd / 8; ++p) {         // the pairs (0,1) (2,3) (4,5) (6,7) of chunk p
+            uint4 *q = reinterpret_cast<uint4 *>(sQ + sw128(r, p));
+            const ulonglong2 cv = __ldg(c + p), sv = __ldg(s + p);
+            float f[8], g[8];
+            Elt<T>::unpack(*q, f);
+            uint64_t a0 = f32x2(f[0], f[2]), b0 = f32x2(f[1], f[3]);
+            uint64_t a1 = f32x2(f[4], f[6]), b1 = f32x2(f[5], f[7]);
+            rotate_pairs2(a0, b0, cv.x, sv.x);
+            rotate_pairs2(a1, b1, cv.y, sv.y);
+            f32x2_split(a0, g[0], g[2]);
+            f32x2_split(b0, g[1], g[3]);
+            f32x2_split(a1, g[4], g[6]);
+            f32x2_split(b1, g[5], g[7]);
+            *q = Elt<T>::pack(g);
+        }
     }
 }
 
@@ -545,7 +621,7 @@ template <typename T, int LAYOUT, int D, typename Source>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
     rope_attn_packed_kernel(const __grid_constant__ Source src, const int lg)
 {
-    constexpr uint32_t kTile = kPackedTile<D>, kHalf = kPackedHalf<D>;
+    constexpr uint32_t kTile = kPackedTile<D>, kHalf = kPackedHalf<D>, kOBufs = kPackedOBufs<D>;
     constexpr uint32_t ab_format = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     const AttnArgs &a = src.a;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -561,15 +637,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
     // done, which releases the value stage (multicast).
     // Per unit with key tiles: query tile landed and rotated (leader only, each
     // helper warp of both CTAs), per query buffer; its last S done (multicast),
-    // per query buffer; its last O += P V done (multicast); its row statistics
-    // written (each softmax warp), per statistics buffer; its O read (leader
-    // only, each helper warp of both CTAs).  At the end: all MMAs of an issuer.
+    // per query buffer; its last O += P V done (multicast) and its O read (leader
+    // only, each helper warp of both CTAs), per O buffer; its row statistics
+    // written (each softmax warp), per statistics buffer.  At the end: all MMAs
+    // of an issuer.
     // A parity wait is sound only for the phase right after the last one known
     // complete: every barrier below is waited for phase by phase, or its next
     // phase cannot complete before the waiter has moved on.
     __shared__ __align__(8) uint64_t bar_kfull[kPackedStages], bar_vfull[kPackedStages],
-        bar_s[k2SBufs], bar_p[k2SBufs], bar_o[k2SBufs], bar_q[2], bar_qr[2], bar_qfree[2], bar_odone,
-        bar_stat[kPackedStats], bar_ofree, bar_drain[2];
+        bar_s[k2SBufs], bar_p[k2SBufs], bar_o[k2SBufs], bar_q[2], bar_qr[2], bar_qfree[2],
+        bar_odone[kOBufs], bar_stat[kPackedStats], bar_ofree[kOBufs], bar_drain[2];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
 
@@ -604,8 +681,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
         }
         for (int b = 0; b < kPackedStats; ++b)
             mbar_init(&bar_stat[b], kAttnRows / 32);
-        mbar_init(&bar_odone, 1);
-        mbar_init(&bar_ofree, kBoth);
+        for (uint32_t b = 0; b < kOBufs; ++b) {
+            mbar_init(&bar_odone[b], 1);
+            mbar_init(&bar_ofree[b], kBoth);
+        }
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -631,8 +710,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
     };
     // what ran before this launch (the prepare kernel) is complete from here on
     pdl_wait();
-    if constexpr (Source::kPrefix)
-        pdl_trigger();                             // (the merge waits for all of this launch)
+    pdl_trigger();                                 // (what follows waits for all of this launch)
     const typename Source::Walk walk = src.template walk<D>(blockIdx.x >> 1, gridDim.x >> 1, smem);   // (CTA-wide)
     using Cursor = typename Source::Cursor;
     auto valid = [&](const Cursor &c) { return src.valid(walk, c); };
@@ -651,18 +729,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
 
     if (warp < 4) {
         // ---- the softmax of this CTA's rows
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        const uint32_t o_base = tmem + k2OCol + lanes;
         uint32_t sb = 0, s_ph = 0;                 // S buffer of this tile and its phase parity
         uint32_t ob = 0, o_ph = 0;                 // the same for the previous tile (O barriers)
-        uint32_t stat = 0;
-        for (Cursor c = with_tiles(src.first(walk)); ok && valid(c); c = next_with_tiles(c)) {
-            const PackedUnit u = unit_of(c);
-            const int32_t n_tiles = u.n_tiles;
-            const int64_t shift = (int64_t)u.n_keys - u.tokens;
-            const int64_t qi = u.tok0 + (int)rank * tokens + (tid >> lg);
-            const int64_t k0 = (int64_t)u.first * kAttnKeys;
+        uint32_t stat = 0;                         // statistics buffer; its low bit: O buffer
+        // the next unit is looked up a unit early: between units, its loads would
+        // be all that the softmax waits for
+        Cursor c = with_tiles(src.first(walk));
+        PackedUnit un = {};
+        if (valid(c))
+            un = unit_of(c);
+        while (ok && valid(c)) {
+            const int32_t n_tiles = un.n_tiles, n_keys = un.n_keys;
+            const int64_t shift = (int64_t)un.n_keys - un.tokens;
+            const int64_t qi = un.tok0 + (int)rank * tokens + (tid >> lg);
+            const int64_t k0 = (int64_t)un.first * kAttnKeys;
+            const uint32_t o_base = tmem + k2OCol + lanes + (stat % kOBufs) * D;
+            c = next_with_tiles(c);
+            const bool more = valid(c);
+            if (more)
+                un = unit_of(c);
             float m_ref = -INFINITY, l_run = 0.0f;
             for (int32_t kt = 0; kt < n_tiles; ++kt) {
                 const uint32_t b = sb;
@@ -677,7 +764,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 };
                 softmax_tile<T, D, true, false>(tmem + b * kAttnKeys + lanes, o_base, qi,
                                                 k0 + (int64_t)kt * kAttnKeys, shift, a, 0, kt > 0, m_ref,
-                                                l_run, o_ready, (int64_t)u.n_keys);
+                                                l_run, o_ready, (int64_t)n_keys);
                 ok = o_ok;
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -691,22 +778,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 if (!ok)
                     break;
             }
-            // (the buffer's previous unit, four before this one, is written: the
-            // last O += P V of the unit after it waited for its O to be read)
+            // (the buffer's previous unit, eight before this one, is written: this
+            // unit's S waited for an O += P V at most three tiles back, and that for
+            // the output of the unit one or two before its own)
             sStat[stat * kAttnRows + tid] = make_float2(m_ref, l_run);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&bar_stat[stat]);
             stat = (stat + 1) % kPackedStats;
+            if (!more)
+                break;
         }
         if (!ok)
             raise_abort();
     } else if (warp < 8) {
         // ---- the helpers.  A pass: rotate the next unit's query tile, then write
         // this unit's output.  The first pass only rotates.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 144;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
         const int row = tid - 128, wq = warp - 4;  // row of the tile = TMEM lane
-        const uint32_t o_base = tmem + k2OCol + ((uint32_t)(wq * 32) << 16);
         uint32_t qn = 0, un = 0;                   // query tiles rotated, units with tiles written
         int32_t o_seq = -1;                        // the sequence whose O map was acquired
         Cursor cq = with_tiles(src.first(walk));   // the unit whose query tile is next
@@ -719,6 +808,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 const uint32_t b = qn & 1u;
                 const int32_t tok = u.tok0 + (int)rank * tokens + (row >> lg);
                 const int64_t trow = tok < u.tokens ? src.table_row(u, tok) : -1;
+                if (trow >= 0)
+                    prefetch_table_row(a, trow, row & ((1 << lg) - 1), 1 << lg);
                 ok = __all_sync(0xffffffffu, attn_wait(&bar_q[b], (qn >> 1) & 1u, abort));
                 if (!ok)
                     break;
@@ -732,30 +823,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 continue;
             const PackedUnit u = unit_of(c);
             src.next(walk, c);
+            // the staging tile is free once the last store has read it
+            if (lane == 0)
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
             float2 stat = make_float2(-INFINITY, 0.0f);
             if (u.n_tiles > 0) {
                 ok = __all_sync(0xffffffffu,
                                 attn_wait(&bar_stat[un % kPackedStats], (un / kPackedStats) & 1u, abort) &&
-                                    attn_wait(&bar_odone, un & 1u, abort));
+                                    attn_wait(&bar_odone[un % kOBufs], (un / kOBufs) & 1u, abort));
                 if (!ok)
                     break;
                 stat = sStat[(un % kPackedStats) * kAttnRows + row];
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             }
             const int32_t y0 = u.tok0 + (int)rank * tokens + wq * (32 >> lg);
+            const uint32_t o_base = tmem + k2OCol + ((uint32_t)(wq * 32) << 16) + (un % kOBufs) * D;
             if constexpr (Source::kPrefix) {
                 src.template store_rows<D>(u, o_base, y0, lane, lg, stat);
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                arrive_leader(&bar_ofree[un % kOBufs]);
             } else {
                 // O / l of the warp's 32 rows, staged and stored by TMA (boxes
                 // of 64 features x GP heads x 32 / GP tokens; tokens past the
                 // sequence's end are not written, and a box that starts past
-                // it is not issued)
-                if (lane == 0)
-                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                __syncwarp();
-                stage_o_row<T, D>(o_base, sO, row, u.n_tiles > 0, stat.y);
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                // it is not issued).  O is free for the next unit's products
+                // as soon as the last of it is in registers.
+                const float inv = stat.y > 0.0f ? 1.0f / stat.y : 0.0f;
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    float ov[64];
+                    if (u.n_tiles > 0) {
+                        tmem_ld32_nowait(o_base + c0, ov);
+                        tmem_ld32_nowait(o_base + c0 + 32, ov + 32);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                        if (c0 + 64 == D) {
+                            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                            arrive_leader(&bar_ofree[un % kOBufs]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            ov[i] = 0.0f;
+                    }
+#pragma unroll
+                    for (int ch = 0; ch < 8; ++ch) {
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            f[e] = ov[ch * 8 + e] * inv;
+                        *reinterpret_cast<uint4 *>(sO + sw128(row, c0 / 8 + ch)) = Elt<T>::pack(f);
+                    }
+                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0 && y0 < u.tokens) {
@@ -769,10 +888,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             }
-            if (u.n_tiles > 0) {
-                arrive_leader(&bar_ofree);
+            if (u.n_tiles > 0)
                 ++un;
-            }
         }
         drain_o_stores();
         if (!ok)
@@ -818,20 +935,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                     }
                 }
             }
-            if (lane == 0)
-                umma2_commit(&bar_drain[0], 1);
-            __syncwarp();
-            if (!__all_sync(0xffffffffu, attn_wait(&bar_drain[0], 0u)))
-                ok = false;
+            if (qn > 0) {
+                if (lane == 0)
+                    umma2_commit(&bar_drain[0], 1);
+                __syncwarp();
+                if (!__all_sync(0xffffffffu, attn_wait(&bar_drain[0], 0u)))
+                    ok = false;
+            }
         } else if (warp == kPackedPVIssueWarp && leader) {
             // ---- O += P V for both CTAs once both P are in TMEM
             const uint32_t idesc = umma_idesc(256, D, ab_format, 1);
             uint32_t sb = 0, ph = 0, un = 0;
             for (Cursor c = with_tiles(src.first(walk)); ok && valid(c); c = next_with_tiles(c)) {
                 const int32_t n_tiles = src.tiles(walk, c);
-                // both CTAs have read the previous unit's O
-                if (un > 0)
-                    ok = __all_sync(0xffffffffu, attn_wait(&bar_ofree, (un - 1) & 1u, abort));
+                // both CTAs have read the O this unit's overwrites
+                const uint32_t o_col = k2OCol + (un % kOBufs) * D, ob = un % kOBufs;
+                if (un >= kOBufs)
+                    ok = __all_sync(0xffffffffu, attn_wait(&bar_ofree[ob], (un / kOBufs - 1) & 1u, abort));
                 ++un;
                 for (int32_t kt = 0; ok && kt < n_tiles; ++kt) {
                     ok = __all_sync(0xffffffffu, attn_wait(&bar_p[sb], ph, abort) &&
@@ -843,11 +963,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                         const uint32_t v_addr = attn_smem_u32(sV(sb));
 #pragma unroll
                         for (int kk = 0; kk < kAttnKeys / 16; ++kk)
-                            umma2_ts(tmem + k2OCol, tmem + sb * kAttnKeys + kk * 8,
+                            umma2_ts(tmem + o_col, tmem + sb * kAttnKeys + kk * 8,
                                      packed_v_desc<D>(v_addr, kk), idesc, (kt > 0 || kk > 0) ? 1u : 0u);
                         umma2_commit(&bar_o[sb], 3);
                         if (kt + 1 == n_tiles)
-                            umma2_commit(&bar_odone, 3);
+                            umma2_commit(&bar_odone[ob], 3);
                     }
                     __syncwarp();
                     if (++sb == k2SBufs) {
@@ -856,11 +976,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                     }
                 }
             }
-            if (lane == 0)
-                umma2_commit(&bar_drain[1], 1);
-            __syncwarp();
-            if (!__all_sync(0xffffffffu, attn_wait(&bar_drain[1], 0u)))
-                ok = false;
+            if (un > 0) {
+                if (lane == 0)
+                    umma2_commit(&bar_drain[1], 1);
+                __syncwarp();
+                if (!__all_sync(0xffffffffu, attn_wait(&bar_drain[1], 0u)))
+                    ok = false;
+            }
         } else if (warp == kPackedKeyWarp) {
             // ---- the first query tile; then per unit this CTA's halves of key
             // tile g into stage g mod 3 once S(g - 3) released it, and, behind the
@@ -1143,6 +1265,8 @@ static cudaError_t launch_packed(const PackedArgs &c, const PackedLayout &lay, c
 
     PackedSource ka;
     memset(&ka, 0, sizeof ka);
+    if (lay.tiles * (c.Hq / gp) >= (1ll << 32) - 1024)
+        return cudaErrorInvalidConfiguration;
     ka.a.cos = k.cos; ka.a.sin = k.sin; ka.a.rotary_dim = k.rotary_dim; ka.a.table_rows = k.table_rows;
     ka.a.scale_log2 = c.scale_log2; ka.a.causal = c.causal; ka.a.flag = k.flag;
     ka.entries = p.entries; ka.n_entries = p.n_entries; ka.maps = p.maps;

@@ -36,6 +36,8 @@ __global__ void __launch_bounds__(kRowThreads) rope_cache_append_kernel(const Ro
     const bool live = t < a.total;
     const RowPart part = row_part<LAYOUT>(j, a.rotary_dim);
 
+    pdl_wait();
+    pdl_trigger();
     uint4 k0[kRowHeads], k1[kRowHeads], v0[kRowHeads], v1[kRowHeads];
     const T *ks = static_cast<const T *>(a.k) + t * a.k_stride;
     const T *vs = static_cast<const T *>(a.v) + t * a.v_stride;
@@ -124,8 +126,7 @@ static cudaError_t append_t(const RowsArgs &a, cudaStream_t st)
     const int64_t blocks = (a.total * chunks + groups - 1) / groups;
     if (blocks > 0x7fffffff)
         return cudaErrorInvalidConfiguration;
-    rope_cache_append_kernel<T, LAYOUT, D><<<(unsigned)blocks, kRowThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_hot(rope_cache_append_kernel<T, LAYOUT, D>, dim3((unsigned)blocks), dim3(kRowThreads), 0, st, a);
 }
 
 template <typename T>
