@@ -44,7 +44,7 @@ struct PlanSizes {
     int32_t clusters, sms;                         // most prefix clusters; SMs
     int32_t tile_ns;                               // a cluster's time per key tile
     int32_t heads, chunk_bytes;                    // pairs of a sequence; keys and values of a chunk
-    float prefix_bytes;
+    float sm_rate, tile_bytes;                     // copies of an SM, bytes/ns; keys and values of a tile
 };
 
 // The prefix on c clusters: `groups` of them (one cluster per row tile in each)
@@ -64,24 +64,30 @@ __host__ __device__ inline PrefixDeal prefix_deal(const PlanSizes &p, int32_t c)
 
 // Estimated time, in ns, with c clusters on the prefix and the suffixes' chunks
 // (of one pair per sequence) on the SMs left over -- or, with every cluster on
-// the prefix, behind it.  Measured here: tile_ns a cluster tile, 4 us from one
-// unit to the next, 45 bytes/ns for the copies of one SM.  All copies together
-// get 6500 bytes/ns; beyond that both sides slow down alike.  An estimate that
-// is off costs balance, never a result.
+// the prefix, behind it.  Measured here: tile_ns a cluster tile, half as long
+// again once all copies together reach 6500 bytes/ns; 4 us from one unit to the
+// next; sm_rate bytes/ns for the copies of one SM.  An estimate that is off
+// costs balance, never a result.  Forced to c clusters, whole calls took (us):
+//   64 sequences, 8k prefix:    c = 12: 61   16: 54   20: 56   32: 65   76: 66
+//   256 sequences, 4k prefix:   c = 4: 357   8: 348  12: 330   16: 348  76: 378
+//   32 sequences, 128k prefix:  c = 60: 131  68: 120  72: 117  76: 122
+// where this picks 19, 8 and 72.
 __host__ __device__ inline float plan_ns(const PlanSizes &p, int32_t c, float chunks)
 {
     const PrefixDeal d = prefix_deal(p, c);
     const int32_t rounds = (p.row_tiles + c - 1) / c;
     const float bytes = chunks * (float)p.heads * (float)p.chunk_bytes;
-    const float prefix = (float)rounds * ((float)d.per * (float)p.tile_ns +
+    const bool beside = 2 * c < p.sms;
+    const float side = p.sm_rate * (float)(p.sms - 2 * c);
+    const float tiles = (float)c * p.tile_bytes / ((float)p.tile_ns * (float)p.row_tiles);
+    const float slow = beside && bytes > 0.0f && side + tiles > 6500.0f ? 1.5f : 1.0f;
+    const float prefix = (float)rounds * ((float)d.per * (float)p.tile_ns * slow +
                                           4000.0f * (float)(1 + d.per / p.tiles));
     if (bytes == 0.0f)
         return prefix;
-    if (2 * c >= p.sms)
-        return prefix + 8000.0f + bytes / 6500.0f;
-    const float suffix = bytes / (45.0f * (float)(p.sms - 2 * c));
-    const float demand = (45.0f * (float)(p.sms - 2 * c) + p.prefix_bytes / prefix) / 6500.0f;
-    return 8000.0f + fmaxf(prefix, suffix) * fmaxf(demand, 1.0f);
+    if (!beside)
+        return prefix + 10000.0f + bytes / fminf(6500.0f, p.sm_rate * (float)p.sms);
+    return fmaxf(prefix, bytes / fminf(side, 6500.0f - tiles / slow));
 }
 
 // Clusters for the prefix, by every thread of a CTA of at least p.clusters
@@ -681,7 +687,7 @@ struct PrefixSource {
         return {(int32_t)cid, d.clusters, d.groups, d.per, chunks};
     }
     // The suffixes, on the CTAs without prefix work, or on all behind it: two
-    // warpgroups, with 216 registers a thread (after the roles' 232 / 128 / 104).
+    // warpgroups, with 216 registers a thread (after the roles' 240 / 112 / 104).
     template <typename T, int LAYOUT, int D>
     __device__ __forceinline__ void finish(const Walk &w, uint8_t *smem) const
     {
@@ -1013,7 +1019,7 @@ static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, c
         s.sizes.sms = 2 * clusters;
         s.sizes.tile_ns = D == 128 ? 850 : 700;
         s.sizes.heads = c.Hk * lay.row_groups; s.sizes.chunk_bytes = kDecStageBytes<D>;
-        s.sizes.prefix_bytes = 4.0f * D * c.Hk * (float)c.n_prefix;
+        s.sizes.sm_rate = D == 128 ? 50.0f : 30.0f; s.sizes.tile_bytes = 4.0f * D * kAttnKeys;
         s.pages = c.prefix_table;
         s.out = reinterpret_cast<float *>(ws + lay.prefix_out);
         s.stats = reinterpret_cast<float2 *>(ws + lay.prefix_stats);

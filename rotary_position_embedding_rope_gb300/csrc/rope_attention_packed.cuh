@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kPackedPrepThreads)
 //   warps 8-11  the leader's S = Q K^T issue, its O += P V issue, the CTA's
 //               copies of queries and keys, and of values.
 // The softmax holds a row's 128 scores in registers, so the warpgroups trade
-// registers (setmaxnreg): 232 / 128 / 104 of the 168 they start with (240 / 144
+// registers (setmaxnreg): 240 / 112 / 104 of the 168 they start with (240 / 144
 // spilled in the tile loop: 340 us against 317 on the prompts below, side by side).
 //
 // With query rotation and epilogue on the softmax warps' path (their loop then
@@ -411,6 +411,30 @@ __device__ __forceinline__ void load_half_box_l2(uint8_t *dst, const CUtensorMap
                      ::"r"(attn_smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z),
                        "r"(peer_addr(bar, 0)), "l"(policy)
                      : "memory");
+}
+
+// The bounded wait of this kernel's roles: attn_wait with tries counted instead
+// of cycles (a failed try_wait suspends the thread for about 4 us here, so the
+// limit is some 2 s), which makes each of its twenty copies half as long.
+constexpr int kRoleTries = 1 << 19;
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, const volatile int *abort)
+{
+    const uint32_t b = attn_smem_u32(bar);
+#pragma unroll 1
+    for (int i = 0; i < kRoleTries; ++i) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done)
+                     : "r"(b), "r"(parity)
+                     : "memory");
+        if (done)
+            return true;
+        if (*abort)
+            break;
+    }
+    return false;
 }
 
 // One unit of work of a cluster: the rows (token, head) of tokens tok0 .. and
@@ -623,6 +647,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
 {
     constexpr uint32_t kTile = kPackedTile<D>, kHalf = kPackedHalf<D>, kOBufs = kPackedOBufs<D>;
     constexpr uint32_t ab_format = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    // How far the issue loops are unrolled.  Fully unrolled, the prefix's kernel and
+    // the D = 64 ones fall into a mode where the softmax step takes twice as long
+    // at full clocks and no wait grows (their code and the softmax's loop no longer
+    // sit together in the instruction cache, as it seems): 32 sequences after 128k
+    // keys 194 us, with 4 / 2 122 us; D = 64 124 and 115 us.  D = 128 over packed
+    // sequences is bound by the issue of its products: 4 / 2 costs 1 %.
+    constexpr bool kIssueBound = D == 128 && !Source::kPrefix;
+    constexpr int kSUnroll = kIssueBound ? 8 : 4, kPVUnroll = kIssueBound ? 4 : 2;
     const AttnArgs &a = src.a;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *sStages = smem + 2 * kTile;
@@ -636,8 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
     // (multicast); P ready (leader only, each softmax warp of both CTAs); O += P V
     // done, which releases the value stage (multicast).
     // Per unit with key tiles: query tile landed and rotated (leader only, each
-    // helper warp of both CTAs), per query buffer; its last S done (multicast),
-    // per query buffer; its last O += P V done (multicast) and its O read (leader
+    // helper warp of both CTAs), per query buffer; its last O += P V done (multicast) and its O read (leader
     // only, each helper warp of both CTAs), per O buffer; its row statistics
     // written (each softmax warp), per statistics buffer.  At the end: all MMAs
     // of an issuer.
@@ -645,7 +676,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
     // complete: every barrier below is waited for phase by phase, or its next
     // phase cannot complete before the waiter has moved on.
     __shared__ __align__(8) uint64_t bar_kfull[kPackedStages], bar_vfull[kPackedStages],
-        bar_s[k2SBufs], bar_p[k2SBufs], bar_o[k2SBufs], bar_q[2], bar_qr[2], bar_qfree[2],
+        bar_s[k2SBufs], bar_p[k2SBufs], bar_o[k2SBufs], bar_q[2], bar_qr[2],
         bar_odone[kOBufs], bar_stat[kPackedStats], bar_ofree[kOBufs], bar_drain[2];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -676,7 +707,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bar_q[b], 1);
             mbar_init(&bar_qr[b], kBoth);
-            mbar_init(&bar_qfree[b], 1);
             mbar_init(&bar_drain[b], 1);
         }
         for (int b = 0; b < kPackedStats; ++b)
@@ -729,7 +759,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
 
     if (warp < 4) {
         // ---- the softmax of this CTA's rows
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         uint32_t sb = 0, s_ph = 0;                 // S buffer of this tile and its phase parity
         uint32_t ob = 0, o_ph = 0;                 // the same for the previous tile (O barriers)
@@ -753,13 +783,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
             float m_ref = -INFINITY, l_run = 0.0f;
             for (int32_t kt = 0; kt < n_tiles; ++kt) {
                 const uint32_t b = sb;
-                ok = __all_sync(0xffffffffu, attn_wait(&bar_s[b], s_ph, abort));
+                ok = __all_sync(0xffffffffu, role_wait(&bar_s[b], s_ph, abort));
                 if (!ok)
                     break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 bool o_ok = true;
                 auto o_ready = [&]() {
-                    o_ok = __all_sync(0xffffffffu, attn_wait(&bar_o[ob], o_ph, abort));
+                    o_ok = __all_sync(0xffffffffu, role_wait(&bar_o[ob], o_ph, abort));
                     return o_ok;
                 };
                 softmax_tile<T, D, true, false>(tmem + b * kAttnKeys + lanes, o_base, qi,
@@ -792,14 +822,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
         if (!ok)
             raise_abort();
     } else if (warp < 8) {
-        // ---- the helpers.  A pass: rotate the next unit's query tile, then write
-        // this unit's output.  The first pass only rotates.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
+        // ---- the helpers.  A pass: rotate the next unit's query tile, write this
+        // unit's output, and (warp 4) request the query tile of the unit after the
+        // next: its buffer is this unit's, whose last product has finished.  The
+        // first pass requests two tiles and only rotates.  (Query tiles requested by
+        // the key warp, between key tiles, held the fourth key tile of every unit
+        // up for 1.5 us: the map has to be acquired first.)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         const int row = tid - 128, wq = warp - 4;  // row of the tile = TMEM lane
         uint32_t qn = 0, un = 0;                   // query tiles rotated, units with tiles written
         int32_t o_seq = -1;                        // the sequence whose O map was acquired
         Cursor cq = with_tiles(src.first(walk));   // the unit whose query tile is next
         Cursor c = src.first(walk);                // the unit whose output is next
+        Cursor cl = cq;                            // the unit whose query tile is requested next
+        uint32_t ln = 0;                           // query tiles requested
+        auto load_query = [&]() {
+            if (wq == 0 && valid(cl)) {
+                const PackedUnit u = unit_of(cl);
+                const CUtensorMap *map;
+                if constexpr (Source::kPrefix) {
+                    map = &src.q_map;
+                } else {
+                    map = src.maps + (int64_t)u.seq * kPackedMaps + 2;
+                    acquire_map(map);
+                }
+                const uint32_t b = ln & 1u;
+                if (lane == 0)
+                    mbar_expect_tx(&bar_q[b], kTile);
+                __syncwarp();
+                // (tokens past the sequence's end arrive as zeros)
+                if (lane < D / 64)
+                    tma_load_3d(sQ(b) + lane * kBoxBytes, map, lane * 64, u.head0,
+                                u.tok0 + (int)rank * tokens, &bar_q[b]);
+                __syncwarp();
+                ++ln;
+                cl = next_with_tiles(cl);
+            }
+        };
+        load_query();
+        load_query();
         for (bool start = true; ok && (start || valid(c)); start = false) {
             // the next query tile, at most one ahead of the unit being written (a
             // second one would wait for products that wait for this output)
@@ -810,7 +871,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 const int64_t trow = tok < u.tokens ? src.table_row(u, tok) : -1;
                 if (trow >= 0)
                     prefetch_table_row(a, trow, row & ((1 << lg) - 1), 1 << lg);
-                ok = __all_sync(0xffffffffu, attn_wait(&bar_q[b], (qn >> 1) & 1u, abort));
+                ok = __all_sync(0xffffffffu, role_wait(&bar_q[b], (qn >> 1) & 1u, abort));
                 if (!ok)
                     break;
                 rotate_packed_row<T, LAYOUT>(sQ(b), trow, a, row);
@@ -830,8 +891,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
             float2 stat = make_float2(-INFINITY, 0.0f);
             if (u.n_tiles > 0) {
                 ok = __all_sync(0xffffffffu,
-                                attn_wait(&bar_stat[un % kPackedStats], (un / kPackedStats) & 1u, abort) &&
-                                    attn_wait(&bar_odone[un % kOBufs], (un / kOBufs) & 1u, abort));
+                                role_wait(&bar_stat[un % kPackedStats], (un / kPackedStats) & 1u, abort) &&
+                                    role_wait(&bar_odone[un % kOBufs], (un / kOBufs) & 1u, abort));
                 if (!ok)
                     break;
                 stat = sStat[(un % kPackedStats) * kAttnRows + row];
@@ -888,12 +949,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             }
-            if (u.n_tiles > 0)
+            if (u.n_tiles > 0) {
+                load_query();
                 ++un;
+            }
         }
         drain_o_stores();
-        if (!ok)
+        if (!ok) {
+            // one more bounded wait for the query tiles requested
             raise_abort();
+            for (uint32_t i = qn; wq == 0 && i < ln; ++i)
+                (void)attn_wait(&bar_q[i & 1u], (i >> 1) & 1u);
+        }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == kPackedSIssueWarp && leader) {
@@ -905,17 +972,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 const int32_t n_tiles = src.tiles(walk, c);
                 const uint32_t qb = qn & 1u;
                 const uint32_t q_addr = attn_smem_u32(sQ(qb));
-                ok = __all_sync(0xffffffffu, attn_wait(&bar_qr[qb], (qn >> 1) & 1u, abort));
+                ok = __all_sync(0xffffffffu, role_wait(&bar_qr[qb], (qn >> 1) & 1u, abort));
                 ++qn;
                 for (int32_t kt = 0; ok && kt < n_tiles; ++kt) {
-                    ok = __all_sync(0xffffffffu, attn_wait(&bar_kfull[sb], ph, abort) &&
-                                                     (first || attn_wait(&bar_o[sb], ph ^ 1u, abort)));
+                    ok = __all_sync(0xffffffffu, role_wait(&bar_kfull[sb], ph, abort) &&
+                                                     (first || role_wait(&bar_o[sb], ph ^ 1u, abort)));
                     if (!ok)
                         break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     if (lane == 0) {
                         const uint32_t k_addr = attn_smem_u32(sK(sb));
-#pragma unroll
+#pragma unroll kSUnroll
                         for (int kk = 0; kk < D / 16; ++kk)
                             umma2_ss(tmem + sb * kAttnKeys,
                                      umma_desc(q_addr + (kk >> 2) * kBoxBytes + (kk & 3) * 32u, 16u,
@@ -924,8 +991,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                                                1024u, kSwizzle128),
                                      idesc, kk > 0);
                         umma2_commit(&bar_s[sb], 3);
-                        if (kt + 1 == n_tiles)
-                            umma2_commit(&bar_qfree[qb], 3);
                     }
                     __syncwarp();
                     if (++sb == k2SBufs) {
@@ -951,17 +1016,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 // both CTAs have read the O this unit's overwrites
                 const uint32_t o_col = k2OCol + (un % kOBufs) * D, ob = un % kOBufs;
                 if (un >= kOBufs)
-                    ok = __all_sync(0xffffffffu, attn_wait(&bar_ofree[ob], (un / kOBufs - 1) & 1u, abort));
+                    ok = __all_sync(0xffffffffu, role_wait(&bar_ofree[ob], (un / kOBufs - 1) & 1u, abort));
                 ++un;
                 for (int32_t kt = 0; ok && kt < n_tiles; ++kt) {
-                    ok = __all_sync(0xffffffffu, attn_wait(&bar_p[sb], ph, abort) &&
-                                                     attn_wait(&bar_vfull[sb], ph, abort));
+                    ok = __all_sync(0xffffffffu, role_wait(&bar_p[sb], ph, abort) &&
+                                                     role_wait(&bar_vfull[sb], ph, abort));
                     if (!ok)
                         break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     if (lane == 0) {
                         const uint32_t v_addr = attn_smem_u32(sV(sb));
-#pragma unroll
+#pragma unroll kPVUnroll
                         for (int kk = 0; kk < kAttnKeys / 16; ++kk)
                             umma2_ts(tmem + o_col, tmem + sb * kAttnKeys + kk * 8,
                                      packed_v_desc<D>(v_addr, kk), idesc, (kt > 0 || kk > 0) ? 1u : 0u);
@@ -984,46 +1049,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                     ok = false;
             }
         } else if (warp == kPackedKeyWarp) {
-            // ---- the first query tile; then per unit this CTA's halves of key
-            // tile g into stage g mod 3 once S(g - 3) released it, and, behind the
-            // unit's third tile (or its last), the next unit's query tile once the
-            // unit before this one has read its buffer
-            uint32_t sb = 0, ph = 0, qn = 0;
+            // ---- this CTA's halves of key tile g into stage g mod 3 once S(g - 3)
+            // released it
+            uint32_t sb = 0, ph = 0;
             bool first = true;
             uint32_t last_ph[kPackedStages];       // parity of the last copy (2: none)
 #pragma unroll
             for (int s = 0; s < kPackedStages; ++s)
                 last_ph[s] = 2;
             int32_t seq = -1;                      // the sequence whose map was acquired
-            auto load_query = [&](const Cursor &c) {
-                const uint32_t b = qn & 1u;
-                if (qn >= 2)
-                    ok = __all_sync(0xffffffffu, attn_wait(&bar_qfree[b], ((qn >> 1) - 1) & 1u, abort));
-                if (!ok)
-                    return;
+            for (Cursor c = with_tiles(src.first(walk)); ok && valid(c); c = next_with_tiles(c)) {
                 const PackedUnit u = unit_of(c);
-                const CUtensorMap *map;
-                if constexpr (Source::kPrefix) {
-                    map = &src.q_map;
-                } else {
-                    map = src.maps + (int64_t)u.seq * kPackedMaps + 2;
-                    acquire_map(map);
-                }
-                if (lane == 0)
-                    mbar_expect_tx(&bar_q[b], kTile);
-                __syncwarp();
-                // (tokens past the sequence's end arrive as zeros)
-                if (lane < D / 64)
-                    tma_load_3d(sQ(b) + lane * kBoxBytes, map, lane * 64, u.head0,
-                                u.tok0 + (int)rank * tokens, &bar_q[b]);
-                ++qn;
-            };
-            Cursor c = with_tiles(src.first(walk));
-            if (valid(c))
-                load_query(c);
-            while (ok && valid(c)) {
-                const PackedUnit u = unit_of(c);
-                const Cursor cn = next_with_tiles(c);
                 if constexpr (!Source::kPrefix) {
                     if (u.seq != seq)
                         acquire_map(src.maps + (int64_t)u.seq * kPackedMaps);
@@ -1032,7 +1068,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 for (int32_t kt = 0; ok && kt < u.n_tiles; ++kt) {
                     const int32_t z = src.template key_place<D>(u, kt, rank, lane);
                     if (!first)
-                        ok = __all_sync(0xffffffffu, attn_wait(&bar_s[sb], ph ^ 1u, abort));
+                        ok = __all_sync(0xffffffffu, role_wait(&bar_s[sb], ph ^ 1u, abort));
                     if (!ok)
                         break;
                     // keys 64 rank .. + 63 of the tile; both CTAs' bytes
@@ -1047,18 +1083,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                         ph ^= 1u;
                         first = false;
                     }
-                    if (kt == (u.n_tiles < 3 ? u.n_tiles : 3) - 1 && valid(cn))
-                        load_query(cn);
                 }
-                c = cn;
             }
             if (!ok) {
-                // one more bounded wait for the last query tiles and, in the
-                // leader (its barriers count both CTAs' bytes), the last copies
-                // into each stage
+                // one more bounded wait, in the leader (its barriers count both
+                // CTAs' bytes), for the last copies into each stage
                 raise_abort();
-                for (uint32_t i = qn < 2 ? 0 : qn - 2; i < qn; ++i)
-                    (void)attn_wait(&bar_q[i & 1u], (i >> 1) & 1u);
 #pragma unroll
                 for (int s = 0; s < kPackedStages; ++s)
                     if (leader && last_ph[s] < 2)
@@ -1085,7 +1115,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 for (int32_t kt = 0; ok && kt < u.n_tiles; ++kt) {
                     const int32_t z = src.template value_place<D>(u, kt, lane);
                     if (!first)
-                        ok = __all_sync(0xffffffffu, attn_wait(&bar_o[sb], ph ^ 1u, abort));
+                        ok = __all_sync(0xffffffffu, role_wait(&bar_o[sb], ph ^ 1u, abort));
                     if (!ok)
                         break;
                     // features D/2 rank .. of the tile's 128 keys
