@@ -30,6 +30,7 @@ with the calls.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -786,10 +787,25 @@ class _Call:
             raise RopeError(st, name)
 
 
-def _type16(x: torch.Tensor, what: str) -> int:
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError("%s takes bf16 or fp16 tensors, got %s" % (what, x.dtype))
-    return _DTYPE_CODE[x.dtype]
+_TYPE16 = {torch.bfloat16: ROPE_BF16, torch.float16: ROPE_F16}
+
+
+def _type16(dtype: torch.dtype, what: str) -> int:
+    code = _TYPE16.get(dtype)
+    if code is None:
+        raise TypeError("%s takes bf16 or fp16 tensors, got %s" % (what, dtype))
+    return code
+
+
+# workspace sizes are functions of a call's sizes alone
+@functools.lru_cache(maxsize=1024)
+def _packed_workspace(*sizes) -> int:
+    return load_library().rope_attention_packed_workspace(*sizes)
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_workspace(*sizes) -> int:
+    return load_library().rope_attention_decode_workspace(*sizes)
 
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -810,7 +826,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     """
     c = _Call(k, stream)
     dtype, i32 = k.dtype, torch.int32
-    code = _type16(k, "cache_append")
+    code = _type16(dtype, "cache_append")
     kp, vp, n_pages, Hk, page, D = c.cache(k_pages, v_pages, dtype)
     ka, ks, T, _, _ = c.rows(k, "k", dtype, Hk, D)
     va, vs, Tv, _, _ = c.rows(v, "v", dtype, Hk, D)
@@ -850,7 +866,7 @@ def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     """
     c = _Call(q, stream)
     dtype, i32 = q.dtype, torch.int32
-    code = _type16(q, "attention_packed")
+    code = _type16(dtype, "attention_packed")
     qa, qs, Tq, Hq, D = c.rows(q, "q", dtype)
     ka, ks, Tk, Hk, _ = c.rows(k, "k", dtype, None, D)
     va, vs, Tv, _, _ = c.rows(v, "v", dtype, Hk, D)
@@ -865,7 +881,7 @@ def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     if out is None:
         out = c.empty((Tq, Hq, D), dtype)
     lib = load_library()
-    ws = c.workspace(workspace, lib.rope_attention_packed_workspace(n, Tq, Tk, Hq, Hk, D),
+    ws = c.workspace(workspace, _packed_workspace(n, Tq, Tk, Hq, Hk, D),
                      "rope_attention_packed_workspace")
     c.run(lib.rope_attention_packed_fwd, "rope_attention_packed_fwd", qa, ka, va,
           c.dense(out, "out", dtype, (Tq, Hq, D)), ca, sa, c.dense(pos_q, "pos_q", i32, (Tq,)),
@@ -898,7 +914,7 @@ def attention_shared_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
     """
     c = _Call(q, stream)
     dtype, i32 = q.dtype, torch.int32
-    code = _type16(q, "attention_shared_prefix")
+    code = _type16(dtype, "attention_shared_prefix")
     qa, qs, B, Hq, D = c.rows(q, "q", dtype)
     kp, vp, n_pages, Hk, page, d = c.cache(k_pages, v_pages, dtype)
     if d != D:
@@ -914,8 +930,7 @@ def attention_shared_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
     if out is None:
         out = c.empty((B, Hq, D), dtype)
     lib = load_library()
-    ws = c.workspace(workspace, lib.rope_attention_decode_workspace(B, Hq, Hk, D, page, blocks,
-                                                                    prefix_len),
+    ws = c.workspace(workspace, _decode_workspace(B, Hq, Hk, D, page, blocks, prefix_len),
                      "rope_attention_decode_workspace")
     c.run(lib.rope_attention_decode_fwd, "rope_attention_decode_fwd", qa, kp, vp,
           c.dense(out, "out", dtype, (B, Hq, D)), c.dense(block_table, "block_table", i32),

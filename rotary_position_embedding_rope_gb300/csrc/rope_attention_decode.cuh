@@ -20,7 +20,7 @@
 // from the suffixes' lengths how many clusters the prefix gets (plan_clusters);
 // those run 1, the SMs of the others run 2 beside them.  (As two launches the
 // parts ran one after the other, or the second kernel's last CTAs started behind
-// the first: 64 sequences, 8k prefix, 70 us against XX.)  When the batch has no
+// the first: 64 sequences, 8k prefix, 70 us against 55.)  When the batch has no
 // more than 16 rows per key head, the prefix is one more sequence of 2, with all
 // the rows of the batch, in a kernel of 2 alone.
 //
@@ -90,18 +90,29 @@ __host__ __device__ inline float plan_ns(const PlanSizes &p, int32_t c, float ch
     return fmaxf(prefix, bytes / fminf(side, 6500.0f - tiles / slow));
 }
 
-// Clusters for the prefix, by every thread of a CTA of at least p.clusters
-// threads (key: one shared word).
-__device__ __forceinline__ int32_t plan_clusters(const PlanSizes &p, int64_t chunks, unsigned long long *key)
+// Clusters for the prefix, by every thread of a CTA (best: 2 words a warp).
+__device__ __forceinline__ int32_t plan_clusters(const PlanSizes &p, int64_t chunks, uint32_t (*best)[2])
 {
-    if (threadIdx.x == 0)
-        *key = ~0ull;
+    const int32_t c = threadIdx.x + 1, warp = threadIdx.x >> 5;
+    if (warp * 32 < p.clusters) {
+        // positive floats order as their bits do
+        const uint32_t t = c <= p.clusters ? __float_as_uint(plan_ns(p, c, (float)chunks)) : 0xffffffffu;
+        const uint32_t m = __reduce_min_sync(0xffffffffu, t);
+        const uint32_t at = __reduce_min_sync(0xffffffffu, t == m ? (uint32_t)c : 0xffffffffu);
+        if ((threadIdx.x & 31) == 0) {
+            best[warp][0] = m;
+            best[warp][1] = at;
+        }
+    }
     __syncthreads();
-    const int32_t c = threadIdx.x + 1;
-    if (c <= p.clusters)
-        atomicMin(key, (unsigned long long)__float_as_uint(plan_ns(p, c, (float)chunks)) << 32 | (unsigned)c);
-    __syncthreads();
-    return (int32_t)(*key & 0xffffffffu);
+    uint32_t m = best[0][0], at = best[0][1];
+    for (int w = 1; w * 32 < p.clusters; ++w) {
+        if (best[w][0] < m) {
+            m = best[w][0];
+            at = best[w][1];
+        }
+    }
+    return (int32_t)at;
 }
 
 // What the merge has to know of the deal, in the workspace.
@@ -191,9 +202,16 @@ struct DecodeArgs {
 // Chunks of a warp: an equal share, and no less than two, so that few warps'
 // results meet in the merge.
 constexpr int kDecMinChunks = 2;
+// a / b of non-negative numbers, in 32 bits when they fit (a quarter of the time)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0)
+        return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
 __device__ __forceinline__ int64_t decode_per_warp(int64_t chunks, int32_t warps)
 {
-    const int64_t per = (chunks + warps - 1) / warps;
+    const int64_t per = divide(chunks + warps - 1, warps);
     return per < kDecMinChunks ? kDecMinChunks : per;
 }
 
@@ -404,12 +422,12 @@ __device__ __forceinline__ SuffixRun suffix_run(const DecodeArgs &g, const int32
     const int64_t c = run.w * per;
     run.left = warp >= kDecWarps ? 0 : total - c < per ? total - c : per;
     if (run.left > 0) {
-        const int32_t b = find_sequence(start, n_seqs + 1, c / heads);
+        const int32_t b = find_sequence(start, n_seqs + 1, divide(c, heads));
         // (the last b whose start is at most c / heads has chunks)
         run.at.b = b;
         run.at.n = start[b + 1] - start[b];
         const int64_t in = c - (int64_t)start[b] * heads;
-        run.at.hr = (int32_t)(in / run.at.n);
+        run.at.hr = (int32_t)divide(in, run.at.n);
         run.at.ch = (int32_t)(in - (int64_t)run.at.hr * run.at.n);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -678,10 +696,10 @@ struct PrefixSource {
     template <int D>
     __device__ __forceinline__ Walk walk(int64_t cid, int64_t, uint8_t *smem) const
     {
-        __shared__ unsigned long long key;
+        __shared__ uint32_t best[kPackedThreads / 32][2];
         __shared__ int32_t warp_sum[kPackedThreads / 32];
         const int32_t chunks = scan_chunks<kPackedThreads>(g, chunk_starts<D>(smem), warp_sum);
-        const PrefixDeal d = prefix_deal(sizes, plan_clusters(sizes, chunks, &key));
+        const PrefixDeal d = prefix_deal(sizes, plan_clusters(sizes, chunks, best));
         if (blockIdx.x == 0 && threadIdx.x == 0)
             g.deal->prefix_per = d.per;
         return {(int32_t)cid, d.clusters, d.groups, d.per, chunks};
@@ -871,8 +889,8 @@ __global__ void __launch_bounds__(128) rope_decode_merge_kernel(const __grid_con
             if (c1 == c0)
                 return;
             const int64_t at = c0 * heads + hr * (c1 - c0), pair = (int64_t)seq * heads + hr;
-            first = at / deal.suffix_per + pair;
-            n = (int32_t)((at + (c1 - c0) - 1) / deal.suffix_per + pair - first + 1);
+            first = divide(at, deal.suffix_per) + pair;
+            n = (int32_t)(divide(at + (c1 - c0) - 1, deal.suffix_per) + pair - first + 1);
         };
         slots(b, kv * g.row_groups + rg, first1, n1);
         if (g.fold)

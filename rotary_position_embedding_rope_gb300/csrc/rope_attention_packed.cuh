@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kPackedPrepThreads)
 // With query rotation and epilogue on the softmax warps' path (their loop then
 // ran tiles, rotation, epilogue in turn, 224 threads a CTA) eight causal prompts
 // of 16.4k tokens in all, Hq 32, Hk 8, D 128 took 384 us in this kernel; with
-// the helpers 336 us, and with the next unit looked up early 305 us.
+// the helpers 336 us, and as it is now 307 us (1250 TFLOP/s).
 
 constexpr int kPackedThreads = 384;
 constexpr int kPackedSIssueWarp = 8, kPackedPVIssueWarp = 9, kPackedKeyWarp = 10, kPackedValueWarp = 11;
@@ -417,11 +417,12 @@ __device__ __forceinline__ void load_half_box_l2(uint8_t *dst, const CUtensorMap
 // of cycles (a failed try_wait suspends the thread for about 4 us here, so the
 // limit is some 2 s), which makes each of its twenty copies half as long.
 constexpr int kRoleTries = 1 << 19;
-__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, const volatile int *abort)
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, const volatile int *abort,
+                                          int tries = kRoleTries)
 {
     const uint32_t b = attn_smem_u32(bar);
 #pragma unroll 1
-    for (int i = 0; i < kRoleTries; ++i) {
+    for (int i = 0; i < tries; ++i) {
         uint32_t done;
         asm volatile("{\n\t.reg .pred p;\n\t"
                      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
@@ -890,8 +891,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
             __syncwarp();
             float2 stat = make_float2(-INFINITY, 0.0f);
             if (u.n_tiles > 0) {
+                // (a wait for a whole unit: its tiles count too)
                 ok = __all_sync(0xffffffffu,
-                                role_wait(&bar_stat[un % kPackedStats], (un / kPackedStats) & 1u, abort) &&
+                                role_wait(&bar_stat[un % kPackedStats], (un / kPackedStats) & 1u, abort,
+                                          kRoleTries + u.n_tiles) &&
                                     role_wait(&bar_odone[un % kOBufs], (un / kOBufs) & 1u, abort));
                 if (!ok)
                     break;

@@ -70,6 +70,33 @@ def _rotated_rounded(x, rows, cos, sin, layout):
     return y.to(x.dtype).double()
 
 
+def tie_slack(x, rows, cos, sin, layout):
+    """Per element of x [n, H, D]: one unit of its type where the rotated value, exact, lies so near the middle of
+    two neighbours (2^-21 of it; the fp32 rotation is within 2^-22) that a correct kernel may round to the other
+    one, else 0."""
+    y = torch.stack([rotate(x[i], rows[i], cos, sin, layout) for i in range(x.shape[0])])
+    r = y.to(x.dtype).double()
+    unit = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=1e-30)))) * torch.finfo(x.dtype).eps
+    return torch.where((unit / 2 - (y - r).abs()).abs() <= y.abs() * 2.0 ** -21, unit, 0.0)
+
+
+def score_slack(q, k, cu, cos, sin, layout="split_half", scale=None):
+    """[T, Hq]: how far a score of a row of packed causal self-attention can lie from the reference's because of such
+    elements: max_j scale sum_d (|dq_d| |k_jd| + |q_d| |dk_jd|), elements a unit larger than they are."""
+    T, Hq, D = q.shape
+    scale = D ** -0.5 if scale is None else scale
+    out = torch.zeros(T, Hq, dtype=torch.float64)
+    for b in range(len(cu) - 1):
+        a, e = int(cu[b]), int(cu[b + 1])
+        dq, dk = (tie_slack(x[a:e], range(e - a), cos, sin, layout) for x in (q, k))
+        qa, ka = (_rotated_rounded(x[a:e], range(e - a), cos, sin, layout).abs() + d for x, d in ((q, dq), (k, dk)))
+        for h in range(Hq):
+            g = h // (Hq // k.shape[1])
+            s = (dq[:, h] @ ka[:, g].T + qa[:, h] @ dk[:, g].T) * scale
+            out[a:e, h] = torch.tril(s).amax(1)
+    return out
+
+
 def packed(q, k, v, cu_q, cu_k, cos, sin, pos_q=None, pos_k=None, layout="split_half",
            causal=False, scale=None):
     """(o, w, a) [Tq, Hq, D] in fp64; rows of no sequence are NaN."""

@@ -247,6 +247,48 @@ def test_captured_replayed_and_on_another_stream():
     assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("prefix", [0, 33])
+def test_the_largest_batch(prefix):
+    """4096 sequences, most with few keys, some with none."""
+    require_gpu()
+    R = lib()
+    c = dict(lens=[(i * 5) % 7 for i in range(4096)], prefix=prefix, Hq=2, Hk=1, D=64, rd=32, page=16, dtype="f16",
+             layout="split_half")
+    q, kp, vp, table, lens, ptable = make(c)
+    cos, sin = S.tables(1e4, 32, 64)
+    ref = S.shared_prefix(q, kp, vp, table, lens, ptable, prefix, cos, sin)
+    check(run(R, c, q, kp, vp, table, lens, ptable, cos, sin), ref, c, "decode largest batch")
+
+
+def test_prefix_alone_and_nothing_at_all():
+    """No suffix blocks; no keys of either kind; no sequences."""
+    require_gpu()
+    R = lib()
+    for B in (2, 20):                                      # the prefix with the suffix kernel, and its own
+        c = dict(lens=[0] * B, prefix=300, Hq=8, Hk=2, D=128, rd=128, page=64, dtype="bf16", layout="split_half")
+        q, kp, vp, table, lens, ptable = make(c)
+        cos, sin = S.tables(1e4, 128, 301)
+        ref = S.shared_prefix(q, kp, vp, table, lens, ptable, 300, cos, sin)
+        check(run(R, c, q, kp, vp, table[:, :0].contiguous(), lens, ptable, cos, sin), ref, c, "decode prefix alone")
+        c["prefix"] = 0
+        for blocks in (0, 1):
+            got = run(R, c, q, kp, vp, table[:, :blocks].contiguous(), lens, ptable, cos, sin)
+            assert torch.count_nonzero(got) == 0
+        assert run(R, c, q[:0], kp, vp, table[:0], lens[:0], ptable, cos, sin).shape == (0, 8, 128)
+
+
+def test_nan_keys_reach_their_sequence_only():
+    require_gpu()
+    R = lib()
+    c = dict(lens=[33, 50, 64], prefix=40, Hq=4, Hk=2, D=64, rd=64, page=16, dtype="bf16", layout="split_half")
+    q, kp, vp, table, lens, ptable = make(c, poison=False)
+    cos, sin = S.tables(1e4, 64, 128)
+    clean = run(R, c, q, kp, vp, table, lens, ptable, cos, sin)
+    kp[int(table[1, 3]), :, 1] = float("nan")              # the last key of sequence 1
+    got = run(R, c, q, kp, vp, table, lens, ptable, cos, sin)
+    assert torch.equal(got[0], clean[0]) and torch.equal(got[2], clean[2]) and got[1].isnan().all()
+
+
 def test_refusals():
     require_gpu()
     R = lib()

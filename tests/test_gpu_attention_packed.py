@@ -193,6 +193,55 @@ def test_captured_replayed_and_on_another_stream():
     assert torch.equal(again, out)
 
 
+def test_thousands_of_sequences():
+    """More sequences than the planner's CTA has threads, map CTAs have warps or offsets are cached for."""
+    require_gpu()
+    R = lib()
+    n = 2500
+    c = dict(q=[(i * 7) % 4 for i in range(n)], Hq=2, Hk=1, D=64, rd=32, dtype="bf16", layout="split_half", causal=True)
+    q, k, v, cu, _ = make(c)
+    cos, sin = S.tables(1e4, 32, 4)
+    ref = S.packed(q, k, v, cu, cu, cos, sin, causal=True)
+    check(run(R, c, q, k, v, cu, cu, cos, sin), ref, c, "packed thousands")
+
+
+def test_no_keys_at_all_and_nothing_at_all():
+    require_gpu()
+    R = lib()
+    cos, sin = (x.cuda() for x in S.tables(1e4, 64, 64))
+    q = torch.randn(50, 4, 64, device="cuda").bfloat16()
+    none = torch.empty(0, 2, 64, device="cuda", dtype=torch.bfloat16)
+    cu, zero = torch.tensor([0, 20, 50], dtype=torch.int32).cuda(), torch.zeros(3, dtype=torch.int32).cuda()
+    out = R.attention_packed(q, none, none, cu, cos, sin, cu_seqlens_k=zero, causal=False)
+    assert R.rope_check_errors() == R.ROPE_OK and torch.count_nonzero(out) == 0
+    assert R.attention_packed(q[:0], none, none, zero, cos, sin).shape == (0, 4, 64)
+    keep = torch.full_like(q, 3.0)
+    R.attention_packed(q, none, none, cu[:1], cos, sin, cu_seqlens_k=zero[:1], out=keep)
+    assert R.rope_check_errors() == R.ROPE_OK and (keep == 3).all()
+
+
+def test_large_scores_and_infinities():
+    """Scores hundreds apart; an infinite key gives what the formula gives (NaN where it is seen)."""
+    require_gpu()
+    R = lib()
+    c = dict(q=[140, 260], Hq=4, Hk=2, D=128, rd=128, dtype="bf16", layout="split_half", causal=True)
+    q, k, v, cu, _ = make(c)
+    q = (q.float() * torch.linspace(0.1, 12, 400)[:, None, None]).bfloat16()
+    cos, sin = S.tables(1e4, 128, 300)
+    o, w, a = S.packed(q, k, v, cu, cu, cos, sin, causal=True)
+    # A rotated element in the middle of two neighbours may be rounded to either, which moves scores of this size by
+    # up to d = score_slack.  Every p_j = e^(s_j) / sum e^(s) then changes by a factor within e^(+-2d), and o by at
+    # most (e^(2d) - 1) sum p_j |v_j| = (e^(2d) - 1) W; the rule's (u + 2^-14) W is widened by that.
+    d = S.score_slack(q, k, cu, cos, sin)
+    w = w * (1 + torch.expm1(2 * d) / (AC.U["bf16"] + AC.ARITH))[..., None]
+    check(run(R, c, q, k, v, cu, cu, cos, sin), (o, w, a), c, "packed large scores")
+    k2 = k.clone()
+    k2[139] = float("nan")                                 # the last key of the first sequence
+    got = run(R, c, q, k2, v, cu, cu, cos, sin)
+    clean = run(R, c, q, k, v, cu, cu, cos, sin)
+    assert torch.equal(got[:139], clean[:139]) and torch.equal(got[140:], clean[140:]) and got[139].isnan().all()
+
+
 def test_refusals():
     require_gpu()
     R = lib()
