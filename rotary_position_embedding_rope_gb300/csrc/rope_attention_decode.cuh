@@ -35,8 +35,12 @@ namespace rope {
 // ---------------------------------------------------------------------------
 // How a call is dealt out to the SMs.
 
-constexpr int kDecKeys = 16;                       // keys of a suffix chunk
 constexpr int kDecWarps = 8;                       // suffix warps of an SM
+// Keys of a suffix chunk: 16 of 128 features or 32 of 64, 8 KB of keys and values
+// (16 keys of 64 features left a warp's chain of dependent steps too little work:
+// 48 sequences, 16 heads of 64: 39 us, now 34.5).
+template <int D>
+static constexpr int kDecKeys = D == 128 ? 16 : 32;
 
 // The sizes decode_plan goes by.
 struct PlanSizes {
@@ -162,14 +166,14 @@ __device__ __forceinline__ int64_t query_row(const int32_t *pos_q, int32_t b, in
 // mma.sync (m16n8k16) instead of tcgen05: a decode step has at most 16 rows per
 // key here, the work is one pass over the keys, and a warp that owns its keys,
 // its stages and its softmax needs no barrier but the copies' own.  K and V
-// arrive by TMA (boxes of 64 features x 16 keys, 128-byte swizzle, so ldmatrix
-// reads without conflicts), three stages (D = 128; six for D = 64) a warp, eight
-// warps an SM: 192 KB in flight or in use.
+// arrive by TMA (boxes of 64 features x the chunk's keys, or a page's where that
+// is less, 128-byte swizzle, so ldmatrix reads without conflicts), three stages a
+// warp, eight warps an SM: 192 KB in flight or in use.
 constexpr int kDecThreads = 32 * kDecWarps;
 template <int D>
-static constexpr int kDecStages = D == 128 ? 3 : 6;
+static constexpr int kDecStages = 3;
 template <int D>
-static constexpr int kDecStageBytes = 2 * kDecKeys * D * 2;
+static constexpr int kDecStageBytes = 2 * kDecKeys<D> * D * 2;
 template <int D>
 static constexpr int kDecQStride = D * 2 + 16;                 // padded rows of the query tile
 template <int D>
@@ -184,6 +188,7 @@ struct DecodeArgs {
     const int32_t *table, *prefix_table, *lens, *pos_q;
     int64_t max_blocks, n_pages;
     int32_t B, Hq, Hk, page_shift, n_prefix;
+    int32_t chunk_shift;                       // log2 of a chunk's keys
     int32_t fold;                              // 1: the prefix is sequence B of the suffix kernel
     int32_t row_groups, rows;                  // of a key head's query heads; rows of a group
     int32_t slot_rows;                         // rows kept per slot (with fold also B * group)
@@ -215,10 +220,15 @@ __device__ __forceinline__ int64_t decode_per_warp(int64_t chunks, int32_t warps
     return per < kDecMinChunks ? kDecMinChunks : per;
 }
 
-// Keys of sequence b, the folded prefix (b = B) included.
+// Keys, and chunks, of sequence b, the folded prefix (b = B) included.
 __device__ __forceinline__ int32_t decode_keys(const DecodeArgs &g, int32_t b, int64_t most)
 {
     return b < g.B ? suffix_keys(g.lens, b, most, g.a.flag) : g.n_prefix;
+}
+__device__ __forceinline__ int32_t decode_chunks(const DecodeArgs &g, int32_t b, int64_t most)
+{
+    const int32_t n = decode_keys(g, b, most);
+    return (n >> g.chunk_shift) + ((n & ((1 << g.chunk_shift) - 1)) != 0);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
@@ -268,7 +278,7 @@ struct ChunkAt {
                 n = 0;
                 return;
             }
-            n = (decode_keys(g, b, most) + kDecKeys - 1) / kDecKeys;
+            n = decode_chunks(g, b, most);
         } while (n == 0);
     }
 };
@@ -351,7 +361,7 @@ __device__ __forceinline__ int32_t scan_chunks(const DecodeArgs &g, int32_t *sta
     int32_t carry = 0;
     for (int32_t b0 = 0; b0 < n_seqs; b0 += NT) {
         const int32_t b = b0 + tid;
-        const int32_t n = b < n_seqs ? (decode_keys(g, b, most) + kDecKeys - 1) / kDecKeys : 0;
+        const int32_t n = b < n_seqs ? decode_chunks(g, b, most) : 0;
         int32_t inc = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -441,7 +451,8 @@ template <typename T, int LAYOUT, int D>
 __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *smem, const SuffixRun &run,
                                                 SuffixShared<D> &sh)
 {
-    constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>, kBox = kDecKeys * 128;
+    constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>, kKeys = kDecKeys<D>;
+    constexpr int kBox = kKeys * 128, kGroups = kKeys / 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t most = g.max_blocks << g.page_shift;
     const int32_t heads = g.Hk * g.row_groups, w = run.w;
@@ -461,31 +472,35 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
     int64_t base_block = 0;
     // (several row groups of a key head read the same keys)
     const uint64_t policy = g.row_groups > 1 ? l2_keep() : l2_once();
+    const int32_t box_shift = g.page_shift < g.chunk_shift ? g.page_shift : g.chunk_shift;
+    const int32_t boxes = kKeys >> box_shift;                  // of a chunk's keys: its pages, or one
     auto load = [&](int st) {
-        const int64_t block = (int64_t)ahead.ch * kDecKeys >> g.page_shift;
-        if (of != ahead.b || block < base_block || block >= base_block + 32) {
+        const int64_t key = (int64_t)ahead.ch * kKeys, block = key >> g.page_shift;
+        if (of != ahead.b || block < base_block || block + boxes > base_block + 32) {
             of = ahead.b;
             base_block = block;
-            const int64_t blocks = ((int64_t)ahead.n * kDecKeys - 1 >> g.page_shift) + 1;
+            const int64_t blocks = (((int64_t)ahead.n * kKeys - 1) >> g.page_shift) + 1;
+            const int64_t listed = of < g.B ? g.max_blocks : ((int64_t)g.n_prefix - 1 >> g.page_shift) + 1;
             const int32_t *list = of < g.B ? g.table + of * g.max_blocks : g.prefix_table;
-            pages = block + lane < blocks ? __ldg(list + block + lane) : 0;
+            // (a chunk's last page may lie behind the list: its keys are not visible)
+            pages = block + lane < (blocks < listed ? blocks : listed) ? __ldg(list + block + lane) : -1;
         }
-        const int32_t page = __shfl_sync(0xffffffffu, pages, (int)(block - base_block));
-        int32_t z = page * g.Hk + ahead.hr / g.row_groups;
-        if (page < 0 || page >= g.n_pages) {
-            if (lane == 0)
-                atomicOr(g.a.flag, kFlagIndex);
-            z = (int32_t)(g.n_pages * g.Hk);                   // arrives as zeros
-        }
-        const int32_t y = ahead.ch * kDecKeys & ((1 << g.page_shift) - 1);
         if (lane == 0)
             mbar_expect_tx(&bar[st], kStage);
-        __syncwarp();
-        if (lane < 2 * (D / 64)) {
-            const int x = lane % (D / 64);
-            const bool v = lane >= D / 64;
-            tma_load_3d_l2(stages + st * kStage + (v ? kStage / 2 : 0) + x * kBox, v ? &g.v_map : &g.k_map,
-                           x * 64, y, z, &bar[st], policy);
+        // a lane's box: keys or values, 64 features, a page's keys
+        const int x = lane % (D / 64), v = lane / (D / 64) & 1, i = lane / (2 * (D / 64));
+        const int32_t page = __shfl_sync(0xffffffffu, pages, (int)(block - base_block) + (i < boxes ? i : 0));
+        if (i < boxes) {
+            int32_t z = page * g.Hk + ahead.hr / g.row_groups;
+            if (page < 0 || page >= g.n_pages) {
+                // (a page without visible keys may have any number)
+                if (key + ((int64_t)i << box_shift) < decode_keys(g, ahead.b, most))
+                    atomicOr(g.a.flag, kFlagIndex);
+                z = (int32_t)(g.n_pages * g.Hk);               // arrives as zeros
+            }
+            const int32_t y = (int32_t)(key + ((int64_t)i << box_shift)) & ((1 << g.page_shift) - 1);
+            tma_load_3d_l2(stages + st * kStage + v * (kStage / 2) + x * kBox + (i << box_shift) * 128,
+                           v ? &g.v_map : &g.k_map, x * 64, y, z, &bar[st], policy);
         }
         --to_load;
         ahead.next(g, most);
@@ -522,39 +537,52 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
         if (!ok)
             break;
         const uint32_t kb = base + st * kStage, vb = kb + kStage / 2;
-        // S = q K^T: 16 rows x 16 keys
-        float s0[4] = {0, 0, 0, 0}, s1[4] = {0, 0, 0, 0};
+        // S = q K^T: 16 rows x the chunk's keys.  Lane: rows lane / 4 (sc) and + 8
+        // (sd), keys 2 (lane mod 4) + {0, 1} of each 8-key tile.
+        float sc[4 * kGroups], sd[4 * kGroups];
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            uint32_t b[4];
-            const int chunk = (k & 3) * 2 + k_half;
-            ldsm4(kb + (k >> 2) * kBox + k_row * 128 + ((chunk ^ (k_row & 7)) << 4), b);
-            mma16816<T>(s0, qf[k], b[0], b[1]);
-            mma16816<T>(s1, qf[k], b[2], b[3]);
+        for (int k16 = 0; k16 < kGroups; ++k16) {
+            float s0[4] = {0, 0, 0, 0}, s1[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t b[4];
+                const int chunk = (k & 3) * 2 + k_half;
+                ldsm4(kb + (k >> 2) * kBox + (k16 * 16 + k_row) * 128 + ((chunk ^ (k_row & 7)) << 4), b);
+                mma16816<T>(s0, qf[k], b[0], b[1]);
+                mma16816<T>(s1, qf[k], b[2], b[3]);
+            }
+            float *c = sc + 4 * k16, *d = sd + 4 * k16;
+            c[0] = s0[0]; c[1] = s0[1]; c[2] = s1[0]; c[3] = s1[1];
+            d[0] = s0[2]; d[1] = s0[3]; d[2] = s1[2]; d[3] = s1[3];
         }
-        // keys of this lane: 2 (lane mod 4) + {0, 1} of either 8-key tile
-        const int32_t nk = keys - at.ch * kDecKeys;            // visible keys of the chunk
+        const int32_t nk = keys - at.ch * kKeys;               // visible keys of the chunk
         const int c0 = 2 * (lane & 3);
-        uint32_t vis0 = 0xffffffffu, vis1 = 0xffffffffu;       // value rows: halves of a register
-        float sc[4] = {s0[0], s0[1], s1[0], s1[1]}, sd[4] = {s0[2], s0[3], s1[2], s1[3]};
+        uint32_t vis[2 * kGroups];                             // value rows: halves of a register
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2 * kGroups; ++i)
+            vis[i] = 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < 4 * kGroups; ++i) {
             sc[i] *= g.a.scale_log2;
             sd[i] *= g.a.scale_log2;
         }
-        if (nk < kDecKeys) {
+        if (nk < kKeys) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 4 * kGroups; ++i) {
                 const int key = c0 + (i & 1) + (i >> 1) * 8;
                 if (key >= nk) {
                     sc[i] = sd[i] = -INFINITY;
                     // what lies behind the last key (anything) must not meet a zero
-                    (i >> 1 ? vis1 : vis0) &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+                    vis[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
                 }
             }
         }
-        float x0 = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
-        float x1 = fmaxf(fmaxf(sd[0], sd[1]), fmaxf(sd[2], sd[3]));
+        float x0 = sc[0], x1 = sd[0];
+#pragma unroll
+        for (int i = 1; i < 4 * kGroups; ++i) {
+            x0 = fmaxf(x0, sc[i]);
+            x1 = fmaxf(x1, sd[i]);
+        }
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
@@ -579,22 +607,27 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
         }
         const float n0 = m0 == -INFINITY ? 0.0f : m0, n1 = m1 == -INFINITY ? 0.0f : m1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4 * kGroups; ++i) {
             sc[i] = fast_exp2(sc[i] - n0);
             sd[i] = fast_exp2(sd[i] - n1);
         }
-        l0 += (sc[0] + sc[1]) + (sc[2] + sc[3]);
-        l1 += (sd[0] + sd[1]) + (sd[2] + sd[3]);
-        // P rounded to the element type for the P V product (the sums keep fp32)
-        const uint32_t p[4] = {Elt<T>::f2_to_word(sc[0], sc[1]), Elt<T>::f2_to_word(sd[0], sd[1]),
-                               Elt<T>::f2_to_word(sc[2], sc[3]), Elt<T>::f2_to_word(sd[2], sd[3])};
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-            uint32_t b[4];
-            const int chunk = (n & 3) * 2 + v_half;
-            ldsm4_t(vb + (n >> 2) * kBox + v_row * 128 + ((chunk ^ (v_row & 7)) << 4), b);
-            mma16816<T>(o[2 * n], p, b[0] & vis0, b[1] & vis1);
-            mma16816<T>(o[2 * n + 1], p, b[2] & vis0, b[3] & vis1);
+        for (int k16 = 0; k16 < kGroups; ++k16) {
+            const float *c = sc + 4 * k16, *d = sd + 4 * k16;
+            l0 += (c[0] + c[1]) + (c[2] + c[3]);
+            l1 += (d[0] + d[1]) + (d[2] + d[3]);
+            // P rounded to the element type for the P V product (the sums keep fp32)
+            const uint32_t p[4] = {Elt<T>::f2_to_word(c[0], c[1]), Elt<T>::f2_to_word(d[0], d[1]),
+                                   Elt<T>::f2_to_word(c[2], c[3]), Elt<T>::f2_to_word(d[2], d[3])};
+            const uint32_t vis0 = vis[2 * k16], vis1 = vis[2 * k16 + 1];
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+                uint32_t b[4];
+                const int chunk = (n & 3) * 2 + v_half;
+                ldsm4_t(vb + (n >> 2) * kBox + (k16 * 16 + v_row) * 128 + ((chunk ^ (v_row & 7)) << 4), b);
+                mma16816<T>(o[2 * n], p, b[0] & vis0, b[1] & vis1);
+                mma16816<T>(o[2 * n + 1], p, b[2] & vis0, b[3] & vis1);
+            }
         }
         __syncwarp();                                          // the stage is read
         if (to_load > 0) {
@@ -1010,9 +1043,11 @@ static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, c
     g.prefix_stats = reinterpret_cast<float2 *>(ws + lay.prefix_stats);
     g.prefix_tiles = prefix_kernel ? tiles : 0;
     g.suffix = lay.suffix_ctas > 0;
+    g.chunk_shift = __builtin_ctz((unsigned)kDecKeys<D>);
+    const uint32_t chunk_box = (uint32_t)(page < kDecKeys<D> ? page : kDecKeys<D>);
     if (g.suffix &&
-        (!encode_3d(enc, &g.k_map, c.k_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, kDecKeys, 1}, sw) ||
-         !encode_3d(enc, &g.v_map, c.v_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, kDecKeys, 1}, sw)))
+        (!encode_3d(enc, &g.k_map, c.k_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, chunk_box, 1}, sw) ||
+         !encode_3d(enc, &g.v_map, c.v_pages, dt, {D, page, z}, {D * 2, page * D * 2}, {64, chunk_box, 1}, sw)))
         return cudaErrorInvalidValue;
 
     if (prefix_kernel) {
