@@ -48,7 +48,7 @@ struct PlanSizes {
     int32_t clusters, sms;                         // most prefix clusters; SMs
     int32_t tile_ns;                               // a cluster's time per key tile
     int32_t heads, chunk_bytes;                    // pairs of a sequence; keys and values of a chunk
-    float sm_rate, tile_bytes;                     // copies of an SM, bytes/ns; keys and values of a tile
+    float sm_rate;                                 // copies of an SM, bytes/ns
 };
 
 // The prefix on c clusters: `groups` of them (one cluster per row tile in each)
@@ -68,30 +68,29 @@ __host__ __device__ inline PrefixDeal prefix_deal(const PlanSizes &p, int32_t c)
 
 // Estimated time, in ns, with c clusters on the prefix and the suffixes' chunks
 // (of one pair per sequence) on the SMs left over -- or, with every cluster on
-// the prefix, behind it.  Measured here: tile_ns a cluster tile, half as long
-// again once all copies together reach 6500 bytes/ns; 4 us from one unit to the
-// next; sm_rate bytes/ns for the copies of one SM.  An estimate that is off
-// costs balance, never a result.  Forced to c clusters, whole calls took (us):
-//   64 sequences, 8k prefix:    c = 12: 61   16: 54   20: 56   32: 65   76: 66
-//   256 sequences, 4k prefix:   c = 4: 357   8: 348  12: 330   16: 348  76: 378
-//   32 sequences, 128k prefix:  c = 60: 131  68: 120  72: 117  76: 122
-// where this picks 19, 8 and 72.
+// the prefix, behind it.  Measured here: tile_ns a cluster tile, 4 us from one
+// unit to the next, sm_rate bytes/ns for the copies of one SM and 6600 for all.
+// Where one side is over long before the other, a little less of it is better
+// (the last term).  An estimate that is off costs balance, never a result.
+// Forced to c clusters, whole calls took (us):
+//   64 sequences, 8k prefix:    c = 8: 73   12: 60   16: 54.5  20: 57   76: 66
+//   256 sequences, 4k prefix:   c = 4: 337  8: 332   12: 335   20: 374  76: 378
+//   32 sequences, 128k prefix:  c = 60: 132 68: 121  71: 117   72: 119  76: 124
+//   48 sequences, 1k prefix, heads of 64:  c = 4: 47  8: 33  12: 34  20: 35
+// where this picks 16, 12, 72 and 14.
 __host__ __device__ inline float plan_ns(const PlanSizes &p, int32_t c, float chunks)
 {
     const PrefixDeal d = prefix_deal(p, c);
     const int32_t rounds = (p.row_tiles + c - 1) / c;
     const float bytes = chunks * (float)p.heads * (float)p.chunk_bytes;
-    const bool beside = 2 * c < p.sms;
-    const float side = p.sm_rate * (float)(p.sms - 2 * c);
-    const float tiles = (float)c * p.tile_bytes / ((float)p.tile_ns * (float)p.row_tiles);
-    const float slow = beside && bytes > 0.0f && side + tiles > 6500.0f ? 1.5f : 1.0f;
-    const float prefix = (float)rounds * ((float)d.per * (float)p.tile_ns * slow +
+    const float prefix = (float)rounds * ((float)d.per * (float)p.tile_ns +
                                           4000.0f * (float)(1 + d.per / p.tiles));
     if (bytes == 0.0f)
         return prefix;
-    if (!beside)
-        return prefix + 10000.0f + bytes / fminf(6500.0f, p.sm_rate * (float)p.sms);
-    return fmaxf(prefix, bytes / fminf(side, 6500.0f - tiles / slow));
+    if (2 * c >= p.sms)
+        return prefix + 10000.0f + bytes / fminf(6600.0f, p.sm_rate * (float)p.sms);
+    const float suffix = bytes / fminf(6600.0f, p.sm_rate * (float)(p.sms - 2 * c));
+    return fmaxf(prefix, suffix) + 0.05f * fminf(prefix, suffix);
 }
 
 // Clusters for the prefix, by every thread of a CTA (best: 2 words a warp).
@@ -167,11 +166,13 @@ __device__ __forceinline__ int64_t query_row(const int32_t *pos_q, int32_t b, in
 // key here, the work is one pass over the keys, and a warp that owns its keys,
 // its stages and its softmax needs no barrier but the copies' own.  K and V
 // arrive by TMA (boxes of 64 features x the chunk's keys, or a page's where that
-// is less, 128-byte swizzle, so ldmatrix reads without conflicts), three stages a
-// warp, eight warps an SM: 192 KB in flight or in use.
+// is less, 128-byte swizzle, so ldmatrix reads without conflicts), two stages a
+// warp, eight warps an SM: 128 KB in flight or in use.  Three stages are slower:
+// 256 sequences of 2080 keys on average (2.2 GB) 352 us, with two 326 (6.6 TB/s);
+// so are six or seven warps of three stages (342, 344).
 constexpr int kDecThreads = 32 * kDecWarps;
 template <int D>
-static constexpr int kDecStages = 3;
+static constexpr int kDecStages = 2;
 template <int D>
 static constexpr int kDecStageBytes = 2 * kDecKeys<D> * D * 2;
 template <int D>
@@ -1072,7 +1073,7 @@ static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, c
         s.sizes.sms = 2 * clusters;
         s.sizes.tile_ns = D == 128 ? 850 : 700;
         s.sizes.heads = c.Hk * lay.row_groups; s.sizes.chunk_bytes = kDecStageBytes<D>;
-        s.sizes.sm_rate = D == 128 ? 50.0f : 30.0f; s.sizes.tile_bytes = 4.0f * D * kAttnKeys;
+        s.sizes.sm_rate = D == 128 ? 53.0f : 48.0f;
         s.pages = c.prefix_table;
         s.out = reinterpret_cast<float *>(ws + lay.prefix_out);
         s.stats = reinterpret_cast<float2 *>(ws + lay.prefix_stats);
