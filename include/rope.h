@@ -352,7 +352,8 @@ rope_status rope_attention_fwd_noalloc(const void *q, const void *k, const void 
  *   element type; page_size is 16, 32, 64 or 128.  A block list (device
  *   int32) names the pages of a sequence in order: its key i lies in row
  *   i mod page_size of page list[i / page_size].  Entries past a sequence's
- *   last key are not read.  Cached keys are rotated keys.
+ *   last key, and rows of a page past it, may hold anything.  Cached keys are
+ *   rotated keys.
  * Element types ROPE_BF16 and ROPE_F16; D is 64 or 128; rotary_dim is a
  *   multiple of 16, 16 <= rotary_dim <= D; pointers to 16-bit and fp32 data
  *   are 16-byte aligned.  What only the device can see -- offsets, lengths,
@@ -424,7 +425,9 @@ rope_status rope_cache_append(const void *k, const void *v, void *k_pages, void 
  *    sequence longer than the table when its positions are NULL
  *    (ROPE_ERR_POS_OUT_OF_RANGE), is found on the device: the flag is raised
  *    and nothing of o is written.
- * Arithmetic: as rope_attention_fwd.
+ * Arithmetic: as rope_attention_fwd.  Nothing of another sequence reaches a
+ *    query, whatever it holds; a NaN or infinity in v may reach queries of its
+ *    own sequence that do not see its key (their probability 0 times it).
  * Errors: ROPE_ERR_UNSUPPORTED for other dtypes, D, rotary_dim, layouts,
  *    strides not a multiple of 8 or unaligned pointers; ROPE_ERR_INVALID_ARG
  *    for bad sizes, token strides below a token's row, null pointers, a

@@ -763,8 +763,9 @@ class _Call:
     def empty(self, shape, dtype):
         """A new tensor, alive until the call's stream is done with it."""
         x = torch.empty(shape, dtype=dtype, device=self.index)
-        if self.other:
-            x.record_stream(torch.cuda.ExternalStream(self.stream, device=self.index))
+        if self.other and self.stream != torch._C._cuda_getCurrentRawStream(self.index):
+            x.record_stream(torch.cuda.ExternalStream(self.stream, device=self.index) if self.stream
+                            else torch.cuda.default_stream(self.index))
         return x
 
     def workspace(self, given, need, name):

@@ -1067,7 +1067,8 @@ static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, c
             return cudaErrorInvalidValue;
         // clusters for the prefix and for the suffixes, as far as the SMs go
         int32_t clusters = lay.clusters + (lay.suffix_ctas + 1) / 2;
-        clusters = clusters < sms / 2 ? clusters : sms / 2;
+        const int32_t pairs = (sms < kDecodeSms ? sms : kDecodeSms) / 2;
+        clusters = clusters < pairs ? clusters : pairs;
         s.sizes.row_tiles = lay.row_tiles; s.sizes.head_units = c.Hq / gp; s.sizes.tiles = tiles;
         s.sizes.clusters = lay.clusters < clusters ? lay.clusters : clusters;
         s.sizes.sms = 2 * clusters;

@@ -913,7 +913,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 // sequence's end are not written, and a box that starts past
                 // it is not issued).  O is free for the next unit's products
                 // as soon as the last of it is in registers.
-                const float inv = stat.y > 0.0f ? 1.0f / stat.y : 0.0f;
+                const bool none = stat.y == 0.0f;  // a row that saw no key (0 * v may be NaN)
+                const float inv = none ? 0.0f : 1.0f / stat.y;
 #pragma unroll
                 for (int c0 = 0; c0 < D; c0 += 64) {
                     float ov[64];
@@ -936,7 +937,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             f[e] = ov[ch * 8 + e] * inv;
-                        *reinterpret_cast<uint4 *>(sO + sw128(row, c0 / 8 + ch)) = Elt<T>::pack(f);
+                        const uint4 w = Elt<T>::pack(f);
+                        *reinterpret_cast<uint4 *>(sO + sw128(row, c0 / 8 + ch)) =
+                            none ? make_uint4(0, 0, 0, 0) : w;
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

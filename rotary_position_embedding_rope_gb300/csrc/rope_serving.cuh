@@ -74,6 +74,9 @@ cudaError_t launch_packed_f16(const PackedArgs &c, const PackedLayout &lay, int3
 // Attention of one token per sequence over a shared prefix and a suffix each
 // (rope_attention_decode.cuh).
 constexpr int32_t kMaxDecodeBatch = 4096;      // sequences of a call (their scan fits an SM)
+// The SMs a decode call is dealt out to, at most (its workspace has slots for
+// their warps); fewer give the same results, less evenly spread.
+constexpr int32_t kDecodeSms = 152;
 struct DecodeCall {
     const void *q;                   // [B][Hq][D], row stride q_stride
     int64_t q_stride;

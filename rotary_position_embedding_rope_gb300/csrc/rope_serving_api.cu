@@ -108,9 +108,7 @@ bool packed_layout(int64_t n_seqs, int64_t total_q, int64_t total_k, int32_t Hq,
     return true;
 }
 
-// The SMs the split rules are made for (any other number gives the same
-// results, less evenly spread).
-constexpr int32_t kSms = 152;
+constexpr int32_t kSms = kDecodeSms;
 
 bool decode_layout(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_shift, int64_t max_blocks,
                    int64_t n_prefix, DecodeLayout *out)

@@ -191,6 +191,12 @@ def test_captured_replayed_and_on_another_stream():
     again = R.attention_packed(*ins, causal=True, stream=side)
     side.synchronize()
     assert torch.equal(again, out)
+    # raw handles, the default stream's among them, from another current stream
+    with torch.cuda.stream(side):
+        for handle in (0, s.cuda_stream):
+            again = R.attention_packed(*ins, causal=True, stream=handle)
+            torch.cuda.synchronize()
+            assert torch.equal(again, out)
 
 
 def test_thousands_of_sequences():
@@ -216,6 +222,12 @@ def test_no_keys_at_all_and_nothing_at_all():
     assert R.rope_check_errors() == R.ROPE_OK and torch.count_nonzero(out) == 0
     assert R.attention_packed(q[:0], none, none, zero, cos, sin).shape == (0, 4, 64)
     keep = torch.full_like(q, 3.0)
+    # rows that see no key stay zeros beside infinite values that other rows see
+    inf = torch.full((30, 2, 64), float("inf"), device="cuda", dtype=torch.bfloat16)
+    one = torch.tensor([0, 50], dtype=torch.int32).cuda()
+    out = R.attention_packed(q, torch.zeros_like(inf), inf, one, cos, sin, causal=True,
+                             cu_seqlens_k=torch.tensor([0, 30], dtype=torch.int32).cuda())
+    assert torch.count_nonzero(out[:20]) == 0 and not out[20:].isfinite().any()
     R.attention_packed(q, none, none, cu[:1], cos, sin, cu_seqlens_k=zero[:1], out=keep)
     assert R.rope_check_errors() == R.ROPE_OK and (keep == 3).all()
 
