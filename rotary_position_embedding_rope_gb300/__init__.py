@@ -30,7 +30,7 @@ with the calls.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 
 import torch
@@ -684,129 +684,29 @@ def rope_attention_decode_workspace(B, Hq, Hk, D, page_size, max_blocks, prefix_
                                                           int(prefix_len))
 
 
-class _Call:
-    """One serving call: the device its tensors live on and the stream it runs
-    on, with that device current while the library is called.  A decode step
-    makes several such calls per layer, so the checks are a few attribute reads
-    a tensor; a tensor that fails one is looked at again to say why."""
-
-    __slots__ = ("index", "stream", "other")
-
-    def __init__(self, first: torch.Tensor, stream):
-        self.index = first.get_device()
-        if self.index < 0:
-            raise ValueError("expected CUDA tensors, got one on %s" % first.device)
-        self.other = stream is not None
-        if stream is None:
-            self.stream = torch._C._cuda_getCurrentRawStream(self.index)
-        elif isinstance(stream, int):
-            self.stream = stream
-        else:
-            if stream.device.index != self.index:
-                raise ValueError("the stream belongs to %s, the tensors to cuda:%d" %
-                                 (stream.device, self.index))
-            self.stream = stream.cuda_stream
-
-    def _wrong(self, x, name, dtype, shape=None):
-        if dtype is not None and x.dtype != dtype:
-            raise ValueError("%s must be a %s tensor, got %s" % (name, dtype, x.dtype))
-        if x.get_device() != self.index:
-            raise ValueError("%s must be on cuda:%d, got %s" % (name, self.index, x.device))
-        if shape is not None and tuple(x.shape) != shape:
-            raise ValueError("%s must be %s, got %s" % (name, shape, tuple(x.shape)))
-        raise ValueError("%s must be contiguous (strides %s)" % (name, x.stride()))
-
-    def rows(self, x, name, dtype, H=None, D=None):
-        """(address, token stride, tokens, heads, D) of a [T, H, D] tensor, dense
-        but for its tokens."""
-        if x.dtype is not dtype or x.get_device() != self.index:
-            self._wrong(x, name, dtype)
-        shape = x.shape
-        if len(shape) != 3:
-            raise ValueError("%s must be [tokens, heads, D], got %s" % (name, tuple(shape)))
-        t, h, d = shape
-        if (H is not None and h != H) or (D is not None and d != D):
-            raise ValueError("%s must be [tokens, %s, %s], got %s" % (name, H, D, tuple(shape)))
-        st, sh, sd = x.stride()
-        if t > 0 and ((d > 1 and sd != 1) or (h > 1 and sh != d)):
-            raise ValueError("%s: heads and features must be dense (strides %s)" %
-                             (name, x.stride()))
-        return x.data_ptr(), (st if t > 1 else h * d), t, h, d
-
-    def dense(self, x, name, dtype, shape=None):
-        """Address of a contiguous tensor of the given type (and shape)."""
-        if x is None:
-            return None
-        if (x.dtype is not dtype or x.get_device() != self.index or not x.is_contiguous() or
-                (shape is not None and x.shape != shape)):
-            self._wrong(x, name, dtype, shape)
-        return x.data_ptr()
-
-    def tables(self, cos, sin, rotary_dim):
-        """(cos address, sin address, rotary_dim, rows)."""
-        shape = cos.shape
-        if len(shape) != 2 or shape != sin.shape:
-            raise ValueError("cos and sin must be [rows, rotary_dim / 2] tables of the same shape")
-        rows, half = shape
-        if rotary_dim is not None and rotary_dim != 2 * half:
-            raise ValueError("table width %d does not match rotary_dim %d" % (half, rotary_dim))
-        f32 = torch.float32
-        return self.dense(cos, "cos", f32), self.dense(sin, "sin", f32), 2 * half, rows
-
-    def cache(self, k_pages, v_pages, dtype):
-        """(k address, v address, pages, Hk, page size, D) of a cache's pools."""
-        shape = k_pages.shape
-        if len(shape) != 4 or shape != v_pages.shape:
-            raise ValueError("k_pages and v_pages must be [pages, Hk, page_size, D] of one shape")
-        return (self.dense(k_pages, "k_pages", dtype), self.dense(v_pages, "v_pages", dtype), *shape)
-
-    def empty(self, shape, dtype):
-        """A new tensor, alive until the call's stream is done with it."""
-        x = torch.empty(shape, dtype=dtype, device=self.index)
-        if self.other and self.stream != torch._C._cuda_getCurrentRawStream(self.index):
-            x.record_stream(torch.cuda.ExternalStream(self.stream, device=self.index) if self.stream
-                            else torch.cuda.default_stream(self.index))
-        return x
-
-    def workspace(self, given, need, name):
-        """The call's workspace: the given tensor, or a new one (None: none needed)."""
-        if need < 0:
-            raise RopeError(ROPE_ERR_INVALID_ARG, name)
-        if given is None:
-            return self.empty(need, torch.uint8) if need else None
-        if given.get_device() != self.index or not given.is_contiguous():
-            self._wrong(given, "workspace", None)
-        return given
-
-    def run(self, fn, name, *args):
-        if self.index == torch.cuda.current_device():
-            st = fn(*args, self.stream)
-        else:
-            with torch.cuda.device(self.index):
-                st = fn(*args, self.stream)
-        if st != ROPE_OK:
-            raise RopeError(st, name)
+_serving = None
 
 
-_TYPE16 = {torch.bfloat16: ROPE_BF16, torch.float16: ROPE_F16}
-
-
-def _type16(dtype: torch.dtype, what: str) -> int:
-    code = _TYPE16.get(dtype)
-    if code is None:
-        raise TypeError("%s takes bf16 or fp16 tensors, got %s" % (what, dtype))
-    return code
-
-
-# workspace sizes are functions of a call's sizes alone
-@functools.lru_cache(maxsize=1024)
-def _packed_workspace(*sizes) -> int:
-    return load_library().rope_attention_packed_workspace(*sizes)
-
-
-@functools.lru_cache(maxsize=1024)
-def _decode_workspace(*sizes) -> int:
-    return load_library().rope_attention_decode_workspace(*sizes)
+def _native():
+    """The binding module of the serving calls (csrc/serving_binding.cpp), given
+    the entry points of the library that is loaded."""
+    global _serving
+    if _serving is None:
+        lib = load_library()
+        path = _build.BINDING
+        if not os.path.exists(path):
+            raise RuntimeError(
+                "%s is not built; run `python -c \"import __graft_entry__ as g; g.build()\"` "
+                "first" % path)
+        spec = importlib.util.spec_from_file_location("_serving", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.rope_cache_append, lib.rope_attention_packed_fwd,
+            lib.rope_attention_packed_workspace, lib.rope_attention_decode_fwd,
+            lib.rope_attention_decode_workspace)))
+        _serving = module
+    return _serving
 
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -825,24 +725,11 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     pos: int32 [T] table rows (-1 = not rotated), or None for pos_offset + the
     key's index in its sequence.
     """
-    c = _Call(k, stream)
-    dtype, i32 = k.dtype, torch.int32
-    code = _type16(dtype, "cache_append")
-    kp, vp, n_pages, Hk, page, D = c.cache(k_pages, v_pages, dtype)
-    ka, ks, T, _, _ = c.rows(k, "k", dtype, Hk, D)
-    va, vs, Tv, _, _ = c.rows(v, "v", dtype, Hk, D)
-    if Tv != T:
-        raise ValueError("k and v must have the same tokens")
-    shape = block_table.shape
-    if len(shape) != 2:
-        raise ValueError("block_table must be [n_seqs, max_blocks]")
-    n, blocks = shape
-    ca, sa, rd, rows = c.tables(cos, sin, rotary_dim)
-    c.run(load_library().rope_cache_append, "rope_cache_append", ka, va, kp, vp,
-          c.dense(block_table, "block_table", i32), c.dense(cu_seqlens, "cu_seqlens", i32, (n + 1,)),
-          c.dense(cache_lens, "cache_lens", i32, (n,)), ca, sa, c.dense(pos, "pos", i32, (T,)),
-          pos_offset, n, T, ks, vs, Hk, D, rd, _LAYOUT_CODE[layout], page, n_pages, blocks, code,
-          rows)
+    st = (_serving or _native()).cache_append(
+        k, v, k_pages, v_pages, block_table, cu_seqlens, cache_lens, cos, sin, pos, pos_offset,
+        rotary_dim, _LAYOUT_CODE[layout], stream)
+    if st != ROPE_OK:
+        raise RopeError(st, "rope_cache_append")
 
 
 def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -865,31 +752,12 @@ def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     workspace: None, or a uint8 tensor of rope_attention_packed_workspace(...)
     bytes to use (128-byte aligned; its contents do not matter).
     """
-    c = _Call(q, stream)
-    dtype, i32 = q.dtype, torch.int32
-    code = _type16(dtype, "attention_packed")
-    qa, qs, Tq, Hq, D = c.rows(q, "q", dtype)
-    ka, ks, Tk, Hk, _ = c.rows(k, "k", dtype, None, D)
-    va, vs, Tv, _, _ = c.rows(v, "v", dtype, Hk, D)
-    if Tv != Tk:
-        raise ValueError("k and v must have the same tokens")
-    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 1:
-        raise ValueError("cu_seqlens_q must be int32 [n_seqs + 1]")
-    n = cu_seqlens_q.shape[0] - 1
-    cuq = c.dense(cu_seqlens_q, "cu_seqlens_q", i32)
-    cuk = cuq if cu_seqlens_k is None else c.dense(cu_seqlens_k, "cu_seqlens_k", i32, (n + 1,))
-    ca, sa, rd, rows = c.tables(cos, sin, rotary_dim)
-    if out is None:
-        out = c.empty((Tq, Hq, D), dtype)
-    lib = load_library()
-    ws = c.workspace(workspace, _packed_workspace(n, Tq, Tk, Hq, Hk, D),
-                     "rope_attention_packed_workspace")
-    c.run(lib.rope_attention_packed_fwd, "rope_attention_packed_fwd", qa, ka, va,
-          c.dense(out, "out", dtype, (Tq, Hq, D)), ca, sa, c.dense(pos_q, "pos_q", i32, (Tq,)),
-          c.dense(pos_k, "pos_k", i32, (Tk,)), cuq, cuk, n, Tq, Tk, qs, ks, vs, Hq, Hk, D, rd,
-          _LAYOUT_CODE[layout], int(causal), -1.0 if scale is None else scale, code, rows,
-          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes)
-    return out
+    o = (_serving or _native()).attention_packed(
+        q, k, v, cu_seqlens_q, cos, sin, cu_seqlens_k, pos_q, pos_k, rotary_dim,
+        _LAYOUT_CODE[layout], causal, scale, out, workspace, stream)
+    if type(o) is int:
+        raise RopeError(o, "rope_attention_packed_fwd")
+    return o
 
 
 def attention_shared_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -913,30 +781,9 @@ def attention_shared_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
     workspace: None, or a uint8 tensor of rope_attention_decode_workspace(...)
     bytes to use (128-byte aligned; its contents do not matter).
     """
-    c = _Call(q, stream)
-    dtype, i32 = q.dtype, torch.int32
-    code = _type16(dtype, "attention_shared_prefix")
-    qa, qs, B, Hq, D = c.rows(q, "q", dtype)
-    kp, vp, n_pages, Hk, page, d = c.cache(k_pages, v_pages, dtype)
-    if d != D:
-        raise ValueError("the cache holds heads of %d features, q of %d" % (d, D))
-    shape = block_table.shape
-    if len(shape) != 2 or shape[0] != B:
-        raise ValueError("block_table must be [%d, max_blocks]" % B)
-    blocks = shape[1]
-    ca, sa, rd, rows = c.tables(cos, sin, rotary_dim)
-    pt = c.dense(prefix_table, "prefix_table", i32)
-    if prefix_len > 0 and (prefix_table is None or prefix_table.numel() * page < prefix_len):
-        raise ValueError("prefix_table must name the pages of %d keys" % prefix_len)
-    if out is None:
-        out = c.empty((B, Hq, D), dtype)
-    lib = load_library()
-    ws = c.workspace(workspace, _decode_workspace(B, Hq, Hk, D, page, blocks, prefix_len),
-                     "rope_attention_decode_workspace")
-    c.run(lib.rope_attention_decode_fwd, "rope_attention_decode_fwd", qa, kp, vp,
-          c.dense(out, "out", dtype, (B, Hq, D)), c.dense(block_table, "block_table", i32),
-          c.dense(seq_lens, "seq_lens", i32, (B,)), pt, prefix_len, ca, sa,
-          c.dense(pos_q, "pos_q", i32, (B,)), B, qs, Hq, Hk, D, rd, _LAYOUT_CODE[layout],
-          -1.0 if scale is None else scale, page, n_pages, blocks, code, rows,
-          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes)
-    return out
+    o = (_serving or _native()).attention_shared_prefix(
+        q, k_pages, v_pages, block_table, seq_lens, prefix_table, prefix_len, cos, sin, pos_q,
+        rotary_dim, _LAYOUT_CODE[layout], scale, out, workspace, stream)
+    if type(o) is int:
+        raise RopeError(o, "rope_attention_decode_fwd")
+    return o
