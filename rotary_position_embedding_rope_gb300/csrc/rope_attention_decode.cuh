@@ -428,7 +428,9 @@ __device__ __forceinline__ SuffixRun suffix_run(const DecodeArgs &g, const int32
             g.deal->suffix_per = per;
     }
     SuffixRun run;
-    run.w = cta * kDecWarps + warp;
+    // (consecutive runs on different SMs: with few of them every SM copies; on few
+    // SMs 4 sequences after 500 keys took 13.6 us, so 12.5)
+    run.w = warp * ctas + cta;
     run.at = {0, 0, 0, 0};
     const int64_t c = run.w * per;
     run.left = warp >= kDecWarps ? 0 : total - c < per ? total - c : per;
@@ -892,13 +894,24 @@ struct PrefixSource {
 };
 
 // ---------------------------------------------------------------------------
-// 3. the merge: a warp per (sequence, query head), a lane per D / 32 features
-template <typename T, int D>
-__global__ void __launch_bounds__(128) rope_decode_merge_kernel(const __grid_constant__ DecodeArgs g)
+// 3. the merge: W warps per (sequence, query head), a lane per D / 32 features
+//
+// Bound by latency: a few dependent reads, then a row's parts, which are many when
+// few sequences hold many keys (one sequence, 8 key heads: 125).  With few rows W
+// warps share a row's parts and join theirs in shared memory.  Whole calls with W = 1 / 4 / 8
+// (us; heads of 128, 32 over 8): 1 sequence, 8k prefix 53.2 / 22.7 / 19.4; 4, 500
+// 18.3 / 14.4 / 13.6; 16, 2k 26.3 / 24.2 / 24.3; 32, 1k 24.3 / 23.4 / 25.1; 64,
+// 8k 54.3 / - / 59.7.  So the most warps that 4096 allow, of 8, 4 and 1.  Four
+// parts at a time, the first of them beside their statistics: 17.9, 11.8, 23.1,
+// 22.4 and 53.5; with eight the registers keep CTAs out, 16.5 but 12.3, 25.2,
+// 24.2.
+constexpr int64_t kMergeWarps = 4096;
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_decode_merge_kernel(const __grid_constant__ DecodeArgs g)
 {
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    constexpr int V = D / 32, kAtOnce = 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = W == 1 ? 0 : warp;
+    const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + warp : (int64_t)blockIdx.x;
     pdl_wait();
     pdl_trigger();
     if (row >= (int64_t)g.B * g.Hq)
@@ -940,9 +953,9 @@ __global__ void __launch_bounds__(128) rope_decode_merge_kernel(const __grid_con
             return (first1 + p) * g.slot_rows + r;
         return (first2 + p - n1) * g.slot_rows + b * group + in_group;
     };
-    // Batches of 32 parts: lane i holds part i's maximum and sum, so the loads of
-    // a batch do not wait for one another.
-    const int32_t n_parts = n0 + n1 + n2;
+    // Batches of 32 of the warp's parts: lane i holds part i's maximum and sum, so
+    // the loads of a batch do not wait for one another.
+    const int32_t all = n0 + n1 + n2, n_parts = (all - share + W - 1) / W;   // parts share, share + W, ...
     float m = -INFINITY, l = 0.0f, o[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -953,10 +966,31 @@ __global__ void __launch_bounds__(128) rope_decode_merge_kernel(const __grid_con
         const float *src = nullptr;
         if (lane < n) {
             bool prefix;
-            const int64_t at = part(p0 + lane, prefix);
+            const int64_t at = part((p0 + lane) * W + share, prefix);
             mine = __ldg((prefix ? g.prefix_stats : g.stats) + at);
             src = (prefix ? g.prefix_out : g.out) + at * D;
         }
+        float v[kAtOnce][V];
+        auto fetch = [&](int i0) {
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const float *x = reinterpret_cast<const float *>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i0 + j));
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    v[j][e] = 0.0f;
+                if (i0 + j < n) {
+                    if constexpr (V == 4) {
+                        const float4 t = __ldg(reinterpret_cast<const float4 *>(x + lane * V));
+                        v[j][0] = t.x; v[j][1] = t.y; v[j][2] = t.z; v[j][3] = t.w;
+                    } else {
+                        const float2 t = __ldg(reinterpret_cast<const float2 *>(x + lane * V));
+                        v[j][0] = t.x; v[j][1] = t.y;
+                    }
+                }
+            }
+        };
+        fetch(0);
         float top = mine.x;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
@@ -973,22 +1007,45 @@ __global__ void __launch_bounds__(128) rope_decode_merge_kernel(const __grid_con
         for (int i = 0; i < V; ++i)
             o[i] *= f;
         m = top;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            const float *x = reinterpret_cast<const float *>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
-            float v[V];
-            if constexpr (V == 4) {
-                const float4 t = __ldg(reinterpret_cast<const float4 *>(x + lane * V));
-                v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-            } else {
-                const float2 t = __ldg(reinterpret_cast<const float2 *>(x + lane * V));
-                v[0] = t.x; v[1] = t.y;
+        for (int i0 = 0; i0 < n; i0 += kAtOnce) {
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const float wi = __shfl_sync(0xffffffffu, w, i0 + j);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    o[e] += wi != 0.0f ? wi * v[j][e] : 0.0f;   // (past the last part: 0)
             }
+            if (i0 + kAtOnce < n)
+                fetch(i0 + kAtOnce);
+        }
+    }
+    if constexpr (W > 1) {
+        __shared__ float2 stat[W];
+        __shared__ __align__(16) float part_o[W][D];
+        if (lane == 0)
+            stat[warp] = make_float2(m, l);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            part_o[warp][lane * V + i] = o[i];
+        __syncthreads();
+        if (warp != 0)
+            return;
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            top = fmaxf(top, stat[i].x);
+        const float ref = top == -INFINITY ? 0.0f : top;
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            o[i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float w = exp2f(stat[i].x - ref);
+            l += w * stat[i].y;
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                o[e] += wi != 0.0f ? wi * v[e] : 0.0f;
+                o[e] += w != 0.0f ? w * part_o[i][lane * V + e] : 0.0f;
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -1093,8 +1150,11 @@ static cudaError_t launch_decode(const DecodeCall &c, const DecodeLayout &lay, c
     if (e != cudaSuccess)
         return e;
     const int64_t rows = (int64_t)c.B * c.Hq;
-    const unsigned blocks = (unsigned)((rows + 3) / 4);
-    return launch_hot(rope_decode_merge_kernel<T, D>, dim3(blocks), dim3(128), 0, st, g);
+    if (rows * 8 <= kMergeWarps)
+        return launch_hot(rope_decode_merge_kernel<T, D, 8>, dim3((unsigned)rows), dim3(256), 0, st, g);
+    if (rows * 4 <= kMergeWarps)
+        return launch_hot(rope_decode_merge_kernel<T, D, 4>, dim3((unsigned)rows), dim3(128), 0, st, g);
+    return launch_hot(rope_decode_merge_kernel<T, D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, g);
 }
 
 template <typename T>

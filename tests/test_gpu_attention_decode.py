@@ -65,6 +65,12 @@ CASES = [
     # more rows than a cluster's tile, long enough for many splits and runs over several pairs
     dict(lens=[(i * 61) % 400 for i in range(70)], prefix=3000, Hq=16, Hk=4, D=128, rd=128, page=64, dtype="bf16", layout="split_half"),
     dict(lens=[3000, 1, 700], prefix=5000, Hq=4, Hk=1, D=128, rd=128, page=128, dtype="f16", layout="interleaved"),
+    # rows between the merge's forms, with and without many parts; one sequence in more than 300 parts
+    dict(lens=[(i * 29) % 200 for i in range(40)], prefix=0, Hq=16, Hk=2, D=128, rd=128, page=32, dtype="bf16", layout="split_half"),
+    dict(lens=[(i * 29) % 70 for i in range(33)], prefix=2000, Hq=16, Hk=2, D=64, rd=32, page=64, dtype="f16", layout="interleaved"),
+    dict(lens=[500] * 32, prefix=0, Hq=32, Hk=8, D=64, rd=64, page=16, dtype="bf16", layout="split_half"),
+    dict(lens=[25000], prefix=0, Hq=4, Hk=1, D=64, rd=64, page=64, dtype="bf16", layout="split_half"),
+    dict(lens=[100], prefix=21000, Hq=8, Hk=1, D=128, rd=128, page=128, dtype="f16", layout="split_half"),
 ]
 
 

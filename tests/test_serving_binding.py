@@ -98,9 +98,9 @@ def test_refusals_name_what_is_wrong():
             (dict(cos=t[:, ::2], sin=t[:, ::2]), ValueError, "cos must be contiguous"),
             (dict(sin=t[:7]), ValueError, "same shape"), (dict(cu_seqlens_q=I), ValueError, "cu_seqlens_q must be on cuda"),
             (dict(cu_seqlens_q=i[:0]), ValueError, "n_seqs"), (dict(v=x[:3]), ValueError, "same tokens"),
-            (dict(out=torch.zeros_like(x)[:3]), ValueError, "out must be"), (dict(scale="1"), TypeError, ""),
+            (dict(out=torch.zeros_like(x)[:3]), ValueError, "out must be"), (dict(scale="1"), TypeError, None),
             (dict(workspace=3), TypeError, "workspace"), (dict(workspace=I), ValueError, "workspace"),
-            (dict(stream=2.5), AttributeError, ""), (dict(scale=float("nan")), R.RopeError, "")]:
+            (dict(stream=2.5), AttributeError, None), (dict(scale=float("nan")), R.RopeError, None)]:
         with pytest.raises(err, match=name):
             R.attention_packed(**dict(packed, **over))
     decode = dict(q=x, k_pages=pool, v_pages=pool, block_table=table, seq_lens=i[:4], prefix_table=None, prefix_len=0,
@@ -109,7 +109,7 @@ def test_refusals_name_what_is_wrong():
             (dict(v_pages=pool[:1]), ValueError, "one shape"), (dict(k_pages=pool.half()), ValueError, "k_pages"),
             (dict(q=x[:, :, :32].contiguous()), ValueError, "features"), (dict(block_table=table[:3]), ValueError, "block_table"),
             (dict(block_table=table.long()), ValueError, "block_table"), (dict(prefix_len=1), ValueError, "prefix_table"),
-            (dict(prefix_len=1.5, prefix_table=i), TypeError, ""), (dict(prefix_len=2 ** 70, prefix_table=i), OverflowError, ""),
+            (dict(prefix_len=1.5, prefix_table=i), TypeError, None), (dict(prefix_len=2 ** 70, prefix_table=i), OverflowError, None),
             (dict(prefix_table=i.float()), ValueError, "prefix_table")]:
         with pytest.raises(err, match=name):
             R.attention_shared_prefix(**dict(decode, **over))
@@ -119,7 +119,7 @@ def test_refusals_name_what_is_wrong():
             (dict(k=x.float()), TypeError, "bf16 or fp16"), (dict(v=x[:, :1]), ValueError, "v must be"),
             (dict(cu_seqlens=i[:4]), ValueError, "cu_seqlens"), (dict(cache_lens=i), ValueError, "cache_lens"),
             (dict(pos=i), ValueError, "pos must be"), (dict(block_table=i), ValueError, "block_table"),
-            (dict(pos_offset=None), TypeError, ""), (dict(v_pages=pool), R.RopeError, "")]:
+            (dict(pos_offset=None), TypeError, None), (dict(v_pages=pool), R.RopeError, None)]:
         with pytest.raises(err, match=name):
             R.cache_append(**dict(append, **over))
     assert R.rope_check_errors() == R.ROPE_OK
