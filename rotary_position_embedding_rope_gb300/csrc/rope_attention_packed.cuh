@@ -99,15 +99,21 @@ __device__ __forceinline__ int32_t packed_key_tiles(int32_t t, int32_t tokens, i
 // the order of work).  One CTA.  When an offset is bad the list stays empty.
 static __device__ void packed_list(const PackedPlan &p, int32_t *bins)
 {
-    __shared__ int32_t warp_sum[kPackedPrepThreads / 32];
+    __shared__ int32_t warp_sum[kPackedPrepThreads / 32], warp_most[kPackedPrepThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kWarps = kPackedPrepThreads / 32;
     bool bad = false, small = false;
+    int32_t most = 0;                          // keys of a sequence
     for (int32_t b = tid; b < p.n_seqs; b += kPackedPrepThreads) {
         bool fits;
         bad = bad || !packed_sequence_ok(p, b, fits);
         small = small || !fits;
+        const int32_t keys = p.cu_k[b + 1] - p.cu_k[b];
+        most = keys > most ? keys : most;
     }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0)
+        warp_most[warp] = most;
     bad = __syncthreads_or(bad);
     small = __syncthreads_or(small);
     if (bad || small) {
@@ -117,11 +123,20 @@ static __device__ void packed_list(const PackedPlan &p, int32_t *bins)
         }
         return;
     }
-    for (int i = tid; i < kPackedBins; i += kPackedPrepThreads)
+    // a bin for each count there is (all 2048 took 3 us of a call of eight short
+    // prompts)
+    for (int w = 0; w < kWarps; ++w)
+        most = warp_most[w] > most ? warp_most[w] : most;
+    const int64_t counts = ((int64_t)most + kAttnKeys - 1) / kAttnKeys + 1;
+    const int32_t per = counts < kPackedBins
+                            ? ((int32_t)counts + kPackedPrepThreads - 1) / kPackedPrepThreads
+                            : kPackedBins / kPackedPrepThreads,
+                  used = per * kPackedPrepThreads;
+    for (int i = tid; i < used; i += kPackedPrepThreads)
         bins[i] = 0;
     __syncthreads();
     // bin of a count: most key tiles in bin 0
-    auto bin_of = [](int32_t n) { return kPackedBins - 1 - (n < kPackedBins - 1 ? n : kPackedBins - 1); };
+    auto bin_of = [used](int32_t n) { return used - 1 - (n < used - 1 ? n : used - 1); };
     for (int pass = 0; pass < 2; ++pass) {
         // short sequences have few tiles: a warp takes 32 sequences at a time,
         // one per lane, then all lanes the tiles of each of them in turn
@@ -150,10 +165,9 @@ static __device__ void packed_list(const PackedPlan &p, int32_t *bins)
         __syncthreads();
         if (pass == 0) {
             // counts -> first index of each bin
-            constexpr int kPer = kPackedBins / kPackedPrepThreads;
             int32_t sum = 0;
-            for (int i = 0; i < kPer; ++i)
-                sum += bins[tid * kPer + i];
+            for (int i = 0; i < per; ++i)
+                sum += bins[tid * per + i];
             int32_t inc = sum;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -167,9 +181,9 @@ static __device__ void packed_list(const PackedPlan &p, int32_t *bins)
             int32_t at = inc - sum;
             for (int w = 0; w < warp; ++w)
                 at += warp_sum[w];
-            for (int i = 0; i < kPer; ++i) {
-                const int32_t n = bins[tid * kPer + i];
-                bins[tid * kPer + i] = at;
+            for (int i = 0; i < per; ++i) {
+                const int32_t n = bins[tid * per + i];
+                bins[tid * per + i] = at;
                 at += n;
             }
             if (tid == kPackedPrepThreads - 1)
@@ -179,43 +193,39 @@ static __device__ void packed_list(const PackedPlan &p, int32_t *bins)
     }
 }
 
-// The four maps of sequence b, one warp: the template with the sequence's
-// address and row count, made in shared memory and published to global memory
-// for the tensor-map proxy.
-static __device__ void packed_maps(const PackedPlan &p, const PackedMapTemplates &tmpl, int32_t b,
-                            CUtensorMap *buf)
+// Map i of sequence b, one warp: the template with the sequence's address and
+// row count, made in shared memory and published to global memory for the
+// tensor-map proxy.
+static __device__ void packed_map(const PackedPlan &p, const PackedMapTemplates &tmpl, int32_t b, int i,
+                                  CUtensorMap *buf)
 {
     const int lane = threadIdx.x & 31;
-    const int32_t q0 = p.cu_q[b], k0 = p.cu_k[b];
-    const int32_t nq = p.cu_q[b + 1] - q0, nk = p.cu_k[b + 1] - k0;
-    for (int i = 0; i < kPackedMaps; ++i) {
-        const bool keys = i < 2;
-        const int32_t start = keys ? k0 : q0, rows = keys ? nk : nq;
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(&tmpl.m[i]);
-        reinterpret_cast<uint32_t *>(buf)[lane] = src[lane];
-        __syncwarp();
-        if (lane == 0) {
-            const uint32_t s = attn_smem_u32(buf);
-            asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;"
-                         ::"r"(s), "l"(p.base[i] + (int64_t)start * p.step[i])
-                         : "memory");
-            // rows are the second dimension of K and V, the third of Q and O
-            if (keys)
-                asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;"
-                             ::"r"(s), "r"(rows < 1 ? 1 : rows)
-                             : "memory");
-            else
-                asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 2, %1;"
-                             ::"r"(s), "r"(rows < 1 ? 1 : rows)
-                             : "memory");
-        }
-        __syncwarp();
-        asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync."
-                     "aligned [%0], [%1], 128;"
-                     ::"l"(p.maps + (int64_t)b * kPackedMaps + i), "r"(attn_smem_u32(buf))
+    const bool keys = i < 2;                   // K and V; else Q and O
+    const int32_t *cu = keys ? p.cu_k : p.cu_q;
+    const int32_t start = cu[b], rows = cu[b + 1] - start;
+    reinterpret_cast<uint32_t *>(buf)[lane] = reinterpret_cast<const uint32_t *>(&tmpl.m[i])[lane];
+    __syncwarp();
+    if (lane == 0) {
+        const uint32_t s = attn_smem_u32(buf);
+        asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;"
+                     ::"r"(s), "l"(p.base[i] + (int64_t)start * p.step[i])
                      : "memory");
-        __syncwarp();
+        // rows are the second dimension of K and V, the third of Q and O
+        if (keys)
+            asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;"
+                         ::"r"(s), "r"(rows < 1 ? 1 : rows)
+                         : "memory");
+        else
+            asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 2, %1;"
+                         ::"r"(s), "r"(rows < 1 ? 1 : rows)
+                         : "memory");
     }
+    __syncwarp();
+    asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync."
+                 "aligned [%0], [%1], 128;"
+                 ::"l"(p.maps + (int64_t)b * kPackedMaps + i), "r"(attn_smem_u32(buf))
+                 : "memory");
+    __syncwarp();
 }
 
 // The list (CTA 0), the maps (the next map_blocks CTAs), and the keys of the
@@ -237,12 +247,11 @@ __global__ void __launch_bounds__(kPackedPrepThreads)
         return;
     }
     if ((int)blockIdx.x <= p.map_blocks) {
-        constexpr int kWarps = kPackedPrepThreads / 32;
-        for (int64_t b = (int64_t)(blockIdx.x - 1) * kWarps + (tid >> 5); b < p.n_seqs;
-             b += (int64_t)p.map_blocks * kWarps) {
+        static_assert(kPackedPrepThreads / 32 == kPackedMaps, "a warp per map");
+        for (int64_t b = blockIdx.x - 1; b < p.n_seqs; b += p.map_blocks) {
             bool fits;
             if (packed_sequence_ok(p, (int32_t)b, fits))
-                packed_maps(p, tmpl, (int32_t)b, &buf[tid >> 5]);
+                packed_map(p, tmpl, (int32_t)b, tid >> 5, &buf[tid >> 5]);
         }
         return;
     }
@@ -1284,9 +1293,8 @@ static cudaError_t launch_packed(const PackedArgs &c, const PackedLayout &lay, c
     p.base[2] = (int64_t)c.q; p.step[2] = c.q_stride * 2;
     p.base[3] = (int64_t)c.o; p.step[3] = (int64_t)c.Hq * D * 2;
     p.flag = k.flag;
-    // four warps a CTA, one sequence a warp, 256 CTAs at most
-    const int64_t map_blocks = (k.n_seqs + 3) / 4;
-    p.map_blocks = (int32_t)(map_blocks < 256 ? map_blocks : 256);
+    // a sequence a CTA, a map a warp; 1024 CTAs at most
+    p.map_blocks = k.n_seqs < 1024 ? k.n_seqs : 1024;
     RowsArgs rows = k;
     rows.k_out = ws + lay.keys;
     const int64_t groups = kPackedPrepThreads / (D / 16);
