@@ -797,7 +797,7 @@ struct PrefixSource {
         const int32_t hu = c.at / sizes.tiles, group = c.v / sizes.row_tiles;
         PackedUnit u;
         u.tok0 = (c.v - group * sizes.row_tiles) * (2 * kAttnRows >> lg);
-        u.seq = 0; u.q_start = 0; u.tokens = B; u.n_keys = n_keys;
+        u.seq = 0; u.q_start = 0; u.k_start = 0; u.tokens = B; u.n_keys = n_keys;
         u.head0 = hu << lg;
         u.kv = hu / units_per_kv;
         u.first = c.at - hu * sizes.tiles;

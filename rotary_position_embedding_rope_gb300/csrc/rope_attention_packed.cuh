@@ -8,16 +8,17 @@
 // Two launches:
 //   1. rope_packed_prepare_kernel rotates the keys into the workspace
 //      ([Hk][total_k][D]), lists the query tiles of all sequences, longest
-//      first, and writes four tensor maps per sequence (rotated K, V, Q, O);
+//      first, and writes a tensor map of each sequence's values;
 //   2. rope_attn_packed_kernel walks the list, one cluster of two CTAs per
 //      pair of SMs.
 //
-// Why maps per sequence: a map whose row count is the sequence's length makes
-// the copy engine itself end every tile where the sequence ends.  Keys, values
-// and queries past it arrive as zeros (so an infinity or NaN of the next
-// sequence never meets a zero probability), and output rows past it are not
-// written.  Nothing in the tile loop asks where a sequence ends, except the
-// score mask.
+// Where a sequence ends: a map whose row count is the sequence's length makes
+// the copy engine itself end a value tile there, with zeros, so an infinity or
+// NaN of the next sequence never meets a zero probability.  Only the values need
+// that: keys past the end become scores that the mask replaces, and queries past
+// it become rows of their own, which are not written.  (A map that a kernel wrote
+// has to be acquired, about a microsecond for the next copy.  With maps of keys,
+// queries and outputs too, the helpers did that twice a unit: MEASURED.)
 //
 // Rows of a tile: GP heads of one group and consecutive tokens, row = token *
 // GP + head, GP the largest power of two (up to 16) that divides the group
@@ -41,10 +42,9 @@ namespace rope {
 // One query tile of a sequence: tokens tok0 .. of sequence seq.
 struct alignas(16) PackedEntry {
     int32_t seq, tok0, Lq, Lk;
-    int32_t q_start, n_tiles, pad0, pad1;      // n_tiles: key tiles the tile's rows can see
+    int32_t q_start, n_tiles, k_start, pad;    // n_tiles: key tiles the tile's rows can see
 };
 
-constexpr int kPackedMaps = 4;                 // K, V, Q, O of a sequence
 constexpr int kPackedPrepThreads = 128;
 constexpr int kPackedBins = 2048;              // key-tile counts told apart when sorting
 
@@ -57,15 +57,10 @@ struct PackedPlan {
     int64_t table_rows;
     int32_t *n_entries;                        // [1]
     PackedEntry *entries;
-    CUtensorMap *maps;                         // [n_seqs][kPackedMaps]
-    int64_t base[kPackedMaps];                 // address of token 0
-    int64_t step[kPackedMaps];                 // bytes from token to token
+    CUtensorMap *maps;                         // [n_seqs]: of the values
+    int64_t base, step;                        // values: address of token 0, bytes from token to token
     int32_t *flag;
     int32_t map_blocks;                        // grid: the planner, the maps, then the rotation
-};
-
-struct PackedMapTemplates {
-    CUtensorMap m[kPackedMaps];
 };
 
 // ---------------------------------------------------------------------------
@@ -142,21 +137,22 @@ static __device__ void packed_list(const PackedPlan &p, int32_t *bins)
         // one per lane, then all lanes the tiles of each of them in turn
         for (int32_t b0 = warp * 32; b0 < p.n_seqs; b0 += kWarps * 32) {
             const int32_t mine = b0 + lane;
-            int32_t q0 = 0, Lq = 0, Lk = 0;
+            int32_t q0 = 0, k0 = 0, Lq = 0, Lk = 0;
             if (mine < p.n_seqs) {
                 q0 = p.cu_q[mine];
+                k0 = p.cu_k[mine];
                 Lq = p.cu_q[mine + 1] - q0;
-                Lk = p.cu_k[mine + 1] - p.cu_k[mine];
+                Lk = p.cu_k[mine + 1] - k0;
             }
             const int n = p.n_seqs - b0 < 32 ? p.n_seqs - b0 : 32;
             for (int s = 0; s < n; ++s) {
                 const int32_t sq0 = __shfl_sync(0xffffffffu, q0, s), sLq = __shfl_sync(0xffffffffu, Lq, s),
-                              sLk = __shfl_sync(0xffffffffu, Lk, s);
+                              sLk = __shfl_sync(0xffffffffu, Lk, s), sk0 = __shfl_sync(0xffffffffu, k0, s);
                 for (int64_t t = (int64_t)lane * p.tile_tokens; t < sLq; t += 32 * (int64_t)p.tile_tokens) {
                     const int32_t nt = packed_key_tiles((int32_t)t, p.tile_tokens, sLq, sLk, p.causal);
                     const int32_t at = atomicAdd(&bins[bin_of(nt)], 1);
                     if (pass == 1) {
-                        PackedEntry e = {b0 + s, (int32_t)t, sLq, sLk, sq0, nt, 0, 0};
+                        PackedEntry e = {b0 + s, (int32_t)t, sLq, sLk, sq0, nt, sk0, 0};
                         p.entries[at] = e;
                     }
                 }
@@ -193,37 +189,28 @@ static __device__ void packed_list(const PackedPlan &p, int32_t *bins)
     }
 }
 
-// Map i of sequence b, one warp: the template with the sequence's address and
-// row count, made in shared memory and published to global memory for the
-// tensor-map proxy.
-static __device__ void packed_map(const PackedPlan &p, const PackedMapTemplates &tmpl, int32_t b, int i,
-                                  CUtensorMap *buf)
+// The map of sequence b's values, one warp: the template with the sequence's
+// address and row count, made in shared memory and published to global memory
+// for the tensor-map proxy.
+static __device__ void packed_map(const PackedPlan &p, const CUtensorMap &tmpl, int32_t b, CUtensorMap *buf)
 {
     const int lane = threadIdx.x & 31;
-    const bool keys = i < 2;                   // K and V; else Q and O
-    const int32_t *cu = keys ? p.cu_k : p.cu_q;
-    const int32_t start = cu[b], rows = cu[b + 1] - start;
-    reinterpret_cast<uint32_t *>(buf)[lane] = reinterpret_cast<const uint32_t *>(&tmpl.m[i])[lane];
+    const int32_t start = p.cu_k[b], rows = p.cu_k[b + 1] - start;
+    reinterpret_cast<uint32_t *>(buf)[lane] = reinterpret_cast<const uint32_t *>(&tmpl)[lane];
     __syncwarp();
     if (lane == 0) {
         const uint32_t s = attn_smem_u32(buf);
         asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;"
-                     ::"r"(s), "l"(p.base[i] + (int64_t)start * p.step[i])
+                     ::"r"(s), "l"(p.base + (int64_t)start * p.step)
                      : "memory");
-        // rows are the second dimension of K and V, the third of Q and O
-        if (keys)
-            asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;"
-                         ::"r"(s), "r"(rows < 1 ? 1 : rows)
-                         : "memory");
-        else
-            asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 2, %1;"
-                         ::"r"(s), "r"(rows < 1 ? 1 : rows)
-                         : "memory");
+        asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;"
+                     ::"r"(s), "r"(rows < 1 ? 1 : rows)
+                     : "memory");
     }
     __syncwarp();
     asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync."
                  "aligned [%0], [%1], 128;"
-                 ::"l"(p.maps + (int64_t)b * kPackedMaps + i), "r"(attn_smem_u32(buf))
+                 ::"l"(p.maps + b), "r"(attn_smem_u32(buf))
                  : "memory");
     __syncwarp();
 }
@@ -234,7 +221,7 @@ static __device__ void packed_map(const PackedPlan &p, const PackedMapTemplates 
 template <typename T, int LAYOUT, int D>
 __global__ void __launch_bounds__(kPackedPrepThreads)
     rope_packed_prepare_kernel(const RowsArgs a, const PackedPlan p,
-                               const __grid_constant__ PackedMapTemplates tmpl)
+                               const __grid_constant__ CUtensorMap tmpl)
 {
     constexpr int L = D / 16, kGroups = kPackedPrepThreads / L, kHeads = 4;
     __shared__ __align__(128) CUtensorMap buf[kPackedPrepThreads / 32];
@@ -247,11 +234,12 @@ __global__ void __launch_bounds__(kPackedPrepThreads)
         return;
     }
     if ((int)blockIdx.x <= p.map_blocks) {
-        static_assert(kPackedPrepThreads / 32 == kPackedMaps, "a warp per map");
-        for (int64_t b = blockIdx.x - 1; b < p.n_seqs; b += p.map_blocks) {
+        constexpr int kWarps = kPackedPrepThreads / 32;
+        for (int64_t b = (int64_t)(blockIdx.x - 1) * kWarps + (tid >> 5); b < p.n_seqs;
+             b += (int64_t)p.map_blocks * kWarps) {
             bool fits;
             if (packed_sequence_ok(p, (int32_t)b, fits))
-                packed_map(p, tmpl, (int32_t)b, tid >> 5, &buf[tid >> 5]);
+                packed_map(p, tmpl, (int32_t)b, &buf[tid >> 5]);
         }
         return;
     }
@@ -452,13 +440,13 @@ __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, const 
 // of key head kv.
 struct PackedUnit {
     int32_t seq, tok0, tokens;                 // tokens: of the sequence (or the batch)
-    int32_t q_start;                           // the sequence's first token
+    int32_t q_start, k_start;                  // the sequence's first query and key
     int32_t first, n_tiles, n_keys;            // n_keys: of the sequence (or the prefix)
     int32_t head0, kv, part;                   // part: which partial result (prefix)
 };
 
 // Where the units come from and where K and V lie.  PackedSource: the list and
-// the maps the prepare kernel wrote; rows end in bf16 / fp16 outputs.
+// the values' maps that the prepare kernel wrote; rows end in bf16 / fp16 outputs.
 struct PackedSource {
     static constexpr bool kPrefix = false;
     template <int D>
@@ -466,10 +454,11 @@ struct PackedSource {
     {
         return (int)kPackedSmem<D>;
     }
-    AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, causal, flag
+    AttnArgs a;                                // o, Hq, cos, sin, table_rows, rotary_dim, scale, causal, flag
+    CUtensorMap k_map, q_map, o_map;           // rotated keys, queries and outputs of all sequences
     const PackedEntry *entries;
     const int32_t *n_entries;
-    const CUtensorMap *maps;
+    const CUtensorMap *maps;                   // [n_seqs]: of the values
     const int32_t *pos_q;
     int32_t head_units;                        // Hq / GP
     int32_t units_per_kv;                      // (Hq / Hk) / GP
@@ -507,10 +496,10 @@ struct PackedSource {
         const uint32_t i = L / (uint32_t)head_units;
         const int32_t hu = (int32_t)(L - i * (uint32_t)head_units);
         const int4 x = __ldg(reinterpret_cast<const int4 *>(entries + i));
-        const int2 y = __ldg(reinterpret_cast<const int2 *>(entries + i) + 2);
+        const int4 y = __ldg(reinterpret_cast<const int4 *>(entries + i) + 1);
         PackedUnit u;
         u.seq = x.x; u.tok0 = x.y; u.tokens = x.z; u.n_keys = x.w;
-        u.q_start = y.x; u.n_tiles = y.y; u.first = 0; u.part = 0;
+        u.q_start = y.x; u.n_tiles = y.y; u.k_start = y.z; u.first = 0; u.part = 0;
         u.head0 = hu << lg;
         u.kv = hu / units_per_kv;
         return u;
@@ -537,16 +526,15 @@ struct PackedSource {
                                               uint64_t *bar, uint32_t rank, int lane) const
     {
         if (lane < D / 64)
-            load_half_box(dst + lane * 8192, maps + (int64_t)u.seq * kPackedMaps, lane * 64,
-                          kt * kAttnKeys + 64 * (int)rank, u.kv, bar, rank);
+            load_half_box(dst + lane * 8192, &k_map, lane * 64,
+                          u.k_start + kt * kAttnKeys + 64 * (int)rank, u.kv, bar, rank);
     }
     template <int D>
     __device__ __forceinline__ void load_values(const PackedUnit &u, int32_t kt, int32_t, uint8_t *dst,
                                                 uint64_t *bar, uint32_t rank, int lane) const
     {
         if (lane == 0)
-            load_half_box(dst, maps + (int64_t)u.seq * kPackedMaps + 1, D / 2 * (int)rank, kt * kAttnKeys,
-                          u.kv, bar, rank);
+            load_half_box(dst, maps + u.seq, D / 2 * (int)rank, kt * kAttnKeys, u.kv, bar, rank);
     }
 };
 
@@ -841,7 +829,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         const int row = tid - 128, wq = warp - 4;  // row of the tile = TMEM lane
         uint32_t qn = 0, un = 0;                   // query tiles rotated, units with tiles written
-        int32_t o_seq = -1;                        // the sequence whose O map was acquired
         Cursor cq = with_tiles(src.first(walk));   // the unit whose query tile is next
         Cursor c = src.first(walk);                // the unit whose output is next
         Cursor cl = cq;                            // the unit whose query tile is requested next
@@ -849,21 +836,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
         auto load_query = [&]() {
             if (wq == 0 && valid(cl)) {
                 const PackedUnit u = unit_of(cl);
-                const CUtensorMap *map;
-                if constexpr (Source::kPrefix) {
-                    map = &src.q_map;
-                } else {
-                    map = src.maps + (int64_t)u.seq * kPackedMaps + 2;
-                    acquire_map(map);
-                }
                 const uint32_t b = ln & 1u;
                 if (lane == 0)
                     mbar_expect_tx(&bar_q[b], kTile);
                 __syncwarp();
-                // (tokens past the sequence's end arrive as zeros)
+                // (rows of tokens past the sequence's end are not looked at)
                 if (lane < D / 64)
-                    tma_load_3d(sQ(b) + lane * kBoxBytes, map, lane * 64, u.head0,
-                                u.tok0 + (int)rank * tokens, &bar_q[b]);
+                    tma_load_3d(sQ(b) + lane * kBoxBytes, &src.q_map, lane * 64, u.head0,
+                                u.q_start + u.tok0 + (int)rank * tokens, &bar_q[b]);
                 __syncwarp();
                 ++ln;
                 cl = next_with_tiles(cl);
@@ -918,10 +898,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 arrive_leader(&bar_ofree[un % kOBufs]);
             } else {
                 // O / l of the warp's 32 rows, staged and stored by TMA (boxes
-                // of 64 features x GP heads x 32 / GP tokens; tokens past the
-                // sequence's end are not written, and a box that starts past
-                // it is not issued).  O is free for the next unit's products
-                // as soon as the last of it is in registers.
+                // of 64 features x GP heads x 32 / GP tokens) or, where the
+                // sequence ends within them, by the warp.  O is free for the next
+                // unit's products as soon as the last of it is in registers.
                 const bool none = stat.y == 0.0f;  // a row that saw no key (0 * v may be NaN)
                 const float inv = none ? 0.0f : 1.0f / stat.y;
 #pragma unroll
@@ -953,15 +932,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0 && y0 < u.tokens) {
-                    const CUtensorMap *om = src.maps + (int64_t)u.seq * kPackedMaps + 3;
-                    if (u.seq != o_seq)
-                        acquire_map(om);
-                    o_seq = u.seq;
+                if (y0 + (32 >> lg) <= u.tokens) {
+                    if (lane == 0) {
 #pragma unroll
-                    for (int bx = 0; bx < D / 64; ++bx)
-                        tma_store_3d(om, sO + bx * kBoxBytes + wq * 32 * 128, bx * 64, u.head0, y0);
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        for (int bx = 0; bx < D / 64; ++bx)
+                            tma_store_3d(&src.o_map, sO + bx * kBoxBytes + wq * 32 * 128, bx * 64, u.head0,
+                                         u.q_start + y0);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                } else {
+                    // the sequence's last rows, a row by D / 8 lanes
+                    constexpr int kRow = D / 8;
+                    T *o = static_cast<T *>(a.o) + ((int64_t)(u.q_start + y0) * a.Hq + u.head0) * D;
+                    const int live = (u.tokens - y0) << lg;        // rows (none: negative)
+                    for (int r = lane / kRow; r < live; r += 32 / kRow)
+                        *reinterpret_cast<uint4 *>(o + ((int64_t)(r >> lg) * a.Hq + (r & ((1 << lg) - 1))) * D +
+                                                   lane % kRow * 8) =
+                            *reinterpret_cast<const uint4 *>(sO + sw128(wq * 32 + r, lane % kRow));
+                    __syncwarp();
                 }
             }
             if (u.n_tiles > 0) {
@@ -1072,14 +1060,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
 #pragma unroll
             for (int s = 0; s < kPackedStages; ++s)
                 last_ph[s] = 2;
-            int32_t seq = -1;                      // the sequence whose map was acquired
             for (Cursor c = with_tiles(src.first(walk)); ok && valid(c); c = next_with_tiles(c)) {
                 const PackedUnit u = unit_of(c);
-                if constexpr (!Source::kPrefix) {
-                    if (u.seq != seq)
-                        acquire_map(src.maps + (int64_t)u.seq * kPackedMaps);
-                    seq = u.seq;
-                }
                 for (int32_t kt = 0; ok && kt < u.n_tiles; ++kt) {
                     const int32_t z = src.template key_place<D>(u, kt, rank, lane);
                     if (!first)
@@ -1119,12 +1101,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
 #pragma unroll
             for (int s = 0; s < kPackedStages; ++s)
                 last_ph[s] = 2;
-            int32_t seq = -1;
+            int32_t seq = -1;                      // the sequence whose map was acquired
             for (Cursor c = with_tiles(src.first(walk)); ok && valid(c); c = next_with_tiles(c)) {
                 const PackedUnit u = unit_of(c);
                 if constexpr (!Source::kPrefix) {
                     if (u.seq != seq)
-                        acquire_map(src.maps + (int64_t)u.seq * kPackedMaps + 1);
+                        acquire_map(src.maps + u.seq);
                     seq = u.seq;
                 }
                 for (int32_t kt = 0; ok && kt < u.n_tiles; ++kt) {
@@ -1261,20 +1243,22 @@ static cudaError_t launch_packed(const PackedArgs &c, const PackedLayout &lay, c
     const int lg = __builtin_ctz((unsigned)gp);
     const int64_t total_k = k.total > 0 ? k.total : 1;
 
-    // map templates: rotated K, V, Q, O (without keys K and V stand on the
-    // workspace and are never used)
-    PackedMapTemplates tmpl;
+    // maps of all sequences (without keys K and V stand on the workspace and are
+    // never used), V's a template for those of each sequence
+    PackedSource ka;
+    memset(&ka, 0, sizeof ka);
+    CUtensorMap v_map;
     const void *v = k.total > 0 ? k.v : ws;
     const int64_t vs = k.total > 0 ? k.v_stride : (int64_t)k.Hk * D;
     const uint32_t g = (uint32_t)gp;
-    if (!encode_3d(enc, &tmpl.m[0], ws + lay.keys, dt, {D, total_k, k.Hk}, {D * 2, total_k * D * 2},
+    if (!encode_3d(enc, &ka.k_map, ws + lay.keys, dt, {D, total_k, k.Hk}, {D * 2, total_k * D * 2},
                    {64, 64, 1}, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_3d(enc, &tmpl.m[1], v, dt, {D, total_k, k.Hk}, {vs * 2, D * 2},
+        !encode_3d(enc, &v_map, v, dt, {D, total_k, k.Hk}, {vs * 2, D * 2},
                    {(uint32_t)D / 2, (uint32_t)kAttnKeys, 1},
                    D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !encode_3d(enc, &tmpl.m[2], c.q, dt, {D, c.Hq, c.total_q}, {D * 2, c.q_stride * 2},
+        !encode_3d(enc, &ka.q_map, c.q, dt, {D, c.Hq, c.total_q}, {D * 2, c.q_stride * 2},
                    {64, g, kAttnRows / g}, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_3d(enc, &tmpl.m[3], c.o, dt, {D, c.Hq, c.total_q}, {D * 2, (int64_t)c.Hq * D * 2},
+        !encode_3d(enc, &ka.o_map, c.o, dt, {D, c.Hq, c.total_q}, {D * 2, (int64_t)c.Hq * D * 2},
                    {64, g, 32 / g}, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
 
@@ -1288,13 +1272,11 @@ static cudaError_t launch_packed(const PackedArgs &c, const PackedLayout &lay, c
     p.n_entries = reinterpret_cast<int32_t *>(ws);
     p.entries = reinterpret_cast<PackedEntry *>(ws + lay.entries);
     p.maps = reinterpret_cast<CUtensorMap *>(ws + lay.maps);
-    p.base[0] = (int64_t)(ws + lay.keys); p.step[0] = D * 2;
-    p.base[1] = (int64_t)v; p.step[1] = vs * 2;
-    p.base[2] = (int64_t)c.q; p.step[2] = c.q_stride * 2;
-    p.base[3] = (int64_t)c.o; p.step[3] = (int64_t)c.Hq * D * 2;
+    p.base = (int64_t)v; p.step = vs * 2;
     p.flag = k.flag;
-    // a sequence a CTA, a map a warp; 1024 CTAs at most
-    p.map_blocks = k.n_seqs < 1024 ? k.n_seqs : 1024;
+    // four warps a CTA, one sequence a warp, 256 CTAs at most
+    const int64_t map_blocks = (k.n_seqs + 3) / 4;
+    p.map_blocks = (int32_t)(map_blocks < 256 ? map_blocks : 256);
     RowsArgs rows = k;
     rows.k_out = ws + lay.keys;
     const int64_t groups = kPackedPrepThreads / (D / 16);
@@ -1303,14 +1285,13 @@ static cudaError_t launch_packed(const PackedArgs &c, const PackedLayout &lay, c
     if (blocks > 0x7fffffff)
         return cudaErrorInvalidConfiguration;
     cudaError_t e = launch_hot(rope_packed_prepare_kernel<T, LAYOUT, D>, dim3((unsigned)blocks),
-                               dim3(kPackedPrepThreads), 0, st, rows, p, tmpl);
+                               dim3(kPackedPrepThreads), 0, st, rows, p, v_map);
     if (e != cudaSuccess)
         return e;
 
-    PackedSource ka;
-    memset(&ka, 0, sizeof ka);
     if (lay.tiles * (c.Hq / gp) >= (1ll << 32) - 1024)
         return cudaErrorInvalidConfiguration;
+    ka.a.o = c.o; ka.a.Hq = c.Hq;
     ka.a.cos = k.cos; ka.a.sin = k.sin; ka.a.rotary_dim = k.rotary_dim; ka.a.table_rows = k.table_rows;
     ka.a.scale_log2 = c.scale_log2; ka.a.causal = c.causal; ka.a.flag = k.flag;
     ka.entries = p.entries; ka.n_entries = p.n_entries; ka.maps = p.maps;

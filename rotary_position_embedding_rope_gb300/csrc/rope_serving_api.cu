@@ -96,7 +96,7 @@ bool packed_layout(int64_t n_seqs, int64_t total_q, int64_t total_k, int32_t Hq,
     // empty ones have none
     const int64_t tokens = 256 / packed_group_heads(Hq, Hk);
     out->tiles = total_q / tokens + (n_seqs < total_q ? n_seqs : total_q);
-    const int64_t entries = product({out->tiles, 32}), maps = product({n_seqs, 4 * 128});
+    const int64_t entries = product({out->tiles, 32}), maps = product({n_seqs, 128});
     const int64_t keys = product({total_k, Hk, D, 2});
     if (entries < 0 || maps < 0 || keys < 0 || entries > (1ll << 60) || maps > (1ll << 60) ||
         keys > (1ll << 60))

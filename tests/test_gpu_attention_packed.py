@@ -270,3 +270,23 @@ def test_refusals():
         with pytest.raises(err):
             R.attention_packed(**dict(ok, **bad))
     assert R.rope_check_errors() == R.ROPE_OK
+
+
+@pytest.mark.parametrize("D, Hq, Hk, causal", [(128, 8, 2, True), (64, 4, 4, False), (128, 32, 1, False)])
+def test_what_neighbours_hold_stays_with_them(D, Hq, Hk, causal):
+    """Sequences whose queries, keys and values are infinities and NaN, between others of every kind of length."""
+    require_gpu()
+    R = lib()
+    lens = [5, 130, 1, 7, 300, 64, 33, 129, 2, 256, 90]
+    c = dict(q=lens, Hq=Hq, Hk=Hk, D=D, rd=D, dtype="bf16", layout="split_half", causal=causal)
+    q, k, v, cu, _ = make(c)
+    cos, sin = S.tables(1e4, D, 300)
+    clean = run(R, c, q, k, v, cu, cu, cos, sin)
+    for x in (q, k, v):
+        for b in range(1, len(lens), 2):
+            rows = x[int(cu[b]):int(cu[b + 1])]
+            rows[:, :, ::2], rows[:, :, 1::2] = float("nan"), float("inf")
+    got = run(R, c, q, k, v, cu, cu, cos, sin)
+    for b in range(0, len(lens), 2):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        assert torch.equal(got[rows], clean[rows])

@@ -102,7 +102,7 @@ def test_packed_of_nothing(lib, over):
 def test_packed_workspace(lib):
     ws = lib.rope_attention_packed_workspace
     need = ws(2, 10, 12, 4, 2, 128)
-    assert need >= 2 * 4 * 128 + 12 * 2 * 128 * 2 and need % 128 == 0
+    assert need >= 2 * 128 + 12 * 2 * 128 * 2 and need % 128 == 0
     assert lib.rope_attention_packed_fwd(*packed_args(wsb=need - 1)) == INV
     assert ws(0, 10, 12, 4, 2, 128) == ws(2, 0, 12, 4, 2, 128) == ws(2, 10, 12, 0, 0, 128) == 0
     assert ws(-1, 10, 12, 4, 2, 128) == ws(2, 10, 12, 4, 3, 128) == ws(2, 10, 12, 4, 2, 96) == -1
