@@ -416,7 +416,7 @@ rope_status rope_cache_append(const void *k, const void *v, void *k_pages, void 
  * pos_q, pos_k: device int32[total_q], int32[total_k] or NULL.  NULL: a
  *    token's table row is its index among its sequence's queries (keys).
  *    -1: not rotated; other rows outside the table are not rotated and raise
- *    the flag.
+ *    the flag.  Entries of tokens of no sequence are not looked at.
  * causal, softmax_scale: as rope_attention_fwd.
  * workspace: device, 128-byte aligned, at least
  *    rope_attention_packed_workspace(...) bytes; overwritten (the rotated

@@ -271,7 +271,8 @@ __global__ void __launch_bounds__(kPackedPrepThreads)
     }
     int64_t row;
     if (a.pos != nullptr) {
-        row = live ? __ldg(a.pos + t) : -1;
+        // (what stands at tokens of no sequence is not looked at)
+        row = live && t >= __ldg(a.cu) && t < __ldg(a.cu + a.n_seqs) ? __ldg(a.pos + t) : -1;
     } else {
         const bool cached = a.n_seqs + 1 <= kPackedBins;
         if (cached) {

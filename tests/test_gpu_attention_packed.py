@@ -290,3 +290,17 @@ def test_what_neighbours_hold_stays_with_them(D, Hq, Hk, causal):
     for b in range(0, len(lens), 2):
         rows = slice(int(cu[b]), int(cu[b + 1]))
         assert torch.equal(got[rows], clean[rows])
+
+
+def test_positions_of_no_sequence_are_not_looked_at():
+    """A padded batch: whatever stands at the tokens before the first and behind the last sequence raises nothing."""
+    require_gpu()
+    R = lib()
+    c = dict(q=[40, 30], Hq=4, Hk=2, D=64, rd=64, dtype="bf16", layout="split_half", causal=True)
+    q, k, v, cu, _ = make(c, first=3, behind=9)
+    cos, sin = S.tables(1e4, 64, 64)
+    pos = torch.full((82,), 10 ** 6, dtype=torch.int32)
+    pos[3:43], pos[43:73] = torch.arange(40), torch.arange(30)
+    plain = run(R, c, q, k, v, cu, cu, cos, sin)
+    got = run(R, c, q, k, v, cu, cu, cos, sin, pos_q=pos.cuda(), pos_k=pos.cuda())
+    assert torch.equal(got[3:73], plain[3:73])
