@@ -105,7 +105,7 @@ int32_t type16(const at::Tensor &t, const char *what)
 struct Call {
     c10::DeviceIndex device;
     cudaStream_t stream;
-    bool own_stream;                           // not the current one: new tensors are recorded on it
+    bool own_stream;                           // not the current one
 
     Call(const at::Tensor &first, PyObject *s)
     {
@@ -171,13 +171,28 @@ struct Call {
         return static_cast<const int32_t *>(dense(o, name, at::kInt, n, optional));
     }
 
-    // A new tensor, alive until the call's stream is done with it.
+    // A new tensor for the call, from the memory of the call's stream: the allocator
+    // hands a block out as soon as the host has dropped it, to calls that run behind
+    // its last use on the same stream.  A block of the current stream could still
+    // be written by work queued there.
     at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const
     {
-        at::Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, device));
+        const at::TensorOptions options = at::TensorOptions().dtype(type).device(at::kCUDA, device);
+        if (!own_stream)
+            return at::empty(shape, options);
+        const c10::cuda::CUDAStreamGuard guard(stream == nullptr
+                                                   ? c10::cuda::getDefaultCUDAStream(device)
+                                                   : c10::cuda::getStreamFromExternal(stream, device));
+        return at::empty(shape, options);
+    }
+
+    // The same, for the caller, who uses it on the current stream next: once
+    // dropped, it is handed out again when the work queued there is done.
+    at::Tensor empty_returned(at::IntArrayRef shape, at::ScalarType type) const
+    {
+        at::Tensor t = empty(shape, type);
         if (own_stream)
-            t.record_stream(stream == nullptr ? c10::cuda::getDefaultCUDAStream(device).unwrap()
-                                              : c10::cuda::getStreamFromExternal(stream, device).unwrap());
+            t.record_stream(c10::cuda::getCurrentCUDAStream(device).unwrap());
         return t;
     }
 
@@ -262,7 +277,7 @@ struct Cache {
 at::Tensor output(const Call &c, PyObject *given, const Rows &like, at::ScalarType type)
 {
     if (given == Py_None)
-        return c.empty({like.n, like.H, like.D}, type);
+        return c.empty_returned({like.n, like.H, like.D}, type);
     const at::Tensor &t = tensor(given, "out");
     c.dense(given, "out", type, -1);
     if (t.dim() != 3 || t.size(0) != like.n || t.size(1) != like.H || t.size(2) != like.D)

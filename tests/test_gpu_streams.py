@@ -1,0 +1,88 @@
+"""Calls on a stream other than the current one: what a call allocates comes
+from the memory of its own stream (a block of the current one may still be in
+use there), and calls of two streams do not disturb one another."""
+import contextlib
+
+import pytest
+import torch
+
+import serving_ref as S
+from gpu_util import lib, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@contextlib.contextmanager
+def allocations(streams):
+    """Collects the stream of every block handed out inside."""
+    torch.cuda.memory._record_memory_history(enabled="all", context=None)
+    try:
+        yield
+        trace = torch.cuda.memory._snapshot()["device_traces"][torch.cuda.current_device()]
+        streams += [e["stream"] for e in trace if e["action"] == "alloc"]
+    finally:
+        torch.cuda.memory._record_memory_history(enabled=None)
+
+
+def serving_inputs(seed=3):
+    g = torch.Generator().manual_seed(seed)
+    x = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()
+    i = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()
+    t = dict(q=x(700, 4, 64), k=x(700, 2, 64), v=x(700, 2, 64), d=x(2, 4, 64), kp=x(8, 2, 16, 64), vp=x(8, 2, 16, 64),
+             cu=i(0, 450, 700), table=i([0, 1], [2, 3]), lens=i(19, 5), prefix=i(4, 5))
+    t["cos"], t["sin"] = (y.cuda() for y in S.tables(1e4, 64, 512))
+    return t
+
+
+def packed(R, t, **more):
+    return R.attention_packed(t["q"], t["k"], t["v"], t["cu"], t["cos"], t["sin"], causal=True, **more)
+
+
+def decode(R, t, **more):
+    return R.attention_shared_prefix(t["d"], t["kp"], t["vp"], t["table"], t["lens"], t["prefix"], 20, t["cos"], t["sin"],
+                                     **more)
+
+
+@pytest.mark.parametrize("call", [packed, decode])
+@pytest.mark.parametrize("raw", [False, True])
+def test_serving_blocks_come_from_the_calls_stream(call, raw):
+    require_gpu()
+    R = lib()
+    t = serving_inputs()
+    want = call(R, t)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    with allocations(got):
+        a = call(R, t, stream=side.cuda_stream if raw else side)
+    assert len(got) == 2 and set(got) == {side.cuda_stream}            # the output and the workspace
+    got = []
+    with torch.cuda.stream(side), allocations(got):
+        b = call(R, t, stream=0 if raw else torch.cuda.default_stream())
+    assert len(got) == 2 and set(got) == {0}
+    got = []
+    with allocations(got):
+        c = call(R, t)
+    assert len(got) == 2 and set(got) == {0}
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in (a, b, c)) and R.rope_check_errors() == R.ROPE_OK
+
+
+@pytest.mark.parametrize("call", [packed, decode])
+def test_serving_calls_of_two_streams_at_once(call):
+    """A call on the current stream, then at once one of the same sizes on another, with nothing between them."""
+    require_gpu()
+    R = lib()
+    a, b = serving_inputs(3), serving_inputs(4)
+    want = call(R, a), call(R, b)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        busy = torch.randn(2048, 2048, device="cuda")
+        for _ in range(4):
+            busy = busy @ busy                                          # the current stream is behind the host
+        x = call(R, a)
+        y = call(R, b, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(x, want[0]) and torch.equal(y, want[1])
+    assert R.rope_check_errors() == R.ROPE_OK
