@@ -302,13 +302,36 @@ def rope_tune_rotation_launch(ctas_per_sm: int = 0, min_units: int = 0, prefetch
 # --------------------------------------------------------------------------
 # conveniences
 # --------------------------------------------------------------------------
+def _allocated(make, stream, device):
+    """What make() allocates, for a call on ``stream``.
+
+    The caching allocator hands a block out again as soon as the host has
+    dropped it, to work that runs behind its last use on the same stream: memory
+    that a call on another stream writes at once has to be that stream's.  It is
+    recorded on the current stream, where the caller uses it next.
+    """
+    if stream is None:
+        return make()
+    current = torch.cuda.current_stream(device)
+    handle = _stream(stream)
+    if handle == current.cuda_stream:
+        return make()
+    own = torch.cuda.ExternalStream(handle, current.device) if handle else \
+        torch.cuda.default_stream(current.device)
+    with torch.cuda.stream(own):
+        made = make()
+    for t in made if isinstance(made, tuple) else (made,):
+        t.record_stream(current)
+    return made
+
+
 def build_tables(theta: float, rotary_dim: int, max_pos: int, interpolate_factor: float = 1.0,
                  device=None, stream=None):
     """Allocate and fill fp32 cos/sin tables [max_pos, rotary_dim // 2]."""
     device = torch.device("cuda") if device is None else torch.device(device)
     h = rotary_dim // 2
-    cos = torch.empty((max_pos, h), dtype=torch.float32, device=device)
-    sin = torch.empty((max_pos, h), dtype=torch.float32, device=device)
+    cos, sin = _allocated(lambda: tuple(torch.empty((max_pos, h), dtype=torch.float32, device=device)
+                                        for _ in range(2)), stream, device)
     rope_tables_build(theta, rotary_dim, max_pos, interpolate_factor, cos, sin, stream)
     return cos, sin
 
@@ -323,8 +346,8 @@ def build_tables_ex(freqs_for: str, rotary_dim: int, rows: int, theta: float = 1
     -1 (keys)."""
     device = torch.device("cuda") if device is None else torch.device(device)
     h = rotary_dim // 2
-    cos = torch.empty((rows, h), dtype=torch.float32, device=device)
-    sin = torch.empty((rows, h), dtype=torch.float32, device=device)
+    cos, sin = _allocated(lambda: tuple(torch.empty((rows, h), dtype=torch.float32, device=device)
+                                        for _ in range(2)), stream, device)
     rope_tables_build_ex(_FREQ_CODE[freqs_for], theta, max_freq, rotary_dim, rows, pos_offset,
                          pos_divisor, xpos_sign, xpos_scale_base, xpos_gamma, xpos_center, cos,
                          sin, stream)
@@ -505,9 +528,9 @@ def rotate_qk(q: torch.Tensor, k: torch.Tensor | None, cos: torch.Tensor, sin: t
     if cos.shape[1] != rd // 2:
         raise ValueError("table width %d does not match rotary_dim %d" % (cos.shape[1], rd))
     pos, stride = _positions(pos_idx, B, S)
-    q_out = torch.empty_like(q) if q_out is None else q_out
+    q_out = _allocated(lambda: torch.empty_like(q), stream, q.device) if q_out is None else q_out
     if k is not None and k_out is None:
-        k_out = torch.empty_like(k)
+        k_out = _allocated(lambda: torch.empty_like(k), stream, k.device)
     for o, x, n in ((q_out, q, "q_out"), (k_out, k, "k_out")):
         if x is not None and (o.shape != x.shape or o.dtype != x.dtype):
             raise ValueError("%s must match its input's shape and dtype" % n)
@@ -603,11 +626,11 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Tens
                         "got %s: convert the inputs first (e.g. q.bfloat16()), a rounding that is "
                         "the caller's choice" % q.dtype)
     rd = 2 * cos.shape[1] if rotary_dim is None else rotary_dim
-    o = torch.empty_like(q) if out is None else out
+    o = _allocated(lambda: torch.empty_like(q), stream, q.device) if out is None else out
     if isinstance(k_workspace, str):
         if k_workspace != "auto":
             raise ValueError("k_workspace must be 'auto', None or a tensor")
-        k_workspace = attention_workspace(k, attn_mask)
+        k_workspace = _allocated(lambda: attention_workspace(k, attn_mask), stream, k.device)
     ws_bytes = 0 if k_workspace is None else k_workspace.numel() * k_workspace.element_size()
     args = (q, k, v, o, cos, sin, pos_q, pos_k, B, Hq, Hk, Sq, Sk, D, rd, _LAYOUT_CODE[layout],
             int(causal), -1.0 if scale is None else scale, _DTYPE_CODE[q.dtype], cos.shape[0])

@@ -18,11 +18,15 @@ import torch
 from . import _DTYPE_CODE, _LAYOUT_CODE, _shape4, rope_apply_qk_out, rope_attention_fwd
 
 
-def _on_streams(t: torch.Tensor, streams) -> torch.Tensor:
-    """Mark a staging tensor as used on the pipeline's streams, so that the
-    caching allocator does not reuse its memory, once it is dropped, before
-    the work queued there by then has finished."""
-    for s in streams:
+def _staging_tensor(dims, dtype, device, streams) -> torch.Tensor:
+    """A staging tensor from the memory of the first of the pipeline's streams,
+    which copies into it first (a block of the current stream could still be in
+    use there), marked as used on the others, so that the caching allocator does
+    not reuse it, once it is dropped, before the work queued there by then has
+    finished."""
+    with torch.cuda.stream(streams[0]):
+        t = torch.empty(dims, dtype=dtype, device=device)
+    for s in streams[1:]:
         t.record_stream(s)
     return t
 
@@ -60,10 +64,10 @@ class HostRotator:
         key = (tuple(q.shape), None if k is None else tuple(k.shape), q.dtype, dims_q, dims_k)
         if key != self._key:
             def dev(dims):
-                return _on_streams(torch.empty(dims, dtype=q.dtype, device=self.device),
-                                   (self.s_in, self.s_run, self.s_out))
+                return _staging_tensor(dims, q.dtype, self.device,
+                                       (self.s_in, self.s_run, self.s_out))
             # the old slots may still be in use by copies and calls queued on
-            # the three streams: recorded on them at creation, their memory is
+            # the three streams: taken from one and recorded on the others, their memory is
             # not handed out again before that work is done
             self._slots = [(dev(dims_q), None if k is None else dev(dims_k))
                            for _ in range(self.nslots)]
@@ -181,9 +185,8 @@ class HostAttention:
         key = (tuple(q.shape), tuple(k.shape), q.dtype, nb, nkv)
         if key != self._key:
             def dev(t, heads):
-                return _on_streams(torch.empty((nb, heads) + tuple(t.shape[2:]), dtype=t.dtype,
-                                               device=self.device),
-                                   (self.s_in, self.s_run, self.s_out))
+                return _staging_tensor((nb, heads) + tuple(t.shape[2:]), t.dtype, self.device,
+                                       (self.s_in, self.s_run, self.s_out))
             self._slots = [(dev(q, nkv * grp), dev(k, nkv), dev(k, nkv), dev(q, nkv * grp))
                            for _ in range(self.nslots)]
             # the calls all run on s_run, one after another: one workspace serves them

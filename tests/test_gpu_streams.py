@@ -86,3 +86,76 @@ def test_serving_calls_of_two_streams_at_once(call):
         torch.cuda.synchronize()
         assert torch.equal(x, want[0]) and torch.equal(y, want[1])
     assert R.rope_check_errors() == R.ROPE_OK
+
+
+def dense_inputs(seed=3):
+    g = torch.Generator().manual_seed(seed)
+    x = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()
+    t = dict(q=x(2, 4, 600, 128), k=x(2, 2, 600, 128), v=x(2, 2, 600, 128))
+    t["mask"] = torch.ones(2, 600, dtype=torch.bool, device="cuda")
+    t["mask"][1, 500:] = False
+    t["cos"], t["sin"] = (y.cuda() for y in S.tables(1e4, 128, 600))
+    return t
+
+
+def dense(R, t, **more):
+    return R.attention(t["q"], t["k"], t["v"], t["cos"], t["sin"], causal=True, **more),
+
+
+def masked(R, t, **more):
+    return R.attention(t["q"], t["k"], t["v"], t["cos"], t["sin"], attn_mask=t["mask"], **more),
+
+
+def rotated(R, t, **more):
+    return R.rotate_qk(t["q"], t["k"], t["cos"], t["sin"], **more)
+
+
+def tables(R, t, **more):
+    return R.build_tables(1e4, 64, 100, **more)
+
+
+def tables_ex(R, t, **more):
+    return R.build_tables_ex("pixel", 64, 100, **more)
+
+
+@pytest.mark.parametrize("call", [dense, masked, rotated, tables, tables_ex])
+@pytest.mark.parametrize("raw", [False, True])
+def test_blocks_come_from_the_calls_stream(call, raw):
+    require_gpu()
+    R = lib()
+    t = dense_inputs()
+    want = call(R, t)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = []
+    for current, other in ((torch.cuda.default_stream(), side), (side, torch.cuda.default_stream())):
+        got = []
+        with torch.cuda.stream(current), allocations(got):
+            outs.append(call(R, t, stream=other.cuda_stream if raw else other))
+        assert len(got) == 2 and set(got) == {other.cuda_stream}
+    got = []
+    with allocations(got):
+        outs.append(call(R, t))
+    assert len(got) == 2 and set(got) == {0}
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want)) and R.rope_check_errors() == R.ROPE_OK
+
+
+def test_host_staging_comes_from_the_copy_streams_memory():
+    require_gpu()
+    R = lib()
+    from rotary_position_embedding_rope_gb300.host import HostAttention, HostRotator
+
+    t = dense_inputs()
+    want = rotated(R, t), dense(R, t)
+    torch.cuda.synchronize()
+    q, k, v = (t[n].cpu().pin_memory() for n in "qkv")
+    qo, ko, o = (torch.empty_like(x).pin_memory() for x in (q, k, q))
+    rot, att = HostRotator(chunks=2), HostAttention(chunks=2)
+    for run, s_in in ((lambda: rot.apply_qk(q, k, t["cos"], t["sin"], qo, ko), rot.s_in),
+                      (lambda: att.forward(q, k, v, o, t["cos"], t["sin"], causal=True), att.s_in)):
+        got = []
+        with allocations(got):
+            run().synchronize()
+        assert got and set(got) == {s_in.cuda_stream}
+    assert torch.equal(qo, want[0][0].cpu()) and torch.equal(ko, want[0][1].cpu()) and torch.equal(o, want[1][0].cpu())
