@@ -403,16 +403,15 @@ struct SuffixShared {
     int abort_flag;
 };
 
-// What the merge has to know of the suffixes' deal to `ctas` CTAs, written by one
-// CTA before anything in it can fail: after an expired wait the merge still runs,
-// and finds the parts' places by it.
-__device__ __forceinline__ void publish_suffixes(const DecodeArgs &g, const int32_t *start, int32_t carry,
-                                                 int32_t ctas)
+// What the merge has to know of the suffixes' deal.  One CTA writes it, whether or
+// not its waits expired: the merge runs in either case, and finds the parts'
+// places by it.
+__device__ __forceinline__ void publish_suffixes(const DecodeArgs &g, const int32_t *start, int64_t per)
 {
     for (int32_t b = threadIdx.x; b <= g.B + g.fold; b += blockDim.x)
         g.chunk_start[b] = start[b];
     if (threadIdx.x == 0)
-        g.deal->suffix_per = decode_per_warp((int64_t)carry * g.Hk * g.row_groups, ctas * kDecWarps);
+        g.deal->suffix_per = per;
 }
 
 // The suffixes' share of CTA `cta` of `ctas`, whose first eight warps work:
@@ -433,6 +432,8 @@ __device__ __forceinline__ SuffixRun suffix_run(const DecodeArgs &g, const int32
     const int32_t heads = g.Hk * g.row_groups;
     const int64_t total = (int64_t)carry * heads;
     const int64_t per = decode_per_warp(total, ctas * kDecWarps);
+    if (cta == 0)
+        publish_suffixes(g, start, per);
     SuffixRun run;
     // (consecutive runs on different SMs: with few of them every SM copies; on few
     // SMs 4 sequences after 500 keys took 13.6 us, so 12.5)
@@ -694,8 +695,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
     pdl_wait();
     pdl_trigger();
     const int32_t carry = scan_chunks<kDecThreads>(g, start, warp_sum);
-    if (blockIdx.x == 0)
-        publish_suffixes(g, start, carry, gridDim.x);
     const SuffixRun run = suffix_run<D>(g, start, carry, blockIdx.x, gridDim.x, sh);
     decode_suffixes<T, LAYOUT, D>(g, smem, run, sh);
 }
@@ -744,30 +743,28 @@ struct PrefixSource {
         __shared__ int32_t warp_sum[kPackedThreads / 32];
         const int32_t chunks = scan_chunks<kPackedThreads>(g, chunk_starts<D>(smem), warp_sum);
         const PrefixDeal d = prefix_deal(sizes, plan_clusters(sizes, chunks, best));
-        const Walk w = {(int32_t)cid, d.clusters, d.groups, d.per, chunks};
-        if (blockIdx.x == 0) {
-            if (threadIdx.x == 0)
-                g.deal->prefix_per = d.per;
-            if (g.suffix)
-                publish_suffixes(g, chunk_starts<D>(smem), chunks, (int32_t)gridDim.x - first_suffix_cta(w));
-        }
-        return w;
-    }
-    // The first CTA without prefix work; 0: all have some, and the suffixes run behind it.
-    static __device__ __forceinline__ int32_t first_suffix_cta(const Walk &w)
-    {
-        return 2 * w.clusters < (int32_t)gridDim.x ? 2 * w.clusters : 0;
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            g.deal->prefix_per = d.per;
+        return {(int32_t)cid, d.clusters, d.groups, d.per, chunks};
     }
     // The suffixes, on the CTAs without prefix work, or on all behind it: two
     // warpgroups, with 216 registers a thread (after the roles' 240 / 112 / 104).
     template <typename T, int LAYOUT, int D>
-    __device__ __forceinline__ void finish(const Walk &w, uint8_t *smem) const
+    __device__ __forceinline__ void finish(const Walk &w, uint8_t *smem, bool failed) const
     {
         __shared__ SuffixShared<D> sh;
-        const int32_t used = first_suffix_cta(w);
+        const int32_t used = 2 * w.clusters < (int32_t)gridDim.x ? 2 * w.clusters : 0;
         const int32_t cta = (int32_t)blockIdx.x - used;
         if (!g.suffix || cta < 0)
             return;
+        if (failed) {                          // copies may still be on their way: no work,
+            // but what the merge needs; the scan lies behind the roles' memory
+            if (cta == 0)
+                publish_suffixes(g, chunk_starts<D>(smem),
+                                 decode_per_warp((int64_t)w.chunks * g.Hk * g.row_groups,
+                                                 ((int32_t)gridDim.x - used) * kDecWarps));
+            return;
+        }
         const SuffixRun run =
             suffix_run<D>(g, chunk_starts<D>(smem), w.chunks, cta, (int32_t)gridDim.x - used, sh);
         const int warp = threadIdx.x >> 5;

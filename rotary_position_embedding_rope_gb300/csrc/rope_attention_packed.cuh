@@ -1163,10 +1163,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols)
                      : "memory");
-    if constexpr (Source::kPrefix) {
-        if (!failed)                               // (else copies may still be on their way)
-            src.template finish<T, LAYOUT, D>(walk, smem);
-    }
+    if constexpr (Source::kPrefix)
+        src.template finish<T, LAYOUT, D>(walk, smem, failed);
 }
 
 // ---------------------------------------------------------------------------
