@@ -457,7 +457,9 @@ int64_t rope_attention_packed_workspace(int64_t n_seqs, int64_t total_q, int64_t
  *
  *   o_b = softmax(scale * rot(q_b) [K_prefix; K_b]^T) [V_prefix; V_b]
  *
- * The prefix's keys and values are read once for the whole batch.
+ * The prefix's keys and values are read once for every 256 rows (sequence, head)
+ * of a key head, not once for every sequence: rows of up to 16 heads of a group
+ * (the largest power of two that divides its size) and of as many sequences as fit.
  * q: device [B, Hq, D], row stride q_stride (elements, a multiple of 8);
  *    o: device [B, Hq, D], dense, written.  Hq is a multiple of Hk.
  * k_pages, v_pages: the cache, [n_pages, Hk, page_size, D].

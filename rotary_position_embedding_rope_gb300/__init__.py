@@ -796,7 +796,7 @@ def attention_shared_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
     sequence; returns [B, Hq, D].  k_pages, v_pages: the cache that
     cache_append writes, [pages, Hk, page_size, D] of rotated keys.
     prefix_table: int32 pages of the prefix_len keys that all sequences share
-    (None with prefix_len 0), read once for the whole batch.
+    (None with prefix_len 0), read for the batch, not for every sequence.
     block_table: int32 [B, max_blocks]; seq_lens: int32 [B], the keys of each
     suffix, the new token's own among them (cache_append it first).
     pos_q: int32 [B] table rows (-1 = not rotated), or None for

@@ -8,13 +8,16 @@
 // i's maximum m_i, sum l_i = sum_j 2^(s_j - m_i) and output O_i = sum_j 2^(s_j -
 // m_i) v_j, and M = max m_i,
 //   o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
-// So the parts run apart, and each key is read once:
-//   1. the prefix, once for the whole batch: its rows (sequence, head) are the
-//      rows of rope_attn_packed_kernel's tiles (the batch is a "sequence" of B
-//      tokens), its keys come from pages, its key tiles are dealt out evenly to
-//      clusters; every piece of a head's keys leaves an fp32 (O, m, l);
-//   2. the suffixes (decode_suffixes): every warp an equal run of 16-key chunks of
-//      all suffixes, laid end to end, so that ragged lengths balance;
+// So the parts run apart:
+//   1. the prefix, for the whole batch: its rows (sequence, head) are the rows of
+//      rope_attn_packed_kernel's tiles (the batch is a "sequence" of B tokens), its
+//      keys come from pages, its key tiles are dealt out evenly to clusters; every
+//      piece of a head's keys leaves an fp32 (O, m, l).  A key is read once for each
+//      tile of 256 rows: GP heads of a group, GP the largest power of two that
+//      divides the group's size (16 at most), and 256 / GP sequences;
+//   2. the suffixes (decode_suffixes): every warp an equal run of chunks (16 keys, 32
+//      of 64 features) of all suffixes, laid end to end, so that ragged lengths
+//      balance; a key is read once for up to 16 heads of its group;
 //   3. rope_decode_merge_kernel.
 // 1 and 2 do not depend on one another and share a launch: every CTA works out
 // from the suffixes' lengths how many clusters the prefix gets (plan_clusters);
@@ -24,8 +27,9 @@
 // more than 16 rows per key head, the prefix is one more sequence of 2, with all
 // the rows of the batch, in a kernel of 2 alone.
 //
-// What bounds it: bytes -- the prefix once, every suffix once; from about 300
-// rows per key head on, the prefix products.
+// What bounds it: bytes -- the prefix once a row tile (from L2 where the batch has
+// several), every suffix once; from about 300 rows per key head on, the prefix
+// products.
 #pragma once
 
 #include "rope_attention_packed.cuh"
@@ -155,8 +159,8 @@ __device__ __forceinline__ int64_t query_row(const int32_t *pos_q, int32_t b, in
 // 2. the suffixes
 //
 // A pair is (sequence, key head, row group): up to 16 query heads of one group,
-// the 16 rows of an mma.  The 16-key chunks of all pairs, sequence after
-// sequence, form one long list; warp w of the grid owns chunks [w * per, (w +
+// the 16 rows of an mma.  The chunks of all pairs, sequence after sequence, form
+// one long list; warp w of the grid owns chunks [w * per, (w +
 // 1) * per) of it, whatever pairs they belong to, and leaves an fp32 (O, m, l)
 // for each pair it touches in slot w + pair (either index grows by one from
 // one slot to the next, so slots are distinct).  Nothing waits on anything
@@ -182,7 +186,7 @@ static constexpr int kDecSmem = kDecWarps * (kDecStages<D> * kDecStageBytes<D> +
 
 struct DecodeArgs {
     AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, flag
-    CUtensorMap k_map, v_map;                  // boxes of 64 features x 16 keys
+    CUtensorMap k_map, v_map;                  // boxes of 64 features x a chunk's keys, or a page's
     const void *q;                             // [B][Hq][D], row stride q_stride
     int64_t q_stride;
     void *o;                                   // [B][Hq][D]
@@ -843,7 +847,10 @@ struct PrefixSource {
         }
         return p * Hk + kv;
     }
-    // (with several row tiles the prefix is read by as many clusters)
+    // (with several row tiles the prefix is read by as many clusters at about the
+    // same time.  The head units of one key head read it one after the other, long
+    // after one another: kept for them, 32 sequences of 24 heads over 8 after 128k
+    // keys took 289 us, so 286, and of 48 over 2 102, so 91)
     __device__ __forceinline__ uint64_t policy() const { return sizes.row_tiles > 1 ? l2_keep() : l2_once(); }
     // Where this lane's boxes of a tile lie, looked up before the stage is waited
     // for: keys (box i of a half, features 64 x ..) and values (page i).
