@@ -27,6 +27,10 @@
 // more than 16 rows per key head, the prefix is one more sequence of 2, with all
 // the rows of the batch, in a kernel of 2 alone.
 //
+// Roundings: rot(q), and P before P V, to the element type (the operands of a 16-bit
+// product), as a prompt's, so that a token's output does not tell whether it came
+// with a prompt or in a step; everything else is fp32 until o.
+//
 // What bounds it: bytes -- the prefix once a row tile (from L2 where the batch has
 // several), every suffix once; from about 300 rows per key head on, the prefix
 // products.

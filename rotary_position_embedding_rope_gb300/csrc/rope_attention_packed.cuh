@@ -5,6 +5,11 @@
 //   o_i = sum_j softmax_j(scale * rot(q_i) . rot(k_j)) v_j
 //
 // over the keys j of token i's own sequence, j <= i + Lk - Lq when causal.
+// Scores, maxima, sums and O are fp32.  Rotated queries and keys, and P before
+// P V, are rounded to the element type: a kind::f16 product takes both operands
+// in one 16-bit type, and two parts of each would be two to four products where
+// their issue is the bound.  The dense attention rounds at the same places, so
+// sequences of one length get its bits.
 // Two launches:
 //   1. rope_packed_prepare_kernel rotates the keys into the workspace
 //      ([Hk][total_k][D]), lists the query tiles of all sequences, longest
@@ -559,8 +564,8 @@ __device__ __forceinline__ void prefetch_table_row(const AttnArgs &a, int64_t tr
     }
 }
 
-// Rotates one query tile in place (rows r = token * GP + head; tokens past the
-// sequence's end hold zeros): a thread per row, its table row read from global
+// Rotates one query tile in place (rows r = token * GP + head; rows of tokens past
+// the sequence's end, the next one's queries or zeros, stay as they are): a thread per row, its table row read from global
 // memory.  The helpers run this beside the tile loop, so its latency is hidden.
 //
 // rotate_pairs2 is rotate_pair on two pairs at once (f32x2 instructions, half
@@ -834,9 +839,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
         // ---- the helpers.  A pass: rotate the next unit's query tile, write this
         // unit's output, and (warp 4) request the query tile of the unit after the
         // next: its buffer is this unit's, whose last product has finished.  The
-        // first pass requests two tiles and only rotates.  (Query tiles requested by
-        // the key warp, between key tiles, held the fourth key tile of every unit
-        // up for 1.5 us: the map has to be acquired first.)
+        // first pass requests two tiles and only rotates.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         const int row = tid - 128, wq = warp - 4;  // row of the tile = TMEM lane
         uint32_t qn = 0, un = 0;                   // query tiles rotated, units with tiles written

@@ -1,6 +1,8 @@
 // rope_rows.cuh -- rows of packed sequences: which sequence a token belongs
 // to, and the rotation of a head row by a group of D / 16 lanes.  Shared by
-// the kernels that write rotated keys (rope_cache.cu).
+// the kernels that write rotated keys (rope_cache.cu, the prepare kernel of
+// rope_attention_packed.cuh) and the decode kernels' queries
+// (rope_attention_decode.cuh).
 #pragma once
 
 #include <cuda_runtime.h>

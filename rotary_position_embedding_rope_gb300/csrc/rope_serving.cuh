@@ -39,7 +39,7 @@ struct RowsArgs {
 cudaError_t launch_cache_append(const RowsArgs &a, int32_t D, int32_t layout, int32_t dtype,
                                 cudaStream_t st);
 
-// Attention over packed sequences (rope_attention_packed.cu).
+// Attention over packed sequences (rope_attention_packed.cuh).
 struct PackedArgs {
     RowsArgs keys;                   // k -> the rotated-key workspace
     const void *q;                   // [total_q][Hq][D]

@@ -135,8 +135,10 @@ bool decode_layout(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_sh
     out->clusters = (int32_t)(work < kSms / 2 ? (work > 0 ? work : 1) : kSms / 2);
     const int64_t groups = out->clusters / out->row_tiles > 0 ? out->clusters / out->row_tiles : 1;
     const int64_t parts = n_prefix > 0 && !out->fold ? groups + head_units : 0;
-    // The suffixes: equal runs of 16-key chunks for the warps of one CTA an SM,
-    // at least two chunks a warp.
+    // The suffixes: a CTA for every 256 keys of a pair, up to one an SM, whose eight
+    // warps take runs of at least two chunks.  Chunks of 64 features are of 32 keys,
+    // so half the warps of a small call have no run then; with a CTA for 512 keys
+    // fewer SMs copy (one sequence of 2000 keys, 16 heads of 64: 11.3 us, so 10.2).
     int64_t chunks = product({B, max_blocks, (int64_t)1 << page_shift >> 4});
     if (chunks < 0 || chunks > kMaxInt32)
         return false;
