@@ -334,14 +334,7 @@ __device__ __forceinline__ void load_query_rows(const DecodeArgs &g, const Chunk
         if (trow[i] < 0)
             continue;
         float c[8], s[8];
-        const int64_t w = trow[i] * (g.a.rotary_dim / 2) + 8 * j;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(g.a.cos + w) + q);
-            const float4 s4 = __ldg(reinterpret_cast<const float4 *>(g.a.sin + w) + q);
-            c[4 * q] = c4.x; c[4 * q + 1] = c4.y; c[4 * q + 2] = c4.z; c[4 * q + 3] = c4.w;
-            s[4 * q] = s4.x; s[4 * q + 1] = s4.y; s[4 * q + 2] = s4.z; s[4 * q + 3] = s4.w;
-        }
+        table_values(g.a.cos, g.a.sin, trow[i] * (g.a.rotary_dim / 2) + 8 * j, c, s);
         rotate_part<T, LAYOUT>(x0[i], x1[i], c, s);
     }
     __syncwarp();                              // the tile's last readers are done

@@ -91,14 +91,7 @@ __global__ void __launch_bounds__(kRowThreads) rope_cache_append_kernel(const Ro
     }
     if (part.rot && row >= 0) {
         float c[8], s[8];
-        const int64_t at = row * (a.rotary_dim / 2) + 8 * j;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(a.cos + at) + q);
-            const float4 s4 = __ldg(reinterpret_cast<const float4 *>(a.sin + at) + q);
-            c[4 * q] = c4.x; c[4 * q + 1] = c4.y; c[4 * q + 2] = c4.z; c[4 * q + 3] = c4.w;
-            s[4 * q] = s4.x; s[4 * q + 1] = s4.y; s[4 * q + 2] = s4.z; s[4 * q + 3] = s4.w;
-        }
+        table_values(a.cos, a.sin, row * (a.rotary_dim / 2) + 8 * j, c, s);
 #pragma unroll
         for (int i = 0; i < kRowHeads; ++i)
             if (h0 + i < a.Hk)

@@ -57,6 +57,19 @@ __device__ __forceinline__ RowPart row_part(int j, int rotary_dim)
     return p;
 }
 
+// Eight cos and eight sin values of a table, from element `at` (a multiple of 8).
+__device__ __forceinline__ void table_values(const float *cos, const float *sin, int64_t at, float (&c)[8],
+                                             float (&s)[8])
+{
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const float4 c4 = __ldg(reinterpret_cast<const float4 *>(cos + at) + q);
+        const float4 s4 = __ldg(reinterpret_cast<const float4 *>(sin + at) + q);
+        c[4 * q] = c4.x; c[4 * q + 1] = c4.y; c[4 * q + 2] = c4.z; c[4 * q + 3] = c4.w;
+        s[4 * q] = s4.x; s[4 * q + 1] = s4.y; s[4 * q + 2] = s4.z; s[4 * q + 3] = s4.w;
+    }
+}
+
 // Rotates the two vectors of a RowPart with rot set.
 template <typename T, int LAYOUT>
 __device__ __forceinline__ void rotate_part(uint4 &x0, uint4 &x1, const float (&c)[8],
