@@ -520,11 +520,12 @@ rope_status rope_check_errors(void *stream);
 
 /*
  * rope_probe_wait_expiry -- diagnostic: exercise the path an expired wait
- * takes, without stalling any real kernel.  One thread of one CTA waits,
- * with the bounded mbarrier wait that the attention kernels use, on a barrier that nothing arrives at; after `cycles` SM clock cycles
- * (1 .. 4e9; 2e6 is about a millisecond) the wait gives up and sets the
- * timeout bit of the device error flag, as an expired wait inside those
- * kernels does.  The next rope_check_errors then returns
+ * takes, without stalling any real kernel.  Two threads of one CTA wait, one
+ * with each of the bounded mbarrier waits that the attention kernels use, on a
+ * barrier that nothing arrives at; after `cycles` SM clock cycles (1 .. 4e9; 2e6
+ * is about a millisecond), or about as long, the waits give up, and the timeout
+ * bit of the device error flag is set, as by an expired wait inside those
+ * kernels.  The next rope_check_errors then returns
  * ROPE_ERR_KERNEL_TIMEOUT and clears the flag.  The pages have no
  * counterpart; this is an addition of this library, for tests and for
  * callers that want to check their error handling.

@@ -14,23 +14,38 @@ cudaError_t launch_attention(const AttnArgs &a, int32_t D, int32_t layout, int32
     return launch_attention_t<false>(a, D, layout, dtype, st);
 }
 
-// Probe of the expiry path: one thread waits, with the attention kernels'
-// bounded wait, on a barrier that nothing arrives at; after `cycles` clock
-// cycles the wait gives up and the thread records the expiry as those kernels
-// do (bit 1 of the device flag).  Nothing else runs, so nothing stalls.
+// Probe of the expiry path: a thread and a warp wait, one with each of the
+// attention kernels' bounded waits, on a barrier that nothing arrives at: for
+// `cycles` clock cycles, and for as many tries as those should last.  When both
+// have given up, the counted wait no sooner than after an eighth of the cycles (one
+// that did would cut real waits short), a thread records the expiry as those
+// kernels do (bit 1 of the device flag).  Nothing else runs, so nothing stalls.
+constexpr long long kTryCycles = 8000;         // of a failed try: 4.05 us, 7964 cycles
 __global__ void rope_wait_probe_kernel(int32_t *flag, long long cycles)
 {
     __shared__ __align__(8) uint64_t bar;
-    if (threadIdx.x == 0)
+    __shared__ int abort;
+    if (threadIdx.x == 0) {
         mbar_init(&bar, 1);
+        abort = 0;
+    }
     __syncthreads();
-    if (threadIdx.x == 0 && !attn_wait(&bar, 0u, nullptr, cycles))
+    bool expired = true;
+    if (threadIdx.x == 0) {
+        expired = !attn_wait(&bar, 0u, nullptr, cycles);
+    } else if (threadIdx.x >= 32) {            // (together, as the roles wait)
+        const long long tries = cycles / kTryCycles + 1, t0 = clock64();
+        expired = !role_wait(&bar, 0u, &abort, (int)(tries < kRoleTries ? tries : kRoleTries)) &&
+                  clock64() - t0 >= cycles / 8;
+    }
+    expired = __syncthreads_and(expired);
+    if (threadIdx.x == 0 && expired)
         atomicOr(flag, 2);
 }
 
 cudaError_t launch_wait_probe(int32_t *flag, long long cycles, cudaStream_t st)
 {
-    rope_wait_probe_kernel<<<1, 32, 0, st>>>(flag, cycles);
+    rope_wait_probe_kernel<<<1, 64, 0, st>>>(flag, cycles);
     return cudaGetLastError();
 }
 

@@ -205,6 +205,32 @@ __device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity,
     }
 }
 
+// The bounded wait of the packed kernel's roles: attn_wait with tries counted instead
+// of cycles, which makes each of its twenty copies half as long.  All threads of
+// a warp wait together: a failed try then suspends the warp for 4 us, so the limit
+// is some 2 s.  (A try of one thread, the others elsewhere, fails after 200 cycles.)
+constexpr int kRoleTries = 1 << 19;
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, const volatile int *abort,
+                                          int tries = kRoleTries)
+{
+    const uint32_t b = attn_smem_u32(bar);
+#pragma unroll 1
+    for (int i = 0; i < tries; ++i) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done)
+                     : "r"(b), "r"(parity)
+                     : "memory");
+        if (done)
+            return true;
+        if (*abort)
+            break;
+    }
+    return false;
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(attn_smem_u32(bar)) : "memory");

@@ -419,31 +419,6 @@ __device__ __forceinline__ void load_half_box_l2(uint8_t *dst, const CUtensorMap
                      : "memory");
 }
 
-// The bounded wait of this kernel's roles: attn_wait with tries counted instead
-// of cycles (a failed try_wait suspends the thread for about 4 us here, so the
-// limit is some 2 s), which makes each of its twenty copies half as long.
-constexpr int kRoleTries = 1 << 19;
-__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, const volatile int *abort,
-                                          int tries = kRoleTries)
-{
-    const uint32_t b = attn_smem_u32(bar);
-#pragma unroll 1
-    for (int i = 0; i < tries; ++i) {
-        uint32_t done;
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(done)
-                     : "r"(b), "r"(parity)
-                     : "memory");
-        if (done)
-            return true;
-        if (*abort)
-            break;
-    }
-    return false;
-}
-
 // One unit of work of a cluster: the rows (token, head) of tokens tok0 .. and
 // heads head0 .. head0 + GP - 1 against the key tiles first .. first + n_tiles - 1
 // of key head kv.
