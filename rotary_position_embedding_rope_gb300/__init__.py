@@ -747,6 +747,8 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     cache_lens: int32 [n_seqs] (not advanced by the call).
     pos: int32 [T] table rows (-1 = not rotated), or None for pos_offset + the
     key's index in its sequence.
+    Not differentiable: the pools carry no graph of k and v, and count as
+    written in place.
     """
     st = (_serving or _native()).cache_append(
         k, v, k_pages, v_pages, block_table, cu_seqlens, cache_lens, cos, sin, pos, pos_offset,
@@ -774,6 +776,9 @@ def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     a token's index among its sequence's queries (keys).
     workspace: None, or a uint8 tensor of rope_attention_packed_workspace(...)
     bytes to use (128-byte aligned; its contents do not matter).
+    stream: what the call runs on (None: the current stream); inputs have to be
+    ready there and to stay until it is done with them.
+    Forward only: the output carries no graph of the inputs.
     """
     o = (_serving or _native()).attention_packed(
         q, k, v, cu_seqlens_q, cos, sin, cu_seqlens_k, pos_q, pos_k, rotary_dim,
@@ -803,6 +808,7 @@ def attention_shared_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
     prefix_len + seq_lens - 1.
     workspace: None, or a uint8 tensor of rope_attention_decode_workspace(...)
     bytes to use (128-byte aligned; its contents do not matter).
+    stream: as attention_packed.  Forward only, as well.
     """
     o = (_serving or _native()).attention_shared_prefix(
         q, k_pages, v_pages, block_table, seq_lens, prefix_table, prefix_len, cos, sin, pos_q,

@@ -286,6 +286,14 @@ at::Tensor output(const Call &c, PyObject *given, const Rows &like, at::ScalarTy
     return t;
 }
 
+// Tells autograd that a tensor the caller holds has been written, as torch's own
+// in-place operations do: a graph that saved it then refuses to run backward.
+void written(const at::Tensor &t)
+{
+    if (!t.is_inference())                     // (these have no version)
+        t.unsafeGetTensorImpl()->bump_version();
+}
+
 void expect(Py_ssize_t got, Py_ssize_t want)
 {
     if (got != want)
@@ -342,10 +350,16 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n)
         const Tables t(c, a[7], a[8], a[11]);
         const int32_t *list = c.ints(a[4], "block_table", -1);
         const c10::cuda::CUDAGuard guard(c.device);
-        return status(unlocked(g_append, kr.p, vr.p, pool.k, pool.v, list, c.ints(a[5], "cu_seqlens", seqs + 1),
-                               c.ints(a[6], "cache_lens", seqs), t.cos, t.sin, c.ints(a[9], "pos", kr.n, true),
-                               integer(a[10]), seqs, kr.n, kr.stride, vr.stride, pool.Hk, pool.D, t.rotary_dim,
-                               (int32_t)integer(a[12]), pool.page, pool.n_pages, blocks, code, t.rows, c.stream));
+        const rope_status st =
+            unlocked(g_append, kr.p, vr.p, pool.k, pool.v, list, c.ints(a[5], "cu_seqlens", seqs + 1),
+                     c.ints(a[6], "cache_lens", seqs), t.cos, t.sin, c.ints(a[9], "pos", kr.n, true), integer(a[10]),
+                     seqs, kr.n, kr.stride, vr.stride, pool.Hk, pool.D, t.rotary_dim, (int32_t)integer(a[12]),
+                     pool.page, pool.n_pages, blocks, code, t.rows, c.stream);
+        if (st == ROPE_OK) {
+            written(tensor(a[2], "k_pages"));
+            written(tensor(a[3], "v_pages"));
+        }
+        return status(st);
     } catch (const PythonError &) {
         return nullptr;
     }
@@ -385,7 +399,11 @@ PyObject *attention_packed(PyObject *, PyObject *const *a, Py_ssize_t n)
             unlocked(g_packed, qr.p, kr.p, vr.p, out.data_ptr(), t.cos, t.sin, pq, pk, cuq, cuk, seqs, qr.n, kr.n, qr.stride,
                      kr.stride, vr.stride, qr.H, kr.H, qr.D, t.rotary_dim, layout, causal, scale, code, t.rows,
                      ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (int64_t)ws.nbytes() : 0, c.stream);
-        return st == ROPE_OK ? THPVariable_Wrap(out) : status(st);
+        if (st != ROPE_OK)
+            return status(st);
+        if (a[13] != Py_None)
+            written(out);
+        return THPVariable_Wrap(out);
     } catch (const PythonError &) {
         return nullptr;
     }
@@ -432,7 +450,11 @@ PyObject *attention_shared_prefix(PyObject *, PyObject *const *a, Py_ssize_t n)
                      qr.stride, qr.H, pool.Hk, qr.D, t.rotary_dim, layout, scale, pool.page, pool.n_pages, blocks,
                      code, t.rows, ws.defined() ? ws.data_ptr() : nullptr,
                      ws.defined() ? (int64_t)ws.nbytes() : 0, c.stream);
-        return st == ROPE_OK ? THPVariable_Wrap(out) : status(st);
+        if (st != ROPE_OK)
+            return status(st);
+        if (a[13] != Py_None)
+            written(out);
+        return THPVariable_Wrap(out);
     } catch (const PythonError &) {
         return nullptr;
     }
