@@ -23,7 +23,7 @@
 // from the suffixes' lengths how many clusters the prefix gets (plan_clusters);
 // those run 1, the SMs of the others run 2 beside them.  (As two launches the
 // parts ran one after the other, or the second kernel's last CTAs started behind
-// the first: 64 sequences, 8k prefix, 70 us against 55.)  When the batch has no
+// the first: 64 sequences, 8k prefix, 70 us, so 55 then and 53 now.)  When the batch has no
 // more than 16 rows per key head, the prefix is one more sequence of 2, with all
 // the rows of the batch, in a kernel of 2 alone.
 //
@@ -81,10 +81,10 @@ __host__ __device__ inline PrefixDeal prefix_deal(const PlanSizes &p, int32_t c)
 // Where one side is over long before the other, a little less of it is better
 // (the last term).  An estimate that is off costs balance, never a result.
 // Forced to c clusters, whole calls took (us):
-//   64 sequences, 8k prefix:    c = 8: 73   12: 60   16: 54.5  20: 57   76: 66
-//   256 sequences, 4k prefix:   c = 4: 337  8: 332   12: 335   20: 374  76: 378
-//   32 sequences, 128k prefix:  c = 60: 132 68: 121  71: 117   72: 119  76: 124
-//   48 sequences, 1k prefix, heads of 64:  c = 4: 47  8: 33  12: 34  20: 35
+//   64 sequences, 8k prefix:    c = 8: 72   12: 58   16: 52.5  20: 55   76: 64
+//   256 sequences, 4k prefix:   c = 4: 330  8: 332   12: 335   20: 375  76: 353
+//   32 sequences, 128k prefix:  c = 60: 128 68: 117  71: 113   72: 117  76: 118
+//   48 sequences, 1k prefix, heads of 64:  c = 4: 46  8: 31  12: 31.4  20: 33
 // where this picks 16, 12, 72 and 14.
 __host__ __device__ inline float plan_ns(const PlanSizes &p, int32_t c, float chunks)
 {
@@ -175,9 +175,9 @@ __device__ __forceinline__ int64_t query_row(const int32_t *pos_q, int32_t b, in
 // its stages and its softmax needs no barrier but the copies' own.  K and V
 // arrive by TMA (boxes of 64 features x the chunk's keys, or a page's where that
 // is less, 128-byte swizzle, so ldmatrix reads without conflicts), two stages a
-// warp, eight warps an SM: 128 KB in flight or in use.  Three stages are slower:
-// 256 sequences of 2080 keys on average (2.2 GB) 352 us, with two 326 (6.6 TB/s);
-// so are six or seven warps of three stages (342, 344).
+// warp, eight warps an SM: 128 KB in flight or in use.  Three stages were slower:
+// 256 sequences of 2080 keys on average without a prefix (2.2 GB) 352 us, with two
+// 326 (now 328, 6.6 TB/s); so were six or seven warps of three stages (342, 344).
 constexpr int kDecThreads = 32 * kDecWarps;
 template <int D>
 static constexpr int kDecStages = 2;
@@ -918,12 +918,12 @@ struct PrefixSource {
 // Bound by latency: a few dependent reads, then a row's parts, which are many when
 // few sequences hold many keys (one sequence, 8 key heads: 125).  With few rows W
 // warps share a row's parts and join theirs in shared memory.  Whole calls with W = 1 / 4 / 8
-// (us; heads of 128, 32 over 8): 1 sequence, 8k prefix 53.2 / 22.7 / 19.4; 4, 500
-// 18.3 / 14.4 / 13.6; 16, 2k 26.3 / 24.2 / 24.3; 32, 1k 24.3 / 23.4 / 25.1; 64,
-// 8k 54.3 / - / 59.7.  So the most warps that 4096 allow, of 8, 4 and 1.  Four
-// parts at a time, the first of them beside their statistics: 17.9, 11.8, 23.1,
-// 22.4 and 53.5; with eight the registers keep CTAs out, 16.5 but 12.3, 25.2,
-// 24.2.
+// (us; heads of 128, 32 over 8): 1 sequence, 8k prefix 39.2 / 22.3 / 19.5; 4, 500
+// 14.4 / 12.6 / 12.3; 16, 2k 29.7 / 27.5 / 27.5; 32, 1k 35.5 / 34.0 / 36.8; 64,
+// 8k 53.5 / 54.9 / 59.4.  So the most warps that 4096 allow, of 8, 4 and 1.  Four
+// parts at a time, the first of them beside their statistics; with eight the
+// registers keep CTAs out: 8 % less for the first of these, 4 to 9 % more for the
+// next three.
 constexpr int64_t kMergeWarps = 4096;
 template <typename T, int D, int W>
 __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_decode_merge_kernel(const __grid_constant__ DecodeArgs g)
