@@ -159,3 +159,33 @@ def test_host_staging_comes_from_the_copy_streams_memory():
             run().synchronize()
         assert got and set(got) == {s_in.cuda_stream}
     assert torch.equal(qo, want[0][0].cpu()) and torch.equal(ko, want[0][1].cpu()) and torch.equal(o, want[1][0].cpu())
+
+
+@pytest.mark.parametrize("call", [packed, decode, dense])
+def test_a_captured_call_on_a_forked_stream(call):
+    """A graph whose call runs on a second stream, forked from and joined with the captured one; replayed on new data, with
+    eager calls of the same sizes between the replays."""
+    require_gpu()
+    R = lib()
+    make = dense_inputs if call is dense else serving_inputs
+    one = lambda o: o[0] if isinstance(o, tuple) else o
+    t, new = make(3), make(4)
+    want, want_new = one(call(R, t)), one(call(R, new))
+    torch.cuda.synchronize()
+    main, side, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        out = one(call(R, t, stream=side))
+        main.wait_stream(side)
+        twice = out * 2                                    # what follows on the captured stream
+    for _ in range(2):
+        graph.replay()
+        other = one(call(R, new))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(twice, want * 2) and torch.equal(other, want_new)
+    for n in t:
+        t[n].copy_(new[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want_new) and torch.equal(twice, want_new * 2)
+    assert R.rope_check_errors() == R.ROPE_OK
