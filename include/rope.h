@@ -64,6 +64,13 @@ typedef enum {
 } rope_mask_kind;
 /* frequency modes ("rotary-embedding-torch", RotaryEmbedding: freqs_for) */
 typedef enum { ROPE_FREQ_LANG = 0, ROPE_FREQ_PIXEL = 1, ROPE_FREQ_CONSTANT = 2 } rope_freq_mode;
+/* rules for contexts longer than those trained on (rope_tables_build_scaled) */
+typedef enum {
+    ROPE_SCALE_LINEAR = 0,     /* every frequency over the factor                 */
+    ROPE_SCALE_NTK = 1,        /* a larger base                                   */
+    ROPE_SCALE_SMOOTH = 2,     /* low frequencies over the factor, high ones kept */
+    ROPE_SCALE_YARN = 3        /* the same along the pairs, values scaled         */
+} rope_scale_kind;
 
 /*
  * rope_tables_build -- fill the cos/sin table.
@@ -205,6 +212,102 @@ rope_status rope_apply_q(void *x, const float *cos, const float *sin, const int3
                          int64_t B, int32_t H, int64_t S, int32_t D, int32_t rotary_dim,
                          int32_t layout, int32_t seq_before_head, int32_t backward, int32_t dtype,
                          int64_t table_rows, void *stream);
+
+/*
+ * rope_tables_build_scaled -- the cos/sin table for a context longer than the
+ * one a model was trained on, by one of the published rules.
+ *
+ * With w_i = theta^(-2i / rotary_dim), f = factor and n_i = original_positions *
+ * w_i / 2 pi (turns that pair i makes over the trained context), pair i turns by
+ *     LINEAR   w_i / f
+ *     NTK      (theta * f^(rotary_dim / (rotary_dim - 2)))^(-2i / rotary_dim)
+ *     SMOOTH   (1 - m) w_i / f + m w_i,  m = clamp((n_i - low_turns) /
+ *              (high_turns - low_turns), 0, 1)
+ *     YARN     r w_i / f + (1 - r) w_i,  r = clamp((i - a) / (b - a), 0, 1), a
+ *              = max(floor(j(high_turns)), 0), b = min(ceil(j(low_turns)),
+ *              rotary_dim - 1), j(n) = rotary_dim ln(original_positions / 2 pi
+ *              n) / (2 ln theta) the pair that makes n turns (b - a = 0.001
+ *              where b <= a)
+ * a position; row m stands for the position pos_offset + m.  Values are multiplied
+ * by value_scale, or, when that is 0, by 1 (YARN: 0.1 ln f + 1).
+ *
+ * cos_out, sin_out: device, caller-owned, float[rows * rotary_dim/2] each.
+ * Accuracy: frequencies in 64 bits on the host, phases as 64-bit fractions of a
+ *   turn (p 2^-65 turns off at position p), values within 5 * 2^-24 of
+ *   themselves besides.
+ * Errors: ROPE_ERR_UNSUPPORTED for an unknown kind or rotary_dim > 512;
+ *   ROPE_ERR_INVALID_ARG if rotary_dim < 2 or odd (NTK: or 2), rows or
+ *   pos_offset < 0 or their sum past 2^31 - 1, theta <= 1, factor < 1,
+ *   value_scale < 0 (or any of them not finite), and for SMOOTH and YARN
+ *   original_positions < 1, low_turns <= 0 or high_turns <= low_turns; null or
+ *   overlapping outputs.  rows = 0 is a no-op.  ROPE_ERR_CUDA if the launch fails.
+ */
+rope_status rope_tables_build_scaled(int32_t kind, double theta, int32_t rotary_dim, int64_t rows,
+                                     int64_t pos_offset, double factor, int64_t original_positions,
+                                     double low_turns, double high_turns, double value_scale,
+                                     float *cos_out, float *sin_out, void *stream);
+
+/*
+ * rope_norm_qk_fwd -- the RMS norm of every query and key head with the
+ * rotation in the same pass, out of place (or in place).
+ *
+ *   n = x / sqrt(mean(x^2) + eps),  y = R(t) (w * n)
+ *
+ * q, k: device, B sequences of S tokens of Hq (Hk) heads of D features; the
+ *    strides of batch, token and head, in elements, stand in q_strides and
+ *    k_strides (host arrays of 3, or NULL: dense, [B, H, S, D] or with
+ *    seq_before_head [B, S, H, D]); features are dense.  Strides of sizes of
+ *    one are not looked at.  Either may be missing (NULL, with 0 heads).
+ * q_out, k_out: device, dense, in the order that seq_before_head says.  They
+ *    may be q and k themselves where those are dense.
+ * wq, wk: device [D], of weight_dtype (ROPE_F32 or dtype), or NULL (ones).
+ * pos_idx: device int32 [S] (pos_batch_stride 0) or one row per sequence,
+ *    pos_batch_stride entries apart, or NULL (row = index in the sequence).  -1: the norm
+ *    alone; other rows outside the table: the norm alone, and the flag is raised.
+ * D, rotary_dim: multiples of 16, 16 <= rotary_dim <= D <= 256; features past
+ *    rotary_dim are normalised and weighted too.  dtype: ROPE_F32, ROPE_BF16 or
+ *    ROPE_F16.  eps: >= 0, finite.
+ * Arithmetic: fp32 throughout, one rounding to dtype at the end.
+ * Errors: ROPE_ERR_UNSUPPORTED for other types, layouts, D, rotary_dim, strides
+ *    that are not whole 16-byte vectors or pointers not 16-byte aligned;
+ *    ROPE_ERR_INVALID_ARG for bad sizes (B * S above 2^31 - 1, negative or zero
+ *    strides, a pos_batch_stride below S), null pointers, an output overlapping
+ *    another argument; ROPE_ERR_CUDA if the launch fails.
+ */
+rope_status rope_norm_qk_fwd(const void *q, const void *k, void *q_out, void *k_out, const void *wq,
+                             const void *wk, const float *cos, const float *sin,
+                             const int32_t *pos_idx, int64_t pos_batch_stride, int64_t B, int32_t Hq,
+                             int32_t Hk, int64_t S, int32_t D, const int64_t *q_strides,
+                             const int64_t *k_strides, int32_t rotary_dim, int32_t layout,
+                             int32_t seq_before_head, float eps, int32_t dtype, int32_t weight_dtype,
+                             int64_t table_rows, void *stream);
+
+/*
+ * rope_norm_qk_bwd -- gradients of rope_norm_qk_fwd.  With r = 1 / sqrt(mean(x^2)
+ * + eps), n = r x and g = R(-t) dy,
+ *   dx = r (w * g - n mean(w * g * n)),   dw = sum over rows of g * n.
+ * gq, gk: gradients of the outputs; dq, dk: gradients of q and k, written: all
+ *    device, dense, in the outputs' order.  q, k: the forward call's inputs.
+ * dwq, dwk: device [D], of weight_dtype, written, or NULL (not wanted).
+ * workspace: device, 16-byte aligned, rope_norm_qk_workspace(D) bytes (NULL where
+ *    neither dwq nor dwk is given); overwritten.
+ * Without tokens dwq and dwk are zeros.  Sums are fp32 in an order that the sizes
+ *    alone give: the same call gives the same bits.
+ * Everything else, and errors: as rope_norm_qk_fwd; an output may overlap no
+ *    other argument.
+ */
+rope_status rope_norm_qk_bwd(const void *q, const void *k, const void *gq, const void *gk, void *dq,
+                             void *dk, const void *wq, const void *wk, void *dwq, void *dwk,
+                             const float *cos, const float *sin, const int32_t *pos_idx,
+                             int64_t pos_batch_stride, int64_t B, int32_t Hq, int32_t Hk, int64_t S,
+                             int32_t D, const int64_t *q_strides, const int64_t *k_strides,
+                             int32_t rotary_dim, int32_t layout, int32_t seq_before_head, float eps,
+                             int32_t dtype, int32_t weight_dtype, int64_t table_rows, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+
+/* rope_norm_qk_workspace -- bytes of workspace of rope_norm_qk_bwd (-1 for a D
+ * that it does not take). */
+int64_t rope_norm_qk_workspace(int32_t D);
 
 /*
  * rope_attention_fwd -- attention forward with the rotation fused into the
@@ -398,6 +501,29 @@ rope_status rope_cache_append(const void *k, const void *v, void *k_pages, void 
                               int32_t D, int32_t rotary_dim, int32_t layout, int32_t page_size,
                               int64_t n_pages, int64_t max_blocks, int32_t dtype,
                               int64_t table_rows, void *stream);
+
+/*
+ * rope_norm_cache_append -- rope_cache_append for a model that normalises
+ * queries and keys: the new tokens' queries, normalised and rotated, into a dense
+ * tensor, their keys, normalised and rotated, and values into the pages.
+ *
+ * q: device [total, Hq, D], token stride q_stride; q_out: device [total, Hq, D],
+ *    dense, written for tokens of the sequences; it may be q itself where that is
+ *    dense.  A token's query is rotated with the table row of its key.
+ * wq, wk, eps, weight_dtype: as rope_norm_qk_fwd.  Hq or Hk may be 0.
+ * Everything else, and errors: as rope_cache_append.  A token whose page is bad has
+ *    its query written and its key and value not.
+ */
+rope_status rope_norm_cache_append(const void *q, const void *k, const void *v, void *q_out,
+                                   void *k_pages, void *v_pages, const void *wq, const void *wk,
+                                   const int32_t *block_table, const int32_t *cu_seqlens,
+                                   const int32_t *cache_lens, const float *cos, const float *sin,
+                                   const int32_t *pos, int64_t pos_offset, int64_t n_seqs,
+                                   int64_t total, int64_t q_stride, int64_t k_stride,
+                                   int64_t v_stride, int32_t Hq, int32_t Hk, int32_t D,
+                                   int32_t rotary_dim, int32_t layout, float eps, int32_t page_size,
+                                   int64_t n_pages, int64_t max_blocks, int32_t dtype,
+                                   int32_t weight_dtype, int64_t table_rows, void *stream);
 
 /*
  * rope_attention_packed_fwd -- attention with rotary Q/K over packed

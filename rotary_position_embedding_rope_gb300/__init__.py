@@ -23,6 +23,10 @@ workspace, keys rotated once beforehand).
 ``attention_packed`` attends over packed prompts of different lengths and
 ``attention_shared_prefix`` runs one new token per sequence over a prefix all
 sequences share and each one's own pages.
+``norm_rotate_qk`` normalises query and key heads (RMS norm) and rotates them in the same
+pass (``norm_rotate_qk_backward`` and ``autograd.norm_rotary_qk`` give the gradients),
+``norm_cache_append`` does it on the way into the paged cache.
+``build_tables_scaled`` builds the tables of contexts longer than those trained on.
 ``host.HostRotator`` and ``host.HostAttention`` run the rotation and the
 attention on tensors that live in pinned host memory, overlapping the copies
 with the calls.
@@ -43,7 +47,8 @@ __all__ = [
     "VARIANT_ELEMENTWISE", "VARIANT_VECTOR",
     "ROPE_SPLIT_HALF", "ROPE_INTERLEAVED", "ROPE_F32", "ROPE_BF16", "ROPE_F16", "ROPE_FREQ_LANG",
     "ROPE_FREQ_PIXEL", "ROPE_FREQ_CONSTANT", "ROPE_MASK_NONE", "ROPE_MASK_KEYS",
-    "ROPE_MASK_QUERY_KEYS", "library_path", "load_library",
+    "ROPE_MASK_QUERY_KEYS", "ROPE_SCALE_LINEAR", "ROPE_SCALE_NTK", "ROPE_SCALE_SMOOTH",
+    "ROPE_SCALE_YARN", "library_path", "load_library",
     # the C ABI, same names
     "rope_tables_build", "rope_tables_build_ex", "rope_apply_qk", "rope_apply_q",
     "rope_apply_qk_out", "rope_attention_fwd", "rope_attention_fwd_masked",
@@ -52,10 +57,13 @@ __all__ = [
     "rope_tune_rotation_launch", "rope_cache_append",
     "rope_attention_packed_fwd", "rope_attention_packed_workspace",
     "rope_attention_decode_fwd", "rope_attention_decode_workspace",
+    "rope_tables_build_scaled", "rope_norm_qk_fwd", "rope_norm_qk_bwd", "rope_norm_qk_workspace",
+    "rope_norm_cache_append",
     # conveniences
     "build_tables", "build_tables_ex", "apply_qk", "apply_q", "apply_qk_xpos", "rotate_qk",
     "attention", "attention_workspace", "PreparedApply", "cache_append",
-    "attention_packed", "attention_shared_prefix",
+    "attention_packed", "attention_shared_prefix", "build_tables_scaled", "norm_rotate_qk",
+    "norm_rotate_qk_backward", "norm_cache_append",
 ]
 
 (ROPE_OK, ROPE_ERR_INVALID_ARG, ROPE_ERR_UNSUPPORTED, ROPE_ERR_CUDA, ROPE_ERR_POS_OUT_OF_RANGE,
@@ -65,7 +73,9 @@ ROPE_SPLIT_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_F32, ROPE_BF16, ROPE_F16 = 0, 1, 2
 ROPE_FREQ_LANG, ROPE_FREQ_PIXEL, ROPE_FREQ_CONSTANT = 0, 1, 2
 ROPE_MASK_NONE, ROPE_MASK_KEYS, ROPE_MASK_QUERY_KEYS = 0, 1, 2
+ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_SMOOTH, ROPE_SCALE_YARN = range(4)
 _FREQ_CODE = {"lang": ROPE_FREQ_LANG, "pixel": ROPE_FREQ_PIXEL, "constant": ROPE_FREQ_CONSTANT}
+_SCALE_CODE = {"linear": ROPE_SCALE_LINEAR, "ntk": ROPE_SCALE_NTK, "smooth": ROPE_SCALE_SMOOTH, "yarn": ROPE_SCALE_YARN}
 _DTYPE_CODE = {torch.float32: ROPE_F32, torch.bfloat16: ROPE_BF16, torch.float16: ROPE_F16}
 _LAYOUT_CODE = {"split_half": ROPE_SPLIT_HALF, "interleaved": ROPE_INTERLEAVED}
 
@@ -161,6 +171,22 @@ def load_library() -> ctypes.CDLL:
     lib.rope_attention_decode_fwd.restype = c.c_int
     lib.rope_attention_decode_workspace.argtypes = [c.c_int64] + [c.c_int32] * 4 + [c.c_int64] * 2
     lib.rope_attention_decode_workspace.restype = c.c_int64
+    lib.rope_tables_build_scaled.argtypes = [c.c_int32, c.c_double, c.c_int32, c.c_int64, c.c_int64, c.c_double,
+                                             c.c_int64, c.c_double, c.c_double, c.c_double, P, P, P]
+    lib.rope_tables_build_scaled.restype = c.c_int
+    lib.rope_norm_qk_fwd.argtypes = [P] * 9 + [c.c_int64, c.c_int64, c.c_int32, c.c_int32, c.c_int64, c.c_int32, P, P,
+                                               c.c_int32, c.c_int32, c.c_int32, c.c_float, c.c_int32, c.c_int32,
+                                               c.c_int64, P]
+    lib.rope_norm_qk_fwd.restype = c.c_int
+    lib.rope_norm_qk_bwd.argtypes = [P] * 13 + [c.c_int64, c.c_int64, c.c_int32, c.c_int32, c.c_int64, c.c_int32, P, P,
+                                                c.c_int32, c.c_int32, c.c_int32, c.c_float, c.c_int32, c.c_int32,
+                                                c.c_int64, P, c.c_int64, P]
+    lib.rope_norm_qk_bwd.restype = c.c_int
+    lib.rope_norm_qk_workspace.argtypes = [c.c_int32]
+    lib.rope_norm_qk_workspace.restype = c.c_int64
+    lib.rope_norm_cache_append.argtypes = [P] * 14 + [c.c_int64] * 6 + [c.c_int32] * 5 + \
+        [c.c_float, c.c_int32, c.c_int64, c.c_int64, c.c_int32, c.c_int32, c.c_int64, P]
+    lib.rope_norm_cache_append.restype = c.c_int
     _lib = lib
     return lib
 
@@ -351,6 +377,45 @@ def build_tables_ex(freqs_for: str, rotary_dim: int, rows: int, theta: float = 1
     rope_tables_build_ex(_FREQ_CODE[freqs_for], theta, max_freq, rotary_dim, rows, pos_offset,
                          pos_divisor, xpos_sign, xpos_scale_base, xpos_gamma, xpos_center, cos,
                          sin, stream)
+    return cos, sin
+
+
+def rope_tables_build_scaled(kind, theta, rotary_dim, rows, pos_offset, factor, original_positions, low_turns,
+                             high_turns, value_scale, cos_out, sin_out, stream=None):
+    lib = load_library()
+    for t, n in ((cos_out, "cos_out"), (sin_out, "sin_out")):
+        if isinstance(t, torch.Tensor) and (t.dtype != torch.float32 or
+                                            t.numel() < rows * (rotary_dim // 2)):
+            raise ValueError("%s must be float32 with at least rows*rotary_dim/2 elements" % n)
+    st = lib.rope_tables_build_scaled(int(kind), float(theta), int(rotary_dim), int(rows), int(pos_offset),
+                                      float(factor), int(original_positions), float(low_turns),
+                                      float(high_turns), float(value_scale), _addr(cos_out, "cos_out"),
+                                      _addr(sin_out, "sin_out"), _stream(stream))
+    _check(st, "rope_tables_build_scaled")
+
+
+def build_tables_scaled(kind: str, rotary_dim: int, rows: int, factor: float, original_positions: int = 0,
+                        theta: float = 10000.0, pos_offset: int = 0, low_turns: float | None = None,
+                        high_turns: float | None = None, value_scale: float | None = None, device=None,
+                        stream=None):
+    """Allocate and fill fp32 cos/sin tables [rows, rotary_dim // 2] for a context ``factor``
+    times the ``original_positions`` a model was trained on; row m stands for position
+    pos_offset + m.
+
+    kind: "linear" (positions divided by the factor), "ntk" (a larger base), "smooth"
+    (pairs that make fewer than low_turns = 1 turns over the trained context are slowed
+    by the factor, those of more than high_turns = 4 kept, a ramp between) or "yarn" (the
+    ramp along the pairs, between those of low_turns = 1 and high_turns = 32 turns).
+    value_scale: factor of all values; None: 1, for "yarn" 0.1 ln(factor) + 1.
+    """
+    device = torch.device("cuda") if device is None else torch.device(device)
+    low = 1.0 if low_turns is None else low_turns
+    high = (32.0 if kind == "yarn" else 4.0) if high_turns is None else high_turns
+    code = _SCALE_CODE[kind]
+    cos, sin = _allocated(lambda: torch.empty((2, rows, rotary_dim // 2), dtype=torch.float32,
+                                              device=device).unbind(0), stream, device)
+    rope_tables_build_scaled(code, theta, rotary_dim, rows, pos_offset, factor, original_positions, low, high,
+                             0.0 if value_scale is None else value_scale, cos, sin, stream)
     return cos, sin
 
 
@@ -711,7 +776,7 @@ _serving = None
 
 
 def _native():
-    """The binding module of the serving calls (csrc/serving_binding.cpp), given
+    """The binding module of the serving and norm calls (csrc/serving_binding.cpp), given
     the entry points of the library that is loaded."""
     global _serving
     if _serving is None:
@@ -727,7 +792,9 @@ def _native():
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.rope_cache_append, lib.rope_attention_packed_fwd,
             lib.rope_attention_packed_workspace, lib.rope_attention_decode_fwd,
-            lib.rope_attention_decode_workspace)))
+            lib.rope_attention_decode_workspace, lib.rope_norm_qk_fwd, lib.rope_norm_qk_bwd,
+            lib.rope_norm_qk_workspace, lib.rope_norm_cache_append,
+            lib.rope_tables_build_scaled)))
         _serving = module
     return _serving
 
@@ -755,6 +822,30 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
         rotary_dim, _LAYOUT_CODE[layout], stream)
     if st != ROPE_OK:
         raise RopeError(st, "rope_cache_append")
+
+
+def norm_cache_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, wq: torch.Tensor | None,
+                      wk: torch.Tensor | None, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                      block_table: torch.Tensor, cu_seqlens: torch.Tensor, cache_lens: torch.Tensor,
+                      cos: torch.Tensor, sin: torch.Tensor, eps: float = 1e-6,
+                      pos: torch.Tensor | None = None, pos_offset: int = 0, rotary_dim: int | None = None,
+                      layout: str = "split_half", q_out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """cache_append of a model that normalises queries and keys (norm_rotate_qk): new keys,
+    normalised and rotated, and values into the pages; returns the queries, normalised and
+    rotated, [T, Hq, D] (rows of tokens of no sequence are not written).
+
+    q: [T, Hq, D], the new tokens' queries (a view with a token stride is taken as it is);
+    wq, wk: [D] weights in fp32 or q's type, or None.  q_out: the output, which may be q
+    itself where that is dense.  Everything else as cache_append; attention_paged takes the
+    result without cos and sin.
+    """
+    o = (_serving or _native()).norm_cache_append(
+        q, k, v, wq, wk, k_pages, v_pages, block_table, cu_seqlens, cache_lens, cos, sin, eps, pos, pos_offset,
+        rotary_dim, _LAYOUT_CODE[layout], q_out, stream)
+    if type(o) is int:
+        raise RopeError(o, "rope_norm_cache_append")
+    return o
 
 
 def attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -815,4 +906,94 @@ def attention_shared_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
         rotary_dim, _LAYOUT_CODE[layout], scale, out, workspace, stream)
     if type(o) is int:
         raise RopeError(o, "rope_attention_decode_fwd")
+    return o
+
+
+# --------------------------------------------------------------------------
+# normalised queries and keys
+# --------------------------------------------------------------------------
+def rope_norm_qk_fwd(q, k, q_out, k_out, wq, wk, cos, sin, pos_idx, pos_batch_stride, B, Hq, Hk, S, D, q_strides,
+                     k_strides, rotary_dim, layout, seq_before_head, eps, dtype, weight_dtype, table_rows, stream=None):
+    """q_strides, k_strides: three integers (batch, token, head), or None for dense; q and k of
+    other strides are given as addresses."""
+    st = load_library().rope_norm_qk_fwd(
+        _addr(q, "q"), _addr(k, "k"), _addr(q_out, "q_out"), _addr(k_out, "k_out"), _addr(wq, "wq"), _addr(wk, "wk"),
+        _addr(cos, "cos"), _addr(sin, "sin"), _addr(pos_idx, "pos_idx"), int(pos_batch_stride), int(B), int(Hq),
+        int(Hk), int(S), int(D), _strides3(q_strides), _strides3(k_strides), int(rotary_dim), int(layout),
+        int(seq_before_head), float(eps), int(dtype), int(weight_dtype), int(table_rows), _stream(stream))
+    _check(st, "rope_norm_qk_fwd")
+
+
+def rope_norm_qk_bwd(q, k, gq, gk, dq, dk, wq, wk, dwq, dwk, cos, sin, pos_idx, pos_batch_stride, B, Hq, Hk, S, D,
+                     q_strides, k_strides, rotary_dim, layout, seq_before_head, eps, dtype, weight_dtype, table_rows,
+                     workspace, workspace_bytes, stream=None):
+    st = load_library().rope_norm_qk_bwd(
+        _addr(q, "q"), _addr(k, "k"), _addr(gq, "gq"), _addr(gk, "gk"), _addr(dq, "dq"), _addr(dk, "dk"),
+        _addr(wq, "wq"), _addr(wk, "wk"), _addr(dwq, "dwq"), _addr(dwk, "dwk"), _addr(cos, "cos"), _addr(sin, "sin"),
+        _addr(pos_idx, "pos_idx"), int(pos_batch_stride), int(B), int(Hq), int(Hk), int(S), int(D),
+        _strides3(q_strides), _strides3(k_strides), int(rotary_dim), int(layout), int(seq_before_head), float(eps),
+        int(dtype), int(weight_dtype), int(table_rows), _addr(workspace, "workspace"), int(workspace_bytes),
+        _stream(stream))
+    _check(st, "rope_norm_qk_bwd")
+
+
+def _strides3(s):
+    return None if s is None else (ctypes.c_int64 * 3)(*s)
+
+
+def rope_norm_qk_workspace(D) -> int:
+    """Bytes of workspace (-1 for a D the call does not take)."""
+    return load_library().rope_norm_qk_workspace(int(D))
+
+
+def rope_norm_cache_append(q, k, v, q_out, k_pages, v_pages, wq, wk, block_table, cu_seqlens, cache_lens, cos, sin, pos,
+                           pos_offset, n_seqs, total, q_stride, k_stride, v_stride, Hq, Hk, D, rotary_dim, layout, eps,
+                           page_size, n_pages, max_blocks, dtype, weight_dtype, table_rows, stream=None):
+    st = load_library().rope_norm_cache_append(
+        _addr(q, "q"), _addr(k, "k"), _addr(v, "v"), _addr(q_out, "q_out"), _addr(k_pages, "k_pages"),
+        _addr(v_pages, "v_pages"), _addr(wq, "wq"), _addr(wk, "wk"), _addr(block_table, "block_table"),
+        _addr(cu_seqlens, "cu_seqlens"), _addr(cache_lens, "cache_lens"), _addr(cos, "cos"), _addr(sin, "sin"),
+        _addr(pos, "pos"), int(pos_offset), int(n_seqs), int(total), int(q_stride), int(k_stride), int(v_stride), int(Hq),
+        int(Hk), int(D), int(rotary_dim), int(layout), float(eps), int(page_size), int(n_pages), int(max_blocks),
+        int(dtype), int(weight_dtype), int(table_rows), _stream(stream))
+    _check(st, "rope_norm_cache_append")
+
+
+def norm_rotate_qk(q: torch.Tensor | None, k: torch.Tensor | None, wq: torch.Tensor | None,
+                   wk: torch.Tensor | None, cos: torch.Tensor, sin: torch.Tensor, eps: float = 1e-6,
+                   pos_idx: torch.Tensor | None = None, rotary_dim: int | None = None,
+                   layout: str = "split_half", seq_before_head: bool = False,
+                   q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """The RMS norm of every query and key head and the rotation, in one pass:
+    y = R(t) (w * x / sqrt(mean(x^2) + eps)).  Returns (q_out, k_out), dense.
+
+    q: [B, Hq, S, D] (or [B, S, Hq, D] with seq_before_head), k likewise with Hk heads, or
+    either None; bf16, fp16 or fp32; views are taken as they are as long as features are
+    dense and strides whole 16-byte vectors (a part of a fused projection's output).
+    wq, wk: [D] weights of all query (key) heads, fp32 or the rows' type, or None (ones).
+    cos/sin: float32 [rows, rotary_dim // 2].  pos_idx: int32 [S] or [B, S] table rows (-1 =
+    normalised, not rotated), or None.  q_out=q (k_out=k) works in place on a dense tensor.
+    Carries no graph: ``autograd.norm_rotary_qk`` is the differentiable form.
+    """
+    o = (_serving or _native()).norm_rotate_qk(q, k, wq, wk, cos, sin, eps, pos_idx, rotary_dim,
+                                               _LAYOUT_CODE[layout], seq_before_head, q_out, k_out, stream)
+    if type(o) is int:
+        raise RopeError(o, "rope_norm_qk_fwd")
+    return o
+
+
+def norm_rotate_qk_backward(gq: torch.Tensor | None, gk: torch.Tensor | None, q: torch.Tensor | None,
+                            k: torch.Tensor | None, wq: torch.Tensor | None, wk: torch.Tensor | None,
+                            cos: torch.Tensor, sin: torch.Tensor, eps: float = 1e-6,
+                            pos_idx: torch.Tensor | None = None, rotary_dim: int | None = None,
+                            layout: str = "split_half", seq_before_head: bool = False,
+                            weight_grads: tuple[bool, bool] = (True, True), stream=None):
+    """Gradients of norm_rotate_qk: (dq, dk, dwq, dwk), dense, None for what is not given or
+    not wanted.  gq, gk: gradients of the outputs, dense; q, k and the rest: what the
+    forward call was given."""
+    o = (_serving or _native()).norm_rotate_qk_backward(
+        gq, gk, q, k, wq, wk, cos, sin, eps, pos_idx, rotary_dim, _LAYOUT_CODE[layout], seq_before_head,
+        weight_grads[0], weight_grads[1], stream)
+    if type(o) is int:
+        raise RopeError(o, "rope_norm_qk_bwd")
     return o

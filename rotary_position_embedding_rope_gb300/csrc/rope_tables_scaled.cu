@@ -1,0 +1,184 @@
+// rope_tables_scaled.cu -- cos/sin tables of contexts longer than those a
+// model was trained on (rope_tables_build_scaled).
+//
+// Every rule gives pair i a frequency w_i; the table holds cos and sin of p w_i
+// for the integer positions p = pos_offset + row.  In turns, p w_i / 2 pi modulo 1
+// is all that matters, so the frequency is kept as a fixed-point fraction of a
+// turn, F_i = round(w_i / 2 pi * 2^64), and the phase is p * F_i modulo 2^64: one
+// 64-bit integer product is the whole range reduction, exact but for F_i's own
+// rounding (p 2^-65 turns: 4e-11 radians at a position of 10^8).  The nearest
+// quarter turn comes off the top two bits, and what is left, at most an eighth of
+// a turn either way, goes to fp32 (relative 2^-24, at most 2.4e-8 of a radian) and
+// to sincospif.  The frequencies are computed on the host in 64 bits and go along as
+// kernel arguments: 64 pow in every CTA would cost more than the table.
+//
+// What bounds it: 8 bytes a pair against some 50 instructions, at 64 pairs a
+// row about even: 131072 rows of 64 pairs write 67 MB.  Angles and sincos in 64
+// bits (rope_tables_build_ex) would be some 100 64-bit operations a pair, of
+// which this GPU does a 64th of its 32-bit ones.
+//
+// A thread owns four pairs of a row (two 16-byte stores) and keeps their F in
+// registers while it walks down the rows.
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "rope.h"
+#include "rope_checks.h"
+#include "rope_kernels.cuh"
+
+namespace rope {
+namespace {
+
+constexpr int kScaledPairs = 256;              // pairs of a row at most
+constexpr int kScaledThreads = 256;
+
+struct ScaledArgs {
+    uint64_t freq[kScaledPairs];               // fractions of a turn, times 2^64
+    float *cos, *sin;
+    int64_t rows;
+    uint64_t first;                            // position of row 0
+    int32_t h;
+    float scale;
+};
+
+__device__ __forceinline__ void phase_cos_sin(uint64_t phase, float scale, float &c, float &s)
+{
+    const uint64_t quarter = (phase + (1ull << 61)) >> 62;
+    const int64_t rest = (int64_t)(phase - (quarter << 62));
+    float a, b;
+    sincospif(__ll2float_rn(rest) * 0x1p-63f, &b, &a);     // half turns
+    // (cos, sin) of rest + quarter * pi / 2
+    const bool swap = quarter & 1;
+    const float x = swap ? b : a, y = swap ? a : b;
+    c = (quarter == 1 || quarter == 2 ? -x : x) * scale;
+    s = (quarter >= 2 ? -y : y) * scale;
+}
+
+// V: pairs of a thread, 4 where rows are whole 16-byte vectors, else 1.
+template <int V>
+__global__ void __launch_bounds__(kScaledThreads) rope_tables_scaled_kernel(const __grid_constant__ ScaledArgs a)
+{
+    const int32_t per_row = a.h / V;           // threads of a row
+    const int64_t threads = (int64_t)gridDim.x * kScaledThreads;
+    const int64_t at = (int64_t)blockIdx.x * kScaledThreads + threadIdx.x;
+    int64_t row = at / per_row;
+    const int32_t col = (int32_t)(at - row * per_row) * V;
+    const int64_t step = threads / per_row;    // rows the grid takes at once
+    if (row >= step)
+        return;                                // the grid's last threads, less than a row of them
+    uint64_t f[V], phase[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        f[i] = a.freq[col + i];
+        phase[i] = f[i] * (a.first + (uint64_t)row);
+        f[i] *= (uint64_t)step;
+    }
+    pdl_wait();
+    pdl_trigger();
+    for (; row < a.rows; row += step) {
+        float c[V], s[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            phase_cos_sin(phase[i], a.scale, c[i], s[i]);
+            phase[i] += f[i];
+        }
+        if constexpr (V == 4) {
+            *reinterpret_cast<float4 *>(a.cos + row * a.h + col) = make_float4(c[0], c[1], c[2], c[3]);
+            *reinterpret_cast<float4 *>(a.sin + row * a.h + col) = make_float4(s[0], s[1], s[2], s[3]);
+        } else {
+            a.cos[row * a.h + col] = c[0];
+            a.sin[row * a.h + col] = s[0];
+        }
+    }
+}
+
+// w_i of every pair, radians per position; the factor of all values.
+void scaled_frequencies(int32_t kind, double theta, int32_t rd, double factor, int64_t original, double low, double high,
+                        double *w, double *scale)
+{
+    const double pi = 3.14159265358979323846;
+    const int32_t h = rd / 2;
+    double ramp0 = 0.0, ramp1 = 0.0;
+    *scale = 1.0;
+    if (kind == ROPE_SCALE_YARN) {
+        // the pair that makes r turns over the trained context
+        auto pair_of = [&](double r) { return rd * std::log((double)original / (r * 2.0 * pi)) / (2.0 * std::log(theta)); };
+        ramp0 = std::fmax(std::floor(pair_of(high)), 0.0);
+        ramp1 = std::fmin(std::ceil(pair_of(low)), (double)rd - 1.0);
+        if (factor > 1.0)
+            *scale = 0.1 * std::log(factor) + 1.0;
+    }
+    for (int32_t i = 0; i < h; ++i) {
+        const double base = kind == ROPE_SCALE_NTK ? theta * std::pow(factor, (double)rd / (double)(rd - 2)) : theta;
+        double x = std::pow(base, -2.0 * (double)i / (double)rd);
+        if (kind == ROPE_SCALE_LINEAR) {
+            x /= factor;
+        } else if (kind == ROPE_SCALE_SMOOTH) {
+            const double turns = (double)original * x / (2.0 * pi);
+            const double mix = std::fmin(std::fmax((turns - low) / (high - low), 0.0), 1.0);
+            x = (1.0 - mix) * x / factor + mix * x;
+        } else if (kind == ROPE_SCALE_YARN) {
+            const double span = ramp1 > ramp0 ? ramp1 - ramp0 : 0.001;
+            const double mix = std::fmin(std::fmax(((double)i - ramp0) / span, 0.0), 1.0);
+            x = x / factor * mix + x * (1.0 - mix);
+        }
+        w[i] = x;
+    }
+}
+
+}  // namespace
+}  // namespace rope
+
+using namespace rope;
+
+extern "C" rope_status rope_tables_build_scaled(int32_t kind, double theta, int32_t rotary_dim, int64_t rows,
+                                                int64_t pos_offset, double factor, int64_t original_positions,
+                                                double low_turns, double high_turns, double value_scale,
+                                                float *cos_out, float *sin_out, void *stream)
+{
+    if (kind != ROPE_SCALE_LINEAR && kind != ROPE_SCALE_NTK && kind != ROPE_SCALE_SMOOTH && kind != ROPE_SCALE_YARN)
+        return ROPE_ERR_UNSUPPORTED;
+    if (rotary_dim > 2 * kScaledPairs)
+        return ROPE_ERR_UNSUPPORTED;
+    if (rotary_dim < 2 || (rotary_dim & 1) || (kind == ROPE_SCALE_NTK && rotary_dim == 2) || rows < 0 || pos_offset < 0 ||
+        pos_offset > kMaxInt32 || rows > kMaxInt32 - pos_offset)
+        return ROPE_ERR_INVALID_ARG;
+    // (below 1 a frequency may pass a turn a position, which the fraction does not hold)
+    if (!(theta > 1.0) || !std::isfinite(theta) || !(factor >= 1.0) || !std::isfinite(factor) || !std::isfinite(value_scale) ||
+        value_scale < 0.0)
+        return ROPE_ERR_INVALID_ARG;
+    const bool turns = kind == ROPE_SCALE_SMOOTH || kind == ROPE_SCALE_YARN;
+    if (turns && (original_positions < 1 || !(low_turns > 0.0) || !(high_turns > low_turns) || !std::isfinite(high_turns)))
+        return ROPE_ERR_INVALID_ARG;
+    if (rows == 0)
+        return ROPE_OK;
+    const int32_t h = rotary_dim / 2;
+    const int64_t bytes = rows * h * 4;
+    if (cos_out == nullptr || sin_out == nullptr || overlap({cos_out, bytes}, {sin_out, bytes}) || !aligned(cos_out, 4) ||
+        !aligned(sin_out, 4))
+        return ROPE_ERR_INVALID_ARG;
+    ScaledArgs a;
+    double w[kScaledPairs], scale;
+    scaled_frequencies(kind, theta, rotary_dim, factor, original_positions, low_turns, high_turns, w, &scale);
+    for (int32_t i = 0; i < h; ++i)            // at most 1 / 2 pi of a turn
+        a.freq[i] = (uint64_t)std::nearbyint(std::ldexp(w[i] / (2.0 * 3.14159265358979323846), 64));
+    for (int32_t i = h; i < kScaledPairs; ++i)
+        a.freq[i] = 0;
+    a.cos = cos_out; a.sin = sin_out; a.rows = rows; a.first = (uint64_t)pos_offset; a.h = h;
+    a.scale = (float)(value_scale > 0.0 ? value_scale : scale);
+    const bool wide = h % 4 == 0 && aligned(cos_out, 16) && aligned(sin_out, 16);
+    const int64_t threads = rows * (wide ? h / 4 : h);
+    int64_t blocks = (threads + kScaledThreads - 1) / kScaledThreads;
+    // a few rows a thread for long tables: its frequencies are read once
+    const int64_t most = 152 * 8;
+    if (blocks > most)
+        blocks = most;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e =
+        wide ? launch_hot(rope_tables_scaled_kernel<4>, dim3((unsigned)blocks), dim3(kScaledThreads), 0, st, a)
+             : launch_hot(rope_tables_scaled_kernel<1>, dim3((unsigned)blocks), dim3(kScaledThreads), 0, st, a);
+    return e == cudaSuccess ? ROPE_OK : ROPE_ERR_CUDA;
+}

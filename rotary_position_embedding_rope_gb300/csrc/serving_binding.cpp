@@ -1,5 +1,5 @@
-// serving_binding.cpp -- the Python side of the serving calls: checks of tensors,
-// allocation of outputs and workspaces, and the call into librope.
+// serving_binding.cpp -- the Python side of the serving and norm calls: checks of
+// tensors, allocation of outputs and workspaces, and the call into librope.
 //
 // A decode step makes these calls once or more per layer, each a few
 // microseconds on the device.  Written in Python over ctypes, an attention call
@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 #include <string>
 
 #include <ATen/core/Tensor.h>
@@ -18,7 +19,9 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 
 #include "rope.h"
 
@@ -29,6 +32,11 @@ decltype(&rope_attention_packed_fwd) g_packed = nullptr;
 decltype(&rope_attention_packed_workspace) g_packed_bytes = nullptr;
 decltype(&rope_attention_decode_fwd) g_decode = nullptr;
 decltype(&rope_attention_decode_workspace) g_decode_bytes = nullptr;
+decltype(&rope_norm_qk_fwd) g_norm = nullptr;
+decltype(&rope_norm_qk_bwd) g_norm_bwd = nullptr;
+decltype(&rope_norm_qk_workspace) g_norm_bytes = nullptr;
+decltype(&rope_norm_cache_append) g_norm_append = nullptr;
+decltype(&rope_tables_build_scaled) g_tables_scaled = nullptr;
 
 // A Python exception has been set.
 struct PythonError {};
@@ -274,14 +282,14 @@ struct Cache {
 };
 
 // The output: the given tensor of that shape, or a new one.
-at::Tensor output(const Call &c, PyObject *given, const Rows &like, at::ScalarType type)
+at::Tensor output(const Call &c, PyObject *given, const Rows &like, at::ScalarType type, const char *name = "out")
 {
     if (given == Py_None)
         return c.empty_returned({like.n, like.H, like.D}, type);
-    const at::Tensor &t = tensor(given, "out");
-    c.dense(given, "out", type, -1);
+    const at::Tensor &t = tensor(given, name);
+    c.dense(given, name, type, -1);
     if (t.dim() != 3 || t.size(0) != like.n || t.size(1) != like.H || t.size(2) != like.D)
-        fail(PyExc_ValueError, "out must be [" + std::to_string(like.n) + ", " + std::to_string(like.H) + ", " +
+        fail(PyExc_ValueError, std::string(name) + " must be [" + std::to_string(like.n) + ", " + std::to_string(like.H) + ", " +
                                    std::to_string(like.D) + "], got " + shape_of(t));
     return t;
 }
@@ -304,15 +312,16 @@ void expect(Py_ssize_t got, Py_ssize_t want)
 
 PyObject *status(rope_status st) { return PyLong_FromLong(st); }
 
-// bind(addresses of the five entry points)
+// bind(addresses of the entry points)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    if (n != 5) {
-        PyErr_SetString(PyExc_TypeError, "expected 5 addresses");
+    constexpr int kEntries = 10;
+    if (n != kEntries) {
+        PyErr_Format(PyExc_TypeError, "expected %d addresses", kEntries);
         return nullptr;
     }
-    void *p[5];
-    for (int i = 0; i < 5; ++i) {
+    void *p[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (p[i] == nullptr) {
             if (!PyErr_Occurred())
@@ -325,6 +334,11 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     g_packed_bytes = reinterpret_cast<decltype(g_packed_bytes)>(p[2]);
     g_decode = reinterpret_cast<decltype(g_decode)>(p[3]);
     g_decode_bytes = reinterpret_cast<decltype(g_decode_bytes)>(p[4]);
+    g_norm = reinterpret_cast<decltype(g_norm)>(p[5]);
+    g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(p[6]);
+    g_norm_bytes = reinterpret_cast<decltype(g_norm_bytes)>(p[7]);
+    g_norm_append = reinterpret_cast<decltype(g_norm_append)>(p[8]);
+    g_tables_scaled = reinterpret_cast<decltype(g_tables_scaled)>(p[9]);
     Py_RETURN_NONE;
 }
 
@@ -461,6 +475,287 @@ PyObject *attention_shared_prefix(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// A weight of the norm: a [D] tensor, in fp32 or the rows' type, or None.
+struct Weight {
+    const void *p = nullptr;
+    at::ScalarType type = at::kFloat;
+    bool given = false;
+
+    Weight(const Call &c, PyObject *o, const char *name, at::ScalarType rows, int64_t D)
+    {
+        if (o == Py_None)
+            return;
+        const at::Tensor &t = tensor(o, name);
+        given = true;
+        type = t.scalar_type();
+        if (type != at::kFloat && type != rows)
+            fail(PyExc_ValueError, std::string(name) + " must be fp32 or of the rows' type, got " + c10::toString(type));
+        p = c.dense(o, name, type, D);
+    }
+};
+
+int32_t weight_code(const Weight &q, const Weight &k, int32_t rows)
+{
+    if (q.given && k.given && q.type != k.type)
+        fail(PyExc_ValueError, "wq and wk must be of one type");
+    return (q.given ? q.type : k.type) == at::kFloat ? ROPE_F32 : rows;
+}
+
+int32_t type_code(const at::Tensor &t, const char *what)
+{
+    return t.scalar_type() == at::kFloat ? ROPE_F32 : type16(t, what);
+}
+
+// A [B, H, S, D] or [B, S, H, D] tensor with dense features, or None.
+struct Heads {
+    const void *p = nullptr;
+    int64_t B = 0, S = 0, strides[3] = {0, 0, 0};
+    int32_t H = 0, D = 0;
+
+    Heads(const Call &c, PyObject *o, const char *name, at::ScalarType type, bool seq_first)
+    {
+        if (o == Py_None)
+            return;
+        const at::Tensor &t = tensor(o, name);
+        c.on_device(t, name, type);
+        if (t.dim() != 4)
+            fail(PyExc_ValueError, std::string(name) + " must be 4-dimensional, got " + shape_of(t));
+        const int s = seq_first ? 1 : 2, h = seq_first ? 2 : 1;
+        if (t.size(h) > INT32_MAX || t.size(3) > INT32_MAX)
+            fail(PyExc_ValueError, std::string(name) + " is too large: " + shape_of(t));
+        if (t.numel() > 0 && t.size(3) > 1 && t.stride(3) != 1)
+            fail(PyExc_ValueError, std::string(name) + ": features must be dense");
+        B = t.size(0);
+        S = t.size(s);
+        H = (int32_t)t.size(h);
+        D = (int32_t)t.size(3);
+        strides[0] = t.stride(0);
+        strides[1] = t.stride(s);
+        strides[2] = t.stride(h);
+        p = t.data_ptr();
+    }
+};
+
+// The sizes that queries and keys share, and their positions.
+struct NormShape {
+    int64_t B, S, pos_stride = 0;
+    int32_t D;
+    const int32_t *pos = nullptr;
+
+    NormShape(const Call &c, const Heads &q, const Heads &k, bool has_q, bool has_k, PyObject *positions)
+    {
+        const Heads &x = has_q ? q : k;
+        B = x.B;
+        S = x.S;
+        D = x.D;
+        if (has_q && has_k && (q.B != k.B || q.S != k.S || q.D != k.D))
+            fail(PyExc_ValueError, "q and k must agree in batch, sequence and head_dim");
+        if (positions == Py_None)
+            return;
+        const at::Tensor &t = tensor(positions, "pos_idx");
+        pos = c.ints(positions, "pos_idx", -1);
+        if (t.dim() == 2 && t.size(0) == B && t.size(1) >= S)
+            pos_stride = t.size(1);
+        else if (t.dim() != 1 || t.size(0) != S)
+            fail(PyExc_ValueError, "pos_idx must be [S] or [B, >=S], got " + shape_of(t));
+        if (S == 0)
+            pos_stride = 0;
+    }
+};
+
+// The given tensor, dense and of the shape of `like`, or a new one.
+at::Tensor like_or_new(const Call &c, PyObject *given, const char *name, const at::Tensor &like)
+{
+    if (given == Py_None)
+        return c.empty_returned(like.sizes(), like.scalar_type());
+    const at::Tensor &t = tensor(given, name);
+    c.dense(given, name, like.scalar_type(), -1);
+    if (t.sizes() != like.sizes())
+        fail(PyExc_ValueError, std::string(name) + " must be " + shape_of(like) + ", got " + shape_of(t));
+    return t;
+}
+
+PyObject *wrapped(const at::Tensor &t)
+{
+    if (!t.defined())
+        Py_RETURN_NONE;
+    return THPVariable_Wrap(t);
+}
+
+PyObject *tuple_of(std::initializer_list<at::Tensor> ts)
+{
+    PyObject *r = PyTuple_New((Py_ssize_t)ts.size());
+    if (r == nullptr)
+        throw PythonError();
+    Py_ssize_t i = 0;
+    for (const at::Tensor &t : ts) {
+        PyObject *o = wrapped(t);
+        if (o == nullptr) {
+            Py_DECREF(r);
+            throw PythonError();
+        }
+        PyTuple_SET_ITEM(r, i++, o);
+    }
+    return r;
+}
+
+// norm_rotate_qk(q, k, wq, wk, cos, sin, eps, pos_idx, rotary_dim, layout,
+//                seq_before_head, q_out, k_out, stream) -> (q_out, k_out), or a status
+PyObject *norm_rotate_qk(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    try {
+        expect(n, 14);
+        const bool has_q = a[0] != Py_None, has_k = a[1] != Py_None;
+        const at::Tensor &x = has_q ? tensor(a[0], "q") : tensor(a[1], "q or k");
+        const Call c(x, a[13]);
+        const int32_t code = type_code(x, "norm_rotate_qk"), seq_first = truth(a[10]);
+        const at::ScalarType type = x.scalar_type();
+        const Heads q(c, a[0], "q", type, seq_first), k(c, a[1], "k", type, seq_first);
+        const NormShape z(c, q, k, has_q, has_k, a[7]);
+        const Weight wq(c, a[2], "wq", type, z.D), wk(c, a[3], "wk", type, z.D);
+        const Tables t(c, a[4], a[5], a[8]);
+        const c10::cuda::CUDAGuard guard(c.device);
+        const at::Tensor qo = has_q ? like_or_new(c, a[11], "q_out", tensor(a[0], "q")) : at::Tensor();
+        const at::Tensor ko = has_k ? like_or_new(c, a[12], "k_out", tensor(a[1], "k")) : at::Tensor();
+        const rope_status st =
+            unlocked(g_norm, q.p, k.p, has_q ? qo.data_ptr() : nullptr, has_k ? ko.data_ptr() : nullptr, wq.p, wk.p, t.cos,
+                     t.sin, z.pos, z.pos_stride, z.B, q.H, k.H, z.S, z.D, q.strides, k.strides, t.rotary_dim,
+                     (int32_t)integer(a[9]), seq_first, (float)number(a[6]), code, weight_code(wq, wk, code), t.rows, c.stream);
+        if (st != ROPE_OK)
+            return status(st);
+        if (has_q && a[11] != Py_None)
+            written(qo);
+        if (has_k && a[12] != Py_None)
+            written(ko);
+        return tuple_of({qo, ko});
+    } catch (const PythonError &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// norm_rotate_qk_backward(gq, gk, q, k, wq, wk, cos, sin, eps, pos_idx, rotary_dim,
+//     layout, seq_before_head, want_wq, want_wk, stream) -> (dq, dk, dwq, dwk), or a status
+PyObject *norm_rotate_qk_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    try {
+        expect(n, 16);
+        const bool has_q = a[2] != Py_None, has_k = a[3] != Py_None;
+        const at::Tensor &x = has_q ? tensor(a[2], "q") : tensor(a[3], "q or k");
+        const Call c(x, a[15]);
+        const int32_t code = type_code(x, "norm_rotate_qk_backward"), seq_first = truth(a[12]);
+        const at::ScalarType type = x.scalar_type();
+        const Heads q(c, a[2], "q", type, seq_first), k(c, a[3], "k", type, seq_first);
+        const NormShape z(c, q, k, has_q, has_k, a[9]);
+        const Weight wq(c, a[4], "wq", type, z.D), wk(c, a[5], "wk", type, z.D);
+        const Tables t(c, a[6], a[7], a[10]);
+        const void *gp[2] = {nullptr, nullptr};
+        for (int i = 0; i < 2; ++i) {
+            if (i == 0 ? !has_q : !has_k)
+                continue;
+            gp[i] = c.dense(a[i], i ? "gk" : "gq", type, -1);
+            if (tensor(a[i], "gq").sizes() != tensor(a[2 + i], "q").sizes())
+                fail(PyExc_ValueError, std::string(i ? "gk" : "gq") + " must be " + shape_of(tensor(a[2 + i], "q")) + ", got " +
+                                           shape_of(tensor(a[i], "gq")));
+        }
+        const c10::cuda::CUDAGuard guard(c.device);
+        at::Tensor d[4];
+        for (int i = 0; i < 2; ++i) {
+            if (i == 0 ? !has_q : !has_k)
+                continue;
+            d[i] = c.empty_returned(tensor(a[2 + i], "q").sizes(), type);
+            const Weight &w = i ? wk : wq;
+            if (truth(a[13 + i]) && w.given)
+                d[2 + i] = c.empty_returned({z.D}, w.type);
+        }
+        auto at_of = [&](int i) { return d[i].defined() ? d[i].data_ptr() : nullptr; };
+        const at::Tensor ws = c.workspace(Py_None, d[2].defined() || d[3].defined() ? g_norm_bytes(z.D) : 0);
+        const rope_status st =
+            unlocked(g_norm_bwd, q.p, k.p, gp[0], gp[1], at_of(0), at_of(1), wq.p, wk.p, at_of(2), at_of(3), t.cos, t.sin,
+                     z.pos, z.pos_stride, z.B, q.H, k.H, z.S, z.D, q.strides, k.strides, t.rotary_dim, (int32_t)integer(a[11]),
+                     seq_first, (float)number(a[8]), code, weight_code(wq, wk, code), t.rows,
+                     ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (int64_t)ws.nbytes() : 0, c.stream);
+        if (st != ROPE_OK)
+            return status(st);
+        return tuple_of({d[0], d[1], d[2], d[3]});
+    } catch (const PythonError &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// accumulates_elsewhere(tensor) -> whether the tensor is a leaf whose gradients a
+// graph that is alive accumulates on another stream than the current one.  (The
+// engine would make that stream wait for a captured backward pass, which ends the
+// capture with an error.)
+PyObject *accumulates_elsewhere(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    try {
+        expect(n, 1);
+        const at::Tensor &t = tensor(a[0], "leaf");
+        if (!t.is_cuda() || !t.is_leaf() || !t.requires_grad())
+            Py_RETURN_FALSE;
+        const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
+        if (node == nullptr)
+            Py_RETURN_FALSE;
+        const auto stream = node->stream();
+        if (stream && *stream != c10::cuda::getCurrentCUDAStream(t.get_device()).unwrap())
+            Py_RETURN_TRUE;
+        Py_RETURN_FALSE;
+    } catch (const PythonError &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// norm_cache_append(q, k, v, wq, wk, k_pages, v_pages, block_table, cu_seqlens,
+//     cache_lens, cos, sin, eps, pos, pos_offset, rotary_dim, layout, q_out, stream)
+// -> q_out, or a status
+PyObject *norm_cache_append(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    try {
+        expect(n, 19);
+        const at::Tensor &q = tensor(a[0], "q");
+        const Call c(q, a[18]);
+        const int32_t code = type16(q, "norm_cache_append");
+        const at::ScalarType type = q.scalar_type();
+        const Cache pool(c, a[5], a[6], type);
+        const Rows qr(c, a[0], "q", type, -1, pool.D), kr(c, a[1], "k", type, pool.Hk, pool.D),
+            vr(c, a[2], "v", type, pool.Hk, pool.D);
+        if (kr.n != vr.n || kr.n != qr.n)
+            fail(PyExc_ValueError, "q, k and v must have the same tokens");
+        const Weight wq(c, a[3], "wq", type, pool.D), wk(c, a[4], "wk", type, pool.D);
+        const at::Tensor &table = tensor(a[7], "block_table");
+        if (table.dim() != 2)
+            fail(PyExc_ValueError, "block_table must be [n_seqs, max_blocks], got " + shape_of(table));
+        const int64_t seqs = table.size(0), blocks = table.size(1);
+        const Tables t(c, a[10], a[11], a[15]);
+        const int32_t *list = c.ints(a[7], "block_table", -1), *cu = c.ints(a[8], "cu_seqlens", seqs + 1),
+                      *lens = c.ints(a[9], "cache_lens", seqs), *pos = c.ints(a[13], "pos", kr.n, true);
+        const c10::cuda::CUDAGuard guard(c.device);
+        const at::Tensor out = output(c, a[17], qr, type, "q_out");
+        const rope_status st =
+            unlocked(g_norm_append, qr.p, kr.p, vr.p, out.data_ptr(), pool.k, pool.v, wq.p, wk.p, list, cu, lens, t.cos, t.sin,
+                     pos, integer(a[14]), seqs, kr.n, qr.stride, kr.stride, vr.stride, qr.H, pool.Hk, pool.D, t.rotary_dim,
+                     (int32_t)integer(a[16]), (float)number(a[12]), pool.page, pool.n_pages, blocks, code,
+                     weight_code(wq, wk, code), t.rows, c.stream);
+        if (st != ROPE_OK)
+            return status(st);
+        written(tensor(a[5], "k_pages"));
+        written(tensor(a[6], "v_pages"));
+        if (a[17] != Py_None)
+            written(out);
+        return THPVariable_Wrap(out);
+    } catch (const PythonError &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef g_methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache_append)), METH_FASTCALL, nullptr},
@@ -468,6 +763,13 @@ PyMethodDef g_methods[] = {
      nullptr},
     {"attention_shared_prefix", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention_shared_prefix)),
      METH_FASTCALL, nullptr},
+    {"norm_rotate_qk", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_rotate_qk)), METH_FASTCALL, nullptr},
+    {"norm_rotate_qk_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_rotate_qk_backward)),
+     METH_FASTCALL, nullptr},
+    {"accumulates_elsewhere", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(accumulates_elsewhere)),
+     METH_FASTCALL, nullptr},
+    {"norm_cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_cache_append)), METH_FASTCALL,
+     nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
