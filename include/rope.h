@@ -631,6 +631,63 @@ int64_t rope_attention_decode_workspace(int64_t B, int32_t Hq, int32_t Hk, int32
                                         int64_t max_blocks, int64_t prefix_len);
 
 /*
+ * rope_attention_paged_fwd -- attention of every sequence's new tokens, one or a
+ * chunk of a prompt, over its keys in a paged cache (rope_cache_append or
+ * rope_norm_cache_append them first).
+ *
+ *   o_i = softmax(scale * rot(q_i) K_b^T + mask) V_b
+ *
+ * for the tokens i of sequence b, whose queries are tokens cu_seqlens_q[b] .. of q
+ * and whose seq_lens[b] keys, the new tokens' own among them, lie in its pages.
+ * With causal, query i of Lq sees key j of Lk when j <= i + Lk - Lq; a query that
+ * sees no key gets zeros.
+ * q: device [total_q, Hq, D], token stride q_stride; o: device [total_q, Hq, D],
+ *    dense, written (rows of no sequence are not).  Hq is a multiple of Hk.
+ * k_pages, v_pages: the cache, [n_pages, Hk, page_size, D] of rotated keys.
+ *    Sequences may share pages.
+ * block_table: device int32[n_seqs, max_blocks]; cu_seqlens_q: device
+ *    int32[n_seqs + 1]; seq_lens: device int32[n_seqs], 0 <= seq_lens[b] <=
+ *    max_blocks * page_size.  A sequence may have no new tokens.
+ * cos, sin: the rotation table, or both NULL: the queries are rotated already
+ *    (rotary_dim and table_rows are not looked at then).
+ * pos_q: device int32[total_q] table rows (-1: not rotated), or NULL for a query's index
+ *    among its sequence's keys, Lk - Lq + i.
+ * causal, softmax_scale: as rope_attention_fwd.
+ * workspace: device, 128-byte aligned, at least
+ *    rope_attention_paged_workspace(...) bytes; overwritten.
+ * An offset or a length out of range (ROPE_ERR_BAD_INDEX) is found on the device:
+ *    the flag is raised and nothing of o is written.  A page number out of range
+ *    reads as zeros and raises the flag: outputs of sequences that use it mean
+ *    nothing.  A table row out of range (but for rows before a sequence's first key
+ *    when causal): the query is not rotated and ROPE_ERR_POS_OUT_OF_RANGE raised.
+ * Arithmetic: as rope_attention_decode_fwd.  What lies behind a sequence's last
+ *    key, and in other pages, reaches no query; a NaN or infinity in a value may
+ *    reach queries of its sequence that do not see its key.  The split of the
+ *    work depends on the sizes and the lengths alone: the same call gives the same
+ *    bits.
+ * Errors: ROPE_ERR_UNSUPPORTED for other dtypes, D, rotary_dim, layouts, page
+ *    sizes, n_seqs > 4096, a stride not a multiple of 8 or unaligned pointers;
+ *    ROPE_ERR_INVALID_ARG for bad sizes, null pointers, a workspace too small,
+ *    o or the workspace overlapping another argument; ROPE_ERR_CUDA if a
+ *    launch fails.  Asynchronous on `stream`; waits inside the kernels are
+ *    bounded as in rope_attention_fwd.
+ */
+rope_status rope_attention_paged_fwd(const void *q, const void *k_pages, const void *v_pages, void *o,
+                                     const int32_t *block_table, const int32_t *cu_seqlens_q,
+                                     const int32_t *seq_lens, const float *cos, const float *sin,
+                                     const int32_t *pos_q, int64_t n_seqs, int64_t total_q,
+                                     int64_t q_stride, int32_t Hq, int32_t Hk, int32_t D,
+                                     int32_t rotary_dim, int32_t layout, int32_t causal,
+                                     float softmax_scale, int32_t page_size, int64_t n_pages,
+                                     int64_t max_blocks, int32_t dtype, int64_t table_rows,
+                                     void *workspace, int64_t workspace_bytes, void *stream);
+
+/* rope_attention_paged_workspace -- bytes of workspace for a call of these
+ * sizes (0 when there is nothing to do, -1 for sizes it does not take). */
+int64_t rope_attention_paged_workspace(int64_t n_seqs, int64_t total_q, int32_t Hq, int32_t Hk, int32_t D,
+                                       int32_t page_size, int64_t max_blocks);
+
+/*
  * rope_check_errors -- synchronise `stream`, then report and clear the
  * current device's error flag.
  * Returns ROPE_ERR_CUDA if the stream reports an error, else

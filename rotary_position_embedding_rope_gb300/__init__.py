@@ -22,7 +22,8 @@ workspace, keys rotated once beforehand).
 ``cache_append`` writes new keys (rotated) and values into a paged cache,
 ``attention_packed`` attends over packed prompts of different lengths and
 ``attention_shared_prefix`` runs one new token per sequence over a prefix all
-sequences share and each one's own pages.
+sequences share and each one's own pages; ``attention_paged`` attends from each sequence's
+new tokens, one or a chunk of a prompt, to its keys in the cache.
 ``norm_rotate_qk`` normalises query and key heads (RMS norm) and rotates them in the same
 pass (``norm_rotate_qk_backward`` and ``autograd.norm_rotary_qk`` give the gradients),
 ``norm_cache_append`` does it on the way into the paged cache.
@@ -58,12 +59,12 @@ __all__ = [
     "rope_attention_packed_fwd", "rope_attention_packed_workspace",
     "rope_attention_decode_fwd", "rope_attention_decode_workspace",
     "rope_tables_build_scaled", "rope_norm_qk_fwd", "rope_norm_qk_bwd", "rope_norm_qk_workspace",
-    "rope_norm_cache_append",
+    "rope_norm_cache_append", "rope_attention_paged_fwd", "rope_attention_paged_workspace",
     # conveniences
     "build_tables", "build_tables_ex", "apply_qk", "apply_q", "apply_qk_xpos", "rotate_qk",
     "attention", "attention_workspace", "PreparedApply", "cache_append",
     "attention_packed", "attention_shared_prefix", "build_tables_scaled", "norm_rotate_qk",
-    "norm_rotate_qk_backward", "norm_cache_append",
+    "norm_rotate_qk_backward", "norm_cache_append", "attention_paged",
 ]
 
 (ROPE_OK, ROPE_ERR_INVALID_ARG, ROPE_ERR_UNSUPPORTED, ROPE_ERR_CUDA, ROPE_ERR_POS_OUT_OF_RANGE,
@@ -187,6 +188,11 @@ def load_library() -> ctypes.CDLL:
     lib.rope_norm_cache_append.argtypes = [P] * 14 + [c.c_int64] * 6 + [c.c_int32] * 5 + \
         [c.c_float, c.c_int32, c.c_int64, c.c_int64, c.c_int32, c.c_int32, c.c_int64, P]
     lib.rope_norm_cache_append.restype = c.c_int
+    lib.rope_attention_paged_fwd.argtypes = [P] * 10 + [c.c_int64] * 3 + [c.c_int32] * 6 + \
+        [c.c_float, c.c_int32, c.c_int64, c.c_int64, c.c_int32, c.c_int64, P, c.c_int64, P]
+    lib.rope_attention_paged_fwd.restype = c.c_int
+    lib.rope_attention_paged_workspace.argtypes = [c.c_int64] * 2 + [c.c_int32] * 4 + [c.c_int64]
+    lib.rope_attention_paged_workspace.restype = c.c_int64
     _lib = lib
     return lib
 
@@ -772,6 +778,25 @@ def rope_attention_decode_workspace(B, Hq, Hk, D, page_size, max_blocks, prefix_
                                                           int(prefix_len))
 
 
+def rope_attention_paged_fwd(q, k_pages, v_pages, o, block_table, cu_seqlens_q, seq_lens, cos, sin, pos_q, n_seqs, total_q,
+                             q_stride, Hq, Hk, D, rotary_dim, layout, causal, softmax_scale, page_size, n_pages,
+                             max_blocks, dtype, table_rows, workspace, workspace_bytes, stream=None):
+    st = load_library().rope_attention_paged_fwd(
+        _addr(q, "q"), _addr(k_pages, "k_pages"), _addr(v_pages, "v_pages"), _addr(o, "o"),
+        _addr(block_table, "block_table"), _addr(cu_seqlens_q, "cu_seqlens_q"), _addr(seq_lens, "seq_lens"),
+        _addr(cos, "cos"), _addr(sin, "sin"), _addr(pos_q, "pos_q"), int(n_seqs), int(total_q), int(q_stride), int(Hq),
+        int(Hk), int(D), int(rotary_dim), int(layout), int(causal), float(softmax_scale), int(page_size), int(n_pages),
+        int(max_blocks), int(dtype), int(table_rows), _addr(workspace, "workspace"), int(workspace_bytes),
+        _stream(stream))
+    _check(st, "rope_attention_paged_fwd")
+
+
+def rope_attention_paged_workspace(n_seqs, total_q, Hq, Hk, D, page_size, max_blocks) -> int:
+    """Bytes of workspace (-1 for sizes the call does not take)."""
+    return load_library().rope_attention_paged_workspace(int(n_seqs), int(total_q), int(Hq), int(Hk), int(D),
+                                                         int(page_size), int(max_blocks))
+
+
 _serving = None
 
 
@@ -794,7 +819,8 @@ def _native():
             lib.rope_attention_packed_workspace, lib.rope_attention_decode_fwd,
             lib.rope_attention_decode_workspace, lib.rope_norm_qk_fwd, lib.rope_norm_qk_bwd,
             lib.rope_norm_qk_workspace, lib.rope_norm_cache_append,
-            lib.rope_tables_build_scaled)))
+            lib.rope_tables_build_scaled, lib.rope_attention_paged_fwd,
+            lib.rope_attention_paged_workspace)))
         _serving = module
     return _serving
 
@@ -845,6 +871,37 @@ def norm_cache_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, wq: tor
         rotary_dim, _LAYOUT_CODE[layout], q_out, stream)
     if type(o) is int:
         raise RopeError(o, "rope_norm_cache_append")
+    return o
+
+
+def attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                    cu_seqlens_q: torch.Tensor, seq_lens: torch.Tensor, cos: torch.Tensor | None = None,
+                    sin: torch.Tensor | None = None, pos_q: torch.Tensor | None = None,
+                    rotary_dim: int | None = None, layout: str = "split_half", causal: bool = True,
+                    scale: float | None = None, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of every sequence's new tokens, one or a chunk of a prompt, over its paged cache.
+
+    q: [Tq, Hq, D] packed new tokens (a view with a token stride is taken as it is);
+    returns [Tq, Hq, D].  Sequence b's queries are tokens cu_seqlens_q[b] ..
+    cu_seqlens_q[b+1] - 1 (none is allowed), the last of its seq_lens[b] keys
+    (cache_append or norm_cache_append them first): with causal, query i of Lq sees the
+    keys j <= i + Lk - Lq.  A query that sees no key gets zeros; rows of ``out`` that
+    belong to no sequence keep what they hold.
+    k_pages, v_pages: the cache, [pages, Hk, page_size, D]; block_table: int32 [n_seqs,
+    max_blocks]; cu_seqlens_q: int32 [n_seqs + 1]; seq_lens: int32 [n_seqs].
+    cos, sin: the rotation table, or None where q is rotated already (norm_cache_append).
+    pos_q: int32 [Tq] table rows (-1 = not rotated), or None for a query's index among its
+    sequence's keys.
+    workspace: None, or a uint8 tensor of rope_attention_paged_workspace(...) bytes to use
+    (128-byte aligned; its contents do not matter).
+    stream: as attention_packed.  Forward only, as well.
+    """
+    o = (_serving or _native()).attention_paged(
+        q, k_pages, v_pages, block_table, cu_seqlens_q, seq_lens, cos, sin, pos_q, rotary_dim,
+        _LAYOUT_CODE[layout], causal, scale, out, workspace, stream)
+    if type(o) is int:
+        raise RopeError(o, "rope_attention_paged_fwd")
     return o
 
 

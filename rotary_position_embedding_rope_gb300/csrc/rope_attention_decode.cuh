@@ -211,6 +211,64 @@ struct DecodeArgs {
     const float2 *prefix_stats;
     int32_t prefix_tiles;                      // key tiles of the prefix kernel (0: it does not run)
     int32_t suffix;                            // 1: the suffix kernel runs
+
+    // What the suffix code below asks of its arguments (the paged attention's
+    // are others, rope_attention_paged.cuh).
+    static constexpr bool kRowLimits = false;  // every row sees all keys of its pair
+    __device__ __forceinline__ int32_t sequences() const { return B + fold; }
+    __device__ __forceinline__ int32_t heads() const { return Hk * row_groups; }
+    __device__ __forceinline__ int64_t most_keys() const { return max_blocks << page_shift; }
+    // Keys of sequence b, the folded prefix (b = B) included.
+    __device__ __forceinline__ int32_t keys(int32_t b, int64_t most) const
+    {
+        return b < B ? suffix_keys(lens, b, most, a.flag) : n_prefix;
+    }
+    __device__ __forceinline__ const int32_t *blocks(int32_t b, int64_t &listed) const
+    {
+        listed = b < B ? max_blocks : ((int64_t)n_prefix - 1 >> page_shift) + 1;
+        return b < B ? table + b * max_blocks : prefix_table;
+    }
+    // Row r of pair (b, hr): where its query lies (null: no such row) and the table
+    // row that rotates it.  The rows are heads of one sequence, or, for the folded
+    // prefix, of the whole batch.
+    template <typename T, int D>
+    __device__ __forceinline__ const T *query(int32_t b, int32_t hr, int32_t r, int64_t most, bool rot,
+                                              int64_t &trow) const
+    {
+        const int32_t kv = hr / row_groups, group = Hq / Hk, r0 = (hr - kv * row_groups) * rows;
+        bool live = r < rows && r0 + r < group;
+        if (b == B) {                          // the folded prefix
+            b = r / group;
+            r -= b * group;
+            live = b < B;
+        }
+        if (!live)
+            return nullptr;
+        if (rot)
+            trow = query_row(pos_q, b,
+                             pos_q != nullptr ? 0 : (int64_t)n_prefix + suffix_keys(lens, b, most, a.flag),
+                             a.table_rows, a.flag);
+        return static_cast<const T *>(q) + b * q_stride + (int64_t)(kv * group + r0 + r) * D;
+    }
+    // Keys that row r of sequence b's pairs sees, of n.
+    __device__ __forceinline__ int32_t limit(int32_t, int32_t, int32_t n) const { return n; }
+    // The first row of warp w's part of pair (b, hr), and how many rows it has.
+    __device__ __forceinline__ int64_t part_row(int32_t w, int32_t b, int32_t hr) const
+    {
+        const int32_t pair = b * (Hk * row_groups) + hr;
+        return ((int64_t)w + pair) * slot_rows;
+    }
+    __device__ __forceinline__ int32_t part_rows(int32_t, int32_t) const { return slot_rows; }
+    // What the merge has to know of the suffixes' deal.  One CTA writes it, whether or
+    // not its waits expired: the merge runs in either case, and finds the parts'
+    // places by it.
+    __device__ __forceinline__ void publish(const int32_t *start, int64_t per) const
+    {
+        for (int32_t b = threadIdx.x; b <= B + fold; b += blockDim.x)
+            chunk_start[b] = start[b];
+        if (threadIdx.x == 0)
+            deal->suffix_per = per;
+    }
 };
 
 // Chunks of a warp: an equal share, and no less than two, so that few warps'
@@ -229,14 +287,11 @@ __device__ __forceinline__ int64_t decode_per_warp(int64_t chunks, int32_t warps
     return per < kDecMinChunks ? kDecMinChunks : per;
 }
 
-// Keys, and chunks, of sequence b, the folded prefix (b = B) included.
-__device__ __forceinline__ int32_t decode_keys(const DecodeArgs &g, int32_t b, int64_t most)
+// Chunks of sequence b.
+template <typename G>
+__device__ __forceinline__ int32_t decode_chunks(const G &g, int32_t b, int64_t most)
 {
-    return b < g.B ? suffix_keys(g.lens, b, most, g.a.flag) : g.n_prefix;
-}
-__device__ __forceinline__ int32_t decode_chunks(const DecodeArgs &g, int32_t b, int64_t most)
-{
-    const int32_t n = decode_keys(g, b, most);
+    const int32_t n = g.keys(b, most);
     return (n >> g.chunk_shift) + ((n & ((1 << g.chunk_shift) - 1)) != 0);
 }
 
@@ -274,16 +329,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // A place in the list of chunks.
 struct ChunkAt {
     int32_t b, hr, ch, n;                      // sequence, key head and row group, chunk of n
-    __device__ __forceinline__ void next(const DecodeArgs &g, int64_t most)
+    template <typename G>
+    __device__ __forceinline__ void next(const G &g, int64_t most)
     {
         if (++ch < n)
             return;
         ch = 0;
-        if (++hr < g.Hk * g.row_groups)
+        if (++hr < g.heads())
             return;
         hr = 0;
         do {
-            if (++b >= g.B + g.fold) {
+            if (++b >= g.sequences()) {
                 n = 0;
                 return;
             }
@@ -293,40 +349,24 @@ struct ChunkAt {
 };
 
 // 16 rows of rotated queries of pair (b, hr) into the warp's tile (zeros past
-// the pair's rows), then as the A operand of every 16-feature step.  The rows
-// are heads of one sequence, or, for the folded prefix, of the whole batch.
-template <typename T, int LAYOUT, int D>
-__device__ __forceinline__ void load_query_rows(const DecodeArgs &g, const ChunkAt &at, int64_t most,
+// the pair's rows), then as the A operand of every 16-feature step.
+template <typename T, int LAYOUT, int D, typename G>
+__device__ __forceinline__ void load_query_rows(const G &g, const ChunkAt &at, int64_t most,
                                                 uint8_t *tile, uint32_t (&qf)[D / 16][4])
 {
     constexpr int L = D / 16, kAtOnce = 32 / L, kSteps = 16 / kAtOnce;
     const int lane = threadIdx.x & 31, j = lane % L;
-    const int32_t kv = at.hr / g.row_groups, group = g.Hq / g.Hk;
-    const int32_t r0 = (at.hr - kv * g.row_groups) * g.rows;
     const RowPart part = row_part<LAYOUT>(j, g.a.rotary_dim);
     uint4 x0[kSteps], x1[kSteps];
     int64_t trow[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-        int32_t r = i * kAtOnce + lane / L, b = at.b;
-        bool live = r < g.rows && r0 + r < group;
-        if (b == g.B) {                        // the folded prefix
-            b = r / group;
-            r -= b * group;
-            live = b < g.B;
-        }
         x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
         trow[i] = -1;
-        if (live) {
-            const T *row = static_cast<const T *>(g.q) + b * g.q_stride + (int64_t)(kv * group + r0 + r) * D;
+        const T *row = g.template query<T, D>(at.b, at.hr, i * kAtOnce + lane / L, most, part.rot, trow[i]);
+        if (row != nullptr) {
             x0[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o0));
             x1[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o1));
-            if (part.rot)
-                trow[i] = query_row(g.pos_q, b,
-                                    g.pos_q != nullptr ? 0
-                                                       : (int64_t)g.n_prefix +
-                                                             suffix_keys(g.lens, b, most, g.a.flag),
-                                    g.a.table_rows, g.a.flag);
         }
     }
 #pragma unroll
@@ -404,37 +444,26 @@ struct SuffixShared {
     int abort_flag;
 };
 
-// What the merge has to know of the suffixes' deal.  One CTA writes it, whether or
-// not its waits expired: the merge runs in either case, and finds the parts'
-// places by it.
-__device__ __forceinline__ void publish_suffixes(const DecodeArgs &g, const int32_t *start, int64_t per)
-{
-    for (int32_t b = threadIdx.x; b <= g.B + g.fold; b += blockDim.x)
-        g.chunk_start[b] = start[b];
-    if (threadIdx.x == 0)
-        g.deal->suffix_per = per;
-}
-
 // The suffixes' share of CTA `cta` of `ctas`, whose first eight warps work:
 // every thread of the CTA calls this, then the working ones decode_suffixes.
-template <int D>
-__device__ __forceinline__ SuffixRun suffix_run(const DecodeArgs &g, const int32_t *start, int32_t carry,
+template <int D, typename G>
+__device__ __forceinline__ SuffixRun suffix_run(const G &g, const int32_t *start, int32_t carry,
                                                 int32_t cta, int32_t ctas, SuffixShared<D> &sh)
 {
     constexpr int kStages = kDecStages<D>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int32_t n_seqs = g.B + g.fold;
+    const int32_t n_seqs = g.sequences();
     if (tid < kDecWarps * kStages)
         mbar_init(&sh.bar[0][0] + tid, 1);
     if (tid == 0)
         sh.abort_flag = 0;
     if (lane == 0 && warp < 2)                 // the maps, before the first copies need them
         asm volatile("prefetch.tensormap [%0];" ::"l"(warp ? &g.v_map : &g.k_map) : "memory");
-    const int32_t heads = g.Hk * g.row_groups;
+    const int32_t heads = g.heads();
     const int64_t total = (int64_t)carry * heads;
     const int64_t per = decode_per_warp(total, ctas * kDecWarps);
     if (cta == 0)
-        publish_suffixes(g, start, per);
+        g.publish(start, per);
     SuffixRun run;
     // (consecutive runs on different SMs: with few of them every SM copies; on few
     // SMs 4 sequences after 500 keys took 13.6 us, so 12.5)
@@ -458,15 +487,15 @@ __device__ __forceinline__ SuffixRun suffix_run(const DecodeArgs &g, const int32
 }
 
 // One warp's run; smem: kDecSmem bytes of the CTA.
-template <typename T, int LAYOUT, int D>
-__device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *smem, const SuffixRun &run,
+template <typename T, int LAYOUT, int D, typename G>
+__device__ __forceinline__ void decode_suffixes(const G &g, uint8_t *smem, const SuffixRun &run,
                                                 SuffixShared<D> &sh)
 {
     constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>, kKeys = kDecKeys<D>;
     constexpr int kBox = kKeys * 128, kGroups = kKeys / 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t most = g.max_blocks << g.page_shift;
-    const int32_t heads = g.Hk * g.row_groups, w = run.w;
+    const int64_t most = g.most_keys();
+    const int32_t w = run.w;
     int64_t left = run.left;
     ChunkAt at = run.at;
     if (left <= 0)
@@ -491,8 +520,8 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
             of = ahead.b;
             base_block = block;
             const int64_t blocks = (((int64_t)ahead.n * kKeys - 1) >> g.page_shift) + 1;
-            const int64_t listed = of < g.B ? g.max_blocks : ((int64_t)g.n_prefix - 1 >> g.page_shift) + 1;
-            const int32_t *list = of < g.B ? g.table + of * g.max_blocks : g.prefix_table;
+            int64_t listed;
+            const int32_t *list = g.blocks(of, listed);
             // (a chunk's last page may lie behind the list: its keys are not visible)
             pages = block + lane < (blocks < listed ? blocks : listed) ? __ldg(list + block + lane) : -1;
         }
@@ -505,7 +534,7 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
             int32_t z = page * g.Hk + ahead.hr / g.row_groups;
             if (page < 0 || page >= g.n_pages) {
                 // (a page without visible keys may have any number)
-                if (key + ((int64_t)i << box_shift) < decode_keys(g, ahead.b, most))
+                if (key + ((int64_t)i << box_shift) < g.keys(ahead.b, most))
                     atomicOr(g.a.flag, kFlagIndex);
                 z = (int32_t)(g.n_pages * g.Hk);               // arrives as zeros
             }
@@ -525,6 +554,7 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
     float o[D / 8][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;   // rows lane / 4 and + 8
     int32_t keys = 0;                                          // of the pair's suffix
+    int32_t lim0 = 0, lim1 = 0, low = 0;                       // keys that the two rows see, and that all rows see
     bool fresh = true;
     int st = 0;
     uint32_t ph = 0;
@@ -535,7 +565,12 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
     const uint32_t base = attn_smem_u32(stages);
     for (; ok && left > 0; --left, ++done) {
         if (fresh) {
-            keys = decode_keys(g, at.b, most);
+            keys = g.keys(at.b, most);
+            if constexpr (G::kRowLimits) {
+                lim0 = g.limit(at.b, lane >> 2, keys);
+                lim1 = g.limit(at.b, (lane >> 2) + 8, keys);
+                low = g.limit(at.b, 0, keys);
+            }
             load_query_rows<T, LAYOUT, D>(g, at, most, qtile, qf);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
@@ -585,6 +620,17 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
                     sc[i] = sd[i] = -INFINITY;
                     // what lies behind the last key (anything) must not meet a zero
                     vis[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+                }
+            }
+        }
+        if constexpr (G::kRowLimits) {
+            if (low - at.ch * kKeys < kKeys) {                 // keys that some row does not see
+                const int32_t n0 = lim0 - at.ch * kKeys, n1 = lim1 - at.ch * kKeys;
+#pragma unroll
+                for (int i = 0; i < 4 * kGroups; ++i) {
+                    const int key = c0 + (i & 1) + (i >> 1) * 8;
+                    sc[i] = key < n0 ? sc[i] : -INFINITY;
+                    sd[i] = key < n1 ? sd[i] : -INFINITY;
                 }
             }
         }
@@ -649,8 +695,6 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
             st = 0;
             ph ^= 1u;
         }
-        const int32_t pair = at.b * heads + at.hr;
-        const int64_t slot = (int64_t)w + pair;
         const ChunkAt was = at;
         at.next(g, most);
         if (left == 1 || at.b != was.b || at.hr != was.hr) {
@@ -659,17 +703,19 @@ __device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *sm
             l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
             const int r = lane >> 2;
+            const int64_t row0 = g.part_row(w, was.b, was.hr);
+            const int32_t rows = g.part_rows(was.b, was.hr);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int rr = r + 8 * half;
-                if (rr < g.slot_rows) {
-                    float *dst = g.out + (slot * g.slot_rows + rr) * D + c0;
+                if (rr < rows) {
+                    float *dst = g.out + (row0 + rr) * D + c0;
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i)
                         *reinterpret_cast<float2 *>(dst + 8 * i) =
                             make_float2(o[i][2 * half], o[i][2 * half + 1]);
                     if ((lane & 3) == 0)
-                        g.stats[slot * g.slot_rows + rr] = half ? make_float2(m1, l1) : make_float2(m0, l0);
+                        g.stats[row0 + rr] = half ? make_float2(m1, l1) : make_float2(m0, l0);
                 }
             }
             fresh = true;
@@ -703,7 +749,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) rope_decode_suffix_kernel(cons
 // ---------------------------------------------------------------------------
 // 1. the prefix, with the suffixes beside or behind it
 struct PrefixSource {
-    static constexpr bool kPrefix = true;
+    static constexpr bool kFullUnroll = false;
+    static constexpr bool kParts = true, kAllParts = true;
+    static constexpr bool kFinish = true;
     template <int D>
     static constexpr int smem_bytes()
     {
@@ -761,9 +809,8 @@ struct PrefixSource {
         if (failed) {                          // copies may still be on their way: no work,
             // but what the merge needs; the scan lies behind the roles' memory
             if (cta == 0)
-                publish_suffixes(g, chunk_starts<D>(smem),
-                                 decode_per_warp((int64_t)w.chunks * g.Hk * g.row_groups,
-                                                 ((int32_t)gridDim.x - used) * kDecWarps));
+                g.publish(chunk_starts<D>(smem), decode_per_warp((int64_t)w.chunks * g.Hk * g.row_groups,
+                                                                 ((int32_t)gridDim.x - used) * kDecWarps));
             return;
         }
         const SuffixRun run =
@@ -830,6 +877,7 @@ struct PrefixSource {
                          a.table_rows, a.flag);
     }
 
+    __device__ __forceinline__ void acquire(const PackedUnit &, int32_t &) const {}   // (no map of a kernel's)
     // z of a prefix page in the pools' maps; past the last page, and for a bad
     // page number, an index that arrives as zeros
     __device__ __forceinline__ int32_t page_z(int32_t i, int32_t kv) const
@@ -925,56 +973,16 @@ struct PrefixSource {
 // registers keep CTAs out: 8 % less for the first of these, 4 to 9 % more for the
 // next three.
 constexpr int64_t kMergeWarps = 4096;
-template <typename T, int D, int W>
-__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_decode_merge_kernel(const __grid_constant__ DecodeArgs g)
+// One row's parts joined into o / l, by a warp (W = 1) or by the W warps of a CTA:
+// part(p, stat) gives the maximum and sum of part p and where its D outputs lie.
+template <typename T, int D, int W, typename Part>
+__device__ __forceinline__ void merge_parts(int32_t all, T *dst, const Part &part)
 {
     constexpr int V = D / 32, kAtOnce = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = W == 1 ? 0 : warp;
-    const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + warp : (int64_t)blockIdx.x;
-    pdl_wait();
-    pdl_trigger();
-    if (row >= (int64_t)g.B * g.Hq)
-        return;
-    const int32_t b = (int32_t)(row / g.Hq), h = (int32_t)(row - (int64_t)b * g.Hq);
-    const int32_t group = g.Hq / g.Hk, kv = h / group, in_group = h - kv * group;
-    const int32_t rg = in_group / g.rows, r = in_group - rg * g.rows;
-    const int32_t heads = g.Hk * g.row_groups;
-    // the parts: groups of the prefix kernel, slots of the pair, slots of the
-    // folded prefix
-    int32_t n0 = 0, n1 = 0, n2 = 0;
-    int64_t first0 = 0, first1 = 0, first2 = 0;
-    const DecodeDeal deal = *g.deal;
-    if (g.prefix_tiles > 0) {
-        const int32_t hu = h >> g.lg;
-        first0 = hu * g.prefix_tiles / deal.prefix_per + hu;
-        n0 = (int32_t)(((hu + 1) * g.prefix_tiles - 1) / deal.prefix_per + hu - first0 + 1);
-    }
-    if (g.suffix) {
-        auto slots = [&](int32_t seq, int32_t hr, int64_t &first, int32_t &n) {
-            const int64_t c0 = g.chunk_start[seq], c1 = g.chunk_start[seq + 1];
-            if (c1 == c0)
-                return;
-            const int64_t at = c0 * heads + hr * (c1 - c0), pair = (int64_t)seq * heads + hr;
-            first = divide(at, deal.suffix_per) + pair;
-            n = (int32_t)(divide(at + (c1 - c0) - 1, deal.suffix_per) + pair - first + 1);
-        };
-        slots(b, kv * g.row_groups + rg, first1, n1);
-        if (g.fold)
-            slots(g.B, kv, first2, n2);
-    }
-    // part p: its row among the statistics, and whose
-    auto part = [&](int32_t p, bool &prefix) -> int64_t {
-        prefix = p < n0;
-        if (prefix)
-            return (((first0 + p) * g.B + b) << g.lg) + (h & ((1 << g.lg) - 1));
-        p -= n0;
-        if (p < n1)
-            return (first1 + p) * g.slot_rows + r;
-        return (first2 + p - n1) * g.slot_rows + b * group + in_group;
-    };
     // Batches of 32 of the warp's parts: lane i holds part i's maximum and sum, so
     // the loads of a batch do not wait for one another.
-    const int32_t all = n0 + n1 + n2, n_parts = (all - share + W - 1) / W;   // parts share, share + W, ...
+    const int32_t n_parts = (all - share + W - 1) / W;         // parts share, share + W, ...
     float m = -INFINITY, l = 0.0f, o[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -983,12 +991,8 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_decode_merge_kerne
         const int n = n_parts - p0 < 32 ? n_parts - p0 : 32;
         float2 mine = make_float2(-INFINITY, 0.0f);
         const float *src = nullptr;
-        if (lane < n) {
-            bool prefix;
-            const int64_t at = part((p0 + lane) * W + share, prefix);
-            mine = __ldg((prefix ? g.prefix_stats : g.stats) + at);
-            src = (prefix ? g.prefix_out : g.out) + at * D;
-        }
+        if (lane < n)
+            src = part((p0 + lane) * W + share, mine);
         float v[kAtOnce][V];
         auto fetch = [&](int i0) {
 #pragma unroll
@@ -1068,12 +1072,66 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_decode_merge_kerne
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    T *dst = static_cast<T *>(g.o) + row * D + lane * V;
+    dst += lane * V;
     if constexpr (V == 4)
         *reinterpret_cast<uint2 *>(dst) = make_uint2(Elt<T>::f2_to_word(o[0] * inv, o[1] * inv),
                                                      Elt<T>::f2_to_word(o[2] * inv, o[3] * inv));
     else
         *reinterpret_cast<uint32_t *>(dst) = Elt<T>::f2_to_word(o[0] * inv, o[1] * inv);
+}
+
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_decode_merge_kernel(const __grid_constant__ DecodeArgs g)
+{
+    const int warp = threadIdx.x >> 5;
+    const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + warp : (int64_t)blockIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    if (row >= (int64_t)g.B * g.Hq)
+        return;
+    const int32_t b = (int32_t)(row / g.Hq), h = (int32_t)(row - (int64_t)b * g.Hq);
+    const int32_t group = g.Hq / g.Hk, kv = h / group, in_group = h - kv * group;
+    const int32_t rg = in_group / g.rows, r = in_group - rg * g.rows;
+    const int32_t heads = g.Hk * g.row_groups;
+    // the parts: groups of the prefix kernel, slots of the pair, slots of the
+    // folded prefix
+    int32_t n0 = 0, n1 = 0, n2 = 0;
+    int64_t first0 = 0, first1 = 0, first2 = 0;
+    const DecodeDeal deal = *g.deal;
+    if (g.prefix_tiles > 0) {
+        const int32_t hu = h >> g.lg;
+        first0 = hu * g.prefix_tiles / deal.prefix_per + hu;
+        n0 = (int32_t)(((hu + 1) * g.prefix_tiles - 1) / deal.prefix_per + hu - first0 + 1);
+    }
+    if (g.suffix) {
+        auto slots = [&](int32_t seq, int32_t hr, int64_t &first, int32_t &n) {
+            const int64_t c0 = g.chunk_start[seq], c1 = g.chunk_start[seq + 1];
+            if (c1 == c0)
+                return;
+            const int64_t at = c0 * heads + hr * (c1 - c0), pair = (int64_t)seq * heads + hr;
+            first = divide(at, deal.suffix_per) + pair;
+            n = (int32_t)(divide(at + (c1 - c0) - 1, deal.suffix_per) + pair - first + 1);
+        };
+        slots(b, kv * g.row_groups + rg, first1, n1);
+        if (g.fold)
+            slots(g.B, kv, first2, n2);
+    }
+    // part p: its row among the statistics, and whose
+    auto part = [&](int32_t p, bool &prefix) -> int64_t {
+        prefix = p < n0;
+        if (prefix)
+            return (((first0 + p) * g.B + b) << g.lg) + (h & ((1 << g.lg) - 1));
+        p -= n0;
+        if (p < n1)
+            return (first1 + p) * g.slot_rows + r;
+        return (first2 + p - n1) * g.slot_rows + b * group + in_group;
+    };
+    merge_parts<T, D, W>(n0 + n1 + n2, static_cast<T *>(g.o) + row * D, [&](int32_t p, float2 &stat) {
+        bool prefix;
+        const int64_t at = part(p, prefix);
+        stat = __ldg((prefix ? g.prefix_stats : g.stats) + at);
+        return (prefix ? g.prefix_out : g.out) + at * D;
+    });
 }
 
 // ---------------------------------------------------------------------------

@@ -432,7 +432,10 @@ struct PackedUnit {
 // Where the units come from and where K and V lie.  PackedSource: the list and
 // the values' maps that the prepare kernel wrote; rows end in bf16 / fp16 outputs.
 struct PackedSource {
-    static constexpr bool kPrefix = false;
+    static constexpr bool kFullUnroll = true;  // of the issue loops (see the kernel)
+    static constexpr bool kParts = false;      // units may end in fp32 parts (part >= 0, store_rows)
+    static constexpr bool kAllParts = false;   // all of them do
+    static constexpr bool kFinish = false;     // other work on SMs without units, or behind them
     template <int D>
     static constexpr int smem_bytes()
     {
@@ -503,6 +506,13 @@ struct PackedSource {
     __device__ __forceinline__ int32_t value_place(const PackedUnit &, int32_t, int) const
     {
         return 0;
+    }
+    // the map of the unit's values, before the first copy with it (seq: the last unit's sequence)
+    __device__ __forceinline__ void acquire(const PackedUnit &u, int32_t &seq) const
+    {
+        if (u.seq != seq)
+            acquire_map(maps + u.seq);
+        seq = u.seq;
     }
     // this CTA's half of key tile kt (64 keys) and of value tile kt (D / 2 features)
     template <int D>
@@ -635,7 +645,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
     // sit together in the instruction cache, as it seems): 32 sequences after 128k
     // keys 194 us, with 4 / 2 122 us; D = 64 124 and 115 us.  D = 128 over packed
     // sequences is bound by the issue of its products: 4 / 2 costs 1 %.
-    constexpr bool kIssueBound = D == 128 && !Source::kPrefix;
+    constexpr bool kIssueBound = D == 128 && Source::kFullUnroll;
     constexpr int kSUnroll = kIssueBound ? 8 : 4, kPVUnroll = kIssueBound ? 4 : 2;
     const AttnArgs &a = src.a;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -874,11 +884,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
             }
             const int32_t y0 = u.tok0 + (int)rank * tokens + wq * (32 >> lg);
             const uint32_t o_base = tmem + k2OCol + ((uint32_t)(wq * 32) << 16) + (un % kOBufs) * D;
-            if constexpr (Source::kPrefix) {
-                src.template store_rows<D>(u, o_base, y0, lane, lg, stat);
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                arrive_leader(&bar_ofree[un % kOBufs]);
-            } else {
+            bool parts = false;
+            if constexpr (Source::kParts) {
+                parts = u.part >= 0;
+                if (parts) {
+                    src.template store_rows<D>(u, o_base, y0, lane, lg, stat);
+                    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                    arrive_leader(&bar_ofree[un % kOBufs]);
+                }
+            }
+            if constexpr (!Source::kAllParts)
+            if (!parts) {
                 // O / l of the warp's 32 rows, staged and stored by TMA (boxes
                 // of 64 features x GP heads x 32 / GP tokens) or, where the
                 // sequence ends within them, by the warp.  O is free for the next
@@ -1086,11 +1102,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
             int32_t seq = -1;                      // the sequence whose map was acquired
             for (Cursor c = with_tiles(src.first(walk)); ok && valid(c); c = next_with_tiles(c)) {
                 const PackedUnit u = unit_of(c);
-                if constexpr (!Source::kPrefix) {
-                    if (u.seq != seq)
-                        acquire_map(src.maps + u.seq);
-                    seq = u.seq;
-                }
+                src.acquire(u, seq);
                 for (int32_t kt = 0; ok && kt < u.n_tiles; ++kt) {
                     const int32_t z = src.template value_place<D>(u, kt, lane);
                     if (!first)
@@ -1134,7 +1146,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols)
                      : "memory");
-    if constexpr (Source::kPrefix)
+    if constexpr (Source::kFinish)
         src.template finish<T, LAYOUT, D>(walk, smem, failed);
 }
 

@@ -1,0 +1,811 @@
+// rope_attention_paged.cuh -- attention of every sequence's new tokens, one or a
+// chunk of a prompt, over its keys in a paged cache (rope_attention_paged_fwd).
+//
+//   o_i = softmax(scale * rot(q_i) K_b^T, j <= i + Lk - Lq) V_b
+//
+// for the Lq new tokens i of sequence b, whose Lk keys (the new tokens' own among
+// them, rotated when they were appended) lie in pages.  A step of a serving loop
+// mixes sequences of a single token with chunks of hundreds, so a call has two
+// kinds of work, side by side in one launch:
+//   tiles   sequences of more than 16 rows (token, head) per key head run on
+//           rope_attn_packed_kernel, whose units here are (query tile, head unit)
+//           pairs.  The key tiles of all units, each unit's with a fixed charge for
+//           its start and end, laid end to end, are cut into equal runs, one per
+//           cluster, wherever the cuts fall: a long context of one sequence and a
+//           batch of ragged chunks both keep every cluster busy to the end.  A unit
+//           that lies in one run is written by it; a cut one leaves an fp32 (O, m,
+//           l) per piece;
+//   few     the others, of at most 16 rows (the 16 rows of an mma), run as the
+//           suffixes of the shared-prefix decode (decode_suffixes): equal runs of
+//           16-key (32 for heads of 64) chunks for all warps of the SMs that have
+//           no tiles, an fp32 (O, m, l) for each pair (sequence, key head) that a
+//           run touches.
+// Three launches:
+//   1. rope_paged_plan_kernel checks the offsets and lengths, lists the units and
+//      cuts them, decides how many SMs each kind gets (plan_ns's estimate), and
+//      writes a tensor map for the last, partly filled page of a sequence (rows
+//      past its end arrive as zeros: what lies there must not meet a probability of
+//      zero);
+//   2. the attention;
+//   3. rope_paged_merge_kernel joins the pieces.
+// The split depends on the sizes and the lengths alone: the same call gives the
+// same bits.
+//
+// Roundings as in the packed and the decode attention: rot(q), and P before P V, to
+// the element type (operands of a 16-bit product), everything else fp32 until o.
+#pragma once
+
+#include "rope_attention_decode.cuh"
+
+namespace rope {
+
+// One query tile of a sequence, 256 / GP tokens; `before`: the weight of the
+// units of all entries before it.
+struct alignas(16) PagedEntry {
+    int32_t seq, tok0, Lq, Lk;
+    int32_t q_start, n_tiles;
+    int64_t before;
+};
+
+// A place among the units' key tiles: entry, head unit, key tile.
+struct PagedCut {
+    int32_t entry, hu, kt;
+    __device__ __forceinline__ bool before(const PagedCut &o) const
+    {
+        return entry != o.entry ? entry < o.entry : hu != o.hu ? hu < o.hu : kt < o.kt;
+    }
+    __device__ __forceinline__ bool same_unit(const PagedCut &o) const { return entry == o.entry && hu == o.hu; }
+};
+
+constexpr int kPagedPlanThreads = 512;
+// What a unit costs besides its key tiles, in tiles (its query tile's way in and
+// its output's way out: about 4 us of 0.9 a tile).
+constexpr int32_t kPagedUnitTiles = 4;
+// Least weight of a cluster's run: shorter runs leave more pieces than they save.
+constexpr int64_t kPagedMinRun = 2 * kPagedUnitTiles;
+constexpr int32_t kPagedClusters = kDecodeSms / 2;   // at most
+
+// The plan, at the start of the workspace.
+struct PagedDeal {
+    int32_t clusters;                              // with tiles
+    int32_t chunks;                                // of the few-row sequences, per pair
+    int64_t per;                                   // chunks of a warp
+    PagedCut cut[kPagedClusters + 1];              // cluster c: cut[c] .. cut[c + 1]
+};
+static_assert(sizeof(PagedDeal) <= kPagedHead, "the plan's place in the workspace");
+
+struct PagedPlan {
+    const int32_t *cu, *lens;
+    int32_t n_seqs, group, tile_tokens, head_units, heads;
+    int64_t total_q, most_keys;
+    int32_t causal, chunk_shift, page_shift, chunk_bytes, tile_ns, grid;
+    float sm_rate;
+    PagedDeal *deal;
+    PagedEntry *entries;
+    int32_t *chunk_start, *few_start;              // [n_seqs + 1]: chunks, tokens of the few-row sequences before b
+    int32_t *few_seq;                              // sequence of each token of those
+    CUtensorMap *maps;                             // [n_seqs]: of a sequence's last page
+    int32_t *flag;
+};
+
+// Rows of a key head that run as a few-row sequence: at most the 16 of an mma, or
+// one token's, in groups of 16.
+__device__ __forceinline__ bool paged_few(int32_t Lq, int32_t group)
+{
+    return Lq == 1 || (int64_t)Lq * group <= 16;
+}
+
+// A sequence's new tokens and keys; false when an offset or the length is out of range.
+__device__ __forceinline__ bool paged_sequence(const int32_t *cu, const int32_t *lens, int32_t b, int64_t total_q,
+                                               int64_t most, int32_t &Lq, int32_t &Lk)
+{
+    const int32_t q0 = __ldg(cu + b), q1 = __ldg(cu + b + 1);
+    Lk = __ldg(lens + b);
+    Lq = q1 - q0;
+    return q0 >= 0 && q0 <= q1 && q1 <= total_q && Lk >= 0 && Lk <= most;
+}
+
+// Inclusive sums over the CTA of two 32-bit and one 64-bit number; returns the totals.
+struct PagedSums {
+    int32_t a, b;
+    int64_t c;
+};
+__device__ __forceinline__ PagedSums paged_scan(PagedSums x, PagedSums &total, PagedSums *warp_sum)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t a = __shfl_up_sync(0xffffffffu, x.a, d), b = __shfl_up_sync(0xffffffffu, x.b, d);
+        const int64_t c = __shfl_up_sync(0xffffffffu, x.c, d);
+        if (lane >= d) {
+            x.a += a;
+            x.b += b;
+            x.c += c;
+        }
+    }
+    __syncthreads();                               // the last scan's sums are read
+    if (lane == 31)
+        warp_sum[warp] = x;
+    __syncthreads();
+    total = {0, 0, 0};
+    for (int w = 0; w < kPagedPlanThreads / 32; ++w) {
+        const PagedSums s = warp_sum[w];
+        if (w < warp) {
+            x.a += s.a;
+            x.b += s.b;
+            x.c += s.c;
+        }
+        total.a += s.a;
+        total.b += s.b;
+        total.c += s.c;
+    }
+    return x;
+}
+
+// Where position p of the weights falls in the units; a cut that would leave a piece
+// of less than two key tiles goes to the unit's start or to the next one's.
+__device__ __forceinline__ PagedCut paged_cut(const PagedPlan &p, int64_t pos, int32_t n_entries)
+{
+    int32_t lo = 0, hi = n_entries - 1;            // the last entry that starts at pos or before
+    while (lo < hi) {
+        const int32_t mid = lo + (hi - lo + 1) / 2;
+        if (p.entries[mid].before <= pos)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int32_t n = p.entries[lo].n_tiles, weight = n + kPagedUnitTiles;
+    const int64_t in = pos - p.entries[lo].before;
+    PagedCut c;
+    c.entry = lo;
+    c.hu = (int32_t)divide(in, weight);
+    const int32_t off = (int32_t)(in - (int64_t)c.hu * weight), kt = off - kPagedUnitTiles / 2;
+    c.kt = kt < 2 ? 0 : kt;
+    if (n < 4 ? 2 * off >= weight : kt > n - 2) {
+        c.kt = 0;
+        ++c.hu;
+    } else if (n < 4) {
+        c.kt = 0;
+    }
+    if (c.hu == p.head_units) {
+        c.hu = 0;
+        ++c.entry;
+    }
+    return c;
+}
+
+// Estimated time, in ns, with c clusters on the tiles and the few-row chunks on the
+// SMs left over (as plan_ns: an estimate that is off costs balance, never a result).
+__device__ __forceinline__ float paged_ns(const PagedPlan &p, int32_t c, float weight, float chunks)
+{
+    const float bytes = chunks * (float)p.heads * (float)p.chunk_bytes;
+    const float tiles = c > 0 ? weight * (float)p.tile_ns / (float)c : 0.0f;
+    if (bytes == 0.0f)
+        return tiles;
+    if (2 * c >= p.grid)
+        return tiles + 10000.0f + bytes / fminf(6600.0f, p.sm_rate * (float)p.grid);
+    const float few = bytes / fminf(6600.0f, p.sm_rate * (float)(p.grid - 2 * c));
+    return fmaxf(tiles, few) + 0.05f * fminf(tiles, few);
+}
+
+static __device__ void paged_plan(const PagedPlan &p)
+{
+    __shared__ int32_t entry_start[kMaxDecodeBatch + 1];
+    __shared__ PagedSums warp_sum[kPagedPlanThreads / 32];
+    __shared__ uint32_t best[kPagedPlanThreads / 32][2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    bool bad = false;
+    for (int32_t b = tid; b < p.n_seqs; b += kPagedPlanThreads) {
+        int32_t Lq, Lk;
+        bad = bad || !paged_sequence(p.cu, p.lens, b, p.total_q, p.most_keys, Lq, Lk);
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) {                                     // nothing is written
+        if (tid == 0) {
+            atomicOr(p.flag, kFlagIndex);
+            p.deal->clusters = 0;
+            p.deal->chunks = 0;
+            p.deal->per = 1;
+            p.few_start[p.n_seqs] = 0;
+        }
+        return;
+    }
+    // entries, chunks and few-row tokens of the sequences before each
+    PagedSums carry = {0, 0, 0};                   // chunks, few-row tokens, entries
+    for (int32_t b0 = 0; b0 < p.n_seqs; b0 += kPagedPlanThreads) {
+        const int32_t b = b0 + tid;
+        PagedSums x = {0, 0, 0};
+        if (b < p.n_seqs) {
+            int32_t Lq, Lk;
+            paged_sequence(p.cu, p.lens, b, p.total_q, p.most_keys, Lq, Lk);
+            if (Lq > 0 && paged_few(Lq, p.group)) {
+                x.a = (int32_t)(((int64_t)Lk + (1 << p.chunk_shift) - 1) >> p.chunk_shift);
+                x.b = Lq;
+            } else {
+                x.c = ((int64_t)Lq + p.tile_tokens - 1) / p.tile_tokens;
+            }
+        }
+        PagedSums total;
+        const PagedSums inc = paged_scan(x, total, warp_sum);
+        if (b < p.n_seqs) {
+            p.chunk_start[b] = carry.a + inc.a - x.a;
+            p.few_start[b] = carry.b + inc.b - x.b;
+            for (int32_t i = 0; i < x.b; ++i)
+                p.few_seq[carry.b + inc.b - x.b + i] = b;
+            entry_start[b] = (int32_t)(carry.c + inc.c - x.c);
+        }
+        carry.a += total.a;
+        carry.b += total.b;
+        carry.c += total.c;
+    }
+    const int32_t n_entries = (int32_t)carry.c;
+    if (tid == 0) {
+        p.chunk_start[p.n_seqs] = carry.a;
+        p.few_start[p.n_seqs] = carry.b;
+        entry_start[p.n_seqs] = n_entries;
+    }
+    __syncthreads();
+    // the entries, and their weights' sums
+    int64_t weight = 0;
+    for (int32_t e0 = 0; e0 < n_entries; e0 += kPagedPlanThreads) {
+        const int32_t e = e0 + tid;
+        PagedEntry x = {};
+        PagedSums w = {0, 0, 0};
+        if (e < n_entries) {
+            x.seq = find_sequence(entry_start, p.n_seqs + 1, e);
+            paged_sequence(p.cu, p.lens, x.seq, p.total_q, p.most_keys, x.Lq, x.Lk);
+            x.q_start = __ldg(p.cu + x.seq);
+            x.tok0 = (e - entry_start[x.seq]) * p.tile_tokens;
+            x.n_tiles = packed_key_tiles(x.tok0, p.tile_tokens, x.Lq, x.Lk, p.causal);
+            w.c = (int64_t)p.head_units * (x.n_tiles + kPagedUnitTiles);
+        }
+        PagedSums total;
+        const PagedSums inc = paged_scan(w, total, warp_sum);
+        if (e < n_entries) {
+            x.before = weight + inc.c - w.c;
+            p.entries[e] = x;
+        }
+        weight += total.c;
+    }
+    // clusters for the tiles
+    int64_t most = weight / kPagedMinRun;
+    most = most < 1 ? 1 : most;
+    const int32_t top = weight == 0 ? 0 : (int32_t)(most < p.grid / 2 ? most : p.grid / 2);
+    if (warp * 32 < kPagedClusters) {
+        const int32_t c = tid + 1;
+        const uint32_t t = c <= top ? __float_as_uint(paged_ns(p, c, (float)weight, (float)carry.a)) : 0xffffffffu;
+        const uint32_t m = __reduce_min_sync(0xffffffffu, t);
+        const uint32_t at = __reduce_min_sync(0xffffffffu, t == m ? (uint32_t)c : 0xffffffffu);
+        if (lane == 0) {
+            best[warp][0] = m;
+            best[warp][1] = at;
+        }
+    }
+    __syncthreads();                               // (the entries are written, too)
+    uint32_t m = best[0][0], at = best[0][1];
+    for (int w = 1; w * 32 < kPagedClusters; ++w) {
+        if (best[w][0] < m) {
+            m = best[w][0];
+            at = best[w][1];
+        }
+    }
+    const int32_t clusters = weight == 0 ? 0 : (int32_t)at;
+    if (tid <= clusters && clusters > 0) {
+        const int64_t per = (weight + clusters - 1) / clusters, pos = per * tid;
+        PagedCut c = {n_entries, 0, 0};
+        if (pos < weight && tid < clusters)
+            c = paged_cut(p, pos, n_entries);
+        p.deal->cut[tid] = c;
+    }
+    if (tid == 0) {
+        const int32_t used = 2 * clusters < p.grid ? 2 * clusters : 0;
+        p.deal->clusters = clusters;
+        p.deal->chunks = carry.a;
+        p.deal->per = decode_per_warp((int64_t)carry.a * p.heads, (p.grid - used) * kDecWarps);
+    }
+}
+
+// The plan (CTA 0), and the maps of last pages (the others, a sequence a warp).
+static __global__ void __launch_bounds__(kPagedPlanThreads)
+    rope_paged_plan_kernel(const PagedPlan p, const __grid_constant__ CUtensorMap tmpl)
+{
+    __shared__ __align__(128) CUtensorMap buf[kPagedPlanThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    if (blockIdx.x == 0) {
+        paged_plan(p);
+        return;
+    }
+    constexpr int kWarps = kPagedPlanThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    CUtensorMap *mine = &buf[warp];
+    for (int32_t b = ((int)blockIdx.x - 1) * kWarps + warp; b < p.n_seqs; b += ((int)gridDim.x - 1) * kWarps) {
+        int32_t Lq, Lk;
+        const int32_t page = 1 << p.page_shift;
+        if (!paged_sequence(p.cu, p.lens, b, p.total_q, p.most_keys, Lq, Lk) || Lq == 0 || paged_few(Lq, p.group) ||
+            (Lk & (page - 1)) == 0)
+            continue;
+        reinterpret_cast<uint32_t *>(mine)[lane] = reinterpret_cast<const uint32_t *>(&tmpl)[lane];
+        __syncwarp();
+        if (lane == 0)
+            asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;"
+                         ::"r"(attn_smem_u32(mine)), "r"(Lk & (page - 1))
+                         : "memory");
+        __syncwarp();
+        asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync."
+                     "aligned [%0], [%1], 128;"
+                     ::"l"(p.maps + b), "r"(attn_smem_u32(mine))
+                     : "memory");
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the few-row sequences: what decode_suffixes asks of its arguments
+
+struct PagedFew {
+    AttnArgs a;                                // cos, sin (null: queries as they are), table_rows, scale, flag
+    CUtensorMap k_map, v_map;                  // boxes of 64 features x a chunk's keys, or a page's
+    const void *q;                             // [total_q][Hq][D], token stride q_stride
+    int64_t q_stride;
+    const int32_t *table, *lens, *cu, *pos_q;
+    int64_t max_blocks, n_pages;
+    int32_t n_seqs, Hq, Hk, page_shift, chunk_shift, row_groups, rows;
+    const int32_t *chunk_start, *few_start;
+    float *out;                                // [rows of all parts][D]
+    float2 *stats;
+
+    static constexpr bool kRowLimits = true;   // causal: a token sees the keys up to its own
+    __device__ __forceinline__ int32_t sequences() const { return n_seqs; }
+    __device__ __forceinline__ int32_t heads() const { return Hk * row_groups; }
+    __device__ __forceinline__ int64_t most_keys() const { return max_blocks << page_shift; }
+    __device__ __forceinline__ int32_t tokens(int32_t b) const { return __ldg(cu + b + 1) - __ldg(cu + b); }
+    // (offsets and lengths are in range: otherwise the plan has no chunks)
+    __device__ __forceinline__ int32_t keys(int32_t b, int64_t) const
+    {
+        const int32_t Lq = tokens(b);
+        return Lq > 0 && paged_few(Lq, Hq / Hk) ? __ldg(lens + b) : 0;
+    }
+    __device__ __forceinline__ const int32_t *blocks(int32_t b, int64_t &listed) const
+    {
+        listed = max_blocks;
+        return table + b * max_blocks;
+    }
+    // Rows of a pair: heads of a token, token after token; with more than 16 heads in
+    // a group 16 of one token.
+    template <typename T, int D>
+    __device__ __forceinline__ const T *query(int32_t b, int32_t hr, int32_t r, int64_t, bool rot,
+                                              int64_t &trow) const
+    {
+        const int32_t kv = hr / row_groups, group = Hq / Hk, h0 = (hr - kv * row_groups) * rows;
+        const int32_t start = __ldg(cu + b), Lq = __ldg(cu + b + 1) - start;
+        const int32_t tok = r / rows, h = h0 + r - tok * rows;
+        if (tok >= Lq || h >= group)
+            return nullptr;
+        if (rot)
+            trow = row_of(start, tok, (int64_t)__ldg(lens + b) - Lq + tok);
+        return static_cast<const T *>(q) + (start + tok) * q_stride + (int64_t)(kv * group + h) * D;
+    }
+    // Table row of a token: pos_q's, or its index among its sequence's keys.  -1: as it is.
+    __device__ __forceinline__ int64_t row_of(int32_t start, int32_t tok, int64_t index) const
+    {
+        if (a.cos == nullptr)
+            return -1;
+        const int64_t row = pos_q != nullptr ? (int64_t)__ldg(pos_q + start + tok) : index;
+        if (row >= 0 && row < a.table_rows)
+            return row;
+        // (a token before the sequence's first key sees none when causal: its row does not matter)
+        if (pos_q != nullptr ? row != -1 : !(a.causal && row < 0))
+            atomicOr(a.flag, kFlagPosition);
+        return -1;
+    }
+    __device__ __forceinline__ int32_t limit(int32_t b, int32_t r, int32_t n) const
+    {
+        if (!a.causal)
+            return n;
+        const int32_t seen = n - tokens(b) + r / rows + 1;
+        return seen < n ? seen : n;
+    }
+    // A run's part of a pair has as many rows as the pair, at row 16 w + the rows of the
+    // pairs before it: w, the pair or both grow from one part to the next, a pair has at
+    // most 16 rows, so parts do not meet.
+    __device__ __forceinline__ int64_t part_row(int32_t w, int32_t b, int32_t hr) const
+    {
+        const int32_t kv = hr / row_groups, group = Hq / Hk;
+        const int64_t in = row_groups > 1 ? (int64_t)kv * group + (hr - kv * row_groups) * rows
+                                          : (int64_t)kv * group * tokens(b);
+        return 16 * (int64_t)w + (int64_t)__ldg(few_start + b) * Hq + in;
+    }
+    __device__ __forceinline__ int32_t part_rows(int32_t b, int32_t hr) const
+    {
+        const int32_t kv = hr / row_groups, group = Hq / Hk, left = group - (hr - kv * row_groups) * rows;
+        return row_groups > 1 ? (left < rows ? left : rows) : group * tokens(b);
+    }
+    __device__ __forceinline__ void publish(const int32_t *, int64_t) const {}     // (the plan has done so)
+};
+
+// ---------------------------------------------------------------------------
+// the tiles, with the few-row sequences beside or behind them
+
+struct PagedSource {
+    static constexpr bool kFullUnroll = true;
+    static constexpr bool kParts = true, kAllParts = false;
+    static constexpr bool kFinish = true;
+    template <int D>
+    static constexpr int smem_bytes()
+    {
+        const int tiles = (int)kPackedSmem<D> + 4 * (kMaxDecodeBatch + 2);
+        return tiles > kDecSmem<D> ? tiles : kDecSmem<D>;
+    }
+    AttnArgs a;                                // o, Hq, cos, sin, table_rows, rotary_dim, scale, causal, flag
+    CUtensorMap k_map, v_map, q_map, o_map;    // the pools; queries and outputs of all sequences
+    PagedFew few;
+    const PagedDeal *deal;
+    const PagedEntry *entries;
+    const CUtensorMap *maps;                   // [n_seqs]: last pages
+    float *out;                                // [2 clusters][256][D]: a run's first piece and its last
+    float2 *stats;
+    int32_t head_units, units_per_kv, tile_tokens;
+
+    using Cursor = PagedCut;
+    struct Walk {
+        PagedCut begin, end;
+        int32_t cid, clusters, chunks;
+    };
+    template <int D>
+    __device__ __forceinline__ Walk walk(int64_t cid, int64_t, uint8_t *) const
+    {
+        Walk w;
+        w.cid = (int32_t)cid;
+        w.clusters = __ldg(&deal->clusters);
+        w.chunks = __ldg(&deal->chunks);
+        w.begin = w.end = {0, 0, 0};
+        if (w.cid < w.clusters) {
+            w.begin = load_cut(w.cid);
+            w.end = load_cut(w.cid + 1);
+        }
+        return w;
+    }
+    __device__ __forceinline__ PagedCut load_cut(int32_t i) const
+    {
+        const PagedCut *c = deal->cut + i;
+        return {__ldg(&c->entry), __ldg(&c->hu), __ldg(&c->kt)};
+    }
+    __device__ __forceinline__ Cursor first(const Walk &w) const { return w.begin; }
+    __device__ __forceinline__ bool valid(const Walk &w, const Cursor &c) const { return c.before(w.end); }
+    __device__ __forceinline__ int32_t tiles(const Walk &w, const Cursor &c) const
+    {
+        const int32_t n = c.same_unit(w.end) ? w.end.kt : __ldg(&entries[c.entry].n_tiles);
+        return n - c.kt;
+    }
+    __device__ __forceinline__ void next(const Walk &w, Cursor &c) const
+    {
+        if (c.same_unit(w.end)) {
+            c.kt = w.end.kt;
+            return;
+        }
+        c.kt = 0;
+        if (++c.hu == head_units) {
+            c.hu = 0;
+            ++c.entry;
+        }
+    }
+    __device__ __forceinline__ PackedUnit unit(const Walk &w, const Cursor &c, int lg) const
+    {
+        const int4 x = __ldg(reinterpret_cast<const int4 *>(entries + c.entry));
+        const int2 y = __ldg(reinterpret_cast<const int2 *>(entries + c.entry) + 2);
+        PackedUnit u;
+        u.seq = x.x; u.tok0 = x.y; u.tokens = x.z; u.n_keys = x.w;
+        u.q_start = y.x; u.k_start = 0;
+        u.first = c.kt;
+        const bool ends = c.same_unit(w.end);      // the run's cut goes through this unit
+        u.n_tiles = (ends ? w.end.kt : y.y) - c.kt;
+        u.head0 = c.hu << lg;
+        u.kv = c.hu / units_per_kv;
+        u.part = c.kt == 0 && !ends ? -1 : 2 * w.cid + (c.same_unit(w.begin) ? 0 : 1);
+        return u;
+    }
+    __device__ __forceinline__ int64_t table_row(const PackedUnit &u, int32_t t) const
+    {
+        return few.row_of(u.q_start, t, (int64_t)u.n_keys - u.tokens + t);
+    }
+
+    // z of page i of the unit's sequence in the pools' maps; past the last page, and for
+    // a bad page number, an index that arrives as zeros
+    __device__ __forceinline__ int32_t page_z(const PackedUnit &u, int32_t i) const
+    {
+        const int32_t none = (int32_t)(few.n_pages * few.Hk);
+        if ((int64_t)i << few.page_shift >= u.n_keys)
+            return none;
+        const int32_t p = __ldg(few.table + u.seq * few.max_blocks + i);
+        if (p < 0 || p >= few.n_pages) {
+            atomicOr(a.flag, kFlagIndex);
+            return none;
+        }
+        return p * few.Hk + u.kv;
+    }
+    // (keys that other units read too stay in L2)
+    __device__ __forceinline__ uint64_t policy(const PackedUnit &u) const
+    {
+        return u.tokens > tile_tokens || units_per_kv > 1 ? l2_keep() : l2_once();
+    }
+    template <int D>
+    __device__ __forceinline__ int32_t key_place(const PackedUnit &u, int32_t kt, uint32_t rank, int lane) const
+    {
+        const int32_t shift = few.page_shift < 6 ? few.page_shift : 6;  // keys of a box: a page or half of one
+        const int32_t key = (u.first + kt) * kAttnKeys + 64 * (int)rank + (lane / (D / 64) << shift);
+        return lane < (64 >> shift) * (D / 64) ? page_z(u, key >> few.page_shift) : 0;
+    }
+    template <int D>
+    __device__ __forceinline__ int32_t value_place(const PackedUnit &u, int32_t kt, int lane) const
+    {
+        return lane < kAttnKeys >> few.page_shift
+                   ? page_z(u, ((u.first + kt) * kAttnKeys >> few.page_shift) + lane)
+                   : 0;
+    }
+    __device__ __forceinline__ void acquire(const PackedUnit &u, int32_t &seq) const
+    {
+        if (u.seq != seq && (u.n_keys & ((1 << few.page_shift) - 1)) != 0)
+            acquire_map(maps + u.seq);
+        seq = u.seq;
+    }
+    template <int D>
+    __device__ __forceinline__ void load_keys(const PackedUnit &u, int32_t, int32_t z, uint8_t *dst,
+                                              uint64_t *bar, uint32_t rank, int lane) const
+    {
+        const int32_t shift = few.page_shift < 6 ? few.page_shift : 6;
+        if (lane < (64 >> shift) * (D / 64)) {
+            const int32_t i = lane / (D / 64), x = lane % (D / 64);
+            load_half_box_l2(dst + x * 8192 + (i << shift) * 128, &k_map, x * 64,
+                             (64 * (int)rank + (i << shift)) & ((1 << few.page_shift) - 1), z, bar, rank,
+                             policy(u));
+        }
+    }
+    template <int D>
+    __device__ __forceinline__ void load_values(const PackedUnit &u, int32_t kt, int32_t z, uint8_t *dst,
+                                                uint64_t *bar, uint32_t rank, int lane) const
+    {
+        if (lane < kAttnKeys >> few.page_shift) {
+            const int32_t page = ((u.first + kt) * kAttnKeys >> few.page_shift) + lane;
+            // the last, partly filled page: rows past the sequence's end arrive as zeros
+            const bool tail = page == u.n_keys >> few.page_shift && (u.n_keys & ((1 << few.page_shift) - 1)) != 0;
+            load_half_box_l2(dst + (lane << few.page_shift) * D, tail ? maps + u.seq : &v_map,
+                             D / 2 * (int)rank, 0, z, bar, rank, policy(u));
+        }
+    }
+    // One helper warp: its rows' O, m and l of a piece, in fp32
+    template <int D>
+    __device__ __forceinline__ void store_rows(const PackedUnit &u, uint32_t o_base, int32_t y0, int lane,
+                                               int lg, float2 stat) const
+    {
+        const int64_t row = (int64_t)u.part * (2 * kAttnRows) + ((y0 - u.tok0) << lg) + lane;
+        const bool live = y0 + (lane >> lg) < u.tokens;
+        if (live)
+            stats[row] = stat;
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+            float ov[32];
+            tmem_ld32(o_base + c0, ov);
+            if (live) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 4)
+                    *reinterpret_cast<float4 *>(out + row * D + c0 + c) =
+                        make_float4(ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
+            }
+        }
+    }
+    // The few-row sequences, on the CTAs without tiles, or on all behind them (as
+    // PrefixSource::finish).
+    template <typename T, int LAYOUT, int D>
+    __device__ __forceinline__ void finish(const Walk &w, uint8_t *smem, bool failed) const
+    {
+        __shared__ SuffixShared<D> sh;
+        const int32_t used = 2 * w.clusters < (int32_t)gridDim.x ? 2 * w.clusters : 0;
+        const int32_t cta = (int32_t)blockIdx.x - used;
+        // (after an expired wait copies may still be on their way: no work)
+        if (w.chunks == 0 || cta < 0 || failed)
+            return;
+        int32_t *start = reinterpret_cast<int32_t *>(smem + kPackedSmem<D>);
+        for (int32_t b = threadIdx.x; b <= few.n_seqs; b += kPackedThreads)
+            start[b] = __ldg(few.chunk_start + b);
+        __syncthreads();
+        const SuffixRun run = suffix_run<D>(few, start, w.chunks, cta, (int32_t)gridDim.x - used, sh);
+        const int warp = threadIdx.x >> 5;
+        if (warp < 8) {
+            if (warp < 4)
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 216;");
+            else
+                asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+            decode_suffixes<T, LAYOUT, D>(few, smem, run, sh);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// the merge: rows of cut units, a warp each, and rows of few-row sequences, W warps
+// each (W > 1 where there are few of them: merge_parts)
+
+struct PagedMerge {
+    PagedFew few;
+    const PagedDeal *deal;
+    const PagedEntry *entries;
+    const float *out;
+    const float2 *stats;
+    void *o;
+    const int32_t *few_seq;
+    int32_t lg;
+};
+
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_paged_merge_kernel(const __grid_constant__ PagedMerge g)
+{
+    constexpr int kWarps = W == 1 ? 4 : W;
+    const int warp = threadIdx.x >> 5;
+    const PagedFew &f = g.few;
+    pdl_wait();
+    pdl_trigger();
+    const int32_t clusters = __ldg(&g.deal->clusters);
+    const int64_t per = __ldg(&g.deal->per);
+    // Cut i, where it goes through a unit that no earlier cut goes through: that unit's
+    // 256 rows, a warp each.
+    constexpr int kSteps = 256 / kWarps;
+    for (int32_t item = blockIdx.x; item < (clusters - 1) * kSteps; item += gridDim.x) {
+        const int32_t i = 1 + item / kSteps, r = (item % kSteps) * kWarps + warp;
+        const PagedCut *cut = g.deal->cut;
+        const PagedCut c = cut[i], before = cut[i - 1];
+        const bool shared = before.same_unit(c);
+        if (c.kt == 0 || (shared && before.kt > 0))
+            continue;
+        const PagedEntry e = g.entries[c.entry];
+        const int32_t tok = e.tok0 + (r >> g.lg);
+        if (tok >= e.Lq)
+            continue;
+        int32_t n = 2;                                         // pieces
+        for (int32_t j = i + 1; j < clusters && cut[j].same_unit(c) && cut[j].kt > 0; ++j)
+            ++n;
+        const int32_t first = 2 * (i - 1) + (shared ? 0 : 1);
+        T *dst = static_cast<T *>(g.o) +
+                 ((int64_t)(e.q_start + tok) * f.Hq + (c.hu << g.lg) + (r & ((1 << g.lg) - 1))) * D;
+        merge_parts<T, D, 1>(n, dst, [&](int32_t p, float2 &stat) {
+            const int64_t at = (int64_t)(p == 0 ? first : 2 * (i + p - 1)) * 256 + r;
+            stat = __ldg(g.stats + at);
+            return g.out + at * D;
+        });
+    }
+    // The few-row sequences: (token, head).
+    constexpr int kRows = W == 1 ? kWarps : 1;                 // of a CTA at once
+    const int64_t rows = (int64_t)__ldg(f.few_start + f.n_seqs) * f.Hq;
+    const int32_t group = f.Hq / f.Hk, heads = f.heads();
+    for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < rows; row0 += (int64_t)gridDim.x * kRows) {
+        const int64_t row = row0 + (W == 1 ? warp : 0);
+        if (row >= rows)
+            continue;
+        const int32_t t = (int32_t)divide(row, f.Hq), h = (int32_t)(row - (int64_t)t * f.Hq);
+        const int32_t b = __ldg(g.few_seq + t), tok = t - __ldg(f.few_start + b), start = __ldg(f.cu + b);
+        const int32_t kv = h / group, in_group = h - kv * group, rg = in_group / f.rows;
+        const int32_t hr = kv * f.row_groups + rg, r = tok * f.rows + in_group - rg * f.rows;
+        const int64_t c0 = __ldg(f.chunk_start + b), c1 = __ldg(f.chunk_start + b + 1);
+        int64_t first = 0;
+        int32_t n = 0;
+        if (c1 > c0) {
+            const int64_t at = c0 * heads + hr * (c1 - c0);
+            first = divide(at, per);
+            n = (int32_t)(divide(at + (c1 - c0) - 1, per) - first + 1);
+        }
+        if constexpr (W > 1)
+            __syncthreads();                                   // the last row's parts are read
+        merge_parts<T, D, W>(n, static_cast<T *>(g.o) + ((int64_t)(start + tok) * f.Hq + h) * D,
+                             [&](int32_t p, float2 &stat) {
+                                 const int64_t at = f.part_row((int32_t)first + p, b, hr) + r;
+                                 stat = __ldg(f.stats + at);
+                                 return (const float *)f.out + at * D;
+                             });
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+template <typename T, int LAYOUT, int D>
+static cudaError_t launch_paged(const PagedCall &c, const PagedLayout &lay, cudaStream_t st)
+{
+    EncodeTiledFn enc = encode_tiled();
+    if (enc == nullptr)
+        return cudaErrorNotSupported;
+    const CUtensorMapDataType dt = std::is_same<T, __nv_bfloat16>::value
+                                       ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    uint8_t *ws = static_cast<uint8_t *>(c.workspace);
+    const int64_t page = (int64_t)1 << c.page_shift, z = c.n_pages * c.Hk;
+    const int32_t group = c.Hq / c.Hk, gp = packed_group_heads(c.Hq, c.Hk), lg = __builtin_ctz((unsigned)gp);
+    int sms = 0, dev = 0;
+    cudaError_t e = sm_count(&sms, &dev);
+    if (e != cudaSuccess)
+        return e;
+    const int32_t clusters = (sms < kDecodeSms ? sms : kDecodeSms) / 2;
+
+    PagedSource s;
+    memset(&s, 0, sizeof s);
+    AttnArgs &a = s.a;
+    a.o = c.o; a.Hq = c.Hq;
+    a.cos = c.cos; a.sin = c.sin; a.rotary_dim = c.rotary_dim; a.table_rows = c.table_rows;
+    a.scale_log2 = c.scale_log2; a.causal = c.causal; a.flag = c.flag;
+    PagedFew &f = s.few;
+    f.a = a;
+    f.q = c.q; f.q_stride = c.q_stride;
+    f.table = c.table; f.lens = c.lens; f.cu = c.cu; f.pos_q = c.pos_q;
+    f.max_blocks = c.max_blocks; f.n_pages = c.n_pages;
+    f.n_seqs = c.n_seqs; f.Hq = c.Hq; f.Hk = c.Hk; f.page_shift = c.page_shift;
+    f.chunk_shift = __builtin_ctz((unsigned)kDecKeys<D>);
+    f.rows = group < 16 ? group : 16;
+    f.row_groups = (group + f.rows - 1) / f.rows;
+    f.chunk_start = reinterpret_cast<int32_t *>(ws + lay.chunk_start);
+    f.few_start = reinterpret_cast<int32_t *>(ws + lay.few_start);
+    f.out = reinterpret_cast<float *>(ws + lay.few_out);
+    f.stats = reinterpret_cast<float2 *>(ws + lay.few_stats);
+    const uint32_t chunk_box = (uint32_t)(page < kDecKeys<D> ? page : kDecKeys<D>), box = (uint32_t)(page < 64 ? page : 64);
+    const uint32_t g = (uint32_t)gp;
+    // (without pages the pools' maps stand on the workspace, and no key is ever copied)
+    const void *kp = z > 0 ? c.k_pages : ws, *vp = z > 0 ? c.v_pages : ws;
+    const int64_t zs = z > 0 ? z : 1;
+    if (!encode_3d(enc, &f.k_map, kp, dt, {D, page, zs}, {D * 2, page * D * 2}, {64, chunk_box, 1}, sw) ||
+        !encode_3d(enc, &f.v_map, vp, dt, {D, page, zs}, {D * 2, page * D * 2}, {64, chunk_box, 1}, sw) ||
+        !encode_3d(enc, &s.k_map, kp, dt, {D, page, zs}, {D * 2, page * D * 2}, {64, box, 1}, sw) ||
+        !encode_3d(enc, &s.v_map, vp, dt, {D, page, zs}, {D * 2, page * D * 2}, {(uint32_t)D / 2, (uint32_t)page, 1},
+                   D == 128 ? sw : CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_3d(enc, &s.q_map, c.q, dt, {D, c.Hq, c.total_q}, {D * 2, c.q_stride * 2}, {64, g, kAttnRows / g}, sw) ||
+        !encode_3d(enc, &s.o_map, c.o, dt, {D, c.Hq, c.total_q}, {D * 2, (int64_t)c.Hq * D * 2}, {64, g, 32 / g}, sw))
+        return cudaErrorInvalidValue;
+    s.deal = reinterpret_cast<PagedDeal *>(ws);
+    s.entries = reinterpret_cast<PagedEntry *>(ws + lay.entries);
+    s.maps = reinterpret_cast<CUtensorMap *>(ws + lay.maps);
+    s.out = reinterpret_cast<float *>(ws + lay.out);
+    s.stats = reinterpret_cast<float2 *>(ws + lay.stats);
+    s.head_units = c.Hq / gp; s.units_per_kv = group / gp; s.tile_tokens = 2 * kAttnRows / gp;
+
+    PagedPlan p;
+    memset(&p, 0, sizeof p);
+    p.cu = c.cu; p.lens = c.lens; p.n_seqs = c.n_seqs; p.group = group; p.tile_tokens = s.tile_tokens;
+    p.head_units = s.head_units; p.heads = c.Hk * f.row_groups;
+    p.total_q = c.total_q; p.most_keys = c.max_blocks << c.page_shift;
+    p.causal = c.causal; p.chunk_shift = f.chunk_shift; p.page_shift = c.page_shift;
+    p.chunk_bytes = kDecStageBytes<D>; p.tile_ns = D == 128 ? 900 : 700; p.grid = 2 * clusters;
+    p.sm_rate = D == 128 ? 53.0f : 48.0f;
+    p.deal = reinterpret_cast<PagedDeal *>(ws);
+    p.entries = reinterpret_cast<PagedEntry *>(ws + lay.entries);
+    p.chunk_start = reinterpret_cast<int32_t *>(ws + lay.chunk_start);
+    p.few_start = reinterpret_cast<int32_t *>(ws + lay.few_start);
+    p.few_seq = reinterpret_cast<int32_t *>(ws + lay.few_seq);
+    p.maps = reinterpret_cast<CUtensorMap *>(ws + lay.maps);
+    p.flag = c.flag;
+    constexpr int32_t kWarps = kPagedPlanThreads / 32;
+    e = launch_hot(rope_paged_plan_kernel, dim3((unsigned)(1 + (c.n_seqs + kWarps - 1) / kWarps)),
+                   dim3(kPagedPlanThreads), 0, st, p, s.v_map);
+    if (e != cudaSuccess)
+        return e;
+    e = launch_packed_kernel<T, LAYOUT, D>(s, clusters, lg, st);
+    if (e != cudaSuccess)
+        return e;
+    PagedMerge m;
+    memset(&m, 0, sizeof m);
+    m.few = f; m.deal = s.deal; m.entries = s.entries; m.out = s.out; m.stats = s.stats; m.o = c.o;
+    m.few_seq = p.few_seq; m.lg = lg;
+    const unsigned grid = 4 * kDecodeSms;
+    if (lay.few_rows * 8 <= kMergeWarps)
+        return launch_hot(rope_paged_merge_kernel<T, D, 8>, dim3(grid), dim3(256), 0, st, m);
+    if (lay.few_rows * 4 <= kMergeWarps)
+        return launch_hot(rope_paged_merge_kernel<T, D, 4>, dim3(2 * grid), dim3(128), 0, st, m);
+    return launch_hot(rope_paged_merge_kernel<T, D, 1>, dim3(2 * grid), dim3(128), 0, st, m);
+}
+
+template <typename T>
+cudaError_t launch_paged_type(const PagedCall &c, const PagedLayout &lay, int32_t D, int32_t layout, cudaStream_t st)
+{
+    if (layout == 0)
+        return D == 64 ? launch_paged<T, 0, 64>(c, lay, st) : launch_paged<T, 0, 128>(c, lay, st);
+    return D == 64 ? launch_paged<T, 1, 64>(c, lay, st) : launch_paged<T, 1, 128>(c, lay, st);
+}
+
+}  // namespace rope

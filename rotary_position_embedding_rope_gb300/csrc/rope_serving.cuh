@@ -104,6 +104,35 @@ struct DecodeLayout {
 // False when a size overflows or is not taken.
 bool decode_layout(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_shift, int64_t max_blocks,
                    int64_t n_prefix, DecodeLayout *out);
+// Attention of new tokens over a paged cache (rope_attention_paged.cuh).
+struct PagedCall {
+    const void *q;                   // [total_q][Hq][D], token stride q_stride
+    int64_t q_stride;
+    const void *k_pages, *v_pages;   // [n_pages][Hk][page][D]
+    void *o;                         // [total_q][Hq][D]
+    const int32_t *table, *cu, *lens;    // [n_seqs][max_blocks], [n_seqs + 1], [n_seqs]
+    const int32_t *pos_q;            // [total_q] or nullptr
+    const float *cos, *sin;          // nullptr: queries as they are
+    int64_t table_rows, total_q, n_pages, max_blocks;
+    int32_t n_seqs, Hq, Hk, rotary_dim, page_shift, causal;
+    float scale_log2;
+    void *workspace;
+    int32_t *flag;
+};
+constexpr int64_t kPagedHead = 1024;           // bytes of the plan's head: a cut for every cluster
+struct PagedLayout {
+    int64_t few_rows;                // most rows (token, head) of few-row sequences
+    int64_t entries, maps, chunk_start, few_start, few_seq, few_out, few_stats, out, stats;    // byte offsets
+    int64_t bytes;
+};
+// False when a size overflows or is not taken.
+bool paged_layout(int64_t n_seqs, int64_t total_q, int32_t Hq, int32_t Hk, int32_t D, int32_t page_shift,
+                  int64_t max_blocks, PagedLayout *out);
+cudaError_t launch_paged_bf16(const PagedCall &c, const PagedLayout &lay, int32_t D, int32_t layout,
+                              cudaStream_t st);
+cudaError_t launch_paged_f16(const PagedCall &c, const PagedLayout &lay, int32_t D, int32_t layout,
+                             cudaStream_t st);
+
 cudaError_t launch_decode_bf16(const DecodeCall &c, const DecodeLayout &lay, int32_t D, int32_t layout,
                                cudaStream_t st);
 cudaError_t launch_decode_f16(const DecodeCall &c, const DecodeLayout &lay, int32_t D, int32_t layout,

@@ -99,6 +99,39 @@ bool decode_layout(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_sh
     return true;
 }
 
+bool paged_layout(int64_t n_seqs, int64_t total_q, int32_t Hq, int32_t Hk, int32_t D, int32_t page_shift,
+                  int64_t max_blocks, PagedLayout *out)
+{
+    const int64_t group = Hq / Hk, few = group < 16 ? 16 / group : 1;
+    const int64_t chunks = product({n_seqs, max_blocks, (int64_t)1 << page_shift >> 4});
+    const int64_t keys = product({max_blocks, (int64_t)1 << page_shift});
+    if (chunks < 0 || chunks > kMaxInt32 || keys < 0 || keys > kMaxInt32 - 256)
+        return false;
+    const int64_t few_tokens = total_q < n_seqs * few ? total_q : n_seqs * few;
+    out->few_rows = few_tokens * Hq;
+    // tiles: a sequence has at most tokens / tile + 1 of them; none where all the
+    // call's rows of a key head are few
+    const int64_t tile = 256 / packed_group_heads(Hq, Hk);
+    const bool tiles = total_q > 1 && total_q * group > 16;
+    const int64_t entries = tiles ? total_q / tile + (n_seqs < total_q ? n_seqs : total_q) : 0;
+    const int64_t parts = tiles ? (int64_t)kDecodeSms * 256 : 0;              // two pieces of 256 rows a cluster
+    const int64_t part_rows = 16 * 8 * (int64_t)kDecodeSms + out->few_rows;   // 16 a warp
+    const int64_t few_out = product({part_rows, D, 4});
+    if (entries > (1ll << 31) || few_out < 0)
+        return false;
+    out->entries = kPagedHead;
+    out->maps = round_up(out->entries + entries * 32, 128);
+    out->chunk_start = out->maps + n_seqs * 128;
+    out->few_start = out->chunk_start + 4 * (n_seqs + 1);
+    out->few_seq = out->few_start + 4 * (n_seqs + 1);
+    out->few_out = round_up(out->few_seq + 4 * few_tokens, 128);
+    out->few_stats = out->few_out + few_out;
+    out->out = round_up(out->few_stats + 8 * part_rows, 128);
+    out->stats = out->out + parts * D * 4;
+    out->bytes = round_up(out->stats + parts * 8, 128);
+    return true;
+}
+
 }  // namespace rope
 
 using namespace rope;
@@ -342,6 +375,94 @@ rope_status rope_attention_decode_fwd(const void *q, const void *k_pages, const 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == ROPE_BF16 ? launch_decode_bf16(c, lay, D, layout, s)
                                              : launch_decode_f16(c, lay, D, layout, s);
+    return e == cudaSuccess ? ROPE_OK : ROPE_ERR_CUDA;
+}
+
+int64_t rope_attention_paged_workspace(int64_t n_seqs, int64_t total_q, int32_t Hq, int32_t Hk, int32_t D,
+                                       int32_t page_size, int64_t max_blocks)
+{
+    const int32_t shift = page_shift(page_size);
+    PagedLayout lay;
+    if (n_seqs < 0 || n_seqs > kMaxDecodeBatch || total_q < 0 || total_q > kMaxInt32 || Hq < 0 || Hk < 0 ||
+        (D != 64 && D != 128) || shift < 0 || max_blocks < 0)
+        return -1;
+    if (n_seqs == 0 || total_q == 0 || Hq == 0)
+        return 0;
+    if (Hk == 0 || Hq % Hk != 0 || !paged_layout(n_seqs, total_q, Hq, Hk, D, shift, max_blocks, &lay))
+        return -1;
+    return lay.bytes;
+}
+
+rope_status rope_attention_paged_fwd(const void *q, const void *k_pages, const void *v_pages, void *o,
+                                     const int32_t *block_table, const int32_t *cu_seqlens_q,
+                                     const int32_t *seq_lens, const float *cos, const float *sin,
+                                     const int32_t *pos_q, int64_t n_seqs, int64_t total_q, int64_t q_stride,
+                                     int32_t Hq, int32_t Hk, int32_t D, int32_t rotary_dim, int32_t layout,
+                                     int32_t causal, float softmax_scale, int32_t page_size, int64_t n_pages,
+                                     int64_t max_blocks, int32_t dtype, int64_t table_rows, void *workspace,
+                                     int64_t workspace_bytes, void *stream)
+{
+    const bool rotate = cos != nullptr || sin != nullptr;
+    rope_status st = check_shape(dtype, layout, D, rotate ? rotary_dim : D);
+    if (st != ROPE_OK)
+        return st;
+    const int32_t shift = page_shift(page_size);
+    if (shift < 0)
+        return ROPE_ERR_UNSUPPORTED;
+    if ((causal != 0 && causal != 1) || softmax_scale != softmax_scale || n_seqs < 0 || total_q < 0 ||
+        total_q > kMaxInt32 || Hq < 0 || Hk < 0 || n_pages < 0 || max_blocks < 0 || table_rows < 0 || workspace_bytes < 0)
+        return ROPE_ERR_INVALID_ARG;
+    if (n_seqs > kMaxDecodeBatch)
+        return ROPE_ERR_UNSUPPORTED;
+    if (Hq > 0 && (Hk == 0 || Hq % Hk != 0))
+        return ROPE_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)Hq * D;
+    if (q_stride < row)
+        return ROPE_ERR_INVALID_ARG;
+    const int64_t z = product({n_pages, Hk});
+    const int64_t qb = view_bytes(total_q, q_stride, row), ob = product({total_q, row, 2});
+    const int64_t pool = product({n_pages, Hk, page_size, D, 2});
+    const int64_t tab = rotate ? product({table_rows, rotary_dim / 2, 4}) : 0, blocks = product({n_seqs, max_blocks, 4});
+    if (z < 0 || z > kMaxInt32 - 1 || qb < 0 || ob < 0 || pool < 0 || tab < 0 || blocks < 0)
+        return ROPE_ERR_INVALID_ARG;
+    if (n_seqs == 0 || total_q == 0 || Hq == 0)
+        return ROPE_OK;                                  // no output rows
+    if (!q || !o || !cu_seqlens_q || !seq_lens || (rotate && (!cos || !sin || table_rows < 1)) ||
+        (max_blocks > 0 && (!block_table || !k_pages || !v_pages || n_pages < 1)))
+        return ROPE_ERR_INVALID_ARG;
+    PagedLayout lay;
+    if (!paged_layout(n_seqs, total_q, Hq, Hk, D, shift, max_blocks, &lay) || !workspace || workspace_bytes < lay.bytes)
+        return ROPE_ERR_INVALID_ARG;
+    if (q_stride % 8 != 0 || !aligned(q, 16) || !aligned(o, 16) || !aligned(cos, 16) || !aligned(sin, 16) ||
+        !aligned(workspace, 128) || !aligned(k_pages, 16) || !aligned(v_pages, 16))
+        return ROPE_ERR_UNSUPPORTED;
+    if (!aligned(block_table, 4) || !aligned(cu_seqlens_q, 4) || !aligned(seq_lens, 4) || !aligned(pos_q, 4))
+        return ROPE_ERR_INVALID_ARG;
+    const Range outs[2] = {{o, ob}, {workspace, lay.bytes}};
+    const Range ins[9] = {{q, qb}, {k_pages, pool}, {v_pages, pool}, {block_table, blocks},
+                          {cu_seqlens_q, 4 * (n_seqs + 1)}, {seq_lens, 4 * n_seqs}, {cos, tab}, {sin, tab},
+                          {pos_q, 4 * total_q}};
+    if (overlap(outs[0], outs[1]))
+        return ROPE_ERR_INVALID_ARG;
+    for (const Range &out : outs)
+        for (const Range &in : ins)
+            if (overlap(out, in))
+                return ROPE_ERR_INVALID_ARG;
+    PagedCall c;
+    std::memset(&c, 0, sizeof c);
+    c.q = q; c.q_stride = q_stride; c.k_pages = k_pages; c.v_pages = v_pages; c.o = o;
+    c.table = block_table; c.cu = cu_seqlens_q; c.lens = seq_lens; c.pos_q = pos_q;
+    c.cos = cos; c.sin = sin; c.table_rows = table_rows; c.total_q = total_q; c.n_pages = n_pages;
+    c.max_blocks = max_blocks;
+    c.n_seqs = (int32_t)n_seqs; c.Hq = Hq; c.Hk = Hk; c.rotary_dim = rotate ? rotary_dim : D; c.page_shift = shift;
+    c.causal = causal; c.workspace = workspace;
+    const double scale = softmax_scale > 0.0f ? softmax_scale : 1.0 / std::sqrt((double)D);
+    c.scale_log2 = (float)(scale * 1.4426950408889634);
+    if (device_flag(&c.flag) != cudaSuccess)
+        return ROPE_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == ROPE_BF16 ? launch_paged_bf16(c, lay, D, layout, s)
+                                             : launch_paged_f16(c, lay, D, layout, s);
     return e == cudaSuccess ? ROPE_OK : ROPE_ERR_CUDA;
 }
 

@@ -37,6 +37,8 @@ decltype(&rope_norm_qk_bwd) g_norm_bwd = nullptr;
 decltype(&rope_norm_qk_workspace) g_norm_bytes = nullptr;
 decltype(&rope_norm_cache_append) g_norm_append = nullptr;
 decltype(&rope_tables_build_scaled) g_tables_scaled = nullptr;
+decltype(&rope_attention_paged_fwd) g_paged = nullptr;
+decltype(&rope_attention_paged_workspace) g_paged_bytes = nullptr;
 
 // A Python exception has been set.
 struct PythonError {};
@@ -315,7 +317,7 @@ PyObject *status(rope_status st) { return PyLong_FromLong(st); }
 // bind(addresses of the entry points)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
-    constexpr int kEntries = 10;
+    constexpr int kEntries = 12;
     if (n != kEntries) {
         PyErr_Format(PyExc_TypeError, "expected %d addresses", kEntries);
         return nullptr;
@@ -339,6 +341,8 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     g_norm_bytes = reinterpret_cast<decltype(g_norm_bytes)>(p[7]);
     g_norm_append = reinterpret_cast<decltype(g_norm_append)>(p[8]);
     g_tables_scaled = reinterpret_cast<decltype(g_tables_scaled)>(p[9]);
+    g_paged = reinterpret_cast<decltype(g_paged)>(p[10]);
+    g_paged_bytes = reinterpret_cast<decltype(g_paged_bytes)>(p[11]);
     Py_RETURN_NONE;
 }
 
@@ -464,6 +468,64 @@ PyObject *attention_shared_prefix(PyObject *, PyObject *const *a, Py_ssize_t n)
                      qr.stride, qr.H, pool.Hk, qr.D, t.rotary_dim, layout, scale, pool.page, pool.n_pages, blocks,
                      code, t.rows, ws.defined() ? ws.data_ptr() : nullptr,
                      ws.defined() ? (int64_t)ws.nbytes() : 0, c.stream);
+        if (st != ROPE_OK)
+            return status(st);
+        if (a[13] != Py_None)
+            written(out);
+        return THPVariable_Wrap(out);
+    } catch (const PythonError &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// attention_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seq_lens, cos, sin,
+//     pos_q, rotary_dim, layout, causal, scale, out, workspace, stream)
+// -> the output, or a status
+PyObject *attention_paged(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    try {
+        expect(n, 16);
+        const at::Tensor &q = tensor(a[0], "q");
+        const Call c(q, a[15]);
+        const int32_t code = type16(q, "attention_paged");
+        const at::ScalarType type = q.scalar_type();
+        const Rows qr(c, a[0], "q", type);
+        const Cache pool(c, a[1], a[2], type);
+        if (pool.D != qr.D)
+            fail(PyExc_ValueError, "the cache holds heads of " + std::to_string(pool.D) + " features, q of " +
+                                       std::to_string(qr.D));
+        const at::Tensor &table = tensor(a[3], "block_table");
+        if (table.dim() != 2)
+            fail(PyExc_ValueError, "block_table must be [n_seqs, max_blocks], got " + shape_of(table));
+        const int64_t seqs = table.size(0), blocks = table.size(1);
+        const int32_t *list = c.ints(a[3], "block_table", -1), *cu = c.ints(a[4], "cu_seqlens_q", seqs + 1),
+                      *lens = c.ints(a[5], "seq_lens", seqs), *pq = c.ints(a[8], "pos_q", qr.n, true);
+        if ((a[6] == Py_None) != (a[7] == Py_None))
+            fail(PyExc_ValueError, "cos and sin are given together, or neither");
+        const float *cos = nullptr, *sin = nullptr;
+        int64_t rows = 0;
+        int32_t rotary_dim = 0;
+        if (a[6] != Py_None) {
+            const Tables t(c, a[6], a[7], a[9]);
+            cos = t.cos;
+            sin = t.sin;
+            rows = t.rows;
+            rotary_dim = t.rotary_dim;
+            if (cos == nullptr || sin == nullptr)          // (an empty table is not a missing one)
+                fail(PyExc_ValueError, "cos and sin must have rows");
+        }
+        const int32_t layout = (int32_t)integer(a[10]), causal = truth(a[11]);
+        const float scale = a[12] == Py_None ? -1.0f : (float)number(a[12]);
+        const int64_t need = g_paged_bytes(seqs, qr.n, qr.H, pool.Hk, qr.D, pool.page, blocks);
+        // (sizes without a workspace are refused by the call, which says why)
+        const c10::cuda::CUDAGuard guard(c.device);
+        const at::Tensor out = output(c, a[13], qr, type), ws = c.workspace(a[14], need);
+        const rope_status st =
+            unlocked(g_paged, qr.p, pool.k, pool.v, out.data_ptr(), list, cu, lens, cos, sin, pq, seqs, qr.n, qr.stride, qr.H,
+                     pool.Hk, qr.D, rotary_dim, layout, causal, scale, pool.page, pool.n_pages, blocks, code, rows,
+                     ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (int64_t)ws.nbytes() : 0, c.stream);
         if (st != ROPE_OK)
             return status(st);
         if (a[13] != Py_None)
@@ -763,6 +825,8 @@ PyMethodDef g_methods[] = {
      nullptr},
     {"attention_shared_prefix", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention_shared_prefix)),
      METH_FASTCALL, nullptr},
+    {"attention_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention_paged)), METH_FASTCALL,
+     nullptr},
     {"norm_rotate_qk", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_rotate_qk)), METH_FASTCALL, nullptr},
     {"norm_rotate_qk_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_rotate_qk_backward)),
      METH_FASTCALL, nullptr},

@@ -120,3 +120,37 @@ def test_python_refuses_host_tensors():
         R.norm_rotate_qk(None, None, w, w, t, t)
     with pytest.raises(KeyError):
         R.norm_rotate_qk(x, x, w, w, t, t, layout="pairs")
+
+
+PAGED = dict(q=A, kp=2 * A, vp=3 * A, o=4 * A, table=5 * A, cu=6 * A, lens=7 * A, cos=8 * A, sin=9 * A, pq=None, n=3, tq=40, qs=512, Hq=4,
+             Hk=2, D=128, rd=128, layout=0, causal=1, scale=-1.0, page=16, n_pages=20, blocks=4, dtype=1, rows=64, ws=10 * A, wsb=1 << 25)
+
+
+def paged_args(**over):
+    a = dict(PAGED, **over)
+    return [a[x] for x in ("q", "kp", "vp", "o", "table", "cu", "lens", "cos", "sin", "pq", "n", "tq", "qs", "Hq", "Hk", "D", "rd",
+                           "layout", "causal", "scale", "page", "n_pages", "blocks", "dtype", "rows", "ws", "wsb")] + [None]
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=0), UNS), (dict(layout=3), UNS), (dict(D=80), UNS), (dict(rd=24), UNS), (dict(page=24), UNS), (dict(page=256), UNS),
+    (dict(n=4097), UNS), (dict(qs=516), UNS), (dict(q=A + 2), UNS), (dict(o=4 * A + 8), UNS), (dict(kp=2 * A + 8), UNS),
+    (dict(sin=9 * A + 8), UNS), (dict(ws=10 * A + 16), UNS), (dict(n=-1), INV), (dict(tq=-1), INV), (dict(tq=1 << 31), INV),
+    (dict(Hq=5, qs=640), INV), (dict(Hk=0), INV), (dict(qs=504), INV), (dict(causal=2), INV), (dict(blocks=-1), INV), (dict(n_pages=0), INV),
+    (dict(n_pages=1 << 30), INV), (dict(blocks=1 << 40), INV), (dict(blocks=1 << 28), INV), (dict(scale=float("nan")), INV), (dict(rows=0), INV),
+    (dict(cos=None), INV), (dict(sin=None), INV), (dict(q=None), INV), (dict(kp=None), INV), (dict(o=None), INV), (dict(table=None), INV),
+    (dict(cu=None), INV), (dict(lens=None), INV), (dict(ws=None), INV), (dict(wsb=1000), INV), (dict(lens=7 * A + 1), INV), (dict(pq=A + 2), INV),
+    (dict(o=A), INV), (dict(o=3 * A + 128), INV), (dict(ws=2 * A), INV), (dict(ws=6 * A - 128), INV), (dict(ws=4 * A), INV)])
+def test_paged_refuses(lib, over, status):
+    assert lib.rope_attention_paged_fwd(*paged_args(**over)) == status
+
+
+def test_paged_workspace(lib):
+    ws = lib.rope_attention_paged_workspace
+    need = ws(3, 40, 4, 2, 128, 16, 4)
+    assert need > 40 * 4 * 128 * 4 and need % 128 == 0
+    assert lib.rope_attention_paged_fwd(*paged_args(wsb=need - 1)) == INV
+    assert ws(0, 40, 4, 2, 128, 16, 4) == ws(3, 0, 4, 2, 128, 16, 4) == ws(3, 40, 0, 0, 128, 16, 4) == 0
+    assert ws(3, 40, 4, 3, 128, 16, 4) == ws(3, 40, 4, 2, 96, 16, 4) == ws(3, 40, 4, 2, 128, 48, 4) == ws(4097, 5000, 4, 2, 128, 16, 4) == -1
+    assert lib.rope_attention_paged_fwd(*paged_args(tq=0, q=None, o=None, ws=None, wsb=0)) == R.ROPE_OK
+    assert ws(64, 64, 32, 8, 128, 64, 128) < 64 << 20
