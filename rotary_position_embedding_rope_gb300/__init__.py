@@ -414,15 +414,20 @@ def build_tables_scaled(kind: str, rotary_dim: int, rows: int, factor: float, or
     ramp along the pairs, between those of low_turns = 1 and high_turns = 32 turns).
     value_scale: factor of all values; None: 1, for "yarn" 0.1 ln(factor) + 1.
     """
-    device = torch.device("cuda") if device is None else torch.device(device)
-    low = 1.0 if low_turns is None else low_turns
-    high = (32.0 if kind == "yarn" else 4.0) if high_turns is None else high_turns
-    code = _SCALE_CODE[kind]
-    cos, sin = _allocated(lambda: torch.empty((2, rows, rotary_dim // 2), dtype=torch.float32,
-                                              device=device).unbind(0), stream, device)
-    rope_tables_build_scaled(code, theta, rotary_dim, rows, pos_offset, factor, original_positions, low, high,
-                             0.0 if value_scale is None else value_scale, cos, sin, stream)
-    return cos, sin
+    at = -1
+    if device is not None:
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("tables are built on a CUDA device, not on %s" % device)
+        at = -1 if device.index is None else device.index
+    o = (_serving or _native()).build_tables_scaled(
+        _SCALE_CODE[kind], theta, rotary_dim, rows, pos_offset, factor, original_positions,
+        1.0 if low_turns is None else low_turns,
+        (32.0 if kind == "yarn" else 4.0) if high_turns is None else high_turns,
+        0.0 if value_scale is None else value_scale, at, stream)
+    if type(o) is int:
+        raise RopeError(o, "rope_tables_build_scaled")
+    return o
 
 
 def _shape4(x: torch.Tensor, seq_before_head: bool):

@@ -12,7 +12,8 @@ backward writes fresh gradient tensors; both are single launches of the
 CUDA library.
 
 ``norm_rotary_qk`` is the same for ``norm_rotate_qk``, with gradients of both
-weights.  Its backward reads the inputs again: only they are kept.
+weights; its node is csrc/serving_binding.cpp's.  Its backward reads the inputs
+again: only they are kept.
 """
 from __future__ import annotations
 
@@ -20,7 +21,7 @@ import torch
 
 import rotary_position_embedding_rope_gb300 as _package
 
-from . import norm_rotate_qk, norm_rotate_qk_backward, rotate_qk
+from . import rotate_qk
 
 
 class RotaryQK(torch.autograd.Function):
@@ -60,50 +61,6 @@ def rotary_qk(q: torch.Tensor, k: torch.Tensor | None, cos: torch.Tensor, sin: t
     return RotaryQK.apply(q, k, cos, sin, pos_idx, rd, layout, seq_before_head)
 
 
-def _vectors(x):
-    """x itself where the library takes its strides (dense features, whole 16-byte vectors), else a dense copy."""
-    if x is None:
-        return None
-    v = 16 // x.element_size()
-    ok = x.data_ptr() % 16 == 0 and (x.shape[-1] <= 1 or x.stride(-1) == 1) and all(
-        n <= 1 or (s > 0 and s % v == 0) for n, s in zip(x.shape[:-1], x.stride()[:-1]))
-    return x if ok else x.clone(memory_format=torch.contiguous_format)
-
-
-def _dense(g):
-    """g, dense and 16-byte aligned."""
-    g = g.contiguous()
-    return g if g.data_ptr() % 16 == 0 else g.clone()
-
-
-class NormRotaryQK(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, q, k, wq, wk, cos, sin, eps, pos_idx, rotary_dim, layout, seq_before_head):
-        q, k = _vectors(q), _vectors(k)
-        ctx.save_for_backward(q, k, wq, wk, cos, sin, pos_idx)
-        ctx.cfg = (eps, rotary_dim, layout, seq_before_head)
-        ctx.set_materialize_grads(False)
-        return norm_rotate_qk(q, k, wq, wk, cos, sin, eps, pos_idx, rotary_dim, layout, seq_before_head)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, grad_q, grad_k):
-        q, k, wq, wk, cos, sin, pos_idx = ctx.saved_tensors
-        eps, rotary_dim, layout, seq_before_head = ctx.cfg
-        need = ctx.needs_input_grad
-        # an output that took no part in the loss arrives as None, and an input (and weight) that needs no
-        # gradient is left out
-        gq = _dense(grad_q) if grad_q is not None and (need[0] or need[2]) else None
-        gk = _dense(grad_k) if grad_k is not None and (need[1] or need[3]) else None
-        if gq is None and gk is None:
-            return (None,) * 11
-        dq, dk, dwq, dwk = norm_rotate_qk_backward(
-            gq, gk, q if gq is not None else None, k if gk is not None else None, wq if gq is not None else None,
-            wk if gk is not None else None, cos, sin, eps, pos_idx, rotary_dim, layout, seq_before_head,
-            (need[2], need[3]))
-        return (dq if need[0] else None, dk if need[1] else None, dwq, dwk) + (None,) * 7
-
-
 def norm_rotary_qk(q: torch.Tensor | None, k: torch.Tensor | None, wq: torch.Tensor | None,
                    wk: torch.Tensor | None, cos: torch.Tensor, sin: torch.Tensor, eps: float = 1e-6,
                    pos_idx: torch.Tensor | None = None, rotary_dim: int | None = None,
@@ -114,9 +71,8 @@ def norm_rotary_qk(q: torch.Tensor | None, k: torch.Tensor | None, wq: torch.Ten
     While a CUDA graph is captured, no other graph of the same leaves made on another
     stream may be alive (drop the outputs of eager calls first): the call refuses, because
     the captured backward pass could not run."""
-    if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing() and torch.is_grad_enabled():
-        for name, x in (("q", q), ("k", k), ("wq", wq), ("wk", wk)):
-            if x is not None and (_package._serving or _package._native()).accumulates_elsewhere(x):
-                raise RuntimeError("a graph of %s made on another stream is alive: drop it before the backward pass "
-                                   "is captured" % name)
-    return NormRotaryQK.apply(q, k, wq, wk, cos, sin, eps, pos_idx, rotary_dim, layout, seq_before_head)
+    o = (_package._serving or _package._native()).norm_rotary_qk(
+        q, k, wq, wk, cos, sin, eps, pos_idx, rotary_dim, _package._LAYOUT_CODE[layout], seq_before_head)
+    if type(o) is int:
+        raise _package.RopeError(o, "rope_norm_qk_fwd")
+    return o

@@ -40,6 +40,7 @@
 #pragma once
 
 #include "rope_attention.cuh"
+#include "rope_launch.cuh"
 #include "rope_rows.cuh"
 #include "rope_serving.cuh"
 
@@ -550,12 +551,6 @@ __device__ __forceinline__ void prefetch_table_row(const AttnArgs &a, int64_t tr
 // as many: the helpers share the issue slots of the softmax warps).  With w =
 // c d rounded, c d - w is exact, so (a b - w) - (c d - w), each fma rounded
 // once, is diff_of_products's sum (equal up to the sign of a zero).
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ void rotate_pairs2(uint64_t &x1, uint64_t &x2, uint64_t c, uint64_t s)
 {
     const uint64_t minus = 0xbf800000bf800000ull, sign = 0x8000000080000000ull;    // (-1, -1), sign bits
@@ -1165,40 +1160,6 @@ static bool encode_3d(EncodeTiledFn enc, CUtensorMap *m, const void *base, CUten
     const cuuint32_t e[3] = {1, 1, 1};
     return enc(m, dt, 3, const_cast<void *>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Multiprocessors of the current device, looked up once per device.
-static cudaError_t sm_count(int *sms, int *device)
-{
-    static std::atomic<int> known[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
-        return e;
-    if (dev < 0 || dev >= 64)
-        return cudaErrorInvalidDevice;
-    int n = known[dev].load(std::memory_order_acquire);
-    if (n == 0) {
-        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess)
-            return e;
-        known[dev].store(n, std::memory_order_release);
-    }
-    *sms = n;
-    *device = dev;
-    return cudaSuccess;
-}
-
-// Raises a kernel's shared-memory limit, once per device.
-static cudaError_t raise_smem(const void *kernel, int bytes, int device, std::atomic<uint64_t> &raised)
-{
-    const uint64_t bit = (uint64_t)1 << device;
-    if (raised.load(std::memory_order_acquire) & bit)
-        return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess)
-        raised.fetch_or(bit, std::memory_order_acq_rel);
-    return e;
 }
 
 // The attention kernel over at most `most` units, one cluster per pair of SMs.

@@ -13,103 +13,173 @@
 //
 // What bounds it: bytes.  Forward reads and writes a row once, backward reads
 // two and writes one.  A group of L lanes (the power of two from D / 16) owns
-// U heads of one token, a lane two vectors of 8 features that hold both
-// elements of its pairs (row_part), so the rotation needs no exchange, the mean
-// log2(L) shuffles, and the loads of all heads are in flight before the first
-// is used.  Cos, sin and weights are read once for the U heads.
+// a token, a lane 16 features of every head that hold both elements of its
+// pairs (NormPart), so the rotation needs no exchange and the mean log2(L)
+// shuffles.
 //
 // All arithmetic is fp32 from the loaded elements on; a result is rounded
 // once, when it is stored.
 #pragma once
 
+#include <cooperative_groups.h>
+
+#include "rope_f32x2.cuh"
+#include "rope_launch.cuh"
 #include "rope_norm_internal.cuh"
 #include "rope_rows.cuh"
 
 namespace rope {
 
 constexpr int kNormThreads = 128;
-// Heads of a token that a group has in flight: 8 KB of a warp's loads either way.
-template <typename T>
-static constexpr int kNormHeads = sizeof(T) == 2 ? 4 : 2;
 
-// Eight consecutive features.
-template <typename T>
-struct Vec8 {
-    static constexpr int N = (int)sizeof(T) / 2;   // 16-byte words
-    uint4 u[N];
-    __device__ __forceinline__ void load(const T *p)
+// The 16 features of a head row that lane j of D / 16 owns: N words of 16 bytes, V
+// features each, neighbouring lanes' words side by side.  Rotated lanes (16 j <
+// rotary_dim) own pairs: with split halves feature i of the lane's first eight pairs
+// with i of its last eight, interleaved 2i with 2i + 1.
+template <typename T, int LAYOUT>
+struct NormPart {
+    static constexpr int N = (int)sizeof(T), V = Elt<T>::V;
+    int32_t first, step, second;               // word n lies at first + n step; with split halves
+    bool rot;                                  // words N / 2 .. at second + (n - N / 2) step
+    __device__ __forceinline__ NormPart(int j, int32_t D, int32_t rotary_dim)
     {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            u[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+        const int32_t lanes = rotary_dim / 16;
+        rot = j < lanes;
+        step = (rot ? lanes : D / 16 - lanes) * V;
+        first = rot ? j * V : rotary_dim + (j - lanes) * V;
+        second = LAYOUT == 0 && rot ? rotary_dim / 2 + first : first + N / 2 * step;
     }
-    __device__ __forceinline__ void store(T *p) const
+    __device__ __forceinline__ int32_t at(int n) const
     {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            __stcs(reinterpret_cast<uint4 *>(p) + i, u[i]);
-    }
-    __device__ __forceinline__ void unpack(float *f) const
-    {
-        constexpr int V = Elt<T>::V;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            Elt<T>::unpack(u[i], *reinterpret_cast<float(*)[V]>(f + i * V));
-    }
-    __device__ __forceinline__ void pack(const float *f)
-    {
-        constexpr int V = Elt<T>::V;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            u[i] = Elt<T>::pack(*reinterpret_cast<const float(*)[V]>(f + i * V));
+        return n < N / 2 ? first + n * step : second + (n - N / 2) * step;
     }
 };
 
-// A lane's 16 features of a row: two vectors.
+// A lane's 16 features as eight pairs (x_i, y_i) that the rotation turns, two at a time:
+// x[q] holds x_2q and x_2q+1, y[q] their partners, so everything is done on pairs of fp32
+// values, half as many instructions, and alike in both layouts.  (One value at a time, the
+// forward kernel issued 16 instructions an element, the backward one 26; now 10 and 17.)
+struct Pairs {
+    uint64_t x[4], y[4];
+    // from and to the lane's features in the order of its words
+    template <int LAYOUT>
+    __device__ __forceinline__ void set(const float (&f)[16])
+    {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            x[q] = LAYOUT == 0 ? f32x2(f[2 * q], f[2 * q + 1]) : f32x2(f[4 * q], f[4 * q + 2]);
+            y[q] = LAYOUT == 0 ? f32x2(f[8 + 2 * q], f[9 + 2 * q]) : f32x2(f[4 * q + 1], f[4 * q + 3]);
+        }
+    }
+    template <int LAYOUT>
+    __device__ __forceinline__ void get(float (&f)[16]) const
+    {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            f32x2_split(x[q], f[LAYOUT == 0 ? 2 * q : 4 * q], f[LAYOUT == 0 ? 2 * q + 1 : 4 * q + 2]);
+            f32x2_split(y[q], f[LAYOUT == 0 ? 8 + 2 * q : 4 * q + 1], f[LAYOUT == 0 ? 9 + 2 * q : 4 * q + 3]);
+        }
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            x[q] = y[q] = 0;
+    }
+};
+
+// Cos, sin and -sin of the eight pairs.
+struct Angles {
+    uint64_t c[4], s[4], n[4];
+};
+
 template <typename T>
-struct RowVecs {
-    Vec8<T> v0, v1;
-    __device__ __forceinline__ void load(const T *row, const RowPart &p)
+struct RowWords {
+    static constexpr int N = (int)sizeof(T), V = Elt<T>::V;
+    uint4 u[N];
+    template <int LAYOUT>
+    __device__ __forceinline__ void store(T *row, const NormPart<T, LAYOUT> &p) const
     {
-        v0.load(row + p.o0);
-        v1.load(row + p.o1);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            __stcs(reinterpret_cast<uint4 *>(row + p.at(n)), u[n]);
     }
-    __device__ __forceinline__ void store(T *row, const RowPart &p) const
+    template <int LAYOUT>
+    __device__ __forceinline__ void unpack(Pairs &p) const
     {
-        v0.store(row + p.o0);
-        v1.store(row + p.o1);
+        float f[16];
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            Elt<T>::unpack(u[n], *reinterpret_cast<float(*)[V]>(f + n * V));
+        p.template set<LAYOUT>(f);
     }
-    __device__ __forceinline__ void unpack(float (&f)[16]) const
+    template <int LAYOUT>
+    __device__ __forceinline__ void pack(const Pairs &p)
     {
-        v0.unpack(f);
-        v1.unpack(f + 8);
-    }
-    __device__ __forceinline__ void pack(const float (&f)[16])
-    {
-        v0.pack(f);
-        v1.pack(f + 8);
+        float f[16];
+        p.template get<LAYOUT>(f);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            u[n] = Elt<T>::pack(*reinterpret_cast<const float(*)[V]>(f + n * V));
     }
 };
 
 // A lane's 16 weights (ones without any), in fp32 or in the rows' type.
-template <typename T>
-__device__ __forceinline__ void norm_weights(const void *w, int32_t w_f32, const RowPart &p, float (&f)[16])
+template <typename T, int LAYOUT>
+__device__ __forceinline__ void norm_weights(const void *w, int32_t w_f32, const NormPart<T, LAYOUT> &p, bool inside, Pairs &to)
 {
-    if (w == nullptr) {
+    constexpr int N = (int)sizeof(T), V = Elt<T>::V;
+    float f[16];
+    if (w == nullptr || !inside) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             f[i] = 1.0f;
     } else if (w_f32) {
-        const float *s = static_cast<const float *>(w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 t = __ldg(reinterpret_cast<const float4 *>(s + (i < 2 ? p.o0 : p.o1)) + (i & 1));
+            const float4 t = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + p.at(4 * i / V) + 4 * i % V));
             f[4 * i] = t.x; f[4 * i + 1] = t.y; f[4 * i + 2] = t.z; f[4 * i + 3] = t.w;
         }
     } else if constexpr (sizeof(T) == 2) {
-        const T *s = static_cast<const T *>(w);
-        Elt<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(s + p.o0)), *reinterpret_cast<float(*)[8]>(f));
-        Elt<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(s + p.o1)), *reinterpret_cast<float(*)[8]>(f + 8));
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            Elt<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(w) + p.at(n))),
+                           *reinterpret_cast<float(*)[V]>(f + n * V));
+    }
+    to.set<LAYOUT>(f);
+}
+
+// Cos and sin of a rotated lane's eight pairs at a table row.
+template <typename T, int LAYOUT, typename Args>
+__device__ __forceinline__ void norm_angles(const Args &a, int64_t row, const NormPart<T, LAYOUT> &p, Angles &to)
+{
+    constexpr int V = Elt<T>::V;
+    float c[8], s[8];
+    const int64_t at = row * (a.rotary_dim / 2);
+    if constexpr (LAYOUT == 1 && V == 4) {     // two pairs a word
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float2 t = __ldg(reinterpret_cast<const float2 *>(a.cos + at + p.at(n) / 2));
+            const float2 u = __ldg(reinterpret_cast<const float2 *>(a.sin + at + p.at(n) / 2));
+            c[2 * n] = t.x; c[2 * n + 1] = t.y;
+            s[2 * n] = u.x; s[2 * n + 1] = u.y;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            // pairs 4q .. 4q + 3: split halves start at their first features
+            const int32_t col = LAYOUT == 0 ? p.at(4 * q / V) + 4 * q % V : p.at(q) / 2;
+            const float4 t = __ldg(reinterpret_cast<const float4 *>(a.cos + at + col));
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(a.sin + at + col));
+            c[4 * q] = t.x; c[4 * q + 1] = t.y; c[4 * q + 2] = t.z; c[4 * q + 3] = t.w;
+            s[4 * q] = u.x; s[4 * q + 1] = u.y; s[4 * q + 2] = u.z; s[4 * q + 3] = u.w;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        to.c[q] = f32x2(c[2 * q], c[2 * q + 1]);
+        to.s[q] = f32x2(s[2 * q], s[2 * q + 1]);
+        to.n[q] = f32x2(-s[2 * q], -s[2 * q + 1]);
     }
 }
 
@@ -123,32 +193,52 @@ __device__ __forceinline__ float group_sum(float x)
     return x;
 }
 
-__device__ __forceinline__ float square_sum(const float (&f)[16])
+__device__ __forceinline__ float pair_sum(uint64_t a)
 {
-    float a = 0.0f, b = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        a = fmaf(f[i], f[i], a);
-        b = fmaf(f[8 + i], f[8 + i], b);
-    }
-    return a + b;
+    float lo, hi;
+    f32x2_split(a, lo, hi);
+    return lo + hi;
 }
 
-// A lane's pairs turned by the angles of (c, s).
-template <int LAYOUT>
-__device__ __forceinline__ void turn(float (&f)[16], const float (&c)[8], const float (&s)[8], float sign)
+__device__ __forceinline__ float square_sum(const Pairs &f)
+{
+    uint64_t a = mul_f32x2(f.x[0], f.x[0]), b = mul_f32x2(f.y[0], f.y[0]);
+#pragma unroll
+    for (int q = 1; q < 4; ++q) {
+        a = fma_f32x2(f.x[q], f.x[q], a);
+        b = fma_f32x2(f.y[q], f.y[q], b);
+    }
+    return pair_sum(add_f32x2(a, b));
+}
+
+// (x, y) <- (x c - y s, x s + y c), or by the negated angles
+template <bool BACK>
+__device__ __forceinline__ void turn(Pairs &f, const Angles &a)
 {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        if constexpr (LAYOUT == 0)
-            rotate_pair(f[e], f[8 + e], c[e], sign * s[e]);
-        else
-            rotate_pair(f[2 * e], f[2 * e + 1], c[e], sign * s[e]);
+    for (int q = 0; q < 4; ++q) {
+        const uint64_t t = fma_f32x2(f.x[q], a.c[q], mul_f32x2(f.y[q], BACK ? a.s[q] : a.n[q]));
+        f.y[q] = fma_f32x2(f.x[q], BACK ? a.n[q] : a.s[q], mul_f32x2(f.y[q], a.c[q]));
+        f.x[q] = t;
     }
 }
 
-// The table row of token t, or -1: not rotated.
-__device__ __forceinline__ int64_t norm_row(const NormArgs &a, int64_t t, int64_t b, int64_t s, bool report)
+// 1 / sqrt(mean + eps) of a row whose squares sum to `sum`
+__device__ __forceinline__ float norm_scale(float sum, float inv_d, float eps) { return rsqrtf(fmaf(sum, inv_d, eps)); }
+
+// f r w
+__device__ __forceinline__ void scale(Pairs &f, float r, const Pairs &w)
+{
+    const uint64_t r2 = f32x2(r, r);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        f.x[q] = mul_f32x2(mul_f32x2(f.x[q], r2), w.x[q]);
+        f.y[q] = mul_f32x2(mul_f32x2(f.y[q], r2), w.y[q]);
+    }
+}
+
+// The table row of token (b, s), or -1: not rotated.
+__device__ __forceinline__ int64_t norm_row(const NormArgs &a, int64_t b, int64_t s, bool report)
 {
     int64_t row = s;
     if (a.pos != nullptr)
@@ -161,214 +251,293 @@ __device__ __forceinline__ int64_t norm_row(const NormArgs &a, int64_t t, int64_
     return row;
 }
 
-// Where a group's unit lies: token t, heads h0 .. of tensor i.  With the
-// sequence before the heads, neighbouring groups take neighbouring heads; with
-// the heads before the sequence, neighbouring tokens: either way a CTA's rows
-// lie together.
-struct NormUnit {
-    int64_t t;
-    int32_t h0;
-};
-__device__ __forceinline__ NormUnit norm_unit(const NormArgs &a, int64_t tile, int32_t g, int32_t groups,
-                                              int32_t chunks)
+// ---------------------------------------------------------------------------
+// Forward and backward: one kernel, a ring of stages per thread.
+//
+// A group of lanes owns a token and walks through its heads, U at a time, with the
+// token's cos and sin in registers; a CTA's groups own neighbouring tokens.  A CTA takes
+// a run of tiles (U heads of its tokens; all query heads' tiles come before the key
+// heads'), from wherever the last CTA's ends, and copies its own words of the tiles to
+// come into shared memory, all stages but one ahead.  A thread reads nothing but what it
+// copied itself, so nothing is synchronised, and more than 100 KB are on their way to
+// every SM whatever the arithmetic is at.
+template <bool BACKWARD>
+static constexpr int kNormCtas = BACKWARD ? 3 : 4;             // of an SM
+template <bool BACKWARD>
+static constexpr int kNormStages = BACKWARD ? 4 : 3;
+constexpr int kNormWords = 8;                  // 16-byte words of a thread's stage
+template <bool BACKWARD>
+static constexpr int kNormSmem = kNormStages<BACKWARD> * kNormWords * kNormThreads * 16;
+
+__device__ __forceinline__ void copy16(uint4 *dst, const void *src)
 {
-    NormUnit u;
-    int32_t c;
-    if (a.seq_first) {
-        const int64_t unit = tile * groups + g;
-        u.t = unit / chunks;
-        c = (int32_t)(unit - u.t * chunks);
-    } else {
-        const int64_t tt = tile / chunks;
-        c = (int32_t)(tile - tt * chunks);
-        u.t = tt * groups + g;
-    }
-    u.h0 = c * a.chunk_heads;
-    return u;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
 }
 
-// Forward.  One tile (a unit per group) per CTA, the query heads' tiles first:
-// the hardware hands them out as CTAs finish.
+// A CTA's sums of g * n for one tensor, into its row of the partial sums.
 template <typename T, int LAYOUT, int L>
-__global__ void __launch_bounds__(kNormThreads) rope_norm_fwd_kernel(const NormArgs a)
+__device__ __forceinline__ void norm_partials(const NormArgs &a, const NormPart<T, LAYOUT> &part, const Pairs &pairs,
+                                              float *to)
 {
-    constexpr int U = kNormHeads<T>, kGroups = kNormThreads / L;
-    const int tid = threadIdx.x, j = tid % L;
-    const bool second = (int64_t)blockIdx.x >= a.tiles[0];
-    const NormTensor &x = a.t[second ? 1 : 0];
-    const int32_t chunks = (x.heads + U - 1) / U;
-    const NormUnit u = norm_unit(a, (int64_t)blockIdx.x - (second ? a.tiles[0] : 0), tid / L, kGroups, chunks);
-    const RowPart part = row_part<LAYOUT>(j, a.rotary_dim);
-    const bool live = u.t < a.tokens && 16 * j < a.D;
-    const int64_t t = u.t < a.tokens ? u.t : 0, b = t / a.S, s = t - b * a.S;
-
-    pdl_wait();
-    pdl_trigger();
-    RowVecs<T> v[U];
-    const T *src = static_cast<const T *>(x.x) + b * x.xs[0] + s * x.xs[1];
+    __shared__ float sums[kNormThreads / 32][16 * L];
+    constexpr int V = Elt<T>::V;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (to == nullptr)
+        return;
+    float acc[16];
+    pairs.get<LAYOUT>(acc);
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-        if (live && u.h0 + i < x.heads)
-            v[i].load(src + (u.h0 + i) * x.xs[2], part);
-    const int64_t row = norm_row(a, t, b, s, live && j == 0);
-    float w[16], c[8], sn[8];
-    const bool rot = live && part.rot && row >= 0;
-    if (live)
-        norm_weights<T>(x.w, a.w_f32, part, w);
-    if (rot)
-        table_values(a.cos, a.sin, row * (a.rotary_dim / 2) + 8 * j, c, sn);
-    T *dst = static_cast<T *>(x.y) + b * x.ys[0] + s * x.ys[1];
+    for (int e = 0; e < 16; ++e) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        float f[16];
-        float sum = 0.0f;
-        if (live && u.h0 + i < x.heads) {
-            v[i].unpack(f);
-            sum = square_sum(f);
-        }
-        const float r = __frsqrt_rn(fmaf(group_sum<L>(sum), a.inv_d, a.eps));
-        if (live && u.h0 + i < x.heads) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                f[e] = f[e] * r * w[e];
-            if (rot)
-                turn<LAYOUT>(f, c, sn, 1.0f);
-            v[i].pack(f);
-            v[i].store(dst + (u.h0 + i) * x.ys[2], part);
-        }
+        for (int d = L; d < 32; d <<= 1)
+            acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], d);
     }
-}
-
-// Backward.  A CTA takes the tiles blockIdx, blockIdx + grid, ... of the query
-// heads, then of the key heads, and keeps its sum of g * n in registers; at the
-// end it leaves one row of D partial sums per tensor, which
-// rope_norm_weights_kernel adds up in a fixed order (no atomics: the same call
-// gives the same bits).
-template <typename T, int LAYOUT, int L>
-__global__ void __launch_bounds__(kNormThreads) rope_norm_bwd_kernel(const NormArgs a)
-{
-    constexpr int U = kNormHeads<T> / 2, kGroups = kNormThreads / L;
-    const int tid = threadIdx.x, j = tid % L, warp = tid >> 5, lane = tid & 31;
-    const RowPart part = row_part<LAYOUT>(j, a.rotary_dim);
-    __shared__ float part_sum[kNormThreads / 32][16 * L];
-    pdl_wait();
-    pdl_trigger();
-    for (int k = 0; k < 2; ++k) {
-        const NormTensor &x = a.t[k];
-        if (x.heads == 0)
-            continue;
-        const int32_t chunks = (x.heads + U - 1) / U;
-        float w[16], acc[16];
+    __syncthreads();                           // the last tensor's sums are read
+    if (lane < L && 16 * lane < a.D) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-            acc[e] = 0.0f;
-        if (16 * j < a.D)
-            norm_weights<T>(x.w, a.w_f32, part, w);
-        for (int64_t tile = blockIdx.x; tile < a.tiles[k]; tile += gridDim.x) {
-            const NormUnit u = norm_unit(a, tile, tid / L, kGroups, chunks);
-            const bool live = u.t < a.tokens && 16 * j < a.D;
-            const int64_t t = u.t < a.tokens ? u.t : 0, b = t / a.S, s = t - b * a.S;
-            RowVecs<T> v[U], gv[U];
-            const T *src = static_cast<const T *>(x.x) + b * x.xs[0] + s * x.xs[1];
-            const T *gsrc = static_cast<const T *>(x.g) + b * x.ys[0] + s * x.ys[1];
+            sums[warp][part.at(e / V) + e % V] = acc[e];
+    }
+    __syncthreads();
+    for (int d = tid; d < a.D; d += kNormThreads) {
+        float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (live && u.h0 + i < x.heads) {
-                    v[i].load(src + (u.h0 + i) * x.xs[2], part);
-                    gv[i].load(gsrc + (u.h0 + i) * x.ys[2], part);
-                }
-            const int64_t row = norm_row(a, t, b, s, live && j == 0);
-            float c[8], sn[8];
-            const bool rot = live && part.rot && row >= 0;
-            if (rot)
-                table_values(a.cos, a.sin, row * (a.rotary_dim / 2) + 8 * j, c, sn);
-            T *dst = static_cast<T *>(x.y) + b * x.ys[0] + s * x.ys[1];
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const bool on = live && u.h0 + i < x.heads;
-                float f[16], g[16];
-                float sum = 0.0f, dot = 0.0f;
-                if (on) {
-                    v[i].unpack(f);
-                    gv[i].unpack(g);
-                    if (rot)
-                        turn<LAYOUT>(g, c, sn, -1.0f);
-                    sum = square_sum(f);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        dot = fmaf(g[e] * w[e], f[e], dot);
-                }
-                const float r = __frsqrt_rn(fmaf(group_sum<L>(sum), a.inv_d, a.eps));
-                // mean(w g n) = r mean(w g x)
-                const float m = group_sum<L>(dot) * r * a.inv_d;
-                if (on) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float n = f[e] * r;
-                        acc[e] = fmaf(g[e], n, acc[e]);
-                        f[e] = r * fmaf(-n, m, g[e] * w[e]);
-                    }
-                    v[i].pack(f);
-                    v[i].store(dst + (u.h0 + i) * x.ys[2], part);
-                }
-            }
-        }
-        if (x.partial == nullptr)
-            continue;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-#pragma unroll
-            for (int d = L; d < 32; d <<= 1)
-                acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], d);
-        }
-        if (lane < L && 16 * j < a.D) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                part_sum[warp][part.o0 + e] = acc[e];
-                part_sum[warp][part.o1 + e] = acc[8 + e];
-            }
-        }
-        __syncthreads();
-        for (int d = tid; d < a.D; d += kNormThreads) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kNormThreads / 32; ++i)
-                sum += part_sum[i][d];
-            x.partial[(int64_t)blockIdx.x * a.D + d] = sum;
-        }
-        __syncthreads();
+        for (int i = 0; i < kNormThreads / 32; ++i)
+            sum += sums[i][d];
+        to[(int64_t)blockIdx.x * a.D + d] = sum;
     }
 }
 
-// dw: the sum of the CTAs' rows, 32 features a CTA, eight runs of rows side by side.
-template <typename T>
-__global__ void __launch_bounds__(256) rope_norm_weights_kernel(const NormArgs a, const int32_t rows)
+// A group's way through the tiles of one tensor: head h of token (b, s).
+struct NormWalk {
+    int32_t b, s, h;
+    // tile `tile`, of chunks of U heads a token
+    __device__ __forceinline__ NormWalk(const NormArgs &a, int64_t tile, int32_t heads, int32_t U, int groups)
+    {
+        const int32_t chunks = (heads + U - 1) / U;
+        const int64_t block = tile / chunks, t = block * groups + threadIdx.x / (kNormThreads / groups);
+        h = (int32_t)(tile - block * chunks) * U;
+        b = (int32_t)(t / a.S);
+        s = (int32_t)(t - b * a.S);
+    }
+    // true: a new token
+    __device__ __forceinline__ bool next(const NormArgs &a, int32_t heads, int32_t U, int groups)
+    {
+        h += U;
+        if (h < heads)
+            return false;
+        h = 0;
+        s += groups;
+        while (s >= a.S) {                     // (once, but for sequences shorter than a CTA's tokens)
+            s -= (int32_t)a.S;
+            ++b;
+        }
+        return true;
+    }
+    __device__ __forceinline__ int64_t at(const int64_t (&st)[3]) const
+    {
+        return b * st[0] + s * st[1] + h * st[2];
+    }
+};
+
+// The tiles first .. first + n - 1 of tensor x, through the ring.  Backward adds its rows'
+// g * n to acc.
+template <typename T, int LAYOUT, int L, bool BACKWARD>
+__device__ __forceinline__ void norm_run(const NormArgs &a, const NormTensor &x, int64_t first, int32_t n,
+                                         const NormPart<T, LAYOUT> &part, uint4 *ring, Pairs &acc)
 {
-    __shared__ float run[8][32];
-    const NormTensor &x = a.t[blockIdx.y];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int d = blockIdx.x * 32 + lane;
+    constexpr int N = (int)sizeof(T), kGroups = kNormThreads / L;
+    constexpr int kStages = kNormStages<BACKWARD>, kWords = kNormWords, U = kWords / N / (BACKWARD ? 2 : 1);
+    const int j = threadIdx.x % L;
+    const bool inside = 16 * j < a.D;
+    const int32_t heads = x.heads;
+    const T *px = static_cast<const T *>(x.x), *pg = static_cast<const T *>(x.g);
+    T *py = static_cast<T *>(x.y);
+    NormWalk in(a, first, heads, U, kGroups), out = in;        // the tile copied next, the tile computed next
+    const T *src = px + in.at(x.xs), *up = BACKWARD ? pg + in.at(x.ys) : nullptr;
+    T *dst = py + out.at(x.ys);
+    int32_t to_copy = n;
+    auto copy = [&](uint4 *to) {
+        if (--to_copy >= 0) {
+            if (in.b < a.B && inside) {
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    if (in.h + i < heads) {
+#pragma unroll
+                        for (int w = 0; w < N; ++w) {
+                            copy16(to + (i * N + w) * kNormThreads, src + i * x.xs[2] + part.at(w));
+                            if constexpr (BACKWARD)
+                                copy16(to + ((U + i) * N + w) * kNormThreads, up + i * x.ys[2] + part.at(w));
+                        }
+                    }
+                }
+            }
+            src += U * x.xs[2];
+            if constexpr (BACKWARD)
+                up += U * x.ys[2];
+            if (in.next(a, heads, U, kGroups)) {
+                src = px + in.at(x.xs);
+                if constexpr (BACKWARD)
+                    up = pg + in.at(x.ys);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    constexpr int kStage = kWords * kNormThreads;
+    uint4 *const end = ring + kStages * kStage;
+#pragma unroll
+    for (int st = 0; st < kStages - 1; ++st)
+        copy(ring + st * kStage);
+    uint4 *now = ring, *free = end - kStage;   // the stage computed next, the one that the last step has read
+    Pairs w;
+    Angles angles;
+    norm_weights(x.w, a.w_f32, part, inside, w);
+    bool rot = false, fresh = true;            // fresh: a new token
+    for (; n > 0; --n) {
+        const bool live = inside && out.b < a.B;
+        if (fresh) {
+            const int64_t row = live ? norm_row(a, out.b, out.s, j == 0) : -1;
+            rot = part.rot && row >= 0;
+            if (rot)
+                norm_angles(a, row, part, angles);
+        }
+        copy(free);
+        free = now;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        // (what a row past the heads or tokens holds is computed, too, and goes nowhere)
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const bool on = live && out.h + i < heads;
+            RowWords<T> v;
+            Pairs f, g;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                v.u[k] = now[(i * N + k) * kNormThreads];
+            v.template unpack<LAYOUT>(f);
+            float sum = square_sum(f), dot = 0.0f;
+            if constexpr (BACKWARD) {
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    v.u[k] = now[((U + i) * N + k) * kNormThreads];
+                v.template unpack<LAYOUT>(g);
+                if (rot)
+                    turn<true>(g, angles);
+                uint64_t d0 = 0, d1 = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    d0 = fma_f32x2(mul_f32x2(g.x[q], f.x[q]), w.x[q], d0);
+                    d1 = fma_f32x2(mul_f32x2(g.y[q], f.y[q]), w.y[q], d1);
+                }
+                dot = pair_sum(add_f32x2(d0, d1));
+            }
+            if (!inside)
+                sum = dot = 0.0f;
+            const float r = norm_scale(group_sum<L>(sum), a.inv_d, a.eps);
+            if constexpr (BACKWARD) {
+                // mean(w g n) n = r^2 mean(w g x) x
+                const float m = group_sum<L>(dot) * a.inv_d * (r * r * r);
+                const uint64_t r2 = f32x2(r, r), m2 = f32x2(-m, -m);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (on) {
+                        acc.x[q] = fma_f32x2(mul_f32x2(g.x[q], f.x[q]), r2, acc.x[q]);
+                        acc.y[q] = fma_f32x2(mul_f32x2(g.y[q], f.y[q]), r2, acc.y[q]);
+                    }
+                    f.x[q] = fma_f32x2(mul_f32x2(g.x[q], w.x[q]), r2, mul_f32x2(f.x[q], m2));
+                    f.y[q] = fma_f32x2(mul_f32x2(g.y[q], w.y[q]), r2, mul_f32x2(f.y[q], m2));
+                }
+            } else {
+                scale(f, r, w);
+                if (rot)
+                    turn<false>(f, angles);
+            }
+            v.template pack<LAYOUT>(f);
+            if (on)
+                v.store(dst + i * x.ys[2], part);
+        }
+        now = now + kStage == end ? ring : now + kStage;
+        dst += U * x.ys[2];
+        fresh = out.next(a, heads, U, kGroups);
+        if (fresh)
+            dst = py + out.at(x.ys);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Backward keeps a thread's sums of g * n in registers; a CTA leaves one row of D partial
+// sums per tensor, which rope_norm_weights_kernel adds up in a fixed order (no atomics: the
+// same call gives the same bits).
+template <typename T, int LAYOUT, int L, bool BACKWARD>
+__global__ void __launch_bounds__(kNormThreads, kNormCtas<BACKWARD>) rope_norm_kernel(const NormArgs a)
+{
+    extern __shared__ __align__(16) uint4 ring[];
+    const NormPart<T, LAYOUT> part(threadIdx.x % L, a.D, a.rotary_dim);
+    // this CTA's run of the tiles, the query heads' first
+    const int64_t tiles = a.tiles[0] + a.tiles[1];
+    const int64_t first = tiles * blockIdx.x / gridDim.x, last = tiles * (blockIdx.x + 1) / gridDim.x;
     pdl_wait();
     pdl_trigger();
-    if (x.partial == nullptr)
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        const int64_t base = k ? a.tiles[0] : 0, end = base + a.tiles[k];
+        const int64_t from = first > base ? first : base, to = last < end ? last : end;
+        Pairs acc;
+        acc.zero();
+        if (from < to)
+            norm_run<T, LAYOUT, L, BACKWARD>(a, a.t[k], from - base, (int32_t)(to - from), part, ring + threadIdx.x, acc);
+        if constexpr (BACKWARD)
+            norm_partials<T, LAYOUT, L>(a, part, acc, a.t[k].partial);
+    }
+}
+
+// dw: the sum of the CTAs' rows.  A cluster sums 32 features of one tensor, a run of rows
+// for each of its 256 warps, in a fixed order: bound by the latency of a few loads one after
+// the other, so as many warps as a cluster has share them (1368 rows: the backward call of 16k
+// tokens 87.3 us with one CTA, 86.4 so; 12000 tokens of 20 heads of 96, 33.8 and 32.6).
+constexpr int kNormSumWarps = 32, kNormSumCtas = 8;
+template <typename T>
+__global__ void __cluster_dims__(kNormSumCtas, 1, 1) __launch_bounds__(32 * kNormSumWarps)
+    rope_norm_weights_kernel(const NormArgs a, const int32_t rows)
+{
+    __shared__ float run[kNormSumWarps][33], part[32];
+    namespace cg = cooperative_groups;
+    const cg::cluster_group cluster = cg::this_cluster();
+    const NormTensor &x = a.t[blockIdx.y];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = (int)cluster.block_rank();
+    const int first = blockIdx.x / kNormSumCtas * 32, d = first + lane;
+    pdl_wait();
+    pdl_trigger();
+    if (x.partial == nullptr)                  // (all of the cluster alike)
         return;
     float sum = 0.0f;
     if (d < a.D) {
 #pragma unroll 8
-        for (int i = warp; i < rows; i += 8)
+        for (int i = rank * kNormSumWarps + warp; i < rows; i += kNormSumCtas * kNormSumWarps)
             sum += __ldcg(x.partial + (int64_t)i * a.D + d);
     }
     run[warp][lane] = sum;
     __syncthreads();
-    if (warp != 0 || d >= a.D)
-        return;
+    // warp w: feature w
+    sum = run[lane][warp];
 #pragma unroll
-    for (int i = 1; i < 8; ++i)
-        sum += run[i][lane];
-    if (a.w_f32)
-        static_cast<float *>(x.dw)[d] = sum;
-    else
-        static_cast<T *>(x.dw)[d] = Elt<T>::from_f(sum);
+    for (int i = 16; i > 0; i >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    if (lane == 0)
+        part[warp] = sum;
+    cluster.sync();
+    if (rank == 0 && warp == 0 && d < a.D) {
+        sum = part[lane];
+#pragma unroll
+        for (int r = 1; r < kNormSumCtas; ++r)
+            sum += *cluster.map_shared_rank(&part[lane], r);
+        if (a.w_f32)
+            static_cast<float *>(x.dw)[d] = sum;
+        else
+            static_cast<T *>(x.dw)[d] = Elt<T>::from_f(sum);
+    }
+    cluster.sync();                            // the others' sums are read
 }
 
 // ---------------------------------------------------------------------------
@@ -377,11 +546,12 @@ __global__ void __launch_bounds__(256) rope_norm_weights_kernel(const NormArgs a
 // which sequence the token belongs to, its page and its table row are looked up
 // while the unit's loads are on their way, as in rope_cache_append_kernel.
 constexpr int kNormCuCached = 1024;            // sequence offsets kept in shared memory
+constexpr int kNormAppendHeads = 4;            // heads of a token that a group has in flight
 
 template <typename T, int LAYOUT, int D>
 __global__ void __launch_bounds__(kNormThreads) rope_norm_append_kernel(const NormAppendArgs a)
 {
-    constexpr int L = D / 16, U = kNormHeads<T>, kGroups = kNormThreads / L;
+    constexpr int L = D / 16, U = kNormAppendHeads, N = (int)sizeof(T), kGroups = kNormThreads / L;
     __shared__ int32_t s_cu[kNormCuCached];
     const RowsArgs &r = a.rows;
     const int tid = threadIdx.x, j = tid % L;
@@ -393,18 +563,21 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_append_kernel(const No
     const int32_t h0 = (c - (kind == 0 ? 0 : (kind == 1 ? cq : cq + ck))) * U;
     const int32_t heads = kind == 0 ? a.Hq : r.Hk;
     const bool live = t < r.total;
-    const RowPart part = row_part<LAYOUT>(j, r.rotary_dim);
+    const NormPart<T, LAYOUT> part(j, D, r.rotary_dim);
 
     pdl_wait();
     pdl_trigger();
-    RowVecs<T> v[U];
+    RowWords<T> v[U];
     const T *src = kind == 0 ? static_cast<const T *>(a.q) + t * a.q_stride
                              : (kind == 1 ? static_cast<const T *>(r.k) + t * r.k_stride
                                           : static_cast<const T *>(r.v) + t * r.v_stride);
 #pragma unroll
     for (int i = 0; i < U; ++i)
-        if (live && h0 + i < heads)
-            v[i].load(src + (h0 + i) * D, part);
+        if (live && h0 + i < heads) {
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                v[i].u[n] = __ldcs(reinterpret_cast<const uint4 *>(src + (h0 + i) * D + part.at(n)));
+        }
     const bool cached = r.n_seqs + 1 <= kNormCuCached;
     if (cached) {
         for (int32_t i = tid; i <= r.n_seqs; i += kNormThreads)
@@ -450,12 +623,13 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_append_kernel(const No
             }
         }
     }
-    float w[16], cs[8], sn[8];
+    Pairs w;
+    Angles angles;
     const bool rot = part.rot && row >= 0;
     if (write && kind < 2)
-        norm_weights<T>(kind == 0 ? a.wq : a.wk, a.w_f32, part, w);
+        norm_weights(kind == 0 ? a.wq : a.wk, a.w_f32, part, true, w);
     if (rot)
-        table_values(r.cos, r.sin, row * (r.rotary_dim / 2) + 8 * j, cs, sn);
+        norm_angles(r, row, part, angles);
     const int64_t in_page = slot & (((int64_t)1 << r.page_shift) - 1);
     T *dst = kind == 0 ? static_cast<T *>(a.q_out) + (t * a.Hq + h0) * D
                        : static_cast<T *>(kind == 1 ? r.k_out : r.v_out) +
@@ -464,19 +638,18 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_append_kernel(const No
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         const bool on = write && h0 + i < heads;
-        float f[16], sum = 0.0f;
+        Pairs f;
+        float sum = 0.0f;
         if (on && kind < 2) {
-            v[i].unpack(f);
+            v[i].template unpack<LAYOUT>(f);
             sum = square_sum(f);
         }
-        const float q = __frsqrt_rn(fmaf(group_sum<L>(sum), 1.0f / D, a.eps));
+        const float q = norm_scale(group_sum<L>(sum), 1.0f / D, a.eps);
         if (on && kind < 2) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                f[e] = f[e] * q * w[e];
+            scale(f, q, w);
             if (rot)
-                turn<LAYOUT>(f, cs, sn, 1.0f);
-            v[i].pack(f);
+                turn<false>(f, angles);
+            v[i].template pack<LAYOUT>(f);
         }
         if (on)
             v[i].store(dst + i * step, part);
@@ -485,37 +658,50 @@ __global__ void __launch_bounds__(kNormThreads) rope_norm_append_kernel(const No
 
 // ---------------------------------------------------------------------------
 // host side
-template <typename T, int LAYOUT, int L>
-static cudaError_t launch_norm_lanes(NormArgs a, bool backward, cudaStream_t st)
+template <typename T, int LAYOUT, int L, bool BACKWARD>
+static cudaError_t launch_norm_lanes(NormArgs a, cudaStream_t st)
 {
-    const int64_t groups = kNormThreads / L;
-    a.chunk_heads = backward ? kNormHeads<T> / 2 : kNormHeads<T>;
-    for (int k = 0; k < 2; ++k) {
-        const int64_t chunks = (a.t[k].heads + a.chunk_heads - 1) / a.chunk_heads;
-        a.tiles[k] = a.seq_first ? (a.tokens * chunks + groups - 1) / groups
-                                 : (a.tokens + groups - 1) / groups * chunks;
-    }
+    constexpr int64_t groups = kNormThreads / L, U = kNormWords / (int)sizeof(T) / (BACKWARD ? 2 : 1);
+    for (int k = 0; k < 2; ++k)
+        a.tiles[k] = (a.tokens + groups - 1) / groups * ((a.t[k].heads + U - 1) / U);
     const int64_t tiles = a.tiles[0] + a.tiles[1];
-    if (tiles > 0x7fffffff)
+    if (tiles > (1ll << 40))                   // (a run has to fit 32 bits)
         return cudaErrorInvalidConfiguration;
-    if (!backward)
-        return launch_hot(rope_norm_fwd_kernel<T, LAYOUT, L>, dim3((unsigned)tiles), dim3(kNormThreads), 0, st, a);
-    const int64_t most = a.tiles[0] > a.tiles[1] ? a.tiles[0] : a.tiles[1];
+    static std::atomic<uint64_t> raised{0};
+    auto *kernel = rope_norm_kernel<T, LAYOUT, L, BACKWARD>;
+    int sms = 0, dev = 0;
+    cudaError_t e = sm_count(&sms, &dev);
+    if (e == cudaSuccess)
+        e = raise_smem(reinterpret_cast<const void *>(kernel), kNormSmem<BACKWARD>, dev, raised);
+    if (e != cudaSuccess)
+        return e;
+    // The CTAs that are resident at once, or twice or three times as many where that leaves
+    // runs of some length: the hardware hands them out as others end, which evens out what the
+    // SMs and their way to memory take.  Once, twice, three times (us): 16k tokens of 40 heads
+    // of 128, forward 60.6, -, 55.1, backward 96, 92, 87; 12000 tokens of 20 heads of 96, 19.5,
+    // -, 23.2 and 34, 37, 41.
+    const int64_t resident = kNormCtas<BACKWARD> * (int64_t)sms;
+    int64_t waves = tiles / ((BACKWARD ? 12 : 5) * resident);
+    waves = waves < 1 ? 1 : waves > 3 ? 3 : waves;
+    int64_t most = waves * resident;
+    if (BACKWARD && most > kNormPartials)
+        most = kNormPartials;
     // (without rows the sums are zeros)
-    const int32_t grid = most < 1 ? 1 : (int32_t)(most < kNormPartials ? most : kNormPartials);
-    cudaError_t e = launch_hot(rope_norm_bwd_kernel<T, LAYOUT, L>, dim3((unsigned)grid), dim3(kNormThreads), 0, st, a);
+    const int32_t grid = (int32_t)(tiles < 1 ? 1 : tiles < most ? tiles : most);
+    e = launch_hot(kernel, dim3((unsigned)grid), dim3(kNormThreads), (size_t)kNormSmem<BACKWARD>, st, a);
     if (e != cudaSuccess || (a.t[0].partial == nullptr && a.t[1].partial == nullptr))
         return e;
-    return launch_hot(rope_norm_weights_kernel<T>, dim3((unsigned)(a.D + 31) / 32, 2), dim3(256), 0, st, a, grid);
+    return launch_hot(rope_norm_weights_kernel<T>, dim3((unsigned)(a.D + 31) / 32 * kNormSumCtas, 2),
+                      dim3(32 * kNormSumWarps), 0, st, a, grid);
 }
 
 template <typename T>
 cudaError_t launch_norm_type(const NormArgs &a, int32_t layout, bool backward, cudaStream_t st)
 {
     const int lanes = a.D / 16;
-#define ROPE_NORM(L)                                                     \
-    (layout == 0 ? launch_norm_lanes<T, 0, L>(a, backward, st)           \
-                 : launch_norm_lanes<T, 1, L>(a, backward, st))
+#define ROPE_NORM(L)                                                                                        \
+    (layout == 0 ? backward ? launch_norm_lanes<T, 0, L, true>(a, st) : launch_norm_lanes<T, 0, L, false>(a, st) \
+                 : backward ? launch_norm_lanes<T, 1, L, true>(a, st) : launch_norm_lanes<T, 1, L, false>(a, st))
     return lanes <= 2 ? ROPE_NORM(2) : lanes <= 4 ? ROPE_NORM(4) : lanes <= 8 ? ROPE_NORM(8) : ROPE_NORM(16);
 #undef ROPE_NORM
 }
@@ -523,7 +709,7 @@ cudaError_t launch_norm_type(const NormArgs &a, int32_t layout, bool backward, c
 template <typename T, int LAYOUT, int D>
 static cudaError_t launch_norm_append_t(const NormAppendArgs &a, cudaStream_t st)
 {
-    constexpr int64_t U = kNormHeads<T>, groups = kNormThreads / (D / 16);
+    constexpr int64_t U = kNormAppendHeads, groups = kNormThreads / (D / 16);
     const int64_t chunks = (a.Hq + U - 1) / U + 2 * ((a.rows.Hk + U - 1) / U);
     const int64_t blocks = (a.rows.total * chunks + groups - 1) / groups;
     if (blocks > 0x7fffffff)

@@ -10,8 +10,8 @@
 namespace rope {
 
 // CTAs of the backward kernel at most: a row of partial weight gradients each
-// (four for each of 152 SMs).
-constexpr int32_t kNormPartials = 608;
+// (nine for each of 152 SMs).
+constexpr int32_t kNormPartials = 1368;
 
 struct NormTensor {
     const void *x, *g, *w;           // rows, their output's gradient, weights [D] or nullptr
@@ -26,9 +26,9 @@ struct NormArgs {
     const float *cos, *sin;
     const int32_t *pos;              // [S] or [B][pos_stride], or nullptr
     int64_t pos_stride;              // 0: one row for all sequences
-    int64_t table_rows, tokens, S;
+    int64_t table_rows, tokens, B, S;
     int64_t tiles[2];
-    int32_t D, rotary_dim, seq_first, w_f32, chunk_heads;
+    int32_t D, rotary_dim, seq_first, w_f32;
     float eps, inv_d;
     int32_t *flag;
 };

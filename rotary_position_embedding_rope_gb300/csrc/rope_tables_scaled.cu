@@ -8,8 +8,8 @@
 // 64-bit integer product is the whole range reduction, exact but for F_i's own
 // rounding (p 2^-65 turns: 4e-11 radians at a position of 10^8).  The nearest
 // quarter turn comes off the top two bits, and what is left, at most an eighth of
-// a turn either way, goes to fp32 (relative 2^-24, at most 2.4e-8 of a radian) and
-// to sincospif.  The frequencies are computed on the host in 64 bits and go along as
+// a turn either way, goes to fp32 (two roundings of 2^-24) and to the series of sine
+// and cosine.  The frequencies are computed on the host in 64 bits and go along as
 // kernel arguments: 64 pow in every CTA would cost more than the table.
 //
 // What bounds it: 8 bytes a pair against some 50 instructions, at 64 pairs a
@@ -27,6 +27,7 @@
 
 #include "rope.h"
 #include "rope_checks.h"
+#include "rope_f32x2.cuh"
 #include "rope_kernels.cuh"
 
 namespace rope {
@@ -44,17 +45,45 @@ struct ScaledArgs {
     float scale;
 };
 
-__device__ __forceinline__ void phase_cos_sin(uint64_t phase, float scale, float &c, float &s)
+// Cos and sin of two phases, times scale.  Each leaves its nearest quarter turn as a rest of
+// at most an eighth of a turn; with y its angle, at most pi / 4, Taylor's series to y^9 and
+// y^10 are within 2^-28 of sin y and cos y.  The rounding of y's product with 2 pi goes along
+// as `low`, so y is as good as the rest in fp32.
+__device__ __forceinline__ void phase_cos_sin(const uint64_t (&phase)[2], float scale, float (&c)[2], float (&s)[2])
 {
-    const uint64_t quarter = (phase + (1ull << 61)) >> 62;
-    const int64_t rest = (int64_t)(phase - (quarter << 62));
-    float a, b;
-    sincospif(__ll2float_rn(rest) * 0x1p-63f, &b, &a);     // half turns
-    // (cos, sin) of rest + quarter * pi / 2
-    const bool swap = quarter & 1;
-    const float x = swap ? b : a, y = swap ? a : b;
-    c = (quarter == 1 || quarter == 2 ? -x : x) * scale;
-    s = (quarter >= 2 ? -y : y) * scale;
+    uint32_t quarter[2];
+    float rest[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t top = (uint32_t)(phase[i] >> 32);
+        quarter[i] = (top + 0x20000000u) >> 30;
+        rest[i] = fmaf((float)(int32_t)(top - (quarter[i] << 30)), 4294967296.0f, (float)(uint32_t)phase[i]);
+    }
+    auto both = [](float x) { return f32x2(x, x); };
+    constexpr double kTurn = 6.283185307179586477 / 18446744073709551616.0;    // 2 pi / 2^64
+    const uint64_t r = f32x2(rest[0], rest[1]), k = both((float)kTurn);
+    const uint64_t y = mul_f32x2(r, k);
+    const uint64_t low = fma_f32x2(r, both((float)(kTurn - (double)(float)kTurn)),
+                                   fma_f32x2(r, k, y ^ 0x8000000080000000ull));
+    const uint64_t z = fma_f32x2(add_f32x2(low, low), y, mul_f32x2(y, y));
+    uint64_t a = fma_f32x2(z, both(-1.0f / 3628800.0f), both(1.0f / 40320.0f));
+    a = fma_f32x2(a, z, both(-1.0f / 720.0f));
+    a = fma_f32x2(a, z, both(1.0f / 24.0f));
+    a = fma_f32x2(a, z, both(-0.5f));
+    a = fma_f32x2(a, z, both(1.0f));
+    uint64_t b = fma_f32x2(z, both(1.0f / 362880.0f), both(-1.0f / 5040.0f));
+    b = fma_f32x2(b, z, both(1.0f / 120.0f));
+    b = fma_f32x2(b, z, both(-1.0f / 6.0f));
+    b = add_f32x2(y, fma_f32x2(b, mul_f32x2(y, z), low));
+    float x[2], w[2];
+    f32x2_split(mul_f32x2(a, both(scale)), x[0], x[1]);
+    f32x2_split(mul_f32x2(b, both(scale)), w[0], w[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {              // (cos, sin) of y + quarter * pi / 2
+        const bool swap = quarter[i] & 1;
+        c[i] = __uint_as_float(__float_as_uint(swap ? w[i] : x[i]) ^ ((quarter[i] + 1) & 2) << 30);
+        s[i] = __uint_as_float(__float_as_uint(swap ? x[i] : w[i]) ^ (quarter[i] & 2) << 30);
+    }
 }
 
 // V: pairs of a thread, 4 where rows are whole 16-byte vectors, else 1.
@@ -81,10 +110,17 @@ __global__ void __launch_bounds__(kScaledThreads) rope_tables_scaled_kernel(cons
     for (; row < a.rows; row += step) {
         float c[V], s[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            phase_cos_sin(phase[i], a.scale, c[i], s[i]);
-            phase[i] += f[i];
+        for (int i = 0; i < V; i += 2) {
+            const int n = V > 1 ? i + 1 : i;   // (alone: the same twice)
+            const uint64_t two[2] = {phase[i], phase[n]};
+            float c2[2], s2[2];
+            phase_cos_sin(two, a.scale, c2, s2);
+            c[i] = c2[0]; c[n] = c2[V > 1];
+            s[i] = s2[0]; s[n] = s2[V > 1];
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            phase[i] += f[i];
         if constexpr (V == 4) {
             *reinterpret_cast<float4 *>(a.cos + row * a.h + col) = make_float4(c[0], c[1], c[2], c[3]);
             *reinterpret_cast<float4 *>(a.sin + row * a.h + col) = make_float4(s[0], s[1], s[2], s[3]);
@@ -111,8 +147,8 @@ void scaled_frequencies(int32_t kind, double theta, int32_t rd, double factor, i
         if (factor > 1.0)
             *scale = 0.1 * std::log(factor) + 1.0;
     }
+    const double base = kind == ROPE_SCALE_NTK ? theta * std::pow(factor, (double)rd / (double)(rd - 2)) : theta;
     for (int32_t i = 0; i < h; ++i) {
-        const double base = kind == ROPE_SCALE_NTK ? theta * std::pow(factor, (double)rd / (double)(rd - 2)) : theta;
         double x = std::pow(base, -2.0 * (double)i / (double)rd);
         if (kind == ROPE_SCALE_LINEAR) {
             x /= factor;
@@ -164,7 +200,7 @@ extern "C" rope_status rope_tables_build_scaled(int32_t kind, double theta, int3
     double w[kScaledPairs], scale;
     scaled_frequencies(kind, theta, rotary_dim, factor, original_positions, low_turns, high_turns, w, &scale);
     for (int32_t i = 0; i < h; ++i)            // at most 1 / 2 pi of a turn
-        a.freq[i] = (uint64_t)std::nearbyint(std::ldexp(w[i] / (2.0 * 3.14159265358979323846), 64));
+        a.freq[i] = (uint64_t)std::nearbyint(w[i] / (2.0 * 3.14159265358979323846) * 18446744073709551616.0);
     for (int32_t i = h; i < kScaledPairs; ++i)
         a.freq[i] = 0;
     a.cos = cos_out; a.sin = sin_out; a.rows = rows; a.first = (uint64_t)pos_offset; a.h = h;

@@ -12,14 +12,18 @@
 #include <algorithm>
 #include <cstdint>
 #include <initializer_list>
+#include <optional>
 #include <string>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/autograd/variable.h>
 
@@ -117,11 +121,17 @@ struct Call {
     cudaStream_t stream;
     bool own_stream;                           // not the current one
 
-    Call(const at::Tensor &first, PyObject *s)
+    Call(const at::Tensor &first, PyObject *s) : Call(cuda_index(first), s) {}
+
+    static c10::DeviceIndex cuda_index(const at::Tensor &first)
     {
         if (!first.is_cuda())
             fail(PyExc_ValueError, "expected CUDA tensors, got one on " + first.device().str());
-        device = first.get_device();
+        return first.get_device();
+    }
+
+    Call(c10::DeviceIndex on, PyObject *s) : device(on)
+    {
         const cudaStream_t current = c10::cuda::getCurrentCUDAStream(device).stream();
         stream = current;
         if (s != Py_None) {
@@ -748,25 +758,272 @@ PyObject *norm_rotate_qk_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// accumulates_elsewhere(tensor) -> whether the tensor is a leaf whose gradients a
-// graph that is alive accumulates on another stream than the current one.  (The
-// engine would make that stream wait for a captured backward pass, which ends the
-// capture with an error.)
-PyObject *accumulates_elsewhere(PyObject *, PyObject *const *a, Py_ssize_t n)
+// ---------------------------------------------------------------------------
+// norm_rotary_qk: the same calls as a node of torch's autograd.  In C++, because a
+// training step makes them once a layer: with a Python node, forward and backward of
+// a small layer took 200 us of the host's time.
+
+// A status that the library returned, on its way to the Python side.
+struct StatusError {
+    rope_status st;
+};
+
+int32_t dtype_code(at::ScalarType t)
+{
+    return t == at::kFloat ? ROPE_F32 : t == at::kBFloat16 ? ROPE_BF16 : ROPE_F16;
+}
+
+void *address(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// What both directions need of queries and keys that the forward call has checked.
+struct NormSizes {
+    int64_t B = 0, S = 0, strides[2][3] = {}, pos_stride = 0, rows = 0;
+    int32_t H[2] = {0, 0}, D = 0, code = 0, w_code = ROPE_F32, rotary_dim = 0;
+
+    NormSizes(const at::Tensor (&x)[2], const at::Tensor (&w)[2], const at::Tensor &cos, const at::Tensor &pos, bool seq_first)
+    {
+        const int s = seq_first ? 1 : 2, h = seq_first ? 2 : 1;
+        for (int i = 0; i < 2; ++i) {
+            if (w[i].defined())
+                w_code = dtype_code(w[i].scalar_type());
+            const at::Tensor &t = x[i];
+            if (!t.defined())
+                continue;
+            B = t.size(0);
+            S = t.size(s);
+            H[i] = (int32_t)t.size(h);
+            D = (int32_t)t.size(3);
+            code = dtype_code(t.scalar_type());
+            strides[i][0] = t.stride(0);
+            strides[i][1] = t.stride(s);
+            strides[i][2] = t.stride(h);
+        }
+        if (pos.defined() && pos.dim() == 2 && S > 0)
+            pos_stride = pos.size(1);
+        rows = cos.size(0);
+        rotary_dim = (int32_t)(2 * cos.size(1));
+    }
+};
+
+// Whether the library takes a tensor's strides: dense features, whole 16-byte vectors.
+bool whole_vectors(const at::Tensor &t)
+{
+    const int64_t v = 16 / t.element_size();
+    if (reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 != 0 || (t.size(3) > 1 && t.stride(3) != 1))
+        return false;
+    for (int i = 0; i < 3; ++i)
+        if (t.size(i) > 1 && (t.stride(i) <= 0 || t.stride(i) % v != 0))
+            return false;
+    return true;
+}
+
+// t, dense and 16-byte aligned.
+at::Tensor dense_vectors(const at::Tensor &t)
+{
+    const at::Tensor d = t.contiguous();
+    return reinterpret_cast<uintptr_t>(d.data_ptr()) % 16 == 0 ? d : d.clone();
+}
+
+using Given = std::optional<at::Tensor>;       // nothing: None
+
+struct NormRotary : torch::autograd::Function<NormRotary> {
+    static torch::autograd::variable_list forward(torch::autograd::AutogradContext *ctx, const Given &q, const Given &k,
+                                                  const Given &gwq, const Given &gwk, const at::Tensor &cos,
+                                                  const at::Tensor &sin, const Given &positions, double eps, int64_t layout,
+                                                  bool seq_first)
+    {
+        const at::Tensor wq = gwq.value_or(at::Tensor()), wk = gwk.value_or(at::Tensor()),
+                         pos = positions.value_or(at::Tensor());
+        at::Tensor x[2] = {q.value_or(at::Tensor()), k.value_or(at::Tensor())}, y[2];
+        for (at::Tensor &t : x)
+            if (t.defined() && !whole_vectors(t))
+                t = t.clone(at::MemoryFormat::Contiguous);
+        const at::Tensor w[2] = {wq, wk};
+        const NormSizes z(x, w, cos, pos, seq_first);
+        torch::autograd::variable_list out;
+        for (int i = 0; i < 2; ++i)
+            if (x[i].defined()) {
+                y[i] = at::empty(x[i].sizes(), x[i].options().memory_format(at::MemoryFormat::Contiguous));
+                out.push_back(y[i]);
+            }
+        const rope_status st = g_norm(address(x[0]), address(x[1]), address(y[0]), address(y[1]), address(wq), address(wk),
+                                      cos.const_data_ptr<float>(), sin.const_data_ptr<float>(),
+                                      static_cast<const int32_t *>(address(pos)), z.pos_stride, z.B, z.H[0], z.H[1], z.S, z.D,
+                                      z.strides[0], z.strides[1], z.rotary_dim, (int32_t)layout, seq_first, (float)eps, z.code,
+                                      z.w_code, z.rows, c10::cuda::getCurrentCUDAStream(cos.get_device()).stream());
+        if (st != ROPE_OK)
+            throw StatusError{st};
+        ctx->save_for_backward({x[0], x[1], wq, wk, cos, sin, pos});
+        ctx->saved_data["eps"] = eps;
+        ctx->saved_data["layout"] = layout;
+        ctx->saved_data["seq_first"] = seq_first;
+        ctx->set_materialize_grads(false);
+        return out;
+    }
+
+    static torch::autograd::variable_list backward(torch::autograd::AutogradContext *ctx, torch::autograd::variable_list grads)
+    {
+        const torch::autograd::variable_list saved = ctx->get_saved_variables();
+        const at::Tensor &cos = saved[4], &sin = saved[5], &pos = saved[6];
+        const bool seq_first = ctx->saved_data["seq_first"].toBool();
+        at::Tensor x[2], w[2], g[2], dx[2], dw[2];
+        // (torch counts the given tensors alone)
+        auto needs = [&](int i) {
+            int at = 0;
+            for (int j = 0; j < i; ++j)
+                at += saved[j].defined();
+            return saved[i].defined() && ctx->needs_input_grad(at);
+        };
+        // an output that took no part in the loss has no gradient, and an input (and weight)
+        // that needs none is left out
+        int next = 0;
+        for (int i = 0; i < 2; ++i) {
+            if (!saved[i].defined())
+                continue;
+            const at::Tensor &up = grads[next++];
+            if (!up.defined() || !(needs(i) || needs(2 + i)))
+                continue;
+            x[i] = saved[i];
+            w[i] = saved[2 + i];
+            g[i] = dense_vectors(up);
+            dx[i] = at::empty(x[i].sizes(), x[i].options().memory_format(at::MemoryFormat::Contiguous));
+            if (needs(2 + i))
+                dw[i] = at::empty({x[i].size(3)}, w[i].options());
+        }
+        if (x[0].defined() || x[1].defined()) {
+            const NormSizes z(x, w, cos, pos, seq_first);
+            const c10::cuda::CUDAGuard guard(cos.get_device());
+            at::Tensor ws;
+            if (dw[0].defined() || dw[1].defined())
+                ws = at::empty({g_norm_bytes(z.D)}, cos.options().dtype(at::kByte));
+            const rope_status st =
+                g_norm_bwd(address(x[0]), address(x[1]), address(g[0]), address(g[1]), address(dx[0]), address(dx[1]),
+                           address(w[0]), address(w[1]), address(dw[0]), address(dw[1]), cos.const_data_ptr<float>(),
+                           sin.const_data_ptr<float>(), static_cast<const int32_t *>(address(pos)), z.pos_stride, z.B, z.H[0],
+                           z.H[1], z.S, z.D, z.strides[0], z.strides[1], z.rotary_dim, (int32_t)ctx->saved_data["layout"].toInt(),
+                           seq_first, (float)ctx->saved_data["eps"].toDouble(), z.code, z.w_code, z.rows, address(ws),
+                           ws.defined() ? (int64_t)ws.nbytes() : 0,
+                           c10::cuda::getCurrentCUDAStream(cos.get_device()).stream());
+            TORCH_CHECK(st == ROPE_OK, "rope_norm_qk_bwd: status ", (int)st);
+        }
+        torch::autograd::variable_list out(10);
+        for (int i = 0; i < 2; ++i) {
+            if (needs(i))
+                out[i] = dx[i];
+            out[2 + i] = dw[i];
+        }
+        if (at::GradMode::is_enabled()) {
+            // differentiable once: a second derivative through these is an error, not a zero
+            for (at::Tensor &t : out)
+                if (t.defined())
+                    t = (*std::make_shared<torch::autograd::DelayedError>(
+                        "norm_rotary_qk: its gradients cannot be differentiated", 1))({t.detach().set_requires_grad(true)})[0];
+        }
+        return out;
+    }
+};
+
+// Whether a tensor is a leaf whose gradients a graph that is alive accumulates on
+// another stream than the current one.  (The engine would make that stream wait for a
+// captured backward pass, which ends the capture with an error.)
+bool accumulates_elsewhere(const at::Tensor &t)
+{
+    if (!t.defined() || !t.is_leaf() || !t.requires_grad())
+        return false;
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
+    if (node == nullptr)
+        return false;
+    const auto stream = node->stream();
+    return stream && *stream != c10::cuda::getCurrentCUDAStream(t.get_device()).unwrap();
+}
+
+// norm_rotary_qk(q, k, wq, wk, cos, sin, eps, pos_idx, rotary_dim, layout, seq_before_head)
+// -> (q_out, k_out), or a status
+PyObject *norm_rotary_qk(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
     try {
-        expect(n, 1);
-        const at::Tensor &t = tensor(a[0], "leaf");
-        if (!t.is_cuda() || !t.is_leaf() || !t.requires_grad())
-            Py_RETURN_FALSE;
-        const auto node = torch::autograd::impl::try_get_grad_accumulator(t);
-        if (node == nullptr)
-            Py_RETURN_FALSE;
-        const auto stream = node->stream();
-        if (stream && *stream != c10::cuda::getCurrentCUDAStream(t.get_device()).unwrap())
-            Py_RETURN_TRUE;
-        Py_RETURN_FALSE;
+        expect(n, 11);
+        const bool has_q = a[0] != Py_None, has_k = a[1] != Py_None;
+        const at::Tensor &first = has_q ? tensor(a[0], "q") : tensor(a[1], "q or k");
+        const Call c(first, Py_None);
+        type_code(first, "norm_rotary_qk");
+        const at::ScalarType type = first.scalar_type();
+        const bool seq_first = truth(a[10]);
+        auto given = [&](int i, const char *name) { return a[i] == Py_None ? at::Tensor() : tensor(a[i], name); };
+        const at::Tensor q = given(0, "q"), k = given(1, "k"), wq = given(2, "wq"), wk = given(3, "wk"), pos = given(7, "pos_idx");
+        // (strides the library does not take are copied, so features need not be dense)
+        struct Shape : Heads {
+            Shape(const Call &c, const at::Tensor &t, const char *name, at::ScalarType type, bool seq_first)
+                : Heads(c, Py_None, name, type, seq_first)
+            {
+                if (!t.defined())
+                    return;
+                c.on_device(t, name, type);
+                if (t.dim() != 4)
+                    fail(PyExc_ValueError, std::string(name) + " must be 4-dimensional, got " + shape_of(t));
+                B = t.size(0);
+                S = t.size(seq_first ? 1 : 2);
+                if (t.size(seq_first ? 2 : 1) > INT32_MAX || t.size(3) > INT32_MAX)
+                    fail(PyExc_ValueError, std::string(name) + " is too large: " + shape_of(t));
+                H = (int32_t)t.size(seq_first ? 2 : 1);
+                D = (int32_t)t.size(3);
+            }
+        };
+        const Shape qs(c, q, "q", type, seq_first), ks(c, k, "k", type, seq_first);
+        const NormShape z(c, qs, ks, has_q, has_k, a[7]);
+        const Weight ww(c, a[2], "wq", type, z.D), wv(c, a[3], "wk", type, z.D);
+        weight_code(ww, wv, ROPE_F32);
+        const Tables t(c, a[4], a[5], a[8]);
+        if (t.cos == nullptr || t.sin == nullptr)
+            fail(PyExc_ValueError, "cos and sin must have rows");
+        const at::Tensor cos = tensor(a[4], "cos"), sin = tensor(a[5], "sin");
+        const double eps = number(a[6]);
+        const int64_t layout = integer(a[9]);
+        const c10::cuda::CUDAGuard guard(c.device);
+        if (at::GradMode::is_enabled() &&
+            c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
+            const at::Tensor leaves[4] = {q, k, wq, wk};
+            for (int i = 0; i < 4; ++i)
+                if (accumulates_elsewhere(leaves[i]))
+                    fail(PyExc_RuntimeError, std::string("a graph of ") + (i < 2 ? "" : "w") + (i % 2 ? "k" : "q") +
+                                                 " made on another stream is alive: drop it before the backward pass is captured");
+        }
+        torch::autograd::variable_list out;
+        {
+            const Unlocked u;
+            auto maybe = [](const at::Tensor &t) { return t.defined() ? Given(t) : Given(); };
+            out = NormRotary::apply(maybe(q), maybe(k), maybe(wq), maybe(wk), cos, sin, maybe(pos), eps, layout, seq_first);
+        }
+        return tuple_of({has_q ? out[0] : at::Tensor(), has_k ? out[has_q ? 1 : 0] : at::Tensor()});
+    } catch (const PythonError &) {
+        return nullptr;
+    } catch (const StatusError &e) {
+        return status(e.st);
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// build_tables_scaled(kind, theta, rotary_dim, rows, pos_offset, factor, original_positions,
+//     low_turns, high_turns, value_scale, device (or -1), stream) -> (cos, sin), or a status
+PyObject *build_tables_scaled(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    try {
+        expect(n, 12);
+        const int64_t rd = integer(a[2]), rows = integer(a[3]), at = integer(a[10]);
+        if (rd < 0 || rd > INT32_MAX || rows < 0)
+            return status(ROPE_ERR_INVALID_ARG);
+        const c10::DeviceIndex device = at < 0 ? c10::cuda::current_device() : (c10::DeviceIndex)at;
+        const Call c(device, a[11]);
+        const c10::cuda::CUDAGuard guard(c.device);
+        const at::Tensor cos = c.empty_returned({rows, rd / 2}, at::kFloat), sin = c.empty_returned({rows, rd / 2}, at::kFloat);
+        const rope_status st = unlocked(g_tables_scaled, (int32_t)integer(a[0]), number(a[1]), (int32_t)rd, rows, integer(a[4]),
+                                        number(a[5]), integer(a[6]), number(a[7]), number(a[8]), number(a[9]),
+                                        static_cast<float *>(cos.data_ptr()), static_cast<float *>(sin.data_ptr()), c.stream);
+        if (st != ROPE_OK)
+            return status(st);
+        return tuple_of({cos, sin});
     } catch (const PythonError &) {
         return nullptr;
     }
@@ -830,8 +1087,9 @@ PyMethodDef g_methods[] = {
     {"norm_rotate_qk", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_rotate_qk)), METH_FASTCALL, nullptr},
     {"norm_rotate_qk_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_rotate_qk_backward)),
      METH_FASTCALL, nullptr},
-    {"accumulates_elsewhere", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(accumulates_elsewhere)),
-     METH_FASTCALL, nullptr},
+    {"norm_rotary_qk", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_rotary_qk)), METH_FASTCALL, nullptr},
+    {"build_tables_scaled", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(build_tables_scaled)), METH_FASTCALL,
+     nullptr},
     {"norm_cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_cache_append)), METH_FASTCALL,
      nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -1,9 +1,9 @@
 """Plain 64-bit forms of the norm of query and key heads with the rotation, of its gradients and of the long-context
 tables, on the CPU, with the bounds that the fp32 kernels' errors obey.
 
-u = 2^-24 is fp32's rounding.  A lane adds 16 squares in two chains and the lanes of a row theirs: at most 14
-roundings on a sum of positive terms, so 1 / sqrt is off by 7 u, its own rounding, eps and the mean included by 10 u; a
-normalised, weighted element by 12 u.  The rotation's two products add at most 4 u of their sizes.
+u = 2^-24 is fp32's rounding.  A lane adds 16 squares in chains of at most eight and the lanes of a row theirs: at most 13
+roundings on a sum of positive terms, 1 for the mean and eps, so the root is off by 7 u, and 1 / sqrt by 11 u (rsqrtf: two
+units, 4 u); a normalised, weighted element by 13 u.  The rotation's product and fma add at most 2 u of their sizes.
 """
 from __future__ import annotations
 

@@ -173,8 +173,10 @@ def test_graphs_of_parts():
     R = lib()
     from rotary_position_embedding_rope_gb300 import autograd
 
-    t = {n: x.cuda() for n, x in make(2, 20, 4, 2, 64, "f32", "f32", True).items()}
+    host = make(2, 20, 4, 2, 64, "f32", "f32", True)
+    t = {n: x.cuda() for n, x in host.items()}
     cos, sin = (x.cuda() for x in S.tables(1e4, 64, 32))
+    exact = reference(host, None, cos.cpu(), sin.cpu(), "split_half", True)
     full = R.norm_rotate_qk_backward(t["gq"], t["gk"], t["q"], t["k"], t["wq"], t["wk"], cos, sin, seq_before_head=True)
     want = dict(zip(("q", "k", "wq", "wk"), full))
     for used in ("q", "k", "qk"):
@@ -188,7 +190,12 @@ def test_graphs_of_parts():
             for n in leaves:
                 g = leaves[n].grad
                 if n in need and n[-1] in used:
-                    assert same(g, want[n])
+                    # (a weight's gradient is summed in an order that the sizes of the call give: queries alone, keys
+                    # alone and both are three orders, each within the bound)
+                    if n[0] == "w":
+                        near(g, *exact["d" + n], n)
+                    else:
+                        assert same(g, want[n])
                 else:
                     assert g is None or not g.any()
     assert R.rope_check_errors() == R.ROPE_OK
