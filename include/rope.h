@@ -660,8 +660,11 @@ int64_t rope_attention_decode_workspace(int64_t B, int32_t Hq, int32_t Hk, int32
  *    reads as zeros and raises the flag: outputs of sequences that use it mean
  *    nothing.  A table row out of range (but for rows before a sequence's first key
  *    when causal): the query is not rotated and ROPE_ERR_POS_OUT_OF_RANGE raised.
- * Arithmetic: as rope_attention_decode_fwd.  What lies behind a sequence's last
- *    key, and in other pages, reaches no query; a NaN or infinity in a value may
+ * Arithmetic: rot(q) and the softmax probabilities are rounded to `dtype` for the
+ *    products (for sequences of at most 8 rows, tokens * Hq / Hk, or one token of a
+ *    group of up to 8 heads, they go in as two parts each and are not); sums, maxima
+ *    and partial outputs are fp32; o is rounded once.  What lies behind a sequence's
+ *    last key, and in other pages, reaches no query; a NaN or infinity in a value may
  *    reach queries of its sequence that do not see its key.  The split of the
  *    work depends on the sizes and the lengths alone: the same call gives the same
  *    bits.

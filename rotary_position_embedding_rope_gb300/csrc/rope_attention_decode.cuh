@@ -185,8 +185,8 @@ template <int D>
 static constexpr int kDecStageBytes = 2 * kDecKeys<D> * D * 2;
 template <int D>
 static constexpr int kDecQStride = D * 2 + 16;                 // padded rows of the query tile
-template <int D>
-static constexpr int kDecSmem = kDecWarps * (kDecStages<D> * kDecStageBytes<D> + 16 * kDecQStride<D>);
+template <int D, int W = kDecWarps>
+static constexpr int kDecSmem = W * (kDecStages<D> * kDecStageBytes<D> + 16 * kDecQStride<D>);
 
 struct DecodeArgs {
     AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, flag
@@ -438,22 +438,22 @@ struct SuffixRun {
 };
 
 // Barriers of the suffix warps of a CTA.
-template <int D>
+template <int D, int W = kDecWarps>
 struct SuffixShared {
-    uint64_t bar[kDecWarps][kDecStages<D>];
+    uint64_t bar[W][kDecStages<D>];
     int abort_flag;
 };
 
-// The suffixes' share of CTA `cta` of `ctas`, whose first eight warps work:
+// The suffixes' share of CTA `cta` of `ctas`, whose first kWarps warps work:
 // every thread of the CTA calls this, then the working ones decode_suffixes.
-template <int D, typename G>
+template <int D, int kWarps, typename G>
 __device__ __forceinline__ SuffixRun suffix_run(const G &g, const int32_t *start, int32_t carry,
-                                                int32_t cta, int32_t ctas, SuffixShared<D> &sh)
+                                                int32_t cta, int32_t ctas, SuffixShared<D, kWarps> &sh)
 {
     constexpr int kStages = kDecStages<D>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t n_seqs = g.sequences();
-    if (tid < kDecWarps * kStages)
+    if (tid < kWarps * kStages)
         mbar_init(&sh.bar[0][0] + tid, 1);
     if (tid == 0)
         sh.abort_flag = 0;
@@ -461,7 +461,7 @@ __device__ __forceinline__ SuffixRun suffix_run(const G &g, const int32_t *start
         asm volatile("prefetch.tensormap [%0];" ::"l"(warp ? &g.v_map : &g.k_map) : "memory");
     const int32_t heads = g.heads();
     const int64_t total = (int64_t)carry * heads;
-    const int64_t per = decode_per_warp(total, ctas * kDecWarps);
+    const int64_t per = decode_per_warp(total, ctas * kWarps);
     if (cta == 0)
         g.publish(start, per);
     SuffixRun run;
@@ -470,7 +470,7 @@ __device__ __forceinline__ SuffixRun suffix_run(const G &g, const int32_t *start
     run.w = warp * ctas + cta;
     run.at = {0, 0, 0, 0};
     const int64_t c = run.w * per;
-    run.left = warp >= kDecWarps ? 0 : total - c < per ? total - c : per;
+    run.left = warp >= kWarps ? 0 : total - c < per ? total - c : per;
     if (run.left > 0) {
         const int32_t b = find_sequence(start, n_seqs + 1, divide(c, heads));
         // (the last b whose start is at most c / heads has chunks)
@@ -486,35 +486,33 @@ __device__ __forceinline__ SuffixRun suffix_run(const G &g, const int32_t *start
     return run;
 }
 
-// One warp's run; smem: kDecSmem bytes of the CTA.
-template <typename T, int LAYOUT, int D, typename G>
-__device__ __forceinline__ void decode_suffixes(const G &g, uint8_t *smem, const SuffixRun &run,
-                                                SuffixShared<D> &sh)
-{
-    constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>, kKeys = kDecKeys<D>;
-    constexpr int kBox = kKeys * 128, kGroups = kKeys / 16;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t most = g.most_keys();
-    const int32_t w = run.w;
-    int64_t left = run.left;
-    ChunkAt at = run.at;
-    if (left <= 0)
-        return;
-    uint64_t *bar = sh.bar[warp];
-    uint8_t *stages = smem + warp * kStages * kStage;
-    uint8_t *qtile = smem + kDecWarps * kStages * kStage + warp * 16 * kDecQStride<D>;
-    volatile int *abort = &sh.abort_flag;
-    // The copies run kStages chunks ahead.  Lane i holds the page of block base +
-    // i of sequence `of`, so that a step seldom waits for the block list.
-    ChunkAt ahead = at;
-    int64_t to_load = left;
+// A warp's copies of chunks into its stages, kDecStages ahead of the arithmetic.  Lane i
+// holds the page of block base + i of sequence `of`, so that a step seldom waits for the
+// block list.
+template <int D, typename G>
+struct SuffixCopies {
+    static constexpr int kStage = kDecStageBytes<D>, kKeys = kDecKeys<D>, kBox = kKeys * 128;
+    const G &g;
+    const int64_t most;
+    uint8_t *const stages;
+    uint64_t *const bar;
+    ChunkAt ahead;
+    int64_t left;                              // chunks to copy
     int32_t pages = 0, of = -1;
     int64_t base_block = 0;
-    // (several row groups of a key head read the same keys)
-    const uint64_t policy = g.row_groups > 1 ? l2_keep() : l2_once();
-    const int32_t box_shift = g.page_shift < g.chunk_shift ? g.page_shift : g.chunk_shift;
-    const int32_t boxes = kKeys >> box_shift;                  // of a chunk's keys: its pages, or one
-    auto load = [&](int st) {
+    uint64_t policy;
+    int32_t box_shift, boxes;
+    __device__ __forceinline__ SuffixCopies(const G &args, const SuffixRun &run, int64_t keys, uint8_t *to, uint64_t *bars)
+        : g(args), most(keys), stages(to), bar(bars), ahead(run.at), left(run.left)
+    {
+        // (several row groups of a key head read the same keys)
+        policy = g.row_groups > 1 ? l2_keep() : l2_once();
+        box_shift = g.page_shift < g.chunk_shift ? g.page_shift : g.chunk_shift;
+        boxes = kKeys >> box_shift;            // of a chunk's keys: its pages, or one
+    }
+    __device__ __forceinline__ void load(int st)
+    {
+        const int lane = threadIdx.x & 31;
         const int64_t key = (int64_t)ahead.ch * kKeys, block = key >> g.page_shift;
         if (of != ahead.b || block < base_block || block + boxes > base_block + 32) {
             of = ahead.b;
@@ -542,13 +540,34 @@ __device__ __forceinline__ void decode_suffixes(const G &g, uint8_t *smem, const
             tma_load_3d_l2(stages + st * kStage + v * (kStage / 2) + x * kBox + (i << box_shift) * 128,
                            v ? &g.v_map : &g.k_map, x * 64, y, z, &bar[st], policy);
         }
-        --to_load;
+        --left;
         ahead.next(g, most);
-    };
+    }
+};
+
+// One warp's run; smem: kDecSmem bytes of the CTA.
+template <typename T, int LAYOUT, int D, int kWarps, typename G>
+__device__ __forceinline__ void decode_suffixes(const G &g, uint8_t *smem, const SuffixRun &run,
+                                                SuffixShared<D, kWarps> &sh)
+{
+    constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>, kKeys = kDecKeys<D>;
+    constexpr int kBox = kKeys * 128, kGroups = kKeys / 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t most = g.most_keys();
+    const int32_t w = run.w;
+    int64_t left = run.left;
+    ChunkAt at = run.at;
+    if (left <= 0)
+        return;
+    uint64_t *bar = sh.bar[warp];
+    uint8_t *stages = smem + warp * kStages * kStage;
+    uint8_t *qtile = smem + kWarps * kStages * kStage + warp * 16 * kDecQStride<D>;
+    volatile int *abort = &sh.abort_flag;
+    SuffixCopies<D, G> copies(g, run, most, stages, bar);
     bool ok = true;
     int64_t issued = 0, done = 0;
-    for (int st = 0; st < kStages && to_load > 0; ++st, ++issued)
-        load(st);
+    for (int st = 0; st < kStages && copies.left > 0; ++st, ++issued)
+        copies.load(st);
 
     uint32_t qf[D / 16][4];
     float o[D / 8][4];
@@ -687,8 +706,8 @@ __device__ __forceinline__ void decode_suffixes(const G &g, uint8_t *smem, const
             }
         }
         __syncwarp();                                          // the stage is read
-        if (to_load > 0) {
-            load(st);
+        if (copies.left > 0) {
+            copies.load(st);
             ++issued;
         }
         if (++st == kStages) {

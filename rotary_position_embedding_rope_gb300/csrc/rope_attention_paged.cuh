@@ -7,7 +7,7 @@
 // them, rotated when they were appended) lie in pages.  A step of a serving loop
 // mixes sequences of a single token with chunks of hundreds, so a call has two
 // kinds of work, side by side in one launch:
-//   tiles   sequences of more than 16 rows (token, head) per key head run on
+//   tiles   sequences of more rows (token, head) per key head run on
 //           rope_attn_packed_kernel, whose units here are (query tile, head unit)
 //           pairs.  The key tiles of all units, each unit's with a fixed charge for
 //           its start and end, laid end to end, are cut into equal runs, one per
@@ -15,11 +15,10 @@
 //           batch of ragged chunks both keep every cluster busy to the end.  A unit
 //           that lies in one run is written by it; a cut one leaves an fp32 (O, m,
 //           l) per piece;
-//   few     the others, of at most 16 rows (the 16 rows of an mma), run as the
-//           suffixes of the shared-prefix decode (decode_suffixes): equal runs of
-//           16-key (32 for heads of 64) chunks for all warps of the SMs that have
-//           no tiles, an fp32 (O, m, l) for each pair (sequence, key head) that a
-//           run touches.
+//   few     the others, of at most eight rows, or a single token, are dealt out as
+//           the suffixes of the shared-prefix decode: equal runs of 16-key (32 for
+//           heads of 64) chunks for all warps of the SMs that have no tiles, an fp32
+//           (O, m, l) for each pair (sequence, key head) that a run touches.
 // Three launches:
 //   1. rope_paged_plan_kernel checks the offsets and lengths, lists the units and
 //      cuts them, decides how many SMs each kind gets (plan_ns's estimate), and
@@ -31,8 +30,10 @@
 // The split depends on the sizes and the lengths alone: the same call gives the
 // same bits.
 //
-// Roundings as in the packed and the decode attention: rot(q), and P before P V, to
-// the element type (operands of a 16-bit product), everything else fp32 until o.
+// Roundings: for the tiles rot(q), and P before P V, to the element type (operands of
+// a 16-bit product, whose issue is the bound), as in the packed attention; for the few
+// rows they go into the products as two 16-bit parts (paged_rows8_run).  Everything
+// else is fp32 until o.
 #pragma once
 
 #include "rope_attention_decode.cuh"
@@ -64,11 +65,25 @@ constexpr int32_t kPagedUnitTiles = 4;
 // Least weight of a cluster's run: shorter runs leave more pieces than they save.
 constexpr int64_t kPagedMinRun = 2 * kPagedUnitTiles;
 constexpr int32_t kPagedClusters = kDecodeSms / 2;   // at most
+// Warps of an SM that take few-row sequences: twelve of paged_rows8 or, for heads of 64,
+// of decode_suffixes, whose rows of heads of 128 leave registers and memory for eight.
+template <int D>
+constexpr int32_t paged_few_warps(bool rows8)
+{
+    return rows8 || D == 64 ? 12 : kDecWarps;
+}
+// Bytes of a warp's eight padded query rows, and of all.
+template <int D>
+static constexpr int kRows8Query = 8 * kDecQStride<D>;
+template <int D>
+static constexpr int kRows8Smem = 12 * (kDecStages<D> * kDecStageBytes<D> + kRows8Query<D>);
+static_assert(kRows8Smem<128> <= 225 * 1024 && kRows8Smem<64> <= 225 * 1024, "a CTA's shared memory");
 
 // The plan, at the start of the workspace.
 struct PagedDeal {
     int32_t clusters;                              // with tiles
     int32_t chunks;                                // of the few-row sequences, per pair
+    int32_t few_tokens;                            // of the few-row sequences
     int64_t per;                                   // chunks of a warp
     PagedCut cut[kPagedClusters + 1];              // cluster c: cut[c] .. cut[c + 1]
 };
@@ -78,7 +93,7 @@ struct PagedPlan {
     const int32_t *cu, *lens;
     int32_t n_seqs, group, tile_tokens, head_units, heads;
     int64_t total_q, most_keys;
-    int32_t causal, chunk_shift, page_shift, chunk_bytes, tile_ns, grid;
+    int32_t causal, chunk_shift, page_shift, chunk_bytes, tile_ns, grid, few_warps;
     float sm_rate;
     PagedDeal *deal;
     PagedEntry *entries;
@@ -88,11 +103,12 @@ struct PagedPlan {
     int32_t *flag;
 };
 
-// Rows of a key head that run as a few-row sequence: at most the 16 of an mma, or
-// one token's, in groups of 16.
+// Rows of a key head that run as a few-row sequence: at most eight (paged_rows8), or,
+// where a token alone has more, its heads in groups of 16 (decode_suffixes).
+__host__ __device__ constexpr bool paged_rows8(int32_t group) { return group <= 8; }
 __device__ __forceinline__ bool paged_few(int32_t Lq, int32_t group)
 {
-    return Lq == 1 || (int64_t)Lq * group <= 16;
+    return Lq == 1 || (int64_t)Lq * group <= 8;
 }
 
 // A sequence's new tokens and keys; false when an offset or the length is out of range.
@@ -205,8 +221,8 @@ static __device__ void paged_plan(const PagedPlan &p)
             atomicOr(p.flag, kFlagIndex);
             p.deal->clusters = 0;
             p.deal->chunks = 0;
+            p.deal->few_tokens = 0;
             p.deal->per = 1;
-            p.few_start[p.n_seqs] = 0;
         }
         return;
     }
@@ -301,7 +317,8 @@ static __device__ void paged_plan(const PagedPlan &p)
         const int32_t used = 2 * clusters < p.grid ? 2 * clusters : 0;
         p.deal->clusters = clusters;
         p.deal->chunks = carry.a;
-        p.deal->per = decode_per_warp((int64_t)carry.a * p.heads, (p.grid - used) * kDecWarps);
+        p.deal->few_tokens = carry.b;
+        p.deal->per = decode_per_warp((int64_t)carry.a * p.heads, (p.grid - used) * p.few_warps);
     }
 }
 
@@ -406,15 +423,15 @@ struct PagedFew {
         const int32_t seen = n - tokens(b) + r / rows + 1;
         return seen < n ? seen : n;
     }
-    // A run's part of a pair has as many rows as the pair, at row 16 w + the rows of the
-    // pairs before it: w, the pair or both grow from one part to the next, a pair has at
-    // most 16 rows, so parts do not meet.
+    // A run's part of a pair has as many rows as the pair, at row 8 w (16 w for 16-row pairs) +
+    // the rows of the pairs before it: the run w, the pair or both grow from one part to the
+    // next, a pair has at most that many rows, so parts do not meet.
     __device__ __forceinline__ int64_t part_row(int32_t w, int32_t b, int32_t hr) const
     {
         const int32_t kv = hr / row_groups, group = Hq / Hk;
         const int64_t in = row_groups > 1 ? (int64_t)kv * group + (hr - kv * row_groups) * rows
                                           : (int64_t)kv * group * tokens(b);
-        return 16 * (int64_t)w + (int64_t)__ldg(few_start + b) * Hq + in;
+        return (int64_t)(paged_rows8(group) ? 8 : 16) * w + (int64_t)__ldg(few_start + b) * Hq + in;
     }
     __device__ __forceinline__ int32_t part_rows(int32_t b, int32_t hr) const
     {
@@ -423,6 +440,291 @@ struct PagedFew {
     }
     __device__ __forceinline__ void publish(const int32_t *, int64_t) const {}     // (the plan has done so)
 };
+
+// Pairs of at most eight rows.  The products are turned round, keys and features being the
+// 16 rows of an mma and the pair's rows its eight columns,
+//   S^T = K q^T (16 keys x 8 rows),  O^T += V^T P^T (16 features x 8 rows),
+// so that a product, an exponential or an accumulator is spent on eight rows, not on 16:
+// with a row of S per thread as in decode_suffixes, one token of a group of four used a
+// quarter of each (40 sequences of 5 tokens, 16 heads of 64: 70 us so).  P leaves S^T's
+// accumulators in 16 bits and gets to its operand's place by movmatrix.
+//
+// Half the products leaves room for twice as many: rot(q) and P go into them as two 16-bit
+// parts each, the rounded value and what it leaves, so nothing is rounded to 16 bits on the
+// way, and the loop still waits for its copies.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// a and b rounded to 16 bits in one word, and the word of what that leaves.
+template <typename T>
+__device__ __forceinline__ uint32_t split2(float a, float b, uint32_t &low)
+{
+    const uint32_t high = Elt<T>::f2_to_word(a, b);
+    const float2 h = Elt<T>::word_to_f2(high);
+    low = Elt<T>::f2_to_word(a - h.x, b - h.y);
+    return high;
+}
+
+// Eight rows of queries of pair (b, hr), rotated in fp32 (zeros past the pair's rows), as
+// two 16-bit parts: one after the other into the warp's tile, and from there as the B operand
+// of every 16-feature step.
+template <typename T, int LAYOUT, int D>
+__device__ __forceinline__ void load_query_rows8(const PagedFew &g, const ChunkAt &at, int64_t most, uint8_t *tile,
+                                                 uint32_t (&qh)[D / 16][2], uint32_t (&ql)[D / 16][2])
+{
+    constexpr int L = D / 16, kAtOnce = 32 / L, kSteps = 8 / kAtOnce;
+    const int lane = threadIdx.x & 31, j = lane % L;
+    const RowPart part = row_part<LAYOUT>(j, g.a.rotary_dim);
+    uint4 x0[kSteps], x1[kSteps];
+    int64_t trow[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
+        trow[i] = -1;
+        const T *row = g.template query<T, D>(at.b, at.hr, i * kAtOnce + lane / L, most, part.rot, trow[i]);
+        if (row != nullptr) {
+            x0[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o0));
+            x1[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o1));
+        }
+    }
+    uint4 y0[kSteps], y1[kSteps];              // what the rounded values leave
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        y0[i] = y1[i] = make_uint4(0, 0, 0, 0);
+        if (trow[i] >= 0) {
+            float c[8], s[8], f0[8], f1[8];
+            table_values(g.a.cos, g.a.sin, trow[i] * (g.a.rotary_dim / 2) + 8 * j, c, s);
+            Elt<T>::unpack(x0[i], f0);
+            Elt<T>::unpack(x1[i], f1);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if constexpr (LAYOUT == 0)
+                    rotate_pair(f0[e], f1[e], c[e], s[e]);
+                else if (e < 4)
+                    rotate_pair(f0[2 * e], f0[2 * e + 1], c[e], s[e]);
+                else
+                    rotate_pair(f1[2 * e - 8], f1[2 * e - 7], c[e], s[e]);
+            }
+            uint32_t *h0 = &x0[i].x, *h1 = &x1[i].x, *l0 = &y0[i].x, *l1 = &y1[i].x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                h0[e] = split2<T>(f0[2 * e], f0[2 * e + 1], l0[e]);
+                h1[e] = split2<T>(f1[2 * e], f1[2 * e + 1], l1[e]);
+            }
+        }
+    }
+    auto through = [&](const uint4 (&a)[kSteps], const uint4 (&b)[kSteps], uint32_t (&f)[D / 16][2]) {
+        __syncwarp();                          // the tile's last readers are done
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            uint8_t *to = tile + (i * kAtOnce + lane / L) * kDecQStride<D>;
+            *reinterpret_cast<uint4 *>(to + part.o0 * 2) = a[i];
+            *reinterpret_cast<uint4 *>(to + part.o1 * 2) = b[i];
+        }
+        __syncwarp();
+        // lanes 8 m ..: rows 0-7, features 8 m .. of two steps
+        const uint32_t addr = attn_smem_u32(tile) + (lane & 7) * kDecQStride<D> + (lane >> 3) * 16;
+#pragma unroll
+        for (int k = 0; k < D / 16; k += 2) {
+            uint32_t r[4];
+            ldsm4(addr + k * 32, r);
+            f[k][0] = r[0]; f[k][1] = r[1]; f[k + 1][0] = r[2]; f[k + 1][1] = r[3];
+        }
+    };
+    through(x0, x1, qh);
+    through(y0, y1, ql);
+}
+
+// One warp's run of chunks; smem: kRows8Smem bytes of the CTA.
+template <typename T, int LAYOUT, int D>
+__device__ __forceinline__ void paged_rows8_run(const PagedFew &g, uint8_t *smem, const SuffixRun &run, SuffixShared<D, 12> &sh)
+{
+    constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>, kKeys = kDecKeys<D>;
+    constexpr int kBox = kKeys * 128, kGroups = kKeys / 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t most = g.most_keys();
+    int64_t left = run.left;
+    ChunkAt at = run.at;
+    if (left <= 0)
+        return;
+    uint64_t *bar = sh.bar[warp];
+    uint8_t *stages = smem + warp * kStages * kStage;
+    uint8_t *qtile = smem + 12 * kStages * kStage + warp * kRows8Query<D>;
+    volatile int *abort = &sh.abort_flag;
+    SuffixCopies<D, PagedFew> copies(g, run, most, stages, bar);
+    bool ok = true;
+    int64_t issued = 0, done = 0;
+    for (int st = 0; st < kStages && copies.left > 0; ++st, ++issued)
+        copies.load(st);
+
+    uint32_t qh[D / 16][2], ql[D / 16][2];
+    float o[D / 16][4];                                        // features lane / 4 and + 8 of 16, rows r0 and r0 + 1
+    const int r0 = 2 * (lane & 3), k0 = lane >> 2;             // S^T: keys k0 and k0 + 8 of 16
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    int32_t keys = 0, lim0 = 0, lim1 = 0, low = 0;             // of the pair; that the two rows see; that all rows see
+    bool fresh = true;
+    int st = 0;
+    uint32_t ph = 0;
+    // ldmatrix rows: K (two 8-key halves x two 8-feature halves of a step), V (the same,
+    // turned: two 8-feature halves x two 8-key halves)
+    const int k_row = lane & 15, k_half = lane >> 4;
+    const int v_row = (lane & 7) + ((lane >> 4) << 3), v_half = lane >> 3 & 1;
+    const uint32_t base = attn_smem_u32(stages);
+    for (; ok && left > 0; --left, ++done) {
+        if (fresh) {
+            keys = g.keys(at.b, most);
+            lim0 = g.limit(at.b, r0, keys);
+            lim1 = g.limit(at.b, r0 + 1, keys);
+            low = g.limit(at.b, 0, keys);
+            load_query_rows8<T, LAYOUT, D>(g, at, most, qtile, qh, ql);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+            m0 = m1 = -INFINITY;
+            l0 = l1 = 0.0f;
+            fresh = false;
+        }
+        ok = __all_sync(0xffffffffu, attn_wait(&bar[st], ph, abort));
+        if (!ok)
+            break;
+        const uint32_t kb = base + st * kStage, vb = kb + kStage / 2;
+        float s[kGroups][4];                                   // (key k0, rows r0, r0 + 1), (key k0 + 8, the same)
+#pragma unroll
+        for (int n = 0; n < kGroups; ++n) {
+            float h[4] = {0, 0, 0, 0}, e[4] = {0, 0, 0, 0};    // of the rounded queries and of the rest
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t a[4];
+                const int chunk = (k & 3) * 2 + k_half;
+                ldsm4(kb + (k >> 2) * kBox + (n * 16 + k_row) * 128 + ((chunk ^ (k_row & 7)) << 4), a);
+                mma16816<T>(h, a, qh[k][0], qh[k][1]);
+                mma16816<T>(e, a, ql[k][0], ql[k][1]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s[n][i] = h[i] + e[i];
+        }
+        if (low - at.ch * kKeys < kKeys) {                     // keys that some row does not see
+            const int32_t n0 = lim0 - at.ch * kKeys, n1 = lim1 - at.ch * kKeys;
+#pragma unroll
+            for (int n = 0; n < kGroups; ++n) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n * 16 + k0 + (i >> 1) * 8 >= (i & 1 ? n1 : n0))
+                        s[n][i] = -INFINITY;
+            }
+            // what lies behind the last key (anything) must not meet a zero
+            const int32_t nk = keys - at.ch * kKeys;
+            if (nk < kKeys) {
+                constexpr int kWords = D / 8;                  // 16-byte words of a value
+                for (int i = nk * kWords + lane; i < kKeys * kWords; i += 32)
+                    *reinterpret_cast<uint4 *>(stages + st * kStage + kStage / 2 + (i % kWords / 8) * kBox +
+                                               i / kWords * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next copy
+                __syncwarp();
+            }
+        }
+        float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
+#pragma unroll
+        for (int n = 1; n < kGroups; ++n) {
+            x0 = fmaxf(x0, fmaxf(s[n][0], s[n][2]));
+            x1 = fmaxf(x1, fmaxf(s[n][1], s[n][3]));
+        }
+        x0 *= g.a.scale_log2;                                  // (the scale is positive)
+        x1 *= g.a.scale_log2;
+        // the reference maxima move only when a key exceeds them by more than 8 (a factor of
+        // 256), so the lanes of a row seldom have to agree on its maximum
+        if (__any_sync(0xffffffffu, x0 > m0 + 8.0f || x1 > m1 + 8.0f)) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
+            }
+            const bool up0 = x0 > m0 + 8.0f, up1 = x1 > m1 + 8.0f;
+            const float f0 = up0 ? (m0 == -INFINITY ? 0.0f : fast_exp2(m0 - x0)) : 1.0f;
+            const float f1 = up1 ? (m1 == -INFINITY ? 0.0f : fast_exp2(m1 - x1)) : 1.0f;
+            m0 = up0 ? x0 : m0;
+            m1 = up1 ? x1 : m1;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                o[i][0] *= f0;
+                o[i][1] *= f1;
+                o[i][2] *= f0;
+                o[i][3] *= f1;
+            }
+        }
+        const float n0 = m0 == -INFINITY ? 0.0f : -m0, n1 = m1 == -INFINITY ? 0.0f : -m1;
+#pragma unroll
+        for (int n = 0; n < kGroups; ++n) {
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                p[i] = fast_exp2(fmaf(s[n][i], g.a.scale_log2, i & 1 ? n1 : n0));
+            l0 += p[0] + p[2];
+            l1 += p[1] + p[3];
+            uint32_t e0, e1;
+            const uint32_t h0 = transpose8(split2<T>(p[0], p[1], e0)), h1 = transpose8(split2<T>(p[2], p[3], e1));
+            e0 = transpose8(e0);
+            e1 = transpose8(e1);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t a[4];
+                const int chunk = (i & 3) * 2 + v_half;
+                ldsm4_t(vb + (i >> 2) * kBox + (n * 16 + v_row) * 128 + ((chunk ^ (v_row & 7)) << 4), a);
+                mma16816<T>(o[i], a, h0, h1);
+                mma16816<T>(o[i], a, e0, e1);
+            }
+        }
+        __syncwarp();                                          // the stage is read
+        if (copies.left > 0) {
+            copies.load(st);
+            ++issued;
+        }
+        if (++st == kStages) {
+            st = 0;
+            ph ^= 1u;
+        }
+        const ChunkAt was = at;
+        at.next(g, most);
+        if (left == 1 || at.b != was.b || at.hr != was.hr) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+                l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+            }
+            const int64_t row0 = g.part_row(run.w, was.b, was.hr) + r0;
+            const int32_t rows = g.part_rows(was.b, was.hr) - r0;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (half < rows) {
+                    float *dst = g.out + (row0 + half) * D + k0;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        dst[16 * i] = o[i][half];
+                        dst[16 * i + 8] = o[i][2 + half];
+                    }
+                    if (k0 == 0)
+                        g.stats[row0 + half] = half ? make_float2(m1, l1) : make_float2(m0, l0);
+                }
+            }
+            fresh = true;
+        }
+    }
+    if (!ok) {
+        *abort = 1;
+        if (lane == 0)
+            atomicOr(g.a.flag, kFlagTimeout);
+        // one more bounded wait for the copies in flight
+        for (int64_t i = done; i < issued; ++i)
+            (void)attn_wait(&bar[i % kStages], (uint32_t)(i / kStages) & 1u);
+    }
+}
 
 // ---------------------------------------------------------------------------
 // the tiles, with the few-row sequences beside or behind them
@@ -435,7 +737,9 @@ struct PagedSource {
     static constexpr int smem_bytes()
     {
         const int tiles = (int)kPackedSmem<D> + 4 * (kMaxDecodeBatch + 2);
-        return tiles > kDecSmem<D> ? tiles : kDecSmem<D>;
+        constexpr int few = kDecSmem<D, paged_few_warps<D>(false)>;
+        constexpr int most = few > kRows8Smem<D> ? few : kRows8Smem<D>;
+        return tiles > most ? tiles : most;
     }
     AttnArgs a;                                // o, Hq, cos, sin, table_rows, rotary_dim, scale, causal, flag
     CUtensorMap k_map, v_map, q_map, o_map;    // the pools; queries and outputs of all sequences
@@ -599,7 +903,7 @@ struct PagedSource {
     template <typename T, int LAYOUT, int D>
     __device__ __forceinline__ void finish(const Walk &w, uint8_t *smem, bool failed) const
     {
-        __shared__ SuffixShared<D> sh;
+        __shared__ SuffixShared<D, 12> sh;
         const int32_t used = 2 * w.clusters < (int32_t)gridDim.x ? 2 * w.clusters : 0;
         const int32_t cta = (int32_t)blockIdx.x - used;
         // (after an expired wait copies may still be on their way: no work)
@@ -609,14 +913,32 @@ struct PagedSource {
         for (int32_t b = threadIdx.x; b <= few.n_seqs; b += kPackedThreads)
             start[b] = __ldg(few.chunk_start + b);
         __syncthreads();
-        const SuffixRun run = suffix_run<D>(few, start, w.chunks, cta, (int32_t)gridDim.x - used, sh);
+        const int32_t ctas = (int32_t)gridDim.x - used;
         const int warp = threadIdx.x >> 5;
-        if (warp < 8) {
+        // registers: from the roles' 240 / 112 / 104 to 168 for all, or 216 for eight warps
+        if (paged_rows8(few.Hq / few.Hk)) {
+            const SuffixRun run = suffix_run<D>(few, start, w.chunks, cta, ctas, sh);
+            if (warp < 4)
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+            else
+                asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+            paged_rows8_run<T, LAYOUT, D>(few, smem, run, sh);
+            return;
+        }
+        SuffixShared<D, paged_few_warps<D>(false)> &sh16 = reinterpret_cast<SuffixShared<D, paged_few_warps<D>(false)> &>(sh);
+        const SuffixRun run = suffix_run<D>(few, start, w.chunks, cta, ctas, sh16);
+        if constexpr (paged_few_warps<D>(false) == 12) {
+            if (warp < 4)
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+            else
+                asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+            decode_suffixes<T, LAYOUT, D>(few, smem, run, sh16);
+        } else if (warp < 8) {
             if (warp < 4)
                 asm volatile("setmaxnreg.dec.sync.aligned.u32 216;");
             else
                 asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-            decode_suffixes<T, LAYOUT, D>(few, smem, run, sh);
+            decode_suffixes<T, LAYOUT, D>(few, smem, run, sh16);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         }
@@ -676,7 +998,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_paged_merge_kernel
     }
     // The few-row sequences: (token, head).
     constexpr int kRows = W == 1 ? kWarps : 1;                 // of a CTA at once
-    const int64_t rows = (int64_t)__ldg(f.few_start + f.n_seqs) * f.Hq;
+    const int64_t rows = (int64_t)__ldg(&g.deal->few_tokens) * f.Hq;
     const int32_t group = f.Hq / f.Hk, heads = f.heads();
     for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < rows; row0 += (int64_t)gridDim.x * kRows) {
         const int64_t row = row0 + (W == 1 ? warp : 0);
@@ -772,6 +1094,7 @@ static cudaError_t launch_paged(const PagedCall &c, const PagedLayout &lay, cuda
     p.total_q = c.total_q; p.most_keys = c.max_blocks << c.page_shift;
     p.causal = c.causal; p.chunk_shift = f.chunk_shift; p.page_shift = c.page_shift;
     p.chunk_bytes = kDecStageBytes<D>; p.tile_ns = D == 128 ? 900 : 700; p.grid = 2 * clusters;
+    p.few_warps = paged_few_warps<D>(paged_rows8(group));
     p.sm_rate = D == 128 ? 53.0f : 48.0f;
     p.deal = reinterpret_cast<PagedDeal *>(ws);
     p.entries = reinterpret_cast<PagedEntry *>(ws + lay.entries);

@@ -13,8 +13,11 @@ pytestmark = pytest.mark.gpu
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
 
 
-def reference(q, kp, vp, table, cu, lens, cos, sin, pos_q=None, layout="split_half", causal=True, scale=None):
-    """(o, w, a) [Tq, Hq, D] in fp64; rows of no sequence are NaN.  cos None: queries as they are."""
+def reference(q, kp, vp, table, cu, lens, cos, sin, pos_q=None, layout="split_half", causal=True, scale=None, rounded=False):
+    """(o, w, a) [Tq, Hq, D] in fp64; rows of no sequence are NaN.  cos None: queries as they are.
+
+    Rotated queries are rounded to their type, but for sequences of at most eight rows (token, head) per key head, whose
+    products take them in two parts (rounded: those too, as the other attentions do)."""
     Tq, Hq, D = q.shape
     _, Hk, page, _ = kp.shape
     scale = D ** -0.5 if scale is None else scale
@@ -30,7 +33,10 @@ def reference(q, kp, vp, table, cu, lens, cos, sin, pos_q=None, layout="split_ha
             qr = q[q0:q1].double()
         else:
             rows = range(n - Lq, n) if pos_q is None else [int(x) for x in pos_q[q0:q1]]
-            qr = S._rotated_rounded(q[q0:q1], rows, cos, sin, layout)
+            if Lq * (Hq // Hk) <= 8 and not rounded:
+                qr = torch.stack([S.rotate(q[q0 + i], r, cos, sin, layout) for i, r in enumerate(rows)])
+            else:
+                qr = S._rotated_rounded(q[q0:q1], rows, cos, sin, layout)
         seen = torch.ones(Lq, n, dtype=torch.bool)
         if causal:
             seen = torch.arange(n)[None] <= torch.arange(Lq)[:, None] + (n - Lq)
@@ -93,6 +99,9 @@ CASES = [
     case([(i * 7) % 5 for i in range(150)], [(i * 37) % 200 + 5 for i in range(150)], 8, 2, 64, 64, 16),
     case([(i * 53) % 90 for i in range(40)], [(i * 53) % 90 + (i * 31) % 300 for i in range(40)], 4, 2, 128, 128, 32),
     case([1] * 40, [(i * 61) % 400 + 1 for i in range(40)], 16, 2, 128, 128, 64, "f16"),
+    case([8, 2, 9, 1, 5], [900, 2, 40, 1500, 70], 3, 3, 64, 48, 16, "f16", "interleaved"),     # rows up to eight and past
+    case([1] * 30, [(i * 67) % 500 for i in range(30)], 24, 2, 64, 64, 16),   # groups of 12: 16-row pairs
+    case([1] * 33, [(i * 67) % 500 for i in range(33)], 28, 2, 128, 128, 32, "f16"),          # groups of 14
     case([700], [2200], 3, 1, 64, 48, 64),                                    # groups of 3, many query tiles
 ]
 
@@ -146,9 +155,25 @@ def test_rotated_queries_positions_scale_and_strides():
     check(run(R, q, kp, vp, table, cu, lens, cos, sin, R.ROPE_ERR_POS_OUT_OF_RANGE, pos_q=bad), ref, c, "paged bad positions")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_few_rows_lose_nothing_before_the_output(dtype):
+    """At most eight rows a key head: rotated queries and P go into the products in two parts, so an output is within its
+    one rounding of the exact one.  Besides: each part's own rounding, 2^-16 of a probability (fp16 2^-22, or 2^-25 of the
+    largest where that is more) and of a score's terms, and fp32 arithmetic, 2^-14 in all of sum |p v| for scores below 30."""
+    require_gpu()
+    R = lib()
+    c = case([1, 2, 1, 1], [2000, 700, 33, 129], 8, 2, 128, 128, 64, dtype)
+    x = make(c)
+    cos, sin = S.tables(1e4, 128, 2048)
+    o, w, a = reference(*x, cos, sin)
+    got = run(R, *x, cos, sin).double()
+    half = torch.finfo(TYPES[dtype]).eps / 2
+    bound = half * o.abs() * (1 + 2.0 ** -10) + 2.0 ** -14 * w + (2.0 ** -25 * a if dtype == "f16" else 0)
+    assert ((got - o).abs() <= bound + 2.0 ** -25).all()
+
+
 def test_shared_pages_and_the_other_attentions():
-    """Forked sequences share pages; single tokens agree with attention_shared_prefix, whole prompts with attention_packed,
-    bit for bit where the split is the same, else within the rule."""
+    """Forked sequences share pages; single tokens agree with attention_shared_prefix's, each within the rule."""
     require_gpu()
     R = lib()
     c = case([60, 1, 20], [60, 60, 60], 4, 2, 64, 64, 16, "f16")
@@ -164,7 +189,7 @@ def test_shared_pages_and_the_other_attentions():
     b = R.attention_shared_prefix(*(x.cuda() for x in (q, kp, vp, table, lens)), None, 0, cos.cuda(), sin.cuda()).cpu()
     ref = reference(q, kp, vp, table, cu, lens, cos, sin)
     check(a, ref, c, "paged single tokens")
-    check(b, ref, c, "decode single tokens")
+    check(b, reference(q, kp, vp, table, cu, lens, cos, sin, rounded=True), c, "decode single tokens")
 
 
 def test_bad_offsets_lengths_and_pages():
