@@ -1095,7 +1095,10 @@ static cudaError_t launch_paged(const PagedCall &c, const PagedLayout &lay, cuda
     p.causal = c.causal; p.chunk_shift = f.chunk_shift; p.page_shift = c.page_shift;
     p.chunk_bytes = kDecStageBytes<D>; p.tile_ns = D == 128 ? 900 : 700; p.grid = 2 * clusters;
     p.few_warps = paged_few_warps<D>(paged_rows8(group));
-    p.sm_rate = D == 128 ? 53.0f : 48.0f;
+    // (65 of paged_rows8: an SM alone copies faster than when all of them share the memory.
+    // Taken as 53, as 65, as 70: 48 single tokens beside 2107 of chunks 262, 255, 266 us; 100
+    // beside a prompt of 2048 192, 168, 166; 16 beside two chunks of 512 129, 133, 137.)
+    p.sm_rate = paged_rows8(group) ? 65.0f : D == 128 ? 53.0f : 48.0f;
     p.deal = reinterpret_cast<PagedDeal *>(ws);
     p.entries = reinterpret_cast<PagedEntry *>(ws + lay.entries);
     p.chunk_start = reinterpret_cast<int32_t *>(ws + lay.chunk_start);
