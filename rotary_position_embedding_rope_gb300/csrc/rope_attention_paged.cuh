@@ -426,12 +426,13 @@ struct PagedFew {
     // A run's part of a pair has as many rows as the pair, at row 8 w (16 w for 16-row pairs) +
     // the rows of the pairs before it: the run w, the pair or both grow from one part to the
     // next, a pair has at most that many rows, so parts do not meet.
+    __device__ __forceinline__ int32_t part_step() const { return paged_rows8(Hq / Hk) ? 8 : 16; }
     __device__ __forceinline__ int64_t part_row(int32_t w, int32_t b, int32_t hr) const
     {
         const int32_t kv = hr / row_groups, group = Hq / Hk;
         const int64_t in = row_groups > 1 ? (int64_t)kv * group + (hr - kv * row_groups) * rows
                                           : (int64_t)kv * group * tokens(b);
-        return (int64_t)(paged_rows8(group) ? 8 : 16) * w + (int64_t)__ldg(few_start + b) * Hq + in;
+        return (int64_t)part_step() * w + (int64_t)__ldg(few_start + b) * Hq + in;
     }
     __device__ __forceinline__ int32_t part_rows(int32_t b, int32_t hr) const
     {
@@ -960,16 +961,44 @@ struct PagedMerge {
     int32_t lg;
 };
 
+// A row of the few-row sequences: its parts, `step` rows from one to the next, and its output.
+struct FewRow {
+    int64_t from, to;
+    int32_t n, step;
+    __device__ __forceinline__ void find(const PagedMerge &g, int64_t row)
+    {
+        const PagedFew &f = g.few;
+        const int32_t group = f.Hq / f.Hk, heads = f.heads();
+        const int32_t t = (int32_t)divide(row, f.Hq), h = (int32_t)(row - (int64_t)t * f.Hq);
+        const int32_t b = __ldg(g.few_seq + t), tok = t - __ldg(f.few_start + b);
+        const int32_t kv = h / group, in_group = h - kv * group, rg = in_group / f.rows;
+        const int32_t hr = kv * f.row_groups + rg, r = tok * f.rows + in_group - rg * f.rows;
+        const int64_t c0 = __ldg(f.chunk_start + b), c1 = __ldg(f.chunk_start + b + 1), per = __ldg(&g.deal->per);
+        const int64_t at = c0 * heads + hr * (c1 - c0), first = divide(at, per);
+        n = c1 > c0 ? (int32_t)(divide(at + (c1 - c0) - 1, per) - first + 1) : 0;
+        from = f.part_row((int32_t)first, b, hr) + r;
+        step = f.part_step();
+        to = ((int64_t)__ldg(f.cu + b) + tok) * f.Hq + h;
+    }
+};
+
 template <typename T, int D, int W>
 __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_paged_merge_kernel(const __grid_constant__ PagedMerge g)
 {
     constexpr int kWarps = W == 1 ? 4 : W;
     const int warp = threadIdx.x >> 5;
     const PagedFew &f = g.few;
+    constexpr int kRows = W == 1 ? kWarps : 1;                 // few-row rows of a CTA at once
+    // The plan is complete before the attention's CTAs let this kernel start (they wait for it
+    // first), so what it says of the first row is looked up beside their end.
+    const int32_t clusters = __ldg(&g.deal->clusters);
+    const int64_t rows = (int64_t)__ldg(&g.deal->few_tokens) * f.Hq;
+    int64_t row = (int64_t)blockIdx.x * kRows + (W == 1 ? warp : 0);
+    FewRow few = {};
+    if (row < rows)
+        few.find(g, row);
     pdl_wait();
     pdl_trigger();
-    const int32_t clusters = __ldg(&g.deal->clusters);
-    const int64_t per = __ldg(&g.deal->per);
     // Cut i, where it goes through a unit that no earlier cut goes through: that unit's
     // 256 rows, a warp each.
     constexpr int kSteps = 256 / kWarps;
@@ -997,33 +1026,16 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_paged_merge_kernel
         });
     }
     // The few-row sequences: (token, head).
-    constexpr int kRows = W == 1 ? kWarps : 1;                 // of a CTA at once
-    const int64_t rows = (int64_t)__ldg(&g.deal->few_tokens) * f.Hq;
-    const int32_t group = f.Hq / f.Hk, heads = f.heads();
-    for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < rows; row0 += (int64_t)gridDim.x * kRows) {
-        const int64_t row = row0 + (W == 1 ? warp : 0);
-        if (row >= rows)
-            continue;
-        const int32_t t = (int32_t)divide(row, f.Hq), h = (int32_t)(row - (int64_t)t * f.Hq);
-        const int32_t b = __ldg(g.few_seq + t), tok = t - __ldg(f.few_start + b), start = __ldg(f.cu + b);
-        const int32_t kv = h / group, in_group = h - kv * group, rg = in_group / f.rows;
-        const int32_t hr = kv * f.row_groups + rg, r = tok * f.rows + in_group - rg * f.rows;
-        const int64_t c0 = __ldg(f.chunk_start + b), c1 = __ldg(f.chunk_start + b + 1);
-        int64_t first = 0;
-        int32_t n = 0;
-        if (c1 > c0) {
-            const int64_t at = c0 * heads + hr * (c1 - c0);
-            first = divide(at, per);
-            n = (int32_t)(divide(at + (c1 - c0) - 1, per) - first + 1);
-        }
+    for (; row < rows; row += (int64_t)gridDim.x * kRows) {
+        if (row >= (int64_t)gridDim.x * kRows)
+            few.find(g, row);
         if constexpr (W > 1)
             __syncthreads();                                   // the last row's parts are read
-        merge_parts<T, D, W>(n, static_cast<T *>(g.o) + ((int64_t)(start + tok) * f.Hq + h) * D,
-                             [&](int32_t p, float2 &stat) {
-                                 const int64_t at = f.part_row((int32_t)first + p, b, hr) + r;
-                                 stat = __ldg(f.stats + at);
-                                 return (const float *)f.out + at * D;
-                             });
+        merge_parts<T, D, W>(few.n, static_cast<T *>(g.o) + few.to * D, [&](int32_t p, float2 &stat) {
+            const int64_t at = few.from + (int64_t)p * few.step;
+            stat = __ldg(f.stats + at);
+            return (const float *)f.out + at * D;
+        });
     }
 }
 
