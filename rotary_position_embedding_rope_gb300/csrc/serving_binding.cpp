@@ -12,7 +12,8 @@
 #include <algorithm>
 #include <cstdint>
 #include <initializer_list>
-#include <optional>
+#include <memory>
+#include <mutex>
 #include <string>
 
 #include <ATen/core/Tensor.h>
@@ -21,10 +22,11 @@
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/saved_variable.h>
 #include <torch/csrc/autograd/variable.h>
 
 #include "rope.h"
@@ -763,11 +765,6 @@ PyObject *norm_rotate_qk_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
 // training step makes them once a layer: with a Python node, forward and backward of
 // a small layer took 200 us of the host's time.
 
-// A status that the library returned, on its way to the Python side.
-struct StatusError {
-    rope_status st;
-};
-
 int32_t dtype_code(at::ScalarType t)
 {
     return t == at::kFloat ? ROPE_F32 : t == at::kBFloat16 ? ROPE_BF16 : ROPE_F16;
@@ -824,72 +821,47 @@ at::Tensor dense_vectors(const at::Tensor &t)
     return reinterpret_cast<uintptr_t>(d.data_ptr()) % 16 == 0 ? d : d.clone();
 }
 
-using Given = std::optional<at::Tensor>;       // nothing: None
+// The backward node: queries, keys and weights (undefined: None), the tables and positions.
+struct NormRotaryBackward : torch::autograd::Node {
+    torch::autograd::SavedVariable saved[7];   // q, k, wq, wk, cos, sin, pos_idx
+    bool given[7] = {};
+    double eps = 0.0;
+    int32_t layout = 0;
+    bool seq_first = false;
 
-struct NormRotary : torch::autograd::Function<NormRotary> {
-    static torch::autograd::variable_list forward(torch::autograd::AutogradContext *ctx, const Given &q, const Given &k,
-                                                  const Given &gwq, const Given &gwk, const at::Tensor &cos,
-                                                  const at::Tensor &sin, const Given &positions, double eps, int64_t layout,
-                                                  bool seq_first)
+    std::string name() const override { return "NormRotaryBackward"; }
+
+    void release_variables() override
     {
-        const at::Tensor wq = gwq.value_or(at::Tensor()), wk = gwk.value_or(at::Tensor()),
-                         pos = positions.value_or(at::Tensor());
-        at::Tensor x[2] = {q.value_or(at::Tensor()), k.value_or(at::Tensor())}, y[2];
-        for (at::Tensor &t : x)
-            if (t.defined() && !whole_vectors(t))
-                t = t.clone(at::MemoryFormat::Contiguous);
-        const at::Tensor w[2] = {wq, wk};
-        const NormSizes z(x, w, cos, pos, seq_first);
-        torch::autograd::variable_list out;
-        for (int i = 0; i < 2; ++i)
-            if (x[i].defined()) {
-                y[i] = at::empty(x[i].sizes(), x[i].options().memory_format(at::MemoryFormat::Contiguous));
-                out.push_back(y[i]);
-            }
-        const rope_status st = g_norm(address(x[0]), address(x[1]), address(y[0]), address(y[1]), address(wq), address(wk),
-                                      cos.const_data_ptr<float>(), sin.const_data_ptr<float>(),
-                                      static_cast<const int32_t *>(address(pos)), z.pos_stride, z.B, z.H[0], z.H[1], z.S, z.D,
-                                      z.strides[0], z.strides[1], z.rotary_dim, (int32_t)layout, seq_first, (float)eps, z.code,
-                                      z.w_code, z.rows, c10::cuda::getCurrentCUDAStream(cos.get_device()).stream());
-        if (st != ROPE_OK)
-            throw StatusError{st};
-        ctx->save_for_backward({x[0], x[1], wq, wk, cos, sin, pos});
-        ctx->saved_data["eps"] = eps;
-        ctx->saved_data["layout"] = layout;
-        ctx->saved_data["seq_first"] = seq_first;
-        ctx->set_materialize_grads(false);
-        return out;
+        const std::lock_guard<std::mutex> lock(mutex_);
+        for (auto &v : saved)
+            v.reset_data();
     }
 
-    static torch::autograd::variable_list backward(torch::autograd::AutogradContext *ctx, torch::autograd::variable_list grads)
+    torch::autograd::variable_list apply(torch::autograd::variable_list &&grads) override
     {
-        const torch::autograd::variable_list saved = ctx->get_saved_variables();
-        const at::Tensor &cos = saved[4], &sin = saved[5], &pos = saved[6];
-        const bool seq_first = ctx->saved_data["seq_first"].toBool();
+        const std::lock_guard<std::mutex> lock(mutex_);
+        const auto self = shared_from_this();
+        auto unpacked = [&](int i) { return given[i] ? saved[i].unpack(self) : at::Tensor(); };
+        const at::Tensor cos = unpacked(4), sin = unpacked(5), pos = unpacked(6);
         at::Tensor x[2], w[2], g[2], dx[2], dw[2];
-        // (torch counts the given tensors alone)
-        auto needs = [&](int i) {
-            int at = 0;
-            for (int j = 0; j < i; ++j)
-                at += saved[j].defined();
-            return saved[i].defined() && ctx->needs_input_grad(at);
-        };
         // an output that took no part in the loss has no gradient, and an input (and weight)
         // that needs none is left out
         int next = 0;
         for (int i = 0; i < 2; ++i) {
-            if (!saved[i].defined())
+            if (!given[i])
                 continue;
             const at::Tensor &up = grads[next++];
-            if (!up.defined() || !(needs(i) || needs(2 + i)))
+            if (!up.defined() || !(task_should_compute_output(i) || task_should_compute_output(2 + i)))
                 continue;
-            x[i] = saved[i];
-            w[i] = saved[2 + i];
+            x[i] = unpacked(i);
+            w[i] = unpacked(2 + i);
             g[i] = dense_vectors(up);
             dx[i] = at::empty(x[i].sizes(), x[i].options().memory_format(at::MemoryFormat::Contiguous));
-            if (needs(2 + i))
+            if (w[i].defined() && task_should_compute_output(2 + i))
                 dw[i] = at::empty({x[i].size(3)}, w[i].options());
         }
+        torch::autograd::variable_list out(4);
         if (x[0].defined() || x[1].defined()) {
             const NormSizes z(x, w, cos, pos, seq_first);
             const c10::cuda::CUDAGuard guard(cos.get_device());
@@ -900,15 +872,13 @@ struct NormRotary : torch::autograd::Function<NormRotary> {
                 g_norm_bwd(address(x[0]), address(x[1]), address(g[0]), address(g[1]), address(dx[0]), address(dx[1]),
                            address(w[0]), address(w[1]), address(dw[0]), address(dw[1]), cos.const_data_ptr<float>(),
                            sin.const_data_ptr<float>(), static_cast<const int32_t *>(address(pos)), z.pos_stride, z.B, z.H[0],
-                           z.H[1], z.S, z.D, z.strides[0], z.strides[1], z.rotary_dim, (int32_t)ctx->saved_data["layout"].toInt(),
-                           seq_first, (float)ctx->saved_data["eps"].toDouble(), z.code, z.w_code, z.rows, address(ws),
-                           ws.defined() ? (int64_t)ws.nbytes() : 0,
+                           z.H[1], z.S, z.D, z.strides[0], z.strides[1], z.rotary_dim, layout, seq_first, (float)eps, z.code,
+                           z.w_code, z.rows, address(ws), ws.defined() ? (int64_t)ws.nbytes() : 0,
                            c10::cuda::getCurrentCUDAStream(cos.get_device()).stream());
             TORCH_CHECK(st == ROPE_OK, "rope_norm_qk_bwd: status ", (int)st);
         }
-        torch::autograd::variable_list out(10);
         for (int i = 0; i < 2; ++i) {
-            if (needs(i))
+            if (task_should_compute_output(i))
                 out[i] = dx[i];
             out[2 + i] = dw[i];
         }
@@ -922,6 +892,48 @@ struct NormRotary : torch::autograd::Function<NormRotary> {
         return out;
     }
 };
+
+// The forward call on checked arguments, and its node where a gradient is wanted.
+rope_status norm_rotary_forward(const at::Tensor (&in)[7], double eps, int32_t layout, bool seq_first, at::Tensor (&y)[2])
+{
+    at::Tensor x[2] = {in[0], in[1]};
+    const at::Tensor w[2] = {in[2], in[3]}, &cos = in[4], &sin = in[5], &pos = in[6];
+    bool graph = false;
+    for (int i = 0; i < 4 && at::GradMode::is_enabled(); ++i)
+        graph = graph || (in[i].defined() && in[i].requires_grad());
+    {
+        const at::AutoGradMode off(false);
+        for (int i = 0; i < 2; ++i)
+            if (x[i].defined()) {
+                if (!whole_vectors(x[i]))
+                    x[i] = x[i].clone(at::MemoryFormat::Contiguous);
+                y[i] = at::empty(x[i].sizes(), x[i].options().memory_format(at::MemoryFormat::Contiguous));
+            }
+    }
+    const NormSizes z(x, w, cos, pos, seq_first);
+    const rope_status st = g_norm(address(x[0]), address(x[1]), address(y[0]), address(y[1]), address(w[0]), address(w[1]),
+                                  cos.const_data_ptr<float>(), sin.const_data_ptr<float>(),
+                                  static_cast<const int32_t *>(address(pos)), z.pos_stride, z.B, z.H[0], z.H[1], z.S, z.D,
+                                  z.strides[0], z.strides[1], z.rotary_dim, layout, seq_first, (float)eps, z.code, z.w_code, z.rows,
+                                  c10::cuda::getCurrentCUDAStream(cos.get_device()).stream());
+    if (st != ROPE_OK || !graph)
+        return st;
+    const std::shared_ptr<NormRotaryBackward> node(new NormRotaryBackward(), torch::autograd::deleteNode);
+    node->set_next_edges(torch::autograd::collect_next_edges(in[0], in[1], in[2], in[3]));
+    for (int i = 0; i < 7; ++i) {
+        const at::Tensor &t = i < 2 ? x[i] : in[i];
+        node->given[i] = t.defined();
+        if (t.defined())
+            node->saved[i] = torch::autograd::SavedVariable(t, false);
+    }
+    node->eps = eps;
+    node->layout = layout;
+    node->seq_first = seq_first;
+    for (at::Tensor &t : y)
+        if (t.defined())
+            torch::autograd::set_history(t, node);
+    return ROPE_OK;
+}
 
 // Whether a tensor is a leaf whose gradients a graph that is alive accumulates on
 // another stream than the current one.  (The engine would make that stream wait for a
@@ -989,17 +1001,18 @@ PyObject *norm_rotary_qk(PyObject *, PyObject *const *a, Py_ssize_t n)
                     fail(PyExc_RuntimeError, std::string("a graph of ") + (i < 2 ? "" : "w") + (i % 2 ? "k" : "q") +
                                                  " made on another stream is alive: drop it before the backward pass is captured");
         }
-        torch::autograd::variable_list out;
+        const at::Tensor in[7] = {q, k, wq, wk, cos, sin, pos};
+        at::Tensor out[2];
+        rope_status st;
         {
             const Unlocked u;
-            auto maybe = [](const at::Tensor &t) { return t.defined() ? Given(t) : Given(); };
-            out = NormRotary::apply(maybe(q), maybe(k), maybe(wq), maybe(wk), cos, sin, maybe(pos), eps, layout, seq_first);
+            st = norm_rotary_forward(in, eps, (int32_t)layout, seq_first, out);
         }
-        return tuple_of({has_q ? out[0] : at::Tensor(), has_k ? out[has_q ? 1 : 0] : at::Tensor()});
+        if (st != ROPE_OK)
+            return status(st);
+        return tuple_of({out[0], out[1]});
     } catch (const PythonError &) {
         return nullptr;
-    } catch (const StatusError &e) {
-        return status(e.st);
     }
     END_HANDLE_TH_ERRORS
 }

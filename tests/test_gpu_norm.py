@@ -201,6 +201,49 @@ def test_graphs_of_parts():
     assert R.rope_check_errors() == R.ROPE_OK
 
 
+def test_graph_rules():
+    """What autograd promises of any node: saved tensors that changed are an error, so is a second backward pass or a second
+    derivative; without a graph there is no node; leaves on several calls add up."""
+    require_gpu()
+    lib()
+    from rotary_position_embedding_rope_gb300 import autograd
+
+    t = {n: x.cuda() for n, x in make(1, 12, 2, 1, 64, "f32", "f32", True).items()}
+    cos, sin = (x.cuda() for x in S.tables(1e4, 64, 16))
+    leaves = [t[n].clone().requires_grad_() for n in ("q", "k", "wq", "wk")]
+    call = lambda: autograd.norm_rotary_qk(*leaves, cos, sin, seq_before_head=True)
+    with torch.no_grad():
+        assert not any(o.requires_grad for o in call())
+    assert not any(o.requires_grad for o in autograd.norm_rotary_qk(*(x.detach() for x in leaves), cos, sin, seq_before_head=True))
+    out = call()
+    assert all(o.requires_grad and not o.is_leaf for o in out)
+    out[0].sum().backward()
+    once = leaves[0].grad.clone()
+    with pytest.raises(RuntimeError, match="second time"):
+        out[0].sum().backward()
+    call()[0].sum().backward()
+    assert torch.equal(leaves[0].grad, 2 * once)
+    out = call()
+    with torch.no_grad():
+        leaves[2].add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        out[0].sum().backward()
+    g, = torch.autograd.grad(call()[0].square().sum(), leaves[0], create_graph=True)
+    with pytest.raises(RuntimeError, match="cannot be differentiated"):
+        g.sum().backward()
+    # a graph behind the inputs, and hooks on the way
+    seen = []
+    x = leaves[0] * 3
+    x.register_hook(lambda d: seen.append(d.shape))
+    o, _ = autograd.norm_rotary_qk(x, None, leaves[2], None, cos, sin, seq_before_head=True)
+    d, = torch.autograd.grad(o.sum(), leaves[0])
+    assert seen == [x.shape] and d.isfinite().all()
+    # saved tensors may be packed elsewhere
+    with torch.autograd.graph.save_on_cpu():
+        o, _ = autograd.norm_rotary_qk(x.detach().requires_grad_(), None, leaves[2], None, cos, sin, seq_before_head=True)
+    o.sum().backward()
+
+
 def test_empty_and_zero_rows():
     require_gpu()
     R = lib()
