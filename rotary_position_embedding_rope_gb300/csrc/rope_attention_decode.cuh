@@ -228,12 +228,10 @@ struct DecodeArgs {
         listed = b < B ? max_blocks : ((int64_t)n_prefix - 1 >> page_shift) + 1;
         return b < B ? table + b * max_blocks : prefix_table;
     }
-    // Row r of pair (b, hr): where its query lies (null: no such row) and the table
-    // row that rotates it.  The rows are heads of one sequence, or, for the folded
-    // prefix, of the whole batch.
+    // Row r of pair (b, hr): where its query lies (null: no such row), and whose it is.  The
+    // rows are heads of one sequence, or, for the folded prefix, of the whole batch.
     template <typename T, int D>
-    __device__ __forceinline__ const T *query(int32_t b, int32_t hr, int32_t r, int64_t most, bool rot,
-                                              int64_t &trow) const
+    __device__ __forceinline__ const T *query(int32_t b, int32_t hr, int32_t r, int32_t &whose) const
     {
         const int32_t kv = hr / row_groups, group = Hq / Hk, r0 = (hr - kv * row_groups) * rows;
         bool live = r < rows && r0 + r < group;
@@ -242,13 +240,16 @@ struct DecodeArgs {
             r -= b * group;
             live = b < B;
         }
-        if (!live)
-            return nullptr;
-        if (rot)
-            trow = query_row(pos_q, b,
-                             pos_q != nullptr ? 0 : (int64_t)n_prefix + suffix_keys(lens, b, most, a.flag),
-                             a.table_rows, a.flag);
-        return static_cast<const T *>(q) + b * q_stride + (int64_t)(kv * group + r0 + r) * D;
+        whose = b;
+        return live ? static_cast<const T *>(q) + b * q_stride + (int64_t)(kv * group + r0 + r) * D : nullptr;
+    }
+    // The table row that rotates it (apart from its place: the query's loads go out before
+    // the position's have come).
+    __device__ __forceinline__ int64_t query_turn(int32_t, int32_t whose, int64_t most) const
+    {
+        return query_row(pos_q, whose,
+                         pos_q != nullptr ? 0 : (int64_t)n_prefix + suffix_keys(lens, whose, most, a.flag),
+                         a.table_rows, a.flag);
     }
     // Keys that row r of sequence b's pairs sees, of n.
     __device__ __forceinline__ int32_t limit(int32_t, int32_t, int32_t n) const { return n; }
@@ -363,10 +364,13 @@ __device__ __forceinline__ void load_query_rows(const G &g, const ChunkAt &at, i
     for (int i = 0; i < kSteps; ++i) {
         x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
         trow[i] = -1;
-        const T *row = g.template query<T, D>(at.b, at.hr, i * kAtOnce + lane / L, most, part.rot, trow[i]);
+        int32_t whose;
+        const T *row = g.template query<T, D>(at.b, at.hr, i * kAtOnce + lane / L, whose);
         if (row != nullptr) {
             x0[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o0));
             x1[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o1));
+            if (part.rot)
+                trow[i] = g.query_turn(at.b, whose, most);
         }
     }
 #pragma unroll

@@ -391,24 +391,25 @@ struct PagedFew {
     // Rows of a pair: heads of a token, token after token; with more than 16 heads in
     // a group 16 of one token.
     template <typename T, int D>
-    __device__ __forceinline__ const T *query(int32_t b, int32_t hr, int32_t r, int64_t, bool rot,
-                                              int64_t &trow) const
+    __device__ __forceinline__ const T *query(int32_t b, int32_t hr, int32_t r, int32_t &token) const
     {
         const int32_t kv = hr / row_groups, group = Hq / Hk, h0 = (hr - kv * row_groups) * rows;
         const int32_t start = __ldg(cu + b), Lq = __ldg(cu + b + 1) - start;
         const int32_t tok = r / rows, h = h0 + r - tok * rows;
-        if (tok >= Lq || h >= group)
-            return nullptr;
-        if (rot)
-            trow = row_of(start, tok, (int64_t)__ldg(lens + b) - Lq + tok);
-        return static_cast<const T *>(q) + (start + tok) * q_stride + (int64_t)(kv * group + h) * D;
+        token = start + tok;
+        return tok < Lq && h < group ? static_cast<const T *>(q) + token * q_stride + (int64_t)(kv * group + h) * D
+                                     : nullptr;
+    }
+    __device__ __forceinline__ int64_t query_turn(int32_t b, int32_t token, int64_t) const
+    {
+        return row_of(token, (int64_t)__ldg(lens + b) - (__ldg(cu + b + 1) - token));
     }
     // Table row of a token: pos_q's, or its index among its sequence's keys.  -1: as it is.
-    __device__ __forceinline__ int64_t row_of(int32_t start, int32_t tok, int64_t index) const
+    __device__ __forceinline__ int64_t row_of(int32_t token, int64_t index) const
     {
         if (a.cos == nullptr)
             return -1;
-        const int64_t row = pos_q != nullptr ? (int64_t)__ldg(pos_q + start + tok) : index;
+        const int64_t row = pos_q != nullptr ? (int64_t)__ldg(pos_q + token) : index;
         if (row >= 0 && row < a.table_rows)
             return row;
         // (a token before the sequence's first key sees none when causal: its row does not matter)
@@ -486,10 +487,13 @@ __device__ __forceinline__ void load_query_rows8(const PagedFew &g, const ChunkA
     for (int i = 0; i < kSteps; ++i) {
         x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
         trow[i] = -1;
-        const T *row = g.template query<T, D>(at.b, at.hr, i * kAtOnce + lane / L, most, part.rot, trow[i]);
+        int32_t token;
+        const T *row = g.template query<T, D>(at.b, at.hr, i * kAtOnce + lane / L, token);
         if (row != nullptr) {
             x0[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o0));
             x1[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o1));
+            if (part.rot)
+                trow[i] = g.query_turn(at.b, token, most);
         }
     }
     uint4 y0[kSteps], y1[kSteps];              // what the rounded values leave
@@ -812,7 +816,7 @@ struct PagedSource {
     }
     __device__ __forceinline__ int64_t table_row(const PackedUnit &u, int32_t t) const
     {
-        return few.row_of(u.q_start, t, (int64_t)u.n_keys - u.tokens + t);
+        return few.row_of(u.q_start + t, (int64_t)u.n_keys - u.tokens + t);
     }
 
     // z of page i of the unit's sequence in the pools' maps; past the last page, and for
@@ -970,15 +974,15 @@ struct FewRow {
         const PagedFew &f = g.few;
         const int32_t group = f.Hq / f.Hk, heads = f.heads();
         const int32_t t = (int32_t)divide(row, f.Hq), h = (int32_t)(row - (int64_t)t * f.Hq);
-        const int32_t b = __ldg(g.few_seq + t), tok = t - __ldg(f.few_start + b);
+        const int32_t b = __ldcg(g.few_seq + t), tok = t - __ldcg(f.few_start + b);
         const int32_t kv = h / group, in_group = h - kv * group, rg = in_group / f.rows;
         const int32_t hr = kv * f.row_groups + rg, r = tok * f.rows + in_group - rg * f.rows;
-        const int64_t c0 = __ldg(f.chunk_start + b), c1 = __ldg(f.chunk_start + b + 1), per = __ldg(&g.deal->per);
+        const int64_t c0 = __ldcg(f.chunk_start + b), c1 = __ldcg(f.chunk_start + b + 1), per = __ldcg(&g.deal->per);
         const int64_t at = c0 * heads + hr * (c1 - c0), first = divide(at, per);
         n = c1 > c0 ? (int32_t)(divide(at + (c1 - c0) - 1, per) - first + 1) : 0;
         from = f.part_row((int32_t)first, b, hr) + r;
         step = f.part_step();
-        to = ((int64_t)__ldg(f.cu + b) + tok) * f.Hq + h;
+        to = ((int64_t)__ldcg(f.cu + b) + tok) * f.Hq + h;
     }
 };
 
@@ -990,9 +994,10 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_paged_merge_kernel
     const PagedFew &f = g.few;
     constexpr int kRows = W == 1 ? kWarps : 1;                 // few-row rows of a CTA at once
     // The plan is complete before the attention's CTAs let this kernel start (they wait for it
-    // first), so what it says of the first row is looked up beside their end.
-    const int32_t clusters = __ldg(&g.deal->clusters);
-    const int64_t rows = (int64_t)__ldg(&g.deal->few_tokens) * f.Hq;
+    // first), so what it says of the first row is looked up beside their end; in L2, since
+    // nothing before the wait below orders it against what this SM's L1 may hold.
+    const int32_t clusters = __ldcg(&g.deal->clusters);
+    const int64_t rows = (int64_t)__ldcg(&g.deal->few_tokens) * f.Hq;
     int64_t row = (int64_t)blockIdx.x * kRows + (W == 1 ? warp : 0);
     FewRow few = {};
     if (row < rows)
