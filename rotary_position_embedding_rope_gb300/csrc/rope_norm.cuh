@@ -436,8 +436,9 @@ __device__ __forceinline__ void norm_run(const NormArgs &a, const NormTensor &x,
                 sum = dot = 0.0f;
             const float r = norm_scale(group_sum<L>(sum), a.inv_d, a.eps);
             if constexpr (BACKWARD) {
-                // mean(w g n) n = r^2 mean(w g x) x
-                const float m = group_sum<L>(dot) * a.inv_d * (r * r * r);
+                // r mean(w g n) n = r^3 mean(w g x) x  (one r at a time: mean(w g x) r is of the
+                // size of w g, where r^3 alone leaves fp32's range for rows of 10^13)
+                const float m = group_sum<L>(dot) * a.inv_d * r * r * r;
                 const uint64_t r2 = f32x2(r, r), m2 = f32x2(-m, -m);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -665,7 +666,7 @@ static cudaError_t launch_norm_lanes(NormArgs a, cudaStream_t st)
     for (int k = 0; k < 2; ++k)
         a.tiles[k] = (a.tokens + groups - 1) / groups * ((a.t[k].heads + U - 1) / U);
     const int64_t tiles = a.tiles[0] + a.tiles[1];
-    if (tiles > (1ll << 40))                   // (a run has to fit 32 bits)
+    if (tiles > (1ll << 38))                   // (a run, of a CTA of hundreds, has to fit 32 bits)
         return cudaErrorInvalidConfiguration;
     static std::atomic<uint64_t> raised{0};
     auto *kernel = rope_norm_kernel<T, LAYOUT, L, BACKWARD>;

@@ -993,6 +993,8 @@ PyObject *norm_rotary_qk(PyObject *, PyObject *const *a, Py_ssize_t n)
         const double eps = number(a[6]);
         const int64_t layout = integer(a[9]);
         const c10::cuda::CUDAGuard guard(c.device);
+        for (const at::Tensor &x : {q, k, wq, wk})
+            TORCH_CHECK(!x.defined() || !x._fw_grad(0).defined(), "norm_rotary_qk: has no forward-mode derivative");
         if (at::GradMode::is_enabled() &&
             c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
             const at::Tensor leaves[4] = {q, k, wq, wk};

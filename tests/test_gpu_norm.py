@@ -244,6 +244,43 @@ def test_graph_rules():
     o.sum().backward()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [2.0 ** 50, 2.0 ** -46])
+def test_rows_of_extreme_size(dtype, size):
+    """Rows whose squares still fit fp32 while the third power of 1 / |x| does not; eps 0, as the formula allows."""
+    require_gpu()
+    R = lib()
+    B, S_, Hq, Hk, D = 1, 40, 3, 2, 64
+    t = make(B, S_, Hq, Hk, D, dtype, "f32", True)
+    t["q"], t["k"] = t["q"] * size, t["k"] * size
+    assert t["q"].isfinite().all() and t["q"].dtype == TYPES[dtype]
+    cos, sin = S.tables(1e4, D, S_)
+    d = {n: x.cuda() for n, x in t.items()}
+    out = R.norm_rotate_qk(d["q"], d["k"], d["wq"], d["wk"], cos.cuda(), sin.cuda(), 0.0, seq_before_head=True)
+    grads = R.norm_rotate_qk_backward(d["gq"], d["gk"], d["q"], d["k"], d["wq"], d["wk"], cos.cuda(), sin.cuda(), 0.0,
+                                      seq_before_head=True)
+    c, s = (x[:, :, None] for x in N.angles(rows_of(None, B, S_), cos, sin))
+    for i, n in enumerate("qk"):
+        near(out[i], *N.forward(t[n], t["w" + n], c, s, "split_half", 0.0), n)
+        dx, bx, dw, bw = N.backward(t[n], t["w" + n], t["g" + n], c, s, "split_half", 0.0)
+        near(grads[i], dx, bx, "d" + n)
+        near(grads[2 + i], dw, bw, "dw" + n)
+
+
+def test_forward_mode_is_refused():
+    """A tangent would be dropped without a word."""
+    require_gpu()
+    lib()
+    from rotary_position_embedding_rope_gb300 import autograd
+
+    t = {n: x.cuda() for n, x in make(1, 12, 2, 1, 64, "f32", "f32", True).items()}
+    cos, sin = (x.cuda() for x in S.tables(1e4, 64, 16))
+    with torch.autograd.forward_ad.dual_level():
+        w = torch.autograd.forward_ad.make_dual(t["wq"], torch.ones_like(t["wq"]))
+        with pytest.raises(RuntimeError, match="forward-mode"):
+            autograd.norm_rotary_qk(t["q"], t["k"], w, t["wk"], cos, sin, seq_before_head=True)
+
+
 def test_empty_and_zero_rows():
     require_gpu()
     R = lib()
