@@ -214,7 +214,7 @@ struct DecodeArgs {
 
     // What the suffix code below asks of its arguments (the paged attention's
     // are others, rope_attention_paged.cuh).
-    static constexpr bool kRowLimits = false;  // every row sees all keys of its pair
+    static constexpr int32_t kPairCost = 0;    // chunks that a pair counts for besides its own
     __device__ __forceinline__ int32_t sequences() const { return B + fold; }
     __device__ __forceinline__ int32_t heads() const { return Hk * row_groups; }
     __device__ __forceinline__ int64_t most_keys() const { return max_blocks << page_shift; }
@@ -251,8 +251,6 @@ struct DecodeArgs {
                          pos_q != nullptr ? 0 : (int64_t)n_prefix + suffix_keys(lens, whose, most, a.flag),
                          a.table_rows, a.flag);
     }
-    // Keys that row r of sequence b's pairs sees, of n.
-    __device__ __forceinline__ int32_t limit(int32_t, int32_t, int32_t n) const { return n; }
     // The first row of warp w's part of pair (b, hr), and how many rows it has.
     __device__ __forceinline__ int64_t part_row(int32_t w, int32_t b, int32_t hr) const
     {
@@ -479,10 +477,15 @@ __device__ __forceinline__ SuffixRun suffix_run(const G &g, const int32_t *start
         const int32_t b = find_sequence(start, n_seqs + 1, divide(c, heads));
         // (the last b whose start is at most c / heads has chunks)
         run.at.b = b;
-        run.at.n = start[b + 1] - start[b];
+        const int32_t n = start[b + 1] - start[b];
+        run.at.n = n - G::kPairCost;
         const int64_t in = c - (int64_t)start[b] * heads;
-        run.at.hr = (int32_t)divide(in, run.at.n);
-        run.at.ch = (int32_t)(in - (int64_t)run.at.hr * run.at.n);
+        run.at.hr = (int32_t)divide(in, n);
+        run.at.ch = (int32_t)(in - (int64_t)run.at.hr * n) - G::kPairCost;
+        if (G::kPairCost > 0 && run.at.ch < 0) {               // in the pair's charge
+            run.left += run.at.ch;
+            run.at.ch = 0;
+        }
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -546,6 +549,8 @@ struct SuffixCopies {
         }
         --left;
         ahead.next(g, most);
+        if (G::kPairCost > 0 && ahead.ch == 0)
+            left -= G::kPairCost;
     }
 };
 
@@ -577,7 +582,6 @@ __device__ __forceinline__ void decode_suffixes(const G &g, uint8_t *smem, const
     float o[D / 8][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;   // rows lane / 4 and + 8
     int32_t keys = 0;                                          // of the pair's suffix
-    int32_t lim0 = 0, lim1 = 0, low = 0;                       // keys that the two rows see, and that all rows see
     bool fresh = true;
     int st = 0;
     uint32_t ph = 0;
@@ -589,11 +593,6 @@ __device__ __forceinline__ void decode_suffixes(const G &g, uint8_t *smem, const
     for (; ok && left > 0; --left, ++done) {
         if (fresh) {
             keys = g.keys(at.b, most);
-            if constexpr (G::kRowLimits) {
-                lim0 = g.limit(at.b, lane >> 2, keys);
-                lim1 = g.limit(at.b, (lane >> 2) + 8, keys);
-                low = g.limit(at.b, 0, keys);
-            }
             load_query_rows<T, LAYOUT, D>(g, at, most, qtile, qf);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
@@ -643,17 +642,6 @@ __device__ __forceinline__ void decode_suffixes(const G &g, uint8_t *smem, const
                     sc[i] = sd[i] = -INFINITY;
                     // what lies behind the last key (anything) must not meet a zero
                     vis[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
-                }
-            }
-        }
-        if constexpr (G::kRowLimits) {
-            if (low - at.ch * kKeys < kKeys) {                 // keys that some row does not see
-                const int32_t n0 = lim0 - at.ch * kKeys, n1 = lim1 - at.ch * kKeys;
-#pragma unroll
-                for (int i = 0; i < 4 * kGroups; ++i) {
-                    const int key = c0 + (i & 1) + (i >> 1) * 8;
-                    sc[i] = key < n0 ? sc[i] : -INFINITY;
-                    sd[i] = key < n1 ? sd[i] : -INFINITY;
                 }
             }
         }

@@ -15,7 +15,7 @@
 //           batch of ragged chunks both keep every cluster busy to the end.  A unit
 //           that lies in one run is written by it; a cut one leaves an fp32 (O, m,
 //           l) per piece;
-//   few     the others, of at most eight rows, or a single token, are dealt out as
+//   few     the others, of at most 16 rows, or a single token, are dealt out as
 //           the suffixes of the shared-prefix decode: equal runs of 16-key (32 for
 //           heads of 64) chunks for all warps of the SMs that have no tiles, an fp32
 //           (O, m, l) for each pair (sequence, key head) that a run touches.
@@ -30,10 +30,10 @@
 // The split depends on the sizes and the lengths alone: the same call gives the
 // same bits.
 //
-// Roundings: for the tiles rot(q), and P before P V, to the element type (operands of
-// a 16-bit product, whose issue is the bound), as in the packed attention; for the few
-// rows they go into the products as two 16-bit parts (paged_rows8_run).  Everything
-// else is fp32 until o.
+// Roundings: for the tiles, and for sequences of nine to 16 rows, rot(q), and P before
+// P V, to the element type (operands of a 16-bit product, whose issue is the bound), as in
+// the packed attention; for at most eight rows they go into the products as two 16-bit
+// parts (few_pair).  Everything else is fp32 until o.
 #pragma once
 
 #include "rope_attention_decode.cuh"
@@ -65,24 +65,26 @@ constexpr int32_t kPagedUnitTiles = 4;
 // Least weight of a cluster's run: shorter runs leave more pieces than they save.
 constexpr int64_t kPagedMinRun = 2 * kPagedUnitTiles;
 constexpr int32_t kPagedClusters = kDecodeSms / 2;   // at most
-// Warps of an SM that take few-row sequences: twelve of paged_rows8 or, for heads of 64,
-// of decode_suffixes, whose rows of heads of 128 leave registers and memory for eight.
+// What a pair (sequence, key head) of a few-row sequence counts for besides its chunks, in
+// chunks: its queries' way in and its outputs' way out, several loads one after the other.
+// Without it the warps that got the short sequences ended last.  0, 2, 5, 12 of them (us): 40
+// drafts of up to five tokens, heads of 64, contexts to 3k 70, 48.7, 47.7, 47.8; 64 of four
+// tokens, groups of four, contexts to 4k 119, 111, 109, 108; 64 single tokens, contexts to 8k
+// 175.5, 172, 170.5, 171.4; 1024 after up to 300 keys 155 (0), 143 (6), 147.
+constexpr int32_t kFewPairCost = 5;
+// Warps of an SM that take few-row sequences, bytes of a warp's eight padded query rows,
+// and of all.
+constexpr int kFewWarps = 12;
 template <int D>
-constexpr int32_t paged_few_warps(bool rows8)
-{
-    return rows8 || D == 64 ? 12 : kDecWarps;
-}
-// Bytes of a warp's eight padded query rows, and of all.
+static constexpr int kFewQuery = 8 * kDecQStride<D>;
 template <int D>
-static constexpr int kRows8Query = 8 * kDecQStride<D>;
-template <int D>
-static constexpr int kRows8Smem = 12 * (kDecStages<D> * kDecStageBytes<D> + kRows8Query<D>);
-static_assert(kRows8Smem<128> <= 225 * 1024 && kRows8Smem<64> <= 225 * 1024, "a CTA's shared memory");
+static constexpr int kFewSmem = kFewWarps * (kDecStages<D> * kDecStageBytes<D> + kFewQuery<D>);
+static_assert(kFewSmem<128> <= 225 * 1024 && kFewSmem<64> <= 225 * 1024, "a CTA's shared memory");
 
 // The plan, at the start of the workspace.
 struct PagedDeal {
     int32_t clusters;                              // with tiles
-    int32_t chunks;                                // of the few-row sequences, per pair
+    int32_t chunks;                                // of the few-row sequences, per pair, charges included
     int32_t few_tokens;                            // of the few-row sequences
     int64_t per;                                   // chunks of a warp
     PagedCut cut[kPagedClusters + 1];              // cluster c: cut[c] .. cut[c + 1]
@@ -93,8 +95,7 @@ struct PagedPlan {
     const int32_t *cu, *lens;
     int32_t n_seqs, group, tile_tokens, head_units, heads;
     int64_t total_q, most_keys;
-    int32_t causal, chunk_shift, page_shift, chunk_bytes, tile_ns, grid, few_warps;
-    float sm_rate;
+    int32_t causal, chunk_shift, page_shift, chunk_bytes, tile_ns, grid;
     PagedDeal *deal;
     PagedEntry *entries;
     int32_t *chunk_start, *few_start;              // [n_seqs + 1]: chunks, tokens of the few-row sequences before b
@@ -103,12 +104,11 @@ struct PagedPlan {
     int32_t *flag;
 };
 
-// Rows of a key head that run as a few-row sequence: at most eight (paged_rows8), or,
-// where a token alone has more, its heads in groups of 16 (decode_suffixes).
-__host__ __device__ constexpr bool paged_rows8(int32_t group) { return group <= 8; }
+// Sequences that run as few-row ones: of at most 16 rows (token, head) per key head, or,
+// where a token alone has more, of that token, its heads in groups of 16.
 __device__ __forceinline__ bool paged_few(int32_t Lq, int32_t group)
 {
-    return Lq == 1 || (int64_t)Lq * group <= 8;
+    return Lq == 1 || (int64_t)Lq * group <= 16;
 }
 
 // A sequence's new tokens and keys; false when an offset or the length is out of range.
@@ -190,6 +190,11 @@ __device__ __forceinline__ PagedCut paged_cut(const PagedPlan &p, int64_t pos, i
     return c;
 }
 
+// Bytes a ns of an SM's few-row warps beside tiles (an SM alone copies faster than when all
+// share the memory).  Taken as 53, as 65, as 70: 48 single tokens beside 2107 of chunks 262, 255,
+// 266 us; 100 beside a prompt of 2048 192, 168, 166; 16 beside two chunks of 512 129, 133, 137.
+constexpr float kFewRate = 65.0f;
+
 // Estimated time, in ns, with c clusters on the tiles and the few-row chunks on the
 // SMs left over (as plan_ns: an estimate that is off costs balance, never a result).
 __device__ __forceinline__ float paged_ns(const PagedPlan &p, int32_t c, float weight, float chunks)
@@ -199,8 +204,8 @@ __device__ __forceinline__ float paged_ns(const PagedPlan &p, int32_t c, float w
     if (bytes == 0.0f)
         return tiles;
     if (2 * c >= p.grid)
-        return tiles + 10000.0f + bytes / fminf(6600.0f, p.sm_rate * (float)p.grid);
-    const float few = bytes / fminf(6600.0f, p.sm_rate * (float)(p.grid - 2 * c));
+        return tiles + 10000.0f + bytes / fminf(6600.0f, kFewRate * (float)p.grid);
+    const float few = bytes / fminf(6600.0f, kFewRate * (float)(p.grid - 2 * c));
     return fmaxf(tiles, few) + 0.05f * fminf(tiles, few);
 }
 
@@ -236,6 +241,7 @@ static __device__ void paged_plan(const PagedPlan &p)
             paged_sequence(p.cu, p.lens, b, p.total_q, p.most_keys, Lq, Lk);
             if (Lq > 0 && paged_few(Lq, p.group)) {
                 x.a = (int32_t)(((int64_t)Lk + (1 << p.chunk_shift) - 1) >> p.chunk_shift);
+                x.a += x.a > 0 ? kFewPairCost : 0;
                 x.b = Lq;
             } else {
                 x.c = ((int64_t)Lq + p.tile_tokens - 1) / p.tile_tokens;
@@ -318,7 +324,7 @@ static __device__ void paged_plan(const PagedPlan &p)
         p.deal->clusters = clusters;
         p.deal->chunks = carry.a;
         p.deal->few_tokens = carry.b;
-        p.deal->per = decode_per_warp((int64_t)carry.a * p.heads, (p.grid - used) * p.few_warps);
+        p.deal->per = decode_per_warp((int64_t)carry.a * p.heads, (p.grid - used) * kFewWarps);
     }
 }
 
@@ -372,7 +378,7 @@ struct PagedFew {
     float *out;                                // [rows of all parts][D]
     float2 *stats;
 
-    static constexpr bool kRowLimits = true;   // causal: a token sees the keys up to its own
+    static constexpr int32_t kPairCost = kFewPairCost;
     __device__ __forceinline__ int32_t sequences() const { return n_seqs; }
     __device__ __forceinline__ int32_t heads() const { return Hk * row_groups; }
     __device__ __forceinline__ int64_t most_keys() const { return max_blocks << page_shift; }
@@ -424,16 +430,17 @@ struct PagedFew {
         const int32_t seen = n - tokens(b) + r / rows + 1;
         return seen < n ? seen : n;
     }
-    // A run's part of a pair has as many rows as the pair, at row 8 w (16 w for 16-row pairs) +
-    // the rows of the pairs before it: the run w, the pair or both grow from one part to the
-    // next, a pair has at most that many rows, so parts do not meet.
-    __device__ __forceinline__ int32_t part_step() const { return paged_rows8(Hq / Hk) ? 8 : 16; }
+    // Whether a sequence's pairs fill a product's eight columns twice.
+    __device__ __forceinline__ bool wide(int32_t b) const { return tokens(b) * (Hq / Hk) > 8; }
+    // A run's part of a pair has as many rows as the pair, at row 16 w + the rows of the
+    // pairs before it: the run w, the pair or both grow from one part to the next, a pair
+    // has at most 16 rows, so parts do not meet.
     __device__ __forceinline__ int64_t part_row(int32_t w, int32_t b, int32_t hr) const
     {
         const int32_t kv = hr / row_groups, group = Hq / Hk;
         const int64_t in = row_groups > 1 ? (int64_t)kv * group + (hr - kv * row_groups) * rows
                                           : (int64_t)kv * group * tokens(b);
-        return (int64_t)part_step() * w + (int64_t)__ldg(few_start + b) * Hq + in;
+        return 16 * (int64_t)w + (int64_t)__ldg(few_start + b) * Hq + in;
     }
     __device__ __forceinline__ int32_t part_rows(int32_t b, int32_t hr) const
     {
@@ -443,17 +450,19 @@ struct PagedFew {
     __device__ __forceinline__ void publish(const int32_t *, int64_t) const {}     // (the plan has done so)
 };
 
-// Pairs of at most eight rows.  The products are turned round, keys and features being the
-// 16 rows of an mma and the pair's rows its eight columns,
+// The products are turned round, keys and features being the 16 rows of an mma and the
+// pair's rows its eight columns,
 //   S^T = K q^T (16 keys x 8 rows),  O^T += V^T P^T (16 features x 8 rows),
 // so that a product, an exponential or an accumulator is spent on eight rows, not on 16:
 // with a row of S per thread as in decode_suffixes, one token of a group of four used a
-// quarter of each (40 sequences of 5 tokens, 16 heads of 64: 70 us so).  P leaves S^T's
+// quarter of each (48 single tokens beside 2107 of chunks 308 us, 260 so).  P leaves S^T's
 // accumulators in 16 bits and gets to its operand's place by movmatrix.
 //
-// Half the products leaves room for twice as many: rot(q) and P go into them as two 16-bit
-// parts each, the rounded value and what it leaves, so nothing is rounded to 16 bits on the
-// way, and the loop still waits for its copies.
+// Every product comes twice.  A pair of at most eight rows has its rot(q) and P in two 16-bit
+// parts, the rounded value and what it leaves, so nothing is rounded to 16 bits on the way; a
+// wide one has its second eight rows in the parts' place, rounded.  Either way the loop still
+// waits for its copies (drafts in wide pairs, 64 of four tokens in groups of four: 109 us, 133
+// as tiles; 64 of twelve, heads of 64: 107 and 213).
 __device__ __forceinline__ uint32_t transpose8(uint32_t a)
 {
     uint32_t d;
@@ -471,58 +480,62 @@ __device__ __forceinline__ uint32_t split2(float a, float b, uint32_t &low)
     return high;
 }
 
-// Eight rows of queries of pair (b, hr), rotated in fp32 (zeros past the pair's rows), as
-// two 16-bit parts: one after the other into the warp's tile, and from there as the B operand
-// of every 16-feature step.
+// Rows first .. first + 7 of the queries of pair (b, hr) (zeros past its rows): a lane's
+// words of them, rotated in fp32 and split into two 16-bit parts.
 template <typename T, int LAYOUT, int D>
-__device__ __forceinline__ void load_query_rows8(const PagedFew &g, const ChunkAt &at, int64_t most, uint8_t *tile,
-                                                 uint32_t (&qh)[D / 16][2], uint32_t (&ql)[D / 16][2])
-{
-    constexpr int L = D / 16, kAtOnce = 32 / L, kSteps = 8 / kAtOnce;
-    const int lane = threadIdx.x & 31, j = lane % L;
-    const RowPart part = row_part<LAYOUT>(j, g.a.rotary_dim);
-    uint4 x0[kSteps], x1[kSteps];
+struct FewQueries {
+    static constexpr int L = D / 16, kAtOnce = 32 / L, kSteps = 8 / kAtOnce;
+    uint4 x0[kSteps], x1[kSteps], y0[kSteps], y1[kSteps];      // the rounded values, and what they leave
     int64_t trow[kSteps];
+    __device__ __forceinline__ void request(const PagedFew &g, const ChunkAt &at, int64_t most, const RowPart &part, int first)
+    {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
-        trow[i] = -1;
-        int32_t token;
-        const T *row = g.template query<T, D>(at.b, at.hr, i * kAtOnce + lane / L, token);
-        if (row != nullptr) {
-            x0[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o0));
-            x1[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o1));
-            if (part.rot)
-                trow[i] = g.query_turn(at.b, token, most);
-        }
-    }
-    uint4 y0[kSteps], y1[kSteps];              // what the rounded values leave
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        y0[i] = y1[i] = make_uint4(0, 0, 0, 0);
-        if (trow[i] >= 0) {
-            float c[8], s[8], f0[8], f1[8];
-            table_values(g.a.cos, g.a.sin, trow[i] * (g.a.rotary_dim / 2) + 8 * j, c, s);
-            Elt<T>::unpack(x0[i], f0);
-            Elt<T>::unpack(x1[i], f1);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if constexpr (LAYOUT == 0)
-                    rotate_pair(f0[e], f1[e], c[e], s[e]);
-                else if (e < 4)
-                    rotate_pair(f0[2 * e], f0[2 * e + 1], c[e], s[e]);
-                else
-                    rotate_pair(f1[2 * e - 8], f1[2 * e - 7], c[e], s[e]);
-            }
-            uint32_t *h0 = &x0[i].x, *h1 = &x1[i].x, *l0 = &y0[i].x, *l1 = &y1[i].x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                h0[e] = split2<T>(f0[2 * e], f0[2 * e + 1], l0[e]);
-                h1[e] = split2<T>(f1[2 * e], f1[2 * e + 1], l1[e]);
+        for (int i = 0; i < kSteps; ++i) {
+            x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
+            trow[i] = -1;
+            int32_t token;
+            const T *row = g.template query<T, D>(at.b, at.hr, first + i * kAtOnce + (threadIdx.x & 31) / L, token);
+            if (row != nullptr) {
+                x0[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o0));
+                x1[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o1));
+                if (part.rot)
+                    trow[i] = g.query_turn(at.b, token, most);
             }
         }
     }
-    auto through = [&](const uint4 (&a)[kSteps], const uint4 (&b)[kSteps], uint32_t (&f)[D / 16][2]) {
+    __device__ __forceinline__ void turn(const PagedFew &g)
+    {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            y0[i] = y1[i] = make_uint4(0, 0, 0, 0);
+            if (trow[i] >= 0) {
+                float c[8], s[8], f0[8], f1[8];
+                table_values(g.a.cos, g.a.sin, trow[i] * (g.a.rotary_dim / 2) + 8 * ((threadIdx.x & 31) % L), c, s);
+                Elt<T>::unpack(x0[i], f0);
+                Elt<T>::unpack(x1[i], f1);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if constexpr (LAYOUT == 0)
+                        rotate_pair(f0[e], f1[e], c[e], s[e]);
+                    else if (e < 4)
+                        rotate_pair(f0[2 * e], f0[2 * e + 1], c[e], s[e]);
+                    else
+                        rotate_pair(f1[2 * e - 8], f1[2 * e - 7], c[e], s[e]);
+                }
+                uint32_t *h0 = &x0[i].x, *h1 = &x1[i].x, *l0 = &y0[i].x, *l1 = &y1[i].x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h0[e] = split2<T>(f0[2 * e], f0[2 * e + 1], l0[e]);
+                    h1[e] = split2<T>(f1[2 * e], f1[2 * e + 1], l1[e]);
+                }
+            }
+        }
+    }
+    // Through the warp's tile into the B operand of every 16-feature step.
+    static __device__ __forceinline__ void operand(const uint4 (&a)[kSteps], const uint4 (&b)[kSteps], const RowPart &part,
+                                                   uint8_t *tile, uint32_t (&f)[D / 16][2])
+    {
+        const int lane = threadIdx.x & 31;
         __syncwarp();                          // the tile's last readers are done
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
@@ -539,186 +552,277 @@ __device__ __forceinline__ void load_query_rows8(const PagedFew &g, const ChunkA
             ldsm4(addr + k * 32, r);
             f[k][0] = r[0]; f[k][1] = r[1]; f[k + 1][0] = r[2]; f[k + 1][1] = r[3];
         }
-    };
-    through(x0, x1, qh);
-    through(y0, y1, ql);
+    }
+};
+
+// A pair's queries as the two operands of few_pair.
+template <typename T, int LAYOUT, int D, bool WIDE>
+__device__ __forceinline__ void load_few_queries(const PagedFew &g, const ChunkAt &at, int64_t most, uint8_t *tile,
+                                                 uint32_t (&qa)[D / 16][2], uint32_t (&qb)[D / 16][2])
+{
+    using Q = FewQueries<T, LAYOUT, D>;
+    const RowPart part = row_part<LAYOUT>((threadIdx.x & 31) % Q::L, g.a.rotary_dim);
+    Q q, second;
+    q.request(g, at, most, part, 0);
+    if constexpr (WIDE)
+        second.request(g, at, most, part, 8);
+    q.turn(g);
+    Q::operand(q.x0, q.x1, part, tile, qa);
+    if constexpr (WIDE) {
+        second.turn(g);
+        Q::operand(second.x0, second.x1, part, tile, qb);
+    } else {
+        Q::operand(q.y0, q.y1, part, tile, qb);
+    }
 }
 
-// One warp's run of chunks; smem: kRows8Smem bytes of the CTA.
-template <typename T, int LAYOUT, int D>
-__device__ __forceinline__ void paged_rows8_run(const PagedFew &g, uint8_t *smem, const SuffixRun &run, SuffixShared<D, 12> &sh)
+// The softmax of a thread's two columns (rows r0 and r0 + 1 of eight).
+struct FewColumns {
+    float m[2], l[2];
+    __device__ __forceinline__ void clear()
+    {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.0f;
+    }
+    // The reference maxima move only when a key exceeds them by more than 8 (a factor of
+    // 256), so the lanes of a row seldom have to agree on its maximum.  True (for all lanes):
+    // what is accumulated has to be scaled by f.
+    template <int kGroups>
+    __device__ __forceinline__ bool maxima(const float (&s)[kGroups][4], float scale_log2, float (&f)[2])
+    {
+        float x[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            x[c] = fmaxf(s[0][c], s[0][2 + c]);
+#pragma unroll
+            for (int n = 1; n < kGroups; ++n)
+                x[c] = fmaxf(x[c], fmaxf(s[n][c], s[n][2 + c]));
+            x[c] *= scale_log2;                // (the scale is positive)
+        }
+        if (!__any_sync(0xffffffffu, x[0] > m[0] + 8.0f || x[1] > m[1] + 8.0f))
+            return false;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1)
+                x[c] = fmaxf(x[c], __shfl_xor_sync(0xffffffffu, x[c], d));
+            const bool up = x[c] > m[c] + 8.0f;
+            f[c] = up ? (m[c] == -INFINITY ? 0.0f : fast_exp2(m[c] - x[c])) : 1.0f;
+            m[c] = up ? x[c] : m[c];
+            l[c] *= f[c];
+        }
+        return true;
+    }
+    __device__ __forceinline__ void weights(const float (&s)[4], float scale_log2, float (&p)[4])
+    {
+        const float n0 = m[0] == -INFINITY ? 0.0f : -m[0], n1 = m[1] == -INFINITY ? 0.0f : -m[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[i] = fast_exp2(fmaf(s[i], scale_log2, i & 1 ? n1 : n0));
+        l[0] += p[0] + p[2];
+        l[1] += p[1] + p[3];
+    }
+    __device__ __forceinline__ void sums()
+    {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
+            l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
+        }
+    }
+};
+
+// A warp's way through its stages.
+struct FewStages {
+    uint64_t *bar;
+    uint8_t *stages;
+    int st;
+    uint32_t ph;
+    int64_t issued, done;
+};
+
+// `count` chunks of pair (at.b, at.hr), from chunk at.ch on, and their part of the pair; false
+// after an expired wait.  The two operands, their outputs and softmax: rows 0-7 rounded, and
+// what that leaves of them, or (WIDE) rows 8-15.
+template <typename T, int LAYOUT, int D, bool WIDE>
+__device__ __forceinline__ bool few_pair(const PagedFew &g, SuffixCopies<D, PagedFew> &copies, FewStages &f, uint8_t *qtile,
+                                         ChunkAt &at, int32_t count, int32_t w, int64_t most, volatile int *abort)
 {
     constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>, kKeys = kDecKeys<D>;
-    constexpr int kBox = kKeys * 128, kGroups = kKeys / 16;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t most = g.most_keys();
-    int64_t left = run.left;
-    ChunkAt at = run.at;
-    if (left <= 0)
-        return;
-    uint64_t *bar = sh.bar[warp];
-    uint8_t *stages = smem + warp * kStages * kStage;
-    uint8_t *qtile = smem + 12 * kStages * kStage + warp * kRows8Query<D>;
-    volatile int *abort = &sh.abort_flag;
-    SuffixCopies<D, PagedFew> copies(g, run, most, stages, bar);
-    bool ok = true;
-    int64_t issued = 0, done = 0;
-    for (int st = 0; st < kStages && copies.left > 0; ++st, ++issued)
-        copies.load(st);
-
-    uint32_t qh[D / 16][2], ql[D / 16][2];
-    float o[D / 16][4];                                        // features lane / 4 and + 8 of 16, rows r0 and r0 + 1
+    constexpr int kBox = kKeys * 128, kGroups = kKeys / 16, kSets = WIDE ? 2 : 1;
+    const int lane = threadIdx.x & 31;
     const int r0 = 2 * (lane & 3), k0 = lane >> 2;             // S^T: keys k0 and k0 + 8 of 16
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-    int32_t keys = 0, lim0 = 0, lim1 = 0, low = 0;             // of the pair; that the two rows see; that all rows see
-    bool fresh = true;
-    int st = 0;
-    uint32_t ph = 0;
     // ldmatrix rows: K (two 8-key halves x two 8-feature halves of a step), V (the same,
     // turned: two 8-feature halves x two 8-key halves)
     const int k_row = lane & 15, k_half = lane >> 4;
     const int v_row = (lane & 7) + ((lane >> 4) << 3), v_half = lane >> 3 & 1;
-    const uint32_t base = attn_smem_u32(stages);
-    for (; ok && left > 0; --left, ++done) {
-        if (fresh) {
-            keys = g.keys(at.b, most);
-            lim0 = g.limit(at.b, r0, keys);
-            lim1 = g.limit(at.b, r0 + 1, keys);
-            low = g.limit(at.b, 0, keys);
-            load_query_rows8<T, LAYOUT, D>(g, at, most, qtile, qh, ql);
+    const uint32_t base = attn_smem_u32(f.stages);
+    const int32_t keys = g.keys(at.b, most), low = g.limit(at.b, 0, keys);     // of the pair; that all rows see
+    int32_t lim[kSets][2];                                     // that the thread's rows see
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-            m0 = m1 = -INFINITY;
-            l0 = l1 = 0.0f;
-            fresh = false;
-        }
-        ok = __all_sync(0xffffffffu, attn_wait(&bar[st], ph, abort));
-        if (!ok)
-            break;
-        const uint32_t kb = base + st * kStage, vb = kb + kStage / 2;
-        float s[kGroups][4];                                   // (key k0, rows r0, r0 + 1), (key k0 + 8, the same)
+    for (int x = 0; x < kSets; ++x) {
+        lim[x][0] = g.limit(at.b, 8 * x + r0, keys);
+        lim[x][1] = g.limit(at.b, 8 * x + r0 + 1, keys);
+    }
+    uint32_t qa[D / 16][2], qb[D / 16][2];
+    load_few_queries<T, LAYOUT, D, WIDE>(g, at, most, qtile, qa, qb);
+    float o[kSets][D / 16][4];                                 // features lane / 4 and + 8 of 16, rows r0 and r0 + 1
+    FewColumns soft[kSets];
+#pragma unroll
+    for (int x = 0; x < kSets; ++x) {
+        soft[x].clear();
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            o[x][i][0] = o[x][i][1] = o[x][i][2] = o[x][i][3] = 0.0f;
+    }
+    for (; count > 0; --count, ++at.ch, ++f.done) {
+        if (!__all_sync(0xffffffffu, attn_wait(&f.bar[f.st], f.ph, abort)))
+            return false;
+        const uint32_t kb = base + f.st * kStage, vb = kb + kStage / 2;
+        float s[2][kGroups][4];                                // (key k0, rows r0, r0 + 1), (key k0 + 8, the same)
 #pragma unroll
         for (int n = 0; n < kGroups; ++n) {
-            float h[4] = {0, 0, 0, 0}, e[4] = {0, 0, 0, 0};    // of the rounded queries and of the rest
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s[0][n][i] = s[1][n][i] = 0.0f;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 uint32_t a[4];
                 const int chunk = (k & 3) * 2 + k_half;
                 ldsm4(kb + (k >> 2) * kBox + (n * 16 + k_row) * 128 + ((chunk ^ (k_row & 7)) << 4), a);
-                mma16816<T>(h, a, qh[k][0], qh[k][1]);
-                mma16816<T>(e, a, ql[k][0], ql[k][1]);
+                mma16816<T>(s[0][n], a, qa[k][0], qa[k][1]);
+                mma16816<T>(s[1][n], a, qb[k][0], qb[k][1]);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s[n][i] = h[i] + e[i];
-        }
-        if (low - at.ch * kKeys < kKeys) {                     // keys that some row does not see
-            const int32_t n0 = lim0 - at.ch * kKeys, n1 = lim1 - at.ch * kKeys;
-#pragma unroll
-            for (int n = 0; n < kGroups; ++n) {
+            if constexpr (!WIDE) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (n * 16 + k0 + (i >> 1) * 8 >= (i & 1 ? n1 : n0))
-                        s[n][i] = -INFINITY;
+                    s[0][n][i] += s[1][n][i];
+            }
+        }
+        if (low - at.ch * kKeys < kKeys) {                     // keys that some row does not see
+#pragma unroll
+            for (int x = 0; x < kSets; ++x) {
+                const int32_t n0 = lim[x][0] - at.ch * kKeys, n1 = lim[x][1] - at.ch * kKeys;
+#pragma unroll
+                for (int n = 0; n < kGroups; ++n) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n * 16 + k0 + (i >> 1) * 8 >= (i & 1 ? n1 : n0))
+                            s[x][n][i] = -INFINITY;
+                }
             }
             // what lies behind the last key (anything) must not meet a zero
             const int32_t nk = keys - at.ch * kKeys;
             if (nk < kKeys) {
                 constexpr int kWords = D / 8;                  // 16-byte words of a value
                 for (int i = nk * kWords + lane; i < kKeys * kWords; i += 32)
-                    *reinterpret_cast<uint4 *>(stages + st * kStage + kStage / 2 + (i % kWords / 8) * kBox +
+                    *reinterpret_cast<uint4 *>(f.stages + f.st * kStage + kStage / 2 + (i % kWords / 8) * kBox +
                                                i / kWords * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next copy
                 __syncwarp();
             }
         }
-        float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
 #pragma unroll
-        for (int n = 1; n < kGroups; ++n) {
-            x0 = fmaxf(x0, fmaxf(s[n][0], s[n][2]));
-            x1 = fmaxf(x1, fmaxf(s[n][1], s[n][3]));
-        }
-        x0 *= g.a.scale_log2;                                  // (the scale is positive)
-        x1 *= g.a.scale_log2;
-        // the reference maxima move only when a key exceeds them by more than 8 (a factor of
-        // 256), so the lanes of a row seldom have to agree on its maximum
-        if (__any_sync(0xffffffffu, x0 > m0 + 8.0f || x1 > m1 + 8.0f)) {
+        for (int x = 0; x < kSets; ++x) {
+            float by[2];
+            if (soft[x].maxima(s[x], g.a.scale_log2, by)) {
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
-                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
-            }
-            const bool up0 = x0 > m0 + 8.0f, up1 = x1 > m1 + 8.0f;
-            const float f0 = up0 ? (m0 == -INFINITY ? 0.0f : fast_exp2(m0 - x0)) : 1.0f;
-            const float f1 = up1 ? (m1 == -INFINITY ? 0.0f : fast_exp2(m1 - x1)) : 1.0f;
-            m0 = up0 ? x0 : m0;
-            m1 = up1 ? x1 : m1;
-            l0 *= f0;
-            l1 *= f1;
+                for (int i = 0; i < D / 16; ++i) {
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                o[i][0] *= f0;
-                o[i][1] *= f1;
-                o[i][2] *= f0;
-                o[i][3] *= f1;
+                    for (int e = 0; e < 4; ++e)
+                        o[x][i][e] *= by[e & 1];
+                }
             }
         }
-        const float n0 = m0 == -INFINITY ? 0.0f : -m0, n1 = m1 == -INFINITY ? 0.0f : -m1;
 #pragma unroll
         for (int n = 0; n < kGroups; ++n) {
             float p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                p[i] = fast_exp2(fmaf(s[n][i], g.a.scale_log2, i & 1 ? n1 : n0));
-            l0 += p[0] + p[2];
-            l1 += p[1] + p[3];
-            uint32_t e0, e1;
-            const uint32_t h0 = transpose8(split2<T>(p[0], p[1], e0)), h1 = transpose8(split2<T>(p[2], p[3], e1));
-            e0 = transpose8(e0);
-            e1 = transpose8(e1);
+            uint32_t a0, a1, b0, b1;
+            soft[0].weights(s[0][n], g.a.scale_log2, p);
+            if constexpr (WIDE) {
+                a0 = Elt<T>::f2_to_word(p[0], p[1]);
+                a1 = Elt<T>::f2_to_word(p[2], p[3]);
+                soft[kSets - 1].weights(s[1][n], g.a.scale_log2, p);
+                b0 = Elt<T>::f2_to_word(p[0], p[1]);
+                b1 = Elt<T>::f2_to_word(p[2], p[3]);
+            } else {
+                a0 = split2<T>(p[0], p[1], b0);
+                a1 = split2<T>(p[2], p[3], b1);
+            }
+            a0 = transpose8(a0);
+            a1 = transpose8(a1);
+            b0 = transpose8(b0);
+            b1 = transpose8(b1);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 uint32_t a[4];
                 const int chunk = (i & 3) * 2 + v_half;
                 ldsm4_t(vb + (i >> 2) * kBox + (n * 16 + v_row) * 128 + ((chunk ^ (v_row & 7)) << 4), a);
-                mma16816<T>(o[i], a, h0, h1);
-                mma16816<T>(o[i], a, e0, e1);
+                mma16816<T>(o[0][i], a, a0, a1);
+                mma16816<T>(o[kSets - 1][i], a, b0, b1);
             }
         }
         __syncwarp();                                          // the stage is read
         if (copies.left > 0) {
-            copies.load(st);
-            ++issued;
+            copies.load(f.st);
+            ++f.issued;
         }
-        if (++st == kStages) {
-            st = 0;
-            ph ^= 1u;
+        if (++f.st == kStages) {
+            f.st = 0;
+            f.ph ^= 1u;
         }
-        const ChunkAt was = at;
-        at.next(g, most);
-        if (left == 1 || at.b != was.b || at.hr != was.hr) {
+    }
+    const int64_t row0 = g.part_row(w, at.b, at.hr);
+    const int32_t rows = g.part_rows(at.b, at.hr);
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-                l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-            }
-            const int64_t row0 = g.part_row(run.w, was.b, was.hr) + r0;
-            const int32_t rows = g.part_rows(was.b, was.hr) - r0;
+    for (int x = 0; x < kSets; ++x) {
+        soft[x].sums();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (half < rows) {
-                    float *dst = g.out + (row0 + half) * D + k0;
+        for (int half = 0; half < 2; ++half) {
+            const int r = 8 * x + r0 + half;
+            if (r < rows) {
+                float *dst = g.out + (row0 + r) * D + k0;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        dst[16 * i] = o[i][half];
-                        dst[16 * i + 8] = o[i][2 + half];
-                    }
-                    if (k0 == 0)
-                        g.stats[row0 + half] = half ? make_float2(m1, l1) : make_float2(m0, l0);
+                for (int i = 0; i < D / 16; ++i) {
+                    dst[16 * i] = o[x][i][half];
+                    dst[16 * i + 8] = o[x][i][2 + half];
                 }
+                if (k0 == 0)
+                    g.stats[row0 + r] = make_float2(soft[x].m[half], soft[x].l[half]);
             }
-            fresh = true;
+        }
+    }
+    return true;
+}
+
+// One warp's run of chunks; smem: kFewSmem bytes of the CTA.
+template <typename T, int LAYOUT, int D>
+__device__ __forceinline__ void paged_few_run(const PagedFew &g, uint8_t *smem, const SuffixRun &run,
+                                              SuffixShared<D, kFewWarps> &sh)
+{
+    constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t most = g.most_keys();
+    int64_t left = run.left;
+    ChunkAt at = run.at;
+    if (left <= 0)
+        return;
+    FewStages f = {sh.bar[warp], smem + warp * kStages * kStage, 0, 0, 0, 0};
+    uint8_t *qtile = smem + kFewWarps * kStages * kStage + warp * kFewQuery<D>;
+    volatile int *abort = &sh.abort_flag;
+    SuffixCopies<D, PagedFew> copies(g, run, most, f.stages, f.bar);
+    bool ok = true;
+    for (int st = 0; st < kStages && copies.left > 0; ++st, ++f.issued)
+        copies.load(st);
+    while (ok && left > 0) {
+        const int32_t here = at.n - at.ch, count = here < left ? here : (int32_t)left;
+        left -= count;
+        ok = g.wide(at.b) ? few_pair<T, LAYOUT, D, true>(g, copies, f, qtile, at, count, run.w, most, abort)
+                          : few_pair<T, LAYOUT, D, false>(g, copies, f, qtile, at, count, run.w, most, abort);
+        if (ok && left > 0) {
+            --at.ch;
+            at.next(g, most);
+            left -= kFewPairCost;
         }
     }
     if (!ok) {
@@ -726,8 +830,8 @@ __device__ __forceinline__ void paged_rows8_run(const PagedFew &g, uint8_t *smem
         if (lane == 0)
             atomicOr(g.a.flag, kFlagTimeout);
         // one more bounded wait for the copies in flight
-        for (int64_t i = done; i < issued; ++i)
-            (void)attn_wait(&bar[i % kStages], (uint32_t)(i / kStages) & 1u);
+        for (int64_t i = f.done; i < f.issued; ++i)
+            (void)attn_wait(&f.bar[i % kStages], (uint32_t)(i / kStages) & 1u);
     }
 }
 
@@ -742,9 +846,7 @@ struct PagedSource {
     static constexpr int smem_bytes()
     {
         const int tiles = (int)kPackedSmem<D> + 4 * (kMaxDecodeBatch + 2);
-        constexpr int few = kDecSmem<D, paged_few_warps<D>(false)>;
-        constexpr int most = few > kRows8Smem<D> ? few : kRows8Smem<D>;
-        return tiles > most ? tiles : most;
+        return tiles > kFewSmem<D> ? tiles : kFewSmem<D>;
     }
     AttnArgs a;                                // o, Hq, cos, sin, table_rows, rotary_dim, scale, causal, flag
     CUtensorMap k_map, v_map, q_map, o_map;    // the pools; queries and outputs of all sequences
@@ -908,7 +1010,7 @@ struct PagedSource {
     template <typename T, int LAYOUT, int D>
     __device__ __forceinline__ void finish(const Walk &w, uint8_t *smem, bool failed) const
     {
-        __shared__ SuffixShared<D, 12> sh;
+        __shared__ SuffixShared<D, kFewWarps> sh;
         const int32_t used = 2 * w.clusters < (int32_t)gridDim.x ? 2 * w.clusters : 0;
         const int32_t cta = (int32_t)blockIdx.x - used;
         // (after an expired wait copies may still be on their way: no work)
@@ -919,34 +1021,13 @@ struct PagedSource {
             start[b] = __ldg(few.chunk_start + b);
         __syncthreads();
         const int32_t ctas = (int32_t)gridDim.x - used;
-        const int warp = threadIdx.x >> 5;
-        // registers: from the roles' 240 / 112 / 104 to 168 for all, or 216 for eight warps
-        if (paged_rows8(few.Hq / few.Hk)) {
-            const SuffixRun run = suffix_run<D>(few, start, w.chunks, cta, ctas, sh);
-            if (warp < 4)
-                asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
-            else
-                asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-            paged_rows8_run<T, LAYOUT, D>(few, smem, run, sh);
-            return;
-        }
-        SuffixShared<D, paged_few_warps<D>(false)> &sh16 = reinterpret_cast<SuffixShared<D, paged_few_warps<D>(false)> &>(sh);
-        const SuffixRun run = suffix_run<D>(few, start, w.chunks, cta, ctas, sh16);
-        if constexpr (paged_few_warps<D>(false) == 12) {
-            if (warp < 4)
-                asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
-            else
-                asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-            decode_suffixes<T, LAYOUT, D>(few, smem, run, sh16);
-        } else if (warp < 8) {
-            if (warp < 4)
-                asm volatile("setmaxnreg.dec.sync.aligned.u32 216;");
-            else
-                asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-            decode_suffixes<T, LAYOUT, D>(few, smem, run, sh16);
-        } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        }
+        const SuffixRun run = suffix_run<D>(few, start, w.chunks, cta, ctas, sh);
+        // registers: from the roles' 240 / 112 / 104 to 168 for all
+        if (threadIdx.x < 128)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        paged_few_run<T, LAYOUT, D>(few, smem, run, sh);
     }
 };
 
@@ -965,10 +1046,10 @@ struct PagedMerge {
     int32_t lg;
 };
 
-// A row of the few-row sequences: its parts, `step` rows from one to the next, and its output.
+// A row of the few-row sequences: its parts, 16 rows from one to the next, and its output.
 struct FewRow {
     int64_t from, to;
-    int32_t n, step;
+    int32_t n;
     __device__ __forceinline__ void find(const PagedMerge &g, int64_t row)
     {
         const PagedFew &f = g.few;
@@ -978,10 +1059,9 @@ struct FewRow {
         const int32_t kv = h / group, in_group = h - kv * group, rg = in_group / f.rows;
         const int32_t hr = kv * f.row_groups + rg, r = tok * f.rows + in_group - rg * f.rows;
         const int64_t c0 = __ldcg(f.chunk_start + b), c1 = __ldcg(f.chunk_start + b + 1), per = __ldcg(&g.deal->per);
-        const int64_t at = c0 * heads + hr * (c1 - c0), first = divide(at, per);
+        const int64_t at = c0 * heads + hr * (c1 - c0), first = divide(at + kFewPairCost, per);
         n = c1 > c0 ? (int32_t)(divide(at + (c1 - c0) - 1, per) - first + 1) : 0;
         from = f.part_row((int32_t)first, b, hr) + r;
-        step = f.part_step();
         to = ((int64_t)__ldcg(f.cu + b) + tok) * f.Hq + h;
     }
 };
@@ -1037,7 +1117,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_paged_merge_kernel
         if constexpr (W > 1)
             __syncthreads();                                   // the last row's parts are read
         merge_parts<T, D, W>(few.n, static_cast<T *>(g.o) + few.to * D, [&](int32_t p, float2 &stat) {
-            const int64_t at = few.from + (int64_t)p * few.step;
+            const int64_t at = few.from + (int64_t)p * 16;
             stat = __ldg(f.stats + at);
             return (const float *)f.out + at * D;
         });
@@ -1111,11 +1191,6 @@ static cudaError_t launch_paged(const PagedCall &c, const PagedLayout &lay, cuda
     p.total_q = c.total_q; p.most_keys = c.max_blocks << c.page_shift;
     p.causal = c.causal; p.chunk_shift = f.chunk_shift; p.page_shift = c.page_shift;
     p.chunk_bytes = kDecStageBytes<D>; p.tile_ns = D == 128 ? 900 : 700; p.grid = 2 * clusters;
-    p.few_warps = paged_few_warps<D>(paged_rows8(group));
-    // (65 of paged_rows8: an SM alone copies faster than when all of them share the memory.
-    // Taken as 53, as 65, as 70: 48 single tokens beside 2107 of chunks 262, 255, 266 us; 100
-    // beside a prompt of 2048 192, 168, 166; 16 beside two chunks of 512 129, 133, 137.)
-    p.sm_rate = paged_rows8(group) ? 65.0f : D == 128 ? 53.0f : 48.0f;
     p.deal = reinterpret_cast<PagedDeal *>(ws);
     p.entries = reinterpret_cast<PagedEntry *>(ws + lay.entries);
     p.chunk_start = reinterpret_cast<int32_t *>(ws + lay.chunk_start);

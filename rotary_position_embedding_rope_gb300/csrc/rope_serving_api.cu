@@ -102,17 +102,17 @@ bool decode_layout(int64_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t page_sh
 bool paged_layout(int64_t n_seqs, int64_t total_q, int32_t Hq, int32_t Hk, int32_t D, int32_t page_shift,
                   int64_t max_blocks, PagedLayout *out)
 {
-    const int64_t group = Hq / Hk, few = group < 8 ? 8 / group : 1;
+    const int64_t group = Hq / Hk, few = group < 16 ? 16 / group : 1;
     const int64_t chunks = product({n_seqs, max_blocks, (int64_t)1 << page_shift >> 4});
     const int64_t keys = product({max_blocks, (int64_t)1 << page_shift});
-    if (chunks < 0 || chunks > kMaxInt32 || keys < 0 || keys > kMaxInt32 - 256)
+    if (chunks < 0 || chunks > kMaxInt32 - 16 * kMaxDecodeBatch || keys < 0 || keys > kMaxInt32 - 256)
         return false;
     const int64_t few_tokens = total_q < n_seqs * few ? total_q : n_seqs * few;
     out->few_rows = few_tokens * Hq;
     // tiles: a sequence has at most tokens / tile + 1 of them; none where all the
     // call's rows of a key head are few
     const int64_t tile = 256 / packed_group_heads(Hq, Hk);
-    const bool tiles = total_q > 1 && total_q * group > 8;
+    const bool tiles = total_q > 1 && total_q * group > 16;
     const int64_t entries = tiles ? total_q / tile + (n_seqs < total_q ? n_seqs : total_q) : 0;
     const int64_t parts = tiles ? (int64_t)kDecodeSms * 256 : 0;              // two pieces of 256 rows a cluster
     const int64_t part_rows = 16 * 12 * (int64_t)kDecodeSms + out->few_rows;  // 16 a warp, at most 12 of an SM

@@ -258,6 +258,23 @@ def test_many_sequences():
         run(R, q, kp, vp, torch.cat([table, table[:1]]), torch.cat([cu, cu[-1:]]), torch.cat([lens, lens[:1]]), cos, sin)
 
 
+@pytest.mark.parametrize("Hq,Hk,D,page", [(8, 2, 128, 16), (6, 6, 64, 32), (16, 2, 128, 128), (3, 1, 64, 16)])
+def test_short_sequences_among_long_ones(Hq, Hk, D, page):
+    """Pairs of no, one and two chunks, of one to 16 rows, between long ones: runs that begin and end everywhere."""
+    require_gpu()
+    R = lib()
+    G = Hq // Hk
+    k = [(0, 1, 15, 16, 17, 700, 33, 2, 64, 3, 31, 1500)[i * 5 % 12] + (i % 3 == 0) for i in range(120)]
+    q = [min(n, 1 + i * 7 % max(16 // G, 1)) if n else i % 2 for i, n in enumerate(k)]
+    c = case(q, k, Hq, Hk, D, D, page)
+    t = make(c)
+    cos, sin = S.tables(1e4, D, 1600)
+    want = reference(*t, cos, sin)
+    got = run(R, *t, cos, sin)
+    check(got, want, c, "short sequences")
+    assert torch.equal(got, run(R, *t, cos, sin))
+
+
 @pytest.mark.parametrize("normed", [False, True])
 def test_prompt_in_chunks_then_single_tokens(normed):
     """A run as a program makes it: the tokens of two sequences appended and attended in steps of ragged chunks, then one by
