@@ -62,7 +62,10 @@ constexpr int kPagedPlanThreads = 512;
 // What a unit costs besides its key tiles, in tiles (its query tile's way in and
 // its output's way out: about 4 us of 0.9 a tile).
 constexpr int32_t kPagedUnitTiles = 4;
-// Least weight of a cluster's run: shorter runs leave more pieces than they save.
+// Least weight of a cluster's run where there are more clusters than units: shorter runs
+// leave more pieces than they save.  (Two units one after the other take longer than either
+// alone: 84 rows of eight key heads after 300 keys, beside three single tokens, on seven
+// clusters 23.3 us, on eight 21.1.)
 constexpr int64_t kPagedMinRun = 2 * kPagedUnitTiles;
 constexpr int32_t kPagedClusters = kDecodeSms / 2;   // at most
 // What a pair (sequence, key head) of a few-row sequence counts for besides its chunks, in
@@ -290,8 +293,7 @@ static __device__ void paged_plan(const PagedPlan &p)
         weight += total.c;
     }
     // clusters for the tiles
-    int64_t most = weight / kPagedMinRun;
-    most = most < 1 ? 1 : most;
+    const int64_t units = (int64_t)n_entries * p.head_units, runs = weight / kPagedMinRun, most = runs > units ? runs : units;
     const int32_t top = weight == 0 ? 0 : (int32_t)(most < p.grid / 2 ? most : p.grid / 2);
     if (warp * 32 < kPagedClusters) {
         const int32_t c = tid + 1;
