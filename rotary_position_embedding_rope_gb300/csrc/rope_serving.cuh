@@ -119,6 +119,24 @@ struct PagedCall {
     void *workspace;
     int32_t *flag;
 };
+// What a unit costs besides its key tiles, in tiles (its query tile's way in and
+// its output's way out: about 4 us of 0.9 a tile).
+constexpr int32_t kPagedUnitTiles = 4;
+// Least weight of a cluster's run where there are more clusters than units: shorter runs
+// leave more pieces than they save.  (Two units one after the other take longer than either
+// alone: 84 rows of eight key heads after 300 keys, beside three single tokens, on seven
+// clusters 23.3 us, on eight 21.1.)
+constexpr int64_t kPagedMinRun = 2 * kPagedUnitTiles;
+// What a pair (sequence, key head) of a few-row sequence counts for besides its chunks, in
+// chunks: its queries' way in and its outputs' way out, several loads one after the other.
+// Without it the warps that got the short sequences ended last.  0, 2, 5, 12 of them (us): 40
+// drafts of up to five tokens, heads of 64, contexts to 3k 70, 48.7, 47.7, 47.8; 64 of four
+// tokens, groups of four, contexts to 4k 119, 111, 109, 108; 64 single tokens, contexts to 8k
+// 175.5, 172, 170.5, 171.4; 1024 after up to 300 keys 155 (0), 143 (6), 147.
+constexpr int32_t kFewPairCost = 5;
+// Warps of an SM that take few-row sequences, and the least charge of such a warp's run.
+constexpr int kFewWarps = 12;
+constexpr int64_t kFewMinRun = 2;
 constexpr int64_t kPagedHead = 1024;           // bytes of the plan's head: a cut for every cluster
 struct PagedLayout {
     int64_t few_rows;                // most rows (token, head) of few-row sequences

@@ -2,6 +2,7 @@
 // argument checks.  Everything the host can see is checked here, before
 // anything is enqueued; offsets, lengths and page numbers are checked by the
 // kernels.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -114,8 +115,16 @@ bool paged_layout(int64_t n_seqs, int64_t total_q, int32_t Hq, int32_t Hk, int32
     const int64_t tile = 256 / packed_group_heads(Hq, Hk);
     const bool tiles = total_q > 1 && total_q * group > 16;
     const int64_t entries = tiles ? total_q / tile + (n_seqs < total_q ? n_seqs : total_q) : 0;
-    const int64_t parts = tiles ? (int64_t)kDecodeSms * 256 : 0;              // two pieces of 256 rows a cluster
-    const int64_t part_rows = 16 * 12 * (int64_t)kDecodeSms + out->few_rows;  // 16 a warp, at most 12 of an SM
+    // at most two pieces of 256 rows for each cluster that the plan may use, and 16 rows for
+    // each run of few-row chunks
+    const int64_t units = product({entries, Hq / packed_group_heads(Hq, Hk)});
+    const int64_t weight = product({units, keys / 128 + 1 + kPagedUnitTiles});   // (tiles of 128 keys)
+    const int64_t charge = product({chunks + kFewPairCost * n_seqs, Hk, (group + 15) / 16});
+    if (units < 0 || weight < 0 || charge < 0)
+        return false;
+    const int64_t runs = weight / kPagedMinRun, clusters = std::min<int64_t>(kDecodeSms / 2, std::max(units, runs));
+    const int64_t parts = clusters * 2 * 256;
+    const int64_t part_rows = 16 * std::min<int64_t>(kFewWarps * kDecodeSms, charge / kFewMinRun + 1) + out->few_rows;
     const int64_t few_out = product({part_rows, D, 4});
     if (entries > (1ll << 31) || few_out < 0)
         return false;

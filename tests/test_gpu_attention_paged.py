@@ -244,6 +244,22 @@ def test_nothing_to_attend():
                              cos.cuda(), sin.cuda()).shape == (0, 4, 64)
 
 
+@pytest.mark.parametrize("c", CASES, ids=lambda c: "n%d_Hq%d_Hk%d_D%d_p%d" % (len(c["q"]), c["Hq"], c["Hk"], c["D"], c["page"]))
+def test_nothing_behind_the_workspace(c):
+    """A workspace of exactly the size asked for: what lies behind it stays, what lies in it beforehand does not matter."""
+    require_gpu()
+    R = lib()
+    q, kp, vp, table, cu, lens = make(c)
+    cos, sin = S.tables(1e4, c["rd"], max(c["k"]) + 8)
+    size = R.rope_attention_paged_workspace(len(lens), q.shape[0], c["Hq"], c["Hk"], c["D"], c["page"], table.shape[1])
+    more = dict(rotary_dim=c["rd"], layout=c["layout"])
+    want = run(R, q, kp, vp, table, cu, lens, cos, sin, **more)
+    for fill in (0, 0xff):
+        big = torch.full((size + (1 << 20),), fill, dtype=torch.uint8, device="cuda")
+        got = run(R, q, kp, vp, table, cu, lens, cos, sin, workspace=big[:size], **more)
+        assert torch.equal(got, want) and bool((big[size:] == fill).all())
+
+
 def test_many_sequences():
     """The most sequences a call takes, a few tokens each, chunks among them; one more is refused."""
     require_gpu()
