@@ -291,8 +291,8 @@ rope_status rope_norm_qk_fwd(const void *q, const void *k, void *q_out, void *k_
  * dwq, dwk: device [D], of weight_dtype, written, or NULL (not wanted).
  * workspace: device, 16-byte aligned, rope_norm_qk_workspace(D) bytes (NULL where
  *    neither dwq nor dwk is given); overwritten.
- * Without tokens dwq and dwk are zeros.  Sums are fp32 in an order that the sizes
- *    alone give: the same call gives the same bits.
+ * Without tokens, or without heads of its kind, a weight's gradient is zeros.  Sums
+ *    are fp32 in an order that the sizes alone give: the same call gives the same bits.
  * Everything else, and errors: as rope_norm_qk_fwd; an output may overlap no
  *    other argument.
  */

@@ -122,26 +122,27 @@ rope_status norm_call(const Sizes &z, const Tensor (&in)[2], const float *cos, c
         return ROPE_ERR_INVALID_ARG;
     const bool sums = backward && (in[0].dw != nullptr || in[1].dw != nullptr);
     const int64_t heads = (int64_t)in[0].heads + in[1].heads;
-    if (heads == 0 || (tokens == 0 && !sums))
+    if ((heads == 0 || tokens == 0) && !sums)
         return ROPE_OK;
     NormArgs a;
     std::memset(&a, 0, sizeof a);
     Range ins[2][3] = {}, outs[2][2] = {};
     for (int i = 0; i < 2; ++i) {
-        if (in[i].heads == 0)
-            continue;
-        if (tokens == 0) {                     // no rows: dw alone is written
+        if (in[i].heads == 0 || tokens == 0) { // no rows: dw alone is written, zeros
+            const int64_t wb = z.D * (z.weight_dtype == ROPE_F32 ? 4 : 2);
             a.t[i].dw = in[i].dw;
             a.t[i].heads = in[i].heads;
             if (!aligned(in[i].dw, 4))
                 return ROPE_ERR_UNSUPPORTED;
+            ins[i][2] = {in[i].w, wb};
+            outs[i][1] = {in[i].dw, wb};
             continue;
         }
         e = check_tensor(z, in[i], backward, &a.t[i], ins[i], outs[i]);
         if (e != ROPE_OK)
             return e;
     }
-    if (tokens > 0 && (cos == nullptr || sin == nullptr || z.table_rows < 1))
+    if (tokens > 0 && heads > 0 && (cos == nullptr || sin == nullptr || z.table_rows < 1))
         return ROPE_ERR_INVALID_ARG;
     if (!aligned(cos, 16) || !aligned(sin, 16))
         return ROPE_ERR_UNSUPPORTED;
@@ -175,7 +176,7 @@ rope_status norm_call(const Sizes &z, const Tensor (&in)[2], const float *cos, c
     a.w_f32 = z.weight_dtype == ROPE_F32;
     a.eps = z.eps; a.inv_d = 1.0f / (float)z.D;
     for (int i = 0; i < 2; ++i)
-        if (backward && in[i].heads > 0 && in[i].dw != nullptr)
+        if (backward && in[i].dw != nullptr)
             a.t[i].partial = static_cast<float *>(workspace) + (int64_t)i * kNormPartials * z.D;
     if (device_flag(&a.flag) != cudaSuccess)
         return ROPE_ERR_CUDA;
