@@ -1088,9 +1088,8 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_paged_merge_kernel
         for (int32_t j = i + 1; j < clusters && cut[j].same_unit(c) && cut[j].kt > 0; ++j)
             ++n;
         const int32_t first = 2 * (i - 1) + (shared ? 0 : 1);
-        T *dst = static_cast<T *>(g.o) +
-                 ((int64_t)(e.q_start + tok) * f.Hq + (c.hu << g.lg) + (r & ((1 << g.lg) - 1))) * D;
-        merge_parts<T, D, 1>(n, dst, [&](int32_t p, float2 &stat) {
+        const int64_t to = (int64_t)(e.q_start + tok) * f.Hq + (c.hu << g.lg) + (r & ((1 << g.lg) - 1));
+        merge_parts<T, D, 1>(n, g.o, to, [&](int32_t p, float2 &stat) {
             const int64_t at = (int64_t)(p == 0 ? first : 2 * (i + p - 1)) * 256 + r;
             stat = __ldg(g.stats + at);
             return g.out + at * D;
@@ -1102,7 +1101,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) rope_paged_merge_kernel
             few.find(g, row);
         if constexpr (W > 1)
             __syncthreads();                                   // the last row's parts are read
-        merge_parts<T, D, W>(few.n, static_cast<T *>(g.o) + few.to * D, [&](int32_t p, float2 &stat) {
+        merge_parts<T, D, W>(few.n, g.o, few.to, [&](int32_t p, float2 &stat) {
             const int64_t at = few.from + (int64_t)p * 16;
             stat = __ldg(f.stats + at);
             return (const float *)f.out + at * D;
