@@ -232,8 +232,8 @@ rope_status rope_apply_q(void *x, const float *cos, const float *sin, const int3
  * by value_scale, or, when that is 0, by 1 (YARN: 0.1 ln f + 1).
  *
  * cos_out, sin_out: device, caller-owned, float[rows * rotary_dim/2] each.
- * Accuracy: frequencies in 64 bits on the host, phases as 64-bit fractions of a
- *   turn (p 2^-65 turns off at position p), values within 5 * 2^-24 of
+ * Accuracy: frequencies in more than 100 bits on the host, phases as 64-bit fractions
+ *   of a turn (p 2^-65 + 2^-57 turns off at position p), values within 6 * 2^-24 of
  *   themselves besides.
  * Errors: ROPE_ERR_UNSUPPORTED for an unknown kind or rotary_dim > 512;
  *   ROPE_ERR_INVALID_ARG if rotary_dim < 2 or odd (NTK: or 2), rows or

@@ -6,11 +6,19 @@
 // is all that matters, so the frequency is kept as a fixed-point fraction of a
 // turn, F_i = round(w_i / 2 pi * 2^64), and the phase is p * F_i modulo 2^64: one
 // 64-bit integer product is the whole range reduction, exact but for F_i's own
-// rounding (p 2^-65 turns: 4e-11 radians at a position of 10^8).  The nearest
+// rounding (p 2^-65 turns: 2e-11 radians at a position of 10^8).  A double has 53 bits
+// of F_i's 62, and a w_i from pow is off by more (pair 1 at theta 5e5: 704 times 2^-65
+// turns a position, 2.6e-7 radians at the last one), so the host computes the
+// frequencies with twice as many (Wide).  The nearest
 // quarter turn comes off the top two bits, and what is left, at most an eighth of
 // a turn either way, goes to fp32 (two roundings of 2^-24) and to the series of sine
-// and cosine.  The frequencies are computed on the host in 64 bits and go along as
-// kernel arguments: 64 pow in every CTA would cost more than the table.
+// and cosine.  The frequencies go along as kernel arguments: computed in every CTA they
+// would cost more than the table.
+//
+// Off by, at most: p 2^-65 turns for F_i; 2^-57 turns for a rest just below zero, whose two
+// parts are rounded before they cancel; and, in units u = 2^-24 of a sine (of a cosine): 2
+// (1.6) for the rest's two roundings, 1 (0.7) for the series' last sum, 0.8 (1.1) for what
+// comes before it, 0.1 for its end, 2 for the factor's rounding and its product: less than 6.
 //
 // What bounds it: 8 bytes a pair against some 50 instructions, at 64 pairs a
 // row about even: 131072 rows of 64 pairs write 67 MB.  Angles and sincos in 64
@@ -131,9 +139,78 @@ __global__ void __launch_bounds__(kScaledThreads) rope_tables_scaled_kernel(cons
     }
 }
 
-// w_i of every pair, radians per position; the factor of all values.
+// Numbers of twice 53 bits: hi + lo, lo at most half a unit of hi.
+struct Wide {
+    double hi, lo;
+};
+
+Wide sum_of(double a, double b)                // exact
+{
+    const double s = a + b, t = s - a;
+    return {s, (a - (s - t)) + (b - t)};
+}
+
+Wide product_of(double a, double b)            // exact
+{
+    // (a * b, but no compiler fuses it into a later sum, where its rounding would be lost)
+    const double p = std::fma(a, b, 0.0);
+    return {p, std::fma(a, b, -p)};
+}
+
+// Off by some 2^-104 of the result (the sum: of the larger term).
+Wide operator+(Wide a, Wide b)
+{
+    const Wide s = sum_of(a.hi, b.hi);
+    return sum_of(s.hi, s.lo + (a.lo + b.lo));
+}
+Wide operator-(Wide a, Wide b) { return a + Wide{-b.hi, -b.lo}; }
+Wide operator*(Wide a, Wide b)
+{
+    const Wide p = product_of(a.hi, b.hi);
+    return sum_of(p.hi, p.lo + std::fma(a.hi, b.lo, a.lo * b.hi));
+}
+Wide operator/(Wide a, Wide b)
+{
+    const double q = a.hi / b.hi;
+    const Wide rest = a - b * Wide{q, 0.0};
+    return sum_of(q, rest.hi / b.hi);
+}
+
+constexpr Wide kOne = {1.0, 0.0};
+// 1 / 2 pi: the nearest double, and the nearest to what that leaves
+constexpr Wide kPerTurn = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};
+
+Wide power(Wide x, int32_t n)                  // x^n, n >= 1
+{
+    int32_t bit = 1;
+    while (bit <= n / 2)
+        bit *= 2;
+    Wide y = x;
+    while ((bit /= 2) > 0) {
+        y = y * y;
+        if (n & bit)
+            y = y * x;
+    }
+    return y;
+}
+
+// x^(-1 / n): a double's power and a step of Newton's method on x y^n = 1
+Wide root(double x, int32_t n)
+{
+    const Wide y = {std::pow(x, -1.0 / n), 0.0};
+    return y + y * ((kOne - Wide{x, 0.0} * power(y, n)) / Wide{(double)n, 0.0});
+}
+
+Wide clamp01(Wide x)
+{
+    if (x.hi < 0.0)
+        return {0.0, 0.0};
+    return x.hi > 1.0 || (x.hi == 1.0 && x.lo > 0.0) ? kOne : x;
+}
+
+// Every pair's turn per position, as a fraction of a turn times 2^64; the factor of all values.
 void scaled_frequencies(int32_t kind, double theta, int32_t rd, double factor, int64_t original, double low, double high,
-                        double *w, double *scale)
+                        uint64_t *freq, double *scale)
 {
     const double pi = 3.14159265358979323846;
     const int32_t h = rd / 2;
@@ -147,21 +224,30 @@ void scaled_frequencies(int32_t kind, double theta, int32_t rd, double factor, i
         if (factor > 1.0)
             *scale = 0.1 * std::log(factor) + 1.0;
     }
-    const double base = kind == ROPE_SCALE_NTK ? theta * std::pow(factor, (double)rd / (double)(rd - 2)) : theta;
+    Wide ratio = root(theta, h);               // w_i+1 / w_i = theta^(-2 / rd)
+    if (kind == ROPE_SCALE_NTK)                // f^(rd / (rd - 2))^(-2 / rd)
+        ratio = ratio * root(factor, h - 1);
+    const Wide slower = kOne / Wide{factor, 0.0}, span = ramp1 > ramp0 ? Wide{ramp1 - ramp0, 0.0} : Wide{0.001, 0.0};
+    const Wide per = kOne / (kind == ROPE_SCALE_SMOOTH ? sum_of(high, -low) : span);
+    const Wide saved = kOne - slower, trained = Wide{(double)original, 0.0} * kPerTurn, twice = ratio * ratio;
+    Wide w[2] = {kOne, ratio};                 // of the next even pair, of the next odd one
     for (int32_t i = 0; i < h; ++i) {
-        double x = std::pow(base, -2.0 * (double)i / (double)rd);
+        Wide x = w[i & 1];
+        w[i & 1] = x * twice;
         if (kind == ROPE_SCALE_LINEAR) {
-            x /= factor;
+            x = x * slower;
         } else if (kind == ROPE_SCALE_SMOOTH) {
-            const double turns = (double)original * x / (2.0 * pi);
-            const double mix = std::fmin(std::fmax((turns - low) / (high - low), 0.0), 1.0);
-            x = (1.0 - mix) * x / factor + mix * x;
+            const Wide kept = clamp01((trained * x - Wide{low, 0.0}) * per);
+            x = kept.hi == 0.0 ? x * slower : kept.hi == 1.0 && kept.lo == 0.0 ? x : x * (slower + kept * saved);
         } else if (kind == ROPE_SCALE_YARN) {
-            const double span = ramp1 > ramp0 ? ramp1 - ramp0 : 0.001;
-            const double mix = std::fmin(std::fmax(((double)i - ramp0) / span, 0.0), 1.0);
-            x = x / factor * mix + x * (1.0 - mix);
+            const Wide slowed = clamp01(Wide{(double)i - ramp0, 0.0} * per);
+            x = slowed.hi == 0.0 ? x : slowed.hi == 1.0 && slowed.lo == 0.0 ? x * slower : x * (kOne - slowed * saved);
         }
-        w[i] = x;
+        // at most 1 / 2 pi of a turn; rounded once, behind hi's whole part
+        const Wide turn = x * kPerTurn;
+        const double hi = turn.hi * 0x1p64;
+        const uint64_t whole = (uint64_t)hi;
+        freq[i] = whole + (uint64_t)(int64_t)std::nearbyint(hi - (double)whole + turn.lo * 0x1p64);
     }
 }
 
@@ -197,10 +283,8 @@ extern "C" rope_status rope_tables_build_scaled(int32_t kind, double theta, int3
         !aligned(sin_out, 4))
         return ROPE_ERR_INVALID_ARG;
     ScaledArgs a;
-    double w[kScaledPairs], scale;
-    scaled_frequencies(kind, theta, rotary_dim, factor, original_positions, low_turns, high_turns, w, &scale);
-    for (int32_t i = 0; i < h; ++i)            // at most 1 / 2 pi of a turn
-        a.freq[i] = (uint64_t)std::nearbyint(w[i] / (2.0 * 3.14159265358979323846) * 18446744073709551616.0);
+    double scale;
+    scaled_frequencies(kind, theta, rotary_dim, factor, original_positions, low_turns, high_turns, a.freq, &scale);
     for (int32_t i = h; i < kScaledPairs; ++i)
         a.freq[i] = 0;
     a.cos = cos_out; a.sin = sin_out; a.rows = rows; a.first = (uint64_t)pos_offset; a.h = h;
