@@ -867,7 +867,7 @@ def norm_cache_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, wq: tor
     rotated, [T, Hq, D] (rows of tokens of no sequence are not written).
 
     q: [T, Hq, D], the new tokens' queries (a view with a token stride is taken as it is);
-    wq, wk: [D] weights in fp32 or q's type, or None.  q_out: the output, which may be q
+    wq, wk: [D] weights in fp32 or q's type, 16-byte aligned, or None.  q_out: the output, which may be q
     itself where that is dense.  Everything else as cache_append; attention_paged takes the
     result without cos and sin.
     """
@@ -1032,7 +1032,8 @@ def norm_rotate_qk(q: torch.Tensor | None, k: torch.Tensor | None, wq: torch.Ten
     q: [B, Hq, S, D] (or [B, S, Hq, D] with seq_before_head), k likewise with Hk heads, or
     either None; bf16, fp16 or fp32; views are taken as they are as long as features are
     dense and strides whole 16-byte vectors (a part of a fused projection's output).
-    wq, wk: [D] weights of all query (key) heads, fp32 or the rows' type, or None (ones).
+    wq, wk: [D] weights of all query (key) heads, fp32 or the rows' type, 16-byte aligned, or
+    None (ones).
     cos/sin: float32 [rows, rotary_dim // 2].  pos_idx: int32 [S] or [B, S] table rows (-1 =
     normalised, not rotated), or None.  q_out=q (k_out=k) works in place on a dense tensor.
     Carries no graph: ``autograd.norm_rotary_qk`` is the differentiable form.

@@ -66,7 +66,8 @@ def norm_rotary_qk(q: torch.Tensor | None, k: torch.Tensor | None, wq: torch.Ten
                    pos_idx: torch.Tensor | None = None, rotary_dim: int | None = None,
                    layout: str = "split_half", seq_before_head: bool = False):
     """Differentiable norm and rotation of q and k (either may be None): (q_out, k_out), with
-    gradients of q, k, wq and wk.  Arguments as ``norm_rotate_qk``.
+    gradients of q, k, wq and wk.  Arguments as ``norm_rotate_qk``; here q, k and weights whose
+    strides or alignment that call does not take are copied.
 
     While a CUDA graph is captured, no other graph of the same leaves made on another
     stream may be alive (drop the outputs of eager calls first): the call refuses, because

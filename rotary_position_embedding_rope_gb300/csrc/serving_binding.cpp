@@ -896,8 +896,8 @@ struct NormRotaryBackward : torch::autograd::Node {
 // The forward call on checked arguments, and its node where a gradient is wanted.
 rope_status norm_rotary_forward(const at::Tensor (&in)[7], double eps, int32_t layout, bool seq_first, at::Tensor (&y)[2])
 {
-    at::Tensor x[2] = {in[0], in[1]};
-    const at::Tensor w[2] = {in[2], in[3]}, &cos = in[4], &sin = in[5], &pos = in[6];
+    at::Tensor x[2] = {in[0], in[1]}, w[2] = {in[2], in[3]};
+    const at::Tensor &cos = in[4], &sin = in[5], &pos = in[6];
     bool graph = false;
     for (int i = 0; i < 4 && at::GradMode::is_enabled(); ++i)
         graph = graph || (in[i].defined() && in[i].requires_grad());
@@ -909,6 +909,9 @@ rope_status norm_rotary_forward(const at::Tensor (&in)[7], double eps, int32_t l
                     x[i] = x[i].clone(at::MemoryFormat::Contiguous);
                 y[i] = at::empty(x[i].sizes(), x[i].options().memory_format(at::MemoryFormat::Contiguous));
             }
+        for (at::Tensor &t : w)                // (a weight may lie anywhere in a buffer of parameters)
+            if (t.defined() && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 != 0)
+                t = t.clone();
     }
     const NormSizes z(x, w, cos, pos, seq_first);
     const rope_status st = g_norm(address(x[0]), address(x[1]), address(y[0]), address(y[1]), address(w[0]), address(w[1]),
@@ -921,7 +924,7 @@ rope_status norm_rotary_forward(const at::Tensor (&in)[7], double eps, int32_t l
     const std::shared_ptr<NormRotaryBackward> node(new NormRotaryBackward(), torch::autograd::deleteNode);
     node->set_next_edges(torch::autograd::collect_next_edges(in[0], in[1], in[2], in[3]));
     for (int i = 0; i < 7; ++i) {
-        const at::Tensor &t = i < 2 ? x[i] : in[i];
+        const at::Tensor &t = i < 2 ? x[i] : i < 4 ? w[i - 2] : in[i];
         node->given[i] = t.defined();
         if (t.defined())
             node->saved[i] = torch::autograd::SavedVariable(t, false);
@@ -964,7 +967,7 @@ PyObject *norm_rotary_qk(PyObject *, PyObject *const *a, Py_ssize_t n)
         const bool seq_first = truth(a[10]);
         auto given = [&](int i, const char *name) { return a[i] == Py_None ? at::Tensor() : tensor(a[i], name); };
         const at::Tensor q = given(0, "q"), k = given(1, "k"), wq = given(2, "wq"), wk = given(3, "wk"), pos = given(7, "pos_idx");
-        // (strides the library does not take are copied, so features need not be dense)
+        // (strides and alignments the library does not take are copied, so features need not be dense)
         struct Shape : Heads {
             Shape(const Call &c, const at::Tensor &t, const char *name, at::ScalarType type, bool seq_first)
                 : Heads(c, Py_None, name, type, seq_first)

@@ -1,4 +1,5 @@
-"""Weight gradients of the norm: of tensors without heads, and at the lengths of a training step."""
+"""Weight gradients of the norm: of tensors without heads, at the lengths of a training step, and of weights that lie
+anywhere in a buffer of parameters."""
 import pytest
 import torch
 
@@ -114,4 +115,31 @@ def test_past_32_bit_offsets():
     dw = R.norm_rotate_qk_backward(up, None, q, None, w, None, cos, sin, EPS, seq_before_head=True)[2]
     want, bound = weight_gradient(q, up, cos, sin, chain)
     assert ((dw.double() - want).abs() <= bound).all()
+    assert R.rope_check_errors() == R.ROPE_OK
+
+
+@pytest.mark.parametrize("wtype", [torch.float32, torch.bfloat16])
+def test_weights_anywhere_in_a_buffer(wtype):
+    """Views of a flat buffer that start at any element, as dense copies of them."""
+    require_gpu()
+    R = lib()
+    from rotary_position_embedding_rope_gb300 import autograd
+
+    D = 64
+    cos, sin = (x.cuda() for x in S.tables(1e4, D, 16))
+    flat = (torch.rand(2 * D + 3, device="cuda") + 0.5).to(wtype).requires_grad_()
+    wq, wk = flat[1:1 + D], flat[D + 2:2 * D + 2]
+    q, k = (torch.randn(2, 9, H, D, device="cuda", dtype=torch.bfloat16, requires_grad=True) for H in (4, 2))
+    out = autograd.norm_rotary_qk(q, k, wq, wk, cos, sin, EPS, seq_before_head=True)
+    up = [torch.randn_like(o) for o in out]
+    dense = [w.detach().clone().requires_grad_() for w in (wq, wk)]
+    same = autograd.norm_rotary_qk(q, k, *dense, cos, sin, EPS, seq_before_head=True)
+    assert all(torch.equal(a, b) for a, b in zip(out, same))
+    got = torch.autograd.grad(out, (q, k, flat), up)
+    want = torch.autograd.grad(same, (q, k, *dense), up)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(got[2][1:1 + D], want[2]) and torch.equal(got[2][D + 2:2 * D + 2], want[3])
+    assert not got[2][[0, D + 1, -1]].any()
+    with pytest.raises(R.RopeError):
+        R.norm_rotate_qk(q.detach(), None, wq.detach(), None, cos, sin, EPS, seq_before_head=True)
     assert R.rope_check_errors() == R.ROPE_OK
