@@ -412,8 +412,10 @@ def build_tables_scaled(kind: str, rotary_dim: int, rows: int, factor: float, or
     (pairs that make fewer than low_turns = 1 turns over the trained context are slowed
     by the factor, those of more than high_turns = 4 kept, a ramp between) or "yarn" (the
     ramp along the pairs, between those of low_turns = 1 and high_turns = 32 turns).
-    value_scale: factor of all values; None: 1, for "yarn" 0.1 ln(factor) + 1.
+    value_scale: factor of all values, above 0; None: 1, for "yarn" 0.1 ln(factor) + 1.
     """
+    if value_scale == 0:                       # (the library's word for "none given")
+        raise ValueError("value_scale must be above 0")
     at = -1
     if device is not None:
         device = torch.device(device)
