@@ -727,7 +727,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPackedThreads, 1)
     };
     // what ran before this launch (the prepare kernel) is complete from here on
     pdl_wait();
-    pdl_trigger();                                 // (what follows waits for all of this launch)
+    // (What follows waits for all of this launch, but for the paged merge's look at the plan:
+    // that it may start means that every CTA here has waited for it, so no trigger stands
+    // before a wait.)
+    pdl_trigger();
     const typename Source::Walk walk = src.template walk<D>(blockIdx.x >> 1, gridDim.x >> 1, smem);   // (CTA-wide)
     using Cursor = typename Source::Cursor;
     auto valid = [&](const Cursor &c) { return src.valid(walk, c); };
