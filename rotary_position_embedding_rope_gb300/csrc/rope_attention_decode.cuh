@@ -185,8 +185,8 @@ template <int D>
 static constexpr int kDecStageBytes = 2 * kDecKeys<D> * D * 2;
 template <int D>
 static constexpr int kDecQStride = D * 2 + 16;                 // padded rows of the query tile
-template <int D, int W = kDecWarps>
-static constexpr int kDecSmem = W * (kDecStages<D> * kDecStageBytes<D> + 16 * kDecQStride<D>);
+template <int D>
+static constexpr int kDecSmem = kDecWarps * (kDecStages<D> * kDecStageBytes<D> + 16 * kDecQStride<D>);
 
 struct DecodeArgs {
     AttnArgs a;                                // cos, sin, table_rows, rotary_dim, scale, flag
@@ -212,8 +212,8 @@ struct DecodeArgs {
     int32_t prefix_tiles;                      // key tiles of the prefix kernel (0: it does not run)
     int32_t suffix;                            // 1: the suffix kernel runs
 
-    // What the suffix code below asks of its arguments (the paged attention's
-    // are others, rope_attention_paged.cuh).
+    // What the runs of chunks below (ChunkAt, suffix_run, SuffixCopies) ask of their
+    // arguments (the paged attention's are others, rope_attention_paged.cuh).
     static constexpr int32_t kPairCost = 0;    // chunks that a pair counts for besides its own
     __device__ __forceinline__ int32_t sequences() const { return B + fold; }
     __device__ __forceinline__ int32_t heads() const { return Hk * row_groups; }
@@ -228,8 +228,19 @@ struct DecodeArgs {
         listed = b < B ? max_blocks : ((int64_t)n_prefix - 1 >> page_shift) + 1;
         return b < B ? table + b * max_blocks : prefix_table;
     }
-    // Row r of pair (b, hr): where its query lies (null: no such row), and whose it is.  The
-    // rows are heads of one sequence, or, for the folded prefix, of the whole batch.
+    // What the merge has to know of the suffixes' deal.  One CTA writes it, whether or
+    // not its waits expired: the merge runs in either case, and finds the parts'
+    // places by it.
+    __device__ __forceinline__ void publish(const int32_t *start, int64_t per) const
+    {
+        for (int32_t b = threadIdx.x; b <= B + fold; b += blockDim.x)
+            chunk_start[b] = start[b];
+        if (threadIdx.x == 0)
+            deal->suffix_per = per;
+    }
+    // What decode_suffixes asks.  Row r of pair (b, hr): where its query lies (null: no
+    // such row), and whose it is.  The rows are heads of one sequence, or, for the folded
+    // prefix, of the whole batch.
     template <typename T, int D>
     __device__ __forceinline__ const T *query(int32_t b, int32_t hr, int32_t r, int32_t &whose) const
     {
@@ -245,28 +256,17 @@ struct DecodeArgs {
     }
     // The table row that rotates it (apart from its place: the query's loads go out before
     // the position's have come).
-    __device__ __forceinline__ int64_t query_turn(int32_t, int32_t whose, int64_t most) const
+    __device__ __forceinline__ int64_t query_turn(int32_t whose, int64_t most) const
     {
         return query_row(pos_q, whose,
                          pos_q != nullptr ? 0 : (int64_t)n_prefix + suffix_keys(lens, whose, most, a.flag),
                          a.table_rows, a.flag);
     }
-    // The first row of warp w's part of pair (b, hr), and how many rows it has.
+    // The first row of warp w's part of pair (b, hr), of slot_rows.
     __device__ __forceinline__ int64_t part_row(int32_t w, int32_t b, int32_t hr) const
     {
         const int32_t pair = b * (Hk * row_groups) + hr;
         return ((int64_t)w + pair) * slot_rows;
-    }
-    __device__ __forceinline__ int32_t part_rows(int32_t, int32_t) const { return slot_rows; }
-    // What the merge has to know of the suffixes' deal.  One CTA writes it, whether or
-    // not its waits expired: the merge runs in either case, and finds the parts'
-    // places by it.
-    __device__ __forceinline__ void publish(const int32_t *start, int64_t per) const
-    {
-        for (int32_t b = threadIdx.x; b <= B + fold; b += blockDim.x)
-            chunk_start[b] = start[b];
-        if (threadIdx.x == 0)
-            deal->suffix_per = per;
     }
 };
 
@@ -349,8 +349,8 @@ struct ChunkAt {
 
 // 16 rows of rotated queries of pair (b, hr) into the warp's tile (zeros past
 // the pair's rows), then as the A operand of every 16-feature step.
-template <typename T, int LAYOUT, int D, typename G>
-__device__ __forceinline__ void load_query_rows(const G &g, const ChunkAt &at, int64_t most,
+template <typename T, int LAYOUT, int D>
+__device__ __forceinline__ void load_query_rows(const DecodeArgs &g, const ChunkAt &at, int64_t most,
                                                 uint8_t *tile, uint32_t (&qf)[D / 16][4])
 {
     constexpr int L = D / 16, kAtOnce = 32 / L, kSteps = 16 / kAtOnce;
@@ -363,12 +363,12 @@ __device__ __forceinline__ void load_query_rows(const G &g, const ChunkAt &at, i
         x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
         trow[i] = -1;
         int32_t whose;
-        const T *row = g.template query<T, D>(at.b, at.hr, i * kAtOnce + lane / L, whose);
+        const T *row = g.query<T, D>(at.b, at.hr, i * kAtOnce + lane / L, whose);
         if (row != nullptr) {
             x0[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o0));
             x1[i] = __ldg(reinterpret_cast<const uint4 *>(row + part.o1));
             if (part.rot)
-                trow[i] = g.query_turn(at.b, whose, most);
+                trow[i] = g.query_turn(whose, most);
         }
     }
 #pragma unroll
@@ -447,7 +447,8 @@ struct SuffixShared {
 };
 
 // The suffixes' share of CTA `cta` of `ctas`, whose first kWarps warps work:
-// every thread of the CTA calls this, then the working ones decode_suffixes.
+// every thread of the CTA calls this, then the working ones decode_suffixes (or
+// the paged attention's paged_few_run).
 template <int D, int kWarps, typename G>
 __device__ __forceinline__ SuffixRun suffix_run(const G &g, const int32_t *start, int32_t carry,
                                                 int32_t cta, int32_t ctas, SuffixShared<D, kWarps> &sh)
@@ -555,9 +556,9 @@ struct SuffixCopies {
 };
 
 // One warp's run; smem: kDecSmem bytes of the CTA.
-template <typename T, int LAYOUT, int D, int kWarps, typename G>
-__device__ __forceinline__ void decode_suffixes(const G &g, uint8_t *smem, const SuffixRun &run,
-                                                SuffixShared<D, kWarps> &sh)
+template <typename T, int LAYOUT, int D>
+__device__ __forceinline__ void decode_suffixes(const DecodeArgs &g, uint8_t *smem, const SuffixRun &run,
+                                                SuffixShared<D> &sh)
 {
     constexpr int kStages = kDecStages<D>, kStage = kDecStageBytes<D>, kKeys = kDecKeys<D>;
     constexpr int kBox = kKeys * 128, kGroups = kKeys / 16;
@@ -570,9 +571,9 @@ __device__ __forceinline__ void decode_suffixes(const G &g, uint8_t *smem, const
         return;
     uint64_t *bar = sh.bar[warp];
     uint8_t *stages = smem + warp * kStages * kStage;
-    uint8_t *qtile = smem + kWarps * kStages * kStage + warp * 16 * kDecQStride<D>;
+    uint8_t *qtile = smem + kDecWarps * kStages * kStage + warp * 16 * kDecQStride<D>;
     volatile int *abort = &sh.abort_flag;
-    SuffixCopies<D, G> copies(g, run, most, stages, bar);
+    SuffixCopies<D, DecodeArgs> copies(g, run, most, stages, bar);
     bool ok = true;
     int64_t issued = 0, done = 0;
     for (int st = 0; st < kStages && copies.left > 0; ++st, ++issued)
@@ -715,11 +716,10 @@ __device__ __forceinline__ void decode_suffixes(const G &g, uint8_t *smem, const
             l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
             const int r = lane >> 2;
             const int64_t row0 = g.part_row(w, was.b, was.hr);
-            const int32_t rows = g.part_rows(was.b, was.hr);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int rr = r + 8 * half;
-                if (rr < rows) {
+                if (rr < g.slot_rows) {
                     float *dst = g.out + (row0 + rr) * D + c0;
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i)

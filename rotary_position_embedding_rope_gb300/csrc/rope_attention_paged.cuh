@@ -350,7 +350,7 @@ static __global__ void __launch_bounds__(kPagedPlanThreads)
 }
 
 // ---------------------------------------------------------------------------
-// the few-row sequences: what decode_suffixes asks of its arguments
+// the few-row sequences: what their runs (ChunkAt, suffix_run, SuffixCopies) and few_pair ask
 
 struct PagedFew {
     AttnArgs a;                                // cos, sin (null: queries as they are), table_rows, scale, flag

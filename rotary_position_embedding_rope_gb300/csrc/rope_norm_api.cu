@@ -172,7 +172,7 @@ rope_status norm_call(const Sizes &z, const Tensor (&in)[2], const float *cos, c
     }
     a.cos = cos; a.sin = sin; a.pos = pos; a.pos_stride = z.pos_stride; a.table_rows = z.table_rows;
     a.tokens = tokens; a.B = z.B; a.S = z.S > 0 ? z.S : 1;
-    a.D = z.D; a.rotary_dim = z.rotary_dim; a.seq_first = z.seq_before_head;
+    a.D = z.D; a.rotary_dim = z.rotary_dim;
     a.w_f32 = z.weight_dtype == ROPE_F32;
     a.eps = z.eps; a.inv_d = 1.0f / (float)z.D;
     for (int i = 0; i < 2; ++i)

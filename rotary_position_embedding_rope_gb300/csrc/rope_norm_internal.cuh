@@ -28,7 +28,7 @@ struct NormArgs {
     int64_t pos_stride;              // 0: one row for all sequences
     int64_t table_rows, tokens, B, S;
     int64_t tiles[2];
-    int32_t D, rotary_dim, seq_first, w_f32;
+    int32_t D, rotary_dim, w_f32;
     float eps, inv_d;
     int32_t *flag;
 };
