@@ -181,6 +181,14 @@ __device__ __forceinline__ PagedCut paged_cut(const PagedPlan &p, int64_t pos, i
 // share the memory).  Taken as 53, as 65, as 70: 48 single tokens beside 2107 of chunks 262, 255,
 // 266 us; 100 beside a prompt of 2048 192, 168, 166; 16 beside two chunks of 512 129, 133, 137.
 constexpr float kFewRate = 65.0f;
+// A cluster's time a key tile beside them, for heads of 128 (of 64).  Taken as 900 (700), 1100
+// (900), 1300 (1050), 1500 (1200), us: 48 single tokens beside 2107 of chunks 250, 246, 263, 286;
+// 16 beside two chunks of 512 61.8, 55.5, 60.0, 64.2; 30 beside two of 300 71, 63, 63, 66; 64
+// beside four of 512 129, 117, 115, 118; 100 beside a prompt of 2048 159, 152, 152, 149; groups of
+// 16, 64 beside a chunk of 1024 80, 85, 91, 96; heads of 64, 16 beside two of 512 46.0, 44.3, 43.3,
+// 45.6, 48 beside a prompt of 2048 70, 65, 66, 69.  (Tiles alone take all clusters whatever it is.)
+template <int D>
+constexpr int32_t kPagedTileNs = D == 128 ? 1100 : 900;
 
 // Estimated time, in ns, with c clusters on the tiles and the few-row chunks on the
 // SMs left over (as plan_ns: an estimate that is off costs balance, never a result).
@@ -1175,7 +1183,7 @@ static cudaError_t launch_paged(const PagedCall &c, const PagedLayout &lay, cuda
     p.head_units = s.head_units; p.heads = c.Hk * f.row_groups;
     p.total_q = c.total_q; p.most_keys = c.max_blocks << c.page_shift;
     p.causal = c.causal; p.chunk_shift = f.chunk_shift; p.page_shift = c.page_shift;
-    p.chunk_bytes = kDecStageBytes<D>; p.tile_ns = D == 128 ? 900 : 700; p.grid = 2 * clusters;
+    p.chunk_bytes = kDecStageBytes<D>; p.tile_ns = kPagedTileNs<D>; p.grid = 2 * clusters;
     p.deal = reinterpret_cast<PagedDeal *>(ws);
     p.entries = reinterpret_cast<PagedEntry *>(ws + lay.entries);
     p.chunk_start = reinterpret_cast<int32_t *>(ws + lay.chunk_start);
