@@ -678,9 +678,13 @@ static cudaError_t launch_norm_lanes(NormArgs a, cudaStream_t st)
         return e;
     // The CTAs that are resident at once, or twice or three times as many where that leaves
     // runs of some length: the hardware hands them out as others end, which evens out what the
-    // SMs and their way to memory take.  Once, twice, three times (us): 16k tokens of 40 heads
-    // of 128, forward 60.6, -, 55.1, backward 96, 92, 87; 12000 tokens of 20 heads of 96, 19.5,
-    // -, 23.2 and 34, 37, 41.
+    // SMs and their way to memory take.  Once, twice, three times (us; forward, then backward,
+    // 40 heads of 128 unless said): 16k tokens 62.1, 59.1, 56.0 and 96.5, 93.2, 88.3; 8k 30.5, 29.4,
+    // 29.6 and 48.0, 47.6, 50.4; 4k 14.2, 16.0, 16.0 and 26.5, 30.0, 32.6; 64k of ten heads 69.6, 65.7,
+    // 65.9 and 110, 98, 97; 12000 of 20 heads of 96 18.8, 20.6, 21.2 and 33.6, 36.5, 39.6; 24000 37.6,
+    // 36.9, 38.2 and 59.4, 61.1, 61.7; 30000 of 16 heads of 64 20.5, 23.8, 24.5 and 37.3, 40.7, 43.9;
+    // 16k of 32 heads of 64 in fp32 46.7, 45.1, 44.0 and 70 each.  The limits below pick within 3 % of
+    // the best of each; 8k of 20 heads of 256 are the exception (forward 32.2, 30.7, 30.1: once).
     const int64_t resident = kNormCtas<BACKWARD> * (int64_t)sms;
     int64_t waves = tiles / ((BACKWARD ? 12 : 5) * resident);
     waves = waves < 1 ? 1 : waves > 3 ? 3 : waves;

@@ -124,8 +124,10 @@ struct PagedCall {
 constexpr int32_t kPagedUnitTiles = 4;
 // Least weight of a cluster's run where there are more clusters than units: shorter runs
 // leave more pieces than they save.  (Two units one after the other take longer than either
-// alone: 84 rows of eight key heads after 300 keys, beside three single tokens, on seven
-// clusters 23.3 us, on eight 21.1.)
+// alone.  Clusters by the weight alone, and no fewer than units, us: 84 rows of eight key heads
+// after 300 keys beside three single tokens, seven and eight clusters, 23.3, 21.1; four chunks of
+// 40 after up to 300 keys 19.6, 18.2, eight of them 20.9, 20.0, 16 of them 23.4, 23.5; three of 30
+// with heads of 64 17.4, 15.4; 24 of 20 29.1, 29.0; 64 prompts of 40 47.5 either way.)
 constexpr int64_t kPagedMinRun = 2 * kPagedUnitTiles;
 // What a pair (sequence, key head) of a few-row sequence counts for besides its chunks, in
 // chunks: its queries' way in and its outputs' way out, several loads one after the other.
