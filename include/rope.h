@@ -267,7 +267,10 @@ rope_status rope_tables_build_scaled(int32_t kind, double theta, int32_t rotary_
  * D, rotary_dim: multiples of 16, 16 <= rotary_dim <= D <= 256; features past
  *    rotary_dim are normalised and weighted too.  dtype: ROPE_F32, ROPE_BF16 or
  *    ROPE_F16.  eps: >= 0, finite.
- * Arithmetic: fp32 throughout, one rounding to dtype at the end.
+ * Arithmetic: fp32 throughout, one rounding to dtype at the end.  So the sum of a
+ *    row's squares has to lie in fp32's range: rows with elements past 10^18 come out
+ *    as zeros, and with eps = 0 rows of elements below 10^-19 lose precision (all
+ *    below 10^-23 they come out as infinities, all zeros as NaN).
  * Errors: ROPE_ERR_UNSUPPORTED for other types, layouts, D, rotary_dim, strides
  *    that are not whole 16-byte vectors or pointers not 16-byte aligned;
  *    ROPE_ERR_INVALID_ARG for bad sizes (B * S above 2^31 - 1, negative or zero
