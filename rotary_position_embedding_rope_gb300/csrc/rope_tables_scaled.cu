@@ -201,11 +201,12 @@ Wide root(double x, int32_t n)
     return y + y * ((kOne - Wide{x, 0.0} * power(y, n)) / Wide{(double)n, 0.0});
 }
 
-Wide clamp01(Wide x)
+// x w, for a weight that goes from `below` at a <= 0 to `above` at a >= span.
+Wide ramp(Wide x, Wide a, Wide span, Wide below, Wide above)
 {
-    if (x.hi < 0.0)
-        return {0.0, 0.0};
-    return x.hi > 1.0 || (x.hi == 1.0 && x.lo > 0.0) ? kOne : x;
+    if (a.hi <= 0.0)
+        return x * below;
+    return (a - span).hi >= 0.0 ? x * above : x * (below + a / span * (above - below));
 }
 
 // Every pair's turn per position, as a fraction of a turn times 2^64; the factor of all values.
@@ -227,22 +228,17 @@ void scaled_frequencies(int32_t kind, double theta, int32_t rd, double factor, i
     Wide ratio = root(theta, h);               // w_i+1 / w_i = theta^(-2 / rd)
     if (kind == ROPE_SCALE_NTK)                // f^(rd / (rd - 2))^(-2 / rd)
         ratio = ratio * root(factor, h - 1);
-    const Wide slower = kOne / Wide{factor, 0.0}, span = ramp1 > ramp0 ? Wide{ramp1 - ramp0, 0.0} : Wide{0.001, 0.0};
-    const Wide per = kOne / (kind == ROPE_SCALE_SMOOTH ? sum_of(high, -low) : span);
-    const Wide saved = kOne - slower, trained = Wide{(double)original, 0.0} * kPerTurn, twice = ratio * ratio;
+    const Wide slower = kOne / Wide{factor, 0.0}, trained = Wide{(double)original, 0.0} * kPerTurn, twice = ratio * ratio;
     Wide w[2] = {kOne, ratio};                 // of the next even pair, of the next odd one
     for (int32_t i = 0; i < h; ++i) {
         Wide x = w[i & 1];
         w[i & 1] = x * twice;
-        if (kind == ROPE_SCALE_LINEAR) {
+        if (kind == ROPE_SCALE_LINEAR)
             x = x * slower;
-        } else if (kind == ROPE_SCALE_SMOOTH) {
-            const Wide kept = clamp01((trained * x - Wide{low, 0.0}) * per);
-            x = kept.hi == 0.0 ? x * slower : kept.hi == 1.0 && kept.lo == 0.0 ? x : x * (slower + kept * saved);
-        } else if (kind == ROPE_SCALE_YARN) {
-            const Wide slowed = clamp01(Wide{(double)i - ramp0, 0.0} * per);
-            x = slowed.hi == 0.0 ? x : slowed.hi == 1.0 && slowed.lo == 0.0 ? x * slower : x * (kOne - slowed * saved);
-        }
+        else if (kind == ROPE_SCALE_SMOOTH)
+            x = ramp(x, trained * x - Wide{low, 0.0}, sum_of(high, -low), slower, kOne);
+        else if (kind == ROPE_SCALE_YARN)
+            x = ramp(x, {(double)i - ramp0, 0.0}, {ramp1 > ramp0 ? ramp1 - ramp0 : 0.001, 0.0}, kOne, slower);
         // at most 1 / 2 pi of a turn; rounded once, behind hi's whole part
         const Wide turn = x * kPerTurn;
         const double hi = turn.hi * 0x1p64;

@@ -54,3 +54,16 @@ def test_phases(kind, rd, theta, offset):
         d = (got.cpu().double() - want).abs()
         bound = 6 * U * want.abs() + off
         assert (d <= bound).all(), "%.2f of the bound" % (d / bound).max()
+
+
+@pytest.mark.parametrize("low,high", [(1e-300, 2e-300), (5e-324, 1e-323), (1.0, math.nextafter(1.0, 2.0)), (1e300, 1.7e308)])
+def test_ramps_of_any_width(low, high):
+    """Pairs beyond the ramp, however narrow or far it is, are the unscaled ones, or those of every position divided."""
+    require_gpu()
+    R = lib()
+    got = R.build_tables_scaled("smooth", 64, 40, 8.0, 4096, low_turns=low, high_turns=high, pos_offset=5)
+    kept = R.build_tables_scaled("linear", 64, 40, 1.0, pos_offset=5)
+    slowed = R.build_tables_scaled("linear", 64, 40, 8.0, pos_offset=5)
+    n = 4096 * 1e4 ** (-torch.arange(32, dtype=torch.float64) / 32) / (2 * math.pi)
+    for a, b, c in zip(got, kept, slowed):
+        assert torch.equal(a.cpu(), torch.where(n > high, b.cpu(), c.cpu()))
